@@ -1,5 +1,7 @@
 """gemm_gather for GB300: tiled all-gather over a symmetric heap, alone and
-fused into the epilogue of a matmul (iris PR #626, iris #594, iris #591).
+fused into the epilogue of a matmul (iris PR #626, iris #594, iris #591), and
+the operators of the training or serving step around it: a linear layer with
+its gradients, a clipped policy loss, AdamW.
 
 Thin Python binding of the C ABI in include/gemm_gather.h (same names, minus
 the ``gg_`` prefix).  It only marshals arguments: torch tensors become device
@@ -21,6 +23,8 @@ from ._lib import (GG_AG_AUTO, GG_AG_BULK, GG_AG_TMA, GG_AG_VECTOR, GG_BF16, GG_
                    GG_FUSED_BLOCK_N_WIDE,
                    GG_CLAIM_ALWAYS, GG_CLAIM_AUTO, GG_CLAIM_NEVER, GG_MAX_WORLD, GG_OK,
                    GG_WORKSPACE_SLOT_BYTES,
+                   GG_ACT_GELU, GG_ACT_GELU_TANH, GG_ACT_NONE, GG_ACT_RELU, GG_ACT_SILU,
+                   GG_LINEAR_AUTO, GG_LINEAR_PAIR, GG_LINEAR_SPLIT, GG_WEIGHT_KN, GG_WEIGHT_NK,
                    GGError, Group, Tile, check, lib, LIB_PATH)
 
 __all__ = [
@@ -28,6 +32,8 @@ __all__ = [
     "all_gather", "all_gather_noalloc",
     "all_gather_check", "all_gather_grouped", "all_gather_partitioned", "all_to_all",
     "collective_check", "matmul_all_gather", "matmul_all_gather_check", "matmul_all_gather_plan",
+    "linear", "linear_check", "linear_backward", "linear_backward_check", "act_backward",
+    "ACTIVATIONS", "WEIGHT_LAYOUTS", "LINEAR_PATHS",
     "set_claim_policy",
     "get_claim_policy", "CLAIM_POLICIES", "set_store_policy", "get_store_policy",
     "STORE_POLICIES", "set_wait_limit_ns",
@@ -41,6 +47,10 @@ PATHS = {"auto": GG_AG_AUTO, "bulk": GG_AG_BULK, "vector": GG_AG_VECTOR, "tma": 
 FUSED_PATHS = {"auto": GG_MAG_AUTO, "1sm": GG_MAG_1SM, "2sm": GG_MAG_2SM}
 FUSED_TILE = (GG_FUSED_BLOCK_M, GG_FUSED_BLOCK_N)             # 128 x 256 per CTA
 FUSED_TILE_WIDE = (GG_FUSED_BLOCK_M, GG_FUSED_BLOCK_N_WIDE)   # 128 x 512 per CTA (CTA pairs)
+ACTIVATIONS = {"none": GG_ACT_NONE, "relu": GG_ACT_RELU, "gelu": GG_ACT_GELU,
+               "gelu_tanh": GG_ACT_GELU_TANH, "silu": GG_ACT_SILU}
+WEIGHT_LAYOUTS = {"kn": GG_WEIGHT_KN, "nk": GG_WEIGHT_NK}     # rows of K x N, or of N x K
+LINEAR_PATHS = {"auto": GG_LINEAR_AUTO, "split": GG_LINEAR_SPLIT, "pair": GG_LINEAR_PAIR}
 CLAIM_POLICIES = {"auto": GG_CLAIM_AUTO, "always": GG_CLAIM_ALWAYS, "never": GG_CLAIM_NEVER}
 STORE_POLICIES = {"plain": 0, "evict_first": 1}  # GG_STORE_PLAIN, GG_STORE_EVICT_FIRST
 
@@ -240,6 +250,77 @@ def matmul_all_gather_plan(heap: Heap, rank: int, A, lda: int, B, ldb: int, outp
                                         comm_programs, Group(*group), FUSED_PATHS[path],
                                         ctypes.byref(chosen)))
     return {GG_MAG_AUTO: "none", GG_MAG_1SM: "1sm", GG_MAG_2SM: "2sm"}[chosen.value]
+
+
+# --------------------------------------------------------------------------- #
+# Operators of the step around the gathered matmul                            #
+# --------------------------------------------------------------------------- #
+
+_LINEAR_NAMES = {0: "none", GG_LINEAR_SPLIT: "split", GG_LINEAR_PAIR: "pair"}
+
+
+def _bias_dtype(bias, bias_dtype, dtype) -> int:
+    if bias_dtype is None and isinstance(bias, torch.Tensor):
+        bias_dtype = bias.dtype
+    return _dtype(dtype if bias_dtype is None else bias_dtype)
+
+
+def linear(X, ldx: int, W, ldw: int, layout: str, bias, act: str, residual, ldr: int, Y, ldy: int,
+           z, ldz: int, M: int, N: int, K: int, dtype, status=None, stream=None, path: str = "auto",
+           bias_dtype=None) -> None:
+    """Y = act(X W + bias) + residual; z (or None) receives X W + bias (gg_linear).
+    ``bias_dtype`` is taken from a bias tensor, else ``dtype``."""
+    check(lib.gg_linear(_ptr(X), ldx, _ptr(W), ldw, WEIGHT_LAYOUTS[layout], _ptr(bias),
+                        _bias_dtype(bias, bias_dtype, dtype), ACTIVATIONS[act], _ptr(residual), ldr,
+                        _ptr(Y), ldy, _ptr(z), ldz, M, N, K, _dtype(dtype), _ptr(status),
+                        _stream(stream), LINEAR_PATHS[path]))
+
+
+def linear_check(X, ldx: int, W, ldw: int, layout: str, bias, act: str, residual, ldr: int, Y,
+                 ldy: int, z, ldz: int, M: int, N: int, K: int, dtype, path: str = "auto",
+                 bias_dtype=None) -> str:
+    """Validate without launching; returns the kernel a launch would run
+    ("split" or "pair"; "none" when no product runs)."""
+    chosen = ctypes.c_int()
+    check(lib.gg_linear_check(_ptr(X), ldx, _ptr(W), ldw, WEIGHT_LAYOUTS[layout], _ptr(bias),
+                              _bias_dtype(bias, bias_dtype, dtype), ACTIVATIONS[act],
+                              _ptr(residual), ldr, _ptr(Y), ldy, _ptr(z), ldz, M, N, K,
+                              _dtype(dtype), LINEAR_PATHS[path], ctypes.byref(chosen)))
+    return _LINEAR_NAMES[chosen.value]
+
+
+def linear_backward(dZ, lddz: int, X, ldx: int, W, ldw: int, layout: str, z_in, ldzin: int,
+                    act_in: str, dX, lddx: int, dW, lddw: int, dbias, grad_dtype, accumulate: bool,
+                    M: int, N: int, K: int, dtype, status=None, stream=None,
+                    path: str = "auto") -> None:
+    """dX = (dZ W^T) act_in'(z_in), dW (+)= X^T dZ, dbias (+)= column sums of dZ
+    (gg_linear_backward); any of the three outputs may be None."""
+    check(lib.gg_linear_backward(_ptr(dZ), lddz, _ptr(X), ldx, _ptr(W), ldw, WEIGHT_LAYOUTS[layout],
+                                 _ptr(z_in), ldzin, ACTIVATIONS[act_in], _ptr(dX), lddx, _ptr(dW),
+                                 lddw, _ptr(dbias), _dtype(grad_dtype), 1 if accumulate else 0, M, N,
+                                 K, _dtype(dtype), _ptr(status), _stream(stream), LINEAR_PATHS[path]))
+
+
+def linear_backward_check(dZ, lddz: int, X, ldx: int, W, ldw: int, layout: str, z_in, ldzin: int,
+                          act_in: str, dX, lddx: int, dW, lddw: int, dbias, grad_dtype,
+                          accumulate: bool, M: int, N: int, K: int, dtype,
+                          path: str = "auto") -> tuple[str, str]:
+    """Validate without launching; returns the kernels of dX and dW."""
+    dx, dw = ctypes.c_int(), ctypes.c_int()
+    check(lib.gg_linear_backward_check(_ptr(dZ), lddz, _ptr(X), ldx, _ptr(W), ldw,
+                                       WEIGHT_LAYOUTS[layout], _ptr(z_in), ldzin,
+                                       ACTIVATIONS[act_in], _ptr(dX), lddx, _ptr(dW), lddw,
+                                       _ptr(dbias), _dtype(grad_dtype), 1 if accumulate else 0, M, N,
+                                       K, _dtype(dtype), LINEAR_PATHS[path], ctypes.byref(dx),
+                                       ctypes.byref(dw)))
+    return _LINEAR_NAMES[dx.value], _LINEAR_NAMES[dw.value]
+
+
+def act_backward(dy, lddy: int, z, ldz: int, dz, lddz: int, act: str, M: int, N: int, dtype,
+                 stream=None) -> None:
+    """dz = dy * act'(z) (gg_act_backward)."""
+    check(lib.gg_act_backward(_ptr(dy), lddy, _ptr(z), ldz, _ptr(dz), lddz, ACTIVATIONS[act], M, N,
+                              _dtype(dtype), _stream(stream)))
 
 
 def set_claim_policy(policy: str) -> None:

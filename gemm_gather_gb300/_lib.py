@@ -35,6 +35,10 @@ GG_FUSED_BLOCK_M, GG_FUSED_BLOCK_N, GG_FUSED_BLOCK_N_WIDE = 128, 256, 512
 GG_WORKSPACE_SLOT_BYTES = 128
 GG_CLAIM_AUTO, GG_CLAIM_ALWAYS, GG_CLAIM_NEVER = 0, 1, 2
 GG_STORE_PLAIN, GG_STORE_EVICT_FIRST = 0, 1
+GG_ACT_NONE, GG_ACT_RELU, GG_ACT_GELU, GG_ACT_GELU_TANH, GG_ACT_SILU = 0, 1, 2, 3, 4
+GG_WEIGHT_KN, GG_WEIGHT_NK = 0, 1
+GG_LINEAR_AUTO, GG_LINEAR_SPLIT, GG_LINEAR_PAIR = 0, 1, 2
+GG_LINEAR_NONE = 0
 
 # Every entry point declared in include/gemm_gather.h.
 EXPORTS = (
@@ -45,6 +49,8 @@ EXPORTS = (
     "gg_all_gather_partitioned", "gg_all_to_all", "gg_collective_check",
     "gg_matmul_all_gather", "gg_matmul_all_gather_path", "gg_matmul_all_gather_check",
     "gg_matmul_all_gather_plan",
+    "gg_linear", "gg_linear_check", "gg_linear_backward", "gg_linear_backward_check",
+    "gg_act_backward",
     "gg_set_claim_policy", "gg_get_claim_policy", "gg_set_store_policy", "gg_get_store_policy",
     "gg_set_wait_limit_ns", "gg_get_wait_limit_ns", "gg_debug_inject_stall",
     "gg_device_status", "gg_clear_device_status",
@@ -102,6 +108,16 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
                                         Tile, i32, Group], i32),
         "gg_matmul_all_gather_plan": ([vp, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32,
                                        Tile, i32, Group, i32, ctypes.POINTER(i32)], i32),
+        "gg_linear": ([vp, i64, vp, i64, i32, vp, i32, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+                       i32, vp, vp, i32], i32),
+        "gg_linear_check": ([vp, i64, vp, i64, i32, vp, i32, i32, vp, i64, vp, i64, vp, i64, i64, i64,
+                             i64, i32, i32, ctypes.POINTER(i32)], i32),
+        "gg_linear_backward": ([vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp, i32,
+                                i32, i64, i64, i64, i32, vp, vp, i32], i32),
+        "gg_linear_backward_check": ([vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp,
+                                      i32, i32, i64, i64, i64, i32, i32, ctypes.POINTER(i32),
+                                      ctypes.POINTER(i32)], i32),
+        "gg_act_backward": ([vp, i64, vp, i64, vp, i64, i32, i64, i64, i32, vp], i32),
         "gg_set_claim_policy": ([i32], i32),
         "gg_get_claim_policy": ([], i32),
         "gg_set_store_policy": ([i32], i32),

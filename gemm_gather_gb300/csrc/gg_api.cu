@@ -13,6 +13,7 @@
 
 #include "../../include/gemm_gather.h"
 #include "gg_internal.h"
+#include "gg_ops.h"
 
 struct gg_heap {
     uint64_t base;
@@ -198,6 +199,28 @@ gg_status resolve_status(int **status)
 }
 
 }  // namespace
+
+// What the operators' entry points (gg_ops.cu) share with the calls below.
+namespace gg {
+
+gg_status op_fail(gg_status s, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return s;
+}
+
+gg_status op_ok() { return ok(); }
+gg_status op_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+gg_status op_status_word(int **status) { return resolve_status(status); }
+uint64_t op_wait_limit_ns() { return g_wait_limit_ns.load(); }
+int op_inject_stall() { return g_inject_stall.load(); }
+
+}  // namespace gg
 
 // The library's trace records (one per device, gg_set_trace): the all-gather
 // family's last traced launch in words 0..3, the fused call's in words 4..7.
@@ -994,7 +1017,7 @@ const char *gg_status_string(gg_status s)
     return "GG_UNKNOWN";
 }
 
-int gg_version(void) { return 100; }
+int gg_version(void) { return 200; }
 
 #ifndef GG_CHECKED
 #define GG_CHECKED 0

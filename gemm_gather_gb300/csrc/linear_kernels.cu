@@ -1,0 +1,1162 @@
+// The linear layer for sm_103a: Y = act(X W + b) + R and its gradients.
+//
+// Every product of the layer is one form,
+//     out[j, i] = epilogue( sum_k A[i, k] B[j, k] ),
+// with i the contiguous index of the output (MMA rows, TMEM lanes) and j its
+// row (MMA columns):
+//     forward        i = out feature, j = token, k = in feature   A = W,  B = X
+//     input gradient i = in feature,  j = token, k = out feature  A = W,  B = dZ
+//     weight gradient, W K x N:  i = n, j = k, contraction over tokens  A = dZ, B = X
+//                      W N x K:  i = k, j = n                           A = X,  B = dZ
+// An operand whose contraction index is contiguous in memory is K-major, else
+// MN-major; tcgen05 reads both from 128-byte swizzled shared memory, so no
+// operand is ever transposed in memory.  Features on the MMA's 128 rows: a
+// thread of the epilogue owns one feature, its warp 32 neighbouring ones, so
+// the bias is one register, every global access of the epilogue is 32
+// neighbouring elements at any alignment, and a product of a few tokens pads
+// only the MMA's columns (16 at least) and not its 128 rows.
+//
+// Two kernels:
+//  * pair_kernel: persistent CTA pairs on 256 x 256 tiles (tcgen05
+//    cta_group::2, 64-deep stages of 32 KB per CTA, 6 in the ring, two
+//    accumulators in TMEM so that a tile's epilogue runs under the next
+//    tile's MMAs).  For products with enough tiles to fill the GPU.
+//  * split_kernel: one CTA per 128 x {16..128} tile and share of the
+//    contraction; the CTAs of a cluster (up to 8) split one tile's
+//    contraction and join their float32 partial tiles through distributed
+//    shared memory in rank order (the same bits on every run, no workspace, no
+//    second launch).  For few tokens, where the time is that of streaming W,
+//    and for few tiles.
+//
+// Sums.  tcgen05's float32 accumulator truncates when it adds: measured
+// against float64 on normal operands, the relative error grows with the
+// length of the contraction (4.7e-7 at 512, 4.4e-6 at 4096, 1.9e-5 at 16384,
+// where a float32 sum rounded to nearest has 1.5e-6).  That is nothing to a
+// 16-bit result, but weight gradients are kept in float32 over long sums of
+// tokens, so the weight gradient accumulates kChunk k-blocks in TMEM and adds
+// the chunks in registers with round-to-nearest.
+//
+// Every mbarrier wait is bounded; one that gives up stores GG_ERR_TIMEOUT in
+// the status word and raises the CTA's abort flag, and every role drains what
+// it has in flight before TMEM is freed and the CTA exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "gg_internal.h"
+#include "gg_ops.h"
+#include "tc.cuh"
+
+namespace gg {
+namespace {
+
+using namespace tc;
+
+constexpr int kSMs = 152;
+constexpr int kBK = 64;                    // k of one stage: a 128-byte swizzle row
+constexpr int UK = 16;                     // k of one MMA
+constexpr int kChunk = 8;                  // k-blocks per TMEM chunk of a weight gradient (512 k)
+constexpr int kMnBox = kBK * 64 * 2;       // 8 KB: 64 k-rows x 64 columns of an MN-major operand
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
+constexpr int kMaxStages = 8;
+
+struct Shared {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// ---- epilogue arithmetic ---------------------------------------------------------
+__device__ __forceinline__ float load16(const void *p, int64_t at, int bf16)
+{
+    const uint16_t u = reinterpret_cast<const uint16_t *>(p)[at];
+    return bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+
+__device__ __forceinline__ void store16(void *p, int64_t at, float v, int bf16)
+{
+    reinterpret_cast<uint16_t *>(p)[at] =
+        bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// Activations in float32.  relu keeps NaN; gelu_tanh's 0.5 (1 + tanh u) is
+// the logistic function of 2u, which keeps its relative precision for u << 0.
+__device__ __forceinline__ float logistic(float x) { return 1.0f / (1.0f + __expf(-x)); }
+__device__ __forceinline__ float gelu_u2(float z)
+{
+    return 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 sqrt(2/pi) (z + ...)
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z)
+{
+    if constexpr (ACT == GG_ACT_RELU)
+        return !(z <= 0.0f) ? z : 0.0f;
+    if constexpr (ACT == GG_ACT_GELU)
+        return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    if constexpr (ACT == GG_ACT_GELU_TANH)
+        return z * logistic(gelu_u2(z));
+    if constexpr (ACT == GG_ACT_SILU)
+        return z * logistic(z);
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
+{
+    if constexpr (ACT == GG_ACT_RELU)
+        return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == GG_ACT_GELU)
+        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    if constexpr (ACT == GG_ACT_GELU_TANH) {
+        const float s = logistic(gelu_u2(z));  // d(z s)/dz = s + z s (1 - s) 2u'
+        return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+    }
+    if constexpr (ACT == GG_ACT_SILU) {
+        const float s = logistic(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    return 1.0f;
+}
+
+// f(ACT) with the activation as a compile-time constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
+{
+    switch (act) {
+    case GG_ACT_RELU: f(std::integral_constant<int, GG_ACT_RELU>()); break;
+    case GG_ACT_GELU: f(std::integral_constant<int, GG_ACT_GELU>()); break;
+    case GG_ACT_GELU_TANH: f(std::integral_constant<int, GG_ACT_GELU_TANH>()); break;
+    case GG_ACT_SILU: f(std::integral_constant<int, GG_ACT_SILU>()); break;
+    default: f(std::integral_constant<int, GG_ACT_NONE>()); break;
+    }
+}
+
+// One feature's sums for columns j0, j0 + jstep, ... (n of them, at most 16):
+// the epilogue and the store.  A warp's 32 lanes hold 32 neighbouring
+// features.  Loads of the 16 columns are issued together, ahead of their use.
+template <int EPI>
+__device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j0, int jstep, int n,
+                                       float (&v)[16], float bias)
+{
+    if (i >= a.I)
+        return;
+    if constexpr (EPI == kEpiGradW) {
+        if (a.out_f32) {
+            float *o = reinterpret_cast<float *>(a.out) + j0 * a.ldo + i;
+            const int64_t step = (int64_t)jstep * a.ldo;
+            if (a.accumulate) {
+                float old[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    old[u] = u < n ? o[u * step] : 0.0f;
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] += old[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                if (u < n)
+                    o[u * step] = v[u];
+            return;
+        }
+    }
+    float x[16];
+    const void *aux = EPI == kEpiGradW ? (a.accumulate ? a.out : nullptr) : a.aux;
+    const int64_t ldaux = EPI == kEpiGradW ? a.ldo : a.ldaux;
+    if (aux != nullptr) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            x[u] = u < n ? load16(aux, (j0 + (int64_t)u * jstep) * ldaux + i, a.is_bf16) : 0.0f;
+    }
+    if constexpr (EPI == kEpiForward) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            v[u] += bias;
+        if (a.zout != nullptr) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                if (u < n)
+                    store16(a.zout, (j0 + (int64_t)u * jstep) * a.ldz + i, v[u], a.is_bf16);
+        }
+        with_act(a.act, [&](auto c) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] = act_value<decltype(c)::value>(v[u]);
+        });
+        if (aux != nullptr) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] += x[u];
+        }
+    } else if constexpr (EPI == kEpiGradIn) {
+        if (aux != nullptr)
+            with_act(a.act, [&](auto c) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] *= act_slope<decltype(c)::value>(x[u]);
+            });
+    } else if (aux != nullptr) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            v[u] += x[u];
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+        if (u < n)
+            store16(a.out, (j0 + (int64_t)u * jstep) * a.ldo + i, v[u], a.is_bf16);
+}
+
+__device__ __forceinline__ float load_bias(const LinearArgs &a, int64_t i)
+{
+    if (a.bias == nullptr || i >= a.I)
+        return 0.0f;
+    return a.bias_f32 ? reinterpret_cast<const float *>(a.bias)[i] : load16(a.bias, i, a.is_bf16);
+}
+
+// Valid columns of the 16 from j0.
+__device__ __forceinline__ int valid16(int64_t J, int64_t j0)
+{
+    return J - j0 >= 16 ? 16 : (J > j0 ? (int)(J - j0) : 0);
+}
+
+// One stage's operand: ROWS rows (or columns) of 64 k.  K-major: one box of
+// 64 k x ROWS rows.  MN-major: ROWS/64 boxes of 64 columns x 64 k-rows.
+template <int CG, int ROWS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int mn, int row0,
+                                             int k0, uint32_t bar, uint64_t policy)
+{
+    if (!mn) {
+        tma_load_2d<CG>(dst, map, k0, row0, bar, policy);
+    } else {
+#pragma unroll
+        for (int b = 0; b < (ROWS + 63) / 64; ++b)
+            tma_load_2d<CG>(dst + b * kMnBox, map, row0 + b * 64, k0, bar, policy);
+    }
+}
+
+// ---- pair kernel: 256 features x 256 tokens per CTA pair ---------------------------
+namespace pair {
+constexpr int kStages = 6;
+constexpr int kOperand = 128 * kBK * 2;  // 16 KB: this CTA's 128 rows of A, or of B
+constexpr int kStage = 2 * kOperand;
+constexpr int kTile = 256;
+constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, 128 columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kOffShared = kStages * kStage;
+constexpr int kSmemBytes = kOffShared + (int)sizeof(Shared) + 1024;
+static_assert(kSmemBytes <= 232448 && kStages <= kMaxStages, "shared memory of a CTA");
+
+struct Tile {
+    int ti, tj;
+};
+
+// Tile order: feature tiles in groups of a.group; group by group, every token
+// tile runs over the group's feature tiles.  The pairs running at one time
+// then cover about as many feature tiles as token tiles, which keeps the
+// slices of A and B that they read from DRAM and share through L2 few.
+__device__ __forceinline__ Tile tile_at(const LinearArgs &a, int64_t t, int tiles_i, int tiles_j)
+{
+    const int64_t full = (int64_t)a.group * tiles_j;
+    const int g = (int)(t / full);
+    const int64_t r = t - g * full;
+    const int left = tiles_i - g * a.group;
+    const int width = left < a.group ? left : a.group;
+    Tile c;
+    c.tj = (int)(r / width);
+    c.ti = g * a.group + (int)(r - (int64_t)c.tj * width);
+    return c;
+}
+}  // namespace pair
+
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ LinearArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;  // 1024-aligned for the 128B swizzle
+    Shared &sh = *reinterpret_cast<Shared *>(smem_raw + (base - raw) + pair::kOffShared);
+    volatile int *abort_flag = &sh.abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t unit = (int64_t)cluster_id_x();
+    const int64_t nunits = (int64_t)ncluster_x();
+    const int tiles_i = (int)((a.I + pair::kTile - 1) / pair::kTile);
+    const int tiles_j = (int)((a.J + pair::kTile - 1) / pair::kTile);
+    const int64_t total = (int64_t)tiles_i * tiles_j;
+    const int num_kb = (int)((a.K + kBK - 1) / kBK);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < pair::kStages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&sh.tmem_full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sh.tmem_empty[s]), 2 * pair::kEpiWarps);
+        }
+        ptx::mbar_init(ptx::smem_addr(&sh.mma_done), 1);
+        sh.abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&map_a);
+        prefetch_tensormap(&map_b);
+    }
+    if (warp == 1) {
+        tmem_alloc<2>(ptx::smem_addr(&sh.tmem_base), 512);
+        fence_before();
+    }
+    __syncthreads();
+    cluster_sync();  // the peer's barriers exist before anything signals them
+    fence_after();
+    const uint32_t tmem = sh.tmem_base;
+
+    if (warp == 0) {
+        // ===================== producer =====================================
+        const uint64_t pol = ptx::policy_evict_normal();
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int64_t t = unit; t < total && ok; t += nunits) {
+            const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
+            const int i0 = c.ti * pair::kTile + (int)rank * 128;
+            const int j0 = c.tj * pair::kTile + (int)rank * 128;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                const bool got = role_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1u,
+                                           a.wait_limit_ns, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const bool stall = a.inject_stall && unit == 0 && issued == 0;
+                if (lane == 0 && !stall) {  // test hook: the first stage is never armed
+                    const uint32_t local_full = ptx::smem_addr(&sh.full[stage]);
+                    const uint32_t bar = map_to_rank(local_full, 0);  // both CTAs' loads
+                    if (leader)
+                        ptx::mbar_arrive_expect_tx(local_full, 2 * pair::kStage);
+                    const uint32_t sa = base + stage * pair::kStage;
+                    load_operand<2, 128>(sa, &map_a, a.a_mn, i0, kb * kBK, bar, pol);
+                    load_operand<2, 128>(sa + pair::kOperand, &map_b, a.b_mn, j0, kb * kBK, bar, pol);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == pair::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            report_status(a.status, kStatusTimeout);
+        }
+        // drain: every load this warp issued has landed before the CTA may exit
+        if (leader) {
+            const int64_t pending = issued < pair::kStages ? issued : pair::kStages;
+            for (int64_t q = 0; q < pending; ++q) {
+                const int64_t idx = issued - 1 - q;
+                ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % pair::kStages]),
+                               (uint32_t)((idx / pair::kStages) & 1), kDrainLimitNs);
+            }
+        } else if (!ok && issued > 0) {
+            sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
+        }
+    } else if (warp == 1) {
+        // ===================== MMA issuer (leader CTA) ======================
+        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, 256);
+        const uint32_t step_a = a.a_mn ? UK * 128 : UK * 2, step_b = a.b_mn ? UK * 128 : UK * 2;
+        const uint32_t lbo_a = a.a_mn ? kMnBox : 16, lbo_b = a.b_mn ? kMnBox : 16;
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t nchunk = 0;  // chunks issued so far: accumulator nchunk & 1
+        bool issued_any = false;
+        bool ok = true;
+        for (int64_t t = unit; leader && t < total && ok; t += nunits) {
+            for (int kb = 0; kb < num_kb; ++kb) {
+                const int in_chunk = kb % a.chunk;
+                const int acc = (int)(nchunk & 1);
+                bool got = true;
+                if (in_chunk == 0) {
+                    got = role_wait(ptx::smem_addr(&sh.tmem_empty[acc]),
+                                    (uint32_t)((nchunk >> 1) & 1) ^ 1u, a.wait_limit_ns, abort_flag);
+                }
+                got = got && role_wait(ptx::smem_addr(&sh.full[stage]), phase, a.wait_limit_ns,
+                                       abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const bool last = in_chunk + 1 == a.chunk || kb + 1 == num_kb;
+                if (lane == 0) {
+                    const uint32_t sa = base + stage * pair::kStage;
+                    const uint32_t sb = sa + pair::kOperand;
+#pragma unroll
+                    for (int k = 0; k < kBK / UK; ++k)
+                        mma_f16<2>(tmem + (uint32_t)(acc * 256), smem_desc(sa + k * step_a, lbo_a, 1024),
+                                   smem_desc(sb + k * step_b, lbo_b, 1024), idesc,
+                                   (in_chunk | k) != 0 ? 1u : 0u);
+                    mma_commit<2>(ptx::smem_addr(&sh.empty[stage]));
+                    if (last)
+                        mma_commit<2>(ptx::smem_addr(&sh.tmem_full[acc]));
+                }
+                __syncwarp();
+                issued_any = true;
+                if (last)
+                    ++nchunk;
+                if (++stage == pair::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            report_status(a.status, kStatusTimeout);
+        }
+        // drain: all MMAs of this thread have completed before TMEM is freed
+        if (issued_any) {
+            if (lane == 0)
+                mma_commit_local<2>(ptx::smem_addr(&sh.mma_done));
+            __syncwarp();
+            ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
+        }
+    } else {
+        // ===================== epilogue (warps 2-9) =========================
+        const int q = warp & 3;              // TMEM lane quarter this warp may access
+        const int half = (warp - 2) >> 2;    // columns [half*128, half*128 + 128)
+        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+        const int chunks = (num_kb + a.chunk - 1) / a.chunk;
+        int64_t nchunk = 0;
+        bool ok = true;
+        for (int64_t t = unit; t < total && ok; t += nunits) {
+            const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
+            const int64_t i = (int64_t)c.ti * pair::kTile + (int)rank * 128 + q * 32 + lane;
+            const int64_t j0 = (int64_t)c.tj * pair::kTile + half * 128;
+            const float bias = EPI == kEpiForward ? load_bias(a, i) : 0.0f;
+            float sum[EPI == kEpiGradW ? 128 : 1];
+            if constexpr (EPI == kEpiGradW) {
+#pragma unroll
+                for (int u = 0; u < 128; ++u)
+                    sum[u] = 0.0f;
+            }
+            for (int h = 0; h < chunks; ++h, ++nchunk) {
+                const int acc = (int)(nchunk & 1);
+                const bool got = role_wait(ptx::smem_addr(&sh.tmem_full[acc]),
+                                           (uint32_t)((nchunk >> 1) & 1), a.wait_limit_ns, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t t_addr = t_lane + (uint32_t)(acc * 256);
+                if constexpr (EPI == kEpiGradW) {
+#pragma unroll
+                    for (int c16 = 0; c16 < 8; ++c16) {
+                        uint32_t r[16];
+                        tmem_ld16(t_addr + c16 * 16, r);
+                        tmem_wait16(r);
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            sum[c16 * 16 + u] += __uint_as_float(r[u]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c16 = 0; c16 < 8; ++c16) {
+                        uint32_t r[16];
+                        tmem_ld16(t_addr + c16 * 16, r);
+                        tmem_wait16(r);
+                        float v[16];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            v[u] = __uint_as_float(r[u]);
+                        const int n = valid16(a.J, j0 + c16 * 16);
+                        emit16<EPI>(a, i, j0 + c16 * 16, 1, n, v, bias);
+                        __syncwarp();
+                    }
+                }
+                // accumulator read: hand it back to the leader's MMA warp
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(map_to_rank(ptx::smem_addr(&sh.tmem_empty[acc]), 0));
+            }
+            if constexpr (EPI == kEpiGradW) {
+                if (ok) {
+#pragma unroll
+                    for (int c16 = 0; c16 < 8; ++c16) {
+                        float v[16];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            v[u] = sum[c16 * 16 + u];
+                        emit16<EPI>(a, i, j0 + c16 * 16, 1, valid16(a.J, j0 + c16 * 16), v, 0.0f);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            report_status(a.status, kStatusTimeout);
+        }
+    }
+
+    // ---- teardown ---------------------------------------------------------------
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // the leader's MMAs into the peer's TMEM and smem are done
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc<2>(tmem, 512);
+    }
+}
+
+// ---- split kernel: 128 features x BT tokens per cluster ------------------------------
+namespace split {
+constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
+constexpr int kA = 128 * kBK * 2;
+template <int BT>
+struct Geo {
+    static constexpr int kB = BT * kBK * 2;
+    static constexpr int kStage = kA + kB;
+    // about 100 KB of ring, so that two CTAs share an SM
+    static constexpr int kStages = BT == 16 ? 6 : BT == 32 ? 5 : BT == 64 ? 4 : 3;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kPartial = 128 * BT * 4;  // float32 partial tile, over the spent ring
+    static constexpr int kTmemCols = 2 * BT;       // two accumulators (a power of two >= 32)
+    static constexpr int kSmemBytes = kRing + (int)sizeof(Shared) + 1024;
+    static_assert(kPartial <= kRing && kStages <= kMaxStages && 2 * (kSmemBytes + 1024) <= 233472,
+                  "shared memory of a CTA");
+};
+}  // namespace split
+
+template <int EPI, int BT>
+__global__ void __launch_bounds__(split::kThreads, 2)
+    split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ LinearArgs a)
+{
+    using G = split::Geo<BT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    Shared &sh = *reinterpret_cast<Shared *>(smem + G::kRing);
+    volatile int *abort_flag = &sh.abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int parts = (int)cluster_size();
+    const int64_t tile = (int64_t)cluster_id_x();
+    const int tiles_i = (int)((a.I + 127) / 128);
+    const int tj = (int)(tile / tiles_i);
+    const int ti = (int)(tile - (int64_t)tj * tiles_i);
+    const int num_kb = (int)((a.K + kBK - 1) / kBK);
+    const int kb0 = (int)((int64_t)num_kb * rank / parts);
+    const int kb1 = (int)((int64_t)num_kb * (rank + 1) / parts);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&sh.tmem_full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sh.tmem_empty[s]), 4);
+        }
+        ptx::mbar_init(ptx::smem_addr(&sh.mma_done), 1);
+        sh.abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&map_a);
+        prefetch_tensormap(&map_b);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(ptx::smem_addr(&sh.tmem_base), G::kTmemCols);
+        fence_before();
+    }
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sh.tmem_base;
+
+    const int q = warp & 3;  // epilogue: TMEM lane quarter
+    const int64_t i = (int64_t)ti * 128 + q * 32 + lane;
+    const int64_t jt = (int64_t)tj * BT;
+    const float bias = EPI == kEpiForward && warp >= 2 ? load_bias(a, i) : 0.0f;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ===================== producer =====================================
+        const uint64_t pol = ptx::policy_evict_normal();
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const bool got = role_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1u,
+                                       a.wait_limit_ns, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            const bool stall = a.inject_stall && tile == 0 && rank == 0 && issued == 0;
+            if (lane == 0 && !stall) {  // test hook: the first stage is never armed
+                const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
+                ptx::mbar_arrive_expect_tx(bar, G::kStage);
+                const uint32_t sa = base + stage * G::kStage;
+                load_operand<1, 128>(sa, &map_a, a.a_mn, ti * 128, kb * kBK, bar, pol);
+                load_operand<1, BT>(sa + split::kA, &map_b, a.b_mn, tj * BT, kb * kBK, bar, pol);
+            }
+            __syncwarp();
+            ++issued;
+            if (++stage == G::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            report_status(a.status, kStatusTimeout);
+        }
+        const int pending = issued < G::kStages ? issued : G::kStages;
+        for (int d = 0; d < pending; ++d) {
+            const int idx = issued - 1 - d;
+            ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
+                           (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
+        }
+    } else if (warp == 1) {
+        // ===================== MMA issuer ===================================
+        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 128, BT);
+        const uint32_t step_a = a.a_mn ? UK * 128 : UK * 2, step_b = a.b_mn ? UK * 128 : UK * 2;
+        const uint32_t lbo_a = a.a_mn ? kMnBox : 16, lbo_b = a.b_mn ? kMnBox : 16;
+        int stage = 0;
+        uint32_t phase = 0;
+        int nchunk = 0;
+        bool issued_any = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const int in_chunk = (kb - kb0) % a.chunk;
+            const int acc = nchunk & 1;
+            bool got = true;
+            if (in_chunk == 0)
+                got = role_wait(ptx::smem_addr(&sh.tmem_empty[acc]), (uint32_t)((nchunk >> 1) & 1) ^ 1u,
+                                a.wait_limit_ns, abort_flag);
+            got = got && role_wait(ptx::smem_addr(&sh.full[stage]), phase, a.wait_limit_ns, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            const bool last = in_chunk + 1 == a.chunk || kb + 1 == kb1;
+            if (lane == 0) {
+                const uint32_t sa = base + stage * G::kStage;
+                const uint32_t sb = sa + split::kA;
+#pragma unroll
+                for (int k = 0; k < kBK / UK; ++k)
+                    mma_f16<1>(tmem + (uint32_t)(acc * BT), smem_desc(sa + k * step_a, lbo_a, 1024),
+                               smem_desc(sb + k * step_b, lbo_b, 1024), idesc,
+                               (in_chunk | k) != 0 ? 1u : 0u);
+                mma_commit<1>(ptx::smem_addr(&sh.empty[stage]));
+                if (last)
+                    mma_commit<1>(ptx::smem_addr(&sh.tmem_full[acc]));
+            }
+            __syncwarp();
+            issued_any = true;
+            if (last)
+                ++nchunk;
+            if (++stage == G::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            report_status(a.status, kStatusTimeout);
+        }
+        if (issued_any) {
+            if (lane == 0)
+                mma_commit_local<1>(ptx::smem_addr(&sh.mma_done));
+            __syncwarp();
+            ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
+        }
+    } else {
+        // ===================== epilogue (warps 2-5) =========================
+        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
+        float *partial = reinterpret_cast<float *>(smem) + q * 32 + lane;  // [column][feature]
+        const int chunks = (kb1 - kb0 + a.chunk - 1) / a.chunk;
+        float sum[EPI == kEpiGradW ? BT : 1];
+        if constexpr (EPI == kEpiGradW) {
+#pragma unroll
+            for (int u = 0; u < BT; ++u)
+                sum[u] = 0.0f;
+        }
+        for (int h = 0; h < chunks; ++h) {
+            const int acc = h & 1;
+            const bool got = role_wait(ptx::smem_addr(&sh.tmem_full[acc]), (uint32_t)((h >> 1) & 1),
+                                       a.wait_limit_ns, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            if constexpr (EPI == kEpiGradW) {
+#pragma unroll
+                for (int c16 = 0; c16 < BT / 16; ++c16) {
+                    uint32_t r[16];
+                    tmem_ld16(t_lane + (uint32_t)(acc * BT + c16 * 16), r);
+                    tmem_wait16(r);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        sum[c16 * 16 + u] += __uint_as_float(r[u]);
+                }
+            } else {  // one chunk: every load and MMA of this CTA is done, the ring is free
+#pragma unroll 1
+                for (int c16 = 0; c16 < BT / 16; ++c16) {
+                    uint32_t r[16];
+                    tmem_ld16(t_lane + (uint32_t)(acc * BT + c16 * 16), r);
+                    tmem_wait16(r);
+                    if (parts > 1) {
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            partial[(c16 * 16 + u) * 128] = __uint_as_float(r[u]);
+                    } else {
+                        float v[16];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            v[u] = __uint_as_float(r[u]);
+                        emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(a.J, jt + c16 * 16), v, bias);
+                        __syncwarp();
+                    }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(ptx::smem_addr(&sh.tmem_empty[acc]));
+        }
+        if constexpr (EPI == kEpiGradW) {
+            if (ok) {  // past the last chunk every load and MMA of this CTA is done
+#pragma unroll
+                for (int c16 = 0; c16 < BT / 16; ++c16) {
+                    if (parts > 1) {
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            partial[(c16 * 16 + u) * 128] = sum[c16 * 16 + u];
+                    } else {
+                        float v[16];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            v[u] = sum[c16 * 16 + u];
+                        emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(a.J, jt + c16 * 16), v, 0.0f);
+                    }
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            report_status(a.status, kStatusTimeout);
+        }
+    }
+
+    __syncthreads();
+    if (parts > 1) {
+        // the cluster's partial tiles, added in rank order; CTA `rank` takes
+        // columns rank, rank + parts, ...
+        cluster_sync();
+        if (warp >= 2 && ok) {
+            const uint32_t mine = base + (uint32_t)(q * 32 + lane) * 4;
+            const int64_t left = a.J - jt;  // valid columns of the tile
+            const int cols = left < BT ? (int)left : BT;
+#pragma unroll 1
+            for (int c0 = rank; c0 < cols; c0 += 16 * parts) {
+                const int n = (cols - c0 + parts - 1) / parts;
+                float v[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = 0.0f;
+#pragma unroll 1
+                for (int s = 0; s < parts; ++s) {
+                    const uint32_t src = map_to_rank(mine, (uint32_t)s);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        if (u < n)
+                            v[u] += ld_cluster_f32(src + (uint32_t)(c0 + u * parts) * 512);
+                }
+                emit16<EPI>(a, i, jt + c0, parts, n < 16 ? n : 16, v, bias);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while its partial tile may still be read
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc<1>(tmem, G::kTmemCols);
+    }
+}
+
+// ---- an empty contraction: the epilogue of zero sums ------------------------------------
+template <int EPI>
+__global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ LinearArgs a)
+{
+    const int64_t blocks_i = (a.I + 31) / 32;
+    const int64_t groups = blocks_i * ((a.J + 15) / 16);
+    const int64_t step = (int64_t)gridDim.x * 8;
+    for (int64_t g = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); g < groups; g += step) {
+        const int64_t i = (g % blocks_i) * 32 + (threadIdx.x & 31);
+        const int64_t j0 = g / blocks_i * 16;
+        float v[16] = {};
+        emit16<EPI>(a, i, j0, 1, valid16(a.J, j0), v, load_bias(a, i));
+    }
+}
+
+// ---- column sums (bias gradient) -----------------------------------------------------
+// A cluster of kSumParts CTAs owns 64 columns; its CTAs split the rows and
+// each reads whole 128-byte row pieces (8 columns per thread, 32 rows at a
+// time), sums in registers, joins its 32 row groups in shared memory and the
+// cluster's 8 sums through distributed shared memory, in a fixed order.
+// Bound: the read of dZ.
+constexpr int kSumParts = 8;
+
+__global__ void __cluster_dims__(kSumParts, 1, 1) __launch_bounds__(256)
+    colsum_kernel(const __grid_constant__ ColSumArgs a)
+{
+    __shared__ float part[32][65];
+    __shared__ float total[64];
+    const int rank = (int)cluster_ctarank();
+    const int64_t i0 = (int64_t)cluster_id_x() * 64;
+    const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+    const int64_t row0 = a.J * rank / kSumParts, row1 = a.J * (rank + 1) / kSumParts;
+    const int64_t col = i0 + c * 8;
+    float s[8] = {};
+    if (col < a.I) {  // a pitch is whole 16-byte units, so a started unit is inside the row's pitch
+        const uint4 *x = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.x) + col);
+        const int64_t ld = a.ldx / 8;
+        const int64_t n = row1 - row0;
+        const bool whole = col + 8 <= a.I;
+#pragma unroll 4
+        for (int64_t k = r; k < n; k += 32) {
+            uint16_t h[8];
+            if (whole) {
+                *reinterpret_cast<uint4 *>(h) = x[(row0 + k) * ld];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    h[u] = col + u < a.I
+                               ? reinterpret_cast<const uint16_t *>(a.x)[(row0 + k) * a.ldx + col + u]
+                               : (uint16_t)0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                s[u] += a.is_bf16 ? __uint_as_float((uint32_t)h[u] << 16)
+                                  : __half2float(__ushort_as_half(h[u]));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        part[r][c * 8 + u] = s[u];
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        float t = 0.0f;
+        for (int k = 0; k < 32; ++k)
+            t += part[k][threadIdx.x];
+        total[threadIdx.x] = t;
+    }
+    __syncthreads();
+    cluster_sync();
+    const int64_t i = i0 + threadIdx.x;
+    if (rank == 0 && threadIdx.x < 64 && i < a.I) {
+        float t = 0.0f;
+        for (int p = 0; p < kSumParts; ++p)
+            t += ld_cluster_f32(map_to_rank(ptx::smem_addr(&total[threadIdx.x]), (uint32_t)p));
+        if (a.out_f32) {
+            float *o = reinterpret_cast<float *>(a.out) + i;
+            *o = a.accumulate ? *o + t : t;
+        } else {
+            store16(a.out, i, a.accumulate ? load16(a.out, i, a.is_bf16) + t : t, a.is_bf16);
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+}
+
+// ---- activation backward: dz = dy * act'(z) --------------------------------------------
+// V elements per thread and step (8: 16-byte accesses when every pointer and
+// pitch allows them, else 1).  Bound: two reads and a write of HBM.
+template <int V>
+__global__ void __launch_bounds__(256) act_backward_kernel(const __grid_constant__ ActBackwardArgs a)
+{
+    const int64_t units = (a.N + V - 1) / V;
+    const int64_t total = a.M * units;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += step) {
+        const int64_t m = t / units, n = (t - m * units) * V;
+        const uint16_t *dy = reinterpret_cast<const uint16_t *>(a.dy) + m * a.lddy + n;
+        const uint16_t *z = reinterpret_cast<const uint16_t *>(a.z) + m * a.ldz + n;
+        uint16_t *dz = reinterpret_cast<uint16_t *>(a.dz) + m * a.lddz + n;
+        uint16_t hy[V], hz[V];
+        const bool whole = n + V <= a.N;
+        if (V == 8 && whole) {
+            *reinterpret_cast<uint4 *>(hy) = *reinterpret_cast<const uint4 *>(dy);
+            *reinterpret_cast<uint4 *>(hz) = *reinterpret_cast<const uint4 *>(z);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                hy[u] = n + u < a.N ? dy[u] : (uint16_t)0;
+                hz[u] = n + u < a.N ? z[u] : (uint16_t)0;
+            }
+        }
+        with_act(a.act, [&](auto c) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                float v[1];
+                v[0] = load16(hy, u, a.is_bf16) * act_slope<decltype(c)::value>(load16(hz, u, a.is_bf16));
+                store16(hy, u, v[0], a.is_bf16);
+            }
+        });
+        if (V == 8 && whole) {
+            *reinterpret_cast<uint4 *>(dz) = *reinterpret_cast<const uint4 *>(hy);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+                if (n + u < a.N)
+                    dz[u] = hy[u];
+        }
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+
+int current_device()
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        dev = 0;
+    return dev;
+}
+
+// Dynamic shared memory of a kernel, set once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::once_flag *once, cudaError_t *result)
+{
+    const int dev = current_device();
+    std::call_once(once[dev], [&] {
+        result[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return result[dev];
+}
+
+bool operand_map(CUtensorMap *map, const LinearArgs &a, const void *p, int64_t rows, int64_t ld, int mn,
+                 uint32_t box_rows)
+{
+    const CUtensorMapDataType dt =
+        a.is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint64_t strides[1] = {(uint64_t)ld * 2};
+    if (mn) {
+        const uint64_t dims[2] = {(uint64_t)rows, (uint64_t)a.K};
+        const uint32_t box[2] = {64, kBK};
+        return encode_map(map, dt, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)rows};
+    const uint32_t box[2] = {kBK, box_rows};
+    return encode_map(map, dt, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int EPI>
+cudaError_t launch_pair(const LinearArgs &args, cudaStream_t s, const char **why)
+{
+    static std::once_flag once[kMaxDevices], once_res[kMaxDevices];
+    static cudaError_t result[kMaxDevices];
+    static int resident_by_dev[kMaxDevices];
+    cudaError_t e = allow_smem(pair_kernel<EPI>, pair::kSmemBytes, once, result);
+    if (e != cudaSuccess) {
+        *why = "setting the shared-memory size of the linear kernel";
+        return e;
+    }
+    const int dev = current_device();
+    std::call_once(once_res[dev], [&] {
+        int resident = 0;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(pair::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = pair::kSmemBytes;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&resident, pair_kernel<EPI>, &cfg) != cudaSuccess)
+            resident = 0;
+        (void)cudaGetLastError();
+        resident_by_dev[dev] = resident;
+    });
+    CUtensorMap map_a, map_b;
+    if (!operand_map(&map_a, args, args.a, args.I, args.lda, args.a_mn, 128) ||
+        !operand_map(&map_b, args, args.b, args.J, args.ldb, args.b_mn, 128)) {
+        *why = "encoding the operands' tensor maps";
+        return cudaErrorInvalidValue;
+    }
+    LinearArgs a = args;
+    const int64_t tiles_i = (a.I + pair::kTile - 1) / pair::kTile;
+    const int64_t tiles_j = (a.J + pair::kTile - 1) / pair::kTile;
+    // feature tiles in equal groups of at most 8: 76 pairs cover about 8 x 9 tiles
+    const int64_t groups = (tiles_i + 7) / 8;
+    a.group = (int)((tiles_i + groups - 1) / groups);
+    const int resident = resident_by_dev[dev] > 0 ? resident_by_dev[dev] : kSMs / 2;
+    const int64_t clusters = gg_min64(resident, tiles_i * tiles_j);
+    pair_kernel<EPI><<<(int)(2 * clusters), pair::kThreads, pair::kSmemBytes, s>>>(map_a, map_b, a);
+    return cudaGetLastError();
+}
+
+template <int EPI, int BT>
+cudaError_t launch_split(const LinearArgs &a, int parts, cudaStream_t s, const char **why)
+{
+    using G = split::Geo<BT>;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t result[kMaxDevices];
+    cudaError_t e = allow_smem(split_kernel<EPI, BT>, G::kSmemBytes, once, result);
+    if (e != cudaSuccess) {
+        *why = "setting the shared-memory size of the linear kernel";
+        return e;
+    }
+    CUtensorMap map_a, map_b;
+    if (!operand_map(&map_a, a, a.a, a.I, a.lda, a.a_mn, 128) ||
+        !operand_map(&map_b, a, a.b, a.J, a.ldb, a.b_mn, BT)) {
+        *why = "encoding the operands' tensor maps";
+        return cudaErrorInvalidValue;
+    }
+    const int64_t tiles = ((a.I + 127) / 128) * ((a.J + BT - 1) / BT);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(tiles * parts), 1, 1);
+    cfg.blockDim = dim3(split::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = G::kSmemBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, split_kernel<EPI, BT>, map_a, map_b, a);
+}
+
+template <int EPI>
+cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s, const char **why)
+{
+    if (a.K == 0) {
+        const int64_t groups = ((a.I + 31) / 32) * ((a.J + 15) / 16);
+        empty_kernel<EPI><<<(int)gg_min64((groups + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    if (p.kernel == GG_LINEAR_PAIR)
+        return launch_pair<EPI>(a, s, why);
+    switch (p.bt) {
+    case 16:
+        if constexpr (EPI != kEpiGradW)
+            return launch_split<EPI, 16>(a, p.split, s, why);
+        break;
+    case 32:
+        if constexpr (EPI != kEpiGradW)
+            return launch_split<EPI, 32>(a, p.split, s, why);
+        break;
+    case 64: return launch_split<EPI, 64>(a, p.split, s, why);
+    case 128: return launch_split<EPI, 128>(a, p.split, s, why);
+    }
+    *why = "no such tile";
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+// Which kernel, tile and split.  Token tiles are the smallest that hold all
+// tokens, 128 at most (64 at least for a weight gradient, whose MN-major B
+// comes in boxes of 64).  The split fills the GPU's SMs: as many CTAs per tile
+// as tiles leave room for, 8 (a portable cluster) and one k-block each at most.
+// The pair kernel takes a product whose estimated time there is shorter: waves
+// of 256 x 256 tiles over 76 pairs at 4 x 128 cycles a k-block, against waves of
+// the split kernel's CTAs (two per SM) at 4 x max(BT / 2, 32) cycles.
+LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
+{
+    LinearPlan p{GG_LINEAR_NONE, 0, 0};
+    if (I <= 0 || J <= 0)
+        return p;
+    if (K <= 0)
+        return p;
+    const int64_t num_kb = (K + kBK - 1) / kBK;
+    int bt = epi == kEpiGradW ? 64 : 16;
+    while (bt < 128 && bt < J)
+        bt *= 2;
+    const int64_t tiles = ((I + 127) / 128) * ((J + bt - 1) / bt);
+    int64_t parts = kSMs / tiles;
+    parts = parts < 1 ? 1 : (parts > 8 ? 8 : parts);
+    parts = gg_min64(parts, num_kb);
+    p.bt = bt;
+    p.split = (int)parts;
+    const int64_t pair_tiles = ((I + 255) / 256) * ((J + 255) / 256);
+    const int64_t pair_cost = (pair_tiles + kSMs / 2 - 1) / (kSMs / 2) * num_kb * 512;
+    const int64_t split_cost = (tiles * parts + kSMs - 1) / kSMs * ((num_kb + parts - 1) / parts) * 4 *
+                               (bt / 2 > 32 ? bt / 2 : 32) * 5 / 4;
+    p.kernel = path != 0 ? path : (pair_cost < split_cost ? GG_LINEAR_PAIR : GG_LINEAR_SPLIT);
+    return p;
+}
+
+cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, cudaStream_t s,
+                          const char **why)
+{
+    if (args.I == 0 || args.J == 0)
+        return cudaSuccess;
+    if (args.K > 0 && !tensor_maps_available()) {
+        *why = "cuTensorMapEncodeTiled is not available";
+        return cudaErrorNotSupported;
+    }
+    LinearArgs a = args;
+    a.chunk = epi == kEpiGradW ? kChunk : 1 << 30;
+    switch (epi) {
+    case kEpiForward: return launch_epi<kEpiForward>(a, p, s, why);
+    case kEpiGradIn: return launch_epi<kEpiGradIn>(a, p, s, why);
+    default: return launch_epi<kEpiGradW>(a, p, s, why);
+    }
+}
+
+cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t s)
+{
+    const int64_t clusters = (a.I + 63) / 64;
+    colsum_kernel<<<(unsigned)(clusters * kSumParts), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_act_backward(const ActBackwardArgs &a, cudaStream_t s)
+{
+    const uint64_t bits = reinterpret_cast<uint64_t>(a.dy) | reinterpret_cast<uint64_t>(a.z) |
+                          reinterpret_cast<uint64_t>(a.dz) |
+                          (uint64_t)((a.lddy | a.ldz | a.lddz) * 2);
+    const bool wide = bits % 16 == 0;
+    const int64_t total = a.M * (wide ? (a.N + 7) / 8 : a.N);
+    const int grid = (int)gg_min64((total + 255) / 256, kSMs * 8);
+    if (wide)
+        act_backward_kernel<8><<<grid, 256, 0, s>>>(a);
+    else
+        act_backward_kernel<1><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace gg

@@ -413,6 +413,114 @@ gg_status gg_matmul_all_gather_check(const gg_heap *heap, int rank, const void *
                                      gg_tile tile, int comm_programs, gg_group group);
 
 /* ---------------------------------------------------------------------------
+ * Operators of the step around the gathered matmul.  The pages have no
+ * counterpart: they end at the gather.  A weight held as row blocks by the
+ * ranks of a heap is gathered (gg_all_gather), applied (gg_linear), turned
+ * into a loss and the logits' gradient (gg_policy_loss), differentiated
+ * (gg_linear_backward) and updated, row block by row block (gg_adamw).
+ *
+ * All of them run on the current device, asynchronously on `stream`; they
+ * allocate nothing, keep nothing between calls and give the same bits for the
+ * same inputs.  Matrices are row-major with a row pitch (ld) in elements.
+ * Sums and statistics are held in float32.  Sizes must be below 2^31 each;
+ * offsets are 64-bit.  An output may overlap no other argument's elements,
+ * unless a call says so (GG_ERR_INVALID_ARG); columns between a row's length
+ * and its pitch are never written.
+ * ------------------------------------------------------------------------- */
+
+/* Activations: max(z, 0); z Phi(z); z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;
+ * z / (1 + exp(-z)). */
+typedef enum {
+    GG_ACT_NONE = 0, GG_ACT_RELU = 1, GG_ACT_GELU = 2, GG_ACT_GELU_TANH = 3, GG_ACT_SILU = 4
+} gg_activation;
+
+/* How a weight lies in memory: K x N rows (as gg_matmul_all_gather's B) or
+ * N x K rows (one row per output feature: what gathering row blocks of
+ * features gives). */
+typedef enum { GG_WEIGHT_KN = 0, GG_WEIGHT_NK = 1 } gg_weight_layout;
+
+/* Kernel of a product: GG_LINEAR_AUTO by sizes; GG_LINEAR_SPLIT one CTA per
+ * 128-feature tile and share of the contraction, joined across a cluster (few
+ * tokens, few tiles); GG_LINEAR_PAIR persistent CTA pairs on 256 x 256 tiles.
+ * The values differ by the order of float32 sums only. */
+typedef enum {
+    GG_LINEAR_AUTO = 0, GG_LINEAR_SPLIT = 1, GG_LINEAR_PAIR = 2
+} gg_linear_path;
+#define GG_LINEAR_NONE 0 /* gg_linear_check: no product kernel runs (an empty size) */
+
+/* ---------------------------------------------------------------------------
+ * gg_linear — Z = X W + bias, Y = act(Z) + residual.
+ * X: M x K; W: K x N or N x K (layout); bias: N elements of bias_dtype (`dtype`
+ * or GG_F32), or NULL; residual: M x N or NULL, may be Y itself (same pointer
+ * and pitch); Y: M x N; z: M x N, Z rounded to `dtype` for the backward pass,
+ * or NULL.  dtype: GG_F16 or GG_BF16 (else GG_ERR_UNSUPPORTED), the type of X,
+ * W, residual, Y and z.  Y is rounded once, to nearest even.
+ * Alignment (GG_ERR_ALIGNMENT): X and W 16-byte aligned, ldx and ldw multiples
+ * of 8 (tensor maps); every other argument at its element's alignment, any
+ * pitch.  M, N and K may be any size: M == 0 or N == 0 launches nothing;
+ * K == 0 gives act(bias) + residual and reads neither X nor W.
+ * dev_status: as for gg_all_gather (GG_ERR_TIMEOUT when a bounded wait gave
+ * up; Y and z are then undefined).
+ * ------------------------------------------------------------------------- */
+gg_status gg_linear(const void *X, int64_t ldx, const void *W, int64_t ldw, gg_weight_layout layout,
+                    const void *bias, gg_dtype bias_dtype, gg_activation act, const void *residual,
+                    int64_t ldr, void *Y, int64_t ldy, void *z, int64_t ldz, int64_t M, int64_t N,
+                    int64_t K, gg_dtype dtype, int *dev_status, gg_stream_t stream,
+                    gg_linear_path path);
+
+/* Validate a gg_linear call exactly as the launching call does and launch
+ * nothing; *chosen (nullable) receives GG_LINEAR_SPLIT, GG_LINEAR_PAIR or
+ * GG_LINEAR_NONE. */
+gg_status gg_linear_check(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                          gg_weight_layout layout, const void *bias, gg_dtype bias_dtype,
+                          gg_activation act, const void *residual, int64_t ldr, const void *Y,
+                          int64_t ldy, const void *z, int64_t ldz, int64_t M, int64_t N, int64_t K,
+                          gg_dtype dtype, gg_linear_path path, int *chosen);
+
+/* ---------------------------------------------------------------------------
+ * gg_linear_backward — gradients of Z = X W + bias, given dZ (M x N):
+ *   dX = dZ W^T, M x K, of type `dtype`; with z_in (M x K, the Z that X =
+ *     act_in(z_in) came from, pitch ldzin) the product is multiplied by
+ *     act_in'(z_in) before its one rounding, which makes dX the dZ of the
+ *     layer below (relu's slope at 0 is 0).  dX may be z_in itself (same
+ *     pointer and pitch).
+ *   dW = X^T dZ in W's layout (pitch lddw) and dbias = the column sums of dZ,
+ *     both of grad_dtype (`dtype` or GG_F32); accumulate != 0 adds them to
+ *     what dW and dbias hold.  Float32 gradients are summed over the tokens
+ *     in chunks of 512, added in float32 with round-to-nearest.
+ * Any of dX, dW and dbias may be NULL; X is read for dW only, W for dX only,
+ * and may be NULL otherwise.
+ * Alignment: dZ, X and W 16-byte aligned with pitches that are multiples of 8,
+ * as far as they are read; the others any.  M == 0 gives zero sums (dW and
+ * dbias are cleared, or kept when accumulating); N == 0 a zero dX.
+ * One launch per gradient asked for, on `stream`.
+ * ------------------------------------------------------------------------- */
+gg_status gg_linear_backward(const void *dZ, int64_t lddz, const void *X, int64_t ldx, const void *W,
+                             int64_t ldw, gg_weight_layout layout, const void *z_in, int64_t ldzin,
+                             gg_activation act_in, void *dX, int64_t lddx, void *dW, int64_t lddw,
+                             void *dbias, gg_dtype grad_dtype, int accumulate, int64_t M, int64_t N,
+                             int64_t K, gg_dtype dtype, int *dev_status, gg_stream_t stream,
+                             gg_linear_path path);
+
+/* Validate a gg_linear_backward call exactly as the launching call does and
+ * launch nothing; *chosen_dx and *chosen_dw (nullable) receive the kernels of
+ * the two products. */
+gg_status gg_linear_backward_check(const void *dZ, int64_t lddz, const void *X, int64_t ldx,
+                                   const void *W, int64_t ldw, gg_weight_layout layout,
+                                   const void *z_in, int64_t ldzin, gg_activation act_in,
+                                   const void *dX, int64_t lddx, const void *dW, int64_t lddw,
+                                   const void *dbias, gg_dtype grad_dtype, int accumulate, int64_t M,
+                                   int64_t N, int64_t K, gg_dtype dtype, gg_linear_path path,
+                                   int *chosen_dx, int *chosen_dw);
+
+/* gg_act_backward — dz = dy * act'(z), M x N of type `dtype` (GG_F16 or
+ * GG_BF16), any alignment and pitch: the dZ of a layer whose output Y goes
+ * elsewhere than into another linear layer.  dz may be dy or z itself. */
+gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz, void *dz,
+                          int64_t lddz, gg_activation act, int64_t M, int64_t N, gg_dtype dtype,
+                          gg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Bounded waits.  Every wait of a kernel on an mbarrier gives up after this
  * many nanoseconds of wall time (default 2e9), stores GG_ERR_TIMEOUT in the
  * call's dev_status, drains the copies it has in flight and returns.  Applies
