@@ -24,8 +24,8 @@ from ._lib import (GG_AG_AUTO, GG_AG_BULK, GG_AG_TMA, GG_AG_VECTOR, GG_BF16, GG_
                    GG_CLAIM_ALWAYS, GG_CLAIM_AUTO, GG_CLAIM_NEVER, GG_MAX_WORLD, GG_OK,
                    GG_WORKSPACE_SLOT_BYTES,
                    GG_ACT_GELU, GG_ACT_GELU_TANH, GG_ACT_NONE, GG_ACT_RELU, GG_ACT_SILU,
-                   GG_LINEAR_AUTO, GG_LINEAR_PAIR, GG_LINEAR_SPLIT, GG_WEIGHT_KN, GG_WEIGHT_NK,
-                   GGError, Group, Tile, check, lib, LIB_PATH)
+                   GG_ADAMW_BLOCK, GG_LINEAR_AUTO, GG_LINEAR_PAIR, GG_LINEAR_SPLIT, GG_WEIGHT_KN, GG_WEIGHT_NK,
+                   AdamwTensor, GGError, Group, Tile, check, lib, LIB_PATH)
 
 __all__ = [
     "heap_create", "heap_wrap", "heap_bases", "heap_info", "heap_destroy", "heap_set_workspace",
@@ -33,7 +33,8 @@ __all__ = [
     "all_gather_check", "all_gather_grouped", "all_gather_partitioned", "all_to_all",
     "collective_check", "matmul_all_gather", "matmul_all_gather_check", "matmul_all_gather_plan",
     "linear", "linear_check", "linear_backward", "linear_backward_check", "act_backward",
-    "ACTIVATIONS", "WEIGHT_LAYOUTS", "LINEAR_PATHS",
+    "policy_loss", "policy_loss_check", "adamw", "adamw_check", "adamw_tensors", "AdamwTensors",
+    "ADAMW_BLOCK", "ACTIVATIONS", "WEIGHT_LAYOUTS", "LINEAR_PATHS",
     "set_claim_policy",
     "get_claim_policy", "CLAIM_POLICIES", "set_store_policy", "get_store_policy",
     "STORE_POLICIES", "set_wait_limit_ns",
@@ -51,6 +52,7 @@ ACTIVATIONS = {"none": GG_ACT_NONE, "relu": GG_ACT_RELU, "gelu": GG_ACT_GELU,
                "gelu_tanh": GG_ACT_GELU_TANH, "silu": GG_ACT_SILU}
 WEIGHT_LAYOUTS = {"kn": GG_WEIGHT_KN, "nk": GG_WEIGHT_NK}     # rows of K x N, or of N x K
 LINEAR_PATHS = {"auto": GG_LINEAR_AUTO, "split": GG_LINEAR_SPLIT, "pair": GG_LINEAR_PAIR}
+ADAMW_BLOCK = GG_ADAMW_BLOCK      # elements that share one scale of 8-bit optimizer states
 CLAIM_POLICIES = {"auto": GG_CLAIM_AUTO, "always": GG_CLAIM_ALWAYS, "never": GG_CLAIM_NEVER}
 STORE_POLICIES = {"plain": 0, "evict_first": 1}  # GG_STORE_PLAIN, GG_STORE_EVICT_FIRST
 
@@ -321,6 +323,80 @@ def act_backward(dy, lddy: int, z, ldz: int, dz, lddz: int, act: str, M: int, N:
     """dz = dy * act'(z) (gg_act_backward)."""
     check(lib.gg_act_backward(_ptr(dy), lddy, _ptr(z), ldz, _ptr(dz), lddz, ACTIVATIONS[act], M, N,
                               _dtype(dtype), _stream(stream)))
+
+
+def policy_loss(logits, ld: int, target, old_logp, ref_logp, advantage, weight, T: int, V: int, dtype,
+                stats, logp_out, dlogits, ldd: int, inv_temperature: float = 1.0,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                grad_scale: float = 1.0, status=None, stream=None) -> None:
+    """Clipped policy loss with a KL term, its statistics and the logits'
+    gradient (gg_policy_loss); dlogits may be the logits themselves, or None."""
+    check(lib.gg_policy_loss(_ptr(logits), ld, _ptr(target), _ptr(old_logp), _ptr(ref_logp),
+                             _ptr(advantage), _ptr(weight), T, V, _dtype(dtype), inv_temperature,
+                             clip_low, clip_high, kl_coef, grad_scale, _ptr(stats), _ptr(logp_out),
+                             _ptr(dlogits), ldd, _ptr(status), _stream(stream)))
+
+
+def policy_loss_check(logits, ld: int, target, old_logp, ref_logp, advantage, weight, T: int, V: int,
+                      dtype, stats, logp_out, dlogits, ldd: int, inv_temperature: float = 1.0,
+                      clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                      grad_scale: float = 1.0) -> None:
+    """Validate without launching."""
+    check(lib.gg_policy_loss_check(_ptr(logits), ld, _ptr(target), _ptr(old_logp), _ptr(ref_logp),
+                                   _ptr(advantage), _ptr(weight), T, V, _dtype(dtype),
+                                   inv_temperature, clip_low, clip_high, kl_coef, grad_scale,
+                                   _ptr(stats), _ptr(logp_out), _ptr(dlogits), ldd))
+
+
+class AdamwTensors:
+    """The tensors of an AdamW step, described once for all steps (host memory
+    only): a ctypes array of ``gg_adamw_tensor``.  Holds on to the tensors."""
+
+    def __init__(self, array, keep):
+        self.array, self.count, self.keep = array, len(array), keep
+
+
+def adamw_tensors(tensors, state_bits: int = 32) -> AdamwTensors:
+    """Describe tensors for ``adamw``: dicts of contiguous torch tensors under
+    "param", "grad", "m", "v", and, as far as they exist, "m_scale" and
+    "v_scale" (8-bit states) and "copy".  8-bit states are uint8 or
+    float8_e4m3fn tensors with a float32 scale per ADAMW_BLOCK elements."""
+    array = (AdamwTensor * len(tensors))()
+    for a, t in zip(array, tensors):
+        n = t["param"].numel()
+        a.n, a.state_bits = n, state_bits
+        a.param_dtype, a.grad_dtype = _dtype(t["param"].dtype), _dtype(t["grad"].dtype)
+        for k in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy"):
+            x = t.get(k)
+            if x is None:
+                continue
+            want = -(-n // ADAMW_BLOCK) if k.endswith("_scale") else n
+            if not x.is_contiguous() or x.numel() != want:
+                raise ValueError(f"{k}: a contiguous tensor of {want} elements is needed")
+            size = {"m": state_bits // 8, "v": state_bits // 8}.get(k, 4 if k.endswith("_scale") else None)
+            if size is not None and x.element_size() != size:
+                raise ValueError(f"{k}: elements of {size} bytes are needed")
+            setattr(a, k, _ptr(x))
+        if t.get("copy") is not None:
+            a.copy_dtype = _dtype(t["copy"].dtype)
+    return AdamwTensors(array, list(tensors))
+
+
+def adamw(tensors: AdamwTensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+          eps: float = 1e-8, weight_decay: float = 0.01, grad_scale=None, seed: int = 0,
+          stream=None) -> None:
+    """One AdamW step over all tensors (gg_adamw); ``step`` counts from 1.
+    ``grad_scale``: a device float the gradients are multiplied by, or None."""
+    check(lib.gg_adamw(tensors.array, tensors.count, step, lr, beta1, beta2, eps, weight_decay,
+                       _ptr(grad_scale), seed, _stream(stream)))
+
+
+def adamw_check(tensors: AdamwTensors, step: int, lr: float, beta1: float = 0.9,
+                beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
+                grad_scale=None) -> None:
+    """Validate without launching."""
+    check(lib.gg_adamw_check(tensors.array, tensors.count, step, lr, beta1, beta2, eps, weight_decay,
+                             _ptr(grad_scale)))
 
 
 def set_claim_policy(policy: str) -> None:

@@ -39,6 +39,7 @@ GG_ACT_NONE, GG_ACT_RELU, GG_ACT_GELU, GG_ACT_GELU_TANH, GG_ACT_SILU = 0, 1, 2, 
 GG_WEIGHT_KN, GG_WEIGHT_NK = 0, 1
 GG_LINEAR_AUTO, GG_LINEAR_SPLIT, GG_LINEAR_PAIR = 0, 1, 2
 GG_LINEAR_NONE = 0
+GG_ADAMW_BLOCK, GG_ADAMW_GROUP = 256, 256
 
 # Every entry point declared in include/gemm_gather.h.
 EXPORTS = (
@@ -50,7 +51,7 @@ EXPORTS = (
     "gg_matmul_all_gather", "gg_matmul_all_gather_path", "gg_matmul_all_gather_check",
     "gg_matmul_all_gather_plan",
     "gg_linear", "gg_linear_check", "gg_linear_backward", "gg_linear_backward_check",
-    "gg_act_backward",
+    "gg_act_backward", "gg_policy_loss", "gg_policy_loss_check", "gg_adamw", "gg_adamw_check",
     "gg_set_claim_policy", "gg_get_claim_policy", "gg_set_store_policy", "gg_get_store_policy",
     "gg_set_wait_limit_ns", "gg_get_wait_limit_ns", "gg_debug_inject_stall",
     "gg_device_status", "gg_clear_device_status",
@@ -68,6 +69,14 @@ class TraceRecord(ctypes.Structure):
                 ("end_ns", ctypes.c_uint64), ("end_cycles", ctypes.c_uint64)]
 
 
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("copy_dtype", ctypes.c_int),
+                ("state_bits", ctypes.c_int)]
+
+
 class Group(ctypes.Structure):
     _fields_ = [("rank_start", ctypes.c_int), ("rank_stride", ctypes.c_int),
                 ("world_size", ctypes.c_int)]
@@ -75,7 +84,7 @@ class Group(ctypes.Structure):
 
 def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     vp, i32, i64, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
-    sz = ctypes.c_size_t
+    sz, f32, f64 = ctypes.c_size_t, ctypes.c_float, ctypes.c_double
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "gg_heap_create": ([vp, sz, i32, vp, vp, pp], i32),
@@ -118,6 +127,12 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
                                       i32, i32, i64, i64, i64, i32, i32, ctypes.POINTER(i32),
                                       ctypes.POINTER(i32)], i32),
         "gg_act_backward": ([vp, i64, vp, i64, vp, i64, i32, i64, i64, i32, vp], i32),
+        "gg_policy_loss": ([vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, f32, f32, f32, f32, f32, vp, vp,
+                            vp, i64, vp, vp], i32),
+        "gg_policy_loss_check": ([vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, f32, f32, f32, f32, f32,
+                                  vp, vp, vp, i64], i32),
+        "gg_adamw": ([vp, i32, i64, f64, f64, f64, f64, f64, vp, u64, vp], i32),
+        "gg_adamw_check": ([vp, i32, i64, f64, f64, f64, f64, f64, vp], i32),
         "gg_set_claim_policy": ([i32], i32),
         "gg_get_claim_policy": ([], i32),
         "gg_set_store_policy": ([i32], i32),

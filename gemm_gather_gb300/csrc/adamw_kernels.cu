@@ -1,0 +1,395 @@
+// AdamW over many tensors at once, for sm_103a.
+//
+// Elementwise: m = b1 m + (1-b1) g, v = b2 v + (1-b2) g^2, p = p (1 - lr wd) -
+// lr' m / (sqrt(v) k + eps).  Bound: HBM; every array is read once and written
+// once.  The tensors' descriptors are the kernel's parameter (up to 256 in a
+// launch: no table in device memory, no copy before the launch), and a CTA
+// finds its tensor by bisection of the running count of chunks.
+//
+// A warp works on blocks of 256 elements, each lane on two quads (elements
+// 4 lane and 128 + 4 lane on): 16-byte accesses of float arrays, 8-byte ones
+// of 16-bit arrays, 4-byte ones of codes, each a whole contiguous piece of the
+// warp's block, all loads ahead of the arithmetic.
+//
+// States in 8 bits.  m and sqrt(v) are e4m3 codes under one power-of-two scale
+// per block, the block's largest magnitude found by a warp reduction, so a
+// scale costs no mantissa bit and scaling is exact.  sqrt(v), because e4m3
+// spans 2^17 and v's range is twice that of g.  Rounding to nearest would
+// freeze v: at b2 = 0.999 a step changes sqrt(v) by less than half an e4m3
+// step (3%) unless g^2 > 60 v, and v would stay up to 60 times too small.
+// So codes are rounded stochastically, and the state follows on average.  The
+// random bits are a hash of (seed, step, tensor, element), 16 for m and 16 for
+// sqrt(v): a published 32-bit integer mixer (xor-shift-multiply, multipliers
+// 0x7feb352d and 0x846ca68b, by C. Wellons), no state to keep.  m, v and
+// sqrt(v) are rounded as written in the formulas above, operation by
+// operation, so that codes and scales do not depend on how a compiler
+// contracts them.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "gg_internal.h"
+#include "gg_ops.h"
+#include "ptx.cuh"
+
+namespace gg {
+namespace {
+
+constexpr int kSMs = 152;
+constexpr int kBlock = GG_ADAMW_BLOCK;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStep = kWarps * kBlock;  // elements of one pass of a CTA
+
+struct Tensor {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    void *copy;
+    int64_t n;
+    uint32_t key;     // hash of (seed, step, position)
+    uint16_t copy_bf16, vec;
+};
+
+struct Group {
+    AdamwStep h;
+    int count;
+    int chunk;                          // elements of a CTA's share, a multiple of kStep
+    uint32_t first[GG_ADAMW_GROUP + 1];  // running count of chunks
+    Tensor t[GG_ADAMW_GROUP];
+};
+static_assert(sizeof(Group) <= 32764, "kernel parameters");
+
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x)
+{
+    x ^= x >> 16;
+    x *= 0x7feb352du;
+    x ^= x >> 15;
+    x *= 0x846ca68bu;
+    return x ^ (x >> 16);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <typename T>
+struct alignas(4 * sizeof(T)) Quad {
+    T e[4];
+};
+
+// Four consecutive elements; `left` of them exist.
+template <typename T>
+__device__ __forceinline__ void load4(const void *p, int64_t at, int left, bool vec, float (&x)[4])
+{
+    const T *q = reinterpret_cast<const T *>(p) + at;
+    if (vec && left >= 4) {
+        const Quad<T> v = *reinterpret_cast<const Quad<T> *>(q);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            x[u] = to_f32<T>(v.e[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            x[u] = u < left ? to_f32<T>(q[u]) : 0.0f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(void *p, int64_t at, int left, bool vec, const float (&x)[4])
+{
+    T *q = reinterpret_cast<T *>(p) + at;
+    if (vec && left >= 4) {
+        Quad<T> v;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            v.e[u] = from_f32<T>(x[u]);
+        *reinterpret_cast<Quad<T> *>(q) = v;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (u < left)
+                q[u] = from_f32<T>(x[u]);
+    }
+}
+
+// Codes: the e4m3 values of four bytes, times the block's scale.
+__device__ __forceinline__ void load_codes(const void *p, int64_t at, int left, bool vec, float scale,
+                                           float (&x)[4])
+{
+    const uint8_t *q = reinterpret_cast<const uint8_t *>(p) + at;
+    uint32_t bytes = 0;
+    if (vec && left >= 4) {
+        bytes = *reinterpret_cast<const uint32_t *>(q);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            bytes |= u < left ? (uint32_t)q[u] << (8 * u) : 0u;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(bytes >> (16 * h)), __NV_E4M3);
+        const float2 f = __half22float2(__half2(r));
+        x[2 * h] = f.x * scale;
+        x[2 * h + 1] = f.y * scale;
+    }
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
+// The block's largest finite magnitude over the warp.
+__device__ __forceinline__ float block_top(const float (&x)[8])
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        top = finite(x[u]) ? fmaxf(top, fabsf(x[u])) : top;
+    return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
+}
+
+// Exponent k of the scale 2^k with top / 2^k in (224, 448]: 448 = 1.75 * 2^8, so
+// adding 0x1fffff to the bits carries into the exponent beyond 1.75.
+__device__ __forceinline__ int scale_exp(float top)
+{
+    const int k = (int)((__float_as_uint(top) + 0x1fffffu) >> 23) - 127 - 8;
+    return k < -118 ? -118 : k;
+}
+
+// One of the two e4m3 neighbours of x (|x| <= 448), upwards with the
+// probability of the remainder: 16 random bits are added below the code's
+// mantissa and the rest cut off.  Below 2^-6, where the code's step stays
+// 2^-9, the same on |x| + 2^-6.
+__device__ __forceinline__ float round_e4m3(float x, uint32_t r16)
+{
+    const float a = fabsf(x);
+    const float off = a < 0.015625f ? 0.015625f : 0.0f;
+    const float y = __uint_as_float((__float_as_uint(a + off) + (r16 << 4)) & 0xfff00000u) - off;
+    return copysignf(finite(x) ? y : NAN, x);
+}
+
+__device__ __forceinline__ void store_codes(void *p, int64_t at, int left, bool vec, const float *x)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t bytes = lo | hi << 16;
+    uint8_t *q = reinterpret_cast<uint8_t *>(p) + at;
+    if (vec && left >= 4) {
+        *reinterpret_cast<uint32_t *>(q) = bytes;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (u < left)
+                q[u] = (uint8_t)(bytes >> (8 * u));
+    }
+}
+
+template <typename P, typename G, int BITS>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Group g)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int lo = 0, hi = g.count - 1;  // the tensor of this CTA's chunk
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (g.first[mid] <= blockIdx.x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const Tensor &t = g.t[lo];
+    const int64_t begin = (int64_t)(blockIdx.x - g.first[lo]) * g.chunk;
+    const int64_t end = gg_min64(begin + g.chunk, t.n);
+    const bool vec = t.vec != 0;
+    const AdamwStep &h = g.h;
+    const float gscale = h.grad_scale ? *h.grad_scale : 1.0f;
+
+#pragma unroll 1
+    for (int64_t base = begin + warp * kBlock; base < end; base += kStep) {
+        const int64_t block = base / kBlock;
+        float p[8], gr[8], m[8], v[8], u[8];
+        const float ms = BITS == 8 ? t.m_scale[block] : 0.0f, vs = BITS == 8 ? t.v_scale[block] : 0.0f;
+        int left[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t at = base + q * 128 + lane * 4;
+            left[q] = t.n - at >= 4 ? 4 : (t.n > at ? (int)(t.n - at) : 0);
+            float(&p4)[4] = *reinterpret_cast<float(*)[4]>(p + 4 * q);
+            float(&g4)[4] = *reinterpret_cast<float(*)[4]>(gr + 4 * q);
+            float(&m4)[4] = *reinterpret_cast<float(*)[4]>(m + 4 * q);
+            float(&v4)[4] = *reinterpret_cast<float(*)[4]>(v + 4 * q);
+            load4<P>(t.param, at, left[q], vec, p4);
+            load4<G>(t.grad, at, left[q], vec, g4);
+            if constexpr (BITS == 8) {
+                load_codes(t.m, at, left[q], vec, ms, m4);
+                load_codes(t.v, at, left[q], vec, vs, v4);
+            } else {
+                load4<float>(t.m, at, left[q], vec, m4);
+                load4<float>(t.v, at, left[q], vec, v4);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = __fmul_rn(gr[e], gscale);
+            if constexpr (BITS == 8)
+                v[e] = __fmul_rn(v[e], v[e]);
+            m[e] = __fadd_rn(__fmul_rn(m[e], h.beta1), __fmul_rn(x, h.one_minus_beta1));
+            v[e] = __fadd_rn(__fmul_rn(v[e], h.beta2), __fmul_rn(__fmul_rn(x, x), h.one_minus_beta2));
+            u[e] = __fsqrt_rn(v[e]);
+            const float den = u[e] * h.inv_sqrt_c2 + h.eps;
+            p[e] = p[e] * h.decay - h.step_size * (m[e] / den);
+        }
+        float ims = 0.0f, ivs = 0.0f;
+        if constexpr (BITS == 8) {
+            // elements past the end hold m = v = 0
+            const int mk = scale_exp(block_top(m)), vk = scale_exp(block_top(u));
+            ims = __uint_as_float((uint32_t)(127 - mk) << 23);
+            ivs = __uint_as_float((uint32_t)(127 - vk) << 23);
+            if (lane == 0) {
+                t.m_scale[block] = __uint_as_float((uint32_t)(127 + mk) << 23);
+                t.v_scale[block] = __uint_as_float((uint32_t)(127 + vk) << 23);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t at = base + q * 128 + lane * 4;
+            const float(&p4)[4] = *reinterpret_cast<float(*)[4]>(p + 4 * q);
+            store4<P>(t.param, at, left[q], vec, p4);
+            if (t.copy) {
+                if (t.copy_bf16)
+                    store4<__nv_bfloat16>(t.copy, at, left[q], vec, p4);
+                else
+                    store4<__half>(t.copy, at, left[q], vec, p4);
+            }
+            if constexpr (BITS == 8) {
+                float cm[4], cv[4];
+                const uint32_t key = mix32((uint32_t)(at >> 32) ^ t.key);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t r = mix32((uint32_t)(at + e) ^ key);
+                    cm[e] = round_e4m3(m[4 * q + e] * ims, r & 0xffffu);
+                    cv[e] = round_e4m3(u[4 * q + e] * ivs, r >> 16);
+                }
+                store_codes(t.m, at, left[q], vec, cm);
+                store_codes(t.v, at, left[q], vec, cv);
+            } else {
+                store4<float>(t.m, at, left[q], vec, *reinterpret_cast<float(*)[4]>(m + 4 * q));
+                store4<float>(t.v, at, left[q], vec, *reinterpret_cast<float(*)[4]>(v + 4 * q));
+            }
+        }
+    }
+}
+
+template <typename P, typename G>
+cudaError_t launch_group(const Group &g, int bits, cudaStream_t s)
+{
+    const unsigned grid = g.first[g.count];
+    if (bits == 8)
+        adamw_kernel<P, G, 8><<<grid, kThreads, 0, s>>>(g);
+    else
+        adamw_kernel<P, G, 32><<<grid, kThreads, 0, s>>>(g);
+    return cudaGetLastError();
+}
+
+template <typename P>
+cudaError_t launch_param(const Group &g, int grad, int bits, cudaStream_t s)
+{
+    if (grad == GG_F32)
+        return launch_group<P, float>(g, bits, s);
+    if (grad == GG_F16)
+        return launch_group<P, __half>(g, bits, s);
+    return launch_group<P, __nv_bfloat16>(g, bits, s);
+}
+
+cudaError_t launch_one(const Group &g, int param, int grad, int bits, cudaStream_t s)
+{
+    if (g.count == 0)
+        return cudaSuccess;
+    if (param == GG_F32)
+        return launch_param<float>(g, grad, bits, s);
+    if (param == GG_F16)
+        return launch_param<__half>(g, grad, bits, s);
+    return launch_param<__nv_bfloat16>(g, grad, bits, s);
+}
+
+bool aligned16(const gg_adamw_tensor &x)
+{
+    const uint64_t all = reinterpret_cast<uint64_t>(x.param) | reinterpret_cast<uint64_t>(x.grad) |
+                         reinterpret_cast<uint64_t>(x.m) | reinterpret_cast<uint64_t>(x.v) |
+                         reinterpret_cast<uint64_t>(x.copy);
+    return all % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const gg_adamw_tensor *tensors, int count, const AdamwStep &h, cudaStream_t s)
+{
+    // Chunks: long ones once there are enough to fill the GPU, so that the search
+    // for the tensor is spread over more elements; short ones for small work.
+    int64_t total = 0;
+    uint32_t kinds = 0;  // combinations of types that occur
+    for (int i = 0; i < count; ++i) {
+        total += tensors[i].n;
+        if (tensors[i].n > 0)
+            kinds |= 1u << (tensors[i].param_dtype * 6 + tensors[i].grad_dtype * 2 +
+                            (tensors[i].state_bits == 8));
+    }
+    const int64_t chunk = total >= (int64_t)kSMs * 8 * 8 * kStep ? 8 * kStep : kStep;
+    static thread_local Group g;
+    g.h = h;
+    g.chunk = (int)chunk;
+    // one kernel per combination of types, each over its tensors in list order
+    for (int kind = 0; kind < 18; ++kind) {
+        if (!(kinds >> kind & 1u))
+            continue;
+        const int param = kind / 6, grad = kind / 2 % 3, bits = kind % 2 ? 8 : 32;
+        g.count = 0;
+        g.first[0] = 0;
+        for (int i = 0; i < count; ++i) {
+            const gg_adamw_tensor &x = tensors[i];
+            if (x.n == 0 || x.param_dtype != param || x.grad_dtype != grad || x.state_bits != bits)
+                continue;
+            const int64_t chunks = (x.n + chunk - 1) / chunk;
+            if (g.count == GG_ADAMW_GROUP || g.first[g.count] + chunks > 0x7fffffffll) {
+                const cudaError_t e = launch_one(g, param, grad, bits, s);
+                if (e != cudaSuccess)
+                    return e;
+                g.count = 0;
+            }
+            Tensor &t = g.t[g.count];
+            t.param = x.param;
+            t.grad = x.grad;
+            t.m = x.m;
+            t.v = x.v;
+            t.m_scale = x.m_scale;
+            t.v_scale = x.v_scale;
+            t.copy = x.copy;
+            t.n = x.n;
+            t.key = mix32(mix32(mix32(mix32((uint32_t)i) ^ h.step) ^ (uint32_t)h.seed) ^
+                          (uint32_t)(h.seed >> 32));
+            t.copy_bf16 = x.copy_dtype == GG_BF16;
+            t.vec = aligned16(x);
+            g.first[g.count + 1] = g.first[g.count] + (uint32_t)chunks;
+            ++g.count;
+        }
+        const cudaError_t e = launch_one(g, param, grad, bits, s);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace gg

@@ -2,6 +2,8 @@
 // Declared in include/gemm_gather.h.
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "gg_ops.h"
 
 namespace {
@@ -284,9 +286,174 @@ gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t 
     return op_ok();
 }
 
+gg_status prepare_loss(const void *logits, int64_t ld, const int64_t *target, const float *old_logp,
+                       const float *ref_logp, const float *advantage, const float *weight, int64_t T,
+                       int64_t V, gg_dtype dtype, float inv_temperature, float clip_low,
+                       float clip_high, float kl_coef, float grad_scale, const float *stats,
+                       const float *logp_out, const void *dlogits, int64_t ldd, gg::LossArgs *out)
+{
+    if (dtype != GG_F16 && dtype != GG_BF16 && dtype != GG_F32)
+        return op_fail(GG_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    GG_TRY(check_sizes(T, V, 0));
+    if (T > 0 && V == 0)
+        return op_fail(GG_ERR_INVALID_ARG, "a token needs a vocabulary: V must be >= 1");
+    if (T > kMaxSize / 8)  // rows x CTAs of a cluster
+        return op_fail(GG_ERR_UNSUPPORTED, "T must be below 2^28");
+    if (!(inv_temperature > 0.0f) || !std::isfinite(inv_temperature))
+        return op_fail(GG_ERR_INVALID_ARG, "inv_temperature must be positive and finite");
+    if (!(clip_low >= 0.0f) || !(clip_high >= 0.0f))
+        return op_fail(GG_ERR_INVALID_ARG, "clip_low and clip_high must be >= 0");
+    if (!std::isfinite(kl_coef) || !std::isfinite(grad_scale))
+        return op_fail(GG_ERR_INVALID_ARG, "kl_coef and grad_scale must be finite");
+    const int64_t es = dtype == GG_F32 ? 4 : 2;
+    const Mat x{"logits", logits, T, V, ld, es}, d{"dlogits", dlogits, T, V, ldd, es};
+    const Mat tg{"target", target, 1, T, T, 8}, ol{"old_logp", old_logp, 1, T, T, 4},
+        rl{"ref_logp", ref_logp, 1, T, T, 4}, ad{"advantage", advantage, 1, T, T, 4},
+        we{"weight", weight, 1, T, T, 4}, lo{"logp_out", logp_out, 1, T, T, 4},
+        st{"stats", stats, 1, 4, 4, 4};
+    GG_TRY(check_mat(x, true));
+    GG_TRY(check_mat(tg, true));
+    GG_TRY(check_mat(ol, false));
+    GG_TRY(check_mat(rl, false));
+    GG_TRY(check_mat(ad, true));
+    GG_TRY(check_mat(we, true));
+    GG_TRY(check_mat(lo, true));
+    GG_TRY(check_mat(st, false));
+    GG_TRY(check_mat(d, false));
+    const Mat *outs[] = {&d, &lo, &st};
+    for (const Mat *o : outs) {
+        for (const Mat *in : {&x, &tg, &ol, &rl, &ad, &we})
+            if (!(o == &d && in == &x && same(d, x)))
+                GG_TRY(check_apart(*o, *in));
+        for (const Mat *p : outs)
+            if (o < p)
+                GG_TRY(check_apart(*o, *p));
+    }
+    *out = gg::LossArgs{logits,    ld,        target,  old_logp, ref_logp,
+                        advantage, weight,    T,       V,        (int)dtype,
+                        inv_temperature, clip_low, clip_high, kl_coef, grad_scale,
+                        const_cast<float *>(stats), const_cast<float *>(logp_out),
+                        const_cast<void *>(dlogits), ldd, nullptr};
+    return op_ok();
+}
+
+gg_status prepare_adamw(const gg_adamw_tensor *tensors, int count, int64_t step, double lr,
+                        double beta1, double beta2, double eps, double weight_decay,
+                        const float *grad_scale, gg::AdamwStep *out)
+{
+    if (count < 0 || (count > 0 && !tensors))
+        return op_fail(GG_ERR_INVALID_ARG, "count must be >= 0 and tensors non-NULL");
+    if (step < 1)
+        return op_fail(GG_ERR_INVALID_ARG, "step %lld: steps count from 1", (long long)step);
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+        return op_fail(GG_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+    if (!std::isfinite(lr) || !(eps >= 0.0) || !std::isfinite(eps) || !std::isfinite(weight_decay))
+        return op_fail(GG_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite, eps >= 0");
+    if (reinterpret_cast<uint64_t>(grad_scale) % 4)
+        return op_fail(GG_ERR_ALIGNMENT, "grad_scale must be 4-byte aligned");
+    for (int i = 0; i < count; ++i) {
+        const gg_adamw_tensor &t = tensors[i];
+        if (t.n < 0)
+            return op_fail(GG_ERR_INVALID_ARG, "tensor %d: n must be >= 0", i);
+        if (t.n > (int64_t)1 << 40)
+            return op_fail(GG_ERR_UNSUPPORTED, "tensor %d: n must be at most 2^40", i);
+        const auto known = [](gg_dtype d) { return d == GG_F16 || d == GG_BF16 || d == GG_F32; };
+        if (!known(t.param_dtype) || !known(t.grad_dtype))
+            return op_fail(GG_ERR_INVALID_ARG, "tensor %d: unknown dtype", i);
+        if (t.state_bits != 32 && t.state_bits != 8)
+            return op_fail(GG_ERR_UNSUPPORTED, "tensor %d: states have 32 or 8 bits", i);
+        if (t.copy && t.copy_dtype != GG_F16 && t.copy_dtype != GG_BF16)
+            return op_fail(GG_ERR_UNSUPPORTED, "tensor %d: the copy is GG_F16 or GG_BF16", i);
+        const bool eight = t.state_bits == 8;
+        if (t.n > 0 && (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale))))
+            return op_fail(GG_ERR_INVALID_ARG, "tensor %d: param, grad and states must be non-NULL", i);
+        const int64_t pe = t.param_dtype == GG_F32 ? 4 : 2, ge = t.grad_dtype == GG_F32 ? 4 : 2;
+        const int64_t blocks = eight ? (t.n + GG_ADAMW_BLOCK - 1) / GG_ADAMW_BLOCK : 0;
+        const Mat all[] = {{"param", t.param, 1, t.n, t.n, pe},
+                           {"m", t.m, 1, t.n, t.n, eight ? 1 : 4},
+                           {"v", t.v, 1, t.n, t.n, eight ? 1 : 4},
+                           {"m_scale", t.m_scale, 1, blocks, blocks, 4},
+                           {"v_scale", t.v_scale, 1, blocks, blocks, 4},
+                           {"copy", t.copy, 1, t.n, t.n, 2},
+                           {"grad", t.grad, 1, t.n, t.n, ge}};
+        for (const Mat &x : all) {
+            GG_TRY(check_mat(x, false));
+            for (const Mat &y : all)
+                if (&x < &y && share(x, y))
+                    return op_fail(GG_ERR_INVALID_ARG, "tensor %d: %s overlaps %s", i, x.name, y.name);
+        }
+    }
+    gg::AdamwStep h{};
+    h.beta1 = (float)beta1;
+    h.one_minus_beta1 = (float)(1.0 - beta1);
+    h.beta2 = (float)beta2;
+    h.one_minus_beta2 = (float)(1.0 - beta2);
+    h.step_size = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+    h.inv_sqrt_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+    h.eps = (float)eps;
+    h.decay = (float)(1.0 - lr * weight_decay);
+    h.grad_scale = grad_scale;
+    h.step = (uint32_t)step;
+    *out = h;
+    return op_ok();
+}
+
 }  // namespace
 
 extern "C" {
+
+gg_status gg_policy_loss(const void *logits, int64_t ld, const int64_t *target,
+                         const float *old_logp, const float *ref_logp, const float *advantage,
+                         const float *weight, int64_t T, int64_t V, gg_dtype dtype,
+                         float inv_temperature, float clip_low, float clip_high, float kl_coef,
+                         float grad_scale, float *stats, float *logp_out, void *dlogits,
+                         int64_t ldd, int *dev_status, gg_stream_t stream)
+{
+    gg::LossArgs a;
+    GG_TRY(prepare_loss(logits, ld, target, old_logp, ref_logp, advantage, weight, T, V, dtype,
+                        inv_temperature, clip_low, clip_high, kl_coef, grad_scale, stats, logp_out,
+                        dlogits, ldd, &a));
+    if (T == 0 && !stats)
+        return op_ok();
+    a.status = dev_status;
+    GG_TRY(gg::op_status_word(&a.status));
+    const cudaError_t e = gg::launch_policy_loss(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? op_ok() : op_cuda_fail(e, "launching the policy loss");
+}
+
+gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *target,
+                               const float *old_logp, const float *ref_logp,
+                               const float *advantage, const float *weight, int64_t T, int64_t V,
+                               gg_dtype dtype, float inv_temperature, float clip_low,
+                               float clip_high, float kl_coef, float grad_scale,
+                               const float *stats, const float *logp_out, const void *dlogits,
+                               int64_t ldd)
+{
+    gg::LossArgs a;
+    return prepare_loss(logits, ld, target, old_logp, ref_logp, advantage, weight, T, V, dtype,
+                        inv_temperature, clip_low, clip_high, kl_coef, grad_scale, stats, logp_out,
+                        dlogits, ldd, &a);
+}
+
+gg_status gg_adamw(const gg_adamw_tensor *tensors, int count, int64_t step, double lr, double beta1,
+                   double beta2, double eps, double weight_decay, const float *grad_scale,
+                   uint64_t seed, gg_stream_t stream)
+{
+    gg::AdamwStep h;
+    GG_TRY(prepare_adamw(tensors, count, step, lr, beta1, beta2, eps, weight_decay, grad_scale, &h));
+    h.seed = seed;
+    const cudaError_t e =
+        gg::launch_adamw(tensors, count, h, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? op_ok() : op_cuda_fail(e, "launching AdamW");
+}
+
+gg_status gg_adamw_check(const gg_adamw_tensor *tensors, int count, int64_t step, double lr,
+                         double beta1, double beta2, double eps, double weight_decay,
+                         const float *grad_scale)
+{
+    gg::AdamwStep h;
+    return prepare_adamw(tensors, count, step, lr, beta1, beta2, eps, weight_decay, grad_scale, &h);
+}
 
 gg_status gg_linear(const void *X, int64_t ldx, const void *W, int64_t ldw, gg_weight_layout layout,
                     const void *bias, gg_dtype bias_dtype, gg_activation act, const void *residual,

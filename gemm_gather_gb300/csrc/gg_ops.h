@@ -75,4 +75,33 @@ struct ActBackwardArgs {  // dz = dy * act'(z)
 };
 cudaError_t launch_act_backward(const ActBackwardArgs &a, cudaStream_t s);
 
+// ---- policy loss -------------------------------------------------------------------
+struct LossArgs {
+    const void *logits;
+    int64_t ld;
+    const int64_t *target;
+    const float *old_logp, *ref_logp, *advantage, *weight;
+    int64_t T, V;
+    int dtype;  // GG_F16 / GG_BF16 / GG_F32
+    float inv_temperature, clip_low, clip_high, kl_coef, grad_scale;
+    float *stats, *logp_out;
+    void *dlogits;
+    int64_t ldd;
+    int *status;
+};
+cudaError_t launch_policy_loss(const LossArgs &a, cudaStream_t s);
+
+// ---- AdamW ---------------------------------------------------------------------------
+struct AdamwStep {  // one step's constants, rounded once from double
+    float beta1, one_minus_beta1, beta2, one_minus_beta2;
+    float step_size;   // lr / (1 - beta1^step)
+    float inv_sqrt_c2; // 1 / sqrt(1 - beta2^step)
+    float eps, decay;  // decay = 1 - lr * weight_decay
+    const float *grad_scale;
+    uint64_t seed;
+    uint32_t step;
+};
+cudaError_t launch_adamw(const gg_adamw_tensor *tensors, int count, const AdamwStep &h,
+                         cudaStream_t s);
+
 }  // namespace gg

@@ -521,6 +521,105 @@ gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t l
                           gg_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * gg_policy_loss — the clipped policy loss of T sampled tokens with a KL term
+ * to a reference policy, and its gradient, from the logits in one call:
+ *   x      = logits[t, :] * inv_temperature
+ *   logp   = x[target] - log sum exp x
+ *   ratio  = exp(logp - old_logp[t])             (old_logp NULL: old_logp =
+ *            logp held fixed, so 1, or NaN where logp is not finite)
+ *   kl     = exp(ref_logp[t] - logp) - (ref_logp[t] - logp) - 1
+ *   loss_t = -min(ratio A, clamp(ratio, 1 - clip_low, 1 + clip_high) A)
+ *            + kl_coef kl,                        A = advantage[t]
+ * stats[0..3] = sum over t of weight[t] * { loss_t, kl, clipped, ratio }, where
+ * clipped is 1 where the clamp holds the minimum (A > 0 and ratio > 1 +
+ * clip_high, or A < 0 and ratio < 1 - clip_low); logp_out[t] = logp; and
+ *   dlogits[t, v] = grad_scale * weight[t] * inv_temperature *
+ *                   d loss_t / d logp * ((v == target) - softmax(x)[v]),
+ *   d loss_t / d logp = -A ratio (0 where clipped) + kl_coef (1 - exp(ref - logp)).
+ * grad_scale (a loss scale for 16-bit gradients) multiplies dlogits alone.
+ * kl_coef == 0 or ref_logp NULL: no KL term (kl counts as 0).
+ *
+ * logits: T x V of `dtype` (GG_F16, GG_BF16 or GG_F32), pitch ld; target:
+ * int64 per token; old_logp, ref_logp, advantage, weight, logp_out: float32
+ * per token; stats: 4 floats.  dlogits (T x V of `dtype`, pitch ldd) may be
+ * logits itself (same pointer and pitch), or NULL for the loss alone.
+ * logp_out is required (the statistics are summed from it); stats may be NULL.
+ * A token of weight 0 is masked: its logits, target and statistics are not
+ * read, its dlogits row is zero and its logp_out 0.  Logits of -inf are
+ * tokens of probability 0; a row of nothing else, or one with NaN or +inf,
+ * gives NaN.  A target outside [0, V) stores GG_ERR_INVALID_ARG in the status
+ * word (dev_status, or the library's when NULL) and its token counts as masked.
+ * Each row is read from memory once.  Any alignment and pitch.
+ * ------------------------------------------------------------------------- */
+gg_status gg_policy_loss(const void *logits, int64_t ld, const int64_t *target,
+                         const float *old_logp, const float *ref_logp, const float *advantage,
+                         const float *weight, int64_t T, int64_t V, gg_dtype dtype,
+                         float inv_temperature, float clip_low, float clip_high, float kl_coef,
+                         float grad_scale, float *stats, float *logp_out, void *dlogits,
+                         int64_t ldd, int *dev_status, gg_stream_t stream);
+
+/* Validate a gg_policy_loss call exactly as the launching call does and launch
+ * nothing. */
+gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *target,
+                               const float *old_logp, const float *ref_logp,
+                               const float *advantage, const float *weight, int64_t T, int64_t V,
+                               gg_dtype dtype, float inv_temperature, float clip_low,
+                               float clip_high, float kl_coef, float grad_scale,
+                               const float *stats, const float *logp_out, const void *dlogits,
+                               int64_t ldd);
+
+/* ---------------------------------------------------------------------------
+ * gg_adamw — one AdamW step (decoupled weight decay) over many tensors in one
+ * launch per group of up to GG_ADAMW_GROUP tensors:
+ *   g = *grad_scale * grad                        (grad_scale NULL: 1)
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32; step counts from 1.  A tensor is n contiguous elements; param and
+ * grad are GG_F32, GG_F16 or GG_BF16 (param rounded to nearest when 16-bit);
+ * copy, if not NULL, receives param rounded to copy_dtype (GG_F16 or GG_BF16):
+ * the 16-bit weights that an all-gather sends, from a float32 master.
+ *
+ * state_bits 32: m and v are float arrays of n.
+ * state_bits 8: m holds m and v holds sqrt(v), as 8-bit e4m3 codes (n bytes
+ * each), and m_scale and v_scale one float per GG_ADAMW_BLOCK elements: a
+ * value is its code times its block's scale.  The scale is the power of two
+ * that brings the block's largest magnitude into (224, 448] (2^-118 at least);
+ * codes are rounded stochastically (up with the probability of the
+ * remainder), with 16 bits each of a hash of (seed, step, the tensor's
+ * position in the list, the element), so that equal calls give equal bits and
+ * states change by less than a rounding step on average.  A value that is not
+ * finite is stored as NaN and does not enter the scale.
+ *
+ * `tensors` is host memory, read during the call.  Tensors must not overlap.
+ * Any alignment (16-byte aligned arrays are the fast case).  n == 0 is skipped.
+ * grad_scale is a device float, read by the kernel (a loss scale's inverse, a
+ * clipping factor).
+ * ------------------------------------------------------------------------- */
+#define GG_ADAMW_BLOCK 256
+#define GG_ADAMW_GROUP 256
+typedef struct {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale; /* state_bits 8; else NULL */
+    void *copy;               /* or NULL */
+    int64_t n;
+    gg_dtype param_dtype, grad_dtype, copy_dtype;
+    int state_bits;           /* 32 or 8 */
+} gg_adamw_tensor;
+
+gg_status gg_adamw(const gg_adamw_tensor *tensors, int count, int64_t step, double lr, double beta1,
+                   double beta2, double eps, double weight_decay, const float *grad_scale,
+                   uint64_t seed, gg_stream_t stream);
+
+/* Validate a gg_adamw call exactly as the launching call does and launch
+ * nothing. */
+gg_status gg_adamw_check(const gg_adamw_tensor *tensors, int count, int64_t step, double lr,
+                         double beta1, double beta2, double eps, double weight_decay,
+                         const float *grad_scale);
+
+/* ---------------------------------------------------------------------------
  * Bounded waits.  Every wait of a kernel on an mbarrier gives up after this
  * many nanoseconds of wall time (default 2e9), stores GG_ERR_TIMEOUT in the
  * call's dev_status, drains the copies it has in flight and returns.  Applies
