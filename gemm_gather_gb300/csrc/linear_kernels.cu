@@ -222,10 +222,181 @@ __device__ __forceinline__ float load_bias(const LinearArgs &a, int64_t i)
     return a.bias_f32 ? reinterpret_cast<const float *>(a.bias)[i] : load16(a.bias, i, a.is_bf16);
 }
 
-// Valid columns of the 16 from j0.
+// Valid columns of the 64, or of the 16, from j0.
+__device__ __forceinline__ int valid64(int64_t J, int64_t j0)
+{
+    return J - j0 >= 64 ? 64 : (J > j0 ? (int)(J - j0) : 0);
+}
+
 __device__ __forceinline__ int valid16(int64_t J, int64_t j0)
 {
     return J - j0 >= 16 ? 16 : (J > j0 ? (int)(J - j0) : 0);
+}
+
+// ---- staged epilogue -----------------------------------------------------------------
+// A lane owns one feature (MMA row), so a warp that stored its values directly
+// would write 64-byte pieces two bytes a lane: measured, 20 cycles of an SM for
+// each such store, 40,000 for a 256 x 256 tile, as long as a contraction over
+// 8192.  Instead a warp turns its 32 features x 64 tokens around in 4 KB of its
+// own shared memory: two-byte stores along a row there, then 16 bytes a lane,
+// 8 rows of 64 bytes per global access.  Tensors read in the epilogue come
+// the same way, loaded into registers ahead of the accumulator.
+constexpr int kStageCols = 64;
+constexpr int kWarpStage = kStageCols * 64;  // 64 tokens x 32 features x 2 bytes
+
+// One 16-bit M x N tensor of the epilogue; vec: 16-byte accesses are aligned.
+struct Rows {
+    uint16_t *p;
+    int64_t ld;
+    bool vec;
+};
+
+__device__ __forceinline__ Rows rows_of(const void *p, int64_t ld)
+{
+    Rows r;
+    r.p = reinterpret_cast<uint16_t *>(const_cast<void *>(p));
+    r.ld = ld;
+    r.vec = ((reinterpret_cast<uint64_t>(p) | (uint64_t)(ld * 2)) & 15) == 0;
+    return r;
+}
+
+// 32 features from i0 of `n` tokens from j0: lane l takes features 8 (l mod 4)
+// on of tokens l / 4 + 8 k.
+__device__ __forceinline__ void read_rows(const Rows &t, int64_t I, int64_t i0, int64_t j0, int n, int lane,
+                                          uint4 (&x)[8])
+{
+    const int64_t i = i0 + (lane & 3) * 8;
+    const uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if ((lane >> 2) + 8 * k < n) {
+            const uint16_t *q = p + (int64_t)(8 * k) * t.ld;
+            if (t.vec && i + 8 <= I) {
+                x[k] = *reinterpret_cast<const uint4 *>(q);
+            } else {
+                uint16_t h[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    h[u] = i + u < I ? q[u] : (uint16_t)0;
+                x[k] = *reinterpret_cast<uint4 *>(h);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void stage_rows(uint8_t *stage, int lane, const uint4 (&x)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4 *>(stage + k * 512 + lane * 16) = x[k];
+    __syncwarp();
+}
+
+__device__ __forceinline__ void write_rows(const Rows &t, int64_t I, int64_t i0, int64_t j0, int n, int lane,
+                                           const uint8_t *stage)
+{
+    __syncwarp();
+    const int64_t i = i0 + (lane & 3) * 8;
+    uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if ((lane >> 2) + 8 * k < n) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + k * 512 + lane * 16);
+            uint16_t *q = p + (int64_t)(8 * k) * t.ld;
+            if (t.vec && i + 8 <= I) {
+                *reinterpret_cast<uint4 *>(q) = x;
+            } else {
+                const uint16_t *h = reinterpret_cast<const uint16_t *>(&x);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + u < I)
+                        q[u] = h[u];
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// This lane's element of a staged token.
+__device__ __forceinline__ uint16_t *staged(uint8_t *stage, int lane, int col)
+{
+    return reinterpret_cast<uint16_t *>(stage + col * 64) + lane;
+}
+
+// The tensor an epilogue reads beside the sums, or a null pointer.
+template <int EPI>
+__device__ __forceinline__ Rows aux_of(const LinearArgs &a)
+{
+    if constexpr (EPI == kEpiGradW)
+        return rows_of(a.accumulate && !a.out_f32 ? a.out : nullptr, a.ldo);
+    return rows_of(a.aux, a.ldaux);
+}
+
+// The epilogue of a warp's 32 features (from i0) and up to 64 tokens (from j0, n
+// of them).  sums(col, v) gives this lane's sums of columns col .. col + 15; it
+// may be called twice.  aux: the rows read beside them (has_aux).
+template <int EPI, typename Sums>
+__device__ __forceinline__ void emit64(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane,
+                                       float bias, bool has_aux, const uint4 (&aux)[8],
+                                       uint8_t *stage, Sums sums)
+{
+    // sums in registers need constant columns; the others keep the code small
+    constexpr int kUnroll = EPI == kEpiGradW ? kStageCols / 16 : 1;
+    if constexpr (EPI == kEpiForward) {
+        if (a.zout != nullptr) {
+#pragma unroll 1
+            for (int c = 0; c < n; c += 16) {
+                float v[16];
+                sums(c, v);
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    store16(staged(stage, lane, c + u), 0, v[u] + bias, a.is_bf16);
+            }
+            write_rows(rows_of(a.zout, a.ldz), a.I, i0, j0, n, lane, stage);
+        }
+    }
+    if (has_aux)
+        stage_rows(stage, lane, aux);
+#pragma unroll(kUnroll)
+    for (int c = 0; c < kStageCols; c += 16) {
+        if (c >= n)
+            break;
+        float v[16], x[16];
+        sums(c, v);
+        if (has_aux) {  // a lane reads its own elements before it writes over them
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                x[u] = load16(staged(stage, lane, c + u), 0, a.is_bf16);
+        }
+        if constexpr (EPI == kEpiForward) {
+            with_act(a.act, [&](auto k) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = act_value<decltype(k)::value>(v[u] + bias);
+            });
+            if (has_aux) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] += x[u];
+            }
+        } else if constexpr (EPI == kEpiGradIn) {
+            if (has_aux)
+                with_act(a.act, [&](auto k) {
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        v[u] *= act_slope<decltype(k)::value>(x[u]);
+                });
+        } else if (has_aux) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] += x[u];
+        }
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            store16(staged(stage, lane, c + u), 0, v[u], a.is_bf16);
+    }
+    write_rows(rows_of(a.out, a.ldo), a.I, i0, j0, n, lane, stage);
 }
 
 // One stage's operand: ROWS rows (or columns) of 64 k.  K-major: one box of
@@ -243,17 +414,25 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *ma
     }
 }
 
-// ---- pair kernel: 256 features x 256 tokens per CTA pair ---------------------------
+// ---- pair kernel: 256 features x BT tokens per CTA pair ----------------------------
 namespace pair {
-constexpr int kStages = 6;
-constexpr int kOperand = 128 * kBK * 2;  // 16 KB: this CTA's 128 rows of A, or of B
-constexpr int kStage = 2 * kOperand;
-constexpr int kTile = 256;
-constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, 128 columns each
+constexpr int kTileI = 256;
+constexpr int kA = 128 * kBK * 2;        // 16 KB: this CTA's 128 features of one k-block
+constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, half the columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kOffShared = kStages * kStage;
-constexpr int kSmemBytes = kOffShared + (int)sizeof(Shared) + 1024;
-static_assert(kSmemBytes <= 232448 && kStages <= kMaxStages, "shared memory of a CTA");
+template <int BT>
+struct Geo {
+    static constexpr int kB = BT / 2 * kBK * 2;  // this CTA's half of the tokens
+    static constexpr int kStage = kA + kB;
+    static constexpr int kStages = BT == 256 ? 6 : 8;  // 192 KB of ring
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kPartial = 128 * BT * 4;  // float32 partial tile, over the spent ring
+    static constexpr int kOffStage = kRing;
+    static constexpr int kOffShared = kOffStage + kEpiWarps * kWarpStage;
+    static constexpr int kSmemBytes = kOffShared + (int)sizeof(Shared) + 1024;
+    static_assert(kSmemBytes <= 232448 && kStages <= kMaxStages && kPartial <= kRing,
+                  "shared memory of a CTA");
+};
 
 struct Tile {
     int ti, tj;
@@ -277,30 +456,41 @@ __device__ __forceinline__ Tile tile_at(const LinearArgs &a, int64_t t, int tile
 }
 }  // namespace pair
 
-template <int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+// A cluster is one CTA pair that walks its share of the tiles, or, when tiles
+// are few, 2 or 4 pairs that split one tile's contraction.
+template <int EPI, int BT>
+__global__ void __launch_bounds__(pair::kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ LinearArgs a)
 {
+    using G = pair::Geo<BT>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // 1024-aligned for the 128B swizzle
-    Shared &sh = *reinterpret_cast<Shared *>(smem_raw + (base - raw) + pair::kOffShared);
+    uint8_t *smem = smem_raw + (base - raw);
+    Shared &sh = *reinterpret_cast<Shared *>(smem + G::kOffShared);
     volatile int *abort_flag = &sh.abort_flag;
 
+    launch_dependents();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t rank = crank & 1u;           // position in the CTA pair
+    const uint32_t lead = crank & ~1u;          // cluster rank of the pair's leader
     const bool leader = rank == 0;
+    const int parts = (int)cluster_size() / 2;  // pairs that share a tile's contraction
+    const int part = (int)crank / 2;
     const int64_t unit = (int64_t)cluster_id_x();
     const int64_t nunits = (int64_t)ncluster_x();
-    const int tiles_i = (int)((a.I + pair::kTile - 1) / pair::kTile);
-    const int tiles_j = (int)((a.J + pair::kTile - 1) / pair::kTile);
+    const int tiles_i = (int)((a.I + pair::kTileI - 1) / pair::kTileI);
+    const int tiles_j = (int)((a.J + BT - 1) / BT);
     const int64_t total = (int64_t)tiles_i * tiles_j;
-    const int num_kb = (int)((a.K + kBK - 1) / kBK);
+    const int all_kb = (int)((a.K + kBK - 1) / kBK);
+    const int kb0 = (int)((int64_t)all_kb * part / parts);
+    const int num_kb = (int)((int64_t)all_kb * (part + 1) / parts) - kb0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < pair::kStages; ++s) {
+        for (int s = 0; s < G::kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), 1);
         }
@@ -317,13 +507,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         prefetch_tensormap(&map_b);
     }
     if (warp == 1) {
-        tmem_alloc<2>(ptx::smem_addr(&sh.tmem_base), 512);
+        tmem_alloc<2>(ptx::smem_addr(&sh.tmem_base), 2 * BT);
         fence_before();
     }
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anything signals them
     fence_after();
     const uint32_t tmem = sh.tmem_base;
+    wait_dependencies();  // what earlier launches write is there from here on
+
+    // epilogue warps: their TMEM lanes, columns and staging
+    const int q = warp & 3;              // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;    // columns [half * BT/2, half * BT/2 + BT/2)
+    uint8_t *stage_buf = smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
+    bool ok = true;
 
     if (warp == 0) {
         // ===================== producer =====================================
@@ -331,11 +528,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
-        bool ok = true;
         for (int64_t t = unit; t < total && ok; t += nunits) {
             const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
-            const int i0 = c.ti * pair::kTile + (int)rank * 128;
-            const int j0 = c.tj * pair::kTile + (int)rank * 128;
+            const int i0 = c.ti * pair::kTileI + (int)rank * 128;
+            const int j0 = c.tj * BT + (int)rank * (BT / 2);
             for (int kb = 0; kb < num_kb; ++kb) {
                 const bool got = role_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1u,
                                            a.wait_limit_ns, abort_flag);
@@ -343,19 +539,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                     ok = false;
                     break;
                 }
-                const bool stall = a.inject_stall && unit == 0 && issued == 0;
+                const bool stall = a.inject_stall && unit == 0 && part == 0 && issued == 0;
                 if (lane == 0 && !stall) {  // test hook: the first stage is never armed
                     const uint32_t local_full = ptx::smem_addr(&sh.full[stage]);
-                    const uint32_t bar = map_to_rank(local_full, 0);  // both CTAs' loads
+                    const uint32_t bar = map_to_rank(local_full, lead);  // both CTAs' loads
                     if (leader)
-                        ptx::mbar_arrive_expect_tx(local_full, 2 * pair::kStage);
-                    const uint32_t sa = base + stage * pair::kStage;
-                    load_operand<2, 128>(sa, &map_a, a.a_mn, i0, kb * kBK, bar, pol);
-                    load_operand<2, 128>(sa + pair::kOperand, &map_b, a.b_mn, j0, kb * kBK, bar, pol);
+                        ptx::mbar_arrive_expect_tx(local_full, 2 * G::kStage);
+                    const uint32_t sa = base + stage * G::kStage;
+                    load_operand<2, 128>(sa, &map_a, a.a_mn, i0, (kb0 + kb) * kBK, bar, pol);
+                    load_operand<2, BT / 2>(sa + pair::kA, &map_b, a.b_mn, j0, (kb0 + kb) * kBK, bar, pol);
                 }
                 __syncwarp();
                 ++issued;
-                if (++stage == pair::kStages) {
+                if (++stage == G::kStages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -367,34 +563,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         // drain: every load this warp issued has landed before the CTA may exit
         if (leader) {
-            const int64_t pending = issued < pair::kStages ? issued : pair::kStages;
-            for (int64_t q = 0; q < pending; ++q) {
-                const int64_t idx = issued - 1 - q;
-                ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % pair::kStages]),
-                               (uint32_t)((idx / pair::kStages) & 1), kDrainLimitNs);
+            const int64_t pending = issued < G::kStages ? issued : G::kStages;
+            for (int64_t d = 0; d < pending; ++d) {
+                const int64_t idx = issued - 1 - d;
+                ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
+                               (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
             }
         } else if (!ok && issued > 0) {
             sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
         }
     } else if (warp == 1) {
         // ===================== MMA issuer (leader CTA) ======================
-        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, 256);
+        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, BT);
         const uint32_t step_a = a.a_mn ? UK * 128 : UK * 2, step_b = a.b_mn ? UK * 128 : UK * 2;
         const uint32_t lbo_a = a.a_mn ? kMnBox : 16, lbo_b = a.b_mn ? kMnBox : 16;
+        const uint16_t both = (uint16_t)(3u << lead);
         int stage = 0;
         uint32_t phase = 0;
         int64_t nchunk = 0;  // chunks issued so far: accumulator nchunk & 1
         bool issued_any = false;
-        bool ok = true;
         for (int64_t t = unit; leader && t < total && ok; t += nunits) {
+            int in_chunk = 0;
             for (int kb = 0; kb < num_kb; ++kb) {
-                const int in_chunk = kb % a.chunk;
                 const int acc = (int)(nchunk & 1);
                 bool got = true;
-                if (in_chunk == 0) {
+                if (in_chunk == 0)
                     got = role_wait(ptx::smem_addr(&sh.tmem_empty[acc]),
                                     (uint32_t)((nchunk >> 1) & 1) ^ 1u, a.wait_limit_ns, abort_flag);
-                }
                 got = got && role_wait(ptx::smem_addr(&sh.full[stage]), phase, a.wait_limit_ns,
                                        abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -404,22 +599,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 fence_after();
                 const bool last = in_chunk + 1 == a.chunk || kb + 1 == num_kb;
                 if (lane == 0) {
-                    const uint32_t sa = base + stage * pair::kStage;
-                    const uint32_t sb = sa + pair::kOperand;
+                    const uint32_t sa = base + stage * G::kStage;
+                    const uint32_t sb = sa + pair::kA;
 #pragma unroll
                     for (int k = 0; k < kBK / UK; ++k)
-                        mma_f16<2>(tmem + (uint32_t)(acc * 256), smem_desc(sa + k * step_a, lbo_a, 1024),
+                        mma_f16<2>(tmem + (uint32_t)(acc * BT), smem_desc(sa + k * step_a, lbo_a, 1024),
                                    smem_desc(sb + k * step_b, lbo_b, 1024), idesc,
                                    (in_chunk | k) != 0 ? 1u : 0u);
-                    mma_commit<2>(ptx::smem_addr(&sh.empty[stage]));
+                    mma_commit_to(ptx::smem_addr(&sh.empty[stage]), both);
                     if (last)
-                        mma_commit<2>(ptx::smem_addr(&sh.tmem_full[acc]));
+                        mma_commit_to(ptx::smem_addr(&sh.tmem_full[acc]), both);
                 }
                 __syncwarp();
                 issued_any = true;
-                if (last)
+                ++in_chunk;
+                if (last) {
                     ++nchunk;
-                if (++stage == pair::kStages) {
+                    in_chunk = 0;
+                }
+                if (++stage == G::kStages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -438,21 +636,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
     } else {
         // ===================== epilogue (warps 2-9) =========================
-        const int q = warp & 3;              // TMEM lane quarter this warp may access
-        const int half = (warp - 2) >> 2;    // columns [half*128, half*128 + 128)
-        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+        constexpr int kCols = BT / 2;            // this warp's columns
+        constexpr int kGroups = kCols / kStageCols;
+        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * kCols);
+        const uint32_t empty0 = map_to_rank(ptx::smem_addr(&sh.tmem_empty[0]), lead);
+        const Rows aux = aux_of<EPI>(a);
+        const bool early = aux.p != nullptr && parts == 1;
         const int chunks = (num_kb + a.chunk - 1) / a.chunk;
         int64_t nchunk = 0;
-        bool ok = true;
         for (int64_t t = unit; t < total && ok; t += nunits) {
             const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
-            const int64_t i = (int64_t)c.ti * pair::kTile + (int)rank * 128 + q * 32 + lane;
-            const int64_t j0 = (int64_t)c.tj * pair::kTile + half * 128;
-            const float bias = EPI == kEpiForward ? load_bias(a, i) : 0.0f;
-            float sum[EPI == kEpiGradW ? 128 : 1];
+            const int64_t i0 = (int64_t)c.ti * pair::kTileI + (int)rank * 128 + q * 32;
+            const int64_t j0 = (int64_t)c.tj * BT + half * kCols;
+            const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
+            uint4 pre[8];
+            if (EPI != kEpiGradW && early)  // the first group's rows, while the MMAs run
+                read_rows(aux, a.I, i0, j0, valid64(a.J, j0), lane, pre);
+            float sum[EPI == kEpiGradW ? kCols : 1];
             if constexpr (EPI == kEpiGradW) {
 #pragma unroll
-                for (int u = 0; u < 128; ++u)
+                for (int u = 0; u < kCols; ++u)
                     sum[u] = 0.0f;
             }
             for (int h = 0; h < chunks; ++h, ++nchunk) {
@@ -464,47 +667,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                     break;
                 }
                 fence_after();
-                const uint32_t t_addr = t_lane + (uint32_t)(acc * 256);
+                const uint32_t t_addr = t_lane + (uint32_t)(acc * BT);
+                const auto from_tmem = [&](int col, float(&v)[16]) {
+                    uint32_t r[16];
+                    tmem_ld16(t_addr + (uint32_t)col, r);
+                    tmem_wait16(r);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        v[u] = __uint_as_float(r[u]);
+                };
                 if constexpr (EPI == kEpiGradW) {
 #pragma unroll
-                    for (int c16 = 0; c16 < 8; ++c16) {
-                        uint32_t r[16];
-                        tmem_ld16(t_addr + c16 * 16, r);
-                        tmem_wait16(r);
+                    for (int col = 0; col < kCols; col += 16) {
+                        float v[16];
+                        from_tmem(col, v);
 #pragma unroll
                         for (int u = 0; u < 16; ++u)
-                            sum[c16 * 16 + u] += __uint_as_float(r[u]);
+                            sum[col + u] += v[u];
+                    }
+                } else if (parts > 1) {  // every load and MMA of this CTA is done: the ring is free
+                    float *partial = reinterpret_cast<float *>(smem) + half * kCols * 128 + q * 32 + lane;
+#pragma unroll 1
+                    for (int col = 0; col < kCols; col += 16) {
+                        float v[16];
+                        from_tmem(col, v);
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            partial[(col + u) * 128] = v[u];
                     }
                 } else {
 #pragma unroll 1
-                    for (int c16 = 0; c16 < 8; ++c16) {
-                        uint32_t r[16];
-                        tmem_ld16(t_addr + c16 * 16, r);
-                        tmem_wait16(r);
-                        float v[16];
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            v[u] = __uint_as_float(r[u]);
-                        const int n = valid16(a.J, j0 + c16 * 16);
-                        emit16<EPI>(a, i, j0 + c16 * 16, 1, n, v, bias);
-                        __syncwarp();
+                    for (int g = 0; g < kGroups; ++g) {
+                        const int64_t jg = j0 + g * kStageCols;
+                        emit64<EPI>(a, i0, jg, valid64(a.J, jg), lane, bias, early, pre, stage_buf,
+                                    [&](int col, float(&v)[16]) { from_tmem(g * kStageCols + col, v); });
+                        if (early && g + 1 < kGroups)
+                            read_rows(aux, a.I, i0, jg + kStageCols, valid64(a.J, jg + kStageCols), lane, pre);
                     }
                 }
                 // accumulator read: hand it back to the leader's MMA warp
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(map_to_rank(ptx::smem_addr(&sh.tmem_empty[acc]), 0));
+                    mbar_arrive_cluster(empty0 + (uint32_t)(acc * sizeof(uint64_t)));
             }
             if constexpr (EPI == kEpiGradW) {
-                if (ok) {
+                if (ok && parts > 1) {
+                    float *partial = reinterpret_cast<float *>(smem) + half * kCols * 128 + q * 32 + lane;
 #pragma unroll
-                    for (int c16 = 0; c16 < 8; ++c16) {
+                    for (int u = 0; u < kCols; ++u)
+                        partial[u * 128] = sum[u];
+                } else if (ok && a.out_f32) {
+#pragma unroll
+                    for (int col = 0; col < kCols; col += 16) {
                         float v[16];
 #pragma unroll
                         for (int u = 0; u < 16; ++u)
-                            v[u] = sum[c16 * 16 + u];
-                        emit16<EPI>(a, i, j0 + c16 * 16, 1, valid16(a.J, j0 + c16 * 16), v, 0.0f);
+                            v[u] = sum[col + u];
+                        emit16<EPI>(a, i0 + lane, j0 + col, 1, valid16(a.J, j0 + col), v, 0.0f);
+                    }
+                } else if (ok) {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        const int64_t jg = j0 + g * kStageCols;
+                        if (early)
+                            read_rows(aux, a.I, i0, jg, valid64(a.J, jg), lane, pre);
+                        emit64<EPI>(a, i0, jg, valid64(a.J, jg), lane, 0.0f, early, pre, stage_buf,
+                                    [&](int col, float(&v)[16]) {
+#pragma unroll
+                                        for (int u = 0; u < 16; ++u)
+                                            v[u] = sum[g * kStageCols + col + u];
+                                    });
                     }
                 }
             }
@@ -516,13 +749,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
     }
 
+    __syncthreads();
+    if (parts > 1) {
+        // the pairs' partial tiles, added in order; pair `part` finishes columns
+        // [part, part + 1) * BT / parts, its CTAs their own 128 features
+        cluster_sync();
+        if (warp >= 2 && ok) {
+            const pair::Tile c = pair::tile_at(a, unit, tiles_i, tiles_j);
+            const int cols = BT / parts / 2;  // per warp: 16, 32 or 64
+            const int col0 = part * (BT / parts) + half * cols;
+            const int64_t i0 = (int64_t)c.ti * pair::kTileI + (int)rank * 128 + q * 32;
+            const int64_t j0 = (int64_t)c.tj * BT + col0;
+            const int64_t left = a.J - j0;
+            const int n = left > cols ? cols : (left > 0 ? (int)left : 0);
+            const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
+            const uint32_t mine = base + (uint32_t)((col0 * 128 + q * 32 + lane) * 4);
+            const auto joined = [&](int col, float(&v)[16]) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = 0.0f;
+#pragma unroll 1
+                for (int s = 0; s < parts; ++s) {
+                    const uint32_t src = map_to_rank(mine, 2 * (uint32_t)s + rank) + (uint32_t)col * 512;
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        v[u] += ld_cluster_f32(src + (uint32_t)u * 512);
+                }
+            };
+            if (EPI == kEpiGradW && a.out_f32) {
+#pragma unroll 1
+                for (int col = 0; col < n; col += 16) {
+                    float v[16];
+                    joined(col, v);
+                    emit16<EPI>(a, i0 + lane, j0 + col, 1, n - col < 16 ? n - col : 16, v, 0.0f);
+                }
+            } else if (n > 0) {
+                const Rows aux = aux_of<EPI>(a);
+                uint4 pre[8];
+                if (aux.p)
+                    read_rows(aux, a.I, i0, j0, n, lane, pre);
+                emit64<EPI>(a, i0, j0, n, lane, bias, aux.p != nullptr, pre, stage_buf, joined);
+            }
+        }
+        __syncwarp();
+    }
+
     // ---- teardown ---------------------------------------------------------------
     fence_before();
     __syncthreads();
-    cluster_sync();  // the leader's MMAs into the peer's TMEM and smem are done
+    cluster_sync();  // the leader's MMAs into the peer's TMEM and smem are done, partials read
     if (warp == 1) {
         fence_after();
-        tmem_dealloc<2>(tmem, 512);
+        tmem_dealloc<2>(tmem, 2 * BT);
     }
 }
 
@@ -535,7 +813,7 @@ struct Geo {
     static constexpr int kB = BT * kBK * 2;
     static constexpr int kStage = kA + kB;
     // about 100 KB of ring, so that two CTAs share an SM
-    static constexpr int kStages = BT == 16 ? 6 : BT == 32 ? 5 : BT == 64 ? 4 : 3;
+    static constexpr int kStages = BT == 16 ? 6 : BT == 32 ? 5 : 4;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kPartial = 128 * BT * 4;  // float32 partial tile, over the spent ring
     static constexpr int kTmemCols = 2 * BT;       // two accumulators (a power of two >= 32)
@@ -558,6 +836,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     Shared &sh = *reinterpret_cast<Shared *>(smem + G::kRing);
     volatile int *abort_flag = &sh.abort_flag;
 
+    launch_dependents();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
@@ -594,6 +873,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem_base;
+    wait_dependencies();
 
     const int q = warp & 3;  // epilogue: TMEM lane quarter
     const int64_t i = (int64_t)ti * 128 + q * 32 + lane;
@@ -646,10 +926,9 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         const uint32_t lbo_a = a.a_mn ? kMnBox : 16, lbo_b = a.b_mn ? kMnBox : 16;
         int stage = 0;
         uint32_t phase = 0;
-        int nchunk = 0;
+        int nchunk = 0, in_chunk = 0;
         bool issued_any = false;
         for (int kb = kb0; kb < kb1; ++kb) {
-            const int in_chunk = (kb - kb0) % a.chunk;
             const int acc = nchunk & 1;
             bool got = true;
             if (in_chunk == 0)
@@ -670,14 +949,17 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                     mma_f16<1>(tmem + (uint32_t)(acc * BT), smem_desc(sa + k * step_a, lbo_a, 1024),
                                smem_desc(sb + k * step_b, lbo_b, 1024), idesc,
                                (in_chunk | k) != 0 ? 1u : 0u);
-                mma_commit<1>(ptx::smem_addr(&sh.empty[stage]));
+                mma_commit_local<1>(ptx::smem_addr(&sh.empty[stage]));
                 if (last)
-                    mma_commit<1>(ptx::smem_addr(&sh.tmem_full[acc]));
+                    mma_commit_local<1>(ptx::smem_addr(&sh.tmem_full[acc]));
             }
             __syncwarp();
             issued_any = true;
-            if (last)
+            ++in_chunk;
+            if (last) {
                 ++nchunk;
+                in_chunk = 0;
+            }
             if (++stage == G::kStages) {
                 stage = 0;
                 phase ^= 1u;
@@ -978,13 +1260,36 @@ bool operand_map(CUtensorMap *map, const LinearArgs &a, const void *p, int64_t r
     return encode_map(map, dt, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int EPI>
-cudaError_t launch_pair(const LinearArgs &args, cudaStream_t s, const char **why)
+// A launch in clusters of `size`, allowed to start while the launch before it on
+// the stream finishes (the kernels wait for it after their own set-up).
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    ClusterLaunch(int size, int64_t grid, int threads, int smem, cudaStream_t s)
+    {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)size;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)grid, 1, 1);
+        cfg.blockDim = dim3((unsigned)threads, 1, 1);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+template <int EPI, int BT>
+cudaError_t launch_pair(const LinearArgs &args, int parts, cudaStream_t s, const char **why)
 {
+    using G = pair::Geo<BT>;
     static std::once_flag once[kMaxDevices], once_res[kMaxDevices];
     static cudaError_t result[kMaxDevices];
     static int resident_by_dev[kMaxDevices];
-    cudaError_t e = allow_smem(pair_kernel<EPI>, pair::kSmemBytes, once, result);
+    cudaError_t e = allow_smem(pair_kernel<EPI, BT>, G::kSmemBytes, once, result);
     if (e != cudaSuccess) {
         *why = "setting the shared-memory size of the linear kernel";
         return e;
@@ -992,38 +1297,30 @@ cudaError_t launch_pair(const LinearArgs &args, cudaStream_t s, const char **why
     const int dev = current_device();
     std::call_once(once_res[dev], [&] {
         int resident = 0;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(2, 1, 1);
-        cfg.blockDim = dim3(pair::kThreads, 1, 1);
-        cfg.dynamicSmemBytes = pair::kSmemBytes;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&resident, pair_kernel<EPI>, &cfg) != cudaSuccess)
+        ClusterLaunch l(2, 2, pair::kThreads, G::kSmemBytes, nullptr);
+        l.cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&resident, pair_kernel<EPI, BT>, &l.cfg) != cudaSuccess)
             resident = 0;
         (void)cudaGetLastError();
         resident_by_dev[dev] = resident;
     });
     CUtensorMap map_a, map_b;
     if (!operand_map(&map_a, args, args.a, args.I, args.lda, args.a_mn, 128) ||
-        !operand_map(&map_b, args, args.b, args.J, args.ldb, args.b_mn, 128)) {
+        !operand_map(&map_b, args, args.b, args.J, args.ldb, args.b_mn, BT / 2)) {
         *why = "encoding the operands' tensor maps";
         return cudaErrorInvalidValue;
     }
     LinearArgs a = args;
-    const int64_t tiles_i = (a.I + pair::kTile - 1) / pair::kTile;
-    const int64_t tiles_j = (a.J + pair::kTile - 1) / pair::kTile;
+    const int64_t tiles_i = (a.I + pair::kTileI - 1) / pair::kTileI;
+    const int64_t tiles_j = (a.J + BT - 1) / BT;
     // feature tiles in equal groups of at most 8: 76 pairs cover about 8 x 9 tiles
     const int64_t groups = (tiles_i + 7) / 8;
     a.group = (int)((tiles_i + groups - 1) / groups);
     const int resident = resident_by_dev[dev] > 0 ? resident_by_dev[dev] : kSMs / 2;
-    const int64_t clusters = gg_min64(resident, tiles_i * tiles_j);
-    pair_kernel<EPI><<<(int)(2 * clusters), pair::kThreads, pair::kSmemBytes, s>>>(map_a, map_b, a);
-    return cudaGetLastError();
+    // split tiles: one cluster each; whole ones: the pairs that fit walk them
+    const int64_t clusters = parts > 1 ? tiles_i * tiles_j : gg_min64(resident, tiles_i * tiles_j);
+    ClusterLaunch l(2 * parts, 2 * parts * clusters, pair::kThreads, G::kSmemBytes, s);
+    return cudaLaunchKernelEx(&l.cfg, pair_kernel<EPI, BT>, map_a, map_b, a);
 }
 
 template <int EPI, int BT>
@@ -1044,19 +1341,8 @@ cudaError_t launch_split(const LinearArgs &a, int parts, cudaStream_t s, const c
         return cudaErrorInvalidValue;
     }
     const int64_t tiles = ((a.I + 127) / 128) * ((a.J + BT - 1) / BT);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)parts;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(tiles * parts), 1, 1);
-    cfg.blockDim = dim3(split::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = G::kSmemBytes;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_kernel<EPI, BT>, map_a, map_b, a);
+    ClusterLaunch l(parts, tiles * parts, split::kThreads, G::kSmemBytes, s);
+    return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }
 
 template <int EPI>
@@ -1068,7 +1354,8 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
         return cudaGetLastError();
     }
     if (p.kernel == GG_LINEAR_PAIR)
-        return launch_pair<EPI>(a, s, why);
+        return p.bt == 256 ? launch_pair<EPI, 256>(a, p.split, s, why)
+                           : launch_pair<EPI, 128>(a, p.split, s, why);
     switch (p.bt) {
     case 16:
         if constexpr (EPI != kEpiGradW)
@@ -1079,7 +1366,6 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
             return launch_split<EPI, 32>(a, p.split, s, why);
         break;
     case 64: return launch_split<EPI, 64>(a, p.split, s, why);
-    case 128: return launch_split<EPI, 128>(a, p.split, s, why);
     }
     *why = "no such tile";
     return cudaErrorInvalidValue;
@@ -1087,36 +1373,56 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
 
 }  // namespace
 
-// Which kernel, tile and split.  Token tiles are the smallest that hold all
-// tokens, 128 at most (64 at least for a weight gradient, whose MN-major B
-// comes in boxes of 64).  The split fills the GPU's SMs: as many CTAs per tile
-// as tiles leave room for, 8 (a portable cluster) and one k-block each at most.
-// The pair kernel takes a product whose estimated time there is shorter: waves
-// of 256 x 256 tiles over 76 pairs at 4 x 128 cycles a k-block, against waves of
-// the split kernel's CTAs (two per SM) at 4 x max(BT / 2, 32) cycles.
+// Which kernel, tile and split, by an estimate of each one's time in SM cycles:
+// waves x k-blocks x cycles of a k-block (the larger of its MMAs and of its
+// operand loads at 56 bytes a cycle and SM), plus what a tile costs besides.
+//  * split kernel: the smallest token tile that holds all tokens, 64 at most (a
+//    weight gradient, whose MN-major B comes in boxes of 64: 64); as many CTAs
+//    per tile as the tiles leave SMs for, 8 (a portable cluster) and one k-block
+//    each at most.
+//  * pair kernel: 256 x 256 or 256 x 128 tiles, whole ones walked by 76 pairs,
+//    or, where all the clusters fit at once, split between 2 or 4 pairs.
 LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
 {
-    LinearPlan p{GG_LINEAR_NONE, 0, 0};
-    if (I <= 0 || J <= 0)
-        return p;
-    if (K <= 0)
-        return p;
+    LinearPlan best{GG_LINEAR_NONE, 0, 0};
+    if (I <= 0 || J <= 0 || K <= 0)
+        return best;
     const int64_t num_kb = (K + kBK - 1) / kBK;
-    int bt = epi == kEpiGradW ? 64 : 16;
-    while (bt < 128 && bt < J)
-        bt *= 2;
-    const int64_t tiles = ((I + 127) / 128) * ((J + bt - 1) / bt);
-    int64_t parts = kSMs / tiles;
-    parts = parts < 1 ? 1 : (parts > 8 ? 8 : parts);
-    parts = gg_min64(parts, num_kb);
-    p.bt = bt;
-    p.split = (int)parts;
-    const int64_t pair_tiles = ((I + 255) / 256) * ((J + 255) / 256);
-    const int64_t pair_cost = (pair_tiles + kSMs / 2 - 1) / (kSMs / 2) * num_kb * 512;
-    const int64_t split_cost = (tiles * parts + kSMs - 1) / kSMs * ((num_kb + parts - 1) / parts) * 4 *
-                               (bt / 2 > 32 ? bt / 2 : 32) * 5 / 4;
-    p.kernel = path != 0 ? path : (pair_cost < split_cost ? GG_LINEAR_PAIR : GG_LINEAR_SPLIT);
-    return p;
+    int64_t cost = INT64_MAX;
+    const auto offer = [&](int kernel, int bt, int64_t parts, int64_t c) {
+        if ((path == GG_LINEAR_AUTO || path == kernel) && c < cost) {
+            cost = c;
+            best = LinearPlan{kernel, bt, (int)parts};
+        }
+    };
+    {
+        int bt = epi == kEpiGradW ? 64 : 16;
+        while (bt < 64 && bt < J)
+            bt *= 2;
+        const int64_t tiles = ((I + 127) / 128) * ((J + bt - 1) / bt);
+        int64_t parts = kSMs / tiles;
+        parts = parts < 1 ? 1 : (parts > 8 ? 8 : parts);
+        parts = gg_min64(parts, num_kb);
+        const int64_t kb_cycles = (128 + bt) * kBK * 2 / 56;
+        offer(GG_LINEAR_SPLIT, bt, parts,
+              (tiles * parts + kSMs - 1) / kSMs * ((num_kb + parts - 1) / parts * kb_cycles + 1000 +
+                                                   bt * 16));
+    }
+    for (int bt = 256; bt >= 128; bt /= 2) {
+        const int64_t tiles = ((I + 255) / 256) * ((J + bt - 1) / bt);
+        for (int parts = 1; parts <= 4; parts *= 2) {
+            // 2 CTAs a pair, and clusters of 4 or 8 CTAs do not fill every SM
+            const int64_t room = parts == 1 ? 76 : parts == 2 ? 36 : 16;
+            if (parts > 1 && (tiles > room || num_kb < parts))
+                break;
+            const int64_t mma = bt * 2, load = (128 + bt / 2) * kBK * 2 / 56;
+            const int64_t waves = (tiles + room - 1) / room;
+            offer(GG_LINEAR_PAIR, bt, parts,
+                  waves * ((num_kb + parts - 1) / parts) * (mma > load ? mma : load) + 2000 + bt * 12 +
+                      (parts > 1 ? 1500 : 0));
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, cudaStream_t s,

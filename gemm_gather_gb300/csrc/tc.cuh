@@ -181,21 +181,15 @@ __device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_
             : "memory");
 }
 
-// Arrive on `bar` once the issuing thread's earlier MMAs are done; with CG = 2
-// the arrival goes to the barrier at that offset in both CTAs of the pair.
-template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+// Arrive on the barrier at that offset in the CTAs of the cluster that `ranks`
+// names, once the issuing thread's earlier MMAs are done.
+__device__ __forceinline__ void mma_commit_to(uint32_t bar, uint16_t ranks)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-            "[%0], %1;" ::"r"(bar),
-            "h"((uint16_t)0x3)
-            : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(ranks)
+        : "memory");
 }
 
 // Arrive on `bar` in the issuing CTA only.
@@ -233,6 +227,19 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
                    "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+
+// ---- dependent launches ----------------------------------------------------------
+// The launch after this one on the stream may begin its own set-up.
+__device__ __forceinline__ void launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Wait until the launch before this one has completed and its writes are visible.
+__device__ __forceinline__ void wait_dependencies()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- bounded waits -----------------------------------------------------------------
