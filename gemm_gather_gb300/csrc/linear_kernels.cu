@@ -10,7 +10,11 @@
 //                      W N x K:  i = k, j = n                           A = X,  B = dZ
 // An operand whose contraction index is contiguous in memory is K-major, else
 // MN-major; tcgen05 reads both from 128-byte swizzled shared memory, so no
-// operand is ever transposed in memory.  Features on the MMA's 128 rows: a
+// operand is ever transposed in memory.  One thread issues the MMAs, chosen by
+// elect.sync: behind `lane == 0`, a condition the compiler takes for any
+// thread's, the issue alone took 645 cycles a k-block of 512 tensor cycles, and
+// the tensor pipes stood at 78%; elected, at 96% (256 x 256 tiles, K = 8192).
+// Features on the MMA's 128 rows: a
 // thread of the epilogue owns one feature, its warp 32 neighbouring ones, so
 // the bias is one register, every global access of the epilogue is 32
 // neighbouring elements at any alignment, and a product of a few tokens pads
@@ -525,6 +529,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     if (warp == 0) {
         // ===================== producer =====================================
         const uint64_t pol = ptx::policy_evict_normal();
+        const bool elected = ptx::elect_one_sync();
         int stage = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
                     break;
                 }
                 const bool stall = a.inject_stall && unit == 0 && part == 0 && issued == 0;
-                if (lane == 0 && !stall) {  // test hook: the first stage is never armed
+                if (elected && !stall) {  // test hook: the first stage is never armed
                     const uint32_t local_full = ptx::smem_addr(&sh.full[stage]);
                     const uint32_t bar = map_to_rank(local_full, lead);  // both CTAs' loads
                     if (leader)
@@ -575,8 +580,11 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     } else if (warp == 1) {
         // ===================== MMA issuer (leader CTA) ======================
         const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, BT);
-        const uint32_t step_a = a.a_mn ? UK * 128 : UK * 2, step_b = a.b_mn ? UK * 128 : UK * 2;
-        const uint32_t lbo_a = a.a_mn ? kMnBox : 16, lbo_b = a.b_mn ? kMnBox : 16;
+        const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;  // 16 k further, in descriptors
+        const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
+        const uint32_t lo_a = desc_lo(base, a.a_mn ? kMnBox : 16);
+        const uint32_t lo_b = desc_lo(base + pair::kA, a.b_mn ? kMnBox : 16);
+        const bool elected = ptx::elect_one_sync();
         const uint16_t both = (uint16_t)(3u << lead);
         int stage = 0;
         uint32_t phase = 0;
@@ -598,14 +606,12 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
                 }
                 fence_after();
                 const bool last = in_chunk + 1 == a.chunk || kb + 1 == num_kb;
-                if (lane == 0) {
-                    const uint32_t sa = base + stage * G::kStage;
-                    const uint32_t sb = sa + pair::kA;
+                if (elected) {
+                    const uint32_t at = (uint32_t)(stage * G::kStage) >> 4;
 #pragma unroll
                     for (int k = 0; k < kBK / UK; ++k)
-                        mma_f16<2>(tmem + (uint32_t)(acc * BT), smem_desc(sa + k * step_a, lbo_a, 1024),
-                                   smem_desc(sb + k * step_b, lbo_b, 1024), idesc,
-                                   (in_chunk | k) != 0 ? 1u : 0u);
+                        mma_f16<2>(tmem + (uint32_t)(acc * BT), lo_a + at + k * step_a,
+                                   lo_b + at + k * step_b, idesc, (uint32_t)(in_chunk | k));
                     mma_commit_to(ptx::smem_addr(&sh.empty[stage]), both);
                     if (last)
                         mma_commit_to(ptx::smem_addr(&sh.tmem_full[acc]), both);
@@ -629,7 +635,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         }
         // drain: all MMAs of this thread have completed before TMEM is freed
         if (issued_any) {
-            if (lane == 0)
+            if (elected)
                 mma_commit_local<2>(ptx::smem_addr(&sh.mma_done));
             __syncwarp();
             ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
@@ -884,6 +890,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     if (warp == 0) {
         // ===================== producer =====================================
         const uint64_t pol = ptx::policy_evict_normal();
+        const bool elected = ptx::elect_one_sync();
         int stage = 0;
         uint32_t phase = 0;
         int issued = 0;
@@ -895,7 +902,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                 break;
             }
             const bool stall = a.inject_stall && tile == 0 && rank == 0 && issued == 0;
-            if (lane == 0 && !stall) {  // test hook: the first stage is never armed
+            if (elected && !stall) {  // test hook: the first stage is never armed
                 const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
                 ptx::mbar_arrive_expect_tx(bar, G::kStage);
                 const uint32_t sa = base + stage * G::kStage;
@@ -922,8 +929,11 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     } else if (warp == 1) {
         // ===================== MMA issuer ===================================
         const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 128, BT);
-        const uint32_t step_a = a.a_mn ? UK * 128 : UK * 2, step_b = a.b_mn ? UK * 128 : UK * 2;
-        const uint32_t lbo_a = a.a_mn ? kMnBox : 16, lbo_b = a.b_mn ? kMnBox : 16;
+        const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;
+        const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
+        const uint32_t lo_a = desc_lo(base, a.a_mn ? kMnBox : 16);
+        const uint32_t lo_b = desc_lo(base + split::kA, a.b_mn ? kMnBox : 16);
+        const bool elected = ptx::elect_one_sync();
         int stage = 0;
         uint32_t phase = 0;
         int nchunk = 0, in_chunk = 0;
@@ -941,14 +951,12 @@ __global__ void __launch_bounds__(split::kThreads, 2)
             }
             fence_after();
             const bool last = in_chunk + 1 == a.chunk || kb + 1 == kb1;
-            if (lane == 0) {
-                const uint32_t sa = base + stage * G::kStage;
-                const uint32_t sb = sa + split::kA;
+            if (elected) {
+                const uint32_t at = (uint32_t)(stage * G::kStage) >> 4;
 #pragma unroll
                 for (int k = 0; k < kBK / UK; ++k)
-                    mma_f16<1>(tmem + (uint32_t)(acc * BT), smem_desc(sa + k * step_a, lbo_a, 1024),
-                               smem_desc(sb + k * step_b, lbo_b, 1024), idesc,
-                               (in_chunk | k) != 0 ? 1u : 0u);
+                    mma_f16<1>(tmem + (uint32_t)(acc * BT), lo_a + at + k * step_a,
+                               lo_b + at + k * step_b, idesc, (uint32_t)(in_chunk | k));
                 mma_commit_local<1>(ptx::smem_addr(&sh.empty[stage]));
                 if (last)
                     mma_commit_local<1>(ptx::smem_addr(&sh.tmem_full[acc]));
@@ -970,7 +978,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
             report_status(a.status, kStatusTimeout);
         }
         if (issued_any) {
-            if (lane == 0)
+            if (elected)
                 mma_commit_local<1>(ptx::smem_addr(&sh.mma_done));
             __syncwarp();
             ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
