@@ -144,10 +144,10 @@ __device__ __forceinline__ void with_act(int act, F f)
     }
 }
 
-// One feature's sums for columns j0, j0 + jstep, ... (n of them, at most 16):
+// One feature's sums for columns j0, j0 + jstep, ... (n of them, at most C):
 // the epilogue and the store.  A warp's 32 lanes hold 32 neighbouring
-// features.  Loads of the 16 columns are issued together, ahead of their use.
-template <int EPI>
+// features.  Loads of the columns are issued together, ahead of their use.
+template <int EPI, int C = 16>
 __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j0, int jstep, int n,
                                        float (&v)[16], float bias)
 {
@@ -158,63 +158,63 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
             float *o = reinterpret_cast<float *>(a.out) + j0 * a.ldo + i;
             const int64_t step = (int64_t)jstep * a.ldo;
             if (a.accumulate) {
-                float old[16];
+                float old[C];
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
+                for (int u = 0; u < C; ++u)
                     old[u] = u < n ? o[u * step] : 0.0f;
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
+                for (int u = 0; u < C; ++u)
                     v[u] += old[u];
             }
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
+            for (int u = 0; u < C; ++u)
                 if (u < n)
                     o[u * step] = v[u];
             return;
         }
     }
-    float x[16];
+    float x[C];
     const void *aux = EPI == kEpiGradW ? (a.accumulate ? a.out : nullptr) : a.aux;
     const int64_t ldaux = EPI == kEpiGradW ? a.ldo : a.ldaux;
     if (aux != nullptr) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
+        for (int u = 0; u < C; ++u)
             x[u] = u < n ? load16(aux, (j0 + (int64_t)u * jstep) * ldaux + i, a.is_bf16) : 0.0f;
     }
     if constexpr (EPI == kEpiForward) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
+        for (int u = 0; u < C; ++u)
             v[u] += bias;
         if (a.zout != nullptr) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
+            for (int u = 0; u < C; ++u)
                 if (u < n)
                     store16(a.zout, (j0 + (int64_t)u * jstep) * a.ldz + i, v[u], a.is_bf16);
         }
         with_act(a.act, [&](auto c) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
+            for (int u = 0; u < C; ++u)
                 v[u] = act_value<decltype(c)::value>(v[u]);
         });
         if (aux != nullptr) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
+            for (int u = 0; u < C; ++u)
                 v[u] += x[u];
         }
     } else if constexpr (EPI == kEpiGradIn) {
         if (aux != nullptr)
             with_act(a.act, [&](auto c) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
+                for (int u = 0; u < C; ++u)
                     v[u] *= act_slope<decltype(c)::value>(x[u]);
             });
     } else if (aux != nullptr) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
+        for (int u = 0; u < C; ++u)
             v[u] += x[u];
     }
 #pragma unroll
-    for (int u = 0; u < 16; ++u)
+    for (int u = 0; u < C; ++u)
         if (u < n)
             store16(a.out, (j0 + (int64_t)u * jstep) * a.ldo + i, v[u], a.is_bf16);
 }
@@ -771,16 +771,18 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
             const uint32_t mine = base + (uint32_t)((col0 * 128 + q * 32 + lane) * 4);
             const auto joined = [&](int col, float(&v)[16]) {
+                float x[4][16];  // every pair's sums, all loads in flight
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    v[u] = 0.0f;
-#pragma unroll 1
-                for (int s = 0; s < parts; ++s) {
-                    const uint32_t src = map_to_rank(mine, 2 * (uint32_t)s + rank) + (uint32_t)col * 512;
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t from = 2 * (uint32_t)(s < parts ? s : 0) + rank;
+                    const uint32_t src = map_to_rank(mine, from) + (uint32_t)col * 512;
 #pragma unroll
                     for (int u = 0; u < 16; ++u)
-                        v[u] += ld_cluster_f32(src + (uint32_t)u * 512);
+                        x[s][u] = s < parts ? ld_cluster_f32(src + (uint32_t)u * 512) : 0.0f;
                 }
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
             };
             if (EPI == kEpiGradW && a.out_f32) {
 #pragma unroll 1
@@ -987,6 +989,10 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         // ===================== epilogue (warps 2-5) =========================
         const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
         float *partial = reinterpret_cast<float *>(smem) + q * 32 + lane;  // [column][feature]
+        uint8_t *stage_buf = smem + q * kWarpStage;  // over the spent ring, like partial
+        const int64_t i0 = i - lane;
+        const Rows aux = aux_of<EPI>(a);
+        uint4 pre[8];
         const int chunks = (kb1 - kb0 + a.chunk - 1) / a.chunk;
         float sum[EPI == kEpiGradW ? BT : 1];
         if constexpr (EPI == kEpiGradW) {
@@ -1019,18 +1025,25 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                     uint32_t r[16];
                     tmem_ld16(t_lane + (uint32_t)(acc * BT + c16 * 16), r);
                     tmem_wait16(r);
-                    if (parts > 1) {
+                    if (parts == 1)
+                        break;
 #pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            partial[(c16 * 16 + u) * 128] = __uint_as_float(r[u]);
-                    } else {
-                        float v[16];
+                    for (int u = 0; u < 16; ++u)
+                        partial[(c16 * 16 + u) * 128] = __uint_as_float(r[u]);
+                }
+                if (parts == 1) {
+                    const int n = valid64(a.J, jt) < BT ? valid64(a.J, jt) : BT;
+                    if (aux.p)
+                        read_rows(aux, a.I, i0, jt, n, lane, pre);
+                    emit64<EPI>(a, i0, jt, n, lane, bias, aux.p != nullptr, pre, stage_buf,
+                                [&](int col, float(&v)[16]) {
+                                    uint32_t r[16];
+                                    tmem_ld16(t_lane + (uint32_t)(acc * BT + col), r);
+                                    tmem_wait16(r);
 #pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            v[u] = __uint_as_float(r[u]);
-                        emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(a.J, jt + c16 * 16), v, bias);
-                        __syncwarp();
-                    }
+                                    for (int u = 0; u < 16; ++u)
+                                        v[u] = __uint_as_float(r[u]);
+                                });
                 }
             }
             fence_before();
@@ -1040,19 +1053,29 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         }
         if constexpr (EPI == kEpiGradW) {
             if (ok) {  // past the last chunk every load and MMA of this CTA is done
+                if (parts > 1) {
 #pragma unroll
-                for (int c16 = 0; c16 < BT / 16; ++c16) {
-                    if (parts > 1) {
+                    for (int u = 0; u < BT; ++u)
+                        partial[u * 128] = sum[u];
+                } else if (a.out_f32) {
 #pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            partial[(c16 * 16 + u) * 128] = sum[c16 * 16 + u];
-                    } else {
+                    for (int c16 = 0; c16 < BT / 16; ++c16) {
                         float v[16];
 #pragma unroll
                         for (int u = 0; u < 16; ++u)
                             v[u] = sum[c16 * 16 + u];
                         emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(a.J, jt + c16 * 16), v, 0.0f);
                     }
+                } else {
+                    const int n = valid64(a.J, jt) < BT ? valid64(a.J, jt) : BT;
+                    if (aux.p)
+                        read_rows(aux, a.I, i0, jt, n, lane, pre);
+                    emit64<EPI>(a, i0, jt, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
+                                [&](int col, float(&v)[16]) {
+#pragma unroll
+                                    for (int u = 0; u < 16; ++u)
+                                        v[u] = sum[col + u];
+                                });
                 }
             }
         }
@@ -1072,21 +1095,25 @@ __global__ void __launch_bounds__(split::kThreads, 2)
             const int64_t left = a.J - jt;  // valid columns of the tile
             const int cols = left < BT ? (int)left : BT;
 #pragma unroll 1
-            for (int c0 = rank; c0 < cols; c0 += 16 * parts) {
+            for (int c0 = rank; c0 < cols; c0 += 4 * parts) {
                 const int n = (cols - c0 + parts - 1) / parts;
-                float v[16];
+                float x[8][4];  // every CTA's sums of four columns, all loads in flight
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    v[u] = 0.0f;
-#pragma unroll 1
-                for (int s = 0; s < parts; ++s) {
-                    const uint32_t src = map_to_rank(mine, (uint32_t)s);
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t src = map_to_rank(mine, (uint32_t)(s < parts ? s : 0));
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        if (u < n)
-                            v[u] += ld_cluster_f32(src + (uint32_t)(c0 + u * parts) * 512);
+                    for (int u = 0; u < 4; ++u)
+                        x[s][u] = s < parts && u < n
+                                      ? ld_cluster_f32(src + (uint32_t)(c0 + u * parts) * 512)
+                                      : 0.0f;
                 }
-                emit16<EPI>(a, i, jt + c0, parts, n < 16 ? n : 16, v, bias);
+                float v[16] = {};
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        v[u] += x[s][u];
+                emit16<EPI, 4>(a, i, jt + c0, parts, n < 4 ? n : 4, v, bias);
             }
         }
         __syncwarp();
