@@ -29,6 +29,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "f32x2.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
 #include "ptx.cuh"
@@ -128,9 +129,8 @@ __device__ __forceinline__ void store4(void *p, int64_t at, int left, bool vec, 
     }
 }
 
-// Codes: the e4m3 values of four bytes, times the block's scale.
-__device__ __forceinline__ void load_codes(const void *p, int64_t at, int left, bool vec, float scale,
-                                           float (&x)[4])
+// Codes: the e4m3 values of four bytes.
+__device__ __forceinline__ void load_codes(const void *p, int64_t at, int left, bool vec, float (&x)[4])
 {
     const uint8_t *q = reinterpret_cast<const uint8_t *>(p) + at;
     uint32_t bytes = 0;
@@ -145,41 +145,9 @@ __device__ __forceinline__ void load_codes(const void *p, int64_t at, int left, 
     for (int h = 0; h < 2; ++h) {
         const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(bytes >> (16 * h)), __NV_E4M3);
         const float2 f = __half22float2(__half2(r));
-        x[2 * h] = f.x * scale;
-        x[2 * h + 1] = f.y * scale;
+        x[2 * h] = f.x;
+        x[2 * h + 1] = f.y;
     }
-}
-
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
-
-// The block's largest finite magnitude over the warp.
-__device__ __forceinline__ float block_top(const float (&x)[8])
-{
-    float top = 0.0f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-        top = finite(x[u]) ? fmaxf(top, fabsf(x[u])) : top;
-    return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-}
-
-// Exponent k of the scale 2^k with top / 2^k in (224, 448]: 448 = 1.75 * 2^8, so
-// adding 0x1fffff to the bits carries into the exponent beyond 1.75.
-__device__ __forceinline__ int scale_exp(float top)
-{
-    const int k = (int)((__float_as_uint(top) + 0x1fffffu) >> 23) - 127 - 8;
-    return k < -118 ? -118 : k;
-}
-
-// One of the two e4m3 neighbours of x (|x| <= 448), upwards with the
-// probability of the remainder: 16 random bits are added below the code's
-// mantissa and the rest cut off.  Below 2^-6, where the code's step stays
-// 2^-9, the same on |x| + 2^-6.
-__device__ __forceinline__ float round_e4m3(float x, uint32_t r16)
-{
-    const float a = fabsf(x);
-    const float off = a < 0.015625f ? 0.015625f : 0.0f;
-    const float y = __uint_as_float((__float_as_uint(a + off) + (r16 << 4)) & 0xfff00000u) - off;
-    return copysignf(finite(x) ? y : NAN, x);
 }
 
 __device__ __forceinline__ void store_codes(void *p, int64_t at, int left, bool vec, const float *x)
@@ -196,6 +164,64 @@ __device__ __forceinline__ void store_codes(void *p, int64_t at, int left, bool 
             if (u < left)
                 q[u] = (uint8_t)(bytes >> (8 * u));
     }
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
+// The largest magnitude of the warp's block, as bits: not below 0x7f800000
+// where a value is not finite.
+__device__ __forceinline__ uint32_t block_top(const float (&x)[8])
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        top = max(top, __float_as_uint(x[u]) & 0x7fffffffu);
+    return __reduce_max_sync(~0u, top);
+}
+
+// The same over the finite values.
+__device__ __forceinline__ uint32_t finite_top(const float (&x)[8])
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        top = finite(x[u]) ? max(top, __float_as_uint(x[u]) & 0x7fffffffu) : top;
+    return __reduce_max_sync(~0u, top);
+}
+
+// Exponent k of the scale 2^k with top / 2^k in (224, 448]: 448 = 1.75 * 2^8, so
+// adding 0x1fffff to the bits carries into the exponent beyond 1.75.
+__device__ __forceinline__ int scale_exp(uint32_t top)
+{
+    const int k = (int)((top + 0x1fffffu) >> 23) - 127 - 8;
+    return k < -118 ? -118 : k;
+}
+
+// One of the two e4m3 neighbours of a finite x (|x| <= 448), away from zero with
+// the probability of the remainder: 16 random bits are added below the code's
+// mantissa and the rest is cut off.  Below 2^-6, where the code's step stays
+// 2^-9, the same on |x| + 2^-6.
+__device__ __forceinline__ float round_e4m3(float x, uint32_t r16_shifted)
+{
+    const bool low = fabsf(x) < 0.015625f;
+    const float off = __uint_as_float((__float_as_uint(x) & 0x80000000u) | 0x3c800000u);
+    const float y = low ? x + off : x;
+    const float z = __uint_as_float((__float_as_uint(y) + r16_shifted) & 0xfff00000u);
+    return low ? z - off : z;
+}
+
+__device__ __forceinline__ float sqrt_approx(float x)
+{
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <typename P, typename G, int BITS>
@@ -215,7 +241,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int64_t end = gg_min64(begin + g.chunk, t.n);
     const bool vec = t.vec != 0;
     const AdamwStep &h = g.h;
-    const float gscale = h.grad_scale ? *h.grad_scale : 1.0f;
+    const F2 gscale = pair_of(h.grad_scale ? *h.grad_scale : 1.0f);
+    const F2 beta1 = pair_of(h.beta1), omb1 = pair_of(h.one_minus_beta1);
+    const F2 beta2 = pair_of(h.beta2), omb2 = pair_of(h.one_minus_beta2);
+    const F2 ic2 = pair_of(h.inv_sqrt_c2), eps = pair_of(h.eps);
+    const F2 decay = pair_of(h.decay), minus_step = pair_of(-h.step_size);
 
 #pragma unroll 1
     for (int64_t base = begin + warp * kBlock; base < end; base += kStep) {
@@ -234,34 +264,35 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
             load4<P>(t.param, at, left[q], vec, p4);
             load4<G>(t.grad, at, left[q], vec, g4);
             if constexpr (BITS == 8) {
-                load_codes(t.m, at, left[q], vec, ms, m4);
-                load_codes(t.v, at, left[q], vec, vs, v4);
+                load_codes(t.m, at, left[q], vec, m4);
+                load_codes(t.v, at, left[q], vec, v4);
             } else {
                 load4<float>(t.m, at, left[q], vec, m4);
                 load4<float>(t.v, at, left[q], vec, v4);
             }
         }
+        // m and v are rounded operation by operation (no fused multiply-add), as the
+        // 8-bit states' definition has them; the update itself need not be
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = __fmul_rn(gr[e], gscale);
-            if constexpr (BITS == 8)
-                v[e] = __fmul_rn(v[e], v[e]);
-            m[e] = __fadd_rn(__fmul_rn(m[e], h.beta1), __fmul_rn(x, h.one_minus_beta1));
-            v[e] = __fadd_rn(__fmul_rn(v[e], h.beta2), __fmul_rn(__fmul_rn(x, x), h.one_minus_beta2));
-            u[e] = __fsqrt_rn(v[e]);
-            const float den = u[e] * h.inv_sqrt_c2 + h.eps;
-            p[e] = p[e] * h.decay - h.step_size * (m[e] / den);
-        }
-        float ims = 0.0f, ivs = 0.0f;
-        if constexpr (BITS == 8) {
-            // elements past the end hold m = v = 0
-            const int mk = scale_exp(block_top(m)), vk = scale_exp(block_top(u));
-            ims = __uint_as_float((uint32_t)(127 - mk) << 23);
-            ivs = __uint_as_float((uint32_t)(127 - vk) << 23);
-            if (lane == 0) {
-                t.m_scale[block] = __uint_as_float((uint32_t)(127 + mk) << 23);
-                t.v_scale[block] = __uint_as_float((uint32_t)(127 + vk) << 23);
+        for (int e = 0; e < 8; e += 2) {
+            const F2 x = mul2(pair_of(gr[e], gr[e + 1]), gscale);
+            F2 m2 = pair_of(m[e], m[e + 1]), v2 = pair_of(v[e], v[e + 1]);
+            if constexpr (BITS == 8) {
+                m2 = mul2(m2, pair_of(ms));
+                v2 = mul2(v2, pair_of(vs));
+                v2 = mul2(v2, v2);
             }
+            m2 = add2(mul2(m2, beta1), mul2(x, omb1));
+            v2 = add2(mul2(v2, beta2), mul2(mul2(x, x), omb2));
+            const float2 vh = halves_of(v2), mh = halves_of(m2);
+            const float2 uh = make_float2(sqrt_approx(vh.x), sqrt_approx(vh.y));
+            const float2 dh = halves_of(fma2(pair_of(uh.x, uh.y), ic2, eps));
+            const F2 q2 = mul2(m2, pair_of(rcp_approx(dh.x), rcp_approx(dh.y)));
+            const float2 ph = halves_of(fma2(q2, minus_step, mul2(pair_of(p[e], p[e + 1]), decay)));
+            m[e] = mh.x, m[e + 1] = mh.y;
+            v[e] = vh.x, v[e + 1] = vh.y;
+            u[e] = uh.x, u[e + 1] = uh.y;
+            p[e] = ph.x, p[e + 1] = ph.y;
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -274,20 +305,47 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 else
                     store4<__half>(t.copy, at, left[q], vec, p4);
             }
-            if constexpr (BITS == 8) {
+            if constexpr (BITS == 32) {
+                store4<float>(t.m, at, left[q], vec, *reinterpret_cast<float(*)[4]>(m + 4 * q));
+                store4<float>(t.v, at, left[q], vec, *reinterpret_cast<float(*)[4]>(v + 4 * q));
+            }
+        }
+        if constexpr (BITS == 8) {
+            // elements past the end hold m = v = 0.  The scale of sqrt(v) comes from
+            // the largest v: the square root rounds monotonically.
+            uint32_t mt = block_top(m), vt = block_top(v);
+            const bool odd = mt >= 0x7f800000u || vt >= 0x7f800000u;  // the whole warp's
+            if (odd) {
+                mt = finite_top(m);
+                vt = finite_top(v);
+            }
+            const int mk = scale_exp(mt);
+            const int vk = scale_exp(__float_as_uint(__fsqrt_rn(__uint_as_float(vt))));
+            const float ims = __uint_as_float((uint32_t)(127 - mk) << 23);
+            const float ivs = __uint_as_float((uint32_t)(127 - vk) << 23);
+            if (lane == 0) {
+                t.m_scale[block] = __uint_as_float((uint32_t)(127 + mk) << 23);
+                t.v_scale[block] = __uint_as_float((uint32_t)(127 + vk) << 23);
+            }
+            const uint32_t key = mix32((uint32_t)(base >> 32) ^ t.key);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t at = base + q * 128 + lane * 4;
+                const uint32_t first = (uint32_t)at ^ key;  // at is a multiple of 4
                 float cm[4], cv[4];
-                const uint32_t key = mix32((uint32_t)(at >> 32) ^ t.key);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t r = mix32((uint32_t)(at + e) ^ key);
-                    cm[e] = round_e4m3(m[4 * q + e] * ims, r & 0xffffu);
-                    cv[e] = round_e4m3(u[4 * q + e] * ivs, r >> 16);
+                    const uint32_t r = mix32(first ^ (uint32_t)e);
+                    const float y = m[4 * q + e] * ims, z = u[4 * q + e] * ivs;
+                    cm[e] = round_e4m3(y, (r & 0xffffu) << 4);
+                    cv[e] = round_e4m3(z, r >> 16 << 4);
+                    if (odd) {
+                        cm[e] = finite(m[4 * q + e]) ? cm[e] : NAN;
+                        cv[e] = finite(v[4 * q + e]) ? cv[e] : NAN;
+                    }
                 }
                 store_codes(t.m, at, left[q], vec, cm);
                 store_codes(t.v, at, left[q], vec, cv);
-            } else {
-                store4<float>(t.m, at, left[q], vec, *reinterpret_cast<float(*)[4]>(m + 4 * q));
-                store4<float>(t.v, at, left[q], vec, *reinterpret_cast<float(*)[4]>(v + 4 * q));
             }
         }
     }

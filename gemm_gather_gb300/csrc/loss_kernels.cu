@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "f32x2.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
 #include "tc.cuh"
@@ -87,35 +88,6 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, float c)
     Sum r;
     r.m = fmaxf(a.m, b.m);
     r.s = a.s * rescale(a.m, r.m, c) + b.s * rescale(b.m, r.m, c);
-    return r;
-}
-
-// Pairs of floats in one instruction each (sm_100 on).
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 pair_of(float lo, float hi)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 halves_of(F2 a)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
 
