@@ -18,6 +18,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "f32x2.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
@@ -30,33 +32,58 @@ constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kInvalidArg = GG_ERR_INVALID_ARG;
 
+// An element type: elements of a 16-byte vector, and pairs of them in (a pair of)
+// its four words.
 template <typename E>
 struct Elem;
 template <>
 struct Elem<float> {
     static constexpr int kVec = 4;
+    static constexpr uint32_t kMinusInf = 0xff800000u;
     static __device__ __forceinline__ float get(float x) { return x; }
     static __device__ __forceinline__ float put(float x) { return x; }
-    static __device__ __forceinline__ void put2(float *e, float2 x) { e[0] = x.x, e[1] = x.y; }
+    static __device__ __forceinline__ F2 pair(const uint32_t (&w)[4], int i)
+    {
+        return pair_of(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    static __device__ __forceinline__ void set(uint32_t (&w)[4], int i, F2 x)
+    {
+        const float2 f = halves_of(x);
+        w[2 * i] = __float_as_uint(f.x);
+        w[2 * i + 1] = __float_as_uint(f.y);
+    }
 };
 template <>
 struct Elem<__half> {
     static constexpr int kVec = 8;
+    static constexpr uint32_t kMinusInf = 0xfc00fc00u;
     static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
     static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
-    static __device__ __forceinline__ void put2(__half *e, float2 x)
+    static __device__ __forceinline__ F2 pair(const uint32_t (&w)[4], int i)
     {
-        *reinterpret_cast<__half2 *>(e) = __float22half2_rn(x);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        return pair_of(f.x, f.y);
+    }
+    static __device__ __forceinline__ void set(uint32_t (&w)[4], int i, F2 x)
+    {
+        const __half2 h = __float22half2_rn(halves_of(x));
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
 };
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int kVec = 8;
+    static constexpr uint32_t kMinusInf = 0xff80ff80u;
     static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-    static __device__ __forceinline__ void put2(__nv_bfloat16 *e, float2 x)
+    static __device__ __forceinline__ F2 pair(const uint32_t (&w)[4], int i)
     {
-        *reinterpret_cast<__nv_bfloat162 *>(e) = __float22bfloat162_rn(x);
+        return pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    static __device__ __forceinline__ void set(uint32_t (&w)[4], int i, F2 x)
+    {
+        const __nv_bfloat162 h = __float22bfloat162_rn(halves_of(x));
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
 };
 
@@ -91,40 +118,12 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, float c)
     return r;
 }
 
-// What a token's logp gives: the loss terms and dloss/dlogp.
-struct Terms {
-    float loss, kl, clipped, ratio, slope;
-};
-
-__device__ __forceinline__ Terms terms_of(const LossArgs &a, int64_t t, float logp)
-{
-    Terms r;
-    const float adv = a.advantage[t];
-    r.ratio = expf(logp - (a.old_logp ? a.old_logp[t] : logp));  // NaN for a row without a logp
-    const bool over = (adv > 0.0f && r.ratio > 1.0f + a.clip_high) ||
-                      (adv < 0.0f && r.ratio < 1.0f - a.clip_low);
-    r.clipped = over ? 1.0f : 0.0f;
-    const float held = fminf(fmaxf(r.ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
-    r.loss = -(over ? held : r.ratio) * adv;
-    r.slope = over ? 0.0f : -adv * r.ratio;
-    r.kl = 0.0f;
-    if (a.ref_logp && a.kl_coef != 0.0f) {
-        const float d = a.ref_logp[t] - logp;
-        const float e = expm1f(d);  // exp(d) - d - 1 without losing it for small d
-        r.kl = e - d;
-        r.loss += a.kl_coef * r.kl;
-        r.slope -= a.kl_coef * e;
-    }
-    return r;
-}
-
+// A vector is kept as its four words: as 16-bit elements the compiler splits it
+// into eight registers and packs and unpacks it at every use.
 template <typename E>
 struct alignas(16) Vec {
-    union {
-        E e[Elem<E>::kVec];
-        uint32_t w[4];
-    };
-    __device__ __forceinline__ Vec() {}
+    uint32_t w[4];
+    __device__ __forceinline__ void fill(uint32_t x) { w[0] = w[1] = w[2] = w[3] = x; }
 };
 
 // Keeps the compiler from carrying a vector's unpacked values from one pass over
@@ -138,239 +137,533 @@ __device__ __forceinline__ void stay_packed(Vec<E> &v)
 // The larger of top and a vector's elements (NaN is passed over, and shows in the sum).
 __device__ __forceinline__ float top_of(const Vec<float> &v, float top)
 {
-    return fmaxf(fmaxf(fmaxf(v.e[0], v.e[1]), fmaxf(v.e[2], v.e[3])), top);
+    return fmaxf(fmaxf(fmaxf(__uint_as_float(v.w[0]), __uint_as_float(v.w[1])),
+                       fmaxf(__uint_as_float(v.w[2]), __uint_as_float(v.w[3]))), top);
 }
 __device__ __forceinline__ float top_of(const Vec<__half> &v, float top)
 {
-    const __half2 *h = reinterpret_cast<const __half2 *>(v.e);
+    const __half2 *h = reinterpret_cast<const __half2 *>(v.w);
     const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(fmaxf(__low2float(m), __high2float(m)), top);
 }
 __device__ __forceinline__ float top_of(const Vec<__nv_bfloat16> &v, float top)
 {
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(v.e);
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(v.w);
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(fmaxf(__low2float(m), __high2float(m)), top);
+    const uint32_t b = *reinterpret_cast<const uint32_t *>(&m);
+    return fmaxf(fmaxf(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), top);
 }
 
-// 2^((x - m) c) of a vector's elements, in pairs.
+// 2^((x - m) c) of the i-th pair of a vector.
 template <typename E>
-__device__ __forceinline__ void powers_of(const Vec<E> &v, float m, float c,
-                                          float2 (&e)[Elem<E>::kVec / 2])
+__device__ __forceinline__ F2 power_of(const Vec<E> &v, int i, F2 minus_m, F2 cc)
 {
-    const F2 minus_m = pair_of(-m, -m), cc = pair_of(c, c);
+    const float2 y = halves_of(mul2(add2(Elem<E>::pair(v.w, i), minus_m), cc));
+    return pair_of(ex2(y.x), ex2(y.y));
+}
+
+// The sum of a vector's powers, added to `part`.
+template <typename E>
+__device__ __forceinline__ void add_powers(const Vec<E> &v, float m, float c, F2 (&part)[2])
+{
+    const F2 minus_m = pair_of(-m), cc = pair_of(c);
 #pragma unroll
-    for (int u = 0; u < Elem<E>::kVec / 2; ++u) {
-        const F2 x = pair_of(Elem<E>::get(v.e[2 * u]), Elem<E>::get(v.e[2 * u + 1]));
-        const float2 y = halves_of(mul2(add2(x, minus_m), cc));
-        e[u] = make_float2(ex2(y.x), ex2(y.y));
+    for (int u = 0; u < Elem<E>::kVec / 2; ++u)
+        part[u & 1] = add2(part[u & 1], power_of(v, u, minus_m, cc));
+}
+
+// One CTA's slice of a token's row, whole vectors from the input's first 16-byte
+// boundary on (V is below 2^31: indices are int).
+template <typename E>
+struct Slice {
+    const E *row;
+    E *out;  // or null
+    int lo, hi, v0, v1, nvec;
+    bool wide;  // the output's vectors are aligned as the input's
+    // The bounds of CTA `rank` of `parts`, the same for every row.
+    __device__ __forceinline__ Slice(const LossArgs &a, int rank, int parts)
+    {
+        constexpr int VEC = Elem<E>::kVec;
+        const int64_t units = (a.V + VEC - 1) / VEC;
+        lo = (int)(units * rank / parts * VEC);
+        hi = (int)gg_min64(units * (rank + 1) / parts * VEC, a.V);
+    }
+    __device__ __forceinline__ void at(const LossArgs &a, int64_t t)
+    {
+        constexpr int VEC = Elem<E>::kVec;
+        row = reinterpret_cast<const E *>(a.logits) + t * a.ld;
+        out = a.dlogits ? reinterpret_cast<E *>(a.dlogits) + t * a.ldd : nullptr;
+        const int head = (int)((16 - (reinterpret_cast<uint64_t>(row + lo) & 15)) & 15) / (int)sizeof(E);
+        v0 = lo + head < hi ? lo + head : hi;
+        nvec = (hi - v0) / VEC;
+        v1 = v0 + nvec * VEC;
+        wide = out && (reinterpret_cast<uint64_t>(out + v0) & 15) == 0;
+    }
+    // The ragged ends hold fewer than VEC elements each: one of either per thread.
+    __device__ __forceinline__ bool has_head(int tid) const { return tid < v0 - lo; }
+    __device__ __forceinline__ bool has_tail(int tid) const { return tid < hi - v1; }
+    __device__ __forceinline__ const Vec<E> *vec() const { return reinterpret_cast<const Vec<E> *>(row + v0); }
+
+    __device__ __forceinline__ void zero(int tid, int threads) const
+    {
+        if (!out)
+            return;
+        if (wide) {
+            for (int i = tid; i < nvec; i += threads)
+                reinterpret_cast<uint4 *>(out + v0)[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = v0 + tid; i < v1; i += threads)
+                out[i] = Elem<E>::put(0.0f);
+        }
+        if (has_head(tid))
+            out[lo + tid] = Elem<E>::put(0.0f);
+        if (has_tail(tid))
+            out[v1 + tid] = Elem<E>::put(0.0f);
+    }
+};
+
+// What a token brings beside its logits.
+struct Token {
+    float weight, advantage, old_logp, ref_logp;
+    int64_t target;
+    __device__ __forceinline__ Token(const LossArgs &a, int64_t t)
+    {
+        const bool there = t < a.T;
+        weight = there ? a.weight[t] : 0.0f;
+        advantage = there ? a.advantage[t] : 0.0f;
+        old_logp = there && a.old_logp ? a.old_logp[t] : 0.0f;
+        ref_logp = there && a.ref_logp ? a.ref_logp[t] : 0.0f;
+        target = there ? a.target[t] : -1;
+    }
+    __device__ __forceinline__ bool in_range(const LossArgs &a) const { return target >= 0 && target < a.V; }
+    __device__ __forceinline__ bool live(const LossArgs &a) const { return weight != 0.0f && in_range(a); }
+};
+
+// What a token's logp gives: the loss terms and dloss/dlogp.
+struct Terms {
+    float loss, kl, clipped, ratio, slope;
+};
+
+__device__ __forceinline__ Terms terms_of(const LossArgs &a, const Token &t, float logp)
+{
+    Terms r;
+    const float adv = t.advantage;
+    r.ratio = expf(logp - (a.old_logp ? t.old_logp : logp));  // NaN for a row without a logp
+    const bool over = (adv > 0.0f && r.ratio > 1.0f + a.clip_high) ||
+                      (adv < 0.0f && r.ratio < 1.0f - a.clip_low);
+    r.clipped = over ? 1.0f : 0.0f;
+    const float held = fminf(fmaxf(r.ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
+    r.loss = -(over ? held : r.ratio) * adv;
+    r.slope = over ? 0.0f : -adv * r.ratio;
+    r.kl = 0.0f;
+    if (a.ref_logp && a.kl_coef != 0.0f) {
+        const float d = t.ref_logp - logp;
+        const float e = expm1f(d);  // exp(d) - d - 1 without losing it for small d
+        r.kl = e - d;
+        r.loss += a.kl_coef * r.kl;
+        r.slope -= a.kl_coef * e;
+    }
+    return r;
+}
+
+// A token's gradient, from its row's sum: dlogits = coef (onehot - e / sum).
+template <typename E>
+struct Gradient {
+    float m, c, k, coef;
+    int target;
+    __device__ __forceinline__ Gradient(const LossArgs &a, const Token &t, const Sum &all, float logp, float c_)
+    {
+        m = base_of(all.m);
+        c = c_;
+        coef = t.weight * terms_of(a, t, logp).slope * a.inv_temperature * a.grad_scale;
+        k = -coef / all.s;
+        target = (int)t.target;
+    }
+    // -coef softmax of an element, and of a vector in place; the target's element
+    // has coef added.
+    __device__ __forceinline__ E one(float x) const { return Elem<E>::put(k * ex2((x - m) * c)); }
+    __device__ __forceinline__ E target_one(float x) const { return Elem<E>::put(fmaf(k, ex2((x - m) * c), coef)); }
+    __device__ __forceinline__ void softmax(Vec<E> &v) const
+    {
+        const F2 minus_m = pair_of(-m), cc = pair_of(c), kk = pair_of(k);
+#pragma unroll
+        for (int u = 0; u < Elem<E>::kVec / 2; ++u)
+            Elem<E>::set(v.w, u, mul2(power_of(v, u, minus_m, cc), kk));
+    }
+};
+
+__device__ __forceinline__ float warp_max(float x)
+{
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float warp_add(float x)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        x += __shfl_xor_sync(~0u, x, d);
+    return x;
+}
+
+// Lanes' sums as one.
+__device__ __forceinline__ Sum warp_join(Sum x, float c)
+{
+    Sum r;
+    r.m = warp_max(x.m);
+    r.s = warp_add(x.s * ex2((x.m - base_of(r.m)) * c));
+    return r;
+}
+
+// The warps' sums of all the cluster's CTAs, from `sums` (one per warp) of each:
+// lane i takes the i-th, from where they lie in distributed shared memory.
+struct Gather {
+    uint32_t at[2];
+    int warps, count;
+    __device__ __forceinline__ Gather(const Sum *sums, int warps_, int parts, int lane)
+        : warps(warps_), count(warps_ * parts)
+    {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            at[j] = address(sums, lane + 32 * j);
+    }
+    __device__ __forceinline__ uint32_t address(const Sum *sums, int i) const
+    {
+        const int p = i < count ? i / warps : 0, w = i < count ? i - p * warps : 0;
+        return tc::map_to_rank(ptx::smem_addr(sums + w), (uint32_t)p);
+    }
+    static __device__ __forceinline__ Sum load(uint32_t at)
+    {
+        Sum x;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.m), "=f"(x.s) : "r"(at) : "memory");
+        return x;
+    }
+    // `offset`: bytes from the sums given to the constructor
+    __device__ __forceinline__ Sum join_all(const Sum *sums, uint32_t offset, int lane, float c) const
+    {
+        Sum x{-INFINITY, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (lane + 32 * j < count) {
+                const Sum y = load(at[j] + offset);
+                x = j == 0 ? y : join(x, y, c);
+            }
+#pragma unroll 1
+        for (int i = lane + 64; i < count; i += 32)
+            x = join(x, load(address(sums, i) + offset), c);
+        return warp_join(x, c);
+    }
+};
+
+__device__ __forceinline__ float logp_of(const LossArgs &a, const Sum &all, float picked)
+{
+    return (picked - base_of(all.m)) * a.inv_temperature - logf(all.s);
+}
+
+// Clusters walk the tokens, each CTA with its slice of the row in shared memory,
+// so that a row is read from memory once.  Two passes: a running maximum and sum
+// of powers over the slice; then the gradient, where each vector that has been
+// used is at once replaced by the next row's (its copy runs under the rest of
+// this pass and the start of the next, which waits for it batch by batch).
+// A warp owns NV x 32 consecutive 16-byte vectors, a lane every 32nd of them: no
+// thread waits for another's copies, and all addresses of a lane are constants
+// apart.  What the kernel costs besides memory is instructions, 8 an element for
+// the powers: with a test and an address computed for each vector it was 24, and
+// the passes took longer than the memory; whole warps take a path without.
+constexpr int kBatch = 4;  // vectors of a lane that are waited for together
+
+// Wait for all but the newest `left` groups of this thread's copies.
+__device__ __forceinline__ void wait_groups(int left)
+{
+    switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
     }
 }
 
-// One cluster per token.  NV > 0: each thread keeps its NV 16-byte vectors of
-// the row in registers, so the row is read from memory once; all NV loads are
-// in flight together, and the sum needs no rescaling (a thread's maximum is
-// known before its first exponential).  NV == 0, for rows beyond what a
-// cluster's registers hold: a running maximum and sum, and a second read.
-template <typename E, int NV>
-__global__ void __launch_bounds__(1024) policy_loss_kernel(const __grid_constant__ LossArgs a)
-{
-    constexpr int VEC = Elem<E>::kVec;
-    __shared__ Sum warps[32];
-    __shared__ Sum mine;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the statistics' launch
-    const int64_t t = tc::cluster_id_x();
-    const int parts = (int)tc::cluster_size(), rank = (int)tc::cluster_ctarank();
-    const int tid = threadIdx.x, threads = blockDim.x;
-    const E *row = reinterpret_cast<const E *>(a.logits) + t * a.ld;
-    E *out = a.dlogits ? reinterpret_cast<E *>(a.dlogits) + t * a.ldd : nullptr;
-    // this CTA's slice, in units of VEC elements (V is below 2^31: row indices are int)
-    const int64_t units = (a.V + VEC - 1) / VEC;
-    const int lo = (int)(units * rank / parts * VEC);
-    const int hi = (int)gg_min64(units * (rank + 1) / parts * VEC, a.V);
-    // whole vectors from the first 16-byte boundary of the input on
-    const int head = (int)((16 - (reinterpret_cast<uint64_t>(row + lo) & 15)) & 15) / (int)sizeof(E);
-    const int v0 = lo + head < hi ? lo + head : hi;
-    const int nvec = (hi - v0) / VEC;
-    const int v1 = v0 + nvec * VEC;
-    const bool wide = out && (reinterpret_cast<uint64_t>(out + v0) & 15) == 0;
+__device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-    const float w = a.weight[t];
-    int target = 0;
-    bool live = w != 0.0f;
-    if (live) {
-        const int64_t id = a.target[t];
-        target = (int)id;
-        if (id < 0 || id >= a.V) {
-            live = false;
-            if (rank == 0 && tid == 0)
-                report_status(a.status, kInvalidArg);
+// A lane's NB * kBatch vectors: `slot` in shared memory, in steps of 512 bytes;
+// `have` of them exist (all, where FULL).
+template <typename E, int NB>
+struct Lane {
+    static constexpr int NV = NB * kBatch;
+    uint8_t *slot;
+    uint32_t slot_at;
+
+    template <bool FULL>
+    __device__ __forceinline__ void fetch(const uint8_t *from, int q, int have) const
+    {
+        if (FULL || q < have)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot_at + q * 512), "l"(from + q * 512)
+                         : "memory");
+    }
+    __device__ __forceinline__ void fetch_all(const uint8_t *from, int have) const
+    {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            fetch<false>(from, q, have);
+            if (q % kBatch == kBatch - 1)
+                commit_group();
         }
     }
-    if (!live) {  // the same for the whole cluster
-        if (rank == 0 && tid == 0)
-            a.logp_out[t] = 0.0f;
-        if (out) {
-            for (int i = lo + tid; i < v0; i += threads)
-                out[i] = Elem<E>::put(0.0f);
-            if (wide) {
-                for (int i = tid; i < nvec; i += threads)
-                    reinterpret_cast<uint4 *>(out + v0)[i] = make_uint4(0, 0, 0, 0);
-            } else {
-                for (int i = v0 + tid; i < v1; i += threads)
-                    out[i] = Elem<E>::put(0.0f);
-            }
-            for (int i = v1 + tid; i < hi; i += threads)
-                out[i] = Elem<E>::put(0.0f);
-        }
-        return;
+    template <bool FULL>
+    __device__ __forceinline__ void take(int q, int have, Vec<E> &v) const
+    {
+        if (!FULL)
+            v.fill(Elem<E>::kMinusInf);
+        if (FULL || q < have)
+            v = *reinterpret_cast<const Vec<E> *>(slot + q * 512);
     }
 
-    const float c = a.inv_temperature * kLog2e;
-    const Vec<E> *vec = reinterpret_cast<const Vec<E> *>(row + v0);
-    Vec<E> held[NV > 0 ? NV : 1];
-    if constexpr (NV > 0) {
+    // The running maximum and sum over the vectors.
+    template <bool FULL>
+    __device__ __forceinline__ void sum_up(Sum &acc, int have, float c) const
+    {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (tid + k * threads < nvec)
-                held[k] = vec[tid + k * threads];
-    }
-    const float picked = Elem<E>::get(row[target]);  // before any CTA may write over it
-    // the ragged ends, fewer than VEC elements each: one of either per thread
-    const bool has_head = tid < v0 - lo, has_tail = tid < hi - v1;
-    const float xh = has_head ? Elem<E>::get(row[lo + tid]) : -INFINITY;
-    const float xt = has_tail ? Elem<E>::get(row[v1 + tid]) : -INFINITY;
-    Sum acc{-INFINITY, 0.0f};
-    if constexpr (NV > 0) {
-        float top = fmaxf(xh, xt);
+        for (int b = 0; b < NB; ++b) {
+            wait_groups(NB - 1 - b);
+            Vec<E> v[kBatch];
+            float top = acc.m;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (tid + k * threads < nvec) {
-                top = top_of(held[k], top);
-                stay_packed(held[k]);
+            for (int q = 0; q < kBatch; ++q) {
+                take<FULL>(b * kBatch + q, have, v[q]);
+                top = top_of(v[q], top);
+                stay_packed(v[q]);
             }
-        const float m = base_of(top);
-        F2 part[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (tid + k * threads < nvec) {
-                float2 e[VEC / 2];
-                powers_of<E>(held[k], m, c, e);
-#pragma unroll
-                for (int u = 0; u < VEC / 2; ++u)
-                    part[u & 1] = add2(part[u & 1], pair_of(e[u].x, e[u].y));
-                stay_packed(held[k]);
-            }
-        const float2 p0 = halves_of(part[0]), p1 = halves_of(part[1]);
-        acc.m = top;
-        acc.s = (p0.x + p0.y) + (p1.x + p1.y);
-        if (has_head)
-            acc.s += ex2((xh - m) * c);
-        if (has_tail)
-            acc.s += ex2((xt - m) * c);
-    } else {
-#pragma unroll 4
-        for (int i = tid; i < nvec; i += threads) {
-            const Vec<E> v = vec[i];
-            const float top = top_of(v, -INFINITY);
             if (top > acc.m) {
                 acc.s *= rescale(acc.m, top, c);
                 acc.m = top;
             }
-            float2 e[VEC / 2];
-            powers_of<E>(v, base_of(acc.m), c, e);
+            F2 part[2] = {pair_of(0.0f), pair_of(0.0f)};
 #pragma unroll
-            for (int u = 0; u < VEC / 2; ++u)
-                acc.s += e[u].x + e[u].y;
+            for (int q = 0; q < kBatch; ++q)
+                add_powers(v[q], base_of(acc.m), c, part);
+            const float2 sum2 = halves_of(add2(part[0], part[1]));
+            acc.s += sum2.x + sum2.y;
         }
-        if (has_head)
-            acc = join(acc, Sum{xh, ex2((xh - base_of(xh)) * c)}, c);
-        if (has_tail)
-            acc = join(acc, Sum{xt, ex2((xt - base_of(xt)) * c)}, c);
     }
+
+    // The gradient's vectors to `to`, the next row's (FETCH, have_next of them) in their
+    // place.
+    template <bool FULL, bool FETCH>
+    __device__ __forceinline__ void write(const Gradient<E> &g, uint8_t *to, int have, const uint8_t *from,
+                                          int have_next) const
+    {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        acc = join(acc, Sum{__shfl_xor_sync(~0u, acc.m, d), __shfl_xor_sync(~0u, acc.s, d)}, c);
-    if ((tid & 31) == 0)
-        warps[tid >> 5] = acc;
-    __syncthreads();
-    if (tid < 32) {
-        acc = tid < threads / 32 ? warps[tid] : Sum{-INFINITY, 0.0f};
+        for (int b = 0; b < NB; ++b) {
+            Vec<E> v[kBatch];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            acc = join(acc, Sum{__shfl_xor_sync(~0u, acc.m, d), __shfl_xor_sync(~0u, acc.s, d)}, c);
-        if (tid == 0)
-            mine = acc;
-    }
-    __syncthreads();
-    tc::cluster_sync();  // every CTA's sum is there, and every read of row[target] is done
-    Sum all{-INFINITY, 0.0f};
-    for (int p = 0; p < parts; ++p) {
-        const uint32_t at = tc::map_to_rank(ptx::smem_addr(&mine), (uint32_t)p);
-        all = join(all, Sum{tc::ld_cluster_f32(at), tc::ld_cluster_f32(at + 4)}, c);
-    }
-    tc::cluster_arrive();  // its sum read, this CTA lets the others go
-    const float m = base_of(all.m);
-    const float logp = (picked - m) * a.inv_temperature - logf(all.s);
-    if (rank == 0 && tid == 0)
-        a.logp_out[t] = logp;
-    if (out) {
-        const float coef = w * terms_of(a, t, logp).slope * a.inv_temperature * a.grad_scale;
-        const float k = -coef / all.s;
-        // the gradient at element i, whose logit is x
-        const auto grad = [&](int i, float x) {
-            return fmaf(k, ex2((x - m) * c), i == target ? coef : 0.0f);
-        };
-        if (wide) {
-            // the vector that holds the target, and the target's place in it
-            const int tv = target >= v0 && target < v1 ? (target - v0) / VEC : -1;
-            const int tu = target - v0 - tv * VEC;
-            const auto put = [&](int i, Vec<E> v) {
-                float2 y[VEC / 2];
-                powers_of<E>(v, m, c, y);
+            for (int q = 0; q < kBatch; ++q)
+                take<FULL>(b * kBatch + q, have, v[q]);
 #pragma unroll
-                for (int u = 0; u < VEC / 2; ++u)
-                    y[u] = halves_of(mul2(pair_of(y[u].x, y[u].y), pair_of(k, k)));
-                if (i == tv) {
-#pragma unroll
-                    for (int u = 0; u < VEC / 2; ++u) {
-                        y[u].x += 2 * u == tu ? coef : 0.0f;
-                        y[u].y += 2 * u + 1 == tu ? coef : 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < VEC / 2; ++u)
-                    Elem<E>::put2(v.e + 2 * u, y[u]);
-                reinterpret_cast<Vec<E> *>(out + v0)[i] = v;
-            };
-            if constexpr (NV > 0) {
-#pragma unroll
-                for (int q = 0; q < NV; ++q)
-                    if (tid + q * threads < nvec)
-                        put(tid + q * threads, held[q]);
-            } else {
-                for (int i = tid; i < nvec; i += threads)
-                    put(i, vec[i]);
+            for (int q = 0; q < kBatch; ++q) {
+                g.softmax(v[q]);  // uses the vector: its place is free
+                if (FULL || b * kBatch + q < have)
+                    *reinterpret_cast<Vec<E> *>(to + (b * kBatch + q) * 512) = v[q];
+                if (FETCH)
+                    fetch<FULL>(from, b * kBatch + q, have_next);
             }
-        } else if constexpr (NV > 0) {
-#pragma unroll
-            for (int q = 0; q < NV; ++q)
-                if (tid + q * threads < nvec) {
-                    const int i = v0 + (tid + q * threads) * VEC;
+            commit_group();
+        }
+    }
+};
+
+template <typename E, int NB>
+__global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const __grid_constant__ LossArgs a)
+{
+    constexpr int VEC = Elem<E>::kVec, NV = NB * kBatch;
+    extern __shared__ __align__(16) uint8_t smem[];  // [warp][vector of a lane][lane]
+    __shared__ Sum sums[2][32];
+    tc::launch_dependents();  // the statistics' launch
+    const int parts = (int)tc::cluster_size(), rank = (int)tc::cluster_ctarank();
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t step = tc::ncluster_x();
+    const float c = a.inv_temperature * kLog2e;
+    const int first = warp * NV * 32 + lane;  // this lane's first vector of the slice
+    Lane<E, NB> mine;
+    mine.slot = smem + first * 16;
+    mine.slot_at = ptx::smem_addr(mine.slot);
+    const Gather gather(sums[0], threads / 32, parts, lane);
+
+    // The next row: its slice, how many vectors this lane has in it (none where the
+    // token is masked), its ragged ends and its target's logit.
+    Slice<E> s(a, rank, parts), n = s;
+    const uint8_t *from = nullptr;
+    int have_next = 0;
+    float xh = 0.0f, xt = 0.0f, picked = 0.0f;
+    const auto look = [&](int64_t t, const Token &k) {
+        n.at(a, t);
+        have_next = 0;
+        if (!k.live(a))
+            return;
+        from = reinterpret_cast<const uint8_t *>(n.vec() + first);
+        have_next = n.nvec > first ? (n.nvec - first + 31) / 32 : 0;
+        have_next = have_next < NV ? have_next : NV;
+        picked = Elem<E>::get(n.row[k.target]);
+        xh = n.has_head(tid) ? Elem<E>::get(n.row[n.lo + tid]) : -INFINITY;
+        xt = n.has_tail(tid) ? Elem<E>::get(n.row[n.v1 + tid]) : -INFINITY;
+    };
+
+    int64_t t = tc::cluster_id_x();
+    Token now(a, t), next(a, t + step);
+    look(t, now);
+    mine.fetch_all(from, have_next);
+    for (uint32_t turn = 0; t < a.T; t += step) {
+        const Token later(a, t + 2 * step);
+        s = n;
+        const bool live = now.live(a);  // the same for the whole cluster
+        const int have = have_next;
+        const float head = xh, tail = xt, logit = picked;
+        look(t + step, next);
+        const bool full = __all_sync(~0u, have == NV);
+        if (live) {
+            Sum acc{fmaxf(head, tail), 0.0f};
+            const float m = base_of(acc.m);
+            acc.s = ex2((head - m) * c) + ex2((tail - m) * c);  // -inf where there is none
+            if (full)
+                mine.template sum_up<true>(acc, NV, c);
+            else
+                mine.template sum_up<false>(acc, have, c);
+            acc = warp_join(acc, c);
+            if (lane == 0)
+                sums[turn][warp] = acc;
+            __syncwarp();
+            // every warp's sum is there and every read of the target's logit is done;
+            // sums[turn] is written again two rows on, behind the next row's barrier
+            tc::cluster_sync();
+            const Sum all = gather.join_all(sums[0], turn * (uint32_t)sizeof(sums[0]), lane, c);
+            turn ^= 1;
+            const float logp = logp_of(a, all, logit);
+            if (rank == 0 && tid == 0)
+                a.logp_out[t] = logp;
+            const Gradient<E> g(a, now, all, logp, c);
+            if (s.wide) {
+                uint8_t *to = reinterpret_cast<uint8_t *>(s.out + s.v0) + first * 16;
+                const bool next_full = __all_sync(~0u, have_next == NV);
+                if (full && next_full)
+                    mine.template write<true, true>(g, to, NV, from, NV);
+                else if (full && __all_sync(~0u, have_next == 0))
+                    mine.template write<true, false>(g, to, NV, from, 0);
+                else
+                    mine.template write<false, true>(g, to, have, from, have_next);
+            } else {  // an output of another alignment, or none
+#pragma unroll 1
+                for (int q = 0; q < have && s.out; ++q) {
+                    Vec<E> v = *reinterpret_cast<const Vec<E> *>(mine.slot + q * 512);
+                    g.softmax(v);
 #pragma unroll
                     for (int u = 0; u < VEC; ++u)
-                        out[i + u] = Elem<E>::put(grad(i + u, Elem<E>::get(held[q].e[u])));
+                        s.out[s.v0 + (first + q * 32) * VEC + u] = reinterpret_cast<const E *>(v.w)[u];
                 }
+                mine.fetch_all(from, have_next);
+            }
+            if (s.out) {
+                if (s.has_head(tid))
+                    s.out[s.lo + tid] = g.one(head);
+                if (s.has_tail(tid))
+                    s.out[s.v1 + tid] = g.one(tail);
+                __syncthreads();  // the target's element after the others
+                if (tid == 0 && g.target >= s.lo && g.target < s.hi)
+                    s.out[g.target] = g.target_one(logit);
+            }
         } else {
-            for (int i = v0 + tid; i < v1; i += threads)
-                out[i] = Elem<E>::put(grad(i, Elem<E>::get(row[i])));
+            mine.fetch_all(from, have_next);
+            if (rank == 0 && tid == 0) {
+                a.logp_out[t] = 0.0f;
+                if (now.weight != 0.0f)
+                    report_status(a.status, kInvalidArg);
+            }
+            s.zero(tid, threads);
         }
-        if (has_head)
-            out[lo + tid] = Elem<E>::put(grad(lo + tid, xh));
-        if (has_tail)
-            out[v1 + tid] = Elem<E>::put(grad(v1 + tid, xt));
+        now = next;
+        next = later;
     }
-    tc::cluster_wait();  // no CTA leaves while its sum may still be read
+    __syncwarp();
+    tc::cluster_sync();  // no CTA leaves while its sums may still be read
+}
+
+// Rows beyond what a cluster's shared memory holds: the second pass reads memory
+// again.  One cluster per token.
+template <typename E>
+__global__ void __launch_bounds__(1024) policy_loss_long_kernel(const __grid_constant__ LossArgs a)
+{
+    constexpr int VEC = Elem<E>::kVec;
+    __shared__ Sum sums[32];
+    tc::launch_dependents();
+    const int64_t t = tc::cluster_id_x();
+    const int parts = (int)tc::cluster_size(), rank = (int)tc::cluster_ctarank();
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+    Slice<E> s(a, rank, parts);
+    s.at(a, t);
+    const Token now(a, t);
+    if (!now.live(a)) {  // the same for the whole cluster
+        if (rank == 0 && tid == 0) {
+            a.logp_out[t] = 0.0f;
+            if (now.weight != 0.0f)
+                report_status(a.status, kInvalidArg);
+        }
+        s.zero(tid, threads);
+        return;
+    }
+    const float c = a.inv_temperature * kLog2e;
+    const float picked = Elem<E>::get(s.row[now.target]);  // before any CTA may write over it
+    const float head = s.has_head(tid) ? Elem<E>::get(s.row[s.lo + tid]) : -INFINITY;
+    const float tail = s.has_tail(tid) ? Elem<E>::get(s.row[s.v1 + tid]) : -INFINITY;
+    Sum acc{-INFINITY, 0.0f};
+#pragma unroll 4
+    for (int i = tid; i < s.nvec; i += threads) {
+        const Vec<E> v = s.vec()[i];
+        const float top = top_of(v, -INFINITY);
+        if (top > acc.m) {
+            acc.s *= rescale(acc.m, top, c);
+            acc.m = top;
+        }
+        F2 part[2] = {pair_of(0.0f), pair_of(0.0f)};
+        add_powers(v, base_of(acc.m), c, part);
+        const float2 sum2 = halves_of(add2(part[0], part[1]));
+        acc.s += sum2.x + sum2.y;
+    }
+    if (s.has_head(tid))
+        acc = join(acc, Sum{head, ex2((head - base_of(head)) * c)}, c);
+    if (s.has_tail(tid))
+        acc = join(acc, Sum{tail, ex2((tail - base_of(tail)) * c)}, c);
+    acc = warp_join(acc, c);
+    if (lane == 0)
+        sums[tid >> 5] = acc;
+    __syncwarp();
+    tc::cluster_sync();  // every warp's sum is there, every read of the target's logit done
+    const Sum all = Gather(sums, threads / 32, parts, lane).join_all(sums, 0, lane, c);
+    const float logp = logp_of(a, all, picked);
+    if (rank == 0 && tid == 0)
+        a.logp_out[t] = logp;
+    if (s.out) {
+        const Gradient<E> g(a, now, all, logp, c);
+#pragma unroll 4
+        for (int i = tid; i < s.nvec; i += threads) {
+            Vec<E> v = s.vec()[i];
+            g.softmax(v);
+            if (s.wide) {
+                reinterpret_cast<Vec<E> *>(s.out + s.v0)[i] = v;
+            } else {
+#pragma unroll
+                for (int u = 0; u < VEC; ++u)
+                    s.out[s.v0 + i * VEC + u] = reinterpret_cast<const E *>(v.w)[u];
+            }
+        }
+        if (s.has_head(tid))
+            s.out[s.lo + tid] = g.one(head);
+        if (s.has_tail(tid))
+            s.out[s.v1 + tid] = g.one(tail);
+        __syncthreads();  // the target's element after the others
+        if (tid == 0 && g.target >= s.lo && g.target < s.hi)
+            s.out[g.target] = g.target_one(picked);
+    }
+    __syncwarp();
+    tc::cluster_sync();  // no CTA leaves while its sums may still be read
 }
 
 // The four statistics from the tokens' logp, in one CTA and a fixed order (in
@@ -378,20 +671,18 @@ __global__ void __launch_bounds__(1024) policy_loss_kernel(const __grid_constant
 __global__ void __launch_bounds__(1024) loss_stats_kernel(const __grid_constant__ LossArgs a)
 {
     __shared__ double part[32][4];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' kernel is done
+    tc::wait_dependencies();  // the rows' kernel is done
     double s[4] = {0, 0, 0, 0};
     for (int64_t t = threadIdx.x; t < a.T; t += 1024) {
-        const float w = a.weight[t];
-        if (w == 0.0f)
+        const Token token(a, t);
+        if (!token.live(a))
             continue;
-        const int64_t target = a.target[t];
-        if (target < 0 || target >= a.V)
-            continue;
-        const Terms r = terms_of(a, t, a.logp_out[t]);
-        s[0] += (double)w * r.loss;
-        s[1] += (double)w * r.kl;
-        s[2] += (double)w * r.clipped;
-        s[3] += (double)w * r.ratio;
+        const Terms r = terms_of(a, token, a.logp_out[t]);
+        const double w = token.weight;
+        s[0] += w * r.loss;
+        s[1] += w * r.kl;
+        s[2] += w * r.clipped;
+        s[3] += w * r.ratio;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -410,47 +701,69 @@ __global__ void __launch_bounds__(1024) loss_stats_kernel(const __grid_constant_
     }
 }
 
-constexpr int kHeld = 8;          // vectors a thread keeps at most (32 registers)
-constexpr int kRowThreads = 256;  // threads of a CTA, unless the row asks for more
+constexpr int kMaxDevices = 64;
+constexpr int kSliceVecs = 6400;             // 100 KB: two CTAs on an SM
+constexpr int kMaxSliceBytes = 224 * 1024;
+
+template <typename E, int NB>
+cudaError_t launch_held(cudaLaunchConfig_t &cfg, const LossArgs &a)
+{
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t result[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        dev = 0;
+    std::call_once(once[dev], [&] {
+        result[dev] = cudaFuncSetAttribute(policy_loss_kernel<E, NB>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceBytes);
+    });
+    if (result[dev] != cudaSuccess)
+        return result[dev];
+    return cudaLaunchKernelEx(&cfg, policy_loss_kernel<E, NB>, a);
+}
 
 template <typename E>
 cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
 {
     // A row's vectors (one more than V needs: a row may start between two
-    // 16-byte boundaries) go to CTAs of 256 threads with 8 vectors each, so that
-    // four CTAs of 64 registers a thread share an SM; to larger CTAs when 8 CTAs
-    // (a portable cluster) of 256 do not hold them.  When the rows are few, more
-    // and smaller CTAs share a row, down to 128 vectors each.
+    // 16-byte boundaries) are shared by as few CTAs as hold 100 KB each, two on an
+    // SM; by up to 8 (a portable cluster) of up to 224 KB where that is not enough.
+    // When the rows are few, more and smaller CTAs share a row, down to 128 vectors
+    // each.  Threads have up to 16 vectors.
     const int64_t vecs = (a.V + Elem<E>::kVec - 1) / Elem<E>::kVec + 1;
-    int64_t parts = (vecs + kHeld * kRowThreads - 1) / (kHeld * kRowThreads);
+    int64_t parts = (vecs + kSliceVecs - 1) / kSliceVecs;
     parts = parts > 8 ? 8 : parts;
     while (parts <= 4 && a.T * parts * 2 <= 2 * kSMs && vecs / (parts * 2) >= 128)
         parts *= 2;
     const int64_t slice = (vecs + parts - 1) / parts + 1;
-    const bool held = slice <= kHeld * 1024;
-    int nv = 1;
-    while (nv < kHeld && slice > (int64_t)nv * kRowThreads)
-        nv *= 2;
-    int64_t threads = held ? ((slice + nv - 1) / nv + 31) / 32 * 32 : 1024;
+    const int nb = slice <= 4 * 128 ? 1 : (slice <= 8 * 128 ? 2 : 4);
+    int64_t threads = (slice + nb * kBatch * 32 - 1) / (nb * kBatch * 32) * 32;
     threads = threads < 64 ? 64 : threads;
+    const int64_t bytes = threads * nb * kBatch * 16;
+    const bool held = bytes <= kMaxSliceBytes;
+    threads = held ? threads : 1024;
+    // clusters: as many as are resident at once (by shared memory) walk the rows
+    const int64_t fit = kMaxSliceBytes / bytes;
+    const int64_t per_sm = fit < 1 ? 1 : gg_min64(fit, gg_min64(16, 896 / threads > 0 ? 896 / threads : 1));
+    const int64_t clusters = held ? gg_min64(a.T, gg_min64(per_sm * kSMs / parts, INT32_MAX)) : a.T;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)parts;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(a.T * parts), 1, 1);
+    cfg.gridDim = dim3((unsigned)(clusters * parts), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = held ? (size_t)bytes : 0;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (!held)
-        return cudaLaunchKernelEx(&cfg, policy_loss_kernel<E, 0>, a);
-    switch (nv) {
-    case 1: return cudaLaunchKernelEx(&cfg, policy_loss_kernel<E, 1>, a);
-    case 2: return cudaLaunchKernelEx(&cfg, policy_loss_kernel<E, 2>, a);
-    case 4: return cudaLaunchKernelEx(&cfg, policy_loss_kernel<E, 4>, a);
-    default: return cudaLaunchKernelEx(&cfg, policy_loss_kernel<E, 8>, a);
+        return cudaLaunchKernelEx(&cfg, policy_loss_long_kernel<E>, a);
+    switch (nb) {
+    case 1: return launch_held<E, 1>(cfg, a);
+    case 2: return launch_held<E, 2>(cfg, a);
+    default: return launch_held<E, 4>(cfg, a);
     }
 }
 

@@ -145,6 +145,13 @@ def test_values(T, V, dtype):
     assert (full[:, V:] == FILL).all()
 
 
+@pytest.mark.parametrize("T,V,dtype,inplace", [(2, 530001, BF16, False), (3, 600000, F16, True), (2, 270003, F32, False)])
+def test_rows_that_no_cluster_holds(T, V, dtype, inplace):
+    c = far_from_clip(make(T, V, dtype, pad=V % 2, masked=0.0, seed=8))
+    before = c["logits"].clone()
+    check(c, call(c, inplace=inplace), before)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("shift,gshift", [(0, 0), (1, 1), (3, 1), (0, 5)])
 def test_alignment_and_in_place(shift, gshift, dtype):
