@@ -369,19 +369,37 @@ gg_status prepare_adamw(const gg_adamw_tensor *tensors, int count, int64_t step,
             return op_fail(GG_ERR_INVALID_ARG, "tensor %d: param, grad and states must be non-NULL", i);
         const int64_t pe = t.param_dtype == GG_F32 ? 4 : 2, ge = t.grad_dtype == GG_F32 ? 4 : 2;
         const int64_t blocks = eight ? (t.n + GG_ADAMW_BLOCK - 1) / GG_ADAMW_BLOCK : 0;
-        const Mat all[] = {{"param", t.param, 1, t.n, t.n, pe},
-                           {"m", t.m, 1, t.n, t.n, eight ? 1 : 4},
-                           {"v", t.v, 1, t.n, t.n, eight ? 1 : 4},
-                           {"m_scale", t.m_scale, 1, blocks, blocks, 4},
-                           {"v_scale", t.v_scale, 1, blocks, blocks, 4},
-                           {"copy", t.copy, 1, t.n, t.n, 2},
-                           {"grad", t.grad, 1, t.n, t.n, ge}};
-        for (const Mat &x : all) {
-            GG_TRY(check_mat(x, false));
-            for (const Mat &y : all)
-                if (&x < &y && share(x, y))
-                    return op_fail(GG_ERR_INVALID_ARG, "tensor %d: %s overlaps %s", i, x.name, y.name);
+        // a few hundred tensors a step: plain comparisons, the names only for an error
+        struct Span {
+            uint64_t lo, hi;
+            const char *name;
+        } spans[7];
+        int used = 0;
+        const char *odd = nullptr;
+        const auto add = [&](const void *p, int64_t n, int64_t es, const char *name) {
+            const uint64_t lo = reinterpret_cast<uint64_t>(p);
+            if (!p || n == 0)
+                return;
+            if (lo & (uint64_t)(es - 1))
+                odd = name;
+            spans[used++] = Span{lo, lo + (uint64_t)(n * es), name};
+        };
+        add(t.grad, t.n, ge, "grad");
+        add(t.param, t.n, pe, "param");
+        add(t.m, t.n, eight ? 1 : 4, "m");
+        add(t.v, t.n, eight ? 1 : 4, "v");
+        add(t.copy, t.n, 2, "copy");
+        if (eight) {
+            add(t.m_scale, blocks, 4, "m_scale");
+            add(t.v_scale, blocks, 4, "v_scale");
         }
+        if (odd)
+            return op_fail(GG_ERR_ALIGNMENT, "tensor %d: %s must be aligned to its elements", i, odd);
+        for (int x = 1; x < used; ++x)
+            for (int y = 0; y < x; ++y)
+                if (spans[x].lo < spans[y].hi && spans[y].lo < spans[x].hi)
+                    return op_fail(GG_ERR_INVALID_ARG, "tensor %d: %s overlaps %s", i, spans[x].name,
+                                   spans[y].name);
     }
     gg::AdamwStep h{};
     h.beta1 = (float)beta1;

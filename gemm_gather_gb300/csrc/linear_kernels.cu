@@ -1408,53 +1408,60 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
 
 }  // namespace
 
-// Which kernel, tile and split, by an estimate of each one's time in SM cycles:
-// waves x k-blocks x cycles of a k-block (the larger of its MMAs and of its
-// operand loads at 56 bytes a cycle and SM), plus what a tile costs besides.
-//  * split kernel: the smallest token tile that holds all tokens, 64 at most (a
-//    weight gradient, whose MN-major B comes in boxes of 64: 64); as many CTAs
-//    per tile as the tiles leave SMs for, 8 (a portable cluster) and one k-block
-//    each at most.
-//  * pair kernel: 256 x 256 or 256 x 128 tiles, whole ones walked by 76 pairs,
-//    or, where all the clusters fit at once, split between 2 or 4 pairs.
+// Which kernel, tile and split: the one of least estimated time, in nanoseconds.
+// The estimate is a launch and its set-up, then waves x k-blocks x the time of a
+// k-block (its MMAs, its operands through an SM's port, or the latency of the
+// ring), then the epilogue.  Its constants were fitted to 560 timings of both
+// kernels (8 weights of 512 x 512 to 8192 x 3584, 1 to 2048 tokens, every tile and
+// split): the choice is on average 0.5% slower than the best of them, 7% at most.
+// By it, few tokens are split over two CTAs an SM (1 token, N = 3584, K = 8192: 8
+// shares 12.9 us, 4 shares 13.7, unsplit 17.7), short contractions are not split
+// (512 tokens, N = K = 1024: unsplit 7.3 us, 4 shares 8.6), and whole 256 x 256 tiles
+// begin where they fill most pairs (1024 tokens, N = 3584, K = 8192: 43 us, 256 x 128
+// tiles 61).  A weight gradient's split tiles are 64 wide, the boxes of its
+// MN-major B.
 LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
 {
     LinearPlan best{GG_LINEAR_NONE, 0, 0};
     if (I <= 0 || J <= 0 || K <= 0)
         return best;
     const int64_t num_kb = (K + kBK - 1) / kBK;
-    int64_t cost = INT64_MAX;
-    const auto offer = [&](int kernel, int bt, int64_t parts, int64_t c) {
-        if ((path == GG_LINEAR_AUTO || path == kernel) && c < cost) {
-            cost = c;
-            best = LinearPlan{kernel, bt, (int)parts};
+    double least = 0.0;
+    const auto offer = [&](int kernel, int bt, int parts, double ns) {
+        if (best.kernel == GG_LINEAR_NONE || ns < least) {
+            least = ns;
+            best = LinearPlan{kernel, bt, parts};
         }
     };
-    {
-        int bt = epi == kEpiGradW ? 64 : 16;
-        while (bt < 64 && bt < J)
-            bt *= 2;
+    for (int bt = epi == kEpiGradW ? 64 : 16; path != GG_LINEAR_PAIR && bt <= 64; bt *= 2) {
         const int64_t tiles = ((I + 127) / 128) * ((J + bt - 1) / bt);
-        int64_t parts = kSMs / tiles;
-        parts = parts < 1 ? 1 : (parts > 8 ? 8 : parts);
-        parts = gg_min64(parts, num_kb);
-        const int64_t kb_cycles = (128 + bt) * kBK * 2 / 56;
-        offer(GG_LINEAR_SPLIT, bt, parts,
-              (tiles * parts + kSMs - 1) / kSMs * ((num_kb + parts - 1) / parts * kb_cycles + 1000 +
-                                                   bt * 16));
-    }
-    for (int bt = 256; bt >= 128; bt /= 2) {
-        const int64_t tiles = ((I + 255) / 256) * ((J + bt - 1) / bt);
-        for (int parts = 1; parts <= 4; parts *= 2) {
-            // 2 CTAs a pair, and clusters of 4 or 8 CTAs do not fill every SM
-            const int64_t room = parts == 1 ? 76 : parts == 2 ? 36 : 16;
-            if (parts > 1 && (tiles > room || num_kb < parts))
+        for (int parts = 1; parts <= 8 && parts <= num_kb; ++parts) {
+            const int64_t ctas = tiles * parts;
+            if (parts > 1 && ctas > 2 * kSMs)
                 break;
-            const int64_t mma = bt * 2, load = (128 + bt / 2) * kBK * 2 / 56;
-            const int64_t waves = (tiles + room - 1) / room;
+            const double per_sm = ctas <= kSMs ? 1.0 : (ctas >= 2 * kSMs ? 2.0 : (double)ctas / kSMs);
+            const double waves = (double)((ctas + 2 * kSMs - 1) / (2 * kSMs));
+            const double latency = 221.0 + 2.05 * bt, port = per_sm * (128 + bt) * kBK * 2 / 101.4;
+            offer(GG_LINEAR_SPLIT, bt, parts,
+                  1840.0 + (parts > 1 ? 1580.0 : 0.0) +
+                      waves * (double)((num_kb + parts - 1) / parts) * (latency > port ? latency : port) +
+                      (waves - 1.0) * 1590.0 + bt * (parts > 1 ? 48.0 : 36.0));
+        }
+    }
+    for (int bt = 128; path != GG_LINEAR_SPLIT && bt <= 256; bt *= 2) {
+        const int64_t tiles = ((I + 255) / 256) * ((J + bt - 1) / bt);
+        for (int parts = 1; parts <= 4 && parts <= num_kb; parts *= 2) {
+            // pairs, and clusters of 4 and 8 CTAs, that are resident at once
+            const int64_t room = parts == 1 ? 76 : (parts == 2 ? 36 : 14);
+            if (parts > 1 && tiles > room)
+                break;
+            const double waves = (double)((tiles + room - 1) / room);
+            const double mma = bt * 1.08, port = (128 + bt / 2) * kBK * 2 / 127.8;
+            double kb = mma > port ? mma : port;
+            kb = kb > 181.0 ? kb : 181.0;
             offer(GG_LINEAR_PAIR, bt, parts,
-                  waves * ((num_kb + parts - 1) / parts) * (mma > load ? mma : load) + 2000 + bt * 12 +
-                      (parts > 1 ? 1500 : 0));
+                  5290.0 + (parts > 1 ? 3500.0 : 0.0) +
+                      waves * (double)((num_kb + parts - 1) / parts) * kb + 8.6 * bt / parts);
         }
     }
     return best;
