@@ -51,6 +51,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
 #include "tc.cuh"
@@ -91,44 +92,120 @@ __device__ __forceinline__ void store16(void *p, int64_t at, float v, int bf16)
         bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
-// Activations in float32.  relu keeps NaN; gelu_tanh's 0.5 (1 + tanh u) is
+// Activations in float32, on pairs (two neighbouring tokens of a feature) where
+// the arithmetic comes in pairs.  relu keeps NaN.  gelu_tanh's 0.5 (1 + tanh u) is
 // the logistic function of 2u, which keeps its relative precision for u << 0.
-__device__ __forceinline__ float logistic(float x) { return 1.0f / (1.0f + __expf(-x)); }
-__device__ __forceinline__ float gelu_u2(float z)
+// gelu's normal distribution function comes from Abramowitz and Stegun's 7.1.26,
+//     Phi(-x) = P(t) exp(-x^2 / 2) / 2,  t = 1 / (1 + p x / sqrt 2),  x >= 0,
+// within 7.5e-8 of Phi, a hundredth of a 16-bit result's rounding; its exponential
+// is also the density that the derivative needs.  (With erff and a float division,
+// the epilogue of a 256 x 256 tile took longer than its MMAs at K = 3584.)
+__device__ __forceinline__ float ex2_approx(float x)
 {
-    return 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 sqrt(2/pi) (z + ...)
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + exp(-x))
+__device__ __forceinline__ float2 logistic(F2 x)
+{
+    const float2 e = halves_of(mul2(x, pair_of(-1.44269504f)));
+    const float2 d = halves_of(add2(pair_of(ex2_approx(e.x), ex2_approx(e.y)), pair_of(1.0f)));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+// 2 sqrt(2/pi) (z + 0.044715 z^3)
+__device__ __forceinline__ F2 gelu_2u(F2 z, F2 zz)
+{
+    return mul2(z, fma2(zz, pair_of(0.071354816f), pair_of(1.59576912f)));
+}
+
+// Phi(z), and exp(-z^2 / 2) in *e.
+__device__ __forceinline__ float2 normal_cdf(F2 z, F2 zz, float2 *e)
+{
+    const float2 y = halves_of(mul2(zz, pair_of(-0.72134752f)));
+    *e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    const float2 v = halves_of(z);
+    const float2 d = halves_of(fma2(pair_of(fabsf(v.x), fabsf(v.y)), pair_of(0.23164189f), pair_of(1.0f)));
+    const F2 t = pair_of(rcp_approx(d.x), rcp_approx(d.y));
+    F2 q = fma2(t, pair_of(0.5f * 1.061405429f), pair_of(0.5f * -1.453152027f));
+    q = fma2(t, q, pair_of(0.5f * 1.421413741f));
+    q = fma2(t, q, pair_of(0.5f * -0.284496736f));
+    q = fma2(t, q, pair_of(0.5f * 0.254829592f));
+    const float2 tail = halves_of(mul2(mul2(t, q), pair_of(e->x, e->y)));  // Phi(-|z|)
+    return make_float2(v.x < 0.0f ? tail.x : 1.0f - tail.x, v.y < 0.0f ? tail.y : 1.0f - tail.y);
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float z)
+__device__ __forceinline__ float2 act_value(float2 v)
 {
+    const F2 z = pair_of(v.x, v.y);
     if constexpr (ACT == GG_ACT_RELU)
-        return !(z <= 0.0f) ? z : 0.0f;
-    if constexpr (ACT == GG_ACT_GELU)
-        return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    if constexpr (ACT == GG_ACT_GELU_TANH)
-        return z * logistic(gelu_u2(z));
-    if constexpr (ACT == GG_ACT_SILU)
-        return z * logistic(z);
-    return z;
+        return make_float2(!(v.x <= 0.0f) ? v.x : 0.0f, !(v.y <= 0.0f) ? v.y : 0.0f);
+    if constexpr (ACT == GG_ACT_GELU) {
+        float2 e;
+        const float2 c = normal_cdf(z, mul2(z, z), &e);
+        return halves_of(mul2(z, pair_of(c.x, c.y)));
+    }
+    if constexpr (ACT == GG_ACT_GELU_TANH || ACT == GG_ACT_SILU) {
+        const float2 s = logistic(ACT == GG_ACT_SILU ? z : gelu_2u(z, mul2(z, z)));
+        return halves_of(mul2(z, pair_of(s.x, s.y)));
+    }
+    return v;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z)
+__device__ __forceinline__ float2 act_slope(float2 v)
 {
+    const F2 z = pair_of(v.x, v.y);
     if constexpr (ACT == GG_ACT_RELU)
-        return z > 0.0f ? 1.0f : 0.0f;
-    if constexpr (ACT == GG_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
-    if constexpr (ACT == GG_ACT_GELU_TANH) {
-        const float s = logistic(gelu_u2(z));  // d(z s)/dz = s + z s (1 - s) 2u'
-        return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+        return make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
+    if constexpr (ACT == GG_ACT_GELU) {  // Phi + z density
+        float2 e;
+        const float2 c = normal_cdf(z, mul2(z, z), &e);
+        return halves_of(fma2(mul2(z, pair_of(0.39894228f)), pair_of(e.x, e.y), pair_of(c.x, c.y)));
     }
-    if constexpr (ACT == GG_ACT_SILU) {
-        const float s = logistic(z);
-        return s * (1.0f + z * (1.0f - s));
+    if constexpr (ACT == GG_ACT_GELU_TANH) {  // d(z s)/dz = s + z s (1 - s) 2u'
+        const F2 zz = mul2(z, z);
+        const float2 h = logistic(gelu_2u(z, zz));
+        const F2 s = pair_of(h.x, h.y), rest = pair_of(1.0f - h.x, 1.0f - h.y);
+        const F2 du = fma2(zz, pair_of(0.21406445f), pair_of(1.59576912f));
+        return halves_of(fma2(mul2(mul2(z, s), rest), du, s));
     }
-    return 1.0f;
+    if constexpr (ACT == GG_ACT_SILU) {  // s + z s (1 - s)
+        const float2 h = logistic(z);
+        const F2 s = pair_of(h.x, h.y), rest = pair_of(1.0f - h.x, 1.0f - h.y);
+        return halves_of(fma2(mul2(z, s), rest, s));
+    }
+    return make_float2(1.0f, 1.0f);
+}
+
+// v = act(v) and v *= act'(x), over an even number of values.
+template <int ACT, int C>
+__device__ __forceinline__ void apply_act(float (&v)[C])
+{
+#pragma unroll
+    for (int u = 0; u < C; u += 2) {
+        const float2 y = act_value<ACT>(make_float2(v[u], v[u + 1]));
+        v[u] = y.x, v[u + 1] = y.y;
+    }
+}
+template <int ACT, int C>
+__device__ __forceinline__ void apply_slope(float (&v)[C], const float (&x)[C])
+{
+#pragma unroll
+    for (int u = 0; u < C; u += 2) {
+        const float2 y = act_slope<ACT>(make_float2(x[u], x[u + 1]));
+        v[u] *= y.x, v[u + 1] *= y.y;
+    }
 }
 
 // f(ACT) with the activation as a compile-time constant.
@@ -157,14 +234,16 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
         if (a.out_f32) {
             float *o = reinterpret_cast<float *>(a.out) + j0 * a.ldo + i;
             const int64_t step = (int64_t)jstep * a.ldo;
+            // added where it lies (one addition to each element, rounded to nearest as
+            // here; the memory's adder takes subnormals for zero): with loads instead,
+            // a warp waited 8 times for memory while the next tile's MMAs ran out of
+            // accumulators
             if (a.accumulate) {
-                float old[C];
 #pragma unroll
                 for (int u = 0; u < C; ++u)
-                    old[u] = u < n ? o[u * step] : 0.0f;
-#pragma unroll
-                for (int u = 0; u < C; ++u)
-                    v[u] += old[u];
+                    if (u < n)
+                        asm volatile("red.global.add.f32 [%0], %1;" ::"l"(o + u * step), "f"(v[u]) : "memory");
+                return;
             }
 #pragma unroll
             for (int u = 0; u < C; ++u)
@@ -191,23 +270,29 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
                 if (u < n)
                     store16(a.zout, (j0 + (int64_t)u * jstep) * a.ldz + i, v[u], a.is_bf16);
         }
-        with_act(a.act, [&](auto c) {
+        float y[C];
 #pragma unroll
-            for (int u = 0; u < C; ++u)
-                v[u] = act_value<decltype(c)::value>(v[u]);
-        });
+        for (int u = 0; u < C; ++u)
+            y[u] = v[u];
+        with_act(a.act, [&](auto k) { apply_act<decltype(k)::value>(y); });
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+            v[u] = y[u];
         if (aux != nullptr) {
 #pragma unroll
             for (int u = 0; u < C; ++u)
                 v[u] += x[u];
         }
     } else if constexpr (EPI == kEpiGradIn) {
-        if (aux != nullptr)
-            with_act(a.act, [&](auto c) {
+        float y[C];
 #pragma unroll
-                for (int u = 0; u < C; ++u)
-                    v[u] *= act_slope<decltype(c)::value>(x[u]);
-            });
+        for (int u = 0; u < C; ++u)
+            y[u] = v[u];
+        if (aux != nullptr)
+            with_act(a.act, [&](auto k) { apply_slope<decltype(k)::value>(y, x); });
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+            v[u] = y[u];
     } else if (aux != nullptr) {
 #pragma unroll
         for (int u = 0; u < C; ++u)
@@ -374,11 +459,10 @@ __device__ __forceinline__ void emit64(const LinearArgs &a, int64_t i0, int64_t 
                 x[u] = load16(staged(stage, lane, c + u), 0, a.is_bf16);
         }
         if constexpr (EPI == kEpiForward) {
-            with_act(a.act, [&](auto k) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    v[u] = act_value<decltype(k)::value>(v[u] + bias);
-            });
+            for (int u = 0; u < 16; ++u)
+                v[u] += bias;
+            with_act(a.act, [&](auto k) { apply_act<decltype(k)::value>(v); });
             if (has_aux) {
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
@@ -386,11 +470,7 @@ __device__ __forceinline__ void emit64(const LinearArgs &a, int64_t i0, int64_t 
             }
         } else if constexpr (EPI == kEpiGradIn) {
             if (has_aux)
-                with_act(a.act, [&](auto k) {
-#pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        v[u] *= act_slope<decltype(k)::value>(x[u]);
-                });
+                with_act(a.act, [&](auto k) { apply_slope<decltype(k)::value>(v, x); });
         } else if (has_aux) {
 #pragma unroll
             for (int u = 0; u < 16; ++u)
@@ -1238,14 +1318,17 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const __grid_constant
                 hz[u] = n + u < a.N ? z[u] : (uint16_t)0;
             }
         }
-        with_act(a.act, [&](auto c) {
+        constexpr int C = V < 2 ? 2 : V;
+        float v[C] = {}, x[C] = {};
 #pragma unroll
-            for (int u = 0; u < V; ++u) {
-                float v[1];
-                v[0] = load16(hy, u, a.is_bf16) * act_slope<decltype(c)::value>(load16(hz, u, a.is_bf16));
-                store16(hy, u, v[0], a.is_bf16);
-            }
-        });
+        for (int u = 0; u < V; ++u) {
+            v[u] = load16(hy, u, a.is_bf16);
+            x[u] = load16(hz, u, a.is_bf16);
+        }
+        with_act(a.act, [&](auto k) { apply_slope<decltype(k)::value>(v, x); });
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+            store16(hy, u, v[u], a.is_bf16);
         if (V == 8 && whole) {
             *reinterpret_cast<uint4 *>(dz) = *reinterpret_cast<const uint4 *>(hy);
         } else {

@@ -666,38 +666,65 @@ __global__ void __launch_bounds__(1024) policy_loss_long_kernel(const __grid_con
     tc::cluster_sync();  // no CTA leaves while its sums may still be read
 }
 
-// The four statistics from the tokens' logp, in one CTA and a fixed order (in
-// double: the float32 terms of either sign may cancel).
+// An unevaluated sum of two floats (Knuth's two-sum): the statistics' terms of
+// either sign may cancel, and double additions are slow here (8 us for 16 tokens).
+struct Two {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Two add_two(Two a, Two b)
+{
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+    const float lo = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+    Two r;
+    r.hi = __fadd_rn(s, lo);
+    r.lo = __fsub_rn(lo, __fsub_rn(r.hi, s));
+    return r;
+}
+
+// weight x, with the product's rounding error in lo.
+__device__ __forceinline__ Two product_two(float w, float x)
+{
+    const float p = __fmul_rn(w, x);
+    return Two{p, __fmaf_rn(w, x, -p)};
+}
+
+// The four statistics from the tokens' logp, in one CTA and a fixed order.
 __global__ void __launch_bounds__(1024) loss_stats_kernel(const __grid_constant__ LossArgs a)
 {
-    __shared__ double part[32][4];
-    tc::wait_dependencies();  // the rows' kernel is done
-    double s[4] = {0, 0, 0, 0};
-    for (int64_t t = threadIdx.x; t < a.T; t += 1024) {
-        const Token token(a, t);
-        if (!token.live(a))
-            continue;
-        const Terms r = terms_of(a, token, a.logp_out[t]);
-        const double w = token.weight;
-        s[0] += w * r.loss;
-        s[1] += w * r.kl;
-        s[2] += w * r.clipped;
-        s[3] += w * r.ratio;
+    __shared__ Two part[4][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+    Two s[4] = {};
+    Token token(a, threadIdx.x);  // what the rows' kernel does not write: ahead of the wait
+    tc::wait_dependencies();      // the rows' kernel is done
+    for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x) {
+        const Token next(a, t + blockDim.x);
+        if (token.live(a)) {
+            const Terms r = terms_of(a, token, a.logp_out[t]);
+            s[0] = add_two(s[0], product_two(token.weight, r.loss));
+            s[1] = add_two(s[1], product_two(token.weight, r.kl));
+            s[2] = add_two(s[2], product_two(token.weight, r.clipped));
+            s[3] = add_two(s[3], product_two(token.weight, r.ratio));
+        }
+        token = next;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
-            s[q] += __shfl_xor_sync(~0u, s[q], d);
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x >> 5][q] = s[q];
+            s[q] = add_two(s[q], Two{__shfl_xor_sync(~0u, s[q].hi, d), __shfl_xor_sync(~0u, s[q].lo, d)});
+        if (lane == 0)
+            part[q][warp] = s[q];
     }
     __syncthreads();
-    if (threadIdx.x < 4) {
-        double t = 0;
-        for (int i = 0; i < 32; ++i)
-            t += part[i][threadIdx.x];
-        a.stats[threadIdx.x] = (float)t;
+    if (warp < 4) {
+        Two t = lane < warps ? part[warp][lane] : Two{0.0f, 0.0f};
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            t = add_two(t, Two{__shfl_xor_sync(~0u, t.hi, d), __shfl_xor_sync(~0u, t.lo, d)});
+        if (lane == 0)
+            a.stats[warp] = t.hi;
     }
 }
 
@@ -792,7 +819,7 @@ cudaError_t launch_policy_loss(const LossArgs &a, cudaStream_t s)
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3(1, 1, 1);
-        cfg.blockDim = dim3(1024, 1, 1);
+        cfg.blockDim = dim3(a.T <= 128 ? 128 : 1024, 1, 1);
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
