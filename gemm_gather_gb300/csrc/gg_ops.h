@@ -43,6 +43,7 @@ struct LinearArgs {
     int64_t ldz;
     int chunk;             // k-blocks accumulated in TMEM before they are added in registers
     int group;             // feature tiles per group of the tile order (pair kernel)
+    int bt;                // tokens of a tile (pair kernel)
     int *status;
     uint64_t wait_limit_ns;
     int inject_stall;
@@ -51,8 +52,8 @@ struct LinearArgs {
 // Which kernel a product runs, with its tile and split (see plan_linear).
 struct LinearPlan {
     int kernel;  // GG_LINEAR_NONE / GG_LINEAR_SPLIT / GG_LINEAR_PAIR
-    int bt;      // split kernel: tokens per tile
-    int split;   // split kernel: CTAs (cluster size) that share one tile's contraction
+    int bt;      // tokens per tile
+    int split;   // CTAs (split kernel) or CTA pairs that share one tile's contraction
 };
 LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path);
 cudaError_t launch_linear(int epi, const LinearArgs &a, const LinearPlan &p, cudaStream_t s,

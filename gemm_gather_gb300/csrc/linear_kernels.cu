@@ -38,7 +38,9 @@
 // where a float32 sum rounded to nearest has 1.5e-6).  That is nothing to a
 // 16-bit result, but weight gradients are kept in float32 over long sums of
 // tokens, so the weight gradient accumulates kChunk k-blocks in TMEM and adds
-// the chunks in registers with round-to-nearest.
+// the chunks in registers with round-to-nearest.  Chunks of 896: 8.1e-7, near a
+// float32 product's own 6.1e-7 at 4096 tokens, and 165 us for the gradient of an
+// 8192 x 3584 weight over them (512: 4.7e-7 and 182 us; one chunk: 4.4e-6, 163 us).
 //
 // Every mbarrier wait is bounded; one that gives up stores GG_ERR_TIMEOUT in
 // the status word and raises the CTA's abort flag, and every role drains what
@@ -64,10 +66,16 @@ using namespace tc;
 constexpr int kSMs = 152;
 constexpr int kBK = 64;                    // k of one stage: a 128-byte swizzle row
 constexpr int UK = 16;                     // k of one MMA
-constexpr int kChunk = 8;                  // k-blocks per TMEM chunk of a weight gradient (512 k)
+constexpr int kChunk = 14;                 // k-blocks per TMEM chunk of a weight gradient (896 k)
 constexpr int kMnBox = kBK * 64 * 2;       // 8 KB: 64 k-rows x 64 columns of an MN-major operand
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 constexpr int kMaxStages = 8;
+
+// The epilogue's staging (see below): tokens at a time, bytes of a warp, 16-byte
+// accesses of a lane.
+constexpr int kStageCols = 32;
+constexpr int kWarpStage = kStageCols * 64;  // 32 tokens x 32 features x 2 bytes
+constexpr int kRowSteps = kStageCols / 8;    // 16-byte accesses of a lane
 
 struct Shared {
     uint64_t full[kMaxStages];
@@ -311,10 +319,10 @@ __device__ __forceinline__ float load_bias(const LinearArgs &a, int64_t i)
     return a.bias_f32 ? reinterpret_cast<const float *>(a.bias)[i] : load16(a.bias, i, a.is_bf16);
 }
 
-// Valid columns of the 64, or of the 16, from j0.
-__device__ __forceinline__ int valid64(int64_t J, int64_t j0)
+// Valid columns of a staging's, or of 16, from j0.
+__device__ __forceinline__ int valid_rows(int64_t J, int64_t j0)
 {
-    return J - j0 >= 64 ? 64 : (J > j0 ? (int)(J - j0) : 0);
+    return J - j0 >= kStageCols ? kStageCols : (J > j0 ? (int)(J - j0) : 0);
 }
 
 __device__ __forceinline__ int valid16(int64_t J, int64_t j0)
@@ -326,12 +334,10 @@ __device__ __forceinline__ int valid16(int64_t J, int64_t j0)
 // A lane owns one feature (MMA row), so a warp that stored its values directly
 // would write 64-byte pieces two bytes a lane: measured, 20 cycles of an SM for
 // each such store, 40,000 for a 256 x 256 tile, as long as a contraction over
-// 8192.  Instead a warp turns its 32 features x 64 tokens around in 4 KB of its
+// 8192.  Instead a warp turns 32 features x 32 tokens around in 2 KB of its
 // own shared memory: two-byte stores along a row there, then 16 bytes a lane,
 // 8 rows of 64 bytes per global access.  Tensors read in the epilogue come
 // the same way, loaded into registers ahead of the accumulator.
-constexpr int kStageCols = 64;
-constexpr int kWarpStage = kStageCols * 64;  // 64 tokens x 32 features x 2 bytes
 
 // One 16-bit M x N tensor of the epilogue; vec: 16-byte accesses are aligned.
 struct Rows {
@@ -352,12 +358,12 @@ __device__ __forceinline__ Rows rows_of(const void *p, int64_t ld)
 // 32 features from i0 of `n` tokens from j0: lane l takes features 8 (l mod 4)
 // on of tokens l / 4 + 8 k.
 __device__ __forceinline__ void read_rows(const Rows &t, int64_t I, int64_t i0, int64_t j0, int n, int lane,
-                                          uint4 (&x)[8])
+                                          uint4 (&x)[kRowSteps])
 {
     const int64_t i = i0 + (lane & 3) * 8;
     const uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kRowSteps; ++k) {
         x[k] = make_uint4(0u, 0u, 0u, 0u);
         if ((lane >> 2) + 8 * k < n) {
             const uint16_t *q = p + (int64_t)(8 * k) * t.ld;
@@ -374,10 +380,10 @@ __device__ __forceinline__ void read_rows(const Rows &t, int64_t I, int64_t i0, 
     }
 }
 
-__device__ __forceinline__ void stage_rows(uint8_t *stage, int lane, const uint4 (&x)[8])
+__device__ __forceinline__ void stage_rows(uint8_t *stage, int lane, const uint4 (&x)[kRowSteps])
 {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < kRowSteps; ++k)
         *reinterpret_cast<uint4 *>(stage + k * 512 + lane * 16) = x[k];
     __syncwarp();
 }
@@ -389,7 +395,7 @@ __device__ __forceinline__ void write_rows(const Rows &t, int64_t I, int64_t i0,
     const int64_t i = i0 + (lane & 3) * 8;
     uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kRowSteps; ++k) {
         if ((lane >> 2) + 8 * k < n) {
             const uint4 x = *reinterpret_cast<const uint4 *>(stage + k * 512 + lane * 16);
             uint16_t *q = p + (int64_t)(8 * k) * t.ld;
@@ -422,12 +428,12 @@ __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
     return rows_of(a.aux, a.ldaux);
 }
 
-// The epilogue of a warp's 32 features (from i0) and up to 64 tokens (from j0, n
+// The epilogue of a warp's 32 features (from i0) and up to 32 tokens (from j0, n
 // of them).  sums(col, v) gives this lane's sums of columns col .. col + 15; it
 // may be called twice.  aux: the rows read beside them (has_aux).
 template <int EPI, typename Sums>
-__device__ __forceinline__ void emit64(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane,
-                                       float bias, bool has_aux, const uint4 (&aux)[8],
+__device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane,
+                                       float bias, bool has_aux, const uint4 (&aux)[kRowSteps],
                                        uint8_t *stage, Sums sums)
 {
     // sums in registers need constant columns; the others keep the code small
@@ -498,11 +504,11 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *ma
     }
 }
 
-// ---- pair kernel: 256 features x BT tokens per CTA pair ----------------------------
+// ---- pair kernel: 256 features x bt <= BT tokens per CTA pair ----------------------------
 namespace pair {
 constexpr int kTileI = 256;
 constexpr int kA = 128 * kBK * 2;        // 16 KB: this CTA's 128 features of one k-block
-constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, half the columns each
+constexpr int kEpiWarps = 16;            // four per TMEM lane quarter, a quarter of the columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 template <int BT>
 struct Geo {
@@ -567,7 +573,8 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     const int64_t unit = (int64_t)cluster_id_x();
     const int64_t nunits = (int64_t)ncluster_x();
     const int tiles_i = (int)((a.I + pair::kTileI - 1) / pair::kTileI);
-    const int tiles_j = (int)((a.J + BT - 1) / BT);
+    const int bt = EPI == kEpiGradW ? BT : a.bt;  // tokens of a tile, BT at most
+    const int tiles_j = (int)((a.J + bt - 1) / bt);
     const int64_t total = (int64_t)tiles_i * tiles_j;
     const int all_kb = (int)((a.K + kBK - 1) / kBK);
     const int kb0 = (int)((int64_t)all_kb * part / parts);
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 
     // epilogue warps: their TMEM lanes, columns and staging
     const int q = warp & 3;              // TMEM lane quarter this warp may access
-    const int half = (warp - 2) >> 2;    // columns [half * BT/2, half * BT/2 + BT/2)
+    const int group = (warp - 2) >> 2;   // columns [group * BT/4, group * BT/4 + BT/4)
     uint8_t *stage_buf = smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
     bool ok = true;
 
@@ -610,13 +617,14 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         // ===================== producer =====================================
         const uint64_t pol = ptx::policy_evict_normal();
         const bool elected = ptx::elect_one_sync();
+        const uint32_t stage_bytes = 2u * (uint32_t)(pair::kA + bt / 2 * kBK * 2);  // both CTAs'
         int stage = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
         for (int64_t t = unit; t < total && ok; t += nunits) {
             const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
             const int i0 = c.ti * pair::kTileI + (int)rank * 128;
-            const int j0 = c.tj * BT + (int)rank * (BT / 2);
+            const int j0 = c.tj * bt + (int)rank * (bt / 2);
             for (int kb = 0; kb < num_kb; ++kb) {
                 const bool got = role_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1u,
                                            a.wait_limit_ns, abort_flag);
@@ -629,7 +637,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
                     const uint32_t local_full = ptx::smem_addr(&sh.full[stage]);
                     const uint32_t bar = map_to_rank(local_full, lead);  // both CTAs' loads
                     if (leader)
-                        ptx::mbar_arrive_expect_tx(local_full, 2 * G::kStage);
+                        ptx::mbar_arrive_expect_tx(local_full, stage_bytes);
                     const uint32_t sa = base + stage * G::kStage;
                     load_operand<2, 128>(sa, &map_a, a.a_mn, i0, (kb0 + kb) * kBK, bar, pol);
                     load_operand<2, BT / 2>(sa + pair::kA, &map_b, a.b_mn, j0, (kb0 + kb) * kBK, bar, pol);
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         }
     } else if (warp == 1) {
         // ===================== MMA issuer (leader CTA) ======================
-        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, BT);
+        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, bt);
         const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;  // 16 k further, in descriptors
         const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
         const uint32_t lo_a = desc_lo(base, a.a_mn ? kMnBox : 16);
@@ -721,10 +729,10 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
         }
     } else {
-        // ===================== epilogue (warps 2-9) =========================
-        constexpr int kCols = BT / 2;            // this warp's columns
+        // ===================== epilogue (warps 2-17) ========================
+        constexpr int kCols = BT / 4;            // this warp's columns
         constexpr int kGroups = kCols / kStageCols;
-        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * kCols);
+        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(group * kCols);
         const uint32_t empty0 = map_to_rank(ptx::smem_addr(&sh.tmem_empty[0]), lead);
         const Rows aux = aux_of<EPI>(a);
         const bool early = aux.p != nullptr && parts == 1;
@@ -733,11 +741,13 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         for (int64_t t = unit; t < total && ok; t += nunits) {
             const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
             const int64_t i0 = (int64_t)c.ti * pair::kTileI + (int)rank * 128 + q * 32;
-            const int64_t j0 = (int64_t)c.tj * BT + half * kCols;
+            const int64_t j0 = (int64_t)c.tj * bt + group * kCols;
+            // the first token that is not this tile's
+            const int64_t end = gg_min64(a.J, (int64_t)(c.tj + 1) * bt);
             const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
-            uint4 pre[8];
+            uint4 pre[kRowSteps];
             if (EPI != kEpiGradW && early)  // the first group's rows, while the MMAs run
-                read_rows(aux, a.I, i0, j0, valid64(a.J, j0), lane, pre);
+                read_rows(aux, a.I, i0, j0, valid_rows(end, j0), lane, pre);
             float sum[EPI == kEpiGradW ? kCols : 1];
             if constexpr (EPI == kEpiGradW) {
 #pragma unroll
@@ -772,7 +782,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
                             sum[col + u] += v[u];
                     }
                 } else if (parts > 1) {  // every load and MMA of this CTA is done: the ring is free
-                    float *partial = reinterpret_cast<float *>(smem) + half * kCols * 128 + q * 32 + lane;
+                    float *partial = reinterpret_cast<float *>(smem) + group * kCols * 128 + q * 32 + lane;
 #pragma unroll 1
                     for (int col = 0; col < kCols; col += 16) {
                         float v[16];
@@ -785,10 +795,10 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 #pragma unroll 1
                     for (int g = 0; g < kGroups; ++g) {
                         const int64_t jg = j0 + g * kStageCols;
-                        emit64<EPI>(a, i0, jg, valid64(a.J, jg), lane, bias, early, pre, stage_buf,
+                        emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, stage_buf,
                                     [&](int col, float(&v)[16]) { from_tmem(g * kStageCols + col, v); });
                         if (early && g + 1 < kGroups)
-                            read_rows(aux, a.I, i0, jg + kStageCols, valid64(a.J, jg + kStageCols), lane, pre);
+                            read_rows(aux, a.I, i0, jg + kStageCols, valid_rows(end, jg + kStageCols), lane, pre);
                     }
                 }
                 // accumulator read: hand it back to the leader's MMA warp
@@ -799,7 +809,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             }
             if constexpr (EPI == kEpiGradW) {
                 if (ok && parts > 1) {
-                    float *partial = reinterpret_cast<float *>(smem) + half * kCols * 128 + q * 32 + lane;
+                    float *partial = reinterpret_cast<float *>(smem) + group * kCols * 128 + q * 32 + lane;
 #pragma unroll
                     for (int u = 0; u < kCols; ++u)
                         partial[u * 128] = sum[u];
@@ -810,15 +820,15 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 16; ++u)
                             v[u] = sum[col + u];
-                        emit16<EPI>(a, i0 + lane, j0 + col, 1, valid16(a.J, j0 + col), v, 0.0f);
+                        emit16<EPI>(a, i0 + lane, j0 + col, 1, valid16(end, j0 + col), v, 0.0f);
                     }
                 } else if (ok) {
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         const int64_t jg = j0 + g * kStageCols;
                         if (early)
-                            read_rows(aux, a.I, i0, jg, valid64(a.J, jg), lane, pre);
-                        emit64<EPI>(a, i0, jg, valid64(a.J, jg), lane, 0.0f, early, pre, stage_buf,
+                            read_rows(aux, a.I, i0, jg, valid_rows(end, jg), lane, pre);
+                        emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, 0.0f, early, pre, stage_buf,
                                     [&](int col, float(&v)[16]) {
 #pragma unroll
                                         for (int u = 0; u < 16; ++u)
@@ -842,27 +852,31 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         cluster_sync();
         if (warp >= 2 && ok) {
             const pair::Tile c = pair::tile_at(a, unit, tiles_i, tiles_j);
-            const int cols = BT / parts / 2;  // per warp: 16, 32 or 64
-            const int col0 = part * (BT / parts) + half * cols;
+            // 16 columns a warp at least: with 32 left for a pair, half the warps finish them
+            const int cols = BT / parts >= 64 ? BT / parts / 4 : 16;
+            const int col0 = part * (BT / parts) + group * cols;
             const int64_t i0 = (int64_t)c.ti * pair::kTileI + (int)rank * 128 + q * 32;
             const int64_t j0 = (int64_t)c.tj * BT + col0;
             const int64_t left = a.J - j0;
-            const int n = left > cols ? cols : (left > 0 ? (int)left : 0);
+            const int n = group * cols >= BT / parts ? 0 : (left > cols ? cols : (left > 0 ? (int)left : 0));
             const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
             const uint32_t mine = base + (uint32_t)((col0 * 128 + q * 32 + lane) * 4);
             const auto joined = [&](int col, float(&v)[16]) {
-                float x[4][16];  // every pair's sums, all loads in flight
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t from = 2 * (uint32_t)(s < parts ? s : 0) + rank;
-                    const uint32_t src = map_to_rank(mine, from) + (uint32_t)col * 512;
+                for (int h = 0; h < 16; h += 8) {
+                    float x[4][8];  // every pair's sums, all loads in flight
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        x[s][u] = s < parts ? ld_cluster_f32(src + (uint32_t)u * 512) : 0.0f;
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t from = 2 * (uint32_t)(s < parts ? s : 0) + rank;
+                        const uint32_t src = map_to_rank(mine, from) + (uint32_t)(col + h) * 512;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            x[s][u] = s < parts ? ld_cluster_f32(src + (uint32_t)u * 512) : 0.0f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        v[h + u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
                 }
-#pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    v[u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
             };
             if (EPI == kEpiGradW && a.out_f32) {
 #pragma unroll 1
@@ -873,10 +887,10 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
                 }
             } else if (n > 0) {
                 const Rows aux = aux_of<EPI>(a);
-                uint4 pre[8];
+                uint4 pre[kRowSteps];
                 if (aux.p)
                     read_rows(aux, a.I, i0, j0, n, lane, pre);
-                emit64<EPI>(a, i0, j0, n, lane, bias, aux.p != nullptr, pre, stage_buf, joined);
+                emit_rows<EPI>(a, i0, j0, n, lane, bias, aux.p != nullptr, pre, stage_buf, joined);
             }
         }
         __syncwarp();
@@ -1072,7 +1086,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         uint8_t *stage_buf = smem + q * kWarpStage;  // over the spent ring, like partial
         const int64_t i0 = i - lane;
         const Rows aux = aux_of<EPI>(a);
-        uint4 pre[8];
+        uint4 pre[kRowSteps];
         const int chunks = (kb1 - kb0 + a.chunk - 1) / a.chunk;
         float sum[EPI == kEpiGradW ? BT : 1];
         if constexpr (EPI == kEpiGradW) {
@@ -1111,14 +1125,15 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                     for (int u = 0; u < 16; ++u)
                         partial[(c16 * 16 + u) * 128] = __uint_as_float(r[u]);
                 }
-                if (parts == 1) {
-                    const int n = valid64(a.J, jt) < BT ? valid64(a.J, jt) : BT;
+#pragma unroll 1
+                for (int g = 0; parts == 1 && g < BT; g += kStageCols) {
+                    const int n = valid_rows(a.J, jt + g) < BT - g ? valid_rows(a.J, jt + g) : BT - g;
                     if (aux.p)
-                        read_rows(aux, a.I, i0, jt, n, lane, pre);
-                    emit64<EPI>(a, i0, jt, n, lane, bias, aux.p != nullptr, pre, stage_buf,
+                        read_rows(aux, a.I, i0, jt + g, n, lane, pre);
+                    emit_rows<EPI>(a, i0, jt + g, n, lane, bias, aux.p != nullptr, pre, stage_buf,
                                 [&](int col, float(&v)[16]) {
                                     uint32_t r[16];
-                                    tmem_ld16(t_lane + (uint32_t)(acc * BT + col), r);
+                                    tmem_ld16(t_lane + (uint32_t)(acc * BT + g + col), r);
                                     tmem_wait16(r);
 #pragma unroll
                                     for (int u = 0; u < 16; ++u)
@@ -1147,15 +1162,18 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                         emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(a.J, jt + c16 * 16), v, 0.0f);
                     }
                 } else {
-                    const int n = valid64(a.J, jt) < BT ? valid64(a.J, jt) : BT;
-                    if (aux.p)
-                        read_rows(aux, a.I, i0, jt, n, lane, pre);
-                    emit64<EPI>(a, i0, jt, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
-                                [&](int col, float(&v)[16]) {
 #pragma unroll
-                                    for (int u = 0; u < 16; ++u)
-                                        v[u] = sum[col + u];
-                                });
+                    for (int g = 0; g < BT; g += kStageCols) {
+                        const int n = valid_rows(a.J, jt + g);
+                        if (aux.p)
+                            read_rows(aux, a.I, i0, jt + g, n, lane, pre);
+                        emit_rows<EPI>(a, i0, jt + g, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
+                                       [&](int col, float(&v)[16]) {
+#pragma unroll
+                                           for (int u = 0; u < 16; ++u)
+                                               v[u] = sum[g + col + u];
+                                       });
+                    }
                 }
             }
         }
@@ -1401,7 +1419,7 @@ struct ClusterLaunch {
 };
 
 template <int EPI, int BT>
-cudaError_t launch_pair(const LinearArgs &args, int parts, cudaStream_t s, const char **why)
+cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, cudaStream_t s, const char **why)
 {
     using G = pair::Geo<BT>;
     static std::once_flag once[kMaxDevices], once_res[kMaxDevices];
@@ -1424,13 +1442,14 @@ cudaError_t launch_pair(const LinearArgs &args, int parts, cudaStream_t s, const
     });
     CUtensorMap map_a, map_b;
     if (!operand_map(&map_a, args, args.a, args.I, args.lda, args.a_mn, 128) ||
-        !operand_map(&map_b, args, args.b, args.J, args.ldb, args.b_mn, BT / 2)) {
+        !operand_map(&map_b, args, args.b, args.J, args.ldb, args.b_mn, (uint32_t)bt / 2)) {
         *why = "encoding the operands' tensor maps";
         return cudaErrorInvalidValue;
     }
     LinearArgs a = args;
+    a.bt = bt;
     const int64_t tiles_i = (a.I + pair::kTileI - 1) / pair::kTileI;
-    const int64_t tiles_j = (a.J + BT - 1) / BT;
+    const int64_t tiles_j = (a.J + bt - 1) / bt;
     // feature tiles in equal groups of at most 8: 76 pairs cover about 8 x 9 tiles
     const int64_t groups = (tiles_i + 7) / 8;
     a.group = (int)((tiles_i + groups - 1) / groups);
@@ -1472,8 +1491,8 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
         return cudaGetLastError();
     }
     if (p.kernel == GG_LINEAR_PAIR)
-        return p.bt == 256 ? launch_pair<EPI, 256>(a, p.split, s, why)
-                           : launch_pair<EPI, 128>(a, p.split, s, why);
+        return p.bt > 128 ? launch_pair<EPI, 256>(a, p.bt, p.split, s, why)
+                          : launch_pair<EPI, 128>(a, p.bt, p.split, s, why);
     switch (p.bt) {
     case 16:
         if constexpr (EPI != kEpiGradW)
@@ -1501,8 +1520,9 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
 // shares 12.9 us, 4 shares 13.7, unsplit 17.7), short contractions are not split
 // (512 tokens, N = K = 1024: unsplit 7.3 us, 4 shares 8.6), and whole 256 x 256 tiles
 // begin where they fill most pairs (1024 tokens, N = 3584, K = 8192: 43 us, 256 x 128
-// tiles 61).  A weight gradient's split tiles are 64 wide, the boxes of its
-// MN-major B.
+// tiles 61).  Where one wave of tiles is not full, tiles of 160, 192 or 224 tokens
+// make it shorter (there: 70 tiles of 224 instead of 56).  A weight gradient keeps
+// to multiples of the 64-wide boxes of its MN-major B: 64 split, 128 or 256.
 LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
 {
     LinearPlan best{GG_LINEAR_NONE, 0, 0};
@@ -1531,12 +1551,15 @@ LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
                       (waves - 1.0) * 1590.0 + bt * (parts > 1 ? 48.0 : 36.0));
         }
     }
-    for (int bt = 128; path != GG_LINEAR_SPLIT && bt <= 256; bt *= 2) {
+    for (int bt = 128; path != GG_LINEAR_SPLIT && bt <= 256; bt += 32) {
+        const bool odd = bt != 128 && bt != 256;
+        if (odd && epi == kEpiGradW)
+            continue;
         const int64_t tiles = ((I + 255) / 256) * ((J + bt - 1) / bt);
         for (int parts = 1; parts <= 4 && parts <= num_kb; parts *= 2) {
             // pairs, and clusters of 4 and 8 CTAs, that are resident at once
             const int64_t room = parts == 1 ? 76 : (parts == 2 ? 36 : 14);
-            if (parts > 1 && tiles > room)
+            if (parts > 1 && (tiles > room || odd))
                 break;
             const double waves = (double)((tiles + room - 1) / room);
             const double mma = bt * 1.08, port = (128 + bt / 2) * kBK * 2 / 127.8;

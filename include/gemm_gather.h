@@ -487,7 +487,7 @@ gg_status gg_linear_check(const void *X, int64_t ldx, const void *W, int64_t ldw
  *   dW = X^T dZ in W's layout (pitch lddw) and dbias = the column sums of dZ,
  *     both of grad_dtype (`dtype` or GG_F32); accumulate != 0 adds them to
  *     what dW and dbias hold.  Float32 gradients are summed over the tokens
- *     in chunks of 512, added in float32 with round-to-nearest (accumulated
+ *     in chunks of 896, added in float32 with round-to-nearest (accumulated
  *     into dW by the memory's adder, which takes subnormals for zero).
  * Any of dX, dW and dbias may be NULL; X is read for dW only, W for dX only,
  * and may be NULL otherwise.

@@ -94,7 +94,7 @@ def status_ok():
 SHAPES = [  # (M, N, K)
     (1, 64, 64), (1, 129, 1000), (2, 1, 1), (3, 257, 63), (16, 128, 65), (17, 300, 520), (33, 96, 2048),
     (64, 513, 129), (100, 1000, 72), (128, 128, 64), (129, 255, 200), (255, 256, 128), (257, 511, 577),
-    (300, 1000, 1024),
+    (300, 1000, 1024), (224, 2560, 64), (1020, 3500, 72), (960, 3300, 136),
 ]
 
 
@@ -296,8 +296,8 @@ def test_gradients_against_differences():
 
 
 def test_float32_weight_gradient_over_many_tokens():
-    """Float32 weight gradients keep float32's precision over long sums: chunks of 512 tokens in
-    the tensor core's accumulator (each within 512 * 2^-23 / 16 truncations of its own size),
+    """Float32 weight gradients keep float32's precision over long sums: chunks of tokens in
+    the tensor core's accumulator (512 of them are within 512 * 2^-23 / 16 truncations of their size),
     added with round-to-nearest; far below the 2^-17 that one long accumulation shows."""
     gen = gg_inputs.generator(2)
     for path in ("split", "pair"):
