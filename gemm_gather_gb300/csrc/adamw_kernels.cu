@@ -765,8 +765,9 @@ cudaError_t launch_adamw(const gg_adamw_tensor *tensors, int count, const AdamwS
             t.v_scale = x.v_scale;
             t.copy = x.copy;
             t.n = x.n;
-            t.key = mix32(mix32(mix32(mix32((uint32_t)i) ^ h.step) ^ (uint32_t)h.seed) ^
-                          (uint32_t)(h.seed >> 32));
+            t.key = bits == 8 ? mix32(mix32(mix32(mix32((uint32_t)i) ^ h.step) ^ (uint32_t)h.seed) ^
+                                      (uint32_t)(h.seed >> 32))
+                              : 0;
             t.copy_bf16 = x.copy_dtype == GG_BF16;
             t.vec = (uint16_t)vector_width(x);
             g.first[g.count + 1] = g.first[g.count] + (uint32_t)chunks;
