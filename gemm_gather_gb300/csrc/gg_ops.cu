@@ -121,7 +121,7 @@ gg_status prepare_linear(const void *X, int64_t ldx, const void *W, int64_t ldw,
                          int64_t ldy, const void *z, int64_t ldz, int64_t M, int64_t N, int64_t K,
                          gg_dtype dtype, gg_linear_path path, gg::LinearArgs *a, gg::LinearPlan *plan)
 {
-    *plan = gg::LinearPlan{GG_LINEAR_NONE, 0, 0};
+    *plan = gg::LinearPlan{};
     GG_TRY(check_types(dtype, act, "linear"));
     GG_TRY(check_route(layout, path));
     GG_TRY(check_sizes(M, N, K));
@@ -171,15 +171,22 @@ gg_status prepare_linear(const void *X, int64_t ldx, const void *W, int64_t ldw,
     return op_ok();
 }
 
+// What a launch takes from the library's settings and the caller's status word.
+gg_status fill_in(gg::LinearArgs *a, int *dev_status)
+{
+    a->status = dev_status;
+    GG_TRY(gg::op_status_word(&a->status));
+    a->wait_limit_ns = gg::op_wait_limit_ns();
+    a->inject_stall = gg::op_inject_stall();
+    return GG_OK;
+}
+
 gg_status run_product(int epi, gg::LinearArgs *a, const gg::LinearPlan &plan, int *dev_status,
                       gg_stream_t stream)
 {
     if (a->I == 0 || a->J == 0)
         return op_ok();
-    a->status = dev_status;
-    GG_TRY(gg::op_status_word(&a->status));
-    a->wait_limit_ns = gg::op_wait_limit_ns();
-    a->inject_stall = gg::op_inject_stall();
+    GG_TRY(fill_in(a, dev_status));
     const char *why = nullptr;
     const cudaError_t e =
         gg::launch_linear(epi, *a, plan, reinterpret_cast<cudaStream_t>(stream), &why);
@@ -194,6 +201,8 @@ struct Backward {
     gg::LinearPlan plan_dx, plan_dw;
     gg::ColSumArgs sum;
     bool run_dx, run_dw, run_sum;
+    bool both;  // dX and dW in one launch, with these tiles
+    int bt_dx, bt_dw;
 };
 
 gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t ldx, const void *W,
@@ -282,6 +291,10 @@ gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t 
                          : gg::LinearPlan{};
     r.plan_dw = r.run_dw ? gg::plan_linear(gg::kEpiGradW, r.dw.I, r.dw.J, r.dw.K, path)
                          : gg::LinearPlan{};
+    r.both = r.run_dx && r.run_dw &&
+             gg::plan_both(r.dx, r.dw, r.plan_dx, r.plan_dw, path, &r.bt_dx, &r.bt_dw);
+    if (r.both)
+        r.plan_dx.kernel = r.plan_dw.kernel = GG_LINEAR_PAIR;
     *out = r;
     return op_ok();
 }
@@ -511,10 +524,20 @@ gg_status gg_linear_backward(const void *dZ, int64_t lddz, const void *X, int64_
     Backward b;
     GG_TRY(prepare_backward(dZ, lddz, X, ldx, W, ldw, layout, z_in, ldzin, act_in, dX, lddx, dW, lddw,
                             dbias, grad_dtype, accumulate, M, N, K, dtype, path, &b));
-    if (b.run_dx)
-        GG_TRY(run_product(gg::kEpiGradIn, &b.dx, b.plan_dx, dev_status, stream));
-    if (b.run_dw)
-        GG_TRY(run_product(gg::kEpiGradW, &b.dw, b.plan_dw, dev_status, stream));
+    if (b.both) {
+        GG_TRY(fill_in(&b.dx, dev_status));
+        GG_TRY(fill_in(&b.dw, dev_status));
+        const char *why = nullptr;
+        const cudaError_t e = gg::launch_both(b.dx, b.bt_dx, b.dw, b.bt_dw,
+                                              reinterpret_cast<cudaStream_t>(stream), &why);
+        if (e != cudaSuccess)
+            return op_cuda_fail(e, why ? why : "launching the gradients");
+    } else {
+        if (b.run_dx)
+            GG_TRY(run_product(gg::kEpiGradIn, &b.dx, b.plan_dx, dev_status, stream));
+        if (b.run_dw)
+            GG_TRY(run_product(gg::kEpiGradW, &b.dw, b.plan_dw, dev_status, stream));
+    }
     if (b.run_sum) {
         const cudaError_t e = gg::launch_colsum(b.sum, reinterpret_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)

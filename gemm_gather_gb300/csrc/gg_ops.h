@@ -54,10 +54,17 @@ struct LinearPlan {
     int kernel;  // GG_LINEAR_NONE / GG_LINEAR_SPLIT / GG_LINEAR_PAIR
     int bt;      // tokens per tile
     int split;   // CTAs (split kernel) or CTA pairs that share one tile's contraction
+    double ns;   // the estimate it was chosen by
 };
 LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path);
 cudaError_t launch_linear(int epi, const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
                           const char **why);
+
+// Both gradients of a layer in one launch (plan_both: whether, and their tiles).
+bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &plan_dx, const LinearPlan &plan_dw,
+               int path, int *bt_dx, int *bt_dw);
+cudaError_t launch_both(const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
+                        const char **why);
 
 struct ColSumArgs {  // out[i] (+)= sum_j x[j*ldx + i]
     const void *x;

@@ -489,17 +489,16 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
     write_rows(rows_of(a.out, a.ldo), a.I, i0, j0, n, lane, stage);
 }
 
-// One stage's operand: ROWS rows (or columns) of 64 k.  K-major: one box of
-// 64 k x ROWS rows.  MN-major: ROWS/64 boxes of 64 columns x 64 k-rows.
-template <int CG, int ROWS>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int mn, int row0,
+// One stage's operand: `rows` rows (or columns) of 64 k.  K-major: one box of
+// 64 k x rows.  MN-major: boxes of 64 columns x 64 k-rows.
+template <int CG>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int mn, int rows, int row0,
                                              int k0, uint32_t bar, uint64_t policy)
 {
     if (!mn) {
         tma_load_2d<CG>(dst, map, k0, row0, bar, policy);
     } else {
-#pragma unroll
-        for (int b = 0; b < (ROWS + 63) / 64; ++b)
+        for (int b = 0; b * 64 < rows; ++b)
             tma_load_2d<CG>(dst + b * kMnBox, map, row0 + b * 64, k0, bar, policy);
     }
 }
@@ -544,41 +543,336 @@ __device__ __forceinline__ Tile tile_at(const LinearArgs &a, int64_t t, int tile
     c.ti = g * a.group + (int)(r - (int64_t)c.tj * width);
     return c;
 }
+
+// One product's tiles, and this pair's share of their contraction.
+struct Product {
+    int tiles_i, tiles_j, kb0, num_kb;
+    int64_t total;
+    __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts)
+    {
+        tiles_i = (int)((a.I + kTileI - 1) / kTileI);
+        tiles_j = (int)((a.J + a.bt - 1) / a.bt);
+        total = (int64_t)tiles_i * tiles_j;
+        const int all_kb = (int)((a.K + kBK - 1) / kBK);
+        kb0 = (int)((int64_t)all_kb * part / parts);
+        num_kb = (int)((int64_t)all_kb * (part + 1) / parts) - kb0;
+    }
+};
+
+// Where a thread block stands: the same for all its roles but the fields a role moves.
+struct Place {
+    uint32_t base;          // shared memory, 1024-aligned
+    uint8_t *smem;
+    Shared *sh;
+    volatile int *abort_flag;
+    uint32_t tmem, rank, lead;  // position in the CTA pair; cluster rank of its leader
+    int part, parts;        // pairs that share a tile's contraction
+    int64_t unit, nunits;
+    int lane, q, group;     // epilogue: TMEM lane quarter, columns [group * BT/4, + BT/4)
+    uint8_t *stage_buf;
+    // a role's progress
+    int stage;
+    uint32_t phase;
+    int64_t count;          // k-blocks issued (producer), chunks (MMA issuer, epilogue)
+};
+
+// The producer's loads of a product's tiles first, first + nunits, ...; false when
+// a wait gave up.
+template <int BT>
+__device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensorMap &map_b, const LinearArgs &a,
+                                        const Product &p, int64_t first, bool elected, Place &at)
+{
+    using G = Geo<BT>;
+    const uint64_t pol = ptx::policy_evict_normal();
+    const uint32_t stage_bytes = 2u * (uint32_t)(kA + a.bt / 2 * kBK * 2);  // both CTAs'
+    for (int64_t t = first; t < p.total; t += at.nunits) {
+        const Tile c = tile_at(a, t, p.tiles_i, p.tiles_j);
+        const int i0 = c.ti * kTileI + (int)at.rank * 128;
+        const int j0 = c.tj * a.bt + (int)at.rank * (a.bt / 2);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+            const bool got = role_wait(ptx::smem_addr(&at.sh->empty[at.stage]), at.phase ^ 1u,
+                                       a.wait_limit_ns, at.abort_flag);
+            if (!__all_sync(0xffffffffu, got))
+                return false;
+            const bool stall = a.inject_stall && at.unit == 0 && at.part == 0 && at.count == 0;
+            if (elected && !stall) {  // test hook: the first stage is never armed
+                const uint32_t local_full = ptx::smem_addr(&at.sh->full[at.stage]);
+                const uint32_t bar = map_to_rank(local_full, at.lead);  // both CTAs' loads
+                if (at.rank == 0)
+                    ptx::mbar_arrive_expect_tx(local_full, stage_bytes);
+                const uint32_t sa = at.base + at.stage * G::kStage;
+                const int k0 = (p.kb0 + kb) * kBK;
+                load_operand<2>(sa, &map_a, a.a_mn, 128, i0, k0, bar, pol);
+                load_operand<2>(sa + kA, &map_b, a.b_mn, a.bt / 2, j0, k0, bar, pol);
+            }
+            __syncwarp();
+            ++at.count;
+            if (++at.stage == G::kStages) {
+                at.stage = 0;
+                at.phase ^= 1u;
+            }
+        }
+    }
+    return true;
+}
+
+// The MMA issuer's share of the same.
+template <int BT>
+__device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, int64_t first, bool elected,
+                                         Place &at, bool *issued_any)
+{
+    using G = Geo<BT>;
+    const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, a.bt);
+    const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;  // 16 k further, in descriptors
+    const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
+    const uint32_t lo_a = desc_lo(at.base, a.a_mn ? kMnBox : 16);
+    const uint32_t lo_b = desc_lo(at.base + kA, a.b_mn ? kMnBox : 16);
+    const uint16_t both = (uint16_t)(3u << at.lead);
+    for (int64_t t = first; t < p.total; t += at.nunits) {
+        int in_chunk = 0;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+            const int acc = (int)(at.count & 1);  // chunks issued so far: accumulator count & 1
+            bool got = true;
+            if (in_chunk == 0)
+                got = role_wait(ptx::smem_addr(&at.sh->tmem_empty[acc]),
+                                (uint32_t)((at.count >> 1) & 1) ^ 1u, a.wait_limit_ns, at.abort_flag);
+            got = got && role_wait(ptx::smem_addr(&at.sh->full[at.stage]), at.phase, a.wait_limit_ns,
+                                   at.abort_flag);
+            if (!__all_sync(0xffffffffu, got))
+                return false;
+            fence_after();
+            const bool last = in_chunk + 1 == a.chunk || kb + 1 == p.num_kb;
+            if (elected) {
+                const uint32_t stage_at = (uint32_t)(at.stage * G::kStage) >> 4;
+#pragma unroll
+                for (int k = 0; k < kBK / UK; ++k)
+                    mma_f16<2>(at.tmem + (uint32_t)(acc * BT), lo_a + stage_at + k * step_a,
+                               lo_b + stage_at + k * step_b, idesc, (uint32_t)(in_chunk | k));
+                mma_commit_to(ptx::smem_addr(&at.sh->empty[at.stage]), both);
+                if (last)
+                    mma_commit_to(ptx::smem_addr(&at.sh->tmem_full[acc]), both);
+            }
+            __syncwarp();
+            *issued_any = true;
+            ++in_chunk;
+            if (last) {
+                ++at.count;
+                in_chunk = 0;
+            }
+            if (++at.stage == G::kStages) {
+                at.stage = 0;
+                at.phase ^= 1u;
+            }
+        }
+    }
+    return true;
+}
+
+// An epilogue warp's share of the same.
+template <int EPI, int BT>
+__device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, int64_t first, Place &at)
+{
+    constexpr int kCols = BT / 4;  // this warp's columns
+    constexpr int kGroups = kCols / kStageCols;
+    const int lane = at.lane;
+    const uint32_t t_lane = at.tmem + ((uint32_t)(at.q * 32) << 16) + (uint32_t)(at.group * kCols);
+    const uint32_t empty0 = map_to_rank(ptx::smem_addr(&at.sh->tmem_empty[0]), at.lead);
+    float *partial = reinterpret_cast<float *>(at.smem) + at.group * kCols * 128 + at.q * 32 + lane;
+    const Rows aux = aux_of<EPI>(a);
+    const bool early = aux.p != nullptr && at.parts == 1;
+    const int chunks = (p.num_kb + a.chunk - 1) / a.chunk;
+    for (int64_t t = first; t < p.total; t += at.nunits) {
+        const Tile c = tile_at(a, t, p.tiles_i, p.tiles_j);
+        const int64_t i0 = (int64_t)c.ti * kTileI + (int)at.rank * 128 + at.q * 32;
+        const int64_t j0 = (int64_t)c.tj * a.bt + at.group * kCols;
+        // the first token that is not this tile's
+        const int64_t end = gg_min64(a.J, (int64_t)(c.tj + 1) * a.bt);
+        const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
+        uint4 pre[kRowSteps];
+        if (EPI != kEpiGradW && early)  // the first group's rows, while the MMAs run
+            read_rows(aux, a.I, i0, j0, valid_rows(end, j0), lane, pre);
+        float sum[EPI == kEpiGradW ? kCols : 1];
+        if constexpr (EPI == kEpiGradW) {
+#pragma unroll
+            for (int u = 0; u < kCols; ++u)
+                sum[u] = 0.0f;
+        }
+        for (int h = 0; h < chunks; ++h, ++at.count) {
+            const int acc = (int)(at.count & 1);
+            const bool got = role_wait(ptx::smem_addr(&at.sh->tmem_full[acc]),
+                                       (uint32_t)((at.count >> 1) & 1), a.wait_limit_ns, at.abort_flag);
+            if (!__all_sync(0xffffffffu, got))
+                return false;
+            fence_after();
+            const uint32_t t_addr = t_lane + (uint32_t)(acc * BT);
+            const auto from_tmem = [&](int col, float(&v)[16]) {
+                uint32_t r[16];
+                tmem_ld16(t_addr + (uint32_t)col, r);
+                tmem_wait16(r);
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = __uint_as_float(r[u]);
+            };
+            if constexpr (EPI == kEpiGradW) {
+#pragma unroll
+                for (int col = 0; col < kCols; col += 16) {
+                    float v[16];
+                    from_tmem(col, v);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        sum[col + u] += v[u];
+                }
+            } else if (at.parts > 1) {  // every load and MMA of this CTA is done: the ring is free
+#pragma unroll 1
+                for (int col = 0; col < kCols; col += 16) {
+                    float v[16];
+                    from_tmem(col, v);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        partial[(col + u) * 128] = v[u];
+                }
+            } else {
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    const int64_t jg = j0 + g * kStageCols;
+                    emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, at.stage_buf,
+                                   [&](int col, float(&v)[16]) { from_tmem(g * kStageCols + col, v); });
+                    if (early && g + 1 < kGroups)
+                        read_rows(aux, a.I, i0, jg + kStageCols, valid_rows(end, jg + kStageCols), lane, pre);
+                }
+            }
+            // accumulator read: hand it back to the leader's MMA warp
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(empty0 + (uint32_t)(acc * sizeof(uint64_t)));
+        }
+        if constexpr (EPI == kEpiGradW) {
+            if (at.parts > 1) {
+#pragma unroll
+                for (int u = 0; u < kCols; ++u)
+                    partial[u * 128] = sum[u];
+            } else if (a.out_f32) {
+#pragma unroll
+                for (int col = 0; col < kCols; col += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        v[u] = sum[col + u];
+                    emit16<EPI>(a, i0 + lane, j0 + col, 1, valid16(end, j0 + col), v, 0.0f);
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int64_t jg = j0 + g * kStageCols;
+                    if (early)
+                        read_rows(aux, a.I, i0, jg, valid_rows(end, jg), lane, pre);
+                    emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
+                                   [&](int col, float(&v)[16]) {
+#pragma unroll
+                                       for (int u = 0; u < 16; ++u)
+                                           v[u] = sum[g * kStageCols + col + u];
+                                   });
+                }
+            }
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+// The end of a split tile: the pairs' partial tiles, added in order.  Pair `part`
+// finishes columns [part, part + 1) * BT / parts, its CTAs their own 128 features.
+template <int EPI, int BT>
+__device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p, Place &at)
+{
+    const int lane = at.lane, parts = at.parts;
+    const Tile c = tile_at(a, at.unit, p.tiles_i, p.tiles_j);
+    // 16 columns a warp at least: with 32 left for a pair, half the warps finish them
+    const int cols = BT / parts >= 64 ? BT / parts / 4 : 16;
+    const int col0 = at.part * (BT / parts) + at.group * cols;
+    const int64_t i0 = (int64_t)c.ti * kTileI + (int)at.rank * 128 + at.q * 32;
+    const int64_t j0 = (int64_t)c.tj * BT + col0;
+    const int64_t left = a.J - j0;
+    const int n = at.group * cols >= BT / parts ? 0 : (left > cols ? cols : (left > 0 ? (int)left : 0));
+    const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
+    const uint32_t mine = at.base + (uint32_t)((col0 * 128 + at.q * 32 + lane) * 4);
+    const auto joined = [&](int col, float(&v)[16]) {
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+            float x[4][8];  // every pair's sums, all loads in flight
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t from = 2 * (uint32_t)(s < parts ? s : 0) + at.rank;
+                const uint32_t src = map_to_rank(mine, from) + (uint32_t)(col + h) * 512;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    x[s][u] = s < parts ? ld_cluster_f32(src + (uint32_t)u * 512) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[h + u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
+        }
+    };
+    if (EPI == kEpiGradW && a.out_f32) {
+#pragma unroll 1
+        for (int col = 0; col < n; col += 16) {
+            float v[16];
+            joined(col, v);
+            emit16<EPI>(a, i0 + lane, j0 + col, 1, n - col < 16 ? n - col : 16, v, 0.0f);
+        }
+    } else if (n > 0) {
+        const Rows aux = aux_of<EPI>(a);
+        uint4 pre[kRowSteps];
+        if (aux.p)
+            read_rows(aux, a.I, i0, j0, n, lane, pre);
+        emit_rows<EPI>(a, i0, j0, n, lane, bias, aux.p != nullptr, pre, at.stage_buf, joined);
+    }
+}
 }  // namespace pair
 
 // A cluster is one CTA pair that walks its share of the tiles, or, when tiles
-// are few, 2 or 4 pairs that split one tile's contraction.
-template <int EPI, int BT>
+// are few, 2 or 4 pairs that split one tile's contraction.  With a second product
+// (EPI1 >= 0: a layer's input and weight gradients, which both read dZ), its
+// tiles follow the first one's in the same walk: one launch, one last wave, and
+// small products side by side.
+template <int EPI, int EPI1, int BT>
 __global__ void __launch_bounds__(pair::kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ LinearArgs a)
+                const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap map_a1,
+                const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ LinearArgs a1)
 {
     using G = pair::Geo<BT>;
+    constexpr bool kTwo = EPI1 >= 0;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;  // 1024-aligned for the 128B swizzle
-    uint8_t *smem = smem_raw + (base - raw);
-    Shared &sh = *reinterpret_cast<Shared *>(smem + G::kOffShared);
-    volatile int *abort_flag = &sh.abort_flag;
+    pair::Place at;
+    at.base = (raw + 1023u) & ~1023u;  // 1024-aligned for the 128B swizzle
+    at.smem = smem_raw + (at.base - raw);
+    at.sh = reinterpret_cast<Shared *>(at.smem + G::kOffShared);
+    at.abort_flag = &at.sh->abort_flag;
+    Shared &sh = *at.sh;
 
     launch_dependents();
     const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
-    const uint32_t rank = crank & 1u;           // position in the CTA pair
-    const uint32_t lead = crank & ~1u;          // cluster rank of the pair's leader
-    const bool leader = rank == 0;
-    const int parts = (int)cluster_size() / 2;  // pairs that share a tile's contraction
-    const int part = (int)crank / 2;
-    const int64_t unit = (int64_t)cluster_id_x();
-    const int64_t nunits = (int64_t)ncluster_x();
-    const int tiles_i = (int)((a.I + pair::kTileI - 1) / pair::kTileI);
-    const int bt = EPI == kEpiGradW ? BT : a.bt;  // tokens of a tile, BT at most
-    const int tiles_j = (int)((a.J + bt - 1) / bt);
-    const int64_t total = (int64_t)tiles_i * tiles_j;
-    const int all_kb = (int)((a.K + kBK - 1) / kBK);
-    const int kb0 = (int)((int64_t)all_kb * part / parts);
-    const int num_kb = (int)((int64_t)all_kb * (part + 1) / parts) - kb0;
+    at.lane = threadIdx.x & 31;
+    at.rank = crank & 1u;
+    at.lead = crank & ~1u;
+    at.parts = kTwo ? 1 : (int)cluster_size() / 2;
+    at.part = kTwo ? 0 : (int)crank / 2;
+    at.unit = (int64_t)cluster_id_x();
+    at.nunits = (int64_t)ncluster_x();
+    at.q = warp & 3;
+    at.group = (warp - 2) >> 2;
+    at.stage_buf = at.smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
+    at.stage = 0;
+    at.phase = 0;
+    at.count = 0;
+    const pair::Product p(a, at.part, at.parts);
+    const pair::Product p1(kTwo ? a1 : a, at.part, at.parts);
+    // this pair's first tile of the second product: the walk goes on where the first ended
+    const int64_t first1 = ((at.unit - p.total) % at.nunits + at.nunits) % at.nunits;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
@@ -593,9 +887,13 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         sh.abort_flag = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && at.lane == 0) {
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
+        if (kTwo) {
+            prefetch_tensormap(&map_a1);
+            prefetch_tensormap(&map_b1);
+        }
     }
     if (warp == 1) {
         tmem_alloc<2>(ptx::smem_addr(&sh.tmem_base), 2 * BT);
@@ -604,121 +902,42 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anything signals them
     fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    at.tmem = sh.tmem_base;
     wait_dependencies();  // what earlier launches write is there from here on
 
-    // epilogue warps: their TMEM lanes, columns and staging
-    const int q = warp & 3;              // TMEM lane quarter this warp may access
-    const int group = (warp - 2) >> 2;   // columns [group * BT/4, group * BT/4 + BT/4)
-    uint8_t *stage_buf = smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
     bool ok = true;
-
     if (warp == 0) {
         // ===================== producer =====================================
-        const uint64_t pol = ptx::policy_evict_normal();
         const bool elected = ptx::elect_one_sync();
-        const uint32_t stage_bytes = 2u * (uint32_t)(pair::kA + bt / 2 * kBK * 2);  // both CTAs'
-        int stage = 0;
-        uint32_t phase = 0;
-        int64_t issued = 0;
-        for (int64_t t = unit; t < total && ok; t += nunits) {
-            const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
-            const int i0 = c.ti * pair::kTileI + (int)rank * 128;
-            const int j0 = c.tj * bt + (int)rank * (bt / 2);
-            for (int kb = 0; kb < num_kb; ++kb) {
-                const bool got = role_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1u,
-                                           a.wait_limit_ns, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                const bool stall = a.inject_stall && unit == 0 && part == 0 && issued == 0;
-                if (elected && !stall) {  // test hook: the first stage is never armed
-                    const uint32_t local_full = ptx::smem_addr(&sh.full[stage]);
-                    const uint32_t bar = map_to_rank(local_full, lead);  // both CTAs' loads
-                    if (leader)
-                        ptx::mbar_arrive_expect_tx(local_full, stage_bytes);
-                    const uint32_t sa = base + stage * G::kStage;
-                    load_operand<2, 128>(sa, &map_a, a.a_mn, i0, (kb0 + kb) * kBK, bar, pol);
-                    load_operand<2, BT / 2>(sa + pair::kA, &map_b, a.b_mn, j0, (kb0 + kb) * kBK, bar, pol);
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == G::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
+        ok = pair::produce<BT>(map_a, map_b, a, p, at.unit, elected, at);
+        if (kTwo && ok)
+            ok = pair::produce<BT>(map_a1, map_b1, a1, p1, first1, elected, at);
         if (!ok) {
-            *abort_flag = 1;
+            *at.abort_flag = 1;
             report_status(a.status, kStatusTimeout);
         }
         // drain: every load this warp issued has landed before the CTA may exit
-        if (leader) {
-            const int64_t pending = issued < G::kStages ? issued : G::kStages;
+        if (at.rank == 0) {
+            const int64_t pending = at.count < G::kStages ? at.count : G::kStages;
             for (int64_t d = 0; d < pending; ++d) {
-                const int64_t idx = issued - 1 - d;
+                const int64_t idx = at.count - 1 - d;
                 ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
                                (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
             }
-        } else if (!ok && issued > 0) {
+        } else if (!ok && at.count > 0) {
             sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
         }
     } else if (warp == 1) {
         // ===================== MMA issuer (leader CTA) ======================
-        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, bt);
-        const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;  // 16 k further, in descriptors
-        const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
-        const uint32_t lo_a = desc_lo(base, a.a_mn ? kMnBox : 16);
-        const uint32_t lo_b = desc_lo(base + pair::kA, a.b_mn ? kMnBox : 16);
         const bool elected = ptx::elect_one_sync();
-        const uint16_t both = (uint16_t)(3u << lead);
-        int stage = 0;
-        uint32_t phase = 0;
-        int64_t nchunk = 0;  // chunks issued so far: accumulator nchunk & 1
         bool issued_any = false;
-        for (int64_t t = unit; leader && t < total && ok; t += nunits) {
-            int in_chunk = 0;
-            for (int kb = 0; kb < num_kb; ++kb) {
-                const int acc = (int)(nchunk & 1);
-                bool got = true;
-                if (in_chunk == 0)
-                    got = role_wait(ptx::smem_addr(&sh.tmem_empty[acc]),
-                                    (uint32_t)((nchunk >> 1) & 1) ^ 1u, a.wait_limit_ns, abort_flag);
-                got = got && role_wait(ptx::smem_addr(&sh.full[stage]), phase, a.wait_limit_ns,
-                                       abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
-                const bool last = in_chunk + 1 == a.chunk || kb + 1 == num_kb;
-                if (elected) {
-                    const uint32_t at = (uint32_t)(stage * G::kStage) >> 4;
-#pragma unroll
-                    for (int k = 0; k < kBK / UK; ++k)
-                        mma_f16<2>(tmem + (uint32_t)(acc * BT), lo_a + at + k * step_a,
-                                   lo_b + at + k * step_b, idesc, (uint32_t)(in_chunk | k));
-                    mma_commit_to(ptx::smem_addr(&sh.empty[stage]), both);
-                    if (last)
-                        mma_commit_to(ptx::smem_addr(&sh.tmem_full[acc]), both);
-                }
-                __syncwarp();
-                issued_any = true;
-                ++in_chunk;
-                if (last) {
-                    ++nchunk;
-                    in_chunk = 0;
-                }
-                if (++stage == G::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
+        if (at.rank == 0) {
+            ok = pair::multiply<BT>(a, p, at.unit, elected, at, &issued_any);
+            if (kTwo && ok)
+                ok = pair::multiply<BT>(a1, p1, first1, elected, at, &issued_any);
         }
         if (!ok) {
-            *abort_flag = 1;
+            *at.abort_flag = 1;
             report_status(a.status, kStatusTimeout);
         }
         // drain: all MMAs of this thread have completed before TMEM is freed
@@ -730,170 +949,25 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         }
     } else {
         // ===================== epilogue (warps 2-17) ========================
-        constexpr int kCols = BT / 4;            // this warp's columns
-        constexpr int kGroups = kCols / kStageCols;
-        const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(group * kCols);
-        const uint32_t empty0 = map_to_rank(ptx::smem_addr(&sh.tmem_empty[0]), lead);
-        const Rows aux = aux_of<EPI>(a);
-        const bool early = aux.p != nullptr && parts == 1;
-        const int chunks = (num_kb + a.chunk - 1) / a.chunk;
-        int64_t nchunk = 0;
-        for (int64_t t = unit; t < total && ok; t += nunits) {
-            const pair::Tile c = pair::tile_at(a, t, tiles_i, tiles_j);
-            const int64_t i0 = (int64_t)c.ti * pair::kTileI + (int)rank * 128 + q * 32;
-            const int64_t j0 = (int64_t)c.tj * bt + group * kCols;
-            // the first token that is not this tile's
-            const int64_t end = gg_min64(a.J, (int64_t)(c.tj + 1) * bt);
-            const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
-            uint4 pre[kRowSteps];
-            if (EPI != kEpiGradW && early)  // the first group's rows, while the MMAs run
-                read_rows(aux, a.I, i0, j0, valid_rows(end, j0), lane, pre);
-            float sum[EPI == kEpiGradW ? kCols : 1];
-            if constexpr (EPI == kEpiGradW) {
-#pragma unroll
-                for (int u = 0; u < kCols; ++u)
-                    sum[u] = 0.0f;
-            }
-            for (int h = 0; h < chunks; ++h, ++nchunk) {
-                const int acc = (int)(nchunk & 1);
-                const bool got = role_wait(ptx::smem_addr(&sh.tmem_full[acc]),
-                                           (uint32_t)((nchunk >> 1) & 1), a.wait_limit_ns, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
-                const uint32_t t_addr = t_lane + (uint32_t)(acc * BT);
-                const auto from_tmem = [&](int col, float(&v)[16]) {
-                    uint32_t r[16];
-                    tmem_ld16(t_addr + (uint32_t)col, r);
-                    tmem_wait16(r);
-#pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        v[u] = __uint_as_float(r[u]);
-                };
-                if constexpr (EPI == kEpiGradW) {
-#pragma unroll
-                    for (int col = 0; col < kCols; col += 16) {
-                        float v[16];
-                        from_tmem(col, v);
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            sum[col + u] += v[u];
-                    }
-                } else if (parts > 1) {  // every load and MMA of this CTA is done: the ring is free
-                    float *partial = reinterpret_cast<float *>(smem) + group * kCols * 128 + q * 32 + lane;
-#pragma unroll 1
-                    for (int col = 0; col < kCols; col += 16) {
-                        float v[16];
-                        from_tmem(col, v);
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            partial[(col + u) * 128] = v[u];
-                    }
-                } else {
-#pragma unroll 1
-                    for (int g = 0; g < kGroups; ++g) {
-                        const int64_t jg = j0 + g * kStageCols;
-                        emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, stage_buf,
-                                    [&](int col, float(&v)[16]) { from_tmem(g * kStageCols + col, v); });
-                        if (early && g + 1 < kGroups)
-                            read_rows(aux, a.I, i0, jg + kStageCols, valid_rows(end, jg + kStageCols), lane, pre);
-                    }
-                }
-                // accumulator read: hand it back to the leader's MMA warp
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(empty0 + (uint32_t)(acc * sizeof(uint64_t)));
-            }
-            if constexpr (EPI == kEpiGradW) {
-                if (ok && parts > 1) {
-                    float *partial = reinterpret_cast<float *>(smem) + group * kCols * 128 + q * 32 + lane;
-#pragma unroll
-                    for (int u = 0; u < kCols; ++u)
-                        partial[u * 128] = sum[u];
-                } else if (ok && a.out_f32) {
-#pragma unroll
-                    for (int col = 0; col < kCols; col += 16) {
-                        float v[16];
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            v[u] = sum[col + u];
-                        emit16<EPI>(a, i0 + lane, j0 + col, 1, valid16(end, j0 + col), v, 0.0f);
-                    }
-                } else if (ok) {
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const int64_t jg = j0 + g * kStageCols;
-                        if (early)
-                            read_rows(aux, a.I, i0, jg, valid_rows(end, jg), lane, pre);
-                        emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, 0.0f, early, pre, stage_buf,
-                                    [&](int col, float(&v)[16]) {
-#pragma unroll
-                                        for (int u = 0; u < 16; ++u)
-                                            v[u] = sum[g * kStageCols + col + u];
-                                    });
-                    }
-                }
-            }
-            __syncwarp();
+        ok = pair::finish<EPI, BT>(a, p, at.unit, at);
+        if constexpr (kTwo) {
+            if (ok)
+                ok = pair::finish<EPI1, BT>(a1, p1, first1, at);
         }
         if (!ok) {
-            *abort_flag = 1;
+            *at.abort_flag = 1;
             report_status(a.status, kStatusTimeout);
         }
     }
 
     __syncthreads();
-    if (parts > 1) {
-        // the pairs' partial tiles, added in order; pair `part` finishes columns
-        // [part, part + 1) * BT / parts, its CTAs their own 128 features
-        cluster_sync();
-        if (warp >= 2 && ok) {
-            const pair::Tile c = pair::tile_at(a, unit, tiles_i, tiles_j);
-            // 16 columns a warp at least: with 32 left for a pair, half the warps finish them
-            const int cols = BT / parts >= 64 ? BT / parts / 4 : 16;
-            const int col0 = part * (BT / parts) + group * cols;
-            const int64_t i0 = (int64_t)c.ti * pair::kTileI + (int)rank * 128 + q * 32;
-            const int64_t j0 = (int64_t)c.tj * BT + col0;
-            const int64_t left = a.J - j0;
-            const int n = group * cols >= BT / parts ? 0 : (left > cols ? cols : (left > 0 ? (int)left : 0));
-            const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
-            const uint32_t mine = base + (uint32_t)((col0 * 128 + q * 32 + lane) * 4);
-            const auto joined = [&](int col, float(&v)[16]) {
-#pragma unroll
-                for (int h = 0; h < 16; h += 8) {
-                    float x[4][8];  // every pair's sums, all loads in flight
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint32_t from = 2 * (uint32_t)(s < parts ? s : 0) + rank;
-                        const uint32_t src = map_to_rank(mine, from) + (uint32_t)(col + h) * 512;
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            x[s][u] = s < parts ? ld_cluster_f32(src + (uint32_t)u * 512) : 0.0f;
-                    }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        v[h + u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
-                }
-            };
-            if (EPI == kEpiGradW && a.out_f32) {
-#pragma unroll 1
-                for (int col = 0; col < n; col += 16) {
-                    float v[16];
-                    joined(col, v);
-                    emit16<EPI>(a, i0 + lane, j0 + col, 1, n - col < 16 ? n - col : 16, v, 0.0f);
-                }
-            } else if (n > 0) {
-                const Rows aux = aux_of<EPI>(a);
-                uint4 pre[kRowSteps];
-                if (aux.p)
-                    read_rows(aux, a.I, i0, j0, n, lane, pre);
-                emit_rows<EPI>(a, i0, j0, n, lane, bias, aux.p != nullptr, pre, stage_buf, joined);
-            }
+    if constexpr (!kTwo) {
+        if (at.parts > 1) {
+            cluster_sync();
+            if (warp >= 2 && ok)
+                pair::join_parts<EPI, BT>(a, p, at);
+            __syncwarp();
         }
-        __syncwarp();
     }
 
     // ---- teardown ---------------------------------------------------------------
@@ -902,7 +976,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     cluster_sync();  // the leader's MMAs into the peer's TMEM and smem are done, partials read
     if (warp == 1) {
         fence_after();
-        tmem_dealloc<2>(tmem, 2 * BT);
+        tmem_dealloc<2>(at.tmem, 2 * BT);
     }
 }
 
@@ -1002,8 +1076,8 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                 const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
                 ptx::mbar_arrive_expect_tx(bar, G::kStage);
                 const uint32_t sa = base + stage * G::kStage;
-                load_operand<1, 128>(sa, &map_a, a.a_mn, ti * 128, kb * kBK, bar, pol);
-                load_operand<1, BT>(sa + split::kA, &map_b, a.b_mn, tj * BT, kb * kBK, bar, pol);
+                load_operand<1>(sa, &map_a, a.a_mn, 128, ti * 128, kb * kBK, bar, pol);
+                load_operand<1>(sa + split::kA, &map_b, a.b_mn, BT, tj * BT, kb * kBK, bar, pol);
             }
             __syncwarp();
             ++issued;
@@ -1248,11 +1322,13 @@ __global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ Line
 // Bound: the read of dZ.
 constexpr int kSumParts = 8;
 
-__global__ void __cluster_dims__(kSumParts, 1, 1) __launch_bounds__(256)
+__global__ void __launch_bounds__(256)
     colsum_kernel(const __grid_constant__ ColSumArgs a)
 {
     __shared__ float part[32][65];
     __shared__ float total[64];
+    launch_dependents();
+    wait_dependencies();
     const int rank = (int)cluster_ctarank();
     const int64_t i0 = (int64_t)cluster_id_x() * 64;
     const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
@@ -1418,14 +1494,16 @@ struct ClusterLaunch {
     }
 };
 
-template <int EPI, int BT>
-cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, cudaStream_t s, const char **why)
+// One product, or two (args1, with bt1) in one walk.
+template <int EPI, int EPI1, int BT>
+cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, const LinearArgs *args1, int bt1, cudaStream_t s,
+                        const char **why)
 {
     using G = pair::Geo<BT>;
     static std::once_flag once[kMaxDevices], once_res[kMaxDevices];
     static cudaError_t result[kMaxDevices];
     static int resident_by_dev[kMaxDevices];
-    cudaError_t e = allow_smem(pair_kernel<EPI, BT>, G::kSmemBytes, once, result);
+    cudaError_t e = allow_smem(pair_kernel<EPI, EPI1, BT>, G::kSmemBytes, once, result);
     if (e != cudaSuccess) {
         *why = "setting the shared-memory size of the linear kernel";
         return e;
@@ -1435,29 +1513,38 @@ cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, cudaStream_t 
         int resident = 0;
         ClusterLaunch l(2, 2, pair::kThreads, G::kSmemBytes, nullptr);
         l.cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&resident, pair_kernel<EPI, BT>, &l.cfg) != cudaSuccess)
+        if (cudaOccupancyMaxActiveClusters(&resident, pair_kernel<EPI, EPI1, BT>, &l.cfg) != cudaSuccess)
             resident = 0;
         (void)cudaGetLastError();
         resident_by_dev[dev] = resident;
     });
-    CUtensorMap map_a, map_b;
-    if (!operand_map(&map_a, args, args.a, args.I, args.lda, args.a_mn, 128) ||
-        !operand_map(&map_b, args, args.b, args.J, args.ldb, args.b_mn, (uint32_t)bt / 2)) {
-        *why = "encoding the operands' tensor maps";
-        return cudaErrorInvalidValue;
+    CUtensorMap maps[4];
+    LinearArgs a[2] = {args, args1 ? *args1 : args};
+    a[0].bt = bt;
+    a[1].bt = args1 ? bt1 : bt;
+    int64_t tiles = 0;
+    for (int k = 0; k < (args1 ? 2 : 1); ++k) {
+        LinearArgs &x = a[k];
+        if (!operand_map(&maps[2 * k], x, x.a, x.I, x.lda, x.a_mn, 128) ||
+            !operand_map(&maps[2 * k + 1], x, x.b, x.J, x.ldb, x.b_mn, (uint32_t)x.bt / 2)) {
+            *why = "encoding the operands' tensor maps";
+            return cudaErrorInvalidValue;
+        }
+        const int64_t tiles_i = (x.I + pair::kTileI - 1) / pair::kTileI;
+        // feature tiles in equal groups of at most 8: 76 pairs cover about 8 x 9 tiles
+        const int64_t groups = (tiles_i + 7) / 8;
+        x.group = (int)((tiles_i + groups - 1) / groups);
+        tiles += tiles_i * ((x.J + x.bt - 1) / x.bt);
     }
-    LinearArgs a = args;
-    a.bt = bt;
-    const int64_t tiles_i = (a.I + pair::kTileI - 1) / pair::kTileI;
-    const int64_t tiles_j = (a.J + bt - 1) / bt;
-    // feature tiles in equal groups of at most 8: 76 pairs cover about 8 x 9 tiles
-    const int64_t groups = (tiles_i + 7) / 8;
-    a.group = (int)((tiles_i + groups - 1) / groups);
+    if (!args1) {
+        maps[2] = maps[0];
+        maps[3] = maps[1];
+    }
     const int resident = resident_by_dev[dev] > 0 ? resident_by_dev[dev] : kSMs / 2;
     // split tiles: one cluster each; whole ones: the pairs that fit walk them
-    const int64_t clusters = parts > 1 ? tiles_i * tiles_j : gg_min64(resident, tiles_i * tiles_j);
+    const int64_t clusters = parts > 1 ? tiles : gg_min64(resident, tiles);
     ClusterLaunch l(2 * parts, 2 * parts * clusters, pair::kThreads, G::kSmemBytes, s);
-    return cudaLaunchKernelEx(&l.cfg, pair_kernel<EPI, BT>, map_a, map_b, a);
+    return cudaLaunchKernelEx(&l.cfg, pair_kernel<EPI, EPI1, BT>, maps[0], maps[1], a[0], maps[2], maps[3], a[1]);
 }
 
 template <int EPI, int BT>
@@ -1491,8 +1578,8 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
         return cudaGetLastError();
     }
     if (p.kernel == GG_LINEAR_PAIR)
-        return p.bt > 128 ? launch_pair<EPI, 256>(a, p.bt, p.split, s, why)
-                          : launch_pair<EPI, 128>(a, p.bt, p.split, s, why);
+        return p.bt > 128 ? launch_pair<EPI, -1, 256>(a, p.bt, p.split, nullptr, 0, s, why)
+                          : launch_pair<EPI, -1, 128>(a, p.bt, p.split, nullptr, 0, s, why);
     switch (p.bt) {
     case 16:
         if constexpr (EPI != kEpiGradW)
@@ -1510,6 +1597,15 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
 
 }  // namespace
 
+// A k-block of a pair's 256 x bt tile: its MMAs, its operands through the SM's port,
+// or the ring's latency.
+static double pair_kb_ns(int bt)
+{
+    const double mma = bt * 1.08, port = (128 + bt / 2) * kBK * 2 / 127.8;
+    const double kb = mma > port ? mma : port;
+    return kb > 181.0 ? kb : 181.0;
+}
+
 // Which kernel, tile and split: the one of least estimated time, in nanoseconds.
 // The estimate is a launch and its set-up, then waves x k-blocks x the time of a
 // k-block (its MMAs, its operands through an SM's port, or the latency of the
@@ -1525,16 +1621,13 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
 // to multiples of the 64-wide boxes of its MN-major B: 64 split, 128 or 256.
 LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
 {
-    LinearPlan best{GG_LINEAR_NONE, 0, 0};
+    LinearPlan best{GG_LINEAR_NONE, 0, 0, 0.0};
     if (I <= 0 || J <= 0 || K <= 0)
         return best;
     const int64_t num_kb = (K + kBK - 1) / kBK;
-    double least = 0.0;
     const auto offer = [&](int kernel, int bt, int parts, double ns) {
-        if (best.kernel == GG_LINEAR_NONE || ns < least) {
-            least = ns;
-            best = LinearPlan{kernel, bt, parts};
-        }
+        if (best.kernel == GG_LINEAR_NONE || ns < best.ns)
+            best = LinearPlan{kernel, bt, parts, ns};
     };
     for (int bt = epi == kEpiGradW ? 64 : 16; path != GG_LINEAR_PAIR && bt <= 64; bt *= 2) {
         const int64_t tiles = ((I + 127) / 128) * ((J + bt - 1) / bt);
@@ -1562,15 +1655,60 @@ LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
             if (parts > 1 && (tiles > room || odd))
                 break;
             const double waves = (double)((tiles + room - 1) / room);
-            const double mma = bt * 1.08, port = (128 + bt / 2) * kBK * 2 / 127.8;
-            double kb = mma > port ? mma : port;
-            kb = kb > 181.0 ? kb : 181.0;
             offer(GG_LINEAR_PAIR, bt, parts,
                   5290.0 + (parts > 1 ? 3500.0 : 0.0) +
-                      waves * (double)((num_kb + parts - 1) / parts) * kb + 8.6 * bt / parts);
+                      waves * (double)((num_kb + parts - 1) / parts) * pair_kb_ns(bt) + 8.6 * bt / parts);
         }
     }
     return best;
+}
+
+// The tiles of both gradients of a layer in one walk of the pairs, where that is
+// estimated to end before the two products one after the other: side by side when
+// all tiles fit one wave, else with one launch and one last wave less (with the bias
+// gradient, apart and together: 41 and 30 us for 777 tokens, K = 1523, N = 1000; 312
+// and 291 us for 4096 tokens, K = 8192, N = 3584).
+bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &plan_dx, const LinearPlan &plan_dw,
+               int path, int *bt_dx, int *bt_dw)
+{
+    if (path == GG_LINEAR_SPLIT || dx.K <= 0 || dw.K <= 0)
+        return false;
+    const auto tiles = [](const LinearArgs &x, int bt) { return ((x.I + 255) / 256) * ((x.J + bt - 1) / bt); };
+    const auto kbs = [](const LinearArgs &x) { return (double)((x.K + kBK - 1) / kBK); };
+    double least = path == GG_LINEAR_PAIR ? 1e300 : plan_dx.ns + plan_dw.ns;
+    bool found = false;
+    for (int b0 = 128; b0 <= 256; b0 += 32)
+        for (int b1 = 128; b1 <= 256; b1 += 128) {
+            const int64_t t0 = tiles(dx, b0), t1 = tiles(dw, b1);
+            const double w0 = kbs(dx) * pair_kb_ns(b0), w1 = kbs(dw) * pair_kb_ns(b1);
+            // waves of tiles; a walk of both kinds ends with either
+            double ns = 0.0;
+            if (t0 + t1 <= 76)
+                ns = w0 > w1 ? w0 : w1;
+            else
+                ns = ((double)t0 * w0 + (double)t1 * w1) / 76.0 + 0.5 * (w0 < w1 ? w0 : w1);
+            ns += 5290.0 + 8.6 * (b0 > b1 ? b0 : b1);
+            if (ns < least) {
+                least = ns;
+                *bt_dx = b0;
+                *bt_dw = b1;
+                found = true;
+            }
+        }
+    return found;
+}
+
+cudaError_t launch_both(const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
+                        const char **why)
+{
+    if (!tensor_maps_available()) {
+        *why = "cuTensorMapEncodeTiled is not available";
+        return cudaErrorNotSupported;
+    }
+    LinearArgs x = dx, w = dw;
+    x.chunk = 1 << 30;
+    w.chunk = kChunk;
+    return launch_pair<kEpiGradIn, kEpiGradW, 256>(x, bt_dx, 1, &w, bt_dw, s, why);
 }
 
 cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, cudaStream_t s,
@@ -1593,9 +1731,8 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
 
 cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t s)
 {
-    const int64_t clusters = (a.I + 63) / 64;
-    colsum_kernel<<<(unsigned)(clusters * kSumParts), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    ClusterLaunch l(kSumParts, (a.I + 63) / 64 * kSumParts, 256, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, colsum_kernel, a);
 }
 
 cudaError_t launch_act_backward(const ActBackwardArgs &a, cudaStream_t s)

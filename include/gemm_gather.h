@@ -494,7 +494,7 @@ gg_status gg_linear_check(const void *X, int64_t ldx, const void *W, int64_t ldw
  * Alignment: dZ, X and W 16-byte aligned with pitches that are multiples of 8,
  * as far as they are read; the others any.  M == 0 gives zero sums (dW and
  * dbias are cleared, or kept when accumulating); N == 0 a zero dX.
- * One launch per gradient asked for, on `stream`.
+ * The two products run in one launch where that is estimated to be faster.
  * ------------------------------------------------------------------------- */
 gg_status gg_linear_backward(const void *dZ, int64_t lddz, const void *X, int64_t ldx, const void *W,
                              int64_t ldw, gg_weight_layout layout, const void *z_in, int64_t ldzin,

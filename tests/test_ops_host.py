@@ -81,14 +81,17 @@ def backward(**kw):
 
 
 def test_backward_accepts():
-    assert backward() == ("split", "split")
+    assert backward() == ("pair", "pair")                  # both in one walk of the pairs
     assert backward(path="pair") == ("pair", "pair")
+    assert backward(path="split") == ("split", "split")
     assert backward(dX=None, W=None) == ("none", "split")
     assert backward(dW=None, X=None) == ("split", "none")
     assert backward(dW=None, dX=None, X=None, W=None) == ("none", "none")
-    assert backward(dX=at(3)) == ("split", "split")        # dX over z_in
-    assert backward(layout="nk", ldw=504, lddw=501, dW=at(5) + 4) == ("split", "split")
-    assert backward(gdt=BF16, db=at(6) + 2) == ("split", "split")
+    for path in ("auto", "split"):
+        want = (("pair", "pair"), ("split", "split"))[path == "split"]
+        assert backward(dX=at(3), path=path) == want       # dX over z_in
+        assert backward(layout="nk", ldw=504, lddw=501, dW=at(5) + 4, path=path) == want
+        assert backward(gdt=BF16, db=at(6) + 2, path=path) == want
     assert backward(M=0, dZ=None, X=None) == ("none", "none")
 
 
