@@ -96,6 +96,7 @@ struct LossArgs {
     void *dlogits;
     int64_t ldd;
     int *status;
+    uint64_t wait_limit_ns;
 };
 cudaError_t launch_policy_loss(const LossArgs &a, cudaStream_t s);
 

@@ -13,7 +13,11 @@
 //
 // A cluster of CTAs owns a row, each CTA a slice, and the CTAs exchange
 // (maximum, sum) through distributed shared memory.
-// Bound: HBM, one read and one write of the logits.
+// Bound: HBM, one read and one write of the logits.  Measured: 8191 x 32768
+// float32 with a tenth of the tokens masked in 320 us (94 % of the copy rate),
+// 4096 x 100003 bfloat16 with a quarter masked in 263 us (80 %; twice the powers a
+// byte, and the passes' ends are not all covered by the SM's other CTA); 16 x 8192
+// in 5.7 us, which is two launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -472,25 +476,52 @@ struct Lane {
     }
 };
 
+// What a warp sends to every CTA of the cluster: its maximum and sum; the first
+// warp of the first CTA also the target's logit.
+struct alignas(16) Message {
+    float m, s, logit, unused;
+};
+
+// One asynchronous store of 16 bytes into CTA `to`'s shared memory, counted on its
+// barrier.  Nobody waits for a fence: with a cluster barrier (release, acquire) in
+// its place, each row also waited for the stores of the row before, and a quarter
+// of the stall cycles were those.
+__device__ __forceinline__ void send(uint32_t dst, uint32_t bar, uint32_t to, const Message &x)
+{
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+            tc::map_to_rank(dst, to)),
+        "r"(__float_as_uint(x.m)), "r"(__float_as_uint(x.s)), "r"(__float_as_uint(x.logit)), "r"(0),
+        "r"(tc::map_to_rank(bar, to))
+        : "memory");
+}
+
 template <typename E, int NB>
 __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const __grid_constant__ LossArgs a)
 {
     constexpr int VEC = Elem<E>::kVec, NV = NB * kBatch;
-    extern __shared__ __align__(16) uint8_t smem[];  // [warp][vector of a lane][lane]
-    __shared__ Sum sums[2][32];
+    extern __shared__ __align__(16) uint8_t smem[];  // [warp][vector of a lane][lane], then the messages
+    __shared__ uint64_t arrived[2];
     tc::launch_dependents();  // the statistics' launch
     const int parts = (int)tc::cluster_size(), rank = (int)tc::cluster_ctarank();
-    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x / 32;
     const int64_t step = tc::ncluster_x();
     const float c = a.inv_temperature * kLog2e;
     const int first = warp * NV * 32 + lane;  // this lane's first vector of the slice
+    const int count = warps * parts;
+    Message *const messages = reinterpret_cast<Message *>(smem + blockDim.x * NV * 16);  // [2][count]
     Lane<E, NB> mine;
     mine.slot = smem + first * 16;
     mine.slot_at = ptx::smem_addr(mine.slot);
-    const Gather gather(sums[0], threads / 32, parts, lane);
+    if (tid < 2)
+        ptx::mbar_init(ptx::smem_addr(&arrived[tid]), 1);
+    ptx::fence_barrier_init();
+    __syncthreads();
+    tc::cluster_sync();  // every CTA's barriers are there
 
     // The next row: its slice, how many vectors this lane has in it (none where the
-    // token is masked), its ragged ends and its target's logit.
+    // token is masked), its ragged ends and, in one thread of the cluster, its
+    // target's logit.
     Slice<E> s(a, rank, parts), n = s;
     const uint8_t *from = nullptr;
     int have_next = 0;
@@ -503,7 +534,8 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
         from = reinterpret_cast<const uint8_t *>(n.vec() + first);
         have_next = n.nvec > first ? (n.nvec - first + 31) / 32 : 0;
         have_next = have_next < NV ? have_next : NV;
-        picked = Elem<E>::get(n.row[k.target]);
+        if (rank == 0 && tid == 0)
+            picked = Elem<E>::get(n.row[k.target]);
         xh = n.has_head(tid) ? Elem<E>::get(n.row[n.lo + tid]) : -INFINITY;
         xt = n.has_tail(tid) ? Elem<E>::get(n.row[n.v1 + tid]) : -INFINITY;
     };
@@ -512,7 +544,8 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
     Token now(a, t), next(a, t + step);
     look(t, now);
     mine.fetch_all(from, have_next);
-    for (uint32_t turn = 0; t < a.T; t += step) {
+    uint32_t turn = 0, phase = 0;  // of the messages: two buffers in turn
+    for (; t < a.T; t += step) {
         const Token later(a, t + 2 * step);
         s = n;
         const bool live = now.live(a);  // the same for the whole cluster
@@ -521,6 +554,10 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
         look(t + step, next);
         const bool full = __all_sync(~0u, have == NV);
         if (live) {
+            const uint32_t bar = ptx::smem_addr(&arrived[turn]);
+            Message *const box = messages + turn * count;
+            if (tid == 0)
+                ptx::mbar_arrive_expect_tx(bar, (uint32_t)(count * (int)sizeof(Message)));
             Sum acc{fmaxf(head, tail), 0.0f};
             const float m = base_of(acc.m);
             acc.s = ex2((head - m) * c) + ex2((tail - m) * c);  // -inf where there is none
@@ -529,15 +566,27 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
             else
                 mine.template sum_up<false>(acc, have, c);
             acc = warp_join(acc, c);
-            if (lane == 0)
-                sums[turn][warp] = acc;
+            // The warps' sums, to every CTA.  The target's logit travels with one of
+            // them, so that no gradient is written over it before it has been read.  A
+            // buffer is filled again two rows on: by then every warp of the cluster has
+            // sent the next row's sum, after it had read this one's.
+            const Message said{acc.m, acc.s, __shfl_sync(~0u, logit, 0), 0.0f};
+            if (lane < parts)
+                send(ptx::smem_addr(box + rank * warps + warp), bar, (uint32_t)lane, said);
+            if (!__all_sync(~0u, ptx::mbar_wait(bar, phase, a.wait_limit_ns))) {
+                if (lane == 0)
+                    report_status(a.status, kStatusTimeout);
+                break;
+            }
+            Sum all{-INFINITY, 0.0f};
+            for (int i = lane; i < count; i += 32)
+                all = join(all, Sum{box[i].m, box[i].s}, c);
+            all = warp_join(all, c);
+            const float target_logit = box[0].logit;
             __syncwarp();
-            // every warp's sum is there and every read of the target's logit is done;
-            // sums[turn] is written again two rows on, behind the next row's barrier
-            tc::cluster_sync();
-            const Sum all = gather.join_all(sums[0], turn * (uint32_t)sizeof(sums[0]), lane, c);
+            phase ^= turn;
             turn ^= 1;
-            const float logp = logp_of(a, all, logit);
+            const float logp = logp_of(a, all, target_logit);
             if (rank == 0 && tid == 0)
                 a.logp_out[t] = logp;
             const Gradient<E> g(a, now, all, logp, c);
@@ -566,9 +615,12 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
                     s.out[s.lo + tid] = g.one(head);
                 if (s.has_tail(tid))
                     s.out[s.v1 + tid] = g.one(tail);
-                __syncthreads();  // the target's element after the others
-                if (tid == 0 && g.target >= s.lo && g.target < s.hi)
-                    s.out[g.target] = g.target_one(logit);
+                // the target's element, by the thread that has just written it
+                const int at = g.target - s.v0, vi = at / VEC;
+                const bool in_vectors = at >= 0 && g.target < s.v1 && vi % 32 == lane && vi / (NV * 32) == warp;
+                if (in_vectors || (s.has_head(tid) && g.target == s.lo + tid) ||
+                    (s.has_tail(tid) && g.target == s.v1 + tid))
+                    s.out[g.target] = g.target_one(target_logit);
             }
         } else {
             mine.fetch_all(from, have_next);
@@ -577,13 +629,14 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
                 if (now.weight != 0.0f)
                     report_status(a.status, kInvalidArg);
             }
-            s.zero(tid, threads);
+            s.zero(tid, blockDim.x);
         }
         now = next;
         next = later;
     }
+    wait_groups(0);
     __syncwarp();
-    tc::cluster_sync();  // no CTA leaves while its sums may still be read
+    tc::cluster_sync();  // no CTA leaves while a message may still be on its way to it
 }
 
 // Rows beyond what a cluster's shared memory holds: the second pass reads memory
@@ -730,7 +783,8 @@ __global__ void __launch_bounds__(1024) loss_stats_kernel(const __grid_constant_
 
 constexpr int kMaxDevices = 64;
 constexpr int kSliceVecs = 6400;             // 100 KB: two CTAs on an SM
-constexpr int kMaxSliceBytes = 224 * 1024;
+constexpr int kMaxSliceBytes = 216 * 1024;
+constexpr int kMaxMessageBytes = 2 * 8 * (kMaxSliceBytes / 8192) * 16;  // of 8 CTAs
 
 template <typename E, int NB>
 cudaError_t launch_held(cudaLaunchConfig_t &cfg, const LossArgs &a)
@@ -742,7 +796,8 @@ cudaError_t launch_held(cudaLaunchConfig_t &cfg, const LossArgs &a)
         dev = 0;
     std::call_once(once[dev], [&] {
         result[dev] = cudaFuncSetAttribute(policy_loss_kernel<E, NB>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceBytes);
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kMaxSliceBytes + kMaxMessageBytes);
     });
     if (result[dev] != cudaSuccess)
         return result[dev];
@@ -754,7 +809,9 @@ cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
 {
     // A row's vectors (one more than V needs: a row may start between two
     // 16-byte boundaries) are shared by as few CTAs as hold 100 KB each, two on an
-    // SM; by up to 8 (a portable cluster) of up to 224 KB where that is not enough.
+    // SM; by up to 8 (a portable cluster) of up to 216 KB where that is not enough.
+    // (Of up to 52 KB each: 294 us for 263 at 4096 x 100003 bfloat16, 332 for 320 at
+    // 8191 x 32768 float32; of up to 200 KB, one on an SM: 293 and 390.)
     // When the rows are few, more and smaller CTAs share a row, down to 128 vectors
     // each.  Threads have up to 16 vectors.
     const int64_t vecs = (a.V + Elem<E>::kVec - 1) / Elem<E>::kVec + 1;
@@ -771,8 +828,9 @@ cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
     threads = held ? threads : 1024;
     // Clusters: one for every 3 rows, as far as there are more rows than clusters
     // resident at once.  Masked rows cost half: with fixed shares for all rows
-    // (resident clusters only) the unluckiest ended a quarter late (297 us; 12 rows
-    // each 315, 3 rows 284, 1 row, with no copy ahead, 305 at 4096 x 100003 bf16).
+    // (resident clusters only) the unluckiest ended a quarter late.  4096 x 100003
+    // bfloat16: 2 rows 267 us, 3 rows 263, 4 rows 262, 6 rows 264; with a slower
+    // exchange 12 rows 315, all rows 297, 1 row (no copy ahead) 305, 3 rows 284.
     const int64_t fit = kMaxSliceBytes / bytes;
     const int64_t per_sm = fit < 1 ? 1 : gg_min64(fit, gg_min64(16, 896 / threads > 0 ? 896 / threads : 1));
     const int64_t resident = per_sm * kSMs / parts;
@@ -786,7 +844,7 @@ cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(clusters * parts), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = held ? (size_t)bytes : 0;
+    cfg.dynamicSmemBytes = held ? (size_t)(bytes + 2 * parts * (threads / 32) * (int64_t)sizeof(Message)) : 0;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

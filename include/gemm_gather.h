@@ -545,11 +545,13 @@ gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t l
  * per token; stats: 4 floats.  dlogits (T x V of `dtype`, pitch ldd) may be
  * logits itself (same pointer and pitch), or NULL for the loss alone.
  * logp_out is required (the statistics are summed from it); stats may be NULL.
- * A token of weight 0 is masked: its logits, target and statistics are not
- * read, its dlogits row is zero and its logp_out 0.  Logits of -inf are
- * tokens of probability 0; a row of nothing else, or one with NaN or +inf,
- * gives NaN.  A target outside [0, V) stores GG_ERR_INVALID_ARG in the status
- * word (dev_status, or the library's when NULL) and its token counts as masked.
+ * A token of weight 0 is masked: its logits are not read, its target, advantage
+ * and log-probabilities are ignored, its dlogits row is zero and its logp_out 0.
+ * Logits of -inf are tokens of probability 0; a row of nothing else, or one with
+ * NaN or +inf, gives NaN.  A target outside [0, V) stores GG_ERR_INVALID_ARG in
+ * the status word (dev_status, or the library's when NULL) and its token counts
+ * as masked; a wait inside the kernel that reaches the wait limit stores
+ * GG_ERR_TIMEOUT and the results are incomplete.
  * Each row is read from memory once.  Any alignment and pitch.
  * ------------------------------------------------------------------------- */
 gg_status gg_policy_loss(const void *logits, int64_t ld, const int64_t *target,
