@@ -44,6 +44,8 @@ struct LinearArgs {
     int chunk;             // k-blocks accumulated in TMEM before they are added in registers
     int group;             // feature tiles per group of the tile order (pair kernel)
     int bt;                // tokens of a tile (pair kernel)
+    int tiles_i, tiles_j, num_kb;  // feature and token tiles, k-blocks
+    int skip;              // pairs of the grid past the end of the first product's walk
     int *status;
     uint64_t wait_limit_ns;
     int inject_stall;

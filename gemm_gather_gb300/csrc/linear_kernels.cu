@@ -504,6 +504,13 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *ma
 }
 
 // ---- pair kernel: 256 features x bt <= BT tokens per CTA pair ----------------------------
+// Part `part`'s k-blocks of num_kb (below 2^26, the tensor map's limit).
+__device__ __forceinline__ void share_of(int num_kb, int part, int parts, int &kb0, int &n)
+{
+    kb0 = (int)((uint32_t)num_kb * (uint32_t)part / (uint32_t)parts);
+    n = (int)((uint32_t)num_kb * (uint32_t)(part + 1) / (uint32_t)parts) - kb0;
+}
+
 namespace pair {
 constexpr int kTileI = 256;
 constexpr int kA = 128 * kBK * 2;        // 16 KB: this CTA's 128 features of one k-block
@@ -531,31 +538,30 @@ struct Tile {
 // tile runs over the group's feature tiles.  The pairs running at one time
 // then cover about as many feature tiles as token tiles, which keeps the
 // slices of A and B that they read from DRAM and share through L2 few.
-__device__ __forceinline__ Tile tile_at(const LinearArgs &a, int64_t t, int tiles_i, int tiles_j)
+// Unsigned: a product has fewer than 2^31 tiles (launch_pair refuses more).
+__device__ __forceinline__ Tile tile_at(const LinearArgs &a, uint32_t t)
 {
-    const int64_t full = (int64_t)a.group * tiles_j;
-    const int g = (int)(t / full);
-    const int64_t r = t - g * full;
-    const int left = tiles_i - g * a.group;
-    const int width = left < a.group ? left : a.group;
+    const uint32_t full = (uint32_t)a.group * (uint32_t)a.tiles_j;
+    const uint32_t g = t / full;
+    const uint32_t r = t - g * full;
+    const uint32_t left = (uint32_t)a.tiles_i - g * (uint32_t)a.group;
+    const uint32_t width = left < (uint32_t)a.group ? left : (uint32_t)a.group;
     Tile c;
     c.tj = (int)(r / width);
-    c.ti = g * a.group + (int)(r - (int64_t)c.tj * width);
+    c.ti = (int)(g * (uint32_t)a.group + r - (uint32_t)c.tj * width);
     return c;
 }
 
-// One product's tiles, and this pair's share of their contraction.
+// One product's tiles (this pair's: first, first + nunits, ...), and this pair's
+// share of their contraction.
 struct Product {
-    int tiles_i, tiles_j, kb0, num_kb;
-    int64_t total;
-    __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts)
+    int kb0, num_kb;
+    uint32_t total, first;
+    __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts, uint32_t first_)
+        : kb0(0), num_kb(a.num_kb), total((uint32_t)a.tiles_i * (uint32_t)a.tiles_j), first(first_)
     {
-        tiles_i = (int)((a.I + kTileI - 1) / kTileI);
-        tiles_j = (int)((a.J + a.bt - 1) / a.bt);
-        total = (int64_t)tiles_i * tiles_j;
-        const int all_kb = (int)((a.K + kBK - 1) / kBK);
-        kb0 = (int)((int64_t)all_kb * part / parts);
-        num_kb = (int)((int64_t)all_kb * (part + 1) / parts) - kb0;
+        if (parts > 1)  // 2 or 4
+            share_of(a.num_kb, part, parts, kb0, num_kb);
     }
 };
 
@@ -567,12 +573,12 @@ struct Place {
     volatile int *abort_flag;
     uint32_t tmem, rank, lead;  // position in the CTA pair; cluster rank of its leader
     int part, parts;        // pairs that share a tile's contraction
-    int64_t unit, nunits;
-    int lane, q, group;     // epilogue: TMEM lane quarter, columns [group * BT/4, + BT/4)
+    int lane, q, group;     // epilogue: TMEM lane quarter, which of every four groups of 32 columns
     uint8_t *stage_buf;
     // a role's progress
     int stage;
     uint32_t phase;
+    uint32_t unit, nunits;  // this pair (or cluster) of the grid
     int64_t count;          // k-blocks issued (producer), chunks (MMA issuer, epilogue)
 };
 
@@ -580,13 +586,13 @@ struct Place {
 // a wait gave up.
 template <int BT>
 __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensorMap &map_b, const LinearArgs &a,
-                                        const Product &p, int64_t first, bool elected, Place &at)
+                                        const Product &p, bool elected, Place &at)
 {
     using G = Geo<BT>;
     const uint64_t pol = ptx::policy_evict_normal();
     const uint32_t stage_bytes = 2u * (uint32_t)(kA + a.bt / 2 * kBK * 2);  // both CTAs'
-    for (int64_t t = first; t < p.total; t += at.nunits) {
-        const Tile c = tile_at(a, t, p.tiles_i, p.tiles_j);
+    for (uint32_t t = p.first; t < p.total; t += at.nunits) {
+        const Tile c = tile_at(a, t);
         const int i0 = c.ti * kTileI + (int)at.rank * 128;
         const int j0 = c.tj * a.bt + (int)at.rank * (a.bt / 2);
         for (int kb = 0; kb < p.num_kb; ++kb) {
@@ -618,7 +624,7 @@ __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensor
 
 // The MMA issuer's share of the same.
 template <int BT>
-__device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, int64_t first, bool elected,
+__device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, bool elected,
                                          Place &at, bool *issued_any)
 {
     using G = Geo<BT>;
@@ -628,7 +634,7 @@ __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, 
     const uint32_t lo_a = desc_lo(at.base, a.a_mn ? kMnBox : 16);
     const uint32_t lo_b = desc_lo(at.base + kA, a.b_mn ? kMnBox : 16);
     const uint16_t both = (uint16_t)(3u << at.lead);
-    for (int64_t t = first; t < p.total; t += at.nunits) {
+    for (uint32_t t = p.first; t < p.total; t += at.nunits) {
         int in_chunk = 0;
         for (int kb = 0; kb < p.num_kb; ++kb) {
             const int acc = (int)(at.count & 1);  // chunks issued so far: accumulator count & 1
@@ -670,21 +676,25 @@ __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, 
 
 // An epilogue warp's share of the same.
 template <int EPI, int BT>
-__device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, int64_t first, Place &at)
+__device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Place &at)
 {
-    constexpr int kCols = BT / 4;  // this warp's columns
+    // This warp's columns: every fourth group of 32, so that tiles of fewer tokens
+    // leave no warp two groups while another has none.
+    constexpr int kCols = BT / 4;
     constexpr int kGroups = kCols / kStageCols;
+    constexpr int kStep = 4 * kStageCols;
     const int lane = at.lane;
-    const uint32_t t_lane = at.tmem + ((uint32_t)(at.q * 32) << 16) + (uint32_t)(at.group * kCols);
+    const uint32_t t_lane = at.tmem + ((uint32_t)(at.q * 32) << 16) + (uint32_t)(at.group * kStageCols);
     const uint32_t empty0 = map_to_rank(ptx::smem_addr(&at.sh->tmem_empty[0]), at.lead);
-    float *partial = reinterpret_cast<float *>(at.smem) + at.group * kCols * 128 + at.q * 32 + lane;
+    float *partial = reinterpret_cast<float *>(at.smem) + at.group * kStageCols * 128 + at.q * 32 + lane;
     const Rows aux = aux_of<EPI>(a);
     const bool early = aux.p != nullptr && at.parts == 1;
     const int chunks = (p.num_kb + a.chunk - 1) / a.chunk;
-    for (int64_t t = first; t < p.total; t += at.nunits) {
-        const Tile c = tile_at(a, t, p.tiles_i, p.tiles_j);
+    const auto column = [](int u) { return u / kStageCols * kStep + u % kStageCols; };
+    for (uint32_t t = p.first; t < p.total; t += at.nunits) {
+        const Tile c = tile_at(a, t);
         const int64_t i0 = (int64_t)c.ti * kTileI + (int)at.rank * 128 + at.q * 32;
-        const int64_t j0 = (int64_t)c.tj * a.bt + at.group * kCols;
+        const int64_t j0 = (int64_t)c.tj * a.bt + at.group * kStageCols;
         // the first token that is not this tile's
         const int64_t end = gg_min64(a.J, (int64_t)(c.tj + 1) * a.bt);
         const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
@@ -716,8 +726,10 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, in
             if constexpr (EPI == kEpiGradW) {
 #pragma unroll
                 for (int col = 0; col < kCols; col += 16) {
+                    if (valid_rows(end, j0 + column(col)) <= 0)
+                        continue;
                     float v[16];
-                    from_tmem(col, v);
+                    from_tmem(column(col), v);
 #pragma unroll
                     for (int u = 0; u < 16; ++u)
                         sum[col + u] += v[u];
@@ -726,19 +738,21 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, in
 #pragma unroll 1
                 for (int col = 0; col < kCols; col += 16) {
                     float v[16];
-                    from_tmem(col, v);
+                    from_tmem(column(col), v);
 #pragma unroll
                     for (int u = 0; u < 16; ++u)
-                        partial[(col + u) * 128] = v[u];
+                        partial[(column(col) + u) * 128] = v[u];
                 }
             } else {
 #pragma unroll 1
                 for (int g = 0; g < kGroups; ++g) {
-                    const int64_t jg = j0 + g * kStageCols;
+                    const int64_t jg = j0 + g * kStep;
+                    if (valid_rows(end, jg) <= 0)
+                        break;
                     emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, at.stage_buf,
-                                   [&](int col, float(&v)[16]) { from_tmem(g * kStageCols + col, v); });
+                                   [&](int col, float(&v)[16]) { from_tmem(g * kStep + col, v); });
                     if (early && g + 1 < kGroups)
-                        read_rows(aux, a.I, i0, jg + kStageCols, valid_rows(end, jg + kStageCols), lane, pre);
+                        read_rows(aux, a.I, i0, jg + kStep, valid_rows(end, jg + kStep), lane, pre);
                 }
             }
             // accumulator read: hand it back to the leader's MMA warp
@@ -751,7 +765,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, in
             if (at.parts > 1) {
 #pragma unroll
                 for (int u = 0; u < kCols; ++u)
-                    partial[u * 128] = sum[u];
+                    partial[column(u) * 128] = sum[u];
             } else if (a.out_f32) {
 #pragma unroll
                 for (int col = 0; col < kCols; col += 16) {
@@ -759,12 +773,13 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, in
 #pragma unroll
                     for (int u = 0; u < 16; ++u)
                         v[u] = sum[col + u];
-                    emit16<EPI>(a, i0 + lane, j0 + col, 1, valid16(end, j0 + col), v, 0.0f);
+                    const int64_t jc = j0 + column(col);
+                    emit16<EPI>(a, i0 + lane, jc, 1, valid16(end, jc), v, 0.0f);
                 }
             } else {
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    const int64_t jg = j0 + g * kStageCols;
+                    const int64_t jg = j0 + g * kStep;
                     if (early)
                         read_rows(aux, a.I, i0, jg, valid_rows(end, jg), lane, pre);
                     emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
@@ -787,7 +802,7 @@ template <int EPI, int BT>
 __device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p, Place &at)
 {
     const int lane = at.lane, parts = at.parts;
-    const Tile c = tile_at(a, at.unit, p.tiles_i, p.tiles_j);
+    const Tile c = tile_at(a, at.unit);
     // 16 columns a warp at least: with 32 left for a pair, half the warps finish them
     const int cols = BT / parts >= 64 ? BT / parts / 4 : 16;
     const int col0 = at.part * (BT / parts) + at.group * cols;
@@ -855,25 +870,9 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 
     launch_dependents();
     const int warp = threadIdx.x >> 5;
-    const uint32_t crank = cluster_ctarank();
-    at.lane = threadIdx.x & 31;
-    at.rank = crank & 1u;
-    at.lead = crank & ~1u;
-    at.parts = kTwo ? 1 : (int)cluster_size() / 2;
-    at.part = kTwo ? 0 : (int)crank / 2;
-    at.unit = (int64_t)cluster_id_x();
-    at.nunits = (int64_t)ncluster_x();
-    at.q = warp & 3;
-    at.group = (warp - 2) >> 2;
-    at.stage_buf = at.smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
-    at.stage = 0;
-    at.phase = 0;
-    at.count = 0;
-    const pair::Product p(a, at.part, at.parts);
-    const pair::Product p1(kTwo ? a1 : a, at.part, at.parts);
-    // this pair's first tile of the second product: the walk goes on where the first ended
-    const int64_t first1 = ((at.unit - p.total) % at.nunits + at.nunits) % at.nunits;
-
+    // Set-up first, the rest of the arithmetic under it: all of it is on the way of
+    // every call (with 64-bit divisions ahead of it, the barriers stood after 1300
+    // cycles and the first load went out 2600 cycles later).
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
@@ -887,7 +886,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         sh.abort_flag = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == 0 && at.lane == 0) {
+    if (threadIdx.x == 0) {
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
         if (kTwo) {
@@ -899,8 +898,26 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         tmem_alloc<2>(ptx::smem_addr(&sh.tmem_base), 2 * BT);
         fence_before();
     }
+    const uint32_t crank = cluster_ctarank();
+    at.lane = threadIdx.x & 31;
+    at.rank = crank & 1u;
+    at.lead = crank & ~1u;
+    at.parts = kTwo ? 1 : (int)cluster_size() / 2;
+    at.part = kTwo ? 0 : (int)crank / 2;
+    at.unit = cluster_id_x();
+    at.nunits = ncluster_x();
+    at.q = warp & 3;
+    at.group = (warp - 2) >> 2;
+    at.stage_buf = at.smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
+    at.stage = 0;
+    at.phase = 0;
+    at.count = 0;
+    const pair::Product p(a, at.part, at.parts, at.unit);
+    // the second product's walk goes on where the first ended
+    const uint32_t at1 = at.unit + (at.unit < (uint32_t)a1.skip ? at.nunits : 0u) - (uint32_t)a1.skip;
+    const pair::Product p1(kTwo ? a1 : a, at.part, at.parts, kTwo ? at1 : 0u);
     __syncthreads();
-    cluster_sync();  // the peer's barriers exist before anything signals them
+    cluster_meet();  // the peer's barriers exist before anything signals them
     fence_after();
     at.tmem = sh.tmem_base;
     wait_dependencies();  // what earlier launches write is there from here on
@@ -909,9 +926,9 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     if (warp == 0) {
         // ===================== producer =====================================
         const bool elected = ptx::elect_one_sync();
-        ok = pair::produce<BT>(map_a, map_b, a, p, at.unit, elected, at);
+        ok = pair::produce<BT>(map_a, map_b, a, p, elected, at);
         if (kTwo && ok)
-            ok = pair::produce<BT>(map_a1, map_b1, a1, p1, first1, elected, at);
+            ok = pair::produce<BT>(map_a1, map_b1, a1, p1, elected, at);
         if (!ok) {
             *at.abort_flag = 1;
             report_status(a.status, kStatusTimeout);
@@ -932,9 +949,9 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         const bool elected = ptx::elect_one_sync();
         bool issued_any = false;
         if (at.rank == 0) {
-            ok = pair::multiply<BT>(a, p, at.unit, elected, at, &issued_any);
+            ok = pair::multiply<BT>(a, p, elected, at, &issued_any);
             if (kTwo && ok)
-                ok = pair::multiply<BT>(a1, p1, first1, elected, at, &issued_any);
+                ok = pair::multiply<BT>(a1, p1, elected, at, &issued_any);
         }
         if (!ok) {
             *at.abort_flag = 1;
@@ -949,10 +966,10 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         }
     } else {
         // ===================== epilogue (warps 2-17) ========================
-        ok = pair::finish<EPI, BT>(a, p, at.unit, at);
+        ok = pair::finish<EPI, BT>(a, p, at);
         if constexpr (kTwo) {
             if (ok)
-                ok = pair::finish<EPI1, BT>(a1, p1, first1, at);
+                ok = pair::finish<EPI1, BT>(a1, p1, at);
         }
         if (!ok) {
             *at.abort_flag = 1;
@@ -960,7 +977,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         }
     }
 
-    __syncthreads();
+    __syncwarp();
     if constexpr (!kTwo) {
         if (at.parts > 1) {
             cluster_sync();
@@ -972,8 +989,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 
     // ---- teardown ---------------------------------------------------------------
     fence_before();
-    __syncthreads();
-    cluster_sync();  // the leader's MMAs into the peer's TMEM and smem are done, partials read
+    cluster_meet();  // the leader's MMAs into the peer's TMEM and smem are done, partials read
     if (warp == 1) {
         fence_after();
         tmem_dealloc<2>(at.tmem, 2 * BT);
@@ -1014,17 +1030,6 @@ __global__ void __launch_bounds__(split::kThreads, 2)
 
     launch_dependents();
     const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank();
-    const int parts = (int)cluster_size();
-    const int64_t tile = (int64_t)cluster_id_x();
-    const int tiles_i = (int)((a.I + 127) / 128);
-    const int tj = (int)(tile / tiles_i);
-    const int ti = (int)(tile - (int64_t)tj * tiles_i);
-    const int num_kb = (int)((a.K + kBK - 1) / kBK);
-    const int kb0 = (int)((int64_t)num_kb * rank / parts);
-    const int kb1 = (int)((int64_t)num_kb * (rank + 1) / parts);
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
@@ -1038,7 +1043,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         sh.abort_flag = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == 0 && lane == 0) {
+    if (threadIdx.x == 0) {
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
     }
@@ -1046,6 +1051,15 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         tmem_alloc<1>(ptx::smem_addr(&sh.tmem_base), G::kTmemCols);
         fence_before();
     }
+    const int lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int parts = (int)cluster_size();
+    const uint32_t tile = cluster_id_x();
+    const int tj = (int)(tile / (uint32_t)a.tiles_i);
+    const int ti = (int)(tile - (uint32_t)tj * (uint32_t)a.tiles_i);
+    int kb0, kb1;
+    share_of(a.num_kb, rank, parts, kb0, kb1);
+    kb1 += kb0;
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem_base;
@@ -1257,7 +1271,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         }
     }
 
-    __syncthreads();
+    __syncwarp();
     if (parts > 1) {
         // the cluster's partial tiles, added in rank order; CTA `rank` takes
         // columns rank, rank + parts, ...
@@ -1289,7 +1303,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
             }
         }
         __syncwarp();
-        cluster_sync();  // no CTA leaves while its partial tile may still be read
+        cluster_meet();  // no CTA leaves while its partial tile may still be read
     }
     fence_before();
     __syncthreads();
@@ -1530,11 +1544,18 @@ cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, const LinearA
             *why = "encoding the operands' tensor maps";
             return cudaErrorInvalidValue;
         }
-        const int64_t tiles_i = (x.I + pair::kTileI - 1) / pair::kTileI;
+        const int64_t tiles_i = (x.I + pair::kTileI - 1) / pair::kTileI, tiles_j = (x.J + x.bt - 1) / x.bt;
         // feature tiles in equal groups of at most 8: 76 pairs cover about 8 x 9 tiles
         const int64_t groups = (tiles_i + 7) / 8;
         x.group = (int)((tiles_i + groups - 1) / groups);
-        tiles += tiles_i * ((x.J + x.bt - 1) / x.bt);
+        x.tiles_i = (int)tiles_i;
+        x.tiles_j = (int)tiles_j;
+        x.num_kb = (int)((x.K + kBK - 1) / kBK);
+        tiles += tiles_i * tiles_j;
+    }
+    if (tiles >= 1ll << 31) {
+        *why = "more than 2^31 tiles";
+        return cudaErrorInvalidValue;
     }
     if (!args1) {
         maps[2] = maps[0];
@@ -1543,12 +1564,13 @@ cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, const LinearA
     const int resident = resident_by_dev[dev] > 0 ? resident_by_dev[dev] : kSMs / 2;
     // split tiles: one cluster each; whole ones: the pairs that fit walk them
     const int64_t clusters = parts > 1 ? tiles : gg_min64(resident, tiles);
+    a[1].skip = (int)((int64_t)a[0].tiles_i * a[0].tiles_j % clusters);
     ClusterLaunch l(2 * parts, 2 * parts * clusters, pair::kThreads, G::kSmemBytes, s);
     return cudaLaunchKernelEx(&l.cfg, pair_kernel<EPI, EPI1, BT>, maps[0], maps[1], a[0], maps[2], maps[3], a[1]);
 }
 
 template <int EPI, int BT>
-cudaError_t launch_split(const LinearArgs &a, int parts, cudaStream_t s, const char **why)
+cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, const char **why)
 {
     using G = split::Geo<BT>;
     static std::once_flag once[kMaxDevices];
@@ -1559,12 +1581,16 @@ cudaError_t launch_split(const LinearArgs &a, int parts, cudaStream_t s, const c
         return e;
     }
     CUtensorMap map_a, map_b;
+    LinearArgs a = args;
     if (!operand_map(&map_a, a, a.a, a.I, a.lda, a.a_mn, 128) ||
         !operand_map(&map_b, a, a.b, a.J, a.ldb, a.b_mn, BT)) {
         *why = "encoding the operands' tensor maps";
         return cudaErrorInvalidValue;
     }
-    const int64_t tiles = ((a.I + 127) / 128) * ((a.J + BT - 1) / BT);
+    a.tiles_i = (int)((a.I + 127) / 128);
+    a.tiles_j = (int)((a.J + BT - 1) / BT);
+    a.num_kb = (int)((a.K + kBK - 1) / kBK);
+    const int64_t tiles = (int64_t)a.tiles_i * a.tiles_j;
     ClusterLaunch l(parts, tiles * parts, split::kThreads, G::kSmemBytes, s);
     return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
         ptx::mbar_init(ptx::smem_addr(&arrived[tid]), 1);
     ptx::fence_barrier_init();
     __syncthreads();
-    tc::cluster_sync();  // every CTA's barriers are there
+    tc::cluster_meet();  // every CTA's barriers are there
 
     // The next row: its slice, how many vectors this lane has in it (none where the
     // token is masked), its ragged ends and, in one thread of the cluster, its
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
     }
     wait_groups(0);
     __syncwarp();
-    tc::cluster_sync();  // no CTA leaves while a message may still be on its way to it
+    tc::cluster_meet();  // no CTA leaves while a message may still be on its way to it
 }
 
 // Rows beyond what a cluster's shared memory holds: the second pass reads memory
