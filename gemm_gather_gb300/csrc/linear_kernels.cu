@@ -557,8 +557,10 @@ __device__ __forceinline__ Tile tile_at(const LinearArgs &a, uint32_t t)
 struct Product {
     int kb0, num_kb;
     uint32_t total, first;
+    Tile tile;  // the first
     __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts, uint32_t first_)
-        : kb0(0), num_kb(a.num_kb), total((uint32_t)a.tiles_i * (uint32_t)a.tiles_j), first(first_)
+        : kb0(0), num_kb(a.num_kb), total((uint32_t)a.tiles_i * (uint32_t)a.tiles_j), first(first_),
+          tile(first_ < total ? tile_at(a, first_) : Tile{0, 0})
     {
         if (parts > 1)  // 2 or 4
             share_of(a.num_kb, part, parts, kb0, num_kb);
@@ -580,52 +582,54 @@ struct Place {
     uint32_t phase;
     uint32_t unit, nunits;  // this pair (or cluster) of the grid
     int64_t count;          // k-blocks issued (producer), chunks (MMA issuer, epilogue)
+    int64_t stall_at;       // the k-block that is not loaded (a test's), or -1
 };
 
-// The producer's loads of a product's tiles first, first + nunits, ...; false when
-// a wait gave up.
+// The producer's loads of a product's tiles; false when a wait gave up.  One
+// thread's loop, as the MMA issuer's is: with the warp's votes and barriers in it a
+// k-block took 570 cycles, more than the MMAs of most tiles, and filling the ring
+// took longer than the first loads.
 template <int BT>
 __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensorMap &map_b, const LinearArgs &a,
-                                        const Product &p, bool elected, Place &at)
+                                        const Product &p, Place &at)
 {
     using G = Geo<BT>;
     const uint64_t pol = ptx::policy_evict_normal();
     const uint32_t stage_bytes = 2u * (uint32_t)(kA + a.bt / 2 * kBK * 2);  // both CTAs'
-    for (uint32_t t = p.first; t < p.total; t += at.nunits) {
-        const Tile c = tile_at(a, t);
+    const uint32_t empty0 = ptx::smem_addr(at.sh->empty), full0 = ptx::smem_addr(at.sh->full);
+    const uint32_t bar0 = map_to_rank(full0, at.lead);  // both CTAs' loads
+    Tile c = p.tile;
+    for (uint32_t t = p.first; t < p.total;) {
         const int i0 = c.ti * kTileI + (int)at.rank * 128;
         const int j0 = c.tj * a.bt + (int)at.rank * (a.bt / 2);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-            const bool got = role_wait(ptx::smem_addr(&at.sh->empty[at.stage]), at.phase ^ 1u,
-                                       a.wait_limit_ns, at.abort_flag);
-            if (!__all_sync(0xffffffffu, got))
+        int k0 = p.kb0 * kBK;
+        for (int kb = 0; kb < p.num_kb; ++kb, k0 += kBK) {
+            const uint32_t bar_at = (uint32_t)at.stage * 8;
+            if (!role_wait(empty0 + bar_at, at.phase ^ 1u, a.wait_limit_ns, at.abort_flag))
                 return false;
-            const bool stall = a.inject_stall && at.unit == 0 && at.part == 0 && at.count == 0;
-            if (elected && !stall) {  // test hook: the first stage is never armed
-                const uint32_t local_full = ptx::smem_addr(&at.sh->full[at.stage]);
-                const uint32_t bar = map_to_rank(local_full, at.lead);  // both CTAs' loads
+            if (at.count != at.stall_at) {  // test hook: the first stage is never armed
                 if (at.rank == 0)
-                    ptx::mbar_arrive_expect_tx(local_full, stage_bytes);
+                    ptx::mbar_arrive_expect_tx(full0 + bar_at, stage_bytes);
                 const uint32_t sa = at.base + at.stage * G::kStage;
-                const int k0 = (p.kb0 + kb) * kBK;
-                load_operand<2>(sa, &map_a, a.a_mn, 128, i0, k0, bar, pol);
-                load_operand<2>(sa + kA, &map_b, a.b_mn, a.bt / 2, j0, k0, bar, pol);
+                load_operand<2>(sa, &map_a, a.a_mn, 128, i0, k0, bar0 + bar_at, pol);
+                load_operand<2>(sa + kA, &map_b, a.b_mn, a.bt / 2, j0, k0, bar0 + bar_at, pol);
             }
-            __syncwarp();
             ++at.count;
             if (++at.stage == G::kStages) {
                 at.stage = 0;
                 at.phase ^= 1u;
             }
         }
+        t += at.nunits;
+        if (t < p.total)
+            c = tile_at(a, t);
     }
     return true;
 }
 
 // The MMA issuer's share of the same.
 template <int BT>
-__device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, bool elected,
-                                         Place &at, bool *issued_any)
+__device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, Place &at, bool *issued_any)
 {
     using G = Geo<BT>;
     const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 256, a.bt);
@@ -633,35 +637,29 @@ __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, 
     const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
     const uint32_t lo_a = desc_lo(at.base, a.a_mn ? kMnBox : 16);
     const uint32_t lo_b = desc_lo(at.base + kA, a.b_mn ? kMnBox : 16);
+    const uint32_t empty0 = ptx::smem_addr(at.sh->empty), full0 = ptx::smem_addr(at.sh->full);
     const uint16_t both = (uint16_t)(3u << at.lead);
     for (uint32_t t = p.first; t < p.total; t += at.nunits) {
         int in_chunk = 0;
         for (int kb = 0; kb < p.num_kb; ++kb) {
             const int acc = (int)(at.count & 1);  // chunks issued so far: accumulator count & 1
-            bool got = true;
-            if (in_chunk == 0)
-                got = role_wait(ptx::smem_addr(&at.sh->tmem_empty[acc]),
-                                (uint32_t)((at.count >> 1) & 1) ^ 1u, a.wait_limit_ns, at.abort_flag);
-            got = got && role_wait(ptx::smem_addr(&at.sh->full[at.stage]), at.phase, a.wait_limit_ns,
-                                   at.abort_flag);
-            if (!__all_sync(0xffffffffu, got))
+            if (in_chunk == 0 &&
+                !role_wait(ptx::smem_addr(&at.sh->tmem_empty[acc]), (uint32_t)((at.count >> 1) & 1) ^ 1u,
+                           a.wait_limit_ns, at.abort_flag))
+                return false;
+            if (!role_wait(full0 + (uint32_t)at.stage * 8, at.phase, a.wait_limit_ns, at.abort_flag))
                 return false;
             fence_after();
-            const bool last = in_chunk + 1 == a.chunk || kb + 1 == p.num_kb;
-            if (elected) {
-                const uint32_t stage_at = (uint32_t)(at.stage * G::kStage) >> 4;
+            const uint32_t stage_at = (uint32_t)(at.stage * G::kStage) >> 4;
 #pragma unroll
-                for (int k = 0; k < kBK / UK; ++k)
-                    mma_f16<2>(at.tmem + (uint32_t)(acc * BT), lo_a + stage_at + k * step_a,
-                               lo_b + stage_at + k * step_b, idesc, (uint32_t)(in_chunk | k));
-                mma_commit_to(ptx::smem_addr(&at.sh->empty[at.stage]), both);
-                if (last)
-                    mma_commit_to(ptx::smem_addr(&at.sh->tmem_full[acc]), both);
-            }
-            __syncwarp();
+            for (int k = 0; k < kBK / UK; ++k)
+                mma_f16<2>(at.tmem + (uint32_t)(acc * BT), lo_a + stage_at + k * step_a,
+                           lo_b + stage_at + k * step_b, idesc, (uint32_t)(in_chunk | k));
+            mma_commit_to(empty0 + (uint32_t)at.stage * 8, both);
             *issued_any = true;
             ++in_chunk;
-            if (last) {
+            if (in_chunk == a.chunk || kb + 1 == p.num_kb) {
+                mma_commit_to(ptx::smem_addr(&at.sh->tmem_full[acc]), both);
                 ++at.count;
                 in_chunk = 0;
             }
@@ -912,6 +910,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     at.stage = 0;
     at.phase = 0;
     at.count = 0;
+    at.stall_at = a.inject_stall && at.unit == 0 && at.part == 0 ? 0 : -1;
     const pair::Product p(a, at.part, at.parts, at.unit);
     // the second product's walk goes on where the first ended
     const uint32_t at1 = at.unit + (at.unit < (uint32_t)a1.skip ? at.nunits : 0u) - (uint32_t)a1.skip;
@@ -924,45 +923,43 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 
     bool ok = true;
     if (warp == 0) {
-        // ===================== producer =====================================
-        const bool elected = ptx::elect_one_sync();
-        ok = pair::produce<BT>(map_a, map_b, a, p, elected, at);
-        if (kTwo && ok)
-            ok = pair::produce<BT>(map_a1, map_b1, a1, p1, elected, at);
-        if (!ok) {
-            *at.abort_flag = 1;
-            report_status(a.status, kStatusTimeout);
-        }
-        // drain: every load this warp issued has landed before the CTA may exit
-        if (at.rank == 0) {
-            const int64_t pending = at.count < G::kStages ? at.count : G::kStages;
-            for (int64_t d = 0; d < pending; ++d) {
-                const int64_t idx = at.count - 1 - d;
-                ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
-                               (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
+        // ===================== producer (one thread) ========================
+        if (ptx::elect_one_sync()) {
+            ok = pair::produce<BT>(map_a, map_b, a, p, at);
+            if (kTwo && ok)
+                ok = pair::produce<BT>(map_a1, map_b1, a1, p1, at);
+            if (!ok) {
+                *at.abort_flag = 1;
+                report_status(a.status, kStatusTimeout);
             }
-        } else if (!ok && at.count > 0) {
-            sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
+            // drain: every load this thread issued has landed before the CTA may exit
+            if (at.rank == 0) {
+                const int64_t pending = at.count < G::kStages ? at.count : G::kStages;
+                for (int64_t d = 0; d < pending; ++d) {
+                    const int64_t idx = at.count - 1 - d;
+                    ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
+                                   (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
+                }
+            } else if (!ok && at.count > 0) {
+                sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
+            }
         }
     } else if (warp == 1) {
-        // ===================== MMA issuer (leader CTA) ======================
-        const bool elected = ptx::elect_one_sync();
-        bool issued_any = false;
-        if (at.rank == 0) {
-            ok = pair::multiply<BT>(a, p, elected, at, &issued_any);
+        // ===================== MMA issuer (one thread of the leader CTA) ====
+        if (at.rank == 0 && ptx::elect_one_sync()) {
+            bool issued_any = false;
+            ok = pair::multiply<BT>(a, p, at, &issued_any);
             if (kTwo && ok)
-                ok = pair::multiply<BT>(a1, p1, elected, at, &issued_any);
-        }
-        if (!ok) {
-            *at.abort_flag = 1;
-            report_status(a.status, kStatusTimeout);
-        }
-        // drain: all MMAs of this thread have completed before TMEM is freed
-        if (issued_any) {
-            if (elected)
+                ok = pair::multiply<BT>(a1, p1, at, &issued_any);
+            if (!ok) {
+                *at.abort_flag = 1;
+                report_status(a.status, kStatusTimeout);
+            }
+            // drain: all its MMAs have completed before TMEM is freed
+            if (issued_any) {
                 mma_commit_local<2>(ptx::smem_addr(&sh.mma_done));
-            __syncwarp();
-            ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
+                ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
+            }
         }
     } else {
         // ===================== epilogue (warps 2-17) ========================
@@ -1072,100 +1069,92 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     bool ok = true;
 
     if (warp == 0) {
-        // ===================== producer =====================================
-        const uint64_t pol = ptx::policy_evict_normal();
-        const bool elected = ptx::elect_one_sync();
-        int stage = 0;
-        uint32_t phase = 0;
-        int issued = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const bool got = role_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1u,
-                                       a.wait_limit_ns, abort_flag);
-            if (!__all_sync(0xffffffffu, got)) {
-                ok = false;
-                break;
+        // ===================== producer (one thread) ========================
+        if (ptx::elect_one_sync()) {
+            const uint64_t pol = ptx::policy_evict_normal();
+            const uint32_t empty0 = ptx::smem_addr(sh.empty), full0 = ptx::smem_addr(sh.full);
+            const bool stall = a.inject_stall && tile == 0 && rank == 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const uint32_t bar = full0 + (uint32_t)stage * 8;
+                if (!role_wait(empty0 + (uint32_t)stage * 8, phase ^ 1u, a.wait_limit_ns, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (!stall || issued > 0) {  // test hook: the first stage is never armed
+                    ptx::mbar_arrive_expect_tx(bar, G::kStage);
+                    const uint32_t sa = base + stage * G::kStage;
+                    load_operand<1>(sa, &map_a, a.a_mn, 128, ti * 128, kb * kBK, bar, pol);
+                    load_operand<1>(sa + split::kA, &map_b, a.b_mn, BT, tj * BT, kb * kBK, bar, pol);
+                }
+                ++issued;
+                if (++stage == G::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            const bool stall = a.inject_stall && tile == 0 && rank == 0 && issued == 0;
-            if (elected && !stall) {  // test hook: the first stage is never armed
-                const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
-                ptx::mbar_arrive_expect_tx(bar, G::kStage);
-                const uint32_t sa = base + stage * G::kStage;
-                load_operand<1>(sa, &map_a, a.a_mn, 128, ti * 128, kb * kBK, bar, pol);
-                load_operand<1>(sa + split::kA, &map_b, a.b_mn, BT, tj * BT, kb * kBK, bar, pol);
+            if (!ok) {
+                *abort_flag = 1;
+                report_status(a.status, kStatusTimeout);
             }
-            __syncwarp();
-            ++issued;
-            if (++stage == G::kStages) {
-                stage = 0;
-                phase ^= 1u;
+            const int pending = issued < G::kStages ? issued : G::kStages;
+            for (int d = 0; d < pending; ++d) {
+                const int idx = issued - 1 - d;
+                ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
+                               (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
             }
-        }
-        if (!ok) {
-            *abort_flag = 1;
-            report_status(a.status, kStatusTimeout);
-        }
-        const int pending = issued < G::kStages ? issued : G::kStages;
-        for (int d = 0; d < pending; ++d) {
-            const int idx = issued - 1 - d;
-            ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
-                           (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
         }
     } else if (warp == 1) {
-        // ===================== MMA issuer ===================================
-        const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 128, BT);
-        const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;
-        const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
-        const uint32_t lo_a = desc_lo(base, a.a_mn ? kMnBox : 16);
-        const uint32_t lo_b = desc_lo(base + split::kA, a.b_mn ? kMnBox : 16);
-        const bool elected = ptx::elect_one_sync();
-        int stage = 0;
-        uint32_t phase = 0;
-        int nchunk = 0, in_chunk = 0;
-        bool issued_any = false;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const int acc = nchunk & 1;
-            bool got = true;
-            if (in_chunk == 0)
-                got = role_wait(ptx::smem_addr(&sh.tmem_empty[acc]), (uint32_t)((nchunk >> 1) & 1) ^ 1u,
-                                a.wait_limit_ns, abort_flag);
-            got = got && role_wait(ptx::smem_addr(&sh.full[stage]), phase, a.wait_limit_ns, abort_flag);
-            if (!__all_sync(0xffffffffu, got)) {
-                ok = false;
-                break;
-            }
-            fence_after();
-            const bool last = in_chunk + 1 == a.chunk || kb + 1 == kb1;
-            if (elected) {
+        // ===================== MMA issuer (one thread) ======================
+        if (ptx::elect_one_sync()) {
+            const uint32_t idesc = instr_desc(a.is_bf16, a.a_mn, a.b_mn, 128, BT);
+            const uint32_t step_a = (a.a_mn ? UK * 128 : UK * 2) >> 4;
+            const uint32_t step_b = (a.b_mn ? UK * 128 : UK * 2) >> 4;
+            const uint32_t lo_a = desc_lo(base, a.a_mn ? kMnBox : 16);
+            const uint32_t lo_b = desc_lo(base + split::kA, a.b_mn ? kMnBox : 16);
+            const uint32_t empty0 = ptx::smem_addr(sh.empty), full0 = ptx::smem_addr(sh.full);
+            int stage = 0;
+            uint32_t phase = 0;
+            int nchunk = 0, in_chunk = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int acc = nchunk & 1;
+                bool got = true;
+                if (in_chunk == 0)
+                    got = role_wait(ptx::smem_addr(&sh.tmem_empty[acc]), (uint32_t)((nchunk >> 1) & 1) ^ 1u,
+                                    a.wait_limit_ns, abort_flag);
+                got = got && role_wait(full0 + (uint32_t)stage * 8, phase, a.wait_limit_ns, abort_flag);
+                if (!got) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
                 const uint32_t at = (uint32_t)(stage * G::kStage) >> 4;
 #pragma unroll
                 for (int k = 0; k < kBK / UK; ++k)
                     mma_f16<1>(tmem + (uint32_t)(acc * BT), lo_a + at + k * step_a,
                                lo_b + at + k * step_b, idesc, (uint32_t)(in_chunk | k));
-                mma_commit_local<1>(ptx::smem_addr(&sh.empty[stage]));
-                if (last)
+                mma_commit_local<1>(empty0 + (uint32_t)stage * 8);
+                ++in_chunk;
+                if (in_chunk == a.chunk || kb + 1 == kb1) {
                     mma_commit_local<1>(ptx::smem_addr(&sh.tmem_full[acc]));
+                    ++nchunk;
+                    in_chunk = 0;
+                }
+                if (++stage == G::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            __syncwarp();
-            issued_any = true;
-            ++in_chunk;
-            if (last) {
-                ++nchunk;
-                in_chunk = 0;
+            if (!ok) {
+                *abort_flag = 1;
+                report_status(a.status, kStatusTimeout);
             }
-            if (++stage == G::kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-        if (!ok) {
-            *abort_flag = 1;
-            report_status(a.status, kStatusTimeout);
-        }
-        if (issued_any) {
-            if (elected)
+            if (nchunk + in_chunk > 0) {
                 mma_commit_local<1>(ptx::smem_addr(&sh.mma_done));
-            __syncwarp();
-            ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
+                ptx::mbar_wait(ptx::smem_addr(&sh.mma_done), 0, kDrainLimitNs);
+            }
         }
     } else {
         // ===================== epilogue (warps 2-5) =========================
