@@ -515,7 +515,8 @@ namespace pair {
 constexpr int kTileI = 256;
 constexpr int kA = 128 * kBK * 2;        // 16 KB: this CTA's 128 features of one k-block
 constexpr int kEpiWarps = 16;            // four per TMEM lane quarter, a quarter of the columns each
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kProducer2 = 2 + kEpiWarps;  // the second producer's warp
+constexpr int kThreads = 32 * (kProducer2 + 1);
 template <int BT>
 struct Geo {
     static constexpr int kB = BT / 2 * kBK * 2;  // this CTA's half of the tokens
@@ -526,7 +527,7 @@ struct Geo {
     static constexpr int kOffStage = kRing;
     static constexpr int kOffShared = kOffStage + kEpiWarps * kWarpStage;
     static constexpr int kSmemBytes = kOffShared + (int)sizeof(Shared) + 1024;
-    static_assert(kSmemBytes <= 232448 && kStages <= kMaxStages && kPartial <= kRing,
+    static_assert(kSmemBytes <= 232448 && kStages <= kMaxStages && kStages % 2 == 0 && kPartial <= kRing,
                   "shared memory of a CTA");
 };
 
@@ -581,14 +582,17 @@ struct Place {
     int stage;
     uint32_t phase;
     uint32_t unit, nunits;  // this pair (or cluster) of the grid
-    int64_t count;          // k-blocks issued (producer), chunks (MMA issuer, epilogue)
+    int64_t count;          // k-blocks (producers), chunks (MMA issuer, epilogue)
+    int half;               // which producer
+    int64_t issued;         // the k-blocks it has loaded
     int64_t stall_at;       // the k-block that is not loaded (a test's), or -1
 };
 
-// The producer's loads of a product's tiles; false when a wait gave up.  One
-// thread's loop, as the MMA issuer's is: with the warp's votes and barriers in it a
-// k-block took 570 cycles, more than the MMAs of most tiles, and filling the ring
-// took longer than the first loads.
+// Producer `half`'s loads of a product's tiles, every second k-block; false when a
+// wait gave up.  A k-block's wait, expectation and two loads take a thread 450
+// cycles whatever their size (570 with a warp's votes around them), as long as the
+// MMAs of a 256 x 224 tile and twice those of smaller ones; so two threads share
+// them, of warps of their own.
 template <int BT>
 __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensorMap &map_b, const LinearArgs &a,
                                         const Product &p, Place &at)
@@ -602,24 +606,26 @@ __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensor
     for (uint32_t t = p.first; t < p.total;) {
         const int i0 = c.ti * kTileI + (int)at.rank * 128;
         const int j0 = c.tj * a.bt + (int)at.rank * (a.bt / 2);
-        int k0 = p.kb0 * kBK;
-        for (int kb = 0; kb < p.num_kb; ++kb, k0 += kBK) {
+        const int skip = (int)(at.count + at.half) & 1;  // the other producer's
+        int k0 = (p.kb0 + skip) * kBK;
+        for (int kb = skip; kb < p.num_kb; kb += 2, k0 += 2 * kBK) {
             const uint32_t bar_at = (uint32_t)at.stage * 8;
             if (!role_wait(empty0 + bar_at, at.phase ^ 1u, a.wait_limit_ns, at.abort_flag))
                 return false;
-            if (at.count != at.stall_at) {  // test hook: the first stage is never armed
+            if (at.count + kb != at.stall_at) {  // test hook: the first stage is never armed
                 if (at.rank == 0)
-                    ptx::mbar_arrive_expect_tx(full0 + bar_at, stage_bytes);
+                    mbar_expect(full0 + bar_at, stage_bytes);
                 const uint32_t sa = at.base + at.stage * G::kStage;
                 load_operand<2>(sa, &map_a, a.a_mn, 128, i0, k0, bar0 + bar_at, pol);
                 load_operand<2>(sa + kA, &map_b, a.b_mn, a.bt / 2, j0, k0, bar0 + bar_at, pol);
             }
-            ++at.count;
-            if (++at.stage == G::kStages) {
-                at.stage = 0;
+            ++at.issued;
+            if ((at.stage += 2) >= G::kStages) {
+                at.stage -= G::kStages;
                 at.phase ^= 1u;
             }
         }
+        at.count += p.num_kb;
         t += at.nunits;
         if (t < p.total)
             c = tile_at(a, t);
@@ -906,10 +912,12 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     at.nunits = ncluster_x();
     at.q = warp & 3;
     at.group = (warp - 2) >> 2;
-    at.stage_buf = at.smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;
-    at.stage = 0;
+    at.stage_buf = at.smem + G::kOffStage + (warp >= 2 ? warp - 2 : 0) * kWarpStage;  // of an epilogue warp
+    at.half = warp == pair::kProducer2 ? 1 : 0;
+    at.stage = at.half;
     at.phase = 0;
     at.count = 0;
+    at.issued = 0;
     at.stall_at = a.inject_stall && at.unit == 0 && at.part == 0 ? 0 : -1;
     const pair::Product p(a, at.part, at.parts, at.unit);
     // the second product's walk goes on where the first ended
@@ -922,8 +930,8 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     wait_dependencies();  // what earlier launches write is there from here on
 
     bool ok = true;
-    if (warp == 0) {
-        // ===================== producer (one thread) ========================
+    if (warp == 0 || warp == pair::kProducer2) {
+        // ===================== producers (a thread each) ====================
         if (ptx::elect_one_sync()) {
             ok = pair::produce<BT>(map_a, map_b, a, p, at);
             if (kTwo && ok)
@@ -934,13 +942,12 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             }
             // drain: every load this thread issued has landed before the CTA may exit
             if (at.rank == 0) {
-                const int64_t pending = at.count < G::kStages ? at.count : G::kStages;
-                for (int64_t d = 0; d < pending; ++d) {
-                    const int64_t idx = at.count - 1 - d;
+                for (int64_t d = 0; d < G::kStages / 2 && d < at.issued; ++d) {
+                    const int64_t idx = at.half + 2 * (at.issued - 1 - d);
                     ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
                                    (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
                 }
-            } else if (!ok && at.count > 0) {
+            } else if (!ok && at.issued > 0) {
                 sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
             }
         }
@@ -978,7 +985,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     if constexpr (!kTwo) {
         if (at.parts > 1) {
             cluster_sync();
-            if (warp >= 2 && ok)
+            if (warp >= 2 && warp < pair::kProducer2 && ok)
                 pair::join_parts<EPI, BT>(a, p, at);
             __syncwarp();
         }
@@ -995,19 +1002,20 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 
 // ---- split kernel: 128 features x BT tokens per cluster ------------------------------
 namespace split {
-constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
+constexpr int kProducer2 = 6;   // warps: producer, MMA, 4 epilogue, second producer
+constexpr int kThreads = 224;
 constexpr int kA = 128 * kBK * 2;
 template <int BT>
 struct Geo {
     static constexpr int kB = BT * kBK * 2;
     static constexpr int kStage = kA + kB;
-    // about 100 KB of ring, so that two CTAs share an SM
-    static constexpr int kStages = BT == 16 ? 6 : BT == 32 ? 5 : 4;
+    // about 100 KB of ring, so that two CTAs share an SM; even: a producer has its own stages
+    static constexpr int kStages = BT == 16 ? 6 : 4;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kPartial = 128 * BT * 4;  // float32 partial tile, over the spent ring
     static constexpr int kTmemCols = 2 * BT;       // two accumulators (a power of two >= 32)
     static constexpr int kSmemBytes = kRing + (int)sizeof(Shared) + 1024;
-    static_assert(kPartial <= kRing && kStages <= kMaxStages && 2 * (kSmemBytes + 1024) <= 233472,
+    static_assert(kPartial <= kRing && kStages <= kMaxStages && kStages % 2 == 0 && 2 * (kSmemBytes + 1024) <= 233472,
                   "shared memory of a CTA");
 };
 }  // namespace split
@@ -1068,30 +1076,31 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     const float bias = EPI == kEpiForward && warp >= 2 ? load_bias(a, i) : 0.0f;
     bool ok = true;
 
-    if (warp == 0) {
-        // ===================== producer (one thread) ========================
+    if (warp == 0 || warp == split::kProducer2) {
+        // ===================== producers (a thread each, see pair) ==========
         if (ptx::elect_one_sync()) {
             const uint64_t pol = ptx::policy_evict_normal();
             const uint32_t empty0 = ptx::smem_addr(sh.empty), full0 = ptx::smem_addr(sh.full);
-            const bool stall = a.inject_stall && tile == 0 && rank == 0;
-            int stage = 0;
+            const int half = warp == 0 ? 0 : 1;
+            const bool stall = a.inject_stall && tile == 0 && rank == 0 && half == 0;
+            int stage = half;
             uint32_t phase = 0;
             int issued = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            for (int kb = kb0 + half; kb < kb1; kb += 2) {
                 const uint32_t bar = full0 + (uint32_t)stage * 8;
                 if (!role_wait(empty0 + (uint32_t)stage * 8, phase ^ 1u, a.wait_limit_ns, abort_flag)) {
                     ok = false;
                     break;
                 }
                 if (!stall || issued > 0) {  // test hook: the first stage is never armed
-                    ptx::mbar_arrive_expect_tx(bar, G::kStage);
+                    mbar_expect(bar, G::kStage);
                     const uint32_t sa = base + stage * G::kStage;
                     load_operand<1>(sa, &map_a, a.a_mn, 128, ti * 128, kb * kBK, bar, pol);
                     load_operand<1>(sa + split::kA, &map_b, a.b_mn, BT, tj * BT, kb * kBK, bar, pol);
                 }
                 ++issued;
-                if (++stage == G::kStages) {
-                    stage = 0;
+                if ((stage += 2) >= G::kStages) {
+                    stage -= G::kStages;
                     phase ^= 1u;
                 }
             }
@@ -1099,9 +1108,8 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                 *abort_flag = 1;
                 report_status(a.status, kStatusTimeout);
             }
-            const int pending = issued < G::kStages ? issued : G::kStages;
-            for (int d = 0; d < pending; ++d) {
-                const int idx = issued - 1 - d;
+            for (int d = 0; d < G::kStages / 2 && d < issued; ++d) {
+                const int idx = half + 2 * (issued - 1 - d);
                 ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
                                (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
             }
@@ -1265,7 +1273,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         // the cluster's partial tiles, added in rank order; CTA `rank` takes
         // columns rank, rank + parts, ...
         cluster_sync();
-        if (warp >= 2 && ok) {
+        if (warp >= 2 && warp < split::kProducer2 && ok) {
             const uint32_t mine = base + (uint32_t)(q * 32 + lane) * 4;
             const int64_t left = a.J - jt;  // valid columns of the tile
             const int cols = left < BT ? (int)left : BT;

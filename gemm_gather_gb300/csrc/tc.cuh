@@ -96,10 +96,12 @@ __device__ __forceinline__ void cluster_meet()
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrive on an mbarrier given by its shared::cluster address (any CTA of the cluster).
+// Arrive on an mbarrier given by its shared::cluster address (any CTA of the cluster),
+// after reads that are complete; nothing is published (a release would wait 1400
+// cycles for an epilogue's stores).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                  : "memory");
 }
 
@@ -243,14 +245,23 @@ __device__ __forceinline__ void wait_dependencies()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Expect bytes on a barrier of this CTA and arrive, ordering nothing before it.
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
 // ---- bounded waits -----------------------------------------------------------------
 // Wait for a barrier's phase; gives up at the wall-clock limit, or as soon as
 // another role of the CTA raised the abort flag.
 __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           volatile int *abort_flag)
 {
-    if (ptx::mbar_try_wait(bar, parity))
-        return true;
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)  // a read of the clock takes as long as a k-block
+        if (ptx::mbar_try_wait(bar, parity))
+            return true;
     const uint64_t t0 = ptx::globaltimer();
     for (;;) {
 #pragma unroll 1
