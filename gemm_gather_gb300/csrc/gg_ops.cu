@@ -167,7 +167,7 @@ gg_status prepare_linear(const void *X, int64_t ldx, const void *W, int64_t ldw,
     l.zout = const_cast<void *>(z);
     l.ldz = ldz;
     *a = l;
-    *plan = gg::plan_linear(gg::kEpiForward, l.I, l.J, l.K, path);
+    *plan = gg::plan_linear(gg::kEpiForward, l, path);
     return op_ok();
 }
 
@@ -287,9 +287,9 @@ gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t 
     r.sum.out = const_cast<void *>(dbias);
     r.sum.out_f32 = grad_dtype == GG_F32;
     r.sum.accumulate = accumulate != 0;
-    r.plan_dx = r.run_dx ? gg::plan_linear(gg::kEpiGradIn, r.dx.I, r.dx.J, r.dx.K, path)
+    r.plan_dx = r.run_dx ? gg::plan_linear(gg::kEpiGradIn, r.dx, path)
                          : gg::LinearPlan{};
-    r.plan_dw = r.run_dw ? gg::plan_linear(gg::kEpiGradW, r.dw.I, r.dw.J, r.dw.K, path)
+    r.plan_dw = r.run_dw ? gg::plan_linear(gg::kEpiGradW, r.dw, path)
                          : gg::LinearPlan{};
     r.both = r.run_dx && r.run_dw &&
              gg::plan_both(r.dx, r.dw, r.plan_dx, r.plan_dw, path, &r.bt_dx, &r.bt_dw);

@@ -58,7 +58,7 @@ struct LinearPlan {
     int split;   // CTAs (split kernel) or CTA pairs that share one tile's contraction
     double ns;   // the estimate it was chosen by
 };
-LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path);
+LinearPlan plan_linear(int epi, const LinearArgs &a, int path);
 cudaError_t launch_linear(int epi, const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
                           const char **why);
 

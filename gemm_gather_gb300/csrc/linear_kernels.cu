@@ -392,6 +392,17 @@ __device__ __forceinline__ void write_rows(const Rows &t, int64_t I, int64_t i0,
                                            const uint8_t *stage)
 {
     __syncwarp();
+    if (!t.vec) {  // a token at a time, its 32 features side by side (see above: 64-byte pieces)
+        uint16_t *q = t.p + j0 * t.ld + i0 + lane;
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(stage) + lane;
+        if (i0 + lane < I) {
+#pragma unroll 8
+            for (int r = 0; r < n; ++r)
+                q[r * t.ld] = h[r * 32];
+        }
+        __syncwarp();
+        return;
+    }
     const int64_t i = i0 + (lane & 3) * 8;
     uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
 #pragma unroll
@@ -399,7 +410,7 @@ __device__ __forceinline__ void write_rows(const Rows &t, int64_t I, int64_t i0,
         if ((lane >> 2) + 8 * k < n) {
             const uint4 x = *reinterpret_cast<const uint4 *>(stage + k * 512 + lane * 16);
             uint16_t *q = p + (int64_t)(8 * k) * t.ld;
-            if (t.vec && i + 8 <= I) {
+            if (i + 8 <= I) {
                 *reinterpret_cast<uint4 *>(q) = x;
             } else {
                 const uint16_t *h = reinterpret_cast<const uint16_t *>(&x);
@@ -1620,33 +1631,47 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
 
 }  // namespace
 
-// A k-block of a pair's 256 x bt tile: its MMAs, its operands through the SM's port,
-// or the ring's latency.
-static double pair_kb_ns(int bt)
+// Everybody's operands of a k-block through the L2 cache, in nanoseconds.
+static double l2_ns(bool lines, double ctas, double bytes)
 {
-    const double mma = bt * 1.08, port = (128 + bt / 2) * kBK * 2 / 127.8;
-    const double kb = mma > port ? mma : port;
-    return kb > 181.0 ? kb : 181.0;
+    return ctas * bytes / (lines ? 15950.0 : 9950.0);
+}
+
+// A k-block of a pair's 256 x bt tile, `ctas` at work: its operands through the SM's
+// port (its MMAs take as long at 256 tokens, less below), the ring's latency, or L2.
+static double pair_kb_ns(int bt, bool lines, double ctas)
+{
+    const double bytes = (128 + bt / 2) * kBK * 2;
+    const double port = bytes / 117.8, l2 = l2_ns(lines, ctas, bytes);
+    const double kb = port > l2 ? port : l2;
+    return kb > 110.7 ? kb : 110.7;
+}
+
+// Launch, set-up and first load of a pair, and its epilogue.
+static double pair_ns(int bt) { return 1724.0 + 23.2 * bt; }
+
+// Whether the operands' rows start on 128-byte lines.  Where they do not, each row
+// of a tile touches two lines: with pitches of 1008 and 1024 elements, 768 tokens,
+// 1536 features and K = 1000 take 8.6 and 6.4 us.
+static bool on_lines(const LinearArgs &a)
+{
+    return ((reinterpret_cast<uint64_t>(a.a) | reinterpret_cast<uint64_t>(a.b) | (uint64_t)(a.lda * 2) |
+             (uint64_t)(a.ldb * 2)) & 127) == 0;
 }
 
 // Which kernel, tile and split: the one of least estimated time, in nanoseconds.
 // The estimate is a launch and its set-up, then waves x k-blocks x the time of a
-// k-block (its MMAs, its operands through an SM's port, or the latency of the
-// ring), then the epilogue.  Its constants were fitted to 560 timings of both
-// kernels (8 weights of 512 x 512 to 8192 x 3584, 1 to 2048 tokens, every tile and
-// split): the choice is on average 0.5% slower than the best of them, 7% at most.
-// By it, few tokens are split over two CTAs an SM (1 token, N = 3584, K = 8192: 8
-// shares 12.9 us, 4 shares 13.7, unsplit 17.7), short contractions are not split
-// (512 tokens, N = K = 1024: unsplit 7.3 us, 4 shares 8.6), and whole 256 x 256 tiles
-// begin where they fill most pairs (1024 tokens, N = 3584, K = 8192: 43 us, 256 x 128
-// tiles 61).  Where one wave of tiles is not full, tiles of 160, 192 or 224 tokens
-// make it shorter (there: 70 tiles of 224 instead of 56).  A weight gradient keeps
-// to multiples of the 64-wide boxes of its MN-major B: 64 split, 128 or 256.
-LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
+// k-block, then the epilogue.  Its constants were fitted to 2300 timings of both
+// kernels (weights of 512 x 512 to 8192 x 3584, 1 to 4096 tokens, rows on and off
+// 128-byte lines, every tile and split, forward and both gradients): the choice is
+// on average 1.4 % slower than the best of them, 15 % at most.
+LinearPlan plan_linear(int epi, const LinearArgs &a, int path)
 {
     LinearPlan best{GG_LINEAR_NONE, 0, 0, 0.0};
+    const int64_t I = a.I, J = a.J, K = a.K;
     if (I <= 0 || J <= 0 || K <= 0)
         return best;
+    const bool lines = on_lines(a);
     const int64_t num_kb = (K + kBK - 1) / kBK;
     const auto offer = [&](int kernel, int bt, int parts, double ns) {
         if (best.kernel == GG_LINEAR_NONE || ns < best.ns)
@@ -1658,29 +1683,33 @@ LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
             const int64_t ctas = tiles * parts;
             if (parts > 1 && ctas > 2 * kSMs)
                 break;
-            const double per_sm = ctas <= kSMs ? 1.0 : (ctas >= 2 * kSMs ? 2.0 : (double)ctas / kSMs);
+            const double here = ctas < 2 * kSMs ? (double)ctas : 2.0 * kSMs;
+            const double per_sm = here <= kSMs ? 1.0 : here / kSMs;
             const double waves = (double)((ctas + 2 * kSMs - 1) / (2 * kSMs));
-            const double latency = 221.0 + 2.05 * bt, port = per_sm * (128 + bt) * kBK * 2 / 101.4;
+            const double bytes = (128 + bt) * kBK * 2;
+            const double latency = 122.3 + 0.867 * bt, port = per_sm * bytes / 91.5, l2 = l2_ns(lines, here, bytes);
+            double kb = latency > port ? latency : port;
+            kb = kb > l2 ? kb : l2;
             offer(GG_LINEAR_SPLIT, bt, parts,
-                  1840.0 + (parts > 1 ? 1580.0 : 0.0) +
-                      waves * (double)((num_kb + parts - 1) / parts) * (latency > port ? latency : port) +
-                      (waves - 1.0) * 1590.0 + bt * (parts > 1 ? 48.0 : 36.0));
+                  2360.0 + (parts > 1 ? 912.0 : 0.0) + waves * (double)((num_kb + parts - 1) / parts) * kb +
+                      (waves - 1.0) * 1328.0 + bt * 40.4);
         }
     }
-    for (int bt = 128; path != GG_LINEAR_SPLIT && bt <= 256; bt += 32) {
-        const bool odd = bt != 128 && bt != 256;
-        if (odd && epi == kEpiGradW)
-            continue;
+    // an MN-major operand is loaded 64 columns at a time by each CTA of a pair
+    const int step = a.b_mn ? 128 : 32;
+    for (int bt = a.b_mn ? 128 : 64; path != GG_LINEAR_SPLIT && bt <= 256; bt += step) {
         const int64_t tiles = ((I + 255) / 256) * ((J + bt - 1) / bt);
         for (int parts = 1; parts <= 4 && parts <= num_kb; parts *= 2) {
             // pairs, and clusters of 4 and 8 CTAs, that are resident at once
             const int64_t room = parts == 1 ? 76 : (parts == 2 ? 36 : 14);
-            if (parts > 1 && (tiles > room || odd))
+            if (parts > 1 && (tiles > room || (bt != 128 && bt != 256)))
                 break;
             const double waves = (double)((tiles + room - 1) / room);
+            const double ctas = 2.0 * parts * (double)(tiles < room ? tiles : room);
             offer(GG_LINEAR_PAIR, bt, parts,
-                  5290.0 + (parts > 1 ? 3500.0 : 0.0) +
-                      waves * (double)((num_kb + parts - 1) / parts) * pair_kb_ns(bt) + 8.6 * bt / parts);
+                  pair_ns(bt / parts) + (parts > 1 ? 3021.0 : 0.0) +
+                      waves * (double)((num_kb + parts - 1) / parts) * pair_kb_ns(bt, lines, ctas) +
+                      (waves - 1.0) * 272.0);
         }
     }
     return best;
@@ -1688,9 +1717,9 @@ LinearPlan plan_linear(int epi, int64_t I, int64_t J, int64_t K, int path)
 
 // The tiles of both gradients of a layer in one walk of the pairs, where that is
 // estimated to end before the two products one after the other: side by side when
-// all tiles fit one wave, else with one launch and one last wave less (with the bias
-// gradient, apart and together: 41 and 30 us for 777 tokens, K = 1523, N = 1000; 312
-// and 291 us for 4096 tokens, K = 8192, N = 3584).
+// all tiles fit one wave, else with one launch and one last wave less (apart and
+// together: 19.0 and 14.2 us for 777 tokens, K = 1523, N = 1000; 298 and 289 us for
+// 4096 tokens, K = 8192, N = 3584).
 bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &plan_dx, const LinearPlan &plan_dw,
                int path, int *bt_dx, int *bt_dw)
 {
@@ -1698,19 +1727,22 @@ bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &pla
         return false;
     const auto tiles = [](const LinearArgs &x, int bt) { return ((x.I + 255) / 256) * ((x.J + bt - 1) / bt); };
     const auto kbs = [](const LinearArgs &x) { return (double)((x.K + kBK - 1) / kBK); };
+    const bool lines_dx = on_lines(dx), lines_dw = on_lines(dw);
     double least = path == GG_LINEAR_PAIR ? 1e300 : plan_dx.ns + plan_dw.ns;
     bool found = false;
-    for (int b0 = 128; b0 <= 256; b0 += 32)
+    for (int b0 = 64; b0 <= 256; b0 += 32)
         for (int b1 = 128; b1 <= 256; b1 += 128) {
             const int64_t t0 = tiles(dx, b0), t1 = tiles(dw, b1);
-            const double w0 = kbs(dx) * pair_kb_ns(b0), w1 = kbs(dw) * pair_kb_ns(b1);
+            const double ctas = 2.0 * (double)(t0 + t1 < 76 ? t0 + t1 : 76);
+            const double w0 = kbs(dx) * pair_kb_ns(b0, lines_dx, ctas) + 196.0;
+            const double w1 = kbs(dw) * pair_kb_ns(b1, lines_dw, ctas) + 196.0;
             // waves of tiles; a walk of both kinds ends with either
             double ns = 0.0;
             if (t0 + t1 <= 76)
                 ns = w0 > w1 ? w0 : w1;
             else
-                ns = ((double)t0 * w0 + (double)t1 * w1) / 76.0 + 0.5 * (w0 < w1 ? w0 : w1);
-            ns += 5290.0 + 8.6 * (b0 > b1 ? b0 : b1);
+                ns = ((double)t0 * w0 + (double)t1 * w1) / 76.0 + 0.695 * (w0 < w1 ? w0 : w1);
+            ns += pair_ns(b0 > b1 ? b0 : b1);
             if (ns < least) {
                 least = ns;
                 *bt_dx = b0;
@@ -1731,7 +1763,8 @@ cudaError_t launch_both(const LinearArgs &dx, int bt_dx, const LinearArgs &dw, i
     LinearArgs x = dx, w = dw;
     x.chunk = 1 << 30;
     w.chunk = kChunk;
-    return launch_pair<kEpiGradIn, kEpiGradW, 256>(x, bt_dx, 1, &w, bt_dw, s, why);
+    return bt_dx > 128 || bt_dw > 128 ? launch_pair<kEpiGradIn, kEpiGradW, 256>(x, bt_dx, 1, &w, bt_dw, s, why)
+                                      : launch_pair<kEpiGradIn, kEpiGradW, 128>(x, bt_dx, 1, &w, bt_dw, s, why);
 }
 
 cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, cudaStream_t s,
