@@ -539,6 +539,7 @@ gg_status gg_linear_backward(const void *dZ, int64_t lddz, const void *X, int64_
             GG_TRY(run_product(gg::kEpiGradW, &b.dw, b.plan_dw, dev_status, stream));
     }
     if (b.run_sum) {
+        b.sum.beside = b.both || (b.run_dx && b.dx.I > 0 && b.dx.J > 0) || (b.run_dw && b.dw.I > 0 && b.dw.J > 0);
         const cudaError_t e = gg::launch_colsum(b.sum, reinterpret_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)
             return op_cuda_fail(e, "launching the bias gradient");

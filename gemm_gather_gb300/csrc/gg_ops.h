@@ -74,6 +74,7 @@ struct ColSumArgs {  // out[i] (+)= sum_j x[j*ldx + i]
     int is_bf16;
     void *out;
     int out_f32, accumulate;
+    int beside;  // launched after the products of the same call, which do not write what it reads
 };
 cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t s);
 

@@ -883,7 +883,6 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     at.abort_flag = &at.sh->abort_flag;
     Shared &sh = *at.sh;
 
-    launch_dependents();
     const int warp = threadIdx.x >> 5;
     // Set-up first, the rest of the arithmetic under it: all of it is on the way of
     // every call (with 64-bit divisions ahead of it, the barriers stood after 1300
@@ -939,6 +938,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     fence_after();
     at.tmem = sh.tmem_base;
     wait_dependencies();  // what earlier launches write is there from here on
+    launch_dependents();
 
     bool ok = true;
     if (warp == 0 || warp == pair::kProducer2) {
@@ -1044,7 +1044,6 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     Shared &sh = *reinterpret_cast<Shared *>(smem + G::kRing);
     volatile int *abort_flag = &sh.abort_flag;
 
-    launch_dependents();
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
@@ -1080,6 +1079,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     fence_after();
     const uint32_t tmem = sh.tmem_base;
     wait_dependencies();
+    launch_dependents();
 
     const int q = warp & 3;  // epilogue: TMEM lane quarter
     const int64_t i = (int64_t)ti * 128 + q * 32 + lane;
@@ -1338,22 +1338,33 @@ __global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ Line
 
 // ---- column sums (bias gradient) -----------------------------------------------------
 // A cluster of kSumParts CTAs owns 64 columns; its CTAs split the rows and
-// each reads whole 128-byte row pieces (8 columns per thread, 32 rows at a
-// time), sums in registers, joins its 32 row groups in shared memory and the
-// cluster's 8 sums through distributed shared memory, in a fixed order.
-// Bound: the read of dZ.
+// each reads whole 128-byte row pieces (8 columns per thread, 16 rows at a
+// time), sums in registers, joins its 16 row groups by shuffles and in shared
+// memory and the cluster's 8 sums through distributed shared memory, in a fixed
+// order.  Bound: the read of dZ.
+//
+// After the products of the same call it runs beside them (a.beside): a CTA fits
+// next to one of theirs (128 threads of at most 56 registers and 0.8 KB of shared
+// memory are what 608 threads of 96 registers and 225 KB leave of an SM), and
+// it need not wait for them.  It may start once every CTA of theirs has passed its
+// own wait for the launches before, so what dZ and dbias hold is there; and one of
+// its CTAs waits for them before it ends, so that whoever waits for this launch has
+// waited for those.  All three gradients of 777 tokens, K = 1523, N = 1000: one after
+// the other 17.5 us, side by side 14.7; of 4096 tokens, K = 8192, N = 3584: 285 both.
 constexpr int kSumParts = 8;
+constexpr int kSumThreads = 128;
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSumThreads, 9)
     colsum_kernel(const __grid_constant__ ColSumArgs a)
 {
-    __shared__ float part[32][65];
-    __shared__ float total[64];
-    launch_dependents();
-    wait_dependencies();
+    __shared__ float part[2][64];
+    if (!a.beside) {
+        wait_dependencies();
+        launch_dependents();
+    }
     const int rank = (int)cluster_ctarank();
     const int64_t i0 = (int64_t)cluster_id_x() * 64;
-    const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+    const int c = threadIdx.x & 7, r = threadIdx.x >> 3, warp = threadIdx.x >> 5;
     const int64_t row0 = a.J * rank / kSumParts, row1 = a.J * (rank + 1) / kSumParts;
     const int64_t col = i0 + c * 8;
     float s[8] = {};
@@ -1363,15 +1374,15 @@ __global__ void __launch_bounds__(256)
         const int64_t n = row1 - row0;
         const bool whole = col + 8 <= a.I;
 #pragma unroll 4
-        for (int64_t k = r; k < n; k += 32) {
+        for (int64_t k = r; k < n; k += kSumThreads / 8) {
             uint16_t h[8];
             if (whole) {
-                *reinterpret_cast<uint4 *>(h) = x[(row0 + k) * ld];
+                *reinterpret_cast<uint4 *>(h) = __ldcg(x + (row0 + k) * ld);
             } else {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
                     h[u] = col + u < a.I
-                               ? reinterpret_cast<const uint16_t *>(a.x)[(row0 + k) * a.ldx + col + u]
+                               ? __ldcg(reinterpret_cast<const uint16_t *>(a.x) + (row0 + k) * a.ldx + col + u)
                                : (uint16_t)0;
             }
 #pragma unroll
@@ -1381,22 +1392,30 @@ __global__ void __launch_bounds__(256)
         }
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-        part[r][c * 8 + u] = s[u];
+    for (int u = 0; u < 8; ++u) {  // the warp's four rows
+        s[u] += __shfl_xor_sync(~0u, s[u], 8);
+        s[u] += __shfl_xor_sync(~0u, s[u], 16);
+    }
+    if (warp >= 2 && (threadIdx.x & 24) == 0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            part[warp - 2][c * 8 + u] = s[u];
+    }
     __syncthreads();
-    if (threadIdx.x < 64) {
-        float t = 0.0f;
-        for (int k = 0; k < 32; ++k)
-            t += part[k][threadIdx.x];
-        total[threadIdx.x] = t;
+    if (warp < 2 && (threadIdx.x & 24) == 0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            part[warp][c * 8 + u] += s[u];
     }
     __syncthreads();
     cluster_sync();
     const int64_t i = i0 + threadIdx.x;
     if (rank == 0 && threadIdx.x < 64 && i < a.I) {
         float t = 0.0f;
-        for (int p = 0; p < kSumParts; ++p)
-            t += ld_cluster_f32(map_to_rank(ptx::smem_addr(&total[threadIdx.x]), (uint32_t)p));
+        for (int p = 0; p < kSumParts; ++p) {
+            t += ld_cluster_f32(map_to_rank(ptx::smem_addr(&part[0][threadIdx.x]), (uint32_t)p));
+            t += ld_cluster_f32(map_to_rank(ptx::smem_addr(&part[1][threadIdx.x]), (uint32_t)p));
+        }
         if (a.out_f32) {
             float *o = reinterpret_cast<float *>(a.out) + i;
             *o = a.accumulate ? *o + t : t;
@@ -1406,6 +1425,8 @@ __global__ void __launch_bounds__(256)
     }
     __syncwarp();
     cluster_sync();
+    if (a.beside && i0 == 0 && rank == 0)
+        wait_dependencies();
 }
 
 // ---- activation backward: dz = dy * act'(z) --------------------------------------------
@@ -1787,7 +1808,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
 
 cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t s)
 {
-    ClusterLaunch l(kSumParts, (a.I + 63) / 64 * kSumParts, 256, 0, s);
+    ClusterLaunch l(kSumParts, (a.I + 63) / 64 * kSumParts, kSumThreads, 0, s);
     return cudaLaunchKernelEx(&l.cfg, colsum_kernel, a);
 }
 
