@@ -21,16 +21,21 @@
 // only the MMA's columns (16 at least) and not its 128 rows.
 //
 // Two kernels:
-//  * pair_kernel: persistent CTA pairs on 256 x 256 tiles (tcgen05
-//    cta_group::2, 64-deep stages of 32 KB per CTA, 6 in the ring, two
-//    accumulators in TMEM so that a tile's epilogue runs under the next
-//    tile's MMAs).  For products with enough tiles to fill the GPU.
-//  * split_kernel: one CTA per 128 x {16..128} tile and share of the
-//    contraction; the CTAs of a cluster (up to 8) split one tile's
+//  * pair_kernel: persistent CTA pairs on tiles of 256 features x 64 to 256
+//    tokens (tcgen05 cta_group::2, 64-deep stages, 6 or 8 in a ring of 192 KB per
+//    CTA, two accumulators in TMEM so that a tile's epilogue runs under the next
+//    tile's MMAs).  Bound: the tensor pipes, under the power limit.  Measured:
+//    16384 x 3584 x 8192 with gelu_tanh and Z stored in 517 to 550 us (1.75 to 1.86
+//    PFLOP/s; cuBLAS's product alone on the same boxes 494 to 547), pipes 90 %
+//    active at 4096 x 4864 x 8192 with gelu and Z.
+//  * split_kernel: one CTA per tile of 128 features x {16, 32, 64} tokens and share
+//    of the contraction; the CTAs of a cluster (up to 8) split one tile's
 //    contraction and join their float32 partial tiles through distributed
 //    shared memory in rank order (the same bits on every run, no workspace, no
 //    second launch).  For few tokens, where the time is that of streaming W,
-//    and for few tiles.
+//    and for few tiles.  Bound: HBM, and below some 10 us the launch, the first
+//    load and the join.  Measured: 1 x 3584 x 8192 in 12.3 us, of which the weights'
+//    bytes take 8.6 (4.7 TB/s over all of it); the join takes 1.6, a launch 1.9.
 //
 // Sums.  tcgen05's float32 accumulator truncates when it adds: measured
 // against float64 on normal operands, the relative error grows with the
@@ -1338,23 +1343,26 @@ __global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ Line
 
 // ---- column sums (bias gradient) -----------------------------------------------------
 // A cluster of kSumParts CTAs owns 64 columns; its CTAs split the rows and
-// each reads whole 128-byte row pieces (8 columns per thread, 16 rows at a
-// time), sums in registers, joins its 16 row groups by shuffles and in shared
+// each reads whole 128-byte row pieces (4 columns per thread, 8 rows at a
+// time), sums in registers, joins its 8 row groups by shuffles and in shared
 // memory and the cluster's 8 sums through distributed shared memory, in a fixed
 // order.  Bound: the read of dZ.
 //
 // After the products of the same call it runs beside them (a.beside): a CTA fits
-// next to one of theirs (128 threads of at most 56 registers and 0.8 KB of shared
-// memory are what 608 threads of 96 registers and 225 KB leave of an SM), and
-// it need not wait for them.  It may start once every CTA of theirs has passed its
-// own wait for the launches before, so what dZ and dbias hold is there; and one of
-// its CTAs waits for them before it ends, so that whoever waits for this launch has
-// waited for those.  All three gradients of 777 tokens, K = 1523, N = 1000: one after
-// the other 17.5 us, side by side 14.7; of 4096 tokens, K = 8192, N = 3584: 285 both.
+// next to one of theirs (19 warps of 96 registers leave a quarter of an SM 1024
+// registers, a warp's 32, and 225 KB of shared memory leave 0.8), and it need not
+// wait for them.  It may start once every CTA of theirs has passed its own wait
+// for the launches before, so what dZ and dbias hold is there; and one of its CTAs
+// waits for them before it ends, so that whoever waits for this launch has waited
+// for those.  All three gradients of 777 tokens, K = 1523, N = 1000: one after the
+// other 17.5 us, side by side 14.7; of 4096 tokens, K = 8192, N = 3584: 289 us with
+// 54 registers a thread, which do not fit, and 278 side by side.
 constexpr int kSumParts = 8;
 constexpr int kSumThreads = 128;
+constexpr int kSumRows = kSumThreads / 16;  // rows at a time
 
-__global__ void __launch_bounds__(kSumThreads, 9)
+template <bool BF16>
+__global__ void __launch_bounds__(kSumThreads, 16)
     colsum_kernel(const __grid_constant__ ColSumArgs a)
 {
     __shared__ float part[2][64];
@@ -1364,50 +1372,52 @@ __global__ void __launch_bounds__(kSumThreads, 9)
     }
     const int rank = (int)cluster_ctarank();
     const int64_t i0 = (int64_t)cluster_id_x() * 64;
-    const int c = threadIdx.x & 7, r = threadIdx.x >> 3, warp = threadIdx.x >> 5;
-    const int64_t row0 = a.J * rank / kSumParts, row1 = a.J * (rank + 1) / kSumParts;
-    const int64_t col = i0 + c * 8;
-    float s[8] = {};
-    if (col < a.I) {  // a pitch is whole 16-byte units, so a started unit is inside the row's pitch
-        const uint4 *x = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.x) + col);
-        const int64_t ld = a.ldx / 8;
-        const int64_t n = row1 - row0;
-        const bool whole = col + 8 <= a.I;
+    const int c = threadIdx.x & 15, warp = threadIdx.x >> 5;
+    const int64_t col = i0 + c * 4;
+    float s[4] = {};
+    if (col < a.I) {
+        const int64_t row0 = a.J * rank / kSumParts + threadIdx.x / 16;
+        int64_t n = (a.J * (rank + 1) / kSumParts - row0 + kSumRows - 1) / kSumRows;
+        const int64_t step = kSumRows * a.ldx;
+        const uint16_t *x = reinterpret_cast<const uint16_t *>(a.x) + row0 * a.ldx + col;
+        if (col + 4 > a.I) {  // nothing is read past a row's end: behind the last there may be none
+            for (; n > 0; --n, x += step)
+                for (int u = 0; u < 3; ++u)
+                    s[u] += col + u < a.I ? load16(x, u, BF16) : 0.0f;
+        }
 #pragma unroll 4
-        for (int64_t k = r; k < n; k += kSumThreads / 8) {
-            uint16_t h[8];
-            if (whole) {
-                *reinterpret_cast<uint4 *>(h) = __ldcg(x + (row0 + k) * ld);
+        for (; n > 0; --n, x += step) {
+            const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(x));
+            if (BF16) {
+                s[0] += __uint_as_float(w.x << 16);
+                s[1] += __uint_as_float(w.x & 0xffff0000u);
+                s[2] += __uint_as_float(w.y << 16);
+                s[3] += __uint_as_float(w.y & 0xffff0000u);
             } else {
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    h[u] = col + u < a.I
-                               ? __ldcg(reinterpret_cast<const uint16_t *>(a.x) + (row0 + k) * a.ldx + col + u)
-                               : (uint16_t)0;
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+                const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+                s[0] += f0.x;
+                s[1] += f0.y;
+                s[2] += f1.x;
+                s[3] += f1.y;
             }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                s[u] += a.is_bf16 ? __uint_as_float((uint32_t)h[u] << 16)
-                                  : __half2float(__ushort_as_half(h[u]));
         }
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {  // the warp's four rows
-        s[u] += __shfl_xor_sync(~0u, s[u], 8);
+    for (int u = 0; u < 4; ++u)  // the warp's two rows
         s[u] += __shfl_xor_sync(~0u, s[u], 16);
-    }
-    if (warp >= 2 && (threadIdx.x & 24) == 0) {
+    if (warp >= 2 && (threadIdx.x & 16) == 0) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            part[warp - 2][c * 8 + u] = s[u];
+        for (int u = 0; u < 4; ++u)
+            part[warp - 2][c * 4 + u] = s[u];
     }
     __syncthreads();
-    if (warp < 2 && (threadIdx.x & 24) == 0) {
+    if (warp < 2 && (threadIdx.x & 16) == 0) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            part[warp][c * 8 + u] += s[u];
+        for (int u = 0; u < 4; ++u)
+            part[warp][c * 4 + u] += s[u];
     }
-    __syncthreads();
+    __syncwarp();
     cluster_sync();
     const int64_t i = i0 + threadIdx.x;
     if (rank == 0 && threadIdx.x < 64 && i < a.I) {
@@ -1420,7 +1430,7 @@ __global__ void __launch_bounds__(kSumThreads, 9)
             float *o = reinterpret_cast<float *>(a.out) + i;
             *o = a.accumulate ? *o + t : t;
         } else {
-            store16(a.out, i, a.accumulate ? load16(a.out, i, a.is_bf16) + t : t, a.is_bf16);
+            store16(a.out, i, a.accumulate ? load16(a.out, i, BF16) + t : t, BF16);
         }
     }
     __syncwarp();
@@ -1809,7 +1819,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
 cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t s)
 {
     ClusterLaunch l(kSumParts, (a.I + 63) / 64 * kSumParts, kSumThreads, 0, s);
-    return cudaLaunchKernelEx(&l.cfg, colsum_kernel, a);
+    return cudaLaunchKernelEx(&l.cfg, a.is_bf16 ? colsum_kernel<true> : colsum_kernel<false>, a);
 }
 
 cudaError_t launch_act_backward(const ActBackwardArgs &a, cudaStream_t s)

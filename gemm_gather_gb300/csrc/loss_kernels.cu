@@ -14,10 +14,10 @@
 // A cluster of CTAs owns a row, each CTA a slice, and the CTAs exchange
 // (maximum, sum) through distributed shared memory.
 // Bound: HBM, one read and one write of the logits.  Measured: 8191 x 32768
-// float32 with a tenth of the tokens masked in 320 us (94 % of the copy rate),
-// 4096 x 100003 bfloat16 with a quarter masked in 263 us (80 %; twice the powers a
-// byte, and the passes' ends are not all covered by the SM's other CTA); 16 x 8192
-// in 5.7 us, which is two launches.
+// float32 with a tenth of the tokens masked in 310 us (97 % of the copy rate),
+// 4096 x 100003 bfloat16 with a quarter masked in 255 us (83 %; twice the powers a
+// byte, instructions issue in 54 % of the cycles, and the passes' ends are not all
+// covered by the SM's other CTA); 16 x 8192 in 5.3 us, which is two launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -810,8 +810,9 @@ cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
     // A row's vectors (one more than V needs: a row may start between two
     // 16-byte boundaries) are shared by as few CTAs as hold 100 KB each, two on an
     // SM; by up to 8 (a portable cluster) of up to 216 KB where that is not enough.
-    // (Of up to 52 KB each: 294 us for 263 at 4096 x 100003 bfloat16, 332 for 320 at
-    // 8191 x 32768 float32; of up to 200 KB, one on an SM: 293 and 390.)
+    // (Of up to 67 KB each: 283 us where this took 262, at 4096 x 100003 bfloat16; of
+    // up to 52 KB 294, of up to 200 KB, one on an SM, 293, at 8191 x 32768 float32
+    // then 332 and 390 for 320.)
     // When the rows are few, more and smaller CTAs share a row, down to 128 vectors
     // each.  Threads have up to 16 vectors.
     const int64_t vecs = (a.V + Elem<E>::kVec - 1) / Elem<E>::kVec + 1;
@@ -829,8 +830,8 @@ cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
     // Clusters: one for every 3 rows, as far as there are more rows than clusters
     // resident at once.  Masked rows cost half: with fixed shares for all rows
     // (resident clusters only) the unluckiest ended a quarter late.  4096 x 100003
-    // bfloat16: 2 rows 267 us, 3 rows 263, 4 rows 262, 6 rows 264; with a slower
-    // exchange 12 rows 315, all rows 297, 1 row (no copy ahead) 305, 3 rows 284.
+    // bfloat16: 2 rows 267 us, 3 rows 263, 4 rows 262, 6 rows 264; with the slower
+    // exchange of an earlier build 12 rows 315, all rows 297, 1 row (no copy ahead) 305, 3 rows 284.
     const int64_t fit = kMaxSliceBytes / bytes;
     const int64_t per_sm = fit < 1 ? 1 : gg_min64(fit, gg_min64(16, 896 / threads > 0 ? 896 / threads : 1));
     const int64_t resident = per_sm * kSMs / parts;
