@@ -346,7 +346,8 @@ gg_status prepare_loss(const void *logits, int64_t ld, const int64_t *target, co
                         advantage, weight,    T,       V,        (int)dtype,
                         inv_temperature, clip_low, clip_high, kl_coef, grad_scale,
                         const_cast<float *>(stats), const_cast<float *>(logp_out),
-                        const_cast<void *>(dlogits), ldd, nullptr, gg::op_wait_limit_ns()};
+                        const_cast<void *>(dlogits), ldd, nullptr, gg::op_wait_limit_ns(),
+                        gg::op_inject_stall()};
     return op_ok();
 }
 

@@ -100,6 +100,7 @@ struct LossArgs {
     int64_t ldd;
     int *status;
     uint64_t wait_limit_ns;
+    int inject_stall;
 };
 cudaError_t launch_policy_loss(const LossArgs &a, cudaStream_t s);
 

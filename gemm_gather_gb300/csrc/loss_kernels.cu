@@ -571,9 +571,11 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
             // buffer is filled again two rows on: by then every warp of the cluster has
             // sent the next row's sum, after it had read this one's.
             const Message said{acc.m, acc.s, __shfl_sync(~0u, logit, 0), 0.0f};
-            if (lane < parts)
+            // test hook: one warp's message is never sent
+            const bool stall = a.inject_stall && t == 0 && rank == 0 && warp == 0;
+            if (lane < parts && !stall)
                 send(ptx::smem_addr(box + rank * warps + warp), bar, (uint32_t)lane, said);
-            if (!__all_sync(~0u, ptx::mbar_wait(bar, phase, a.wait_limit_ns))) {
+            if (!__all_sync(~0u, tc::bounded_wait(bar, phase, a.wait_limit_ns))) {
                 if (lane == 0)
                     report_status(a.status, kStatusTimeout);
                 break;

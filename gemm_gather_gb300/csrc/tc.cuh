@@ -253,15 +253,28 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
 }
 
 // ---- bounded waits -----------------------------------------------------------------
-// Wait for a barrier's phase; gives up at the wall-clock limit, or as soon as
-// another role of the CTA raised the abort flag.
+// Some tries without a look at the clock: a read of it takes as long as a k-block.
+__device__ __forceinline__ bool first_tries(uint32_t bar, uint32_t parity)
+{
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (ptx::mbar_try_wait(bar, parity))
+            return true;
+    return false;
+}
+
+// Wait for a barrier's phase; gives up at the wall-clock limit.
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    return first_tries(bar, parity) || ptx::mbar_wait(bar, parity, limit_ns);
+}
+
+// The same, and gives up as soon as another role of the CTA raised the abort flag.
 __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           volatile int *abort_flag)
 {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)  // a read of the clock takes as long as a k-block
-        if (ptx::mbar_try_wait(bar, parity))
-            return true;
+    if (first_tries(bar, parity))
+        return true;
     const uint64_t t0 = ptx::globaltimer();
     for (;;) {
 #pragma unroll 1

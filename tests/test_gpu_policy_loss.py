@@ -260,3 +260,26 @@ def test_no_tokens_and_same_bits():
         b = call(c)
     side.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("T,V", [(1, 64), (5, 4097), (400, 100003)])
+def test_a_wait_that_runs_out_is_reported(T, V):
+    """One message of the first token's cluster is never sent: the bounded wait gives up, the status
+    word says so, and the same call afterwards is right."""
+    import gemm_gather_gb300 as gg
+    c = far_from_clip(make(T, V, BF16, masked=0.0, seed=11))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    old = gg.get_wait_limit_ns()
+    try:
+        gg.set_wait_limit_ns(20_000_000)
+        gg.debug_inject_stall(True)
+        call(c, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == -6
+    finally:
+        gg.debug_inject_stall(False)
+        gg.set_wait_limit_ns(old)
+    status.zero_()
+    got = call(c, status=status)
+    assert int(status.item()) == 0
+    check(c, got)
