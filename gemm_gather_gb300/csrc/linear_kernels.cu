@@ -1293,15 +1293,20 @@ __global__ void __launch_bounds__(split::kThreads, 2)
             const uint32_t mine = base + (uint32_t)(q * 32 + lane) * 4;
             const int64_t left = a.J - jt;  // valid columns of the tile
             const int cols = left < BT ? (int)left : BT;
+            // Columns at a time: as many as a CTA of a full cluster has, up to 4.  This is
+            // code that runs once, and what it costs is mostly its fetching: with 4 instead
+            // of 2 for 16-token tiles, one token took 12.6 us instead of 12.35, 27 tokens 5.35
+            // instead of 5.1; with 1, 12.3 and 5.4.
+            constexpr int C = BT == 16 ? 2 : 4;
 #pragma unroll 1
-            for (int c0 = rank; c0 < cols; c0 += 4 * parts) {
+            for (int c0 = rank; c0 < cols; c0 += C * parts) {
                 const int n = (cols - c0 + parts - 1) / parts;
-                float x[8][4];  // every CTA's sums of four columns, all loads in flight
+                float x[8][C];  // every CTA's sums of C columns, all loads in flight
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
                     const uint32_t src = map_to_rank(mine, (uint32_t)(s < parts ? s : 0));
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < C; ++u)
                         x[s][u] = s < parts && u < n
                                       ? ld_cluster_f32(src + (uint32_t)(c0 + u * parts) * 512)
                                       : 0.0f;
@@ -1310,9 +1315,9 @@ __global__ void __launch_bounds__(split::kThreads, 2)
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < C; ++u)
                         v[u] += x[s][u];
-                emit16<EPI, 4>(a, i, jt + c0, parts, n < 4 ? n : 4, v, bias);
+                emit16<EPI, C>(a, i, jt + c0, parts, n < C ? n : C, v, bias);
             }
         }
         __syncwarp();
