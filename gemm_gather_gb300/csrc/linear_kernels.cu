@@ -34,8 +34,8 @@
 //    shared memory in rank order (the same bits on every run, no workspace, no
 //    second launch).  For few tokens, where the time is that of streaming W,
 //    and for few tiles.  Bound: HBM, and below some 10 us the launch, the first
-//    load and the join.  Measured: 1 x 3584 x 8192 in 12.3 us, of which the weights'
-//    bytes take 8.6 (4.7 TB/s over all of it); the join takes 1.6, a launch 1.9.
+//    load and the join.  Measured: 1 x 3584 x 8192 in 12.2 us, of which the weights'
+//    bytes take 8.6 (4.8 TB/s over all of it); the join takes 1.5, a launch 1.9.
 //
 // Sums.  tcgen05's float32 accumulator truncates when it adds: measured
 // against float64 on normal operands, the relative error grows with the
