@@ -390,6 +390,26 @@ __device__ __forceinline__ void wait_groups(int left)
 
 __device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// How much of a row a lane has: `have` vectors; of batches, `whole` that every lane
+// of the warp has in full, `some` that any has of (the warp's vectors are dealt out
+// in turn: lane 31 has the fewest, lane 0 the most).
+struct Share {
+    int have, whole, some;
+    // a warp's vectors from `base` on, of nvec, at most NV a lane
+    template <int NV>
+    static __device__ __forceinline__ Share of(int nvec, int base, int lane)
+    {
+        const int left = nvec > base ? nvec - base : 0;
+        const int least = left / 32, most = (left + 31) / 32;
+        Share r;
+        r.have = least + (lane < left % 32 ? 1 : 0);
+        r.have = r.have < NV ? r.have : NV;
+        r.whole = (least < NV ? least : NV) / kBatch;
+        r.some = ((most < NV ? most : NV) + kBatch - 1) / kBatch;
+        return r;
+    }
+};
+
 // A lane's NB * kBatch vectors: `slot` in shared memory, in steps of 512 bytes;
 // `have` of them exist (all, where FULL).
 template <typename E, int NB>
@@ -423,54 +443,73 @@ struct Lane {
             v = *reinterpret_cast<const Vec<E> *>(slot + q * 512);
     }
 
-    // The running maximum and sum over the vectors.
+    // The running maximum and sum over batch `b`.
     template <bool FULL>
-    __device__ __forceinline__ void sum_up(Sum &acc, int have, float c) const
+    __device__ __forceinline__ void sum_batch(int b, Sum &acc, int have, float c) const
+    {
+        Vec<E> v[kBatch];
+        float top = acc.m;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            take<FULL>(b * kBatch + q, have, v[q]);
+            top = top_of(v[q], top);
+            stay_packed(v[q]);
+        }
+        if (top > acc.m) {
+            acc.s *= rescale(acc.m, top, c);
+            acc.m = top;
+        }
+        F2 part[2] = {pair_of(0.0f), pair_of(0.0f)};
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            add_powers(v[q], base_of(acc.m), c, part);
+        const float2 sum2 = halves_of(add2(part[0], part[1]));
+        acc.s += sum2.x + sum2.y;
+    }
+
+    // All batches: those that every lane has whole without tests, none that no lane has.
+    __device__ __forceinline__ void sum_up(Sum &acc, const Share &now, float c) const
     {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             wait_groups(NB - 1 - b);
-            Vec<E> v[kBatch];
-            float top = acc.m;
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                take<FULL>(b * kBatch + q, have, v[q]);
-                top = top_of(v[q], top);
-                stay_packed(v[q]);
-            }
-            if (top > acc.m) {
-                acc.s *= rescale(acc.m, top, c);
-                acc.m = top;
-            }
-            F2 part[2] = {pair_of(0.0f), pair_of(0.0f)};
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-                add_powers(v[q], base_of(acc.m), c, part);
-            const float2 sum2 = halves_of(add2(part[0], part[1]));
-            acc.s += sum2.x + sum2.y;
+            if (b < now.whole)
+                sum_batch<true>(b, acc, NV, c);
+            else if (b < now.some)
+                sum_batch<false>(b, acc, now.have, c);
         }
     }
 
-    // The gradient's vectors to `to`, the next row's (FETCH, have_next of them) in their
-    // place.
+    // Batch `b` of the gradient to `to`, the next row's vectors (FETCH) in its place.
     template <bool FULL, bool FETCH>
-    __device__ __forceinline__ void write(const Gradient<E> &g, uint8_t *to, int have, const uint8_t *from,
-                                          int have_next) const
+    __device__ __forceinline__ void write_batch(int b, const Gradient<E> &g, uint8_t *to, int have,
+                                                const uint8_t *from, int have_next) const
+    {
+        Vec<E> v[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            take<FULL>(b * kBatch + q, have, v[q]);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            g.softmax(v[q]);  // uses the vector: its place is free
+            if (FULL || b * kBatch + q < have)
+                *reinterpret_cast<Vec<E> *>(to + (b * kBatch + q) * 512) = v[q];
+            if (FETCH)
+                fetch<FULL>(from, b * kBatch + q, have_next);
+        }
+    }
+
+    __device__ __forceinline__ void write(const Gradient<E> &g, uint8_t *to, const Share &now, const uint8_t *from,
+                                          const Share &next) const
     {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            Vec<E> v[kBatch];
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-                take<FULL>(b * kBatch + q, have, v[q]);
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                g.softmax(v[q]);  // uses the vector: its place is free
-                if (FULL || b * kBatch + q < have)
-                    *reinterpret_cast<Vec<E> *>(to + (b * kBatch + q) * 512) = v[q];
-                if (FETCH)
-                    fetch<FULL>(from, b * kBatch + q, have_next);
-            }
+            if (b < now.whole && b < next.whole)
+                write_batch<true, true>(b, g, to, NV, from, NV);
+            else if (b < now.whole && b >= next.some)
+                write_batch<true, false>(b, g, to, NV, from, 0);
+            else if (b < now.some || b < next.some)
+                write_batch<false, true>(b, g, to, now.have, from, next.have);
             commit_group();
         }
     }
@@ -524,16 +563,15 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
     // target's logit.
     Slice<E> s(a, rank, parts), n = s;
     const uint8_t *from = nullptr;
-    int have_next = 0;
+    Share share_next{0, 0, 0};
     float xh = 0.0f, xt = 0.0f, picked = 0.0f;
     const auto look = [&](int64_t t, const Token &k) {
         n.at(a, t);
-        have_next = 0;
+        share_next = Share{0, 0, 0};
         if (!k.live(a))
             return;
         from = reinterpret_cast<const uint8_t *>(n.vec() + first);
-        have_next = n.nvec > first ? (n.nvec - first + 31) / 32 : 0;
-        have_next = have_next < NV ? have_next : NV;
+        share_next = Share::of<NV>(n.nvec, warp * NV * 32, lane);
         if (rank == 0 && tid == 0)
             picked = Elem<E>::get(n.row[k.target]);
         xh = n.has_head(tid) ? Elem<E>::get(n.row[n.lo + tid]) : -INFINITY;
@@ -543,74 +581,67 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
     int64_t t = tc::cluster_id_x();
     Token now(a, t), next(a, t + step);
     look(t, now);
-    mine.fetch_all(from, have_next);
+    mine.fetch_all(from, share_next.have);
     uint32_t turn = 0, phase = 0;  // of the messages: two buffers in turn
     for (; t < a.T; t += step) {
         const Token later(a, t + 2 * step);
         s = n;
         const bool live = now.live(a);  // the same for the whole cluster
-        const int have = have_next;
+        const Share share = share_next;
         const float head = xh, tail = xt, logit = picked;
         look(t + step, next);
-        const bool full = __all_sync(~0u, have == NV);
         if (live) {
             const uint32_t bar = ptx::smem_addr(&arrived[turn]);
             Message *const box = messages + turn * count;
-            if (tid == 0)
+            if (tid == 0 && count > 1)
                 ptx::mbar_arrive_expect_tx(bar, (uint32_t)(count * (int)sizeof(Message)));
             Sum acc{fmaxf(head, tail), 0.0f};
             const float m = base_of(acc.m);
             acc.s = ex2((head - m) * c) + ex2((tail - m) * c);  // -inf where there is none
-            if (full)
-                mine.template sum_up<true>(acc, NV, c);
-            else
-                mine.template sum_up<false>(acc, have, c);
-            acc = warp_join(acc, c);
-            // The warps' sums, to every CTA.  The target's logit travels with one of
-            // them, so that no gradient is written over it before it has been read.  A
-            // buffer is filled again two rows on: by then every warp of the cluster has
-            // sent the next row's sum, after it had read this one's.
-            const Message said{acc.m, acc.s, __shfl_sync(~0u, logit, 0), 0.0f};
-            // test hook: one warp's message is never sent
-            const bool stall = a.inject_stall && t == 0 && rank == 0 && warp == 0;
-            if (lane < parts && !stall)
-                send(ptx::smem_addr(box + rank * warps + warp), bar, (uint32_t)lane, said);
-            if (!__all_sync(~0u, tc::bounded_wait(bar, phase, a.wait_limit_ns))) {
-                if (lane == 0)
-                    report_status(a.status, kStatusTimeout);
-                break;
+            mine.sum_up(acc, share, c);
+            Sum all = warp_join(acc, c);
+            float target_logit = __shfl_sync(~0u, logit, 0);
+            if (count > 1) {
+                // The warps' sums, to every CTA.  The target's logit travels with one of
+                // them, so that no gradient is written over it before it has been read.  A
+                // buffer is filled again two rows on: by then every warp of the cluster has
+                // sent the next row's sum, after it had read this one's.
+                const Message said{all.m, all.s, target_logit, 0.0f};
+                // test hook: one warp's message is never sent
+                const bool stall = a.inject_stall && t == 0 && rank == 0 && warp == 0;
+                if (lane < parts && !stall)
+                    send(ptx::smem_addr(box + rank * warps + warp), bar, (uint32_t)lane, said);
+                if (!__all_sync(~0u, tc::bounded_wait(bar, phase, a.wait_limit_ns))) {
+                    if (lane == 0)
+                        report_status(a.status, kStatusTimeout);
+                    break;
+                }
+                all = Sum{-INFINITY, 0.0f};
+                for (int i = lane; i < count; i += 32)
+                    all = join(all, Sum{box[i].m, box[i].s}, c);
+                all = warp_join(all, c);
+                target_logit = box[0].logit;
+                __syncwarp();
+                phase ^= turn;
+                turn ^= 1;
             }
-            Sum all{-INFINITY, 0.0f};
-            for (int i = lane; i < count; i += 32)
-                all = join(all, Sum{box[i].m, box[i].s}, c);
-            all = warp_join(all, c);
-            const float target_logit = box[0].logit;
-            __syncwarp();
-            phase ^= turn;
-            turn ^= 1;
             const float logp = logp_of(a, all, target_logit);
             if (rank == 0 && tid == 0)
                 a.logp_out[t] = logp;
             const Gradient<E> g(a, now, all, logp, c);
             if (s.wide) {
                 uint8_t *to = reinterpret_cast<uint8_t *>(s.out + s.v0) + first * 16;
-                const bool next_full = __all_sync(~0u, have_next == NV);
-                if (full && next_full)
-                    mine.template write<true, true>(g, to, NV, from, NV);
-                else if (full && __all_sync(~0u, have_next == 0))
-                    mine.template write<true, false>(g, to, NV, from, 0);
-                else
-                    mine.template write<false, true>(g, to, have, from, have_next);
+                mine.write(g, to, share, from, share_next);
             } else {  // an output of another alignment, or none
 #pragma unroll 1
-                for (int q = 0; q < have && s.out; ++q) {
+                for (int q = 0; q < share.have && s.out; ++q) {
                     Vec<E> v = *reinterpret_cast<const Vec<E> *>(mine.slot + q * 512);
                     g.softmax(v);
 #pragma unroll
                     for (int u = 0; u < VEC; ++u)
                         s.out[s.v0 + (first + q * 32) * VEC + u] = reinterpret_cast<const E *>(v.w)[u];
                 }
-                mine.fetch_all(from, have_next);
+                mine.fetch_all(from, share_next.have);
             }
             if (s.out) {
                 if (s.has_head(tid))
@@ -625,7 +656,7 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
                     s.out[g.target] = g.target_one(target_logit);
             }
         } else {
-            mine.fetch_all(from, have_next);
+            mine.fetch_all(from, share_next.have);
             if (rank == 0 && tid == 0) {
                 a.logp_out[t] = 0.0f;
                 if (now.weight != 0.0f)
@@ -809,23 +840,21 @@ cudaError_t launch_held(cudaLaunchConfig_t &cfg, const LossArgs &a)
 template <typename E>
 cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
 {
-    // A row's vectors (one more than V needs: a row may start between two
-    // 16-byte boundaries) are shared by as few CTAs as hold 100 KB each, two on an
+    // A row's vectors are shared by as few CTAs as hold 100 KB each, two on an
     // SM; by up to 8 (a portable cluster) of up to 216 KB where that is not enough.
     // (Of up to 67 KB each: 283 us where this took 262, at 4096 x 100003 bfloat16; of
     // up to 52 KB 294, of up to 200 KB, one on an SM, 293, at 8191 x 32768 float32
     // then 332 and 390 for 320.)
     // When the rows are few, more and smaller CTAs share a row, down to 128 vectors
     // each.  Threads have up to 16 vectors.
-    const int64_t vecs = (a.V + Elem<E>::kVec - 1) / Elem<E>::kVec + 1;
+    const int64_t vecs = (a.V + Elem<E>::kVec - 1) / Elem<E>::kVec;
     int64_t parts = (vecs + kSliceVecs - 1) / kSliceVecs;
     parts = parts > 8 ? 8 : parts;
     while (parts <= 4 && a.T * parts * 2 <= 2 * kSMs && vecs / (parts * 2) >= 128)
         parts *= 2;
-    const int64_t slice = (vecs + parts - 1) / parts + 1;
+    const int64_t slice = (vecs + parts - 1) / parts;  // a row that starts between two 16-byte boundaries has no more
     const int nb = slice <= 4 * 128 ? 1 : (slice <= 8 * 128 ? 2 : 4);
     int64_t threads = (slice + nb * kBatch * 32 - 1) / (nb * kBatch * 32) * 32;
-    threads = threads < 64 ? 64 : threads;
     const int64_t bytes = threads * nb * kBatch * 16;
     const bool held = bytes <= kMaxSliceBytes;
     threads = held ? threads : 1024;
@@ -835,7 +864,7 @@ cudaError_t launch_rows(const LossArgs &a, cudaStream_t s)
     // bfloat16: 2 rows 267 us, 3 rows 263, 4 rows 262, 6 rows 264; with the slower
     // exchange of an earlier build 12 rows 315, all rows 297, 1 row (no copy ahead) 305, 3 rows 284.
     const int64_t fit = kMaxSliceBytes / bytes;
-    const int64_t per_sm = fit < 1 ? 1 : gg_min64(fit, gg_min64(16, 896 / threads > 0 ? 896 / threads : 1));
+    const int64_t per_sm = fit < 1 ? 1 : gg_min64(fit, gg_min64(32, 896 / threads > 0 ? 896 / threads : 1));
     const int64_t resident = per_sm * kSMs / parts;
     const int64_t thirds = (a.T + 2) / 3;
     const int64_t clusters = !held || a.T <= resident ? a.T : (thirds > resident ? thirds : resident);
