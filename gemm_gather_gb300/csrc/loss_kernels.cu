@@ -15,9 +15,9 @@
 // (maximum, sum) through distributed shared memory.
 // Bound: HBM, one read and one write of the logits.  Measured: 8191 x 32768
 // float32 with a tenth of the tokens masked in 310 us (97 % of the copy rate),
-// 4096 x 100003 bfloat16 with a quarter masked in 255 us (83 %; twice the powers a
-// byte, instructions issue in 54 % of the cycles, and the passes' ends are not all
-// covered by the SM's other CTA); 16 x 8192 in 5.3 us, which is two launches.
+// 4096 x 100003 bfloat16 with a quarter masked in 250 us (85 %; twice the powers a
+// byte, instructions issue in 57 % of the cycles, and the passes' ends are not all
+// covered by the SM's other CTA); 16 x 8192 in 5.4 us, which is two launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -411,7 +411,9 @@ struct Share {
 };
 
 // A lane's NB * kBatch vectors: `slot` in shared memory, in steps of 512 bytes;
-// `have` of them exist (all, where FULL).
+// `have` of them exist (all, where FULL).  A warp skips the batches that it has none
+// of: when the last warp of a row took the tests for all 16 of its vectors, the
+// others waited for it (8000 x 8192 float16: 86 us, then 64).
 template <typename E, int NB>
 struct Lane {
     static constexpr int NV = NB * kBatch;
