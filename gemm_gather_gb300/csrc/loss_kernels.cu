@@ -188,9 +188,16 @@ struct Slice {
     __device__ __forceinline__ Slice(const LossArgs &a, int rank, int parts)
     {
         constexpr int VEC = Elem<E>::kVec;
-        const int64_t units = (a.V + VEC - 1) / VEC;
-        lo = (int)(units * rank / parts * VEC);
-        hi = (int)gg_min64(units * (rank + 1) / parts * VEC, a.V);
+        const uint32_t units = ((uint32_t)a.V + VEC - 1) / VEC;
+        uint32_t each = units, more = 0;  // the first `more` have one unit more
+        if (parts > 1) {
+            each = units / (uint32_t)parts;
+            more = units - each * (uint32_t)parts;
+        }
+        const uint32_t r = (uint32_t)rank, from = each * r + (r < more ? r : more);
+        const uint32_t to = (from + each + (r < more ? 1u : 0u)) * VEC;
+        lo = (int)(from * VEC);
+        hi = to < (uint32_t)a.V ? (int)to : (int)a.V;
     }
     __device__ __forceinline__ void at(const LossArgs &a, int64_t t)
     {
