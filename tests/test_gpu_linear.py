@@ -374,3 +374,52 @@ def test_a_wait_that_runs_out_is_reported(path):
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     assert torch.equal(y, (x.double() @ w.double()).to(dtype))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("M,N,K", [(777, 40, 48), (64, 104, 200), (2048, 240, 248)])
+def test_each_reads_what_the_one_before_wrote(M, N, K, graph):
+    """Launches that may start under the ones before them: every operand of a call was written by the
+    call just before it, and the buffers are overwritten right after the last.  Integers: exact."""
+    import gemm_gather_gb300 as gg
+    gen = gg_inputs.generator(M + N)
+
+    def ints(r, c):
+        return torch.randint(-1, 2, (r, c), generator=gen).to(BF16).cuda()
+
+    dz, x, w, w2 = ints(M, N), ints(M, K), ints(K, N), ints(K, 64)
+    dx, dw = (torch.full(s, 99.0, dtype=BF16, device="cuda") for s in ((M, K), (K, N)))
+    db, y, y2 = (torch.empty(s, dtype=BF16, device="cuda") for s in ((N,), (M, 64), (M, N)))
+    db2 = torch.empty(N, device="cuda")
+
+    def calls():
+        gg.linear_backward(dz, N, x, K, w, N, "kn", None, 0, "none", dx, K, dw, N, db, BF16, False, M, N, K, BF16)
+        gg.linear(dx, K, w2, 64, "kn", None, "none", None, 0, y, 64, None, 0, M, 64, K, BF16)
+        gg.linear(x, K, dw, N, "kn", db, "none", None, 0, y2, N, None, 0, M, N, K, BF16)
+        gg.linear_backward(y2, N, None, 0, None, 0, "kn", None, 0, "none", None, 0, None, 0, db2, F32, False, M, N, K,
+                           BF16)
+        dx.fill_(99.0)
+        dw.fill_(99.0)
+
+    if graph:
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            calls()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            calls()
+        for out in (y, y2, db, db2):
+            out.zero_()
+        for _ in range(3):
+            g.replay()
+    else:
+        calls()
+    want_dx, want_dw = (dz.double() @ w.double().t()).to(BF16), (x.double().t() @ dz.double()).to(BF16)
+    want_db = dz.double().sum(0).to(BF16)
+    assert torch.equal(db, want_db)
+    assert torch.equal(y, (want_dx.double() @ w2.double()).to(BF16))
+    want_y2 = (x.double() @ want_dw.double() + want_db.double()).to(BF16)
+    assert torch.equal(y2, want_y2)
+    total = want_y2.double().abs().sum(0)  # of whole numbers; float32 is exact below 2^24
+    assert (((db2.double() - want_y2.double().sum(0)).abs() == 0) | (total >= 2.0 ** 24)).all()
