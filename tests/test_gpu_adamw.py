@@ -256,3 +256,20 @@ def test_zero_gradients_and_graph():
     torch.cuda.synchronize()
     for k in ("param", "m", "v", "m_scale", "v_scale", "copy"):
         assert torch.equal(a[k], b[k])
+
+
+@pytest.mark.parametrize("param,grad,copy", [(F32, BF16, BF16), (BF16, BF16, None), (F32, F32, None)])
+def test_8_bit_states_do_not_depend_on_where_the_tensors_lie(param, grad, copy):
+    """At a 16-byte boundary, 8 and 4 elements behind one (tensors of a flat buffer) and 1 element:
+    the same codes and scales, whichever way the blocks are loaded."""
+    first = None
+    for shift in (0, 8, 4, 1):
+        t = make(70000, param, grad, 8, copy, shift)
+        (p, m, v, upd), before = expected(t, 3), t["param"].clone()
+        run([t], 3, 8)
+        check_params(t, p, upd, before)
+        check_guards(t)
+        assert neighbours_ok(t["m"], t["m_scale"], m) and neighbours_ok(t["v"], t["v_scale"], v.sqrt())
+        got = [t[k].clone() for k in ("m", "v", "m_scale", "v_scale")]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
