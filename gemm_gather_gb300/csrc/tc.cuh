@@ -89,7 +89,9 @@ __device__ __forceinline__ void cluster_sync()
 
 // The same without waiting for this thread's stores to become visible (hundreds of
 // cycles where they went to global memory): every thread of the cluster has got
-// here, and no more.
+// here, and no more.  It does not wait for reads in flight either: before a CTA may
+// leave whose shared memory others read, each value read has to have been used (a
+// store that it goes into, issued before the barrier, is such a use).
 __device__ __forceinline__ void cluster_meet()
 {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"

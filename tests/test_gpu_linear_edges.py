@@ -1,0 +1,45 @@
+"""The linear layer at its edges: tiles that a matrix fills in part, weight gradients on their own.
+
+Integer-valued operands make every product and partial sum an exact float32 integer, so results have
+to be equal bit for bit.
+"""
+import pytest
+import torch
+
+import gg_inputs
+from tests.test_gpu_linear import (BF16, F16, F32, FILL, call_backward, call_linear, mat, out_mat, padding, status_ok,
+                                   weight64)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 2048), (1, 64, 4096), (3, 33, 4000), (16, 129, 1000), (40, 160, 1500),
+                                   (60, 257, 1024)])
+def test_split_tiles_with_warps_past_the_last_feature(M, N, K):
+    """Tiles split between the CTAs of a cluster, of which whole warps have no feature: 20 launches
+    back to back, each with its CTAs leaving while the next starts."""
+    gen = gg_inputs.generator(M + N)
+    x, w = mat(M, K, BF16, gen, ints=True), mat(N, K, BF16, gen, ints=True)
+    ys = [out_mat(M, N, BF16, 3) for _ in range(20)]
+    for y in ys:
+        call_linear(x, w, "nk", None, "none", None, y, None, "split")
+    want = (x.double() @ w.double().t()).to(BF16)
+    for y in ys:
+        assert torch.equal(y, want) and (padding(y) == FILL).all()
+    status_ok()
+
+
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("M,N,K", [(1100, 96, 515), (640, 257, 300), (900, 129, 70), (2048, 256, 512)])
+def test_split_float32_gradients_past_the_last_feature_and_token(M, N, K, layout):
+    """Weight gradients whose tokens are split between CTA pairs, added to what the gradient holds."""
+    gen = gg_inputs.generator(M + N + K)
+    dz, x = mat(M, N, F16, gen, ints=True), mat(M, K, F16, gen, ints=True)
+    dw = out_mat(*((K, N) if layout == "kn" else (N, K)), F32, 1)
+    dw.zero_()
+    for _ in range(20):
+        call_backward(dz, x, x, layout, None, "none", None, dw, None, True, "pair")
+    g = x.double().t() @ dz.double()
+    assert torch.equal(dw.double(), 20 * (g if layout == "kn" else g.t()))
+    assert (padding(dw) == FILL).all()
+    status_ok()
