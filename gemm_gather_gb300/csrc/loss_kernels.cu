@@ -35,6 +35,7 @@ namespace {
 constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kInvalidArg = GG_ERR_INVALID_ARG;
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
 // An element type: elements of a 16-byte vector, and pairs of them in (a pair of)
 // its four words.
@@ -623,6 +624,9 @@ __global__ void __launch_bounds__(NB == 4 ? 896 : 512) policy_loss_kernel(const 
                 if (!__all_sync(~0u, tc::bounded_wait(bar, phase, a.wait_limit_ns))) {
                     if (lane == 0)
                         report_status(a.status, kStatusTimeout);
+                    // Messages that are only late still come: they have to find this CTA.  Later
+                    // rows' cannot be missed: their senders wait as long for this warp's.
+                    ptx::mbar_wait(bar, phase, kDrainLimitNs);
                     break;
                 }
                 all = Sum{-INFINITY, 0.0f};
