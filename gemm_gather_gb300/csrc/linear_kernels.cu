@@ -966,9 +966,11 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
                     ptx::mbar_wait(ptx::smem_addr(&sh.full[idx % G::kStages]),
                                    (uint32_t)((idx / G::kStages) & 1), kDrainLimitNs);
                 }
-            } else if (!ok && at.issued > 0) {
-                sleep_ns(200000);  // its loads complete on the leader's barriers: let them land
             }
+            // The other CTA's loads complete on the leader's barriers, and where either gave up
+            // the leader need not have armed them, nor waited for them: let them land.
+            if (!ok)
+                sleep_ns(200000);
         }
     } else if (warp == 1) {
         // ===================== MMA issuer (one thread of the leader CTA) ====
