@@ -4,7 +4,8 @@ the operators of the training or serving step around it: a linear layer with
 its gradients, a clipped policy loss, AdamW.
 
 Thin Python binding of the C ABI in include/gemm_gather.h (same names, minus
-the ``gg_`` prefix).  It only marshals arguments: torch tensors become device
+the ``gg_`` prefix).  It only marshals arguments (the operators also look at a
+tensor's type, size and device before they hand out its address): torch tensors become device
 pointers, the current torch stream becomes the launch stream.  Every step of
 the data path runs in the library's CUDA kernels; there is no fallback.
 """
@@ -14,6 +15,7 @@ import ctypes
 from dataclasses import dataclass
 
 import torch
+from torch import Tensor
 
 from ._lib import (GG_AG_AUTO, GG_AG_BULK, GG_AG_TMA, GG_AG_VECTOR, GG_BF16, GG_MAG_1SM, GG_MAG_2SM,
                    GG_MAG_AUTO, GG_COLL_ALL_GATHER, GG_COLL_ALL_GATHER_PARTITIONED,
@@ -259,23 +261,75 @@ def matmul_all_gather_plan(heap: Heap, rank: int, A, lda: int, B, ldb: int, outp
 # --------------------------------------------------------------------------- #
 
 _LINEAR_NAMES = {0: "none", GG_LINEAR_SPLIT: "split", GG_LINEAR_PAIR: "pair"}
+_TORCH_DTYPES = {code: dtype for dtype, code in DTYPE_CODES.items()}
+_F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
+_SIZES = {torch.float16: 2, torch.bfloat16: 2, torch.float32: 4, torch.int64: 8, torch.int32: 4}
 
 
-def _bias_dtype(bias, bias_dtype, dtype) -> int:
-    if bias_dtype is None and isinstance(bias, torch.Tensor):
-        bias_dtype = bias.dtype
-    return _dtype(dtype if bias_dtype is None else bias_dtype)
+def _held(x, name: str, dtype, rows: int, cols: int, ld: int) -> int | None:
+    """Address of a matrix of rows x cols elements at a pitch of ld.  Of an address nothing is known;
+    a tensor has to be of the type (a torch dtype, or None where the library refuses the code), hold
+    all of them from its first element on, and be on the GPU.  (The first lines are the common case:
+    these checks are on the way of every call.)"""
+    if x.__class__ is Tensor and x.dtype is dtype and x.is_cuda and (
+            x.untyped_storage().nbytes() >= (x.storage_offset() + (rows - 1) * ld + cols) * _SIZES[dtype]):
+        return x.data_ptr()
+    return _looked_at(x, name, dtype, (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0)
+
+
+def _vector(x, name: str, dtype, n: int) -> int | None:
+    """Address of n elements in a row; a tensor has to be contiguous, and the rest as for a matrix."""
+    if x.__class__ is Tensor and x.dtype is dtype and x.is_cuda and x.numel() >= n and x.is_contiguous():
+        return x.data_ptr()
+    if isinstance(x, Tensor) and not x.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is needed")
+    return _looked_at(x, name, dtype, n)
+
+
+def _looked_at(x, name: str, dtype, need: int) -> int | None:
+    if x is None:
+        return None
+    if not isinstance(x, Tensor):
+        return int(x)
+    if x.dtype is not dtype and dtype is not None:
+        raise ValueError(f"{name}: a tensor of {dtype} is needed, not of {x.dtype}")
+    if need > 0 and x.untyped_storage().nbytes() < (x.storage_offset() + need) * x.element_size():
+        raise ValueError(f"{name}: {need} elements are needed from the tensor's first on")
+    if not x.is_cuda:
+        raise ValueError(f"{name}: a tensor on the GPU is needed")
+    return x.data_ptr()
+
+
+def _word(status) -> int | None:
+    return None if status is None else _vector(status, "status", _I32, 1)
+
+
+def _linear_args(X, ldx, W, ldw, layout, bias, act, residual, ldr, Y, ldy, z, ldz, M, N, K, dtype,
+                 bias_dtype) -> tuple:
+    code = _dtype(dtype)
+    t = _TORCH_DTYPES.get(code)
+    if bias_dtype is not None:
+        bias_code = _dtype(bias_dtype)
+    else:
+        bias_code = DTYPE_CODES.get(bias.dtype, -1) if isinstance(bias, Tensor) else code
+    k = K if M > 0 and N > 0 else 0
+    w_rows, w_cols = (k, N) if layout == "kn" else (N, k)
+    return (_held(X, "X", t, M, k, ldx), ldx, _held(W, "W", t, w_rows, w_cols, ldw), ldw,
+            WEIGHT_LAYOUTS[layout],
+            _vector(bias, "bias", _TORCH_DTYPES.get(bias_code), N if M > 0 else 0), bias_code,
+            ACTIVATIONS[act], _held(residual, "residual", t, M, N, ldr), ldr,
+            _held(Y, "Y", t, M, N, ldy), ldy, _held(z, "z", t, M, N, ldz), ldz, M, N, K, code)
 
 
 def linear(X, ldx: int, W, ldw: int, layout: str, bias, act: str, residual, ldr: int, Y, ldy: int,
            z, ldz: int, M: int, N: int, K: int, dtype, status=None, stream=None, path: str = "auto",
            bias_dtype=None) -> None:
     """Y = act(X W + bias) + residual; z (or None) receives X W + bias (gg_linear).
-    ``bias_dtype`` is taken from a bias tensor, else ``dtype``."""
-    check(lib.gg_linear(_ptr(X), ldx, _ptr(W), ldw, WEIGHT_LAYOUTS[layout], _ptr(bias),
-                        _bias_dtype(bias, bias_dtype, dtype), ACTIVATIONS[act], _ptr(residual), ldr,
-                        _ptr(Y), ldy, _ptr(z), ldz, M, N, K, _dtype(dtype), _ptr(status),
-                        _stream(stream), LINEAR_PATHS[path]))
+    ``bias_dtype`` is taken from a bias tensor, else ``dtype``.  Matrices are device addresses or
+    tensors; a tensor of another type, too small or not on the GPU raises ValueError."""
+    check(lib.gg_linear(*_linear_args(X, ldx, W, ldw, layout, bias, act, residual, ldr, Y, ldy, z, ldz,
+                                      M, N, K, dtype, bias_dtype),
+                        _word(status), _stream(stream), LINEAR_PATHS[path]))
 
 
 def linear_check(X, ldx: int, W, ldw: int, layout: str, bias, act: str, residual, ldr: int, Y,
@@ -284,11 +338,28 @@ def linear_check(X, ldx: int, W, ldw: int, layout: str, bias, act: str, residual
     """Validate without launching; returns the kernel a launch would run
     ("split" or "pair"; "none" when no product runs)."""
     chosen = ctypes.c_int()
-    check(lib.gg_linear_check(_ptr(X), ldx, _ptr(W), ldw, WEIGHT_LAYOUTS[layout], _ptr(bias),
-                              _bias_dtype(bias, bias_dtype, dtype), ACTIVATIONS[act],
-                              _ptr(residual), ldr, _ptr(Y), ldy, _ptr(z), ldz, M, N, K,
-                              _dtype(dtype), LINEAR_PATHS[path], ctypes.byref(chosen)))
+    check(lib.gg_linear_check(*_linear_args(X, ldx, W, ldw, layout, bias, act, residual, ldr, Y, ldy, z,
+                                            ldz, M, N, K, dtype, bias_dtype),
+                              LINEAR_PATHS[path], ctypes.byref(chosen)))
     return _LINEAR_NAMES[chosen.value]
+
+
+def _backward_args(dZ, lddz, X, ldx, W, ldw, layout, z_in, ldzin, act_in, dX, lddx, dW, lddw, dbias,
+                   grad_dtype, accumulate, M, N, K, dtype) -> tuple:
+    code, grad = _dtype(dtype), _dtype(grad_dtype)
+    t, g = _TORCH_DTYPES.get(code), _TORCH_DTYPES.get(grad)
+    kn = layout == "kn"
+    # X is read for dW only, W and z_in for dX only
+    no_dx, no_dw = dX is None, dW is None
+    read = M if not (no_dx and no_dw and dbias is None) else 0
+    w_rows, w_cols = (K, N) if kn else (N, K)
+    return (_held(dZ, "dZ", t, read, N, lddz), lddz,
+            _ptr(X) if no_dw else _held(X, "X", t, M if N > 0 else 0, K, ldx), ldx,
+            _ptr(W) if no_dx else _held(W, "W", t, w_rows if M > 0 else 0, w_cols, ldw), ldw,
+            WEIGHT_LAYOUTS[layout], _ptr(z_in) if no_dx else _held(z_in, "z_in", t, M, K, ldzin), ldzin,
+            ACTIVATIONS[act_in], _held(dX, "dX", t, M, K, lddx), lddx,
+            _held(dW, "dW", g, w_rows, w_cols, lddw), lddw, _vector(dbias, "dbias", g, N), grad,
+            1 if accumulate else 0, M, N, K, code)
 
 
 def linear_backward(dZ, lddz: int, X, ldx: int, W, ldw: int, layout: str, z_in, ldzin: int,
@@ -296,11 +367,12 @@ def linear_backward(dZ, lddz: int, X, ldx: int, W, ldw: int, layout: str, z_in, 
                     M: int, N: int, K: int, dtype, status=None, stream=None,
                     path: str = "auto") -> None:
     """dX = (dZ W^T) act_in'(z_in), dW (+)= X^T dZ, dbias (+)= column sums of dZ
-    (gg_linear_backward); any of the three outputs may be None."""
-    check(lib.gg_linear_backward(_ptr(dZ), lddz, _ptr(X), ldx, _ptr(W), ldw, WEIGHT_LAYOUTS[layout],
-                                 _ptr(z_in), ldzin, ACTIVATIONS[act_in], _ptr(dX), lddx, _ptr(dW),
-                                 lddw, _ptr(dbias), _dtype(grad_dtype), 1 if accumulate else 0, M, N,
-                                 K, _dtype(dtype), _ptr(status), _stream(stream), LINEAR_PATHS[path]))
+    (gg_linear_backward); any of the three outputs may be None.  Tensors are checked as for
+    ``linear``, as far as they are read or written."""
+    check(lib.gg_linear_backward(*_backward_args(dZ, lddz, X, ldx, W, ldw, layout, z_in, ldzin, act_in,
+                                                 dX, lddx, dW, lddw, dbias, grad_dtype, accumulate, M, N,
+                                                 K, dtype),
+                                 _word(status), _stream(stream), LINEAR_PATHS[path]))
 
 
 def linear_backward_check(dZ, lddz: int, X, ldx: int, W, ldw: int, layout: str, z_in, ldzin: int,
@@ -309,20 +381,33 @@ def linear_backward_check(dZ, lddz: int, X, ldx: int, W, ldw: int, layout: str, 
                           path: str = "auto") -> tuple[str, str]:
     """Validate without launching; returns the kernels of dX and dW."""
     dx, dw = ctypes.c_int(), ctypes.c_int()
-    check(lib.gg_linear_backward_check(_ptr(dZ), lddz, _ptr(X), ldx, _ptr(W), ldw,
-                                       WEIGHT_LAYOUTS[layout], _ptr(z_in), ldzin,
-                                       ACTIVATIONS[act_in], _ptr(dX), lddx, _ptr(dW), lddw,
-                                       _ptr(dbias), _dtype(grad_dtype), 1 if accumulate else 0, M, N,
-                                       K, _dtype(dtype), LINEAR_PATHS[path], ctypes.byref(dx),
-                                       ctypes.byref(dw)))
+    check(lib.gg_linear_backward_check(*_backward_args(dZ, lddz, X, ldx, W, ldw, layout, z_in, ldzin,
+                                                       act_in, dX, lddx, dW, lddw, dbias, grad_dtype,
+                                                       accumulate, M, N, K, dtype),
+                                       LINEAR_PATHS[path], ctypes.byref(dx), ctypes.byref(dw)))
     return _LINEAR_NAMES[dx.value], _LINEAR_NAMES[dw.value]
 
 
 def act_backward(dy, lddy: int, z, ldz: int, dz, lddz: int, act: str, M: int, N: int, dtype,
                  stream=None) -> None:
-    """dz = dy * act'(z) (gg_act_backward)."""
-    check(lib.gg_act_backward(_ptr(dy), lddy, _ptr(z), ldz, _ptr(dz), lddz, ACTIVATIONS[act], M, N,
-                              _dtype(dtype), _stream(stream)))
+    """dz = dy * act'(z) (gg_act_backward).  Tensors are checked as for ``linear``."""
+    code = _dtype(dtype)
+    t = _TORCH_DTYPES.get(code)
+    check(lib.gg_act_backward(_held(dy, "dy", t, M, N, lddy), lddy, _held(z, "z", t, M, N, ldz), ldz,
+                              _held(dz, "dz", t, M, N, lddz), lddz, ACTIVATIONS[act], M, N, code,
+                              _stream(stream)))
+
+
+def _loss_args(logits, ld, target, old_logp, ref_logp, advantage, weight, T, V, dtype, stats, logp_out,
+               dlogits, ldd, inv_temperature, clip_low, clip_high, kl_coef, grad_scale) -> tuple:
+    code = _dtype(dtype)
+    t, f = _TORCH_DTYPES.get(code), _F32
+    return (_held(logits, "logits", t, T, V, ld), ld, _vector(target, "target", _I64, T),
+            _vector(old_logp, "old_logp", f, T), _vector(ref_logp, "ref_logp", f, T),
+            _vector(advantage, "advantage", f, T), _vector(weight, "weight", f, T), T, V, code,
+            inv_temperature, clip_low, clip_high, kl_coef, grad_scale,
+            _vector(stats, "stats", f, 4), _vector(logp_out, "logp_out", f, T),
+            _held(dlogits, "dlogits", t, T, V, ldd), ldd)
 
 
 def policy_loss(logits, ld: int, target, old_logp, ref_logp, advantage, weight, T: int, V: int, dtype,
@@ -330,11 +415,13 @@ def policy_loss(logits, ld: int, target, old_logp, ref_logp, advantage, weight, 
                 clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                 grad_scale: float = 1.0, status=None, stream=None) -> None:
     """Clipped policy loss with a KL term, its statistics and the logits'
-    gradient (gg_policy_loss); dlogits may be the logits themselves, or None."""
-    check(lib.gg_policy_loss(_ptr(logits), ld, _ptr(target), _ptr(old_logp), _ptr(ref_logp),
-                             _ptr(advantage), _ptr(weight), T, V, _dtype(dtype), inv_temperature,
-                             clip_low, clip_high, kl_coef, grad_scale, _ptr(stats), _ptr(logp_out),
-                             _ptr(dlogits), ldd, _ptr(status), _stream(stream)))
+    gradient (gg_policy_loss); dlogits may be the logits themselves, or None.
+    Tensors are checked as for ``linear``: targets are int64, what a token
+    brings else float32."""
+    check(lib.gg_policy_loss(*_loss_args(logits, ld, target, old_logp, ref_logp, advantage, weight, T, V,
+                                         dtype, stats, logp_out, dlogits, ldd, inv_temperature, clip_low,
+                                         clip_high, kl_coef, grad_scale),
+                             _word(status), _stream(stream)))
 
 
 def policy_loss_check(logits, ld: int, target, old_logp, ref_logp, advantage, weight, T: int, V: int,
@@ -342,18 +429,22 @@ def policy_loss_check(logits, ld: int, target, old_logp, ref_logp, advantage, we
                       clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                       grad_scale: float = 1.0) -> None:
     """Validate without launching."""
-    check(lib.gg_policy_loss_check(_ptr(logits), ld, _ptr(target), _ptr(old_logp), _ptr(ref_logp),
-                                   _ptr(advantage), _ptr(weight), T, V, _dtype(dtype),
-                                   inv_temperature, clip_low, clip_high, kl_coef, grad_scale,
-                                   _ptr(stats), _ptr(logp_out), _ptr(dlogits), ldd))
+    check(lib.gg_policy_loss_check(*_loss_args(logits, ld, target, old_logp, ref_logp, advantage, weight,
+                                               T, V, dtype, stats, logp_out, dlogits, ldd,
+                                               inv_temperature, clip_low, clip_high, kl_coef,
+                                               grad_scale)))
 
 
 class AdamwTensors:
     """The tensors of an AdamW step, described once for all steps (host memory
     only): a ctypes array of ``gg_adamw_tensor``.  Holds on to the tensors."""
 
-    def __init__(self, array, keep):
+    def __init__(self, array, keep, elsewhere=None):
         self.array, self.count, self.keep = array, len(array), keep
+        self.elsewhere = elsewhere      # the first tensor that is not on the GPU, by name
+
+
+_STATE_DTYPES = {32: (torch.float32,), 8: (torch.uint8, torch.float8_e4m3fn)}
 
 
 def adamw_tensors(tensors, state_bits: int = 32) -> AdamwTensors:
@@ -362,10 +453,12 @@ def adamw_tensors(tensors, state_bits: int = 32) -> AdamwTensors:
     "v_scale" (8-bit states) and "copy".  8-bit states are uint8 or
     float8_e4m3fn tensors with a float32 scale per ADAMW_BLOCK elements."""
     array = (AdamwTensor * len(tensors))()
-    for a, t in zip(array, tensors):
+    elsewhere = None
+    types = {"m_scale": (torch.float32,), "v_scale": (torch.float32,)}
+    types["m"] = types["v"] = _STATE_DTYPES.get(state_bits)
+    for i, (a, t) in enumerate(zip(array, tensors)):
         n = t["param"].numel()
         a.n, a.state_bits = n, state_bits
-        a.param_dtype, a.grad_dtype = _dtype(t["param"].dtype), _dtype(t["grad"].dtype)
         for k in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy"):
             x = t.get(k)
             if x is None:
@@ -373,13 +466,21 @@ def adamw_tensors(tensors, state_bits: int = 32) -> AdamwTensors:
             want = -(-n // ADAMW_BLOCK) if k.endswith("_scale") else n
             if not x.is_contiguous() or x.numel() != want:
                 raise ValueError(f"{k}: a contiguous tensor of {want} elements is needed")
-            size = {"m": state_bits // 8, "v": state_bits // 8}.get(k, 4 if k.endswith("_scale") else None)
-            if size is not None and x.element_size() != size:
-                raise ValueError(f"{k}: elements of {size} bytes are needed")
+            if types.get(k, DTYPE_CODES) and x.dtype not in types.get(k, DTYPE_CODES):
+                raise ValueError(f"{k}: a tensor of {x.dtype} does not do")
+            if not x.is_cuda:
+                elsewhere = elsewhere or f"{k} of tensor {i}"
             setattr(a, k, _ptr(x))
+        a.param_dtype, a.grad_dtype = _dtype(t["param"].dtype), _dtype(t["grad"].dtype)
         if t.get("copy") is not None:
             a.copy_dtype = _dtype(t["copy"].dtype)
-    return AdamwTensors(array, list(tensors))
+    return AdamwTensors(array, list(tensors), elsewhere)
+
+
+def _placed(tensors: AdamwTensors):
+    if tensors.elsewhere is not None:
+        raise ValueError(f"{tensors.elsewhere}: a tensor on the GPU is needed")
+    return tensors.array
 
 
 def adamw(tensors: AdamwTensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
@@ -387,16 +488,17 @@ def adamw(tensors: AdamwTensors, step: int, lr: float, beta1: float = 0.9, beta2
           stream=None) -> None:
     """One AdamW step over all tensors (gg_adamw); ``step`` counts from 1.
     ``grad_scale``: a device float the gradients are multiplied by, or None."""
-    check(lib.gg_adamw(tensors.array, tensors.count, step, lr, beta1, beta2, eps, weight_decay,
-                       _ptr(grad_scale), seed, _stream(stream)))
+    check(lib.gg_adamw(_placed(tensors), tensors.count, step, lr, beta1, beta2, eps, weight_decay,
+                       None if grad_scale is None else _vector(grad_scale, "grad_scale", _F32, 1), seed,
+                       _stream(stream)))
 
 
 def adamw_check(tensors: AdamwTensors, step: int, lr: float, beta1: float = 0.9,
                 beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
                 grad_scale=None) -> None:
     """Validate without launching."""
-    check(lib.gg_adamw_check(tensors.array, tensors.count, step, lr, beta1, beta2, eps, weight_decay,
-                             _ptr(grad_scale)))
+    check(lib.gg_adamw_check(_placed(tensors), tensors.count, step, lr, beta1, beta2, eps, weight_decay,
+                             None if grad_scale is None else _vector(grad_scale, "grad_scale", _F32, 1)))
 
 
 def set_claim_policy(policy: str) -> None:

@@ -82,9 +82,15 @@ class Group(ctypes.Structure):
                 ("world_size", ctypes.c_int)]
 
 
+class Int64:
+    """A 64-bit integer argument, by c_void_p's converter: the same 8 bytes as by c_int64's in half
+    the time (60 against 120 ns), which calls of 20 arguments notice."""
+    from_param = ctypes.c_void_p.from_param
+
+
 def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     vp, i32, i64, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
-    sz, f32, f64 = ctypes.c_size_t, ctypes.c_float, ctypes.c_double
+    sz, f32, f64, n64 = ctypes.c_size_t, ctypes.c_float, ctypes.c_double, Int64
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "gg_heap_create": ([vp, sz, i32, vp, vp, pp], i32),
@@ -117,20 +123,20 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
                                         Tile, i32, Group], i32),
         "gg_matmul_all_gather_plan": ([vp, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32,
                                        Tile, i32, Group, i32, ctypes.POINTER(i32)], i32),
-        "gg_linear": ([vp, i64, vp, i64, i32, vp, i32, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+        "gg_linear": ([vp, n64, vp, n64, i32, vp, i32, i32, vp, n64, vp, n64, vp, n64, n64, n64, n64,
                        i32, vp, vp, i32], i32),
-        "gg_linear_check": ([vp, i64, vp, i64, i32, vp, i32, i32, vp, i64, vp, i64, vp, i64, i64, i64,
-                             i64, i32, i32, ctypes.POINTER(i32)], i32),
-        "gg_linear_backward": ([vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp, i32,
-                                i32, i64, i64, i64, i32, vp, vp, i32], i32),
-        "gg_linear_backward_check": ([vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp,
-                                      i32, i32, i64, i64, i64, i32, i32, ctypes.POINTER(i32),
+        "gg_linear_check": ([vp, n64, vp, n64, i32, vp, i32, i32, vp, n64, vp, n64, vp, n64, n64, n64,
+                             n64, i32, i32, ctypes.POINTER(i32)], i32),
+        "gg_linear_backward": ([vp, n64, vp, n64, vp, n64, i32, vp, n64, i32, vp, n64, vp, n64, vp, i32,
+                                i32, n64, n64, n64, i32, vp, vp, i32], i32),
+        "gg_linear_backward_check": ([vp, n64, vp, n64, vp, n64, i32, vp, n64, i32, vp, n64, vp, n64, vp,
+                                      i32, i32, n64, n64, n64, i32, i32, ctypes.POINTER(i32),
                                       ctypes.POINTER(i32)], i32),
-        "gg_act_backward": ([vp, i64, vp, i64, vp, i64, i32, i64, i64, i32, vp], i32),
-        "gg_policy_loss": ([vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, f32, f32, f32, f32, f32, vp, vp,
-                            vp, i64, vp, vp], i32),
-        "gg_policy_loss_check": ([vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, f32, f32, f32, f32, f32,
-                                  vp, vp, vp, i64], i32),
+        "gg_act_backward": ([vp, n64, vp, n64, vp, n64, i32, n64, n64, i32, vp], i32),
+        "gg_policy_loss": ([vp, n64, vp, vp, vp, vp, vp, n64, n64, i32, f32, f32, f32, f32, f32, vp, vp,
+                            vp, n64, vp, vp], i32),
+        "gg_policy_loss_check": ([vp, n64, vp, vp, vp, vp, vp, n64, n64, i32, f32, f32, f32, f32, f32,
+                                  vp, vp, vp, n64], i32),
         "gg_adamw": ([vp, i32, i64, f64, f64, f64, f64, f64, vp, u64, vp], i32),
         "gg_adamw_check": ([vp, i32, i64, f64, f64, f64, f64, f64, vp], i32),
         "gg_set_claim_policy": ([i32], i32),
