@@ -1698,19 +1698,16 @@ static double pair_kb_ns(int bt, bool lines, double ctas)
 // Launch, set-up and first load of a pair, and its epilogue.
 static double pair_ns(int bt) { return 1724.0 + 23.2 * bt; }
 
-// Whether the operands' rows start on 128-byte lines.  Where they do not, each row
-// of a tile touches two lines: with pitches of 1008 and 1024 elements, 768 tokens,
-// 1536 features and K = 1000 take 8.6 and 6.4 us.
-static bool on_lines(const LinearArgs &a)
-{
-    return ((reinterpret_cast<uint64_t>(a.a) | reinterpret_cast<uint64_t>(a.b) | (uint64_t)(a.lda * 2) |
-             (uint64_t)(a.ldb * 2)) & 127) == 0;
-}
+// Whether the operands' pitches keep their rows on 128-byte lines.  Where they do not,
+// each row of a tile touches two lines: with pitches of 1008 and 1024 elements, 768
+// tokens, 1536 features and K = 1000 take 8.6 and 6.4 us.  The addresses stay out of it:
+// the same values elsewhere have to be summed in the same order.
+static bool on_lines(const LinearArgs &a) { return ((a.lda | a.ldb) * 2 & 127) == 0; }
 
 // Which kernel, tile and split: the one of least estimated time, in nanoseconds.
 // The estimate is a launch and its set-up, then waves x k-blocks x the time of a
 // k-block, then the epilogue.  Its constants were fitted to 2300 timings of both
-// kernels (weights of 512 x 512 to 8192 x 3584, 1 to 4096 tokens, rows on and off
+// kernels (weights of 512 x 512 to 8192 x 3584, 1 to 4096 tokens, pitches on and off
 // 128-byte lines, every tile and split, forward and both gradients): the choice is
 // on average 1.4 % slower than the best of them, 15 % at most.
 LinearPlan plan_linear(int epi, const LinearArgs &a, int path)

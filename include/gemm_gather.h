@@ -421,7 +421,10 @@ gg_status gg_matmul_all_gather_check(const gg_heap *heap, int rank, const void *
  *
  * All of them run on the current device, asynchronously on `stream`; they
  * allocate nothing, keep nothing between calls and give the same bits for the
- * same inputs.  Matrices are row-major with a row pitch (ld) in elements.
+ * same inputs, sizes, pitches and path, wherever these lie in memory (the policy
+ * loss: wherever the logits lie at the same offset from a 16-byte boundary, at
+ * which it starts its vectors).  Matrices are row-major with a row pitch (ld) in
+ * elements.
  * Sums and statistics are held in float32.  Sizes must be below 2^31 each;
  * offsets are 64-bit.  An output may overlap no other argument's elements,
  * unless a call says so (GG_ERR_INVALID_ARG); columns between a row's length

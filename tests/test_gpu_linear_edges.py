@@ -43,3 +43,29 @@ def test_split_float32_gradients_past_the_last_feature_and_token(M, N, K, layout
     assert torch.equal(dw.double(), 20 * (g if layout == "kn" else g.t()))
     assert (padding(dw) == FILL).all()
     status_ok()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (27, 3584, 512), (300, 1024, 1024), (700, 640, 2048)])
+def test_same_bits_wherever_the_operands_lie(M, N, K):
+    """The same matrices 16 and 112 bytes behind a 128-byte line: equal sums, bit for bit, of values whose
+    sum depends on its order."""
+    gen = gg_inputs.generator(M)
+
+    def copies(t):
+        out = []
+        for shift in (0, 8, 56):
+            buf = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+            assert buf.data_ptr() % 128 == 0
+            out.append(buf[shift:shift + t.numel()].view(t.shape).copy_(t))
+        return out
+
+    xs, ws, dzs = copies(mat(M, K, F16, gen)), copies(mat(N, K, F16, gen)), copies(mat(M, N, F16, gen))
+    got = []
+    for x, w, dz in zip(xs, ws, dzs):
+        y, dx, dw, db = out_mat(M, N, F16), out_mat(M, K, F16), out_mat(N, K, F32), torch.zeros(N, device="cuda")
+        call_linear(x, w, "nk", None, "none", None, y, None)
+        call_backward(dz, x, w, "nk", None, "none", dx, dw, db, False)
+        got.append((y, dx, dw, db))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    status_ok()

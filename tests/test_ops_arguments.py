@@ -82,3 +82,18 @@ def test_adamw():
             gg.adamw_tensors([{**t, **bad}], state_bits=bits)
     with pytest.raises(ValueError, match="grad_scale: a tensor of torch.float32"):
         gg.adamw_check(gg.adamw_tensors([]), 1, 1e-3, grad_scale=zeros(1, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("M", [1, 16, 27, 100, 300, 777, 2048])
+def test_the_kernel_does_not_depend_on_addresses(M):
+    """Where operands lie may not change the order of their sums."""
+    for N in (512, 1024, 3584, 8192):
+        for K in (512, 1000, 2048, 4096):
+            def chosen(shift):
+                a = dict(X=A + shift, ldx=K, W=A + (1 << 34) + shift, ldw=K, layout="nk", bias=None, act="none",
+                         residual=None, ldr=N, Y=A + (2 << 34), ldy=N, z=None, ldz=N, M=M, N=N, K=K, dtype=BF16)
+                b = dict(dZ=A + shift, lddz=N, X=A + (1 << 34) + shift, ldx=K, W=A + (2 << 34) + shift, ldw=K,
+                         layout="nk", z_in=None, ldzin=K, act="none", dX=A + (3 << 34), lddx=K, dW=A + (4 << 34), lddw=K,
+                         db=None, gdt=F32, acc=False, M=M, N=N, K=K, dtype=BF16)
+                return gg.linear_check(*a.values()), gg.linear_backward_check(*b.values())
+            assert chosen(0) == chosen(16) == chosen(112)
