@@ -108,11 +108,15 @@ __device__ __forceinline__ void store16(void *p, int64_t at, float v, int bf16)
 // Activations in float32, on pairs (two neighbouring tokens of a feature) where
 // the arithmetic comes in pairs.  relu keeps NaN.  gelu_tanh's 0.5 (1 + tanh u) is
 // the logistic function of 2u, which keeps its relative precision for u << 0.
-// gelu's normal distribution function comes from Abramowitz and Stegun's 7.1.26,
-//     Phi(-x) = P(t) exp(-x^2 / 2) / 2,  t = 1 / (1 + p x / sqrt 2),  x >= 0,
-// within 7.5e-8 of Phi, a hundredth of a 16-bit result's rounding; its exponential
-// is also the density that the derivative needs.  (With erff and a float division,
-// the epilogue of a 256 x 256 tile took longer than its MMAs at K = 3584.)
+// gelu's normal distribution function has Abramowitz and Stegun's form (7.1.26),
+//     Phi(-x) = P(t) exp(-x^2 / 2),  t = 1 / (1 + 0.35 x),  x >= 0,
+// P of degree 7 without a constant, fitted here for the least relative error (a linear
+// program over 3000 points of [0, 13.5]): 1.5e-7 (1 + x^2 / 4), and 5e-7 at x < 1, 1.7e-6
+// at 6 as evaluated.  So Y = max(z, 0) - |z| Phi(-|z|) is as near in the left tail, where
+// it is tiny, as the power of two itself.  (7.1.26's own coefficients are within 7.5e-8 of
+// Phi, which at z = -4 is a float16's half ulp of Y and at -7 more than a bfloat16's ulp.)
+// The exponential is also the density that the derivative needs.  (With erff and a float
+// division, the epilogue of a 256 x 256 tile took longer than its MMAs at K = 3584.)
 __device__ __forceinline__ float ex2_approx(float x)
 {
     float y;
@@ -141,20 +145,20 @@ __device__ __forceinline__ F2 gelu_2u(F2 z, F2 zz)
     return mul2(z, fma2(zz, pair_of(0.071354816f), pair_of(1.59576912f)));
 }
 
-// Phi(z), and exp(-z^2 / 2) in *e.
-__device__ __forceinline__ float2 normal_cdf(F2 z, F2 zz, float2 *e)
+// Phi(-|z|), and exp(-z^2 / 2) in *e.
+__device__ __forceinline__ F2 normal_tail(float2 z, F2 zz, float2 *e)
 {
     const float2 y = halves_of(mul2(zz, pair_of(-0.72134752f)));
     *e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-    const float2 v = halves_of(z);
-    const float2 d = halves_of(fma2(pair_of(fabsf(v.x), fabsf(v.y)), pair_of(0.23164189f), pair_of(1.0f)));
+    const float2 d = halves_of(fma2(pair_of(fabsf(z.x), fabsf(z.y)), pair_of(0.35f), pair_of(1.0f)));
     const F2 t = pair_of(rcp_approx(d.x), rcp_approx(d.y));
-    F2 q = fma2(t, pair_of(0.5f * 1.061405429f), pair_of(0.5f * -1.453152027f));
-    q = fma2(t, q, pair_of(0.5f * 1.421413741f));
-    q = fma2(t, q, pair_of(0.5f * -0.284496736f));
-    q = fma2(t, q, pair_of(0.5f * 0.254829592f));
-    const float2 tail = halves_of(mul2(mul2(t, q), pair_of(e->x, e->y)));  // Phi(-|z|)
-    return make_float2(v.x < 0.0f ? tail.x : 1.0f - tail.x, v.y < 0.0f ? tail.y : 1.0f - tail.y);
+    F2 q = fma2(t, pair_of(0.0462695388f), pair_of(-0.190911355f));
+    q = fma2(t, q, pair_of(0.221250296f));
+    q = fma2(t, q, pair_of(0.00082826442f));
+    q = fma2(t, q, pair_of(0.146570468f));
+    q = fma2(t, q, pair_of(0.136159971f));
+    q = fma2(t, q, pair_of(0.139832881f));
+    return mul2(mul2(t, q), pair_of(e->x, e->y));
 }
 
 template <int ACT>
@@ -164,9 +168,12 @@ __device__ __forceinline__ float2 act_value(float2 v)
     if constexpr (ACT == GG_ACT_RELU)
         return make_float2(!(v.x <= 0.0f) ? v.x : 0.0f, !(v.y <= 0.0f) ? v.y : 0.0f);
     if constexpr (ACT == GG_ACT_GELU) {
+        // max(z, 0) - |z| Phi(-|z|), |z| held below 64, where the product is long 0; NaN is in
+        // the tail
         float2 e;
-        const float2 c = normal_cdf(z, mul2(z, z), &e);
-        return halves_of(mul2(z, pair_of(c.x, c.y)));
+        const F2 tail = normal_tail(v, mul2(z, z), &e);
+        const F2 size = pair_of(-fminf(fabsf(v.x), 64.0f), -fminf(fabsf(v.y), 64.0f));
+        return halves_of(fma2(size, tail, pair_of(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f))));
     }
     if constexpr (ACT == GG_ACT_GELU_TANH || ACT == GG_ACT_SILU) {
         const float2 s = logistic(ACT == GG_ACT_SILU ? z : gelu_2u(z, mul2(z, z)));
@@ -183,7 +190,8 @@ __device__ __forceinline__ float2 act_slope(float2 v)
         return make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
     if constexpr (ACT == GG_ACT_GELU) {  // Phi + z density
         float2 e;
-        const float2 c = normal_cdf(z, mul2(z, z), &e);
+        const float2 tail = halves_of(normal_tail(v, mul2(z, z), &e));
+        const float2 c = make_float2(v.x < 0.0f ? tail.x : 1.0f - tail.x, v.y < 0.0f ? tail.y : 1.0f - tail.y);
         return halves_of(fma2(mul2(z, pair_of(0.39894228f)), pair_of(e.x, e.y), pair_of(c.x, c.y)));
     }
     if constexpr (ACT == GG_ACT_GELU_TANH) {  // d(z s)/dz = s + z s (1 - s) 2u'
