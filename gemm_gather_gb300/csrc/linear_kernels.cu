@@ -106,7 +106,7 @@ __device__ __forceinline__ void store16(void *p, int64_t at, float v, int bf16)
 }
 
 // Activations in float32, on pairs (two neighbouring tokens of a feature) where
-// the arithmetic comes in pairs.  relu keeps NaN.  gelu_tanh's 0.5 (1 + tanh u) is
+// the arithmetic comes in pairs.  relu keeps NaN (its slope there is 0).  gelu_tanh's 0.5 (1 + tanh u) is
 // the logistic function of 2u, which keeps its relative precision for u << 0.
 // gelu's normal distribution function has Abramowitz and Stegun's form (7.1.26),
 //     Phi(-x) = P(t) exp(-x^2 / 2),  t = 1 / (1 + 0.35 x),  x >= 0,
@@ -182,9 +182,22 @@ __device__ __forceinline__ float2 act_value(float2 v)
     return v;
 }
 
+// x between -128 and 128, where every smooth slope is 0 or 1; NaN stays NaN.
+__device__ __forceinline__ float held128(float x)
+{
+    float y;
+    asm("min.NaN.f32 %0, %1, 0f43000000;\n\tmax.NaN.f32 %0, %0, 0fC3000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The derivative at z.  A stored Z may be infinite where the sum was not (16 bits), and the
+// square of a large one is: the smooth slopes see z held between -128 and 128, so that
+// infinity times 0 meets none of them.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope(float2 v)
 {
+    if constexpr (ACT != GG_ACT_RELU && ACT != GG_ACT_NONE)
+        v = make_float2(held128(v.x), held128(v.y));
     const F2 z = pair_of(v.x, v.y);
     if constexpr (ACT == GG_ACT_RELU)
         return make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);

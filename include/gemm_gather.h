@@ -432,7 +432,9 @@ gg_status gg_matmul_all_gather_check(const gg_heap *heap, int rank, const void *
  * ------------------------------------------------------------------------- */
 
 /* Activations: max(z, 0); z Phi(z); z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;
- * z / (1 + exp(-z)). */
+ * z / (1 + exp(-z)).  At z = -inf the last two are NaN (-inf times 0) and the others 0;
+ * NaN gives NaN.  The derivatives are finite for every z but NaN: at an infinite z their
+ * limits, 0 and 1; relu's is 0 at 0 and at NaN. */
 typedef enum {
     GG_ACT_NONE = 0, GG_ACT_RELU = 1, GG_ACT_GELU = 2, GG_ACT_GELU_TANH = 3, GG_ACT_SILU = 4
 } gg_activation;

@@ -71,3 +71,47 @@ def test_slopes_in_the_left_tails(act, dtype):
     _, a, b = terms(z64, act)
     off = (2.0 ** -18 + 2.0 ** -21 * exponent(z64, act)) * (a.abs() + b.abs())  # two terms, one more product
     assert ((dz.double() - (a + b)).abs() <= off + half_ulp((a + b).abs() + off, dtype)).all()
+
+
+ALL = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+@pytest.mark.parametrize("act", ALL)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_beyond_all_bounds(act, dtype):
+    """Large, infinite and NaN Z: slopes are 1 to the right, 0 to the left (none: 1) and NaN at NaN (relu: 0),
+    through the elementwise gradient, the input gradient's epilogue, and for Y itself."""
+    import gemm_gather_gb300 as gg
+    big = torch.finfo(dtype).max
+    z = torch.zeros((64, 64), dtype=dtype, device="cuda")
+    right = torch.tensor([200.0, 3e4, big / 2, big, math.inf], dtype=dtype)
+    if dtype == BF16:
+        right = torch.cat([right, torch.tensor([1e15, 1.9e19, 4e30]).to(dtype)])
+    n = len(right)
+    z[3, :n], z[3, 20:20 + n], z[3, 40] = right, -right, math.nan
+    unit = torch.eye(64, dtype=dtype, device="cuda")
+    ones, dz = torch.ones_like(z), out_mat(64, 64, dtype)
+    gg.act_backward(ones, 64, z, 64, dz, 64, act, 64, 64, dtype)
+    for path in ("split", "pair"):
+        dx = out_mat(64, 64, dtype)
+        gg.linear_backward(ones, 64, None, 64, unit, 64, "kn", z, 64, act, dx, 64, None, 0, None, dtype, False, 64, 64, 64,
+                           dtype, path=path)
+        assert torch.equal(dx[:, :40], dz[:, :40]) and torch.equal(dx[3, 40].isnan(), dz[3, 40].isnan())
+    assert (dz[3, :n] == 1).all() and (dz[3, 20:20 + n] == (1 if act == "none" else 0)).all()
+    if act == "relu":
+        assert dz[3, 40] == 0
+    else:
+        assert dz[3, 40].isnan() or act == "none"
+    # Y: finite operands only reach the product; the largest finite Z
+    y, y2 = out_mat(64, 64, dtype), out_mat(64, 64, dtype)
+    x = torch.where(z.isfinite(), z, torch.zeros_like(z))
+    for path in ("split", "pair"):
+        gg.linear(x, 64, unit, 64, "kn", None, act, None, 0, y, 64, None, 0, 64, 64, 64, dtype, path=path)
+        assert torch.equal(y[3, :n], x[3, :n])
+        assert torch.equal(y[3, 20:20 + n], x[3, 20:20 + n] if act == "none" else torch.zeros_like(x[3, :n]))
+    # an infinite or NaN bias reaches Z as it is
+    bias = torch.tensor([math.inf, -math.inf, math.nan] + [0.0] * 61, device="cuda")
+    gg.linear(x, 64, unit, 64, "kn", bias, act, None, 0, y, 64, y2, 64, 64, 64, 64, dtype)
+    assert (y[5, 0] == math.inf) and y[5, 2].isnan() and y2[5, 1] == -math.inf
+    want = {"none": -math.inf, "relu": 0.0, "gelu": 0.0}.get(act, math.nan)
+    assert y[5, 1].isnan() if math.isnan(want) else y[5, 1] == want
