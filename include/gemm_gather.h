@@ -596,8 +596,10 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * codes are rounded stochastically (up with the probability of the
  * remainder), with 16 bits each of a hash of (seed, step, the tensor's
  * position in the list, the element), so that equal calls give equal bits and
- * states change by less than a rounding step on average.  A value that is not
- * finite is stored as NaN and does not enter the scale.
+ * states change by less than a rounding step on average.  Before that g, m, v and
+ * sqrt(v) are rounded to nearest float32, operation by operation, so that the
+ * codes and scales are determined by the inputs.  A value that is not finite is
+ * stored as NaN and does not enter the scale.
  *
  * `tensors` is host memory, read during the call.  Tensors must not overlap.
  * Any alignment (16-byte aligned arrays are the fast case).  n == 0 is skipped.
