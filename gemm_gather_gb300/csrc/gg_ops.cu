@@ -71,6 +71,8 @@ gg_status check_tma(const Mat &m)
     if (m.begin() % 16 != 0 || m.ld % 8 != 0)
         return op_fail(GG_ERR_ALIGNMENT, "%s must be 16-byte aligned with a pitch that is a multiple "
                                          "of 8", m.name);
+    if (m.ld >= (int64_t)1 << 39)  // a tensor map's strides are below 2^40 bytes
+        return op_fail(GG_ERR_UNSUPPORTED, "%s: its pitch must be below 2^39 elements", m.name);
     return GG_OK;
 }
 

@@ -461,8 +461,8 @@ typedef enum {
  * or NULL.  dtype: GG_F16 or GG_BF16 (else GG_ERR_UNSUPPORTED), the type of X,
  * W, residual, Y and z.  Y is rounded once, to nearest even.
  * Alignment (GG_ERR_ALIGNMENT): X and W 16-byte aligned, ldx and ldw multiples
- * of 8 (tensor maps); every other argument at its element's alignment, any
- * pitch.  M, N and K may be any size: M == 0 or N == 0 launches nothing;
+ * of 8 below 2^39 (tensor maps); every other argument at its element's alignment,
+ * any pitch.  M, N and K may be any size: M == 0 or N == 0 launches nothing;
  * K == 0 gives act(bias) + residual and reads neither X nor W.
  * dev_status: as for gg_all_gather (GG_ERR_TIMEOUT when a bounded wait gave
  * up; Y and z are then undefined).

@@ -97,3 +97,15 @@ def test_the_kernel_does_not_depend_on_addresses(M):
                          db=None, gdt=F32, acc=False, M=M, N=N, K=K, dtype=BF16)
                 return gg.linear_check(*a.values()), gg.linear_backward_check(*b.values())
             assert chosen(0) == chosen(16) == chosen(112)
+
+
+def test_pitches_that_a_tensor_map_does_not_hold():
+    """A single row may have any pitch as far as memory goes; the check refuses what the launch would."""
+    from gemm_gather_gb300 import _lib
+    limit = 1 << 39
+    assert linear(M=1, ldx=limit - 8) == "split"
+    assert linear(M=1, ldy=limit, residual=A + (3 << 30), ldr=limit) == "split"
+    for kw in (dict(M=1, ldx=limit), dict(N=1, ldw=limit)):
+        with pytest.raises(gg.GGError) as e:
+            linear(**kw)
+        assert e.value.status == _lib.GG_ERR_UNSUPPORTED
