@@ -69,3 +69,42 @@ def test_same_bits_wherever_the_operands_lie(M, N, K):
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
     status_ok()
+
+
+# One gradient at a time, where nothing else shares the launch: tiles of 128 and 256 tokens, whole, or their
+# contraction split between 2 and 4 CTA pairs (weight gradients on "pair": 128 whole, 128 by 2, 128 by 4, 256 by 2, 256 by
+# 4, 256 whole), with ragged edges on both sides.
+GRADIENTS = [(70, 96, 130), (2048, 515, 1030), (640, 257, 300), (5000, 1030, 1030), (900, 300, 1030), (300, 3500, 2050)]
+
+
+@pytest.mark.parametrize("path", ["split", "pair", "auto"])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("grad", [F16, BF16, F32])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("M,N,K", GRADIENTS)
+def test_weight_gradients_alone(M, N, K, accumulate, grad, layout, path):
+    gen = gg_inputs.generator(M + N + K)
+    dtype = F16 if grad == F32 else grad
+    dz, x = mat(M, N, dtype, gen, ints=True), mat(M, K, dtype, gen, ints=True, pad=8)
+    dw = out_mat(*((K, N) if layout == "kn" else (N, K)), grad, 3)
+    dw.copy_(gg_inputs.integers(tuple(dw.shape), -2, 2, F32, gen))
+    before = dw.double()
+    call_backward(dz, x, x, layout, None, "none", None, dw, None, accumulate, path)
+    g = x.double().t() @ dz.double()
+    assert torch.equal(dw, ((g if layout == "kn" else g.t()) + before * accumulate).to(grad))
+    assert (padding(dw) == FILL).all()
+    status_ok()
+
+
+@pytest.mark.parametrize("path", ["split", "pair", "auto"])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("M,N,K", GRADIENTS + [(256, 4100, 1000), (600, 8000, 700)])
+def test_input_gradients_alone(M, N, K, layout, path):
+    gen = gg_inputs.generator(M + N + K)
+    dz, z = mat(M, N, BF16, gen, ints=True), mat(M, K, BF16, gen, ints=True, pad=8)
+    w = mat(*((K, N) if layout == "kn" else (N, K)), BF16, gen, ints=True)
+    dx = out_mat(M, K, BF16, 5)
+    call_backward(dz, z, w, layout, z, "relu", dx, None, None, False, path)
+    assert torch.equal(dx, ((dz.double() @ weight64(w, layout).t()) * (z > 0)).to(BF16))
+    assert (padding(dx) == FILL).all()
+    status_ok()
