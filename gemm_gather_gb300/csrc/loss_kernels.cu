@@ -328,45 +328,21 @@ __device__ __forceinline__ Sum warp_join(Sum x, float c)
     return r;
 }
 
-// The warps' sums of all the cluster's CTAs, from `sums` (one per warp) of each:
-// lane i takes the i-th, from where they lie in distributed shared memory.
-struct Gather {
-    uint32_t at[2];
-    int warps, count;
-    __device__ __forceinline__ Gather(const Sum *sums, int warps_, int parts, int lane)
-        : warps(warps_), count(warps_ * parts)
-    {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            at[j] = address(sums, lane + 32 * j);
-    }
-    __device__ __forceinline__ uint32_t address(const Sum *sums, int i) const
-    {
-        const int p = i < count ? i / warps : 0, w = i < count ? i - p * warps : 0;
-        return tc::map_to_rank(ptx::smem_addr(sums + w), (uint32_t)p);
-    }
-    static __device__ __forceinline__ Sum load(uint32_t at)
-    {
-        Sum x;
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.m), "=f"(x.s) : "r"(at) : "memory");
-        return x;
-    }
-    // `offset`: bytes from the sums given to the constructor
-    __device__ __forceinline__ Sum join_all(const Sum *sums, uint32_t offset, int lane, float c) const
-    {
-        Sum x{-INFINITY, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (lane + 32 * j < count) {
-                const Sum y = load(at[j] + offset);
-                x = j == 0 ? y : join(x, y, c);
-            }
+// The warps' sums of all the cluster's CTAs, from `sums` (one per warp) of each, as they
+// lie in distributed shared memory: lane i takes the i-th, the (i + 32)th and so on.
+__device__ __forceinline__ Sum cluster_join(const Sum *sums, int warps, int parts, int lane, float c)
+{
+    Sum x{-INFINITY, 0.0f};
 #pragma unroll 1
-        for (int i = lane + 64; i < count; i += 32)
-            x = join(x, load(address(sums, i) + offset), c);
-        return warp_join(x, c);
+    for (int i = lane; i < warps * parts; i += 32) {
+        const int p = i / warps;
+        const uint32_t at = tc::map_to_rank(ptx::smem_addr(sums + (i - p * warps)), (uint32_t)p);
+        Sum y;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.m), "=f"(y.s) : "r"(at) : "memory");
+        x = join(x, y, c);
     }
-};
+    return warp_join(x, c);
+}
 
 __device__ __forceinline__ float logp_of(const LossArgs &a, const Sum &all, float picked)
 {
@@ -735,7 +711,7 @@ __global__ void __launch_bounds__(1024) policy_loss_long_kernel(const __grid_con
         sums[tid >> 5] = acc;
     __syncwarp();
     tc::cluster_sync();  // every warp's sum is there, every read of the target's logit done
-    const Sum all = Gather(sums, threads / 32, parts, lane).join_all(sums, 0, lane, c);
+    const Sum all = cluster_join(sums, threads / 32, parts, lane, c);
     const float logp = logp_of(a, all, picked);
     if (rank == 0 && tid == 0)
         a.logp_out[t] = logp;

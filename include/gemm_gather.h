@@ -446,7 +446,8 @@ typedef enum { GG_WEIGHT_KN = 0, GG_WEIGHT_NK = 1 } gg_weight_layout;
 
 /* Kernel of a product: GG_LINEAR_AUTO by sizes; GG_LINEAR_SPLIT one CTA per
  * 128-feature tile and share of the contraction, joined across a cluster (few
- * tokens, few tiles); GG_LINEAR_PAIR persistent CTA pairs on 256 x 256 tiles.
+ * tokens, few tiles); GG_LINEAR_PAIR persistent CTA pairs on tiles of 256 features
+ * by 64 to 256 tokens, a contraction of few tiles split between 2 or 4 pairs.
  * The values differ by the order of float32 sums only. */
 typedef enum {
     GG_LINEAR_AUTO = 0, GG_LINEAR_SPLIT = 1, GG_LINEAR_PAIR = 2
@@ -557,7 +558,9 @@ gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t l
  * the status word (dev_status, or the library's when NULL) and its token counts
  * as masked; a wait inside the kernel that reaches the wait limit stores
  * GG_ERR_TIMEOUT and the results are incomplete.
- * Each row is read from memory once.  Any alignment and pitch.
+ * Each row is read from memory once, up to some 880,000 16-bit or 440,000 float32
+ * logits (what the shared memory of 8 CTAs holds); longer ones twice.  Any alignment
+ * and pitch; T below 2^28.
  * ------------------------------------------------------------------------- */
 gg_status gg_policy_loss(const void *logits, int64_t ld, const int64_t *target,
                          const float *old_logp, const float *ref_logp, const float *advantage,
@@ -578,7 +581,7 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
 
 /* ---------------------------------------------------------------------------
  * gg_adamw — one AdamW step (decoupled weight decay) over many tensors in one
- * launch per group of up to GG_ADAMW_GROUP tensors:
+ * launch per group of up to GG_ADAMW_GROUP tensors of the same types:
  *   g = *grad_scale * grad                        (grad_scale NULL: 1)
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   param = param (1 - lr weight_decay)
@@ -604,7 +607,9 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * `tensors` is host memory, read during the call.  Tensors must not overlap.
  * Any alignment (16-byte aligned arrays are the fast case).  n == 0 is skipped.
  * grad_scale is a device float, read by the kernel (a loss scale's inverse, a
- * clipping factor).
+ * clipping factor).  step, lr and seed are host values: a captured call replays
+ * its own bias correction, rate and rounding bits, so a graph that trains has to
+ * capture the call anew each step (cudaGraphExecUpdate takes the new one over).
  * ------------------------------------------------------------------------- */
 #define GG_ADAMW_BLOCK 256
 #define GG_ADAMW_GROUP 256
