@@ -21,16 +21,14 @@ def zeros(*shape, dtype=BF16):
 
 
 @pytest.mark.parametrize("kw,says", [
-    (dict(X=zeros(5, 24, dtype=F32)), "X: a tensor of torch.bfloat16"), (dict(X=zeros(4, 24)), "X: 120 elements"),
-    (dict(X=zeros(5, 24)), "X: a tensor on the GPU"), (dict(W=zeros(16, 23)), "W: 384 elements"),
-    (dict(X=zeros(5, 32)[:, 8:], ldx=32), "X: a tensor on the GPU"),      # padded rows: what follows is there
-    (dict(X=zeros(5, 32)[:, 8:], ldx=40), "X: 184 elements"),
-    (dict(X=zeros(1, 24).expand(5, 24)), "X: 120 elements"),              # one row, five times the same
-    (dict(bias=zeros(15)), "bias: 16 elements"), (dict(bias=zeros(32)[::2]), "bias: a contiguous tensor"),
+    (dict(X=zeros(5, 24, dtype=F32)), "X: a tensor of torch.bfloat16"), (dict(X=zeros(4, 24)), "X: a tensor of 120 elements"),
+    (dict(X=zeros(5, 24)), "X: a tensor on the GPU"), (dict(W=zeros(16, 23)), "W: a tensor of 384 elements"),
+    (dict(X=zeros(5, 32)[:, 8:], ldx=32), "X: a tensor on the GPU"),      # a part of wider rows
+    (dict(bias=zeros(15)), "bias: a tensor of 16 elements"), (dict(bias=zeros(32)[::2]), "bias: a contiguous tensor"),
     (dict(bias=zeros(16, dtype=F16), bias_dtype=F32), "bias: a tensor of torch.float32"),
     (dict(bias=zeros(16, dtype=F32)), "bias: a tensor on the GPU"),       # a float32 bias is one of the types
-    (dict(residual=zeros(5, 15)), "residual: 80 elements"), (dict(Y=zeros(5, 16, dtype=F16)), "Y: a tensor of torch.bfl"),
-    (dict(z=zeros(79)), "z: 80 elements"), (dict(z=zeros(80)), "z: a tensor on the GPU")])
+    (dict(residual=zeros(5, 15)), "residual: a tensor of 80"), (dict(Y=zeros(5, 16, dtype=F16)), "Y: a tensor of torch.bfl"),
+    (dict(z=zeros(79)), "z: a tensor of 80"), (dict(z=zeros(80)), "z: a tensor on the GPU")])
 def test_linear(kw, says):
     with pytest.raises(ValueError, match=says):
         linear(**kw)
@@ -48,7 +46,7 @@ def test_what_is_not_read_may_be_anything():
     with pytest.raises(ValueError, match="W: a tensor of torch.bfloat16"):
         gg.linear_backward_check(*b.values())
     b.update(W=A + (4 << 30), dW=zeros(16, 24))
-    with pytest.raises(ValueError, match="z_in: 120 elements"):
+    with pytest.raises(ValueError, match="z_in: a tensor of 120"):
         gg.linear_backward_check(*b.values())
     b.update(z_in=None)
     with pytest.raises(ValueError, match="dW: a tensor of torch.float32"):
@@ -57,11 +55,11 @@ def test_what_is_not_read_may_be_anything():
 
 @pytest.mark.parametrize("kw,says", [
     (dict(target=zeros(6, dtype=torch.int32)), "target: a tensor of torch.int64"),
-    (dict(target=zeros(5, dtype=torch.int64)), "target: 6 elements"),
+    (dict(target=zeros(5, dtype=torch.int64)), "target: a tensor of 6"),
     (dict(weight=torch.tensor(1.0).expand(6)), "weight: a contiguous tensor"),
     (dict(advantage=zeros(6, dtype=torch.float64)), "advantage: a tensor of torch.float32"),
-    (dict(old_logp=zeros(6, dtype=BF16)), "old_logp: a tensor of"), (dict(stats=zeros(3, dtype=F32)), "stats: 4 elements"),
-    (dict(logits=zeros(6, 99)), "logits: 600 elements"), (dict(dlogits=zeros(6, 100, dtype=F32)), "dlogits: a tensor of"),
+    (dict(old_logp=zeros(6, dtype=BF16)), "old_logp: a tensor of"), (dict(stats=zeros(3, dtype=F32)), "stats: a tensor of 4"),
+    (dict(logits=zeros(6, 99)), "logits: a tensor of 600"), (dict(dlogits=zeros(6, 100, dtype=F32)), "dlogits: a tensor of"),
     (dict(logp_out=zeros(6, dtype=F32)), "logp_out: a tensor on the GPU")])
 def test_policy_loss(kw, says):
     a = dict(logits=A, ld=100, target=A + (1 << 30), old_logp=None, ref_logp=None, advantage=A + (2 << 30),
