@@ -3,7 +3,7 @@
 // Elementwise: m = b1 m + (1-b1) g, v = b2 v + (1-b2) g^2, p = p (1 - lr wd) -
 // lr' m / (sqrt(v) k + eps).  Bound: HBM; every array is read once and written
 // once.  Measured: 117M float32 parameters with bfloat16 gradients and copies, float32
-// states 495 us, 6.6 TB/s; 8-bit states 275 us, 6.9 TB/s (a copy's rate is 6.8); 200
+// states 495 us, 6.6 TB/s; 8-bit states 277 us, 6.8 TB/s (a copy's rate is 6.8); 200
 // small tensors 3.1 us.  The tensors' descriptors are the kernel's parameter (up to 256 in a
 // launch: no table in device memory, no copy before the launch), and a CTA
 // finds its tensor by bisection of the running count of chunks.

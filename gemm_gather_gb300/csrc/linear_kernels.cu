@@ -25,8 +25,8 @@
 //    tokens (tcgen05 cta_group::2, 64-deep stages, 6 or 8 in a ring of 192 KB per
 //    CTA, two accumulators in TMEM so that a tile's epilogue runs under the next
 //    tile's MMAs).  Bound: the tensor pipes, under the power limit.  Measured:
-//    16384 x 3584 x 8192 with gelu_tanh and Z stored in 517 to 550 us (1.75 to 1.86
-//    PFLOP/s; cuBLAS's product alone on the same boxes 494 to 547), pipes 90 %
+//    16384 x 3584 x 8192 with gelu_tanh and Z stored in 503 to 594 us (1.62 to 1.91
+//    PFLOP/s; cuBLAS's product alone on the same boxes 494 to 574), pipes 90 %
 //    active at 4096 x 4864 x 8192 with gelu and Z.
 //  * split_kernel: one CTA per tile of 128 features x {16, 32, 64} tokens and share
 //    of the contraction; the CTAs of a cluster (up to 8) split one tile's
