@@ -477,6 +477,7 @@ def _exact_codes(x):
     whole = torch.zeros((M, -(-N // BLOCK) * BLOCK), dtype=torch.float64, device="cuda")
     whole[:, :N] = x.double()
     frac, power = torch.frexp(whole.abs().view(M, -1, BLOCK).max(2).values)   # frac in [0.5, 1)
+    power = torch.where(frac == 0, -200, power)     # nothing but zeros: the least scale
     scale = _power_of_two(torch.clamp(power - 9 + (frac > 0.875).to(power.dtype), min=-118))
     y = whole[:, :N] / scale.repeat_interleave(BLOCK, 1)[:, :N]
     quantum = _power_of_two(torch.clamp(torch.frexp(y).exponent - 4, min=-9))
