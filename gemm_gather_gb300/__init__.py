@@ -26,7 +26,7 @@ from ._lib import (GG_AG_AUTO, GG_AG_BULK, GG_AG_TMA, GG_AG_VECTOR, GG_BF16, GG_
                    GG_CLAIM_ALWAYS, GG_CLAIM_AUTO, GG_CLAIM_NEVER, GG_MAX_WORLD, GG_OK,
                    GG_WORKSPACE_SLOT_BYTES,
                    GG_ACT_GELU, GG_ACT_GELU_TANH, GG_ACT_NONE, GG_ACT_RELU, GG_ACT_SILU,
-                   GG_ADAMW_BLOCK, GG_LINEAR_AUTO, GG_LINEAR_PAIR, GG_LINEAR_SPLIT, GG_WEIGHT_KN, GG_WEIGHT_NK,
+                   GG_ADAMW_BLOCK, GG_PACK_BLOCK, GG_LINEAR_AUTO, GG_LINEAR_PAIR, GG_LINEAR_SPLIT, GG_WEIGHT_KN, GG_WEIGHT_NK,
                    AdamwTensor, GGError, Group, Tile, check, lib, LIB_PATH)
 
 __all__ = [
@@ -35,6 +35,9 @@ __all__ = [
     "all_gather_check", "all_gather_grouped", "all_gather_partitioned", "all_to_all",
     "collective_check", "matmul_all_gather", "matmul_all_gather_check", "matmul_all_gather_plan",
     "linear", "linear_check", "linear_backward", "linear_backward_check", "act_backward",
+    "pack8", "unpack8", "linear_backward8", "linear_backward8_check", "linear_backward8_workspace",
+    "rms_norm", "rms_norm_check", "rms_norm_backward", "rms_norm_backward_check", "rms_norm_backward_workspace",
+    "PACK_BLOCK",
     "policy_loss", "policy_loss_check", "adamw", "adamw_check", "adamw_tensors", "AdamwTensors",
     "ADAMW_BLOCK", "ACTIVATIONS", "WEIGHT_LAYOUTS", "LINEAR_PATHS",
     "set_claim_policy",
@@ -55,6 +58,7 @@ ACTIVATIONS = {"none": GG_ACT_NONE, "relu": GG_ACT_RELU, "gelu": GG_ACT_GELU,
 WEIGHT_LAYOUTS = {"kn": GG_WEIGHT_KN, "nk": GG_WEIGHT_NK}     # rows of K x N, or of N x K
 LINEAR_PATHS = {"auto": GG_LINEAR_AUTO, "split": GG_LINEAR_SPLIT, "pair": GG_LINEAR_PAIR}
 ADAMW_BLOCK = GG_ADAMW_BLOCK      # elements that share one scale of 8-bit optimizer states
+PACK_BLOCK = GG_PACK_BLOCK        # elements of a row that share one scale of an 8-bit activation
 CLAIM_POLICIES = {"auto": GG_CLAIM_AUTO, "always": GG_CLAIM_ALWAYS, "never": GG_CLAIM_NEVER}
 STORE_POLICIES = {"plain": 0, "evict_first": 1}  # GG_STORE_PLAIN, GG_STORE_EVICT_FIRST
 
@@ -398,6 +402,170 @@ def act_backward(dy, lddy: int, z, ldz: int, dz, lddz: int, act: str, M: int, N:
     check(lib.gg_act_backward(_held(dy, "dy", t, M, N), lddy, _held(z, "z", t, M, N), ldz,
                               _held(dz, "dz", t, M, N), lddz, ACTIVATIONS[act], M, N, code,
                               _stream(stream)))
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _packed(codes, scales, M: int, N: int) -> tuple:
+    """Addresses of an 8-bit activation's codes (uint8 or float8_e4m3fn) and scales."""
+    t = codes.dtype if isinstance(codes, Tensor) and codes.dtype in _CODES else torch.uint8
+    return _held(codes, "codes", t, M, N), _held(scales, "scales", _F32, M, -(-N // PACK_BLOCK))
+
+
+def _room(workspace, workspace_bytes) -> tuple:
+    """Address and bytes of a call's scratch memory: a contiguous tensor of any type, or an address with
+    its bytes."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, Tensor):
+        return int(workspace), int(workspace_bytes or 0)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is needed")
+    have = workspace.numel() * workspace.element_size()
+    if workspace_bytes is not None and workspace_bytes > have:
+        raise ValueError(f"workspace: a tensor of {workspace_bytes} bytes is needed")
+    if not workspace.is_cuda:
+        raise ValueError("workspace: a tensor on the GPU is needed")
+    return workspace.data_ptr(), have if workspace_bytes is None else workspace_bytes
+
+
+def pack8(x, ldx: int, codes, ldc: int, scales, lds: int, M: int, N: int, dtype, stream=None) -> None:
+    """M x N activations to 8-bit codes and a scale per PACK_BLOCK elements of a row (gg_pack8).
+    codes: uint8 or float8_e4m3fn.  Tensors are checked as for ``linear``."""
+    code = _dtype(dtype)
+    c, s = _packed(codes, scales, M, N)
+    check(lib.gg_pack8(_held(x, "x", _TORCH_DTYPES.get(code), M, N), ldx, c, ldc, s, lds, M, N, code,
+                       _stream(stream)))
+
+
+def unpack8(codes, ldc: int, scales, lds: int, act: str, out, ldo: int, M: int, N: int, dtype,
+            stream=None) -> None:
+    """out = act(what 8-bit codes and scales stand for) (gg_unpack8)."""
+    code = _dtype(dtype)
+    c, s = _packed(codes, scales, M, N)
+    check(lib.gg_unpack8(c, ldc, s, lds, ACTIVATIONS[act], _held(out, "out", _TORCH_DTYPES.get(code), M, N), ldo,
+                         M, N, code, _stream(stream)))
+
+
+def _backward8_args(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx, dW, lddw, dbias,
+                    grad_dtype, accumulate, workspace, workspace_bytes, M, N, K, dtype) -> tuple:
+    code, grad = _dtype(dtype), _dtype(grad_dtype)
+    t, g = _TORCH_DTYPES.get(code), _TORCH_DTYPES.get(grad)
+    kn = layout == "kn"
+    read = M if not (dX is None and dW is None and dbias is None) else 0
+    # the codes are read for dW, and for dX where there is an activation; W for dX
+    used = (dW is not None and N > 0) or (dX is not None and act != "none")
+    c, s = _packed(codes, scales, M if used else 0, K if used else 0)
+    w_rows, w_cols = (K, N) if kn else (N, K)
+    room, room_bytes = _room(workspace, workspace_bytes)
+    return (_held(dZ, "dZ", t, read, N), lddz, c, ldc, s, lds, ACTIVATIONS[act],
+            _ptr(W) if dX is None else _held(W, "W", t, w_rows if M > 0 else 0, w_cols), ldw,
+            WEIGHT_LAYOUTS[layout], _held(dX, "dX", t, M, K), lddx, _held(dW, "dW", g, w_rows, w_cols), lddw,
+            _vector(dbias, "dbias", g, N), grad, 1 if accumulate else 0, room, room_bytes, M, N, K, code)
+
+
+def linear_backward8(dZ, lddz: int, codes, ldc: int, scales, lds: int, act: str, W, ldw: int, layout: str, dX,
+                     lddx: int, dW, lddw: int, dbias, grad_dtype, accumulate: bool, workspace, M: int, N: int,
+                     K: int, dtype, status=None, stream=None, path: str = "auto", workspace_bytes=None) -> None:
+    """``linear_backward`` of a layer whose input is act(P), P kept in 8 bits: dX = (dZ W^T) act'(P),
+    dW (+)= act(P)^T dZ, dbias (+)= column sums of dZ (gg_linear_backward8).  ``workspace``: a contiguous tensor
+    on the GPU of at least ``linear_backward8_workspace(M, K)`` bytes where dW is asked for (or an address, with
+    ``workspace_bytes``)."""
+    check(lib.gg_linear_backward8(*_backward8_args(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx,
+                                                   dW, lddw, dbias, grad_dtype, accumulate, workspace,
+                                                   workspace_bytes, M, N, K, dtype),
+                                  _word(status), _stream(stream), LINEAR_PATHS[path]))
+
+
+def linear_backward8_check(dZ, lddz: int, codes, ldc: int, scales, lds: int, act: str, W, ldw: int, layout: str, dX,
+                           lddx: int, dW, lddw: int, dbias, grad_dtype, accumulate: bool, workspace, M: int, N: int,
+                           K: int, dtype, path: str = "auto", workspace_bytes=None) -> tuple[str, str]:
+    """Validate without launching; returns the kernels of dX and dW."""
+    dx, dw = ctypes.c_int(), ctypes.c_int()
+    check(lib.gg_linear_backward8_check(*_backward8_args(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX,
+                                                         lddx, dW, lddw, dbias, grad_dtype, accumulate, workspace,
+                                                         workspace_bytes, M, N, K, dtype),
+                                        LINEAR_PATHS[path], ctypes.byref(dx), ctypes.byref(dw)))
+    return _LINEAR_NAMES[dx.value], _LINEAR_NAMES[dw.value]
+
+
+def linear_backward8_workspace(M: int, K: int) -> int:
+    """Bytes of ``linear_backward8``'s workspace."""
+    return lib.gg_linear_backward8_workspace(M, K)
+
+
+def _weight_code(weight, weight_dtype, code: int) -> int:
+    if weight_dtype is not None:
+        return _dtype(weight_dtype)
+    return DTYPE_CODES.get(weight.dtype, -1) if isinstance(weight, Tensor) else code
+
+
+def _norm_args(x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, codes, ldc, scales, lds, rstd, M, N, dtype,
+               weight_dtype) -> tuple:
+    code = _dtype(dtype)
+    t = _TORCH_DTYPES.get(code)
+    wcode = _weight_code(weight, weight_dtype, code)
+    c, s = _packed(codes, scales, M, N)
+    return (_held(x, "x", t, M, N), ldx, _held(residual, "residual", t, M, N), ldr,
+            _vector(weight, "weight", _TORCH_DTYPES.get(wcode), N if M > 0 else 0), wcode, eps,
+            _held(h, "h", t, M, N), ldh, _held(y, "y", t, M, N), ldy, c, ldc, s, lds,
+            _vector(rstd, "rstd", _F32, M if N > 0 else 0), M, N, code)
+
+
+def rms_norm(x, ldx: int, residual, ldr: int, weight, eps: float, h, ldh: int, y, ldy: int, codes, ldc: int, scales,
+             lds: int, rstd, M: int, N: int, dtype, stream=None, weight_dtype=None) -> None:
+    """h = x + residual, y = h rstd weight, rstd = 1 / sqrt(mean h^2 + eps) (gg_rms_norm); codes and scales
+    (both or neither) receive y in 8 bits, as ``pack8`` of y.  residual, h, codes, scales and rstd may be None, y
+    with codes.  ``weight_dtype`` is taken from a weight tensor, else ``dtype``."""
+    check(lib.gg_rms_norm(*_norm_args(x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, codes, ldc, scales, lds,
+                                      rstd, M, N, dtype, weight_dtype), _stream(stream)))
+
+
+def rms_norm_check(x, ldx: int, residual, ldr: int, weight, eps: float, h, ldh: int, y, ldy: int, codes, ldc: int,
+                   scales, lds: int, rstd, M: int, N: int, dtype, weight_dtype=None) -> None:
+    """Validate without launching."""
+    check(lib.gg_rms_norm_check(*_norm_args(x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, codes, ldc, scales,
+                                            lds, rstd, M, N, dtype, weight_dtype)))
+
+
+def _norm_backward_args(dy, lddy, h, ldh, rstd, weight, dh_in, lddhin, dh, lddh, dweight, grad_dtype, accumulate,
+                        workspace, workspace_bytes, M, N, dtype, weight_dtype) -> tuple:
+    code, grad = _dtype(dtype), _dtype(grad_dtype)
+    t = _TORCH_DTYPES.get(code)
+    wcode = _weight_code(weight, weight_dtype, code)
+    room, room_bytes = _room(workspace, workspace_bytes)
+    return (_held(dy, "dy", t, M, N), lddy, _held(h, "h", t, M, N), ldh,
+            _vector(rstd, "rstd", _F32, M if N > 0 else 0),
+            _vector(weight, "weight", _TORCH_DTYPES.get(wcode), N if M > 0 else 0), wcode,
+            _ptr(dh_in) if dh is None else _held(dh_in, "dh_in", t, M, N), lddhin, _held(dh, "dh", t, M, N), lddh,
+            _vector(dweight, "dweight", _TORCH_DTYPES.get(grad), N), grad, 1 if accumulate else 0, room, room_bytes,
+            M, N, code)
+
+
+def rms_norm_backward(dy, lddy: int, h, ldh: int, rstd, weight, dh_in, lddhin: int, dh, lddh: int, dweight,
+                      grad_dtype, accumulate: bool, workspace, M: int, N: int, dtype, stream=None, weight_dtype=None,
+                      workspace_bytes=None) -> None:
+    """dh = rstd (g - u mean(g u)) + dh_in with g = dy weight and u = h rstd, dweight (+)= sum over rows of
+    dy u (gg_rms_norm_backward); dh and dweight may each be None.  ``workspace``: a contiguous tensor on the GPU of at
+    least ``rms_norm_backward_workspace(M, N)`` bytes where dweight is asked for."""
+    check(lib.gg_rms_norm_backward(*_norm_backward_args(dy, lddy, h, ldh, rstd, weight, dh_in, lddhin, dh, lddh,
+                                                        dweight, grad_dtype, accumulate, workspace, workspace_bytes,
+                                                        M, N, dtype, weight_dtype), _stream(stream)))
+
+
+def rms_norm_backward_check(dy, lddy: int, h, ldh: int, rstd, weight, dh_in, lddhin: int, dh, lddh: int, dweight,
+                            grad_dtype, accumulate: bool, workspace, M: int, N: int, dtype, weight_dtype=None,
+                            workspace_bytes=None) -> None:
+    """Validate without launching."""
+    check(lib.gg_rms_norm_backward_check(*_norm_backward_args(dy, lddy, h, ldh, rstd, weight, dh_in, lddhin, dh, lddh,
+                                                              dweight, grad_dtype, accumulate, workspace,
+                                                              workspace_bytes, M, N, dtype, weight_dtype)))
+
+
+def rms_norm_backward_workspace(M: int, N: int) -> int:
+    """Bytes of ``rms_norm_backward``'s workspace."""
+    return lib.gg_rms_norm_backward_workspace(M, N)
 
 
 def _loss_args(logits, ld, target, old_logp, ref_logp, advantage, weight, T, V, dtype, stats, logp_out,

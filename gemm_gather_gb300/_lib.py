@@ -40,6 +40,7 @@ GG_WEIGHT_KN, GG_WEIGHT_NK = 0, 1
 GG_LINEAR_AUTO, GG_LINEAR_SPLIT, GG_LINEAR_PAIR = 0, 1, 2
 GG_LINEAR_NONE = 0
 GG_ADAMW_BLOCK, GG_ADAMW_GROUP = 256, 256
+GG_PACK_BLOCK = 128
 
 # Every entry point declared in include/gemm_gather.h.
 EXPORTS = (
@@ -51,7 +52,9 @@ EXPORTS = (
     "gg_matmul_all_gather", "gg_matmul_all_gather_path", "gg_matmul_all_gather_check",
     "gg_matmul_all_gather_plan",
     "gg_linear", "gg_linear_check", "gg_linear_backward", "gg_linear_backward_check",
-    "gg_act_backward", "gg_policy_loss", "gg_policy_loss_check", "gg_adamw", "gg_adamw_check",
+    "gg_act_backward", "gg_pack8", "gg_unpack8", "gg_linear_backward8", "gg_linear_backward8_check",
+    "gg_linear_backward8_workspace", "gg_rms_norm", "gg_rms_norm_check", "gg_rms_norm_backward",
+    "gg_rms_norm_backward_check", "gg_rms_norm_backward_workspace", "gg_policy_loss", "gg_policy_loss_check", "gg_adamw", "gg_adamw_check",
     "gg_set_claim_policy", "gg_get_claim_policy", "gg_set_store_policy", "gg_get_store_policy",
     "gg_set_wait_limit_ns", "gg_get_wait_limit_ns", "gg_debug_inject_stall",
     "gg_device_status", "gg_clear_device_status",
@@ -133,6 +136,23 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
                                       i32, i32, n64, n64, n64, i32, i32, ctypes.POINTER(i32),
                                       ctypes.POINTER(i32)], i32),
         "gg_act_backward": ([vp, n64, vp, n64, vp, n64, i32, n64, n64, i32, vp], i32),
+        "gg_pack8": ([vp, n64, vp, n64, vp, n64, n64, n64, i32, vp], i32),
+        "gg_unpack8": ([vp, n64, vp, n64, i32, vp, n64, n64, n64, i32, vp], i32),
+        "gg_linear_backward8": ([vp, n64, vp, n64, vp, n64, i32, vp, n64, i32, vp, n64, vp, n64, vp, i32, i32,
+                                 vp, sz, n64, n64, n64, i32, vp, vp, i32], i32),
+        "gg_linear_backward8_check": ([vp, n64, vp, n64, vp, n64, i32, vp, n64, i32, vp, n64, vp, n64, vp, i32,
+                                       i32, vp, sz, n64, n64, n64, i32, i32, ctypes.POINTER(i32),
+                                       ctypes.POINTER(i32)], i32),
+        "gg_linear_backward8_workspace": ([i64, i64], u64),
+        "gg_rms_norm": ([vp, n64, vp, n64, vp, i32, f32, vp, n64, vp, n64, vp, n64, vp, n64, vp, n64, n64, i32,
+                         vp], i32),
+        "gg_rms_norm_check": ([vp, n64, vp, n64, vp, i32, f32, vp, n64, vp, n64, vp, n64, vp, n64, vp, n64, n64,
+                               i32], i32),
+        "gg_rms_norm_backward": ([vp, n64, vp, n64, vp, vp, i32, vp, n64, vp, n64, vp, i32, i32, vp, sz, n64, n64,
+                                  i32, vp], i32),
+        "gg_rms_norm_backward_check": ([vp, n64, vp, n64, vp, vp, i32, vp, n64, vp, n64, vp, i32, i32, vp, sz, n64,
+                                        n64, i32], i32),
+        "gg_rms_norm_backward_workspace": ([i64, i64], u64),
         "gg_policy_loss": ([vp, n64, vp, vp, vp, vp, vp, n64, n64, i32, f32, f32, f32, f32, f32, vp, vp,
                             vp, n64, vp, vp], i32),
         "gg_policy_loss_check": ([vp, n64, vp, vp, vp, vp, vp, n64, n64, i32, f32, f32, f32, f32, f32,

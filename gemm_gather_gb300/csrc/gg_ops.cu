@@ -5,116 +5,11 @@
 #include <cmath>
 
 #include "gg_ops.h"
+#include "op_args.h"
 
 namespace {
 
-using gg::op_cuda_fail;
-using gg::op_fail;
-using gg::op_ok;
-
-constexpr int64_t kMaxSize = ((int64_t)1 << 31) - 1;
-
-// A rows x cols matrix argument of a call (element size es, pitch in elements).
-struct Mat {
-    const char *name;
-    const void *p;
-    int64_t rows, cols, ld, es;
-
-    uint64_t begin() const { return reinterpret_cast<uint64_t>(p); }
-    uint64_t bytes() const
-    {
-        return rows > 0 && cols > 0 ? (uint64_t)((rows - 1) * ld + cols) * (uint64_t)es : 0;
-    }
-};
-
-// Whether two matrices share an element's bytes.  Matrices of one pitch may
-// interleave (column ranges of one buffer): their rows are compared then.
-bool share(const Mat &a, const Mat &b)
-{
-    if (!a.p || !b.p || a.bytes() == 0 || b.bytes() == 0)
-        return false;
-    if (a.begin() + a.bytes() <= b.begin() || b.begin() + b.bytes() <= a.begin())
-        return false;
-    const uint64_t pa = (uint64_t)(a.ld * a.es), pb = (uint64_t)(b.ld * b.es);
-    if (pa != pb || a.rows < 2 || b.rows < 2)
-        return true;
-    const Mat &lo = a.begin() <= b.begin() ? a : b, &hi = a.begin() <= b.begin() ? b : a;
-    const uint64_t shift = (hi.begin() - lo.begin()) % pa;  // hi's first column within lo's row
-    const uint64_t wl = (uint64_t)(lo.cols * lo.es), wh = (uint64_t)(hi.cols * hi.es);
-    return !(shift >= wl && shift + wh <= pa);
-}
-
-bool same(const Mat &a, const Mat &b) { return a.p == b.p && a.ld == b.ld; }
-
-gg_status check_mat(const Mat &m, bool needed)
-{
-    if (m.rows == 0 || m.cols == 0)
-        return GG_OK;
-    if (!m.p)
-        return needed ? op_fail(GG_ERR_INVALID_ARG, "%s must be non-NULL", m.name) : GG_OK;
-    if (m.ld < m.cols)
-        return op_fail(GG_ERR_INVALID_ARG, "%s: the pitch %lld is below the row length %lld", m.name,
-                       (long long)m.ld, (long long)m.cols);
-    if (m.ld > INT64_MAX / 16 / (m.rows > 0 ? m.rows : 1))
-        return op_fail(GG_ERR_UNSUPPORTED, "%s: its extent passes 2^59 bytes", m.name);
-    if (m.begin() % (uint64_t)m.es != 0)
-        return op_fail(GG_ERR_ALIGNMENT, "%s must be aligned to its %lld-byte elements", m.name,
-                       (long long)m.es);
-    return GG_OK;
-}
-
-// Matrices that tensor maps (or 16-byte loads) read.
-gg_status check_tma(const Mat &m)
-{
-    if (m.rows == 0 || m.cols == 0)
-        return GG_OK;
-    if (m.begin() % 16 != 0 || m.ld % 8 != 0)
-        return op_fail(GG_ERR_ALIGNMENT, "%s must be 16-byte aligned with a pitch that is a multiple "
-                                         "of 8", m.name);
-    if (m.ld >= (int64_t)1 << 39)  // a tensor map's strides are below 2^40 bytes
-        return op_fail(GG_ERR_UNSUPPORTED, "%s: its pitch must be below 2^39 elements", m.name);
-    return GG_OK;
-}
-
-gg_status check_apart(const Mat &out, const Mat &other)
-{
-    return share(out, other) ? op_fail(GG_ERR_INVALID_ARG, "%s overlaps %s", out.name, other.name)
-                             : GG_OK;
-}
-
-gg_status check_sizes(int64_t M, int64_t N, int64_t K)
-{
-    if (M < 0 || N < 0 || K < 0)
-        return op_fail(GG_ERR_INVALID_ARG, "sizes must be >= 0");
-    if (M > kMaxSize || N > kMaxSize || K > kMaxSize)
-        return op_fail(GG_ERR_UNSUPPORTED, "sizes must be below 2^31");
-    return GG_OK;
-}
-
-gg_status check_types(gg_dtype dtype, gg_activation act, const char *what)
-{
-    if (dtype != GG_F16 && dtype != GG_BF16)
-        return op_fail(GG_ERR_UNSUPPORTED, "%s takes GG_F16 or GG_BF16", what);
-    if (act < GG_ACT_NONE || act > GG_ACT_SILU)
-        return op_fail(GG_ERR_INVALID_ARG, "unknown activation %d", (int)act);
-    return GG_OK;
-}
-
-gg_status check_route(gg_weight_layout layout, gg_linear_path path)
-{
-    if (layout != GG_WEIGHT_KN && layout != GG_WEIGHT_NK)
-        return op_fail(GG_ERR_INVALID_ARG, "unknown weight layout %d", (int)layout);
-    if (path != GG_LINEAR_AUTO && path != GG_LINEAR_SPLIT && path != GG_LINEAR_PAIR)
-        return op_fail(GG_ERR_INVALID_ARG, "unknown linear path %d", (int)path);
-    return GG_OK;
-}
-
-#define GG_TRY(x)                  \
-    do {                           \
-        const gg_status st_ = (x); \
-        if (st_ != GG_OK)          \
-            return st_;            \
-    } while (0)
+using namespace gg;
 
 // Validation of gg_linear; *a and *plan describe the launch.
 gg_status prepare_linear(const void *X, int64_t ldx, const void *W, int64_t ldw,
@@ -205,6 +100,7 @@ struct Backward {
     bool run_dx, run_dw, run_sum;
     bool both;  // dX and dW in one launch, with these tiles
     int bt_dx, bt_dw;
+    int epi_dx; // kEpiGradIn, or kEpiGradIn8 where z_in is kept in 8 bits
 };
 
 gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t ldx, const void *W,
@@ -215,6 +111,7 @@ gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t 
                            Backward *out)
 {
     Backward r{};
+    r.epi_dx = gg::kEpiGradIn;
     GG_TRY(check_types(dtype, act_in, "linear_backward"));
     GG_TRY(check_route(layout, path));
     GG_TRY(check_sizes(M, N, K));
@@ -298,6 +195,82 @@ gg_status prepare_backward(const void *dZ, int64_t lddz, const void *X, int64_t 
     if (r.both)
         r.plan_dx.kernel = r.plan_dw.kernel = GG_LINEAR_PAIR;
     *out = r;
+    return op_ok();
+}
+
+gg_status run_backward(Backward *b, int *dev_status, gg_stream_t stream)
+{
+    if (b->both) {
+        GG_TRY(fill_in(&b->dx, dev_status));
+        GG_TRY(fill_in(&b->dw, dev_status));
+        const char *why = nullptr;
+        const cudaError_t e = gg::launch_both(b->epi_dx, b->dx, b->bt_dx, b->dw, b->bt_dw,
+                                              reinterpret_cast<cudaStream_t>(stream), &why);
+        if (e != cudaSuccess)
+            return op_cuda_fail(e, why ? why : "launching the gradients");
+    } else {
+        if (b->run_dx)
+            GG_TRY(run_product(b->epi_dx, &b->dx, b->plan_dx, dev_status, stream));
+        if (b->run_dw)
+            GG_TRY(run_product(gg::kEpiGradW, &b->dw, b->plan_dw, dev_status, stream));
+    }
+    if (b->run_sum) {
+        b->sum.beside = b->both || (b->run_dx && b->dx.I > 0 && b->dx.J > 0) || (b->run_dw && b->dw.I > 0 && b->dw.J > 0);
+        const cudaError_t e = gg::launch_colsum(b->sum, reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return op_cuda_fail(e, "launching the bias gradient");
+    }
+    return op_ok();
+}
+
+// Device bytes of gg_linear_backward8: X in 16 bits, rows on 16-byte boundaries.
+int64_t unpacked_pitch(int64_t K) { return (K + 7) / 8 * 8; }
+
+// Validation of gg_linear_backward8: the plan of gg_linear_backward on the unpacked X, with z_in read
+// from the codes.  *u: what unpacks X (M == 0 where nothing reads it).
+gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int64_t ldc, const float *scales,
+                            int64_t lds, gg_activation act, const void *W, int64_t ldw, gg_weight_layout layout,
+                            const void *dX, int64_t lddx, const void *dW, int64_t lddw, const void *dbias,
+                            gg_dtype grad_dtype, int accumulate, const void *workspace, size_t workspace_bytes,
+                            int64_t M, int64_t N, int64_t K, gg_dtype dtype, gg_linear_path path, Backward *out,
+                            gg::UnpackArgs *u)
+{
+    GG_TRY(check_types(dtype, act, "linear_backward8"));
+    GG_TRY(check_sizes(M, N, K));
+    const bool x = dW && N > 0, z = dX && act != GG_ACT_NONE;  // what the codes are read for
+    const bool unpacks = x && M > 0 && K > 0;
+    const int64_t rows = x || z ? M : 0;
+    const Mat c{"codes", codes, rows, K, ldc, 1},
+        sc{"scales", scales, rows, (K + GG_PACK_BLOCK - 1) / GG_PACK_BLOCK, lds, 4};
+    GG_TRY(check_mat(c, true));
+    GG_TRY(check_mat(sc, true));
+    const int64_t ldx = unpacked_pitch(K);
+    const Mat ws{"workspace", workspace, unpacks ? M : 0, ldx, ldx, 2};
+    if (unpacks && (!workspace || workspace_bytes < (size_t)(M * ldx * 2)))
+        return op_fail(GG_ERR_INVALID_ARG, "workspace: %lld bytes are needed", (long long)(M * ldx * 2));
+    Backward r;
+    // the workspace is checked as X is: 16-byte aligned, apart from the outputs
+    GG_TRY(prepare_backward(dZ, lddz, unpacks ? workspace : nullptr, ldx, W, ldw, layout, nullptr, 0, act, dX, lddx,
+                            dW, lddw, dbias, grad_dtype, accumulate, M, N, K, dtype, path, &r));
+    const bool kn = layout == GG_WEIGHT_KN;
+    const int64_t ge = grad_dtype == GG_F32 ? 4 : 2;
+    const Mat gx{"dX", dX, M, K, lddx, 2}, gw{"dW", dW, kn ? K : N, kn ? N : K, lddw, ge}, gb{"dbias", dbias, 1, N, N, ge};
+    for (const Mat *in : {&c, &sc}) {
+        for (const Mat *o : {&gx, &gw, &gb})
+            GG_TRY(check_apart(*o, *in));
+        GG_TRY(check_apart(ws, *in));
+    }
+    const Mat dz{"dZ", dZ, M, N, lddz, 2}, w{"W", W, r.run_dx ? (kn ? K : N) : 0, kn ? N : K, ldw, 2};
+    GG_TRY(check_apart(ws, dz));
+    GG_TRY(check_apart(ws, w));
+    r.epi_dx = gg::kEpiGradIn8;
+    r.dx.aux = act != GG_ACT_NONE ? codes : nullptr;
+    r.dx.ldaux = ldc;
+    r.dx.scales = scales;
+    r.dx.lds = lds;
+    *out = r;
+    *u = gg::UnpackArgs{reinterpret_cast<const uint8_t *>(codes), ldc, scales, lds, (int)act,
+                        const_cast<void *>(workspace), ldx, unpacks ? M : 0, K, dtype == GG_BF16};
     return op_ok();
 }
 
@@ -527,27 +500,7 @@ gg_status gg_linear_backward(const void *dZ, int64_t lddz, const void *X, int64_
     Backward b;
     GG_TRY(prepare_backward(dZ, lddz, X, ldx, W, ldw, layout, z_in, ldzin, act_in, dX, lddx, dW, lddw,
                             dbias, grad_dtype, accumulate, M, N, K, dtype, path, &b));
-    if (b.both) {
-        GG_TRY(fill_in(&b.dx, dev_status));
-        GG_TRY(fill_in(&b.dw, dev_status));
-        const char *why = nullptr;
-        const cudaError_t e = gg::launch_both(b.dx, b.bt_dx, b.dw, b.bt_dw,
-                                              reinterpret_cast<cudaStream_t>(stream), &why);
-        if (e != cudaSuccess)
-            return op_cuda_fail(e, why ? why : "launching the gradients");
-    } else {
-        if (b.run_dx)
-            GG_TRY(run_product(gg::kEpiGradIn, &b.dx, b.plan_dx, dev_status, stream));
-        if (b.run_dw)
-            GG_TRY(run_product(gg::kEpiGradW, &b.dw, b.plan_dw, dev_status, stream));
-    }
-    if (b.run_sum) {
-        b.sum.beside = b.both || (b.run_dx && b.dx.I > 0 && b.dx.J > 0) || (b.run_dw && b.dw.I > 0 && b.dw.J > 0);
-        const cudaError_t e = gg::launch_colsum(b.sum, reinterpret_cast<cudaStream_t>(stream));
-        if (e != cudaSuccess)
-            return op_cuda_fail(e, "launching the bias gradient");
-    }
-    return op_ok();
+    return run_backward(&b, dev_status, stream);
 }
 
 gg_status gg_linear_backward_check(const void *dZ, int64_t lddz, const void *X, int64_t ldx,
@@ -567,6 +520,49 @@ gg_status gg_linear_backward_check(const void *dZ, int64_t lddz, const void *X, 
     if (chosen_dw)
         *chosen_dw = b.plan_dw.kernel;
     return st;
+}
+
+gg_status gg_linear_backward8(const void *dZ, int64_t lddz, const void *codes, int64_t ldc, const float *scales,
+                              int64_t lds, gg_activation act, const void *W, int64_t ldw, gg_weight_layout layout,
+                              void *dX, int64_t lddx, void *dW, int64_t lddw, void *dbias, gg_dtype grad_dtype,
+                              int accumulate, void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                              int64_t K, gg_dtype dtype, int *dev_status, gg_stream_t stream, gg_linear_path path)
+{
+    Backward b;
+    gg::UnpackArgs u;
+    GG_TRY(prepare_backward8(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx, dW, lddw, dbias,
+                             grad_dtype, accumulate, workspace, workspace_bytes, M, N, K, dtype, path, &b, &u));
+    if (u.M > 0) {
+        const cudaError_t e = gg::launch_unpack(u, reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return op_cuda_fail(e, "unpacking the activations");
+    }
+    return run_backward(&b, dev_status, stream);
+}
+
+gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *codes, int64_t ldc,
+                                    const float *scales, int64_t lds, gg_activation act, const void *W,
+                                    int64_t ldw, gg_weight_layout layout, const void *dX, int64_t lddx,
+                                    const void *dW, int64_t lddw, const void *dbias, gg_dtype grad_dtype,
+                                    int accumulate, const void *workspace, size_t workspace_bytes, int64_t M,
+                                    int64_t N, int64_t K, gg_dtype dtype, gg_linear_path path, int *chosen_dx,
+                                    int *chosen_dw)
+{
+    Backward b{};
+    gg::UnpackArgs u;
+    const gg_status st = prepare_backward8(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx, dW,
+                                           lddw, dbias, grad_dtype, accumulate, workspace, workspace_bytes, M, N,
+                                           K, dtype, path, &b, &u);
+    if (chosen_dx)
+        *chosen_dx = b.plan_dx.kernel;
+    if (chosen_dw)
+        *chosen_dw = b.plan_dw.kernel;
+    return st;
+}
+
+uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K)
+{
+    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? (size_t)M * (size_t)unpacked_pitch(K) * 2 : 0;
 }
 
 gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz, void *dz,

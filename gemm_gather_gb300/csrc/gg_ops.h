@@ -1,6 +1,7 @@
 // Declarations shared by the operators' translation units (host side): the
-// linear layer (linear_kernels.cu), the policy loss (loss_kernels.cu) and
-// AdamW (adamw_kernels.cu), whose C entry points are in gg_ops.cu.
+// linear layer (linear_kernels.cu), the policy loss (loss_kernels.cu), AdamW
+// (adamw_kernels.cu), the norm and 8-bit activations (norm_kernels.cu), whose C
+// entry points are in gg_ops.cu and gg_block_ops.cu.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -25,6 +26,7 @@ int op_inject_stall();
 constexpr int kEpiForward = 0;  // act(acc + bias) + aux, zout = acc + bias
 constexpr int kEpiGradIn = 1;   // acc * act'(aux)
 constexpr int kEpiGradW = 2;    // acc (+ out)
+constexpr int kEpiGradIn8 = 3;  // acc * act'(aux), aux kept in 8 bits (codes, with scales)
 
 struct LinearArgs {
     int64_t I, J, K;
@@ -39,6 +41,8 @@ struct LinearArgs {
     int bias_f32, act;
     const void *aux;       // residual (forward) or Z_in (input gradient); may be null
     int64_t ldaux;
+    const float *scales;   // kEpiGradIn8: aux's, one for GG_PACK_BLOCK features of a token
+    int64_t lds;
     void *zout;
     int64_t ldz;
     int chunk;             // k-blocks accumulated in TMEM before they are added in registers
@@ -65,7 +69,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &a, const LinearPlan &p, cud
 // Both gradients of a layer in one launch (plan_both: whether, and their tiles).
 bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &plan_dx, const LinearPlan &plan_dw,
                int path, int *bt_dx, int *bt_dw);
-cudaError_t launch_both(const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
+cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
                         const char **why);
 
 struct ColSumArgs {  // out[i] (+)= sum_j x[j*ldx + i]
@@ -85,6 +89,62 @@ struct ActBackwardArgs {  // dz = dy * act'(z)
     int is_bf16, act;
 };
 cudaError_t launch_act_backward(const ActBackwardArgs &a, cudaStream_t s);
+
+// ---- norm, 8-bit activations (norm_kernels.cu) -------------------------------------
+struct NormArgs {
+    const void *x, *residual, *weight;
+    int64_t ldx, ldr;
+    int weight_f32, weight_vec;  // weight_vec: 16-byte loads of weights are aligned
+    float eps;
+    void *h, *y;
+    int64_t ldh, ldy;
+    uint8_t *codes;
+    int64_t ldc;
+    float *scales;
+    int64_t lds;
+    float *rstd;
+    int64_t M, N;
+    int is_bf16;
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t s);
+
+struct NormBackwardArgs {
+    const void *dy, *h, *weight, *dh_in;
+    int64_t lddy, ldh, lddhin;
+    const float *rstd;
+    int weight_f32, weight_vec;
+    void *dh, *dweight;
+    int64_t lddh;
+    int grad_f32, accumulate;
+    float *partial;  // norm_backward_parts(M) rows of N sums, or null
+    int64_t M, N;
+    int is_bf16;
+};
+int norm_backward_parts(int64_t M);
+cudaError_t launch_norm_backward(const NormBackwardArgs &a, cudaStream_t s);
+
+struct PackArgs {
+    const void *x;
+    int64_t ldx;
+    uint8_t *codes;
+    int64_t ldc;
+    float *scales;
+    int64_t lds, M, N;
+    int is_bf16;
+};
+cudaError_t launch_pack(const PackArgs &a, cudaStream_t s);
+
+struct UnpackArgs {
+    const uint8_t *codes;
+    int64_t ldc;
+    const float *scales;
+    int64_t lds;
+    int act;
+    void *out;
+    int64_t ldo, M, N;
+    int is_bf16;
+};
+cudaError_t launch_unpack(const UnpackArgs &a, cudaStream_t s);
 
 // ---- policy loss -------------------------------------------------------------------
 struct LossArgs {

@@ -58,9 +58,11 @@
 #include <mutex>
 #include <type_traits>
 
+#include "act.cuh"
 #include "f32x2.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
+#include "pack8.cuh"
 #include "tc.cuh"
 
 namespace gg {
@@ -93,166 +95,18 @@ struct Shared {
 };
 
 // ---- epilogue arithmetic ---------------------------------------------------------
-__device__ __forceinline__ float load16(const void *p, int64_t at, int bf16)
+// An element of the tensor beside the sums.  One kept in 8 bits (its codes are at p) is taken in the
+// layer's 16-bit type, which holds its four significant bits.
+template <int EPI>
+__device__ __forceinline__ float load_aux(const LinearArgs &a, const void *p, int64_t ld, int64_t j, int64_t i)
 {
-    const uint16_t u = reinterpret_cast<const uint16_t *>(p)[at];
-    return bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-}
-
-__device__ __forceinline__ void store16(void *p, int64_t at, float v, int bf16)
-{
-    reinterpret_cast<uint16_t *>(p)[at] =
-        bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
-
-// Activations in float32, on pairs (two neighbouring tokens of a feature) where
-// the arithmetic comes in pairs.  relu keeps NaN (its slope there is 0).  gelu_tanh's 0.5 (1 + tanh u) is
-// the logistic function of 2u, which keeps its relative precision for u << 0.
-// gelu's normal distribution function has Abramowitz and Stegun's form (7.1.26),
-//     Phi(-x) = P(t) exp(-x^2 / 2),  t = 1 / (1 + 0.35 x),  x >= 0,
-// P of degree 7 without a constant, fitted here for the least relative error (a linear
-// program over 3000 points of [0, 13.5]): 1.5e-7 (1 + x^2 / 4), and 5e-7 at x < 1, 1.7e-6
-// at 6 as evaluated.  So Y = max(z, 0) - |z| Phi(-|z|) is as near in the left tail, where
-// it is tiny, as the power of two itself.  (7.1.26's own coefficients are within 7.5e-8 of
-// Phi, which at z = -4 is a float16's half ulp of Y and at -7 more than a bfloat16's ulp.)
-// The exponential is also the density that the derivative needs.  (With erff and a float
-// division, the epilogue of a 256 x 256 tile took longer than its MMAs at K = 3584.)
-__device__ __forceinline__ float ex2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float rcp_approx(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 1 / (1 + exp(-x))
-__device__ __forceinline__ float2 logistic(F2 x)
-{
-    const float2 e = halves_of(mul2(x, pair_of(-1.44269504f)));
-    const float2 d = halves_of(add2(pair_of(ex2_approx(e.x), ex2_approx(e.y)), pair_of(1.0f)));
-    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
-}
-
-// 2 sqrt(2/pi) (z + 0.044715 z^3)
-__device__ __forceinline__ F2 gelu_2u(F2 z, F2 zz)
-{
-    return mul2(z, fma2(zz, pair_of(0.071354816f), pair_of(1.59576912f)));
-}
-
-// Phi(-|z|), and exp(-z^2 / 2) in *e.
-__device__ __forceinline__ F2 normal_tail(float2 z, F2 zz, float2 *e)
-{
-    const float2 y = halves_of(mul2(zz, pair_of(-0.72134752f)));
-    *e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-    const float2 d = halves_of(fma2(pair_of(fabsf(z.x), fabsf(z.y)), pair_of(0.35f), pair_of(1.0f)));
-    const F2 t = pair_of(rcp_approx(d.x), rcp_approx(d.y));
-    F2 q = fma2(t, pair_of(0.0462695388f), pair_of(-0.190911355f));
-    q = fma2(t, q, pair_of(0.221250296f));
-    q = fma2(t, q, pair_of(0.00082826442f));
-    q = fma2(t, q, pair_of(0.146570468f));
-    q = fma2(t, q, pair_of(0.136159971f));
-    q = fma2(t, q, pair_of(0.139832881f));
-    return mul2(mul2(t, q), pair_of(e->x, e->y));
-}
-
-template <int ACT>
-__device__ __forceinline__ float2 act_value(float2 v)
-{
-    const F2 z = pair_of(v.x, v.y);
-    if constexpr (ACT == GG_ACT_RELU)
-        return make_float2(!(v.x <= 0.0f) ? v.x : 0.0f, !(v.y <= 0.0f) ? v.y : 0.0f);
-    if constexpr (ACT == GG_ACT_GELU) {
-        // max(z, 0) - |z| Phi(-|z|), |z| held below 64, where the product is long 0; NaN is in
-        // the tail
-        float2 e;
-        const F2 tail = normal_tail(v, mul2(z, z), &e);
-        const F2 size = pair_of(-fminf(fabsf(v.x), 64.0f), -fminf(fabsf(v.y), 64.0f));
-        return halves_of(fma2(size, tail, pair_of(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f))));
+    if constexpr (EPI == kEpiGradIn8) {
+        float x[4];
+        unpack4(reinterpret_cast<const uint8_t *>(p)[j * ld + i], x);
+        const float v = x[0] * a.scales[j * a.lds + i / kPackBlock];
+        return a.is_bf16 ? held16<true>(v) : pair16<false>(pair16_of<false>(held16<false>(v), 0.0f)).x;
     }
-    if constexpr (ACT == GG_ACT_GELU_TANH || ACT == GG_ACT_SILU) {
-        const float2 s = logistic(ACT == GG_ACT_SILU ? z : gelu_2u(z, mul2(z, z)));
-        return halves_of(mul2(z, pair_of(s.x, s.y)));
-    }
-    return v;
-}
-
-// x between -128 and 128, where every smooth slope is 0 or 1; NaN stays NaN.
-__device__ __forceinline__ float held128(float x)
-{
-    float y;
-    asm("min.NaN.f32 %0, %1, 0f43000000;\n\tmax.NaN.f32 %0, %0, 0fC3000000;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// The derivative at z.  A stored Z may be infinite where the sum was not (16 bits), and the
-// square of a large one is: the smooth slopes see z held between -128 and 128, so that
-// infinity times 0 meets none of them.
-template <int ACT>
-__device__ __forceinline__ float2 act_slope(float2 v)
-{
-    if constexpr (ACT != GG_ACT_RELU && ACT != GG_ACT_NONE)
-        v = make_float2(held128(v.x), held128(v.y));
-    const F2 z = pair_of(v.x, v.y);
-    if constexpr (ACT == GG_ACT_RELU)
-        return make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
-    if constexpr (ACT == GG_ACT_GELU) {  // Phi + z density
-        float2 e;
-        const float2 tail = halves_of(normal_tail(v, mul2(z, z), &e));
-        const float2 c = make_float2(v.x < 0.0f ? tail.x : 1.0f - tail.x, v.y < 0.0f ? tail.y : 1.0f - tail.y);
-        return halves_of(fma2(mul2(z, pair_of(0.39894228f)), pair_of(e.x, e.y), pair_of(c.x, c.y)));
-    }
-    if constexpr (ACT == GG_ACT_GELU_TANH) {  // d(z s)/dz = s + z s (1 - s) 2u'
-        const F2 zz = mul2(z, z);
-        const float2 h = logistic(gelu_2u(z, zz));
-        const F2 s = pair_of(h.x, h.y), rest = pair_of(1.0f - h.x, 1.0f - h.y);
-        const F2 du = fma2(zz, pair_of(0.21406445f), pair_of(1.59576912f));
-        return halves_of(fma2(mul2(mul2(z, s), rest), du, s));
-    }
-    if constexpr (ACT == GG_ACT_SILU) {  // s + z s (1 - s)
-        const float2 h = logistic(z);
-        const F2 s = pair_of(h.x, h.y), rest = pair_of(1.0f - h.x, 1.0f - h.y);
-        return halves_of(fma2(mul2(z, s), rest, s));
-    }
-    return make_float2(1.0f, 1.0f);
-}
-
-// v = act(v) and v *= act'(x), over an even number of values.
-template <int ACT, int C>
-__device__ __forceinline__ void apply_act(float (&v)[C])
-{
-#pragma unroll
-    for (int u = 0; u < C; u += 2) {
-        const float2 y = act_value<ACT>(make_float2(v[u], v[u + 1]));
-        v[u] = y.x, v[u + 1] = y.y;
-    }
-}
-template <int ACT, int C>
-__device__ __forceinline__ void apply_slope(float (&v)[C], const float (&x)[C])
-{
-#pragma unroll
-    for (int u = 0; u < C; u += 2) {
-        const float2 y = act_slope<ACT>(make_float2(x[u], x[u + 1]));
-        v[u] *= y.x, v[u + 1] *= y.y;
-    }
-}
-
-// f(ACT) with the activation as a compile-time constant.
-template <typename F>
-__device__ __forceinline__ void with_act(int act, F f)
-{
-    switch (act) {
-    case GG_ACT_RELU: f(std::integral_constant<int, GG_ACT_RELU>()); break;
-    case GG_ACT_GELU: f(std::integral_constant<int, GG_ACT_GELU>()); break;
-    case GG_ACT_GELU_TANH: f(std::integral_constant<int, GG_ACT_GELU_TANH>()); break;
-    case GG_ACT_SILU: f(std::integral_constant<int, GG_ACT_SILU>()); break;
-    default: f(std::integral_constant<int, GG_ACT_NONE>()); break;
-    }
+    return load16(p, j * ld + i, a.is_bf16);
 }
 
 // One feature's sums for columns j0, j0 + jstep, ... (n of them, at most C):
@@ -292,7 +146,7 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
     if (aux != nullptr) {
 #pragma unroll
         for (int u = 0; u < C; ++u)
-            x[u] = u < n ? load16(aux, (j0 + (int64_t)u * jstep) * ldaux + i, a.is_bf16) : 0.0f;
+            x[u] = u < n ? load_aux<EPI>(a, aux, ldaux, j0 + (int64_t)u * jstep, i) : 0.0f;
     }
     if constexpr (EPI == kEpiForward) {
 #pragma unroll
@@ -317,7 +171,7 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
             for (int u = 0; u < C; ++u)
                 v[u] += x[u];
         }
-    } else if constexpr (EPI == kEpiGradIn) {
+    } else if constexpr (EPI == kEpiGradIn || EPI == kEpiGradIn8) {
         float y[C];
 #pragma unroll
         for (int u = 0; u < C; ++u)
@@ -406,6 +260,58 @@ __device__ __forceinline__ void read_rows(const Rows &t, int64_t I, int64_t i0, 
     }
 }
 
+// The same of a tensor kept in 8 bits: a lane's eight features lie in one block of 128, under one
+// scale.
+template <bool BF16>
+__device__ __forceinline__ void read_codes(const LinearArgs &a, int64_t i, int64_t j0, int n, int lane, bool vec,
+                                           uint4 (&x)[kRowSteps])
+{
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(a.aux) + (j0 + (lane >> 2)) * a.ldaux + i;
+    const float *s = a.scales + (j0 + (lane >> 2)) * a.lds + i / kPackBlock;
+#pragma unroll
+    for (int k = 0; k < kRowSteps; ++k) {
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if ((lane >> 2) + 8 * k < n && i < a.I) {
+            const uint8_t *q = p + (int64_t)(8 * k) * a.ldaux;
+            uint2 c = make_uint2(0u, 0u);
+            if (vec && i + 8 <= a.I) {
+                c = *reinterpret_cast<const uint2 *>(q);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + u < a.I)
+                        (u < 4 ? c.x : c.y) |= (uint32_t)q[u] << (8 * (u & 3));
+            }
+            const float scale = s[(int64_t)(8 * k) * a.lds];
+            float v[4], w[4];
+            unpack4(c.x, v);
+            unpack4(c.y, w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                v[u] = held16<BF16>(v[u] * scale);
+                w[u] = held16<BF16>(w[u] * scale);
+            }
+            x[k] = make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]), pair16_of<BF16>(w[0], w[1]),
+                              pair16_of<BF16>(w[2], w[3]));
+        }
+    }
+}
+
+// The rows that an epilogue reads beside the sums.
+template <int EPI>
+__device__ __forceinline__ void read_aux(const LinearArgs &a, const Rows &t, int64_t i0, int64_t j0, int n, int lane,
+                                         uint4 (&x)[kRowSteps])
+{
+    if constexpr (EPI == kEpiGradIn8) {
+        if (a.is_bf16)
+            read_codes<true>(a, i0 + (lane & 3) * 8, j0, n, lane, t.vec, x);
+        else
+            read_codes<false>(a, i0 + (lane & 3) * 8, j0, n, lane, t.vec, x);
+    } else {
+        read_rows(t, a.I, i0, j0, n, lane, x);
+    }
+}
+
 __device__ __forceinline__ void stage_rows(uint8_t *stage, int lane, const uint4 (&x)[kRowSteps])
 {
 #pragma unroll
@@ -462,6 +368,11 @@ __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
 {
     if constexpr (EPI == kEpiGradW)
         return rows_of(a.accumulate && !a.out_f32 ? a.out : nullptr, a.ldo);
+    if constexpr (EPI == kEpiGradIn8) {  // codes: eight bytes a lane
+        Rows r = rows_of(a.aux, 0);
+        r.vec = ((reinterpret_cast<uint64_t>(a.aux) | (uint64_t)a.ldaux) & 7) == 0;
+        return r;
+    }
     return rows_of(a.aux, a.ldaux);
 }
 
@@ -511,7 +422,7 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
                 for (int u = 0; u < 16; ++u)
                     v[u] += x[u];
             }
-        } else if constexpr (EPI == kEpiGradIn) {
+        } else if constexpr (EPI == kEpiGradIn || EPI == kEpiGradIn8) {
             if (has_aux)
                 with_act(a.act, [&](auto k) { apply_slope<decltype(k)::value>(v, x); });
         } else if (has_aux) {
@@ -741,7 +652,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
         const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
         uint4 pre[kRowSteps];
         if (EPI != kEpiGradW && early)  // the first group's rows, while the MMAs run
-            read_rows(aux, a.I, i0, j0, valid_rows(end, j0), lane, pre);
+            read_aux<EPI>(a, aux, i0, j0, valid_rows(end, j0), lane, pre);
         float sum[EPI == kEpiGradW ? kCols : 1];
         if constexpr (EPI == kEpiGradW) {
 #pragma unroll
@@ -793,7 +704,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                     emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, at.stage_buf,
                                    [&](int col, float(&v)[16]) { from_tmem(g * kStep + col, v); });
                     if (early && g + 1 < kGroups)
-                        read_rows(aux, a.I, i0, jg + kStep, valid_rows(end, jg + kStep), lane, pre);
+                        read_aux<EPI>(a, aux, i0, jg + kStep, valid_rows(end, jg + kStep), lane, pre);
                 }
             }
             // accumulator read: hand it back to the leader's MMA warp
@@ -822,7 +733,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                 for (int g = 0; g < kGroups; ++g) {
                     const int64_t jg = j0 + g * kStep;
                     if (early)
-                        read_rows(aux, a.I, i0, jg, valid_rows(end, jg), lane, pre);
+                        read_aux<EPI>(a, aux, i0, jg, valid_rows(end, jg), lane, pre);
                     emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
                                    [&](int col, float(&v)[16]) {
 #pragma unroll
@@ -884,7 +795,7 @@ __device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p
         const Rows aux = aux_of<EPI>(a);
         uint4 pre[kRowSteps];
         if (aux.p)
-            read_rows(aux, a.I, i0, j0, n, lane, pre);
+            read_aux<EPI>(a, aux, i0, j0, n, lane, pre);
         emit_rows<EPI>(a, i0, j0, n, lane, bias, aux.p != nullptr, pre, at.stage_buf, joined);
     }
 }
@@ -1258,7 +1169,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                 for (int g = 0; parts == 1 && g < BT; g += kStageCols) {
                     const int n = valid_rows(a.J, jt + g) < BT - g ? valid_rows(a.J, jt + g) : BT - g;
                     if (aux.p)
-                        read_rows(aux, a.I, i0, jt + g, n, lane, pre);
+                        read_aux<EPI>(a, aux, i0, jt + g, n, lane, pre);
                     emit_rows<EPI>(a, i0, jt + g, n, lane, bias, aux.p != nullptr, pre, stage_buf,
                                 [&](int col, float(&v)[16]) {
                                     uint32_t r[16];
@@ -1295,7 +1206,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                     for (int g = 0; g < BT; g += kStageCols) {
                         const int n = valid_rows(a.J, jt + g);
                         if (aux.p)
-                            read_rows(aux, a.I, i0, jt + g, n, lane, pre);
+                            read_aux<EPI>(a, aux, i0, jt + g, n, lane, pre);
                         emit_rows<EPI>(a, i0, jt + g, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
                                        [&](int col, float(&v)[16]) {
 #pragma unroll
@@ -1819,7 +1730,15 @@ bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &pla
     return found;
 }
 
-cudaError_t launch_both(const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
+template <int EPI>
+static cudaError_t launch_both_of(const LinearArgs &x, int bt_dx, const LinearArgs &w, int bt_dw, cudaStream_t s,
+                                  const char **why)
+{
+    return bt_dx > 128 || bt_dw > 128 ? launch_pair<EPI, kEpiGradW, 256>(x, bt_dx, 1, &w, bt_dw, s, why)
+                                      : launch_pair<EPI, kEpiGradW, 128>(x, bt_dx, 1, &w, bt_dw, s, why);
+}
+
+cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
                         const char **why)
 {
     if (!tensor_maps_available()) {
@@ -1829,8 +1748,8 @@ cudaError_t launch_both(const LinearArgs &dx, int bt_dx, const LinearArgs &dw, i
     LinearArgs x = dx, w = dw;
     x.chunk = 1 << 30;
     w.chunk = kChunk;
-    return bt_dx > 128 || bt_dw > 128 ? launch_pair<kEpiGradIn, kEpiGradW, 256>(x, bt_dx, 1, &w, bt_dw, s, why)
-                                      : launch_pair<kEpiGradIn, kEpiGradW, 128>(x, bt_dx, 1, &w, bt_dw, s, why);
+    return epi == kEpiGradIn8 ? launch_both_of<kEpiGradIn8>(x, bt_dx, w, bt_dw, s, why)
+                              : launch_both_of<kEpiGradIn>(x, bt_dx, w, bt_dw, s, why);
 }
 
 cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, cudaStream_t s,
@@ -1847,6 +1766,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
     switch (epi) {
     case kEpiForward: return launch_epi<kEpiForward>(a, p, s, why);
     case kEpiGradIn: return launch_epi<kEpiGradIn>(a, p, s, why);
+    case kEpiGradIn8: return launch_epi<kEpiGradIn8>(a, p, s, why);
     default: return launch_epi<kEpiGradW>(a, p, s, why);
     }
 }

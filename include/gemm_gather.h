@@ -528,6 +528,126 @@ gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t l
                           gg_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Activations in 8 bits: what a backward pass needs of a forward pass, kept in
+ * about half the bytes.  An M x N matrix is M x N e4m3 codes (one byte each,
+ * row pitch ldc) and one float for every GG_PACK_BLOCK neighbouring elements of a
+ * row, M x ceil(N / GG_PACK_BLOCK) of them (row pitch lds); an element is its code
+ * times its block's float.  The float is the power of two that brings the
+ * block's largest finite magnitude into (224, 448], 2^-118 at least; codes are
+ * rounded to nearest, ties to even, so an element is off by half a step of four
+ * significant bits at most (2^-4 of it; 2^-10 times the float below 2^-6 times
+ * the float).  What is not finite is stored as NaN and does not enter the float.
+ *
+ * gg_pack8: x (M x N of `dtype`, GG_F16 or GG_BF16) to codes and scales.
+ * gg_unpack8: out = act(element), of type `dtype`, rounded once; an element that
+ * its rounding took beyond the type's range counts as the type's largest number.
+ * Any alignment and pitch (16-byte aligned rows and 8-byte aligned rows of codes are
+ * the fast case).
+ * ------------------------------------------------------------------------- */
+#define GG_PACK_BLOCK 128
+gg_status gg_pack8(const void *x, int64_t ldx, void *codes, int64_t ldc, float *scales, int64_t lds,
+                   int64_t M, int64_t N, gg_dtype dtype, gg_stream_t stream);
+gg_status gg_unpack8(const void *codes, int64_t ldc, const float *scales, int64_t lds,
+                     gg_activation act, void *out, int64_t ldo, int64_t M, int64_t N, gg_dtype dtype,
+                     gg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gg_linear_backward8 — gg_linear_backward of a layer whose input is X = act(P), with P
+ * (M x K) kept in 8 bits: the packed pre-activation of the layer below, or with
+ * GG_ACT_NONE the packed input itself (a norm's codes):
+ *   dX = (dZ W^T) act'(P), dW (+)= act(P)^T dZ, dbias (+)= the column sums of dZ.
+ * P is taken in `dtype` (as gg_unpack8 with GG_ACT_NONE gives it) for act', and X as
+ * gg_unpack8 gives it.  Types, layouts, alignment, accumulation and errors as for
+ * gg_linear_backward; codes and scales may have any alignment and pitch.
+ * workspace: device memory, 16-byte aligned, of at least
+ * gg_linear_backward8_workspace(M, K) bytes where dW is asked for (X in 16 bits), else
+ * not used.  What it held is lost; calls that may run at the same time, or replays of
+ * graphs that captured them, need workspaces of their own.
+ * ------------------------------------------------------------------------- */
+uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K);
+gg_status gg_linear_backward8(const void *dZ, int64_t lddz, const void *codes, int64_t ldc,
+                              const float *scales, int64_t lds, gg_activation act, const void *W,
+                              int64_t ldw, gg_weight_layout layout, void *dX, int64_t lddx, void *dW,
+                              int64_t lddw, void *dbias, gg_dtype grad_dtype, int accumulate,
+                              void *workspace, size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                              gg_dtype dtype, int *dev_status, gg_stream_t stream,
+                              gg_linear_path path);
+
+/* Validate a gg_linear_backward8 call exactly as the launching call does and launch
+ * nothing; *chosen_dx and *chosen_dw (nullable) receive the kernels of the two
+ * products. */
+gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *codes, int64_t ldc,
+                                    const float *scales, int64_t lds, gg_activation act, const void *W,
+                                    int64_t ldw, gg_weight_layout layout, const void *dX, int64_t lddx,
+                                    const void *dW, int64_t lddw, const void *dbias,
+                                    gg_dtype grad_dtype, int accumulate, const void *workspace,
+                                    size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                                    gg_dtype dtype, gg_linear_path path, int *chosen_dx, int *chosen_dw);
+
+/* ---------------------------------------------------------------------------
+ * gg_rms_norm — root-mean-square norm with the residual's addition:
+ *   h = x + residual (rounded to `dtype`; h = x without a residual)
+ *   rstd[m] = 1 / sqrt(mean over n of h[m, n]^2 + eps)
+ *   y = h rstd weight (rounded once)
+ * x, residual, h, y: M x N of `dtype` (GG_F16 or GG_BF16); weight: N elements of
+ * weight_dtype (`dtype` or GG_F32); rstd: M floats.  codes and scales (both or
+ * neither) receive y in 8 bits, as gg_pack8 of y gives it: what gg_linear_backward8
+ * needs of the layer that reads y.
+ * residual, h, rstd, codes and scales may be NULL, y only with codes.  h and y may each
+ * be x or residual (same pointer and pitch), not both the same one.  The squares are
+ * summed in float32: rows beyond 1e19 in size, or with an infinity, have rstd 0 (y is
+ * NaN at the infinity).  A row of zeros with eps 0, or one that holds NaN, gives NaN.
+ * Any alignment and pitch; 16-byte aligned rows (8-byte aligned codes) of up to 32768
+ * elements are the fast case, where each row is read once.
+ * ------------------------------------------------------------------------- */
+gg_status gg_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                      const void *weight, gg_dtype weight_dtype, float eps, void *h, int64_t ldh,
+                      void *y, int64_t ldy, void *codes, int64_t ldc, float *scales, int64_t lds,
+                      float *rstd, int64_t M, int64_t N, gg_dtype dtype, gg_stream_t stream);
+
+/* Validate a gg_rms_norm call exactly as the launching call does and launch nothing. */
+gg_status gg_rms_norm_check(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                            const void *weight, gg_dtype weight_dtype, float eps, const void *h,
+                            int64_t ldh, const void *y, int64_t ldy, const void *codes, int64_t ldc,
+                            const float *scales, int64_t lds, const float *rstd, int64_t M, int64_t N,
+                            gg_dtype dtype);
+
+/* ---------------------------------------------------------------------------
+ * gg_rms_norm_backward — gradients of y = h rstd weight, given dy (M x N), the
+ * h and rstd of the forward call:
+ *   u = h rstd,  g = dy weight
+ *   dh = rstd (g - u mean(g u)) + dh_in     (M x N of `dtype`, rounded once)
+ *   dweight (+)= sum over rows of dy u      (N of grad_dtype, `dtype` or GG_F32)
+ * dh_in (M x N or NULL) is what reaches h along the residual, so dh is the
+ * gradient of x and of the residual.  dh and dweight may each be NULL; dh may be dy, h
+ * or dh_in (same pointer and pitch).  accumulate != 0 adds to what dweight holds.  The
+ * sums over rows are float32, in an order fixed by M, N, the pitches and whether rows
+ * are 16-byte aligned.  M == 0 gives zero sums.
+ * workspace: 4-byte aligned device memory of at least
+ * gg_rms_norm_backward_workspace(M, N) bytes where dweight is asked for, else not used.
+ * What it held is lost; calls that may run at the same time, or replays of graphs that
+ * captured them, need workspaces of their own.
+ * Any alignment and pitch; 16-byte aligned rows of up to 16384 elements are the
+ * fast case.
+ * ------------------------------------------------------------------------- */
+uint64_t gg_rms_norm_backward_workspace(int64_t M, int64_t N);
+gg_status gg_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh,
+                               const float *rstd, const void *weight, gg_dtype weight_dtype,
+                               const void *dh_in, int64_t lddhin, void *dh, int64_t lddh, void *dweight,
+                               gg_dtype grad_dtype, int accumulate, void *workspace,
+                               size_t workspace_bytes, int64_t M, int64_t N, gg_dtype dtype,
+                               gg_stream_t stream);
+
+/* Validate a gg_rms_norm_backward call exactly as the launching call does and launch
+ * nothing. */
+gg_status gg_rms_norm_backward_check(const void *dy, int64_t lddy, const void *h, int64_t ldh,
+                                     const float *rstd, const void *weight, gg_dtype weight_dtype,
+                                     const void *dh_in, int64_t lddhin, const void *dh, int64_t lddh,
+                                     const void *dweight, gg_dtype grad_dtype, int accumulate,
+                                     const void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                                     gg_dtype dtype);
+
+/* ---------------------------------------------------------------------------
  * gg_policy_loss — the clipped policy loss of T sampled tokens with a KL term
  * to a reference policy, and its gradient, from the logits in one call:
  *   x      = logits[t, :] * inv_temperature
