@@ -37,7 +37,7 @@ __all__ = [
     "linear", "linear_check", "linear_backward", "linear_backward_check", "act_backward",
     "pack8", "unpack8", "linear_backward8", "linear_backward8_check", "linear_backward8_workspace",
     "rms_norm", "rms_norm_check", "rms_norm_backward", "rms_norm_backward_check", "rms_norm_backward_workspace",
-    "PACK_BLOCK",
+    "PACK_BLOCK", "linear_cross_entropy", "linear_cross_entropy_check", "linear_cross_entropy_workspace",
     "policy_loss", "policy_loss_check", "adamw", "adamw_check", "adamw_tensors", "AdamwTensors",
     "ADAMW_BLOCK", "ACTIVATIONS", "WEIGHT_LAYOUTS", "LINEAR_PATHS",
     "set_claim_policy",
@@ -603,6 +603,47 @@ def policy_loss_check(logits, ld: int, target, old_logp, ref_logp, advantage, we
                                                T, V, dtype, stats, logp_out, dlogits, ldd,
                                                inv_temperature, clip_low, clip_high, kl_coef,
                                                grad_scale)))
+
+
+def _entropy_args(X, ldx, W, ldw, layout, target, weight, stats, loss, lse, dX, lddx, dW, lddw, grad_dtype,
+                  accumulate, workspace, workspace_bytes, T, V, K, dtype, piece, grad_scale) -> tuple:
+    code, grad = _dtype(dtype), _dtype(grad_dtype)
+    t, f = _TORCH_DTYPES.get(code), _F32
+    w_rows, w_cols = (K, V) if layout == "kn" else (V, K)
+    room, room_bytes = _room(workspace, workspace_bytes)
+    return (_held(X, "X", t, T, K), ldx, _held(W, "W", t, w_rows if T > 0 else 0, w_cols), ldw,
+            WEIGHT_LAYOUTS[layout], _vector(target, "target", _I64, T), _vector(weight, "weight", f, T),
+            _vector(stats, "stats", f, 2), _vector(loss, "loss", f, T), _vector(lse, "lse", f, T),
+            _held(dX, "dX", t, T, K), lddx, _held(dW, "dW", _TORCH_DTYPES.get(grad), w_rows, w_cols), lddw, grad,
+            1 if accumulate else 0, room, room_bytes, T, V, K, code, piece, grad_scale)
+
+
+def linear_cross_entropy(X, ldx: int, W, ldw: int, layout: str, target, weight, stats, loss, lse, dX, lddx: int, dW,
+                         lddw: int, grad_dtype, accumulate: bool, workspace, T: int, V: int, K: int, dtype,
+                         piece: int = 0, grad_scale: float = 1.0, status=None, stream=None,
+                         workspace_bytes=None) -> None:
+    """Softmax cross entropy over a vocabulary from the hidden states X and the weight W, without storing the
+    logits, and its gradients dX and dW (either or both may be None: no gradient) (gg_linear_cross_entropy).
+    Targets are int64; tokens of weight 0 are masked.  ``grad_dtype`` is dW's type.  ``workspace``: a contiguous
+    tensor on the GPU of at least ``linear_cross_entropy_workspace(...)`` bytes.  Tensors are checked as for ``linear``."""
+    check(lib.gg_linear_cross_entropy(*_entropy_args(X, ldx, W, ldw, layout, target, weight, stats, loss, lse, dX, lddx,
+                                                     dW, lddw, grad_dtype, accumulate, workspace, workspace_bytes, T, V,
+                                                     K, dtype, piece, grad_scale),
+                                      _word(status), _stream(stream)))
+
+
+def linear_cross_entropy_check(X, ldx: int, W, ldw: int, layout: str, target, weight, stats, loss, lse, dX, lddx: int,
+                               dW, lddw: int, grad_dtype, accumulate: bool, workspace, T: int, V: int, K: int, dtype,
+                               piece: int = 0, grad_scale: float = 1.0, workspace_bytes=None) -> None:
+    """Validate without launching."""
+    check(lib.gg_linear_cross_entropy_check(*_entropy_args(X, ldx, W, ldw, layout, target, weight, stats, loss, lse, dX,
+                                                           lddx, dW, lddw, grad_dtype, accumulate, workspace,
+                                                           workspace_bytes, T, V, K, dtype, piece, grad_scale)))
+
+
+def linear_cross_entropy_workspace(T: int, V: int, K: int, piece: int = 0, gradients: bool = True) -> int:
+    """Bytes of ``linear_cross_entropy``'s workspace; ``gradients``: whether dX or dW is asked for."""
+    return lib.gg_linear_cross_entropy_workspace(T, V, K, piece, 1 if gradients else 0)
 
 
 class AdamwTensors:

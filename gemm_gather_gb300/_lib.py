@@ -54,7 +54,8 @@ EXPORTS = (
     "gg_linear", "gg_linear_check", "gg_linear_backward", "gg_linear_backward_check",
     "gg_act_backward", "gg_pack8", "gg_unpack8", "gg_linear_backward8", "gg_linear_backward8_check",
     "gg_linear_backward8_workspace", "gg_rms_norm", "gg_rms_norm_check", "gg_rms_norm_backward",
-    "gg_rms_norm_backward_check", "gg_rms_norm_backward_workspace", "gg_policy_loss", "gg_policy_loss_check", "gg_adamw", "gg_adamw_check",
+    "gg_rms_norm_backward_check", "gg_rms_norm_backward_workspace", "gg_linear_cross_entropy", "gg_linear_cross_entropy_check",
+    "gg_linear_cross_entropy_workspace", "gg_policy_loss", "gg_policy_loss_check", "gg_adamw", "gg_adamw_check",
     "gg_set_claim_policy", "gg_get_claim_policy", "gg_set_store_policy", "gg_get_store_policy",
     "gg_set_wait_limit_ns", "gg_get_wait_limit_ns", "gg_debug_inject_stall",
     "gg_device_status", "gg_clear_device_status",
@@ -139,24 +140,29 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
         "gg_pack8": ([vp, n64, vp, n64, vp, n64, n64, n64, i32, vp], i32),
         "gg_unpack8": ([vp, n64, vp, n64, i32, vp, n64, n64, n64, i32, vp], i32),
         "gg_linear_backward8": ([vp, n64, vp, n64, vp, n64, i32, vp, n64, i32, vp, n64, vp, n64, vp, i32, i32,
-                                 vp, sz, n64, n64, n64, i32, vp, vp, i32], i32),
+                                 vp, n64, n64, n64, n64, i32, vp, vp, i32], i32),
         "gg_linear_backward8_check": ([vp, n64, vp, n64, vp, n64, i32, vp, n64, i32, vp, n64, vp, n64, vp, i32,
-                                       i32, vp, sz, n64, n64, n64, i32, i32, ctypes.POINTER(i32),
+                                       i32, vp, n64, n64, n64, n64, i32, i32, ctypes.POINTER(i32),
                                        ctypes.POINTER(i32)], i32),
         "gg_linear_backward8_workspace": ([i64, i64], u64),
         "gg_rms_norm": ([vp, n64, vp, n64, vp, i32, f32, vp, n64, vp, n64, vp, n64, vp, n64, vp, n64, n64, i32,
                          vp], i32),
         "gg_rms_norm_check": ([vp, n64, vp, n64, vp, i32, f32, vp, n64, vp, n64, vp, n64, vp, n64, vp, n64, n64,
                                i32], i32),
-        "gg_rms_norm_backward": ([vp, n64, vp, n64, vp, vp, i32, vp, n64, vp, n64, vp, i32, i32, vp, sz, n64, n64,
+        "gg_rms_norm_backward": ([vp, n64, vp, n64, vp, vp, i32, vp, n64, vp, n64, vp, i32, i32, vp, n64, n64, n64,
                                   i32, vp], i32),
-        "gg_rms_norm_backward_check": ([vp, n64, vp, n64, vp, vp, i32, vp, n64, vp, n64, vp, i32, i32, vp, sz, n64,
+        "gg_rms_norm_backward_check": ([vp, n64, vp, n64, vp, vp, i32, vp, n64, vp, n64, vp, i32, i32, vp, n64, n64,
                                         n64, i32], i32),
         "gg_rms_norm_backward_workspace": ([i64, i64], u64),
         "gg_policy_loss": ([vp, n64, vp, vp, vp, vp, vp, n64, n64, i32, f32, f32, f32, f32, f32, vp, vp,
                             vp, n64, vp, vp], i32),
         "gg_policy_loss_check": ([vp, n64, vp, vp, vp, vp, vp, n64, n64, i32, f32, f32, f32, f32, f32,
                                   vp, vp, vp, n64], i32),
+        "gg_linear_cross_entropy": ([vp, n64, vp, n64, i32, vp, vp, vp, vp, vp, vp, n64, vp, n64, i32, i32, vp, n64,
+                                     n64, n64, n64, i32, n64, f32, vp, vp], i32),
+        "gg_linear_cross_entropy_check": ([vp, n64, vp, n64, i32, vp, vp, vp, vp, vp, vp, n64, vp, n64, i32, i32, vp,
+                                           n64, n64, n64, n64, i32, n64, f32], i32),
+        "gg_linear_cross_entropy_workspace": ([i64, i64, i64, i64, i32], u64),
         "gg_adamw": ([vp, i32, i64, f64, f64, f64, f64, f64, vp, u64, vp], i32),
         "gg_adamw_check": ([vp, i32, i64, f64, f64, f64, f64, f64, vp], i32),
         "gg_set_claim_policy": ([i32], i32),

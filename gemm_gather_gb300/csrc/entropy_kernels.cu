@@ -1,0 +1,344 @@
+// Softmax cross entropy of a vocabulary's logits z = X W that are never stored, and its gradients, for
+// sm_103a: what stands around the products (linear_kernels.cu).
+//
+//     lse = log sum exp z,  loss = lse - z[target],  stats = sums of weight loss and of weight
+//     dZ = weight (softmax(z) - onehot(target)),  dX = dZ W^T,  dW = X^T dZ
+//
+// 1. tokens_kernel counts the tokens whose weight is not 0 and gathers their rows of X: a masked token
+//    costs no multiplication, and what its row holds (NaN, say) meets nothing.
+// 2. The product z = X W over the whole vocabulary, in 32-bit sums that stay on chip: its epilogue keeps
+//    of every 32 entries the largest logit and the sum of exponentials (8 bytes for 32 logits).
+// 3. join_kernel makes lse and loss of them.
+// 4. For a piece of the vocabulary at a time: the product again, its epilogue turning the logits into
+//    dZ in 16 bits; then dX += dZ W^T (float32, in memory) and the piece's dW = X^T dZ in one launch.
+// 5. dx_kernel rounds dX once, in the tokens' own order, zeros for the masked ones.
+//
+// Logits are multiplied twice (8 T V K operations instead of 6) so that they need not be kept, nor rounded
+// to 16 bits before the softmax.  dZ is the only 16-bit step: weights enter it times a power of two that
+// takes the largest into [2^13, 2^14), which keeps probabilities down to 2^-27 at float16's full
+// precision whatever the weights' size, and leaves dX and dW again in float32.
+//
+// Bound: the tensor cores, under the power limit.
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "gg_internal.h"
+#include "gg_ops.h"
+#include "pack8.cuh"
+#include "tc.cuh"
+
+namespace gg {
+namespace {
+
+using namespace tc;
+
+constexpr int kSMs = 152;
+constexpr int kThreads = 1024;
+constexpr int kEach = 16;                      // tokens of a thread at a time
+constexpr int kChunkTokens = kThreads * kEach;
+constexpr int kMaxRows = 64;                   // rows a block copies for one such chunk
+constexpr int kPad = 64;                       // a k-block of the products
+
+// What the blocks of a launch share out: at most kChunkTokens / kBlocks + 1 rows each.
+constexpr int kBlocks = 2 * kSMs;
+static_assert(kChunkTokens / kBlocks + 2 <= kMaxRows, "a block's list of rows");
+
+__device__ __forceinline__ void copy_row(uint16_t *to, const uint16_t *from, int64_t K, int lane)
+{
+    const int64_t whole = K / 8;
+    int64_t c = lane;
+    for (; c + 96 < whole; c += 128) {
+        uint4 q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            q[u] = reinterpret_cast<const uint4 *>(from)[c + 32 * u];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            reinterpret_cast<uint4 *>(to)[c + 32 * u] = q[u];
+    }
+    for (; c < whole; c += 32)
+        reinterpret_cast<uint4 *>(to)[c] = reinterpret_cast<const uint4 *>(from)[c];
+    if (whole * 8 + lane < K)
+        to[whole * 8 + lane] = from[whole * 8 + lane];
+}
+
+// Every block counts all the tokens (so that none waits for another) and copies its share of rows.
+__global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant__ EntropyArgs a)
+{
+    __shared__ int counts[kEach * 32], offsets[kEach * 32], sums[kEach];
+    __shared__ int list_token[kMaxRows], list_place[kMaxRows], listed;
+    __shared__ float tops[32];
+    wait_dependencies();
+    launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t blocks = gridDim.x, me = blockIdx.x;
+    int64_t base = 0;
+    float top = 0.0f;
+    for (int64_t c0 = 0; c0 < a.T; c0 += kChunkTokens) {
+        float w[kEach];
+        int64_t tg[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int64_t t = c0 + k * kThreads + threadIdx.x;
+            w[k] = t < a.T ? a.weight[t] : 0.0f;
+            tg[k] = t < a.T ? a.target[t] : 0;
+        }
+        unsigned live[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            bool counts_in = w[k] != 0.0f;
+            if (counts_in && (tg[k] < 0 || tg[k] >= a.V)) {
+                counts_in = false;
+                if (me == 0)
+                    report_status(a.status, GG_ERR_INVALID_ARG);
+            }
+            live[k] = __ballot_sync(0xffffffffu, counts_in);
+            if (counts_in)
+                top = pack_top(top, w[k]);
+            if (lane == 0)
+                counts[k * 32 + warp] = __popc(live[k]);
+        }
+        if (threadIdx.x == 0)
+            listed = 0;
+        __syncthreads();
+        if (warp < kEach) {  // warp k: the 32 warps of step k
+            const int own = counts[warp * 32 + lane];
+            int sum = own;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int other = __shfl_up_sync(0xffffffffu, sum, d);
+                sum += lane >= d ? other : 0;
+            }
+            offsets[warp * 32 + lane] = sum - own;
+            if (lane == 31)
+                sums[warp] = sum;
+        }
+        __syncthreads();
+        int before = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int64_t t = c0 + k * kThreads + threadIdx.x;
+            const bool on = live[k] >> lane & 1;
+            const int64_t p = base + before + offsets[k * 32 + warp] + __popc(live[k] & ((1u << lane) - 1u));
+            before += sums[k];
+            if (on && p % blocks == me) {
+                const int at = atomicAdd(&listed, 1);
+                list_token[at] = (int)t;
+                list_place[at] = (int)p;
+            }
+            // the small per-token arrays: a warp's 32 tokens by one block
+            if (t < a.T && (t / 32) % blocks == me) {
+                a.place[t] = on ? (int)p : -1;
+                if (on) {
+                    a.token[p] = (int)t;
+                    a.tgt[p] = (int)tg[k];
+                    a.wt[p] = w[k];
+                } else {
+                    a.loss[t] = 0.0f;
+                    if (a.lse)
+                        a.lse[t] = 0.0f;
+                }
+            }
+        }
+        __syncthreads();
+        for (int r = warp; r < listed; r += 32)
+            copy_row(reinterpret_cast<uint16_t *>(a.x) + (int64_t)list_place[r] * a.ldw,
+                     reinterpret_cast<const uint16_t *>(a.X) + (int64_t)list_token[r] * a.ldx, a.K, lane);
+        base += before;
+        __syncthreads();  // the lists and counts are written again
+    }
+    const int n = (int)base;
+    const int64_t pad = gg_min64(a.T, (base + kPad - 1) / kPad * kPad);
+    for (int64_t p = base + warp; p < pad; p += 32)
+        if (p % blocks == me) {
+            uint16_t *row = reinterpret_cast<uint16_t *>(a.x) + p * a.ldw;
+            for (int64_t c = lane; c < a.K; c += 32)
+                row[c] = 0;
+            if (lane == 0) {
+                a.tgt[p] = -1;
+                a.wt[p] = 0.0f;
+            }
+        }
+    if (me != 0)
+        return;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane == 0)
+        tops[warp] = top;
+    __syncthreads();
+    if (warp > 0)
+        return;
+    top = tops[lane];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane == 0) {
+        const int e = top > 0.0f ? ilogbf(top) : 13;
+        const int k = 13 - e < -100 ? -100 : (13 - e > 100 ? 100 : 13 - e);
+        a.head->live = n;
+        a.head->live_pad = (int)pad;
+        a.head->ticket = 0;
+        a.head->scale = power_of_two(k);
+        a.head->alpha = a.grad_scale * power_of_two(-k);
+    }
+}
+
+// (largest, sum) of two parts.
+__device__ __forceinline__ void merge(float &m, float &s, float m1, float s1)
+{
+    const float top = fmaxf(m, m1);
+    if (top == -INFINITY) {  // nothing yet; a NaN's sum is NaN and stays
+        s += s1;
+        return;
+    }
+    s = s * expf(m - top) + s1 * expf(m1 - top);
+    m = top;
+}
+
+// 32 tokens a block, 32 shares of the rows.
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ EntropyArgs a)
+{
+    __shared__ float ms[32][33], ss[32][33];
+    __shared__ unsigned turn;
+    __shared__ double sums[2][32];
+    wait_dependencies();
+    launch_dependents();
+    const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int live = a.head->live, pad = a.head->live_pad;
+    const int64_t p = (int64_t)blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.0f;
+    if (p < live) {
+#pragma unroll 4
+        for (int64_t r = g; r < a.rows; r += 32) {
+            const float2 q = a.partial[r * a.T + p];
+            merge(m, s, q.x, q.y);
+        }
+    }
+    ms[g][lane] = m;
+    ss[g][lane] = s;
+    __syncthreads();
+    if (g == 0 && p < pad) {
+        float lse = 0.0f;
+        if (p < live) {
+#pragma unroll 1
+            for (int k = 1; k < 32; ++k)
+                merge(m, s, ms[k][lane], ss[k][lane]);
+            lse = m + logf(s);
+            const float loss = lse - a.ztarget[p];
+            const int t = a.token[p];
+            a.loss[t] = loss;
+            if (a.lse)
+                a.lse[t] = lse;
+            a.lossc[p] = loss;
+        }
+        a.lsec[p] = lse;
+        a.coef[p] = a.wt[p] * a.head->scale;
+    }
+    if (!a.stats)
+        return;
+    // the last block to be done adds up the statistics, in an order that does not depend on which it is
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        turn = atomicAdd(&a.head->ticket, 1u);
+    __syncthreads();
+    if (turn + 1 != gridDim.x)
+        return;
+    __threadfence();
+    double loss = 0.0, weight = 0.0;
+    for (int k = threadIdx.x; k < live; k += kThreads) {
+        const double w = (double)a.wt[k];
+        loss += w * (double)__ldcg(a.lossc + k);
+        weight += w;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        loss += __shfl_xor_sync(0xffffffffu, loss, d);
+        weight += __shfl_xor_sync(0xffffffffu, weight, d);
+    }
+    if (lane == 0) {
+        sums[0][g] = loss;
+        sums[1][g] = weight;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        double t = 0.0;
+        for (int k = 0; k < 32; ++k)
+            t += sums[threadIdx.x][k];
+        a.stats[threadIdx.x] = (float)t;
+    }
+}
+
+// V elements per thread and step (8 where dX's rows are 16-byte aligned).
+template <bool BF16, int V>
+__global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ EntropyArgs a)
+{
+    wait_dependencies();
+    launch_dependents();
+    const float alpha = a.head->alpha;
+    const int64_t units = (a.K + V - 1) / V, total = a.T * units;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / units, n = (i - t * units) * V;
+        const int p = a.place[t];
+        uint16_t *out = reinterpret_cast<uint16_t *>(a.dX) + t * a.lddx + n;
+        const float *from = a.dx32 + p * a.ldw + n;  // (rows of whole 8 elements)
+        if constexpr (V == 8) {
+            float v[8] = {};
+            if (p >= 0) {
+                const float4 x = *reinterpret_cast<const float4 *>(from), y = *reinterpret_cast<const float4 *>(from + 4);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] *= alpha;
+            store8(out, a.K - n,
+                   p >= 0 ? make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]),
+                                       pair16_of<BF16>(v[4], v[5]), pair16_of<BF16>(v[6], v[7]))
+                          : make_uint4(0u, 0u, 0u, 0u));
+        } else {
+            store16(out, 0, p >= 0 ? *from * alpha : 0.0f, BF16);
+        }
+    }
+}
+
+// A launch that may begin its set-up while the one before it on the stream ends.
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, const EntropyArgs &a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s)
+{
+    return launch(tokens_kernel, gg_min64(a.T, kBlocks), kThreads, s, a);
+}
+
+cudaError_t launch_entropy_join(const EntropyArgs &a, cudaStream_t s)
+{
+    return launch(join_kernel, (a.T + 31) / 32, kThreads, s, a);
+}
+
+cudaError_t launch_entropy_dx(const EntropyArgs &a, cudaStream_t s)
+{
+    const bool wide = ((reinterpret_cast<uint64_t>(a.dX) | (uint64_t)(a.lddx * 2)) & 15) == 0;
+    const int64_t total = a.T * (wide ? (a.K + 7) / 8 : a.K);
+    const int64_t grid = gg_min64((total + 255) / 256, kSMs * 8);
+    if (wide)
+        return launch(a.is_bf16 ? dx_kernel<true, 8> : dx_kernel<false, 8>, grid, 256, s, a);
+    return launch(a.is_bf16 ? dx_kernel<true, 1> : dx_kernel<false, 1>, grid, 256, s, a);
+}
+
+}  // namespace gg

@@ -1,4 +1,5 @@
-// C entry points of the norm and of activations in 8 bits: argument validation and launches.
+// C entry points of the norm, of activations in 8 bits and of the vocabulary's cross entropy: argument
+// validation and launches.
 // Declared in include/gemm_gather.h.
 #include <cuda_runtime.h>
 
@@ -76,7 +77,7 @@ gg_status prepare_norm(const void *x, int64_t ldx, const void *residual, int64_t
 gg_status prepare_norm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const float *rstd,
                                 const void *weight, gg_dtype weight_dtype, const void *dh_in, int64_t lddhin,
                                 const void *dh, int64_t lddh, const void *dweight, gg_dtype grad_dtype,
-                                int accumulate, const void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                                int accumulate, const void *workspace, uint64_t workspace_bytes, int64_t M, int64_t N,
                                 gg_dtype dtype, NormBackwardArgs *out)
 {
     GG_TRY(check_16bit(dtype, "rms_norm_backward"));
@@ -95,7 +96,7 @@ gg_status prepare_norm_backward(const void *dy, int64_t lddy, const void *h, int
     GG_TRY(check_mat(min, false));
     GG_TRY(check_mat(mo, false));
     GG_TRY(check_mat(mg, false));
-    const size_t need = dweight ? gg_rms_norm_backward_workspace(M, N) : 0;
+    const uint64_t need = dweight ? gg_rms_norm_backward_workspace(M, N) : 0;
     if (workspace_bytes < need || (need && !workspace))
         return op_fail(GG_ERR_INVALID_ARG, "workspace: %llu bytes are needed", (unsigned long long)need);
     const int64_t parts = need ? norm_backward_parts(M) : 0;
@@ -118,9 +119,316 @@ gg_status prepare_norm_backward(const void *dy, int64_t lddy, const void *h, int
     return op_ok();
 }
 
+// ---- cross entropy --------------------------------------------------------------------------
+// A piece of the vocabulary: as many columns as make the float32 additions of dX a small part of
+// its products (8 bytes against 2 piece operations for an element of dX), so that the gradient of
+// its logits is what takes memory; equal pieces, in whole 128.
+constexpr int64_t kPiece = 32768;
+
+int64_t piece_of(int64_t V, int64_t piece)
+{
+    if (piece == 0) {
+        const int64_t n = (V + kPiece - 1) / kPiece;
+        piece = n > 0 ? (V + n - 1) / n : 0;
+    }
+    piece = (piece + 127) / 128 * 128;
+    const int64_t most = (V + 127) / 128 * 128;
+    return piece < most ? piece : most;
+}
+
+// The workspace's parts, one behind the other on 256-byte boundaries.
+struct EntropyPlaces {
+    uint64_t x, place, token, tgt, wt, lossc, lsec, coef, ztarget, partial, dx32, dz, end;
+};
+
+EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, bool gradients)
+{
+    EntropyPlaces w{};
+    uint64_t at = 256;  // EntropyHead
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const uint64_t t = (uint64_t)T, kp = (uint64_t)((K + 7) / 8 * 8);
+    w.x = take(t * kp * 2);
+    for (uint64_t *p : {&w.place, &w.token, &w.tgt, &w.wt, &w.lossc, &w.lsec, &w.coef, &w.ztarget})
+        *p = take(t * 4);
+    w.partial = take(t * (uint64_t)((V + 31) / 32) * 8);
+    if (gradients) {
+        w.dx32 = take(t * kp * 4);
+        w.dz = take(t * (uint64_t)piece_of(V, piece) * 2);
+    }
+    w.end = at;
+    return w;
+}
+
+struct Entropy {
+    EntropyArgs a;
+    const void *W;
+    int64_t ldw;
+    bool kn;
+    void *dW;
+    int64_t lddw;
+    int grad_f32, accumulate;
+    uint16_t *dz;
+    int64_t piece;
+};
+
+gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw, gg_weight_layout layout,
+                          const int64_t *target, const float *weight, const float *stats, const float *loss,
+                          const float *lse, const void *dX, int64_t lddx, const void *dW, int64_t lddw,
+                          gg_dtype grad_dtype, int accumulate, const void *workspace, uint64_t workspace_bytes,
+                          int64_t T, int64_t V, int64_t K, gg_dtype dtype, int64_t piece, float grad_scale,
+                          Entropy *out)
+{
+    GG_TRY(check_16bit(dtype, "linear_cross_entropy"));
+    GG_TRY(check_route(layout, GG_LINEAR_AUTO));
+    GG_TRY(check_sizes(T, V, K));
+    if (T > 0 && V == 0)
+        return op_fail(GG_ERR_INVALID_ARG, "a token needs a vocabulary: V must be >= 1");
+    if (piece < 0 || piece % 128 != 0)
+        return op_fail(GG_ERR_INVALID_ARG, "piece must be 0 or a positive multiple of 128");
+    if (!std::isfinite(grad_scale))
+        return op_fail(GG_ERR_INVALID_ARG, "grad_scale must be finite");
+    if (dW && grad_dtype != dtype && grad_dtype != GG_F32)
+        return op_fail(GG_ERR_UNSUPPORTED, "dW is of the layer's type or GG_F32");
+    const bool kn = layout == GG_WEIGHT_KN;
+    const int64_t used = T > 0 ? V : 0;  // entries that W is read for
+    const Mat x{"X", X, T, K, ldx, 2}, w{"W", W, kn ? (T > 0 ? K : 0) : used, kn ? used : K, ldw, 2};
+    const Mat tg{"target", target, 1, T, T, 8}, we{"weight", weight, 1, T, T, 4};
+    const Mat st{"stats", stats, 1, 2, 2, 4}, lo{"loss", loss, 1, T, T, 4}, ls{"lse", lse, 1, T, T, 4};
+    const Mat gx{"dX", dX, T, K, lddx, 2},
+        gw{"dW", dW, kn ? K : V, kn ? V : K, lddw, grad_dtype == GG_F32 ? 4 : 2};
+    GG_TRY(check_mat(x, true));
+    GG_TRY(check_mat(w, true));
+    GG_TRY(check_tma(x));
+    GG_TRY(check_tma(w));
+    GG_TRY(check_mat(tg, true));
+    GG_TRY(check_mat(we, true));
+    GG_TRY(check_mat(st, false));
+    GG_TRY(check_mat(lo, true));
+    GG_TRY(check_mat(ls, false));
+    GG_TRY(check_mat(gx, false));
+    GG_TRY(check_mat(gw, false));
+    const bool gradients = dX || dW;
+    const uint64_t need = T > 0 ? entropy_places(T, V, K, piece, gradients).end : 0;
+    if (need >= (uint64_t)1 << 59)
+        return op_fail(GG_ERR_UNSUPPORTED, "the workspace passes 2^59 bytes");
+    if (workspace_bytes < need || (need && !workspace))
+        return op_fail(GG_ERR_INVALID_ARG, "workspace: %llu bytes are needed", (unsigned long long)need);
+    if (need && reinterpret_cast<uint64_t>(workspace) % 16 != 0)
+        return op_fail(GG_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    const Mat ws{"workspace", workspace, need ? 1 : 0, (int64_t)need, (int64_t)need, 1};
+    const Mat *outs[] = {&st, &lo, &ls, &gx, &gw, &ws};
+    for (const Mat *o : outs) {
+        for (const Mat *in : {&x, &w, &tg, &we})
+            if (!(o == &gx && in == &x && same(gx, x)))
+                GG_TRY(check_apart(*o, *in));
+        for (const Mat *p : outs)
+            if (o < p)
+                GG_TRY(check_apart(*o, *p));
+    }
+    const EntropyPlaces at = entropy_places(T, V, K, piece, gradients);
+    uint8_t *const base = reinterpret_cast<uint8_t *>(const_cast<void *>(workspace));
+    const auto floats = [&](uint64_t o) { return reinterpret_cast<float *>(base + o); };
+    const auto ints = [&](uint64_t o) { return reinterpret_cast<int *>(base + o); };
+    Entropy e{};
+    if (need) {
+        e.a.head = reinterpret_cast<EntropyHead *>(base);
+        e.a.x = base + at.x;
+        e.a.place = ints(at.place);
+        e.a.token = ints(at.token);
+        e.a.tgt = ints(at.tgt);
+        e.a.wt = floats(at.wt);
+        e.a.lossc = floats(at.lossc);
+        e.a.lsec = floats(at.lsec);
+        e.a.coef = floats(at.coef);
+        e.a.ztarget = floats(at.ztarget);
+        e.a.partial = reinterpret_cast<float2 *>(base + at.partial);
+        e.a.dx32 = gradients ? floats(at.dx32) : nullptr;
+        e.dz = gradients ? reinterpret_cast<uint16_t *>(base + at.dz) : nullptr;
+    }
+    e.a.X = X;
+    e.a.ldx = ldx;
+    e.a.target = target;
+    e.a.weight = weight;
+    e.a.T = T;
+    e.a.V = V;
+    e.a.K = K;
+    e.a.is_bf16 = dtype == GG_BF16;
+    e.a.grad_scale = grad_scale;
+    e.a.stats = const_cast<float *>(stats);
+    e.a.loss = const_cast<float *>(loss);
+    e.a.lse = const_cast<float *>(lse);
+    e.a.dX = const_cast<void *>(dX);
+    e.a.lddx = lddx;
+    e.a.ldw = (K + 7) / 8 * 8;
+    e.a.rows = (V + 31) / 32;
+    e.W = W;
+    e.ldw = ldw;
+    e.kn = kn;
+    e.dW = const_cast<void *>(dW);
+    e.lddw = lddw;
+    e.grad_f32 = grad_dtype == GG_F32;
+    e.accumulate = accumulate != 0;
+    e.piece = piece_of(V, piece);
+    *out = e;
+    return op_ok();
+}
+
+gg_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? GG_OK : op_cuda_fail(e, what); }
+
+gg_status product(int epi, const LinearArgs &a, cudaStream_t s)
+{
+    const char *why = nullptr;
+    const cudaError_t e = launch_linear(epi, a, plan_linear(epi, a, GG_LINEAR_AUTO), s, &why);
+    return launched(e, why ? why : "launching a product of the vocabulary");
+}
+
+gg_status run_entropy(const Entropy &e, cudaStream_t s)
+{
+    const EntropyArgs &a = e.a;
+    LinearArgs l{};
+    l.is_bf16 = a.is_bf16;
+    l.status = a.status;
+    l.wait_limit_ns = op_wait_limit_ns();
+    l.inject_stall = op_inject_stall();
+    if (a.T == 0) {
+        if (a.stats)
+            GG_TRY(launched(cudaMemsetAsync(a.stats, 0, 8, s), "clearing the statistics"));
+        if (e.dW && !e.accumulate) {  // the sum over no tokens
+            l.I = e.kn ? a.V : a.K;
+            l.J = e.kn ? a.K : a.V;
+            l.out = e.dW;
+            l.ldo = e.lddw;
+            l.out_f32 = e.grad_f32;
+            GG_TRY(product(kEpiGradW, l, s));
+        }
+        return op_ok();
+    }
+    const int64_t es = 2;
+    const auto entries = [&](int64_t v0) {  // W from entry v0 on
+        return reinterpret_cast<const uint8_t *>(e.W) + v0 * (e.kn ? 1 : e.ldw) * es;
+    };
+    // logits of entries v0 on: features are entries, columns are tokens
+    const auto logits = [&](int64_t v0, int64_t n, const int *live) {
+        LinearArgs z = l;
+        z.I = n;
+        z.J = a.T;
+        z.K = a.K;
+        z.a = entries(v0);
+        z.lda = e.ldw;
+        z.a_mn = e.kn;
+        z.b = a.x;
+        z.ldb = a.ldw;
+        z.live = live;
+        z.target = a.tgt;
+        z.v0 = (int)v0;
+        return z;
+    };
+    GG_TRY(launched(launch_entropy_tokens(a, s), "gathering the tokens"));
+    LinearArgs z = logits(0, a.V, &a.head->live);
+    z.partial = a.partial;
+    z.ldpartial = a.T;
+    z.ztarget = a.ztarget;
+    GG_TRY(product(kEpiLse, z, s));
+    GG_TRY(launched(launch_entropy_join(a, s), "joining the vocabulary's sums"));
+    if ((!a.dX && !e.dW) || a.K == 0)
+        return op_ok();
+    for (int64_t v0 = 0; v0 < a.V; v0 += e.piece) {
+        const int64_t n = a.V - v0 < e.piece ? a.V - v0 : e.piece;
+        z = logits(v0, n, &a.head->live_pad);
+        z.lse = a.lsec;
+        z.coef = a.coef;
+        z.out = e.dz;
+        z.ldo = e.piece;
+        GG_TRY(product(kEpiSoftGrad, z, s));
+        LinearArgs x = l, w = l;
+        x.I = a.K;
+        x.J = a.T;
+        x.K = n;
+        x.a = entries(v0);
+        x.lda = e.ldw;
+        x.a_mn = !e.kn;
+        x.b = e.dz;
+        x.ldb = e.piece;
+        x.out = a.dx32;
+        x.ldo = a.ldw;
+        x.out_f32 = 1;
+        x.accumulate = v0 > 0;
+        x.live = &a.head->live;
+        w.I = e.kn ? n : a.K;
+        w.J = e.kn ? a.K : n;
+        w.K = a.T;
+        w.a = e.kn ? (const void *)e.dz : a.x;
+        w.lda = e.kn ? e.piece : a.ldw;
+        w.b = e.kn ? a.x : (const void *)e.dz;
+        w.ldb = e.kn ? a.ldw : e.piece;
+        w.a_mn = w.b_mn = 1;
+        w.out = reinterpret_cast<uint8_t *>(e.dW) + v0 * (e.kn ? 1 : e.lddw) * (e.grad_f32 ? 4 : 2);
+        w.ldo = e.lddw;
+        w.out_f32 = e.grad_f32;
+        w.accumulate = e.accumulate;
+        w.live = &a.head->live_pad;
+        w.live_k = 1;
+        w.alpha = &a.head->alpha;
+        int bt_dx, bt_dw;
+        if (a.dX && e.dW &&
+            plan_both(x, w, plan_linear(kEpiVocab, x, GG_LINEAR_AUTO), plan_linear(kEpiVocab, w, GG_LINEAR_AUTO),
+                      GG_LINEAR_AUTO, &bt_dx, &bt_dw)) {
+            const char *why = nullptr;
+            const cudaError_t err = launch_both(kEpiVocab, x, bt_dx, w, bt_dw, s, &why);
+            GG_TRY(launched(err, why ? why : "launching the gradients of a piece"));
+        } else {
+            if (a.dX)
+                GG_TRY(product(kEpiVocab, x, s));
+            if (e.dW)
+                GG_TRY(product(kEpiVocab, w, s));
+        }
+    }
+    if (a.dX)
+        GG_TRY(launched(launch_entropy_dx(a, s), "rounding dX"));
+    return op_ok();
+}
+
 }  // namespace
 
 extern "C" {
+
+uint64_t gg_linear_cross_entropy_workspace(int64_t T, int64_t V, int64_t K, int64_t piece, int gradients)
+{
+    if (T <= 0 || V <= 0 || K < 0 || T > kMaxSize || V > kMaxSize || K > kMaxSize || piece < 0 || piece > kMaxSize)
+        return 0;
+    return entropy_places(T, V, K, piece, gradients != 0).end;
+}
+
+gg_status gg_linear_cross_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw, gg_weight_layout layout,
+                                  const int64_t *target, const float *weight, float *stats, float *loss,
+                                  float *lse, void *dX, int64_t lddx, void *dW, int64_t lddw, gg_dtype grad_dtype,
+                                  int accumulate, void *workspace, uint64_t workspace_bytes, int64_t T, int64_t V,
+                                  int64_t K, gg_dtype dtype, int64_t piece, float grad_scale, int *dev_status,
+                                  gg_stream_t stream)
+{
+    Entropy e;
+    GG_TRY(prepare_entropy(X, ldx, W, ldw, layout, target, weight, stats, loss, lse, dX, lddx, dW, lddw, grad_dtype,
+                           accumulate, workspace, workspace_bytes, T, V, K, dtype, piece, grad_scale, &e));
+    e.a.status = dev_status;
+    GG_TRY(op_status_word(&e.a.status));
+    return run_entropy(e, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gg_status gg_linear_cross_entropy_check(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                        gg_weight_layout layout, const int64_t *target, const float *weight,
+                                        const float *stats, const float *loss, const float *lse, const void *dX,
+                                        int64_t lddx, const void *dW, int64_t lddw, gg_dtype grad_dtype,
+                                        int accumulate, const void *workspace, uint64_t workspace_bytes, int64_t T,
+                                        int64_t V, int64_t K, gg_dtype dtype, int64_t piece, float grad_scale)
+{
+    Entropy e;
+    return prepare_entropy(X, ldx, W, ldw, layout, target, weight, stats, loss, lse, dX, lddx, dW, lddw, grad_dtype,
+                           accumulate, workspace, workspace_bytes, T, V, K, dtype, piece, grad_scale, &e);
+}
 
 gg_status gg_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
                       gg_dtype weight_dtype, float eps, void *h, int64_t ldh, void *y, int64_t ldy, void *codes,
@@ -150,13 +458,13 @@ uint64_t gg_rms_norm_backward_workspace(int64_t M, int64_t N)
 {
     if (M <= 0 || N <= 0 || M > kMaxSize || N > kMaxSize)
         return 0;
-    return (size_t)norm_backward_parts(M) * (size_t)N * 4;
+    return (uint64_t)norm_backward_parts(M) * (uint64_t)N * 4;
 }
 
 gg_status gg_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const float *rstd,
                                const void *weight, gg_dtype weight_dtype, const void *dh_in, int64_t lddhin,
                                void *dh, int64_t lddh, void *dweight, gg_dtype grad_dtype, int accumulate,
-                               void *workspace, size_t workspace_bytes, int64_t M, int64_t N, gg_dtype dtype,
+                               void *workspace, uint64_t workspace_bytes, int64_t M, int64_t N, gg_dtype dtype,
                                gg_stream_t stream)
 {
     NormBackwardArgs a;
@@ -171,7 +479,7 @@ gg_status gg_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
 gg_status gg_rms_norm_backward_check(const void *dy, int64_t lddy, const void *h, int64_t ldh, const float *rstd,
                                      const void *weight, gg_dtype weight_dtype, const void *dh_in, int64_t lddhin,
                                      const void *dh, int64_t lddh, const void *dweight, gg_dtype grad_dtype,
-                                     int accumulate, const void *workspace, size_t workspace_bytes, int64_t M,
+                                     int accumulate, const void *workspace, uint64_t workspace_bytes, int64_t M,
                                      int64_t N, gg_dtype dtype)
 {
     NormBackwardArgs a;

@@ -231,7 +231,7 @@ int64_t unpacked_pitch(int64_t K) { return (K + 7) / 8 * 8; }
 gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int64_t ldc, const float *scales,
                             int64_t lds, gg_activation act, const void *W, int64_t ldw, gg_weight_layout layout,
                             const void *dX, int64_t lddx, const void *dW, int64_t lddw, const void *dbias,
-                            gg_dtype grad_dtype, int accumulate, const void *workspace, size_t workspace_bytes,
+                            gg_dtype grad_dtype, int accumulate, const void *workspace, uint64_t workspace_bytes,
                             int64_t M, int64_t N, int64_t K, gg_dtype dtype, gg_linear_path path, Backward *out,
                             gg::UnpackArgs *u)
 {
@@ -246,7 +246,7 @@ gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int
     GG_TRY(check_mat(sc, true));
     const int64_t ldx = unpacked_pitch(K);
     const Mat ws{"workspace", workspace, unpacks ? M : 0, ldx, ldx, 2};
-    if (unpacks && (!workspace || workspace_bytes < (size_t)(M * ldx * 2)))
+    if (unpacks && (!workspace || workspace_bytes < (uint64_t)M * (uint64_t)ldx * 2))
         return op_fail(GG_ERR_INVALID_ARG, "workspace: %lld bytes are needed", (long long)(M * ldx * 2));
     Backward r;
     // the workspace is checked as X is: 16-byte aligned, apart from the outputs
@@ -525,7 +525,7 @@ gg_status gg_linear_backward_check(const void *dZ, int64_t lddz, const void *X, 
 gg_status gg_linear_backward8(const void *dZ, int64_t lddz, const void *codes, int64_t ldc, const float *scales,
                               int64_t lds, gg_activation act, const void *W, int64_t ldw, gg_weight_layout layout,
                               void *dX, int64_t lddx, void *dW, int64_t lddw, void *dbias, gg_dtype grad_dtype,
-                              int accumulate, void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                              int accumulate, void *workspace, uint64_t workspace_bytes, int64_t M, int64_t N,
                               int64_t K, gg_dtype dtype, int *dev_status, gg_stream_t stream, gg_linear_path path)
 {
     Backward b;
@@ -544,7 +544,7 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
                                     const float *scales, int64_t lds, gg_activation act, const void *W,
                                     int64_t ldw, gg_weight_layout layout, const void *dX, int64_t lddx,
                                     const void *dW, int64_t lddw, const void *dbias, gg_dtype grad_dtype,
-                                    int accumulate, const void *workspace, size_t workspace_bytes, int64_t M,
+                                    int accumulate, const void *workspace, uint64_t workspace_bytes, int64_t M,
                                     int64_t N, int64_t K, gg_dtype dtype, gg_linear_path path, int *chosen_dx,
                                     int *chosen_dw)
 {
@@ -562,7 +562,7 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
 
 uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K)
 {
-    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? (size_t)M * (size_t)unpacked_pitch(K) * 2 : 0;
+    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? (uint64_t)M * (uint64_t)unpacked_pitch(K) * 2 : 0;
 }
 
 gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz, void *dz,

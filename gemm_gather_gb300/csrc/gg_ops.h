@@ -27,6 +27,10 @@ constexpr int kEpiForward = 0;  // act(acc + bias) + aux, zout = acc + bias
 constexpr int kEpiGradIn = 1;   // acc * act'(aux)
 constexpr int kEpiGradW = 2;    // acc (+ out)
 constexpr int kEpiGradIn8 = 3;  // acc * act'(aux), aux kept in 8 bits (codes, with scales)
+// The vocabulary's products (entropy_kernels.cu): i is a vocabulary entry of a piece, j a token.
+constexpr int kEpiLse = 4;       // (largest, sum of exponentials) of every 32 entries, and the target's logit
+constexpr int kEpiSoftGrad = 5;  // coef (exp(acc - lse) - (i is the target)), in 16 bits
+constexpr int kEpiVocab = 6;     // alpha acc (+ out): what the gradient of the logits is multiplied into
 
 struct LinearArgs {
     int64_t I, J, K;
@@ -49,6 +53,17 @@ struct LinearArgs {
     int group;             // feature tiles per group of the tile order (pair kernel)
     int bt;                // tokens of a tile (pair kernel)
     int tiles_i, tiles_j, num_kb;  // feature and token tiles, k-blocks
+    // The vocabulary's products.  live: the tokens there are, counted on the device (J or, with
+    // live_k, K is the most there can be).
+    const int *live;
+    int live_k;
+    const int *target;     // a token's, within the vocabulary
+    int v0;                // the piece's first entry
+    float2 *partial;       // kEpiLse: (I + 31) / 32 rows, a place per token
+    int64_t ldpartial;
+    float *ztarget;
+    const float *lse, *coef;
+    const float *alpha;    // kEpiVocab; null: 1
     int skip;              // pairs of the grid past the end of the first product's walk
     int *status;
     uint64_t wait_limit_ns;
@@ -145,6 +160,43 @@ struct UnpackArgs {
     int is_bf16;
 };
 cudaError_t launch_unpack(const UnpackArgs &a, cudaStream_t s);
+
+// ---- cross entropy over a vocabulary (entropy_kernels.cu) ------------------------------
+// What the device knows of a call, at the start of its workspace.
+struct EntropyHead {
+    int live, live_pad;  // tokens that count; the same in whole k-blocks of 64, at most T
+    unsigned ticket;     // blocks of the join that are done
+    float scale;         // power of two that takes the largest |weight| to [2^13, 2^14)
+    float alpha;         // grad_scale / scale
+};
+
+struct EntropyArgs {
+    const void *X;
+    int64_t ldx;
+    const int64_t *target;  // per token, as the caller has them
+    const float *weight;
+    int64_t T, V, K;
+    int is_bf16;
+    float grad_scale;
+    float *stats, *loss, *lse;
+    void *dX;
+    int64_t lddx;
+    // workspace; "compact": the tokens that count, in their order
+    EntropyHead *head;
+    void *x;             // compact X, pitch ldw
+    int64_t ldw;
+    int *place;          // a token's compact place, or -1
+    int *token;          // compact: its token
+    int *tgt;            // compact targets (-1 behind the last)
+    float *wt, *lossc, *lsec, *coef, *ztarget;
+    float2 *partial;     // rows x T
+    int64_t rows;
+    float *dx32;         // compact dX before its rounding, pitch ldw
+    int *status;
+};
+cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s);  // counts and gathers the tokens
+cudaError_t launch_entropy_join(const EntropyArgs &a, cudaStream_t s);    // partial sums to losses
+cudaError_t launch_entropy_dx(const EntropyArgs &a, cudaStream_t s);      // dX, rounded, in the tokens' order
 
 // ---- policy loss -------------------------------------------------------------------
 struct LossArgs {

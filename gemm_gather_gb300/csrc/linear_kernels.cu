@@ -84,6 +84,14 @@ constexpr int kStageCols = 32;
 constexpr int kWarpStage = kStageCols * 64;  // 32 tokens x 32 features x 2 bytes
 constexpr int kRowSteps = kStageCols / 8;    // 16-byte accesses of a lane
 
+// Epilogues that add the chunks of a long contraction in registers, and those of the vocabulary's
+// products, whose number of tokens (their columns, or their contraction) is known on the device only.
+template <int EPI>
+constexpr bool kSums = EPI == kEpiGradW || EPI == kEpiVocab || EPI == kEpiLse;
+template <int EPI>
+constexpr bool kLive = EPI == kEpiLse || EPI == kEpiSoftGrad || EPI == kEpiVocab;
+constexpr float kLog2e = 1.44269504f;
+
 struct Shared {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
@@ -109,6 +117,86 @@ __device__ __forceinline__ float load_aux(const LinearArgs &a, const void *p, in
     return load16(p, j * ld + i, a.is_bf16);
 }
 
+// ---- the vocabulary's softmax -----------------------------------------------------------
+// The gradient over a logit z of token j, for vocabulary entry i of a piece:
+// coef (exp(z - lse) - (i is the target)).  The difference first: it is small where it counts,
+// however large z and lse are.
+struct TokenTerms {
+    float lse, coef;
+    int target;  // within the piece; any other number: not there
+};
+
+__device__ __forceinline__ float soft_grad(float z, int64_t i, const TokenTerms &t)
+{
+    const float p = ex2_approx((z - t.lse) * kLog2e);
+    return ((int)i == t.target ? p - 1.0f : p) * t.coef;
+}
+
+// (largest z, sum of exp(z - largest)) of a warp's 32 vocabulary entries, for each of n columns: a row of
+// the partial results is the warp's, place j is token j.  Every lane calls it; where all of them are past
+// the vocabulary's end there is no such row.
+template <int C>
+__device__ __forceinline__ void emit_lse(const LinearArgs &a, int64_t i, int64_t j0, int jstep, int n,
+                                         const float (&v)[16])
+{
+    const int lane = threadIdx.x & 31;
+    const bool in = i < a.I;
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+        if (u >= n)
+            break;
+        const int64_t j = j0 + (int64_t)u * jstep;
+        const float z = in ? v[u] : -INFINITY;
+        float m = z;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        float e = in ? ex2_approx((z - (m == -INFINITY ? 0.0f : m)) * kLog2e) : 0.0f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            e += __shfl_xor_sync(0xffffffffu, e, d);
+        if (lane == 0 && in)
+            a.partial[i / 32 * a.ldpartial + j] = make_float2(m, e);
+        if (in && (int)i == a.target[j])
+            a.ztarget[j] = z;
+    }
+}
+
+// The same of 16 neighbouring columns in 2 KB of shared memory: a lane turns from a vocabulary entry
+// to half a column's entries (the exclusive or spreads both over the banks).  target: lane c mod 16
+// has column c's.
+__device__ __forceinline__ void emit_lse16(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane, int target,
+                                           const float (&v)[16], uint8_t *stage)
+{
+    float *t = reinterpret_cast<float *>(stage);
+    const bool in = i0 + lane < a.I;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+        t[u * 32 + (lane ^ u)] = in ? v[u] : -INFINITY;
+    __syncwarp();
+    const int c = lane & 15, half = lane & 16;
+    float x[16], m = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        x[k] = t[c * 32 + ((half + k) ^ c)];
+        m = fmaxf(m, x[k]);
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        s += ex2_approx((x[k] - from) * kLog2e);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (c < n) {
+        const int64_t at = (int64_t)target - i0;
+        if (at >= half && at < half + 16 && at + i0 < a.I)
+            a.ztarget[j0 + c] = t[c * 32 + ((int)at ^ c)];
+        if (half == 0 && i0 < a.I)
+            a.partial[i0 / 32 * a.ldpartial + j0 + c] = make_float2(m, s);
+    }
+    __syncwarp();
+}
+
 // One feature's sums for columns j0, j0 + jstep, ... (n of them, at most C):
 // the epilogue and the store.  A warp's 32 lanes hold 32 neighbouring
 // features.  Loads of the columns are issued together, ahead of their use.
@@ -116,9 +204,19 @@ template <int EPI, int C = 16>
 __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j0, int jstep, int n,
                                        float (&v)[16], float bias)
 {
+    if constexpr (EPI == kEpiLse) {
+        emit_lse<C>(a, i, j0, jstep, n, v);
+        return;
+    }
     if (i >= a.I)
         return;
-    if constexpr (EPI == kEpiGradW) {
+    if constexpr (EPI == kEpiVocab) {
+        const float alpha = a.alpha ? *a.alpha : 1.0f;
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+            v[u] *= alpha;
+    }
+    if constexpr (EPI == kEpiGradW || EPI == kEpiVocab) {
         if (a.out_f32) {
             float *o = reinterpret_cast<float *>(a.out) + j0 * a.ldo + i;
             const int64_t step = (int64_t)jstep * a.ldo;
@@ -141,8 +239,9 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
         }
     }
     float x[C];
-    const void *aux = EPI == kEpiGradW ? (a.accumulate ? a.out : nullptr) : a.aux;
-    const int64_t ldaux = EPI == kEpiGradW ? a.ldo : a.ldaux;
+    constexpr bool kOwn = EPI == kEpiGradW || EPI == kEpiVocab;  // added to what is there
+    const void *aux = kOwn ? (a.accumulate ? a.out : nullptr) : (EPI == kEpiSoftGrad ? nullptr : a.aux);
+    const int64_t ldaux = kOwn ? a.ldo : a.ldaux;
     if (aux != nullptr) {
 #pragma unroll
         for (int u = 0; u < C; ++u)
@@ -181,6 +280,13 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
 #pragma unroll
         for (int u = 0; u < C; ++u)
             v[u] = y[u];
+    } else if constexpr (EPI == kEpiSoftGrad) {
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+            if (u < n) {
+                const int64_t j = j0 + (int64_t)u * jstep;
+                v[u] = soft_grad(v[u], i, TokenTerms{a.lse[j], a.coef[j], a.target[j] - a.v0});
+            }
     } else if (aux != nullptr) {
 #pragma unroll
         for (int u = 0; u < C; ++u)
@@ -366,7 +472,9 @@ __device__ __forceinline__ uint16_t *staged(uint8_t *stage, int lane, int col)
 template <int EPI>
 __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
 {
-    if constexpr (EPI == kEpiGradW)
+    if constexpr (EPI == kEpiLse || EPI == kEpiSoftGrad)
+        return rows_of(nullptr, 0);
+    if constexpr (EPI == kEpiGradW || EPI == kEpiVocab)
         return rows_of(a.accumulate && !a.out_f32 ? a.out : nullptr, a.ldo);
     if constexpr (EPI == kEpiGradIn8) {  // codes: eight bytes a lane
         Rows r = rows_of(a.aux, 0);
@@ -382,10 +490,10 @@ __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
 template <int EPI, typename Sums>
 __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane,
                                        float bias, bool has_aux, const uint4 (&aux)[kRowSteps],
-                                       uint8_t *stage, Sums sums)
+                                       uint8_t *stage, Sums sums, const TokenTerms &terms = TokenTerms{})
 {
     // sums in registers need constant columns; the others keep the code small
-    constexpr int kUnroll = EPI == kEpiGradW ? kStageCols / 16 : 1;
+    constexpr int kUnroll = kSums<EPI> ? kStageCols / 16 : 1;
     if constexpr (EPI == kEpiForward) {
         if (a.zout != nullptr) {
 #pragma unroll 1
@@ -407,6 +515,12 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
             break;
         float v[16], x[16];
         sums(c, v);
+        if constexpr (EPI == kEpiVocab) {
+            const float alpha = a.alpha ? *a.alpha : 1.0f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] *= alpha;
+        }
         if (has_aux) {  // a lane reads its own elements before it writes over them
 #pragma unroll
             for (int u = 0; u < 16; ++u)
@@ -425,6 +539,13 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
         } else if constexpr (EPI == kEpiGradIn || EPI == kEpiGradIn8) {
             if (has_aux)
                 with_act(a.act, [&](auto k) { apply_slope<decltype(k)::value>(v, x); });
+        } else if constexpr (EPI == kEpiSoftGrad) {  // lane c has column c's terms
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] = soft_grad(v[u], i0 + lane,
+                                 TokenTerms{__shfl_sync(0xffffffffu, terms.lse, c + u),
+                                            __shfl_sync(0xffffffffu, terms.coef, c + u),
+                                            __shfl_sync(0xffffffffu, terms.target, c + u)});
         } else if (has_aux) {
 #pragma unroll
             for (int u = 0; u < 16; ++u)
@@ -435,6 +556,22 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
             store16(staged(stage, lane, c + u), 0, v[u], a.is_bf16);
     }
     write_rows(rows_of(a.out, a.ldo), a.I, i0, j0, n, lane, stage);
+}
+
+// Column j0 + lane's terms, of n columns.
+template <int EPI>
+__device__ __forceinline__ TokenTerms terms_of(const LinearArgs &a, int64_t j0, int n, int lane)
+{
+    TokenTerms t{0.0f, 0.0f, -1};
+    if constexpr (EPI == kEpiLse) {
+        if (lane < n)
+            t.target = a.target[j0 + lane];
+    }
+    if constexpr (EPI == kEpiSoftGrad) {
+        if (lane < n)
+            t = TokenTerms{a.lse[j0 + lane], a.coef[j0 + lane], a.target[j0 + lane] - a.v0};
+    }
+    return t;
 }
 
 // One stage's operand: `rows` rows (or columns) of 64 k.  K-major: one box of
@@ -488,9 +625,9 @@ struct Tile {
 // then cover about as many feature tiles as token tiles, which keeps the
 // slices of A and B that they read from DRAM and share through L2 few.
 // Unsigned: a product has fewer than 2^31 tiles (launch_pair refuses more).
-__device__ __forceinline__ Tile tile_at(const LinearArgs &a, uint32_t t)
+__device__ __forceinline__ Tile tile_at(const LinearArgs &a, uint32_t tiles_j, uint32_t t)
 {
-    const uint32_t full = (uint32_t)a.group * (uint32_t)a.tiles_j;
+    const uint32_t full = (uint32_t)a.group * tiles_j;
     const uint32_t g = t / full;
     const uint32_t r = t - g * full;
     const uint32_t left = (uint32_t)a.tiles_i - g * (uint32_t)a.group;
@@ -507,14 +644,50 @@ struct Product {
     int kb0, num_kb;
     uint32_t total, first;
     Tile tile;  // the first
+    // kLive: the columns and their tiles that the device knows (see columns_of and tiles_of)
+    int64_t J;
+    uint32_t tiles_j;
+    __device__ __forceinline__ Product() : kb0(0), num_kb(0), total(0), first(0), tile{0, 0}, J(0), tiles_j(0) {}
     __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts, uint32_t first_)
         : kb0(0), num_kb(a.num_kb), total((uint32_t)a.tiles_i * (uint32_t)a.tiles_j), first(first_),
-          tile(first_ < total ? tile_at(a, first_) : Tile{0, 0})
+          tile(first_ < total ? tile_at(a, (uint32_t)a.tiles_j, first_) : Tile{0, 0})
     {
         if (parts > 1)  // 2 or 4
             share_of(a.num_kb, part, parts, kb0, num_kb);
     }
+    // The same with the tokens that the device counted; the launches before have to be waited for.
+    __device__ __forceinline__ void count(const LinearArgs &a, int part, int parts)
+    {
+        const int live = *a.live;
+        num_kb = a.live_k ? (live + kBK - 1) / kBK : a.num_kb;
+        J = a.live_k ? a.J : (int64_t)live;
+        tiles_j = (uint32_t)((J + a.bt - 1) / a.bt);
+        total = (uint32_t)a.tiles_i * tiles_j;
+        if (parts > 1)
+            share_of(num_kb, part, parts, kb0, num_kb);
+    }
+    __device__ __forceinline__ void start(const LinearArgs &a, uint32_t first_)
+    {
+        first = first_;
+        if (first < total)
+            tile = tile_at(a, tiles_j, first);
+    }
 };
+
+template <int EPI>
+__device__ __forceinline__ int64_t columns_of(const LinearArgs &a, const Product &p)
+{
+    if constexpr (kLive<EPI>)
+        return p.J;
+    return a.J;
+}
+template <bool LIVE>
+__device__ __forceinline__ uint32_t tiles_of(const LinearArgs &a, const Product &p)
+{
+    if constexpr (LIVE)
+        return p.tiles_j;
+    return (uint32_t)a.tiles_j;
+}
 
 // Where a thread block stands: the same for all its roles but the fields a role moves.
 struct Place {
@@ -541,7 +714,7 @@ struct Place {
 // cycles whatever their size (570 with a warp's votes around them), as long as the
 // MMAs of a 256 x 224 tile and twice those of smaller ones; so two threads share
 // them, of warps of their own.
-template <int BT>
+template <int BT, bool LIVE>
 __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensorMap &map_b, const LinearArgs &a,
                                         const Product &p, Place &at)
 {
@@ -576,7 +749,7 @@ __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensor
         at.count += p.num_kb;
         t += at.nunits;
         if (t < p.total)
-            c = tile_at(a, t);
+            c = tile_at(a, tiles_of<LIVE>(a, p), t);
     }
     return true;
 }
@@ -644,17 +817,23 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
     const int chunks = (p.num_kb + a.chunk - 1) / a.chunk;
     const auto column = [](int u) { return u / kStageCols * kStep + u % kStageCols; };
     for (uint32_t t = p.first; t < p.total; t += at.nunits) {
-        const Tile c = tile_at(a, t);
+        const Tile c = tile_at(a, tiles_of<kLive<EPI>>(a, p), t);
         const int64_t i0 = (int64_t)c.ti * kTileI + (int)at.rank * 128 + at.q * 32;
         const int64_t j0 = (int64_t)c.tj * a.bt + at.group * kStageCols;
         // the first token that is not this tile's
-        const int64_t end = gg_min64(a.J, (int64_t)(c.tj + 1) * a.bt);
+        const int64_t end = gg_min64(columns_of<EPI>(a, p), (int64_t)(c.tj + 1) * a.bt);
         const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
         uint4 pre[kRowSteps];
-        if (EPI != kEpiGradW && early)  // the first group's rows, while the MMAs run
+        if (!kSums<EPI> && early)  // the first group's rows, while the MMAs run
             read_aux<EPI>(a, aux, i0, j0, valid_rows(end, j0), lane, pre);
-        float sum[EPI == kEpiGradW ? kCols : 1];
-        if constexpr (EPI == kEpiGradW) {
+        TokenTerms terms[kGroups];
+        if constexpr (EPI == kEpiLse || EPI == kEpiSoftGrad) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+                terms[g] = terms_of<EPI>(a, j0 + g * kStep, valid_rows(end, j0 + g * kStep), lane);
+        }
+        float sum[kSums<EPI> ? kCols : 1];
+        if constexpr (kSums<EPI>) {
 #pragma unroll
             for (int u = 0; u < kCols; ++u)
                 sum[u] = 0.0f;
@@ -675,7 +854,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                 for (int u = 0; u < 16; ++u)
                     v[u] = __uint_as_float(r[u]);
             };
-            if constexpr (EPI == kEpiGradW) {
+            if constexpr (kSums<EPI>) {
 #pragma unroll
                 for (int col = 0; col < kCols; col += 16) {
                     if (valid_rows(end, j0 + column(col)) <= 0)
@@ -702,7 +881,8 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                     if (valid_rows(end, jg) <= 0)
                         break;
                     emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, at.stage_buf,
-                                   [&](int col, float(&v)[16]) { from_tmem(g * kStep + col, v); });
+                                   [&](int col, float(&v)[16]) { from_tmem(g * kStep + col, v); },
+                                   terms[kGroups > 1 && g > 0 ? kGroups - 1 : 0]);
                     if (early && g + 1 < kGroups)
                         read_aux<EPI>(a, aux, i0, jg + kStep, valid_rows(end, jg + kStep), lane, pre);
                 }
@@ -713,7 +893,22 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
             if (lane == 0)
                 mbar_arrive_cluster(empty0 + (uint32_t)(acc * sizeof(uint64_t)));
         }
-        if constexpr (EPI == kEpiGradW) {
+        if constexpr (EPI == kEpiLse) {
+#pragma unroll
+            for (int col = 0; col < kCols; col += 16) {
+                const int64_t jc = j0 + column(col);
+                const int n = valid16(end, jc);
+                if (n <= 0)
+                    continue;
+                float v[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = sum[col + u];
+                const int target =
+                    __shfl_sync(0xffffffffu, terms[col / kStageCols].target, (lane & 15) + col % kStageCols);
+                emit_lse16(a, i0, jc, n, lane, target, v, at.stage_buf);
+            }
+        } else if constexpr (kSums<EPI>) {
             if (at.parts > 1) {
 #pragma unroll
                 for (int u = 0; u < kCols; ++u)
@@ -754,13 +949,15 @@ template <int EPI, int BT>
 __device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p, Place &at)
 {
     const int lane = at.lane, parts = at.parts;
-    const Tile c = tile_at(a, at.unit);
+    if (kLive<EPI> && at.unit >= p.total)
+        return;
+    const Tile c = tile_at(a, tiles_of<kLive<EPI>>(a, p), at.unit);
     // 16 columns a warp at least: with 32 left for a pair, half the warps finish them
     const int cols = BT / parts >= 64 ? BT / parts / 4 : 16;
     const int col0 = at.part * (BT / parts) + at.group * cols;
     const int64_t i0 = (int64_t)c.ti * kTileI + (int)at.rank * 128 + at.q * 32;
     const int64_t j0 = (int64_t)c.tj * BT + col0;
-    const int64_t left = a.J - j0;
+    const int64_t left = columns_of<EPI>(a, p) - j0;
     const int n = at.group * cols >= BT / parts ? 0 : (left > cols ? cols : (left > 0 ? (int)left : 0));
     const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
     const uint32_t mine = at.base + (uint32_t)((col0 * 128 + at.q * 32 + lane) * 4);
@@ -781,7 +978,7 @@ __device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p
                 v[h + u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
         }
     };
-    if (EPI == kEpiGradW && a.out_f32) {
+    if ((EPI == kEpiGradW || EPI == kEpiVocab) && a.out_f32) {
         // nothing is read past the last feature or token: reads that no store waits for
         // could outlive the CTA (the staged rows below store all that they read)
 #pragma unroll 1
@@ -869,24 +1066,36 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     at.count = 0;
     at.issued = 0;
     at.stall_at = a.inject_stall && at.unit == 0 && at.part == 0 ? 0 : -1;
-    const pair::Product p(a, at.part, at.parts, at.unit);
-    // the second product's walk goes on where the first ended
-    const uint32_t at1 = at.unit + (at.unit < (uint32_t)a1.skip ? at.nunits : 0u) - (uint32_t)a1.skip;
-    const pair::Product p1(kTwo ? a1 : a, at.part, at.parts, kTwo ? at1 : 0u);
+    pair::Product p, p1;
+    if constexpr (!kLive<EPI>) {
+        p = pair::Product(a, at.part, at.parts, at.unit);
+        // the second product's walk goes on where the first ended
+        const uint32_t at1 = at.unit + (at.unit < (uint32_t)a1.skip ? at.nunits : 0u) - (uint32_t)a1.skip;
+        p1 = pair::Product(kTwo ? a1 : a, at.part, at.parts, kTwo ? at1 : 0u);
+    }
     __syncthreads();
     cluster_meet();  // the peer's barriers exist before anything signals them
     fence_after();
     at.tmem = sh.tmem_base;
     wait_dependencies();  // what earlier launches write is there from here on
     launch_dependents();
+    if constexpr (kLive<EPI>) {
+        p.count(a, at.part, at.parts);
+        p.start(a, at.unit);
+        if constexpr (kTwo) {
+            const uint32_t skip = p.total % at.nunits;
+            p1.count(a1, at.part, at.parts);
+            p1.start(a1, at.unit + (at.unit < skip ? at.nunits : 0u) - skip);
+        }
+    }
 
     bool ok = true;
     if (warp == 0 || warp == pair::kProducer2) {
         // ===================== producers (a thread each) ====================
         if (ptx::elect_one_sync()) {
-            ok = pair::produce<BT>(map_a, map_b, a, p, at);
+            ok = pair::produce<BT, kLive<EPI>>(map_a, map_b, a, p, at);
             if (kTwo && ok)
-                ok = pair::produce<BT>(map_a1, map_b1, a1, p1, at);
+                ok = pair::produce<BT, kLive<EPI>>(map_a1, map_b1, a1, p1, at);
             if (!ok) {
                 *at.abort_flag = 1;
                 report_status(a.status, kStatusTimeout);
@@ -938,8 +1147,10 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     if constexpr (!kTwo) {
         if (at.parts > 1) {
             cluster_sync();
-            if (warp >= 2 && warp < pair::kProducer2 && ok)
-                pair::join_parts<EPI, BT>(a, p, at);
+            if constexpr (EPI != kEpiLse && EPI != kEpiSoftGrad) {  // (these do not split tiles)
+                if (warp >= 2 && warp < pair::kProducer2 && ok)
+                    pair::join_parts<EPI, BT>(a, p, at);
+            }
             __syncwarp();
         }
     }
@@ -1017,13 +1228,23 @@ __global__ void __launch_bounds__(split::kThreads, 2)
     const int tj = (int)(tile / (uint32_t)a.tiles_i);
     const int ti = (int)(tile - (uint32_t)tj * (uint32_t)a.tiles_i);
     int kb0, kb1;
-    share_of(a.num_kb, rank, parts, kb0, kb1);
-    kb1 += kb0;
+    int64_t J = a.J;
+    if constexpr (!kLive<EPI>) {
+        share_of(a.num_kb, rank, parts, kb0, kb1);
+        kb1 += kb0;
+    }
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem_base;
     wait_dependencies();
     launch_dependents();
+    if constexpr (kLive<EPI>) {  // (a tile past the last token multiplies zeros or stale rows, and writes nothing)
+        const int live = *a.live;
+        share_of(a.live_k ? (live + kBK - 1) / kBK : a.num_kb, rank, parts, kb0, kb1);
+        kb1 += kb0;
+        if (!a.live_k)
+            J = live;
+    }
 
     const int q = warp & 3;  // epilogue: TMEM lane quarter
     const int64_t i = (int64_t)ti * 128 + q * 32 + lane;
@@ -1128,8 +1349,8 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         const Rows aux = aux_of<EPI>(a);
         uint4 pre[kRowSteps];
         const int chunks = (kb1 - kb0 + a.chunk - 1) / a.chunk;
-        float sum[EPI == kEpiGradW ? BT : 1];
-        if constexpr (EPI == kEpiGradW) {
+        float sum[kSums<EPI> ? BT : 1];
+        if constexpr (kSums<EPI>) {
 #pragma unroll
             for (int u = 0; u < BT; ++u)
                 sum[u] = 0.0f;
@@ -1143,7 +1364,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                 break;
             }
             fence_after();
-            if constexpr (EPI == kEpiGradW) {
+            if constexpr (kSums<EPI>) {
 #pragma unroll
                 for (int c16 = 0; c16 < BT / 16; ++c16) {
                     uint32_t r[16];
@@ -1167,7 +1388,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
                 }
 #pragma unroll 1
                 for (int g = 0; parts == 1 && g < BT; g += kStageCols) {
-                    const int n = valid_rows(a.J, jt + g) < BT - g ? valid_rows(a.J, jt + g) : BT - g;
+                    const int n = valid_rows(J, jt + g) < BT - g ? valid_rows(J, jt + g) : BT - g;
                     if (aux.p)
                         read_aux<EPI>(a, aux, i0, jt + g, n, lane, pre);
                     emit_rows<EPI>(a, i0, jt + g, n, lane, bias, aux.p != nullptr, pre, stage_buf,
@@ -1178,7 +1399,8 @@ __global__ void __launch_bounds__(split::kThreads, 2)
 #pragma unroll
                                     for (int u = 0; u < 16; ++u)
                                         v[u] = __uint_as_float(r[u]);
-                                });
+                                },
+                                terms_of<EPI>(a, jt + g, n, lane));
                 }
             }
             fence_before();
@@ -1186,25 +1408,25 @@ __global__ void __launch_bounds__(split::kThreads, 2)
             if (lane == 0)
                 ptx::mbar_arrive(ptx::smem_addr(&sh.tmem_empty[acc]));
         }
-        if constexpr (EPI == kEpiGradW) {
+        if constexpr (kSums<EPI>) {
             if (ok) {  // past the last chunk every load and MMA of this CTA is done
                 if (parts > 1) {
 #pragma unroll
                     for (int u = 0; u < BT; ++u)
                         partial[u * 128] = sum[u];
-                } else if (a.out_f32) {
+                } else if (EPI == kEpiLse || a.out_f32) {
 #pragma unroll
                     for (int c16 = 0; c16 < BT / 16; ++c16) {
                         float v[16];
 #pragma unroll
                         for (int u = 0; u < 16; ++u)
                             v[u] = sum[c16 * 16 + u];
-                        emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(a.J, jt + c16 * 16), v, 0.0f);
+                        emit16<EPI>(a, i, jt + c16 * 16, 1, valid16(J, jt + c16 * 16), v, 0.0f);
                     }
                 } else {
 #pragma unroll
                     for (int g = 0; g < BT; g += kStageCols) {
-                        const int n = valid_rows(a.J, jt + g);
+                        const int n = valid_rows(J, jt + g);
                         if (aux.p)
                             read_aux<EPI>(a, aux, i0, jt + g, n, lane, pre);
                         emit_rows<EPI>(a, i0, jt + g, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
@@ -1232,7 +1454,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
         // it, and could leave, and let the others leave, with its reads in flight.
         if (warp >= 2 && warp < split::kProducer2 && ok && i - lane < a.I) {
             const uint32_t mine = base + (uint32_t)(q * 32 + lane) * 4;
-            const int64_t left = a.J - jt;  // valid columns of the tile
+            const int64_t left = J - jt;  // valid columns of the tile
             const int cols = left < BT ? (int)left : BT;
             // Columns at a time: as many as a CTA of a full cluster has, up to 4.  This is
             // code that runs once, and what it costs is mostly its fetching: with 4 instead
@@ -1286,7 +1508,8 @@ __global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ Line
         const int64_t i = (g % blocks_i) * 32 + (threadIdx.x & 31);
         const int64_t j0 = g / blocks_i * 16;
         float v[16] = {};
-        emit16<EPI>(a, i, j0, 1, valid16(a.J, j0), v, load_bias(a, i));
+        const int64_t J = kLive<EPI> && !a.live_k ? (int64_t)*a.live : a.J;
+        emit16<EPI>(a, i, j0, 1, valid16(J, j0), v, load_bias(a, i));
     }
 }
 
@@ -1596,11 +1819,11 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
                           : launch_pair<EPI, -1, 128>(a, p.bt, p.split, nullptr, 0, s, why);
     switch (p.bt) {
     case 16:
-        if constexpr (EPI != kEpiGradW)
+        if constexpr (EPI != kEpiGradW && EPI != kEpiVocab)
             return launch_split<EPI, 16>(a, p.split, s, why);
         break;
     case 32:
-        if constexpr (EPI != kEpiGradW)
+        if constexpr (EPI != kEpiGradW && EPI != kEpiVocab)
             return launch_split<EPI, 32>(a, p.split, s, why);
         break;
     case 64: return launch_split<EPI, 64>(a, p.split, s, why);
@@ -1654,7 +1877,7 @@ LinearPlan plan_linear(int epi, const LinearArgs &a, int path)
         if (best.kernel == GG_LINEAR_NONE || ns < best.ns)
             best = LinearPlan{kernel, bt, parts, ns};
     };
-    for (int bt = epi == kEpiGradW ? 64 : 16; path != GG_LINEAR_PAIR && bt <= 64; bt *= 2) {
+    for (int bt = epi == kEpiGradW || epi == kEpiVocab ? 64 : 16; path != GG_LINEAR_PAIR && bt <= 64; bt *= 2) {
         const int64_t tiles = ((I + 127) / 128) * ((J + bt - 1) / bt);
         for (int parts = 1; parts <= 8 && parts <= num_kb; ++parts) {
             const int64_t ctas = tiles * parts;
@@ -1676,7 +1899,8 @@ LinearPlan plan_linear(int epi, const LinearArgs &a, int path)
     const int step = a.b_mn ? 128 : 32;
     for (int bt = a.b_mn ? 128 : 64; path != GG_LINEAR_SPLIT && bt <= 256; bt += step) {
         const int64_t tiles = ((I + 255) / 256) * ((J + bt - 1) / bt);
-        for (int parts = 1; parts <= 4 && parts <= num_kb; parts *= 2) {
+        const int most = epi == kEpiLse || epi == kEpiSoftGrad ? 1 : 4;  // they join no partial tiles
+        for (int parts = 1; parts <= most && parts <= num_kb; parts *= 2) {
             // pairs, and clusters of 4 and 8 CTAs, that are resident at once
             const int64_t room = parts == 1 ? 76 : (parts == 2 ? 36 : 14);
             if (parts > 1 && (tiles > room || (bt != 128 && bt != 256)))
@@ -1730,12 +1954,12 @@ bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &pla
     return found;
 }
 
-template <int EPI>
+template <int EPI, int EPI1>
 static cudaError_t launch_both_of(const LinearArgs &x, int bt_dx, const LinearArgs &w, int bt_dw, cudaStream_t s,
                                   const char **why)
 {
-    return bt_dx > 128 || bt_dw > 128 ? launch_pair<EPI, kEpiGradW, 256>(x, bt_dx, 1, &w, bt_dw, s, why)
-                                      : launch_pair<EPI, kEpiGradW, 128>(x, bt_dx, 1, &w, bt_dw, s, why);
+    return bt_dx > 128 || bt_dw > 128 ? launch_pair<EPI, EPI1, 256>(x, bt_dx, 1, &w, bt_dw, s, why)
+                                      : launch_pair<EPI, EPI1, 128>(x, bt_dx, 1, &w, bt_dw, s, why);
 }
 
 cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
@@ -1746,10 +1970,13 @@ cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearAr
         return cudaErrorNotSupported;
     }
     LinearArgs x = dx, w = dw;
-    x.chunk = 1 << 30;
+    x.chunk = epi == kEpiVocab ? kChunk : 1 << 30;
     w.chunk = kChunk;
-    return epi == kEpiGradIn8 ? launch_both_of<kEpiGradIn8>(x, bt_dx, w, bt_dw, s, why)
-                              : launch_both_of<kEpiGradIn>(x, bt_dx, w, bt_dw, s, why);
+    switch (epi) {
+    case kEpiVocab: return launch_both_of<kEpiVocab, kEpiVocab>(x, bt_dx, w, bt_dw, s, why);
+    case kEpiGradIn8: return launch_both_of<kEpiGradIn8, kEpiGradW>(x, bt_dx, w, bt_dw, s, why);
+    default: return launch_both_of<kEpiGradIn, kEpiGradW>(x, bt_dx, w, bt_dw, s, why);
+    }
 }
 
 cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, cudaStream_t s,
@@ -1762,11 +1989,14 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
         return cudaErrorNotSupported;
     }
     LinearArgs a = args;
-    a.chunk = epi == kEpiGradW ? kChunk : 1 << 30;
+    a.chunk = epi == kEpiGradW || epi == kEpiVocab || epi == kEpiLse ? kChunk : 1 << 30;
     switch (epi) {
     case kEpiForward: return launch_epi<kEpiForward>(a, p, s, why);
     case kEpiGradIn: return launch_epi<kEpiGradIn>(a, p, s, why);
     case kEpiGradIn8: return launch_epi<kEpiGradIn8>(a, p, s, why);
+    case kEpiLse: return launch_epi<kEpiLse>(a, p, s, why);
+    case kEpiSoftGrad: return launch_epi<kEpiSoftGrad>(a, p, s, why);
+    case kEpiVocab: return launch_epi<kEpiVocab>(a, p, s, why);
     default: return launch_epi<kEpiGradW>(a, p, s, why);
     }
 }

@@ -569,7 +569,7 @@ gg_status gg_linear_backward8(const void *dZ, int64_t lddz, const void *codes, i
                               const float *scales, int64_t lds, gg_activation act, const void *W,
                               int64_t ldw, gg_weight_layout layout, void *dX, int64_t lddx, void *dW,
                               int64_t lddw, void *dbias, gg_dtype grad_dtype, int accumulate,
-                              void *workspace, size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                              void *workspace, uint64_t workspace_bytes, int64_t M, int64_t N, int64_t K,
                               gg_dtype dtype, int *dev_status, gg_stream_t stream,
                               gg_linear_path path);
 
@@ -581,7 +581,7 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
                                     int64_t ldw, gg_weight_layout layout, const void *dX, int64_t lddx,
                                     const void *dW, int64_t lddw, const void *dbias,
                                     gg_dtype grad_dtype, int accumulate, const void *workspace,
-                                    size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                                    uint64_t workspace_bytes, int64_t M, int64_t N, int64_t K,
                                     gg_dtype dtype, gg_linear_path path, int *chosen_dx, int *chosen_dw);
 
 /* ---------------------------------------------------------------------------
@@ -635,7 +635,7 @@ gg_status gg_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
                                const float *rstd, const void *weight, gg_dtype weight_dtype,
                                const void *dh_in, int64_t lddhin, void *dh, int64_t lddh, void *dweight,
                                gg_dtype grad_dtype, int accumulate, void *workspace,
-                               size_t workspace_bytes, int64_t M, int64_t N, gg_dtype dtype,
+                               uint64_t workspace_bytes, int64_t M, int64_t N, gg_dtype dtype,
                                gg_stream_t stream);
 
 /* Validate a gg_rms_norm_backward call exactly as the launching call does and launch
@@ -644,7 +644,7 @@ gg_status gg_rms_norm_backward_check(const void *dy, int64_t lddy, const void *h
                                      const float *rstd, const void *weight, gg_dtype weight_dtype,
                                      const void *dh_in, int64_t lddhin, const void *dh, int64_t lddh,
                                      const void *dweight, gg_dtype grad_dtype, int accumulate,
-                                     const void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                                     const void *workspace, uint64_t workspace_bytes, int64_t M, int64_t N,
                                      gg_dtype dtype);
 
 /* ---------------------------------------------------------------------------
@@ -698,6 +698,63 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
                                float clip_high, float kl_coef, float grad_scale,
                                const float *stats, const float *logp_out, const void *dlogits,
                                int64_t ldd);
+
+/* ---------------------------------------------------------------------------
+ * gg_linear_cross_entropy — the softmax cross entropy of T tokens over a vocabulary
+ * of V entries, from the hidden states and the vocabulary's weight, and its
+ * gradients, in one call.  The T x V logits are never stored:
+ *   z      = X W                                   (T x V, float32 sums, on chip)
+ *   lse[t] = log sum over v of exp z[t, v]
+ *   loss[t] = lse[t] - z[t, target[t]]
+ * stats[0] = sum over t of weight[t] loss[t], stats[1] = sum of weight[t]; with
+ *   dZ[t, v] = grad_scale weight[t] (exp(z[t, v] - lse[t]) - (v == target[t]))
+ *   dX = dZ W^T  (T x K of `dtype`, rounded once),  dW (+)= X^T dZ  (in W's layout, of grad_dtype)
+ * X: T x K; W: K x V or V x K (layout), both of `dtype` (GG_F16 or GG_BF16); target:
+ * int64 per token; weight, loss, lse: float32 per token; stats: 2 floats; grad_dtype:
+ * `dtype` or GG_F32; accumulate != 0 adds to what dW holds.  stats, lse, dX and dW may
+ * be NULL; with neither dX nor dW the call computes the loss alone.  dX may be X itself
+ * (same pointer and pitch).
+ * A token of weight 0 is masked: its target and its row of X are ignored, whatever
+ * they hold, its loss and lse are 0, its dX row is zero, and it costs no
+ * multiplication.  A target outside [0, V) stores GG_ERR_INVALID_ARG in the status word
+ * (dev_status, or the library's when NULL) and its token counts as masked.  Logits of
+ * -inf are entries of probability 0; a row of nothing else, or one with NaN or +inf,
+ * gives NaN.  Sums, softmax and both gradients' sums are float32; dZ is multiplied in
+ * `dtype`, for which weights are scaled by a power of two (so that their size
+ * does not matter to float16); logits are computed twice.
+ * The gradients go through the vocabulary in pieces: `piece` entries (a multiple of
+ * 128) at a time, 0 for the library's choice (equal pieces of at most 32768).  The
+ * values differ by the order of float32 sums only.
+ * Alignment: X and W 16-byte aligned with pitches that are multiples of 8; every other
+ * argument at its element's alignment, any pitch.  V >= 1 where T > 0; T == 0 gives zero
+ * statistics and a zero (or kept) dW; K == 0 gives logits of 0.
+ * workspace: 16-byte aligned device memory of at least
+ * gg_linear_cross_entropy_workspace(T, V, K, piece, gradients) bytes (gradients: whether dX or
+ * dW is asked for): about 2 T K + T V / 4 bytes for the loss, 4 T K + 2 T piece more for the
+ * gradients.  What it held is lost; calls that may run at the same time, or replays of
+ * graphs that captured them, need workspaces of their own.
+ * dev_status: as for gg_linear.
+ * ------------------------------------------------------------------------- */
+uint64_t gg_linear_cross_entropy_workspace(int64_t T, int64_t V, int64_t K, int64_t piece,
+                                           int gradients);
+gg_status gg_linear_cross_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                  gg_weight_layout layout, const int64_t *target, const float *weight,
+                                  float *stats, float *loss, float *lse, void *dX, int64_t lddx,
+                                  void *dW, int64_t lddw, gg_dtype grad_dtype, int accumulate,
+                                  void *workspace, uint64_t workspace_bytes, int64_t T, int64_t V,
+                                  int64_t K, gg_dtype dtype, int64_t piece, float grad_scale,
+                                  int *dev_status, gg_stream_t stream);
+
+/* Validate a gg_linear_cross_entropy call exactly as the launching call does and launch
+ * nothing. */
+gg_status gg_linear_cross_entropy_check(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                                        gg_weight_layout layout, const int64_t *target,
+                                        const float *weight, const float *stats, const float *loss,
+                                        const float *lse, const void *dX, int64_t lddx, const void *dW,
+                                        int64_t lddw, gg_dtype grad_dtype, int accumulate,
+                                        const void *workspace, uint64_t workspace_bytes, int64_t T,
+                                        int64_t V, int64_t K, gg_dtype dtype, int64_t piece,
+                                        float grad_scale);
 
 /* ---------------------------------------------------------------------------
  * gg_adamw — one AdamW step (decoupled weight decay) over many tensors in one

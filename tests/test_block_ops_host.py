@@ -171,3 +171,56 @@ def test_the_others_look_at_tensors():
             packed(**kw)
     with pytest.raises(ValueError, match="out: a tensor of torch.float16"):
         gg.unpack8(at(0), 128, at(1), 1, "none", zeros(4, 128), 128, 4, 128, F16, stream=0)
+
+
+def entropy(**kw):
+    a = dict(X=at(0), ldx=520, W=at(1), ldw=520, layout="nk", target=at(2), weight=at(3), stats=at(4), loss=at(5), lse=at(6),
+             dX=at(7), lddx=513, dW=at(8), lddw=513, gdt=F32, acc=False, ws=at(9), T=100, V=5000, K=513, dtype=BF16, piece=0,
+             grad_scale=1.0, ws_bytes=None)
+    a.update(kw)
+    if a["ws_bytes"] is None:
+        a["ws_bytes"] = gg.linear_cross_entropy_workspace(a["T"], a["V"], a["K"], max(a["piece"], 0),
+                                                          a["dX"] is not None or a["dW"] is not None)
+    gg.linear_cross_entropy_check(*list(a.values())[:-3], piece=a["piece"], grad_scale=a["grad_scale"],
+                                  workspace_bytes=a["ws_bytes"])
+
+
+def test_entropy_accepts():
+    entropy()
+    entropy(layout="kn", ldw=5000, lddw=5000)
+    entropy(dX=None, dW=None), entropy(dX=None), entropy(dW=None), entropy(stats=None, lse=None)
+    entropy(dX=at(0), lddx=520)                           # dX over X
+    entropy(gdt=BF16, dW=at(8) + 2), entropy(piece=128), entropy(piece=1 << 20)
+    entropy(T=0, X=None, W=None, target=None, weight=None, loss=None, ws=None, ws_bytes=0)
+    entropy(T=0, V=0, X=None, W=None, target=None, weight=None, loss=None, ws=None, ws_bytes=0)
+    entropy(K=0, X=None, W=None)
+    small = gg.linear_cross_entropy_workspace(4096, 100003, 2048, 0, False)
+    assert 4096 * 2048 * 2 < small < 4096 * 100003 * 2 // 5
+    assert gg.linear_cross_entropy_workspace(100, 5000, 513, 1024) < gg.linear_cross_entropy_workspace(100, 5000, 513)
+    assert gg.linear_cross_entropy_workspace(0, 5, 5) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=F32), UNSUP), (dict(gdt=F16), UNSUP), (dict(T=-1), INVALID), (dict(V=0, W=None), INVALID), (dict(V=1 << 31), UNSUP),
+    (dict(piece=100), INVALID), (dict(piece=-128), INVALID), (dict(grad_scale=float("nan")), INVALID),
+    (dict(grad_scale=float("inf")), INVALID), (dict(X=None), INVALID), (dict(W=None), INVALID), (dict(target=None), INVALID),
+    (dict(weight=None), INVALID), (dict(loss=None), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=1000), INVALID),
+    (dict(ws=at(9) + 8), ALIGN), (dict(X=at(0) + 8), ALIGN), (dict(W=at(1) + 2), ALIGN), (dict(ldx=521), ALIGN),
+    (dict(ldw=512), INVALID), (dict(ldw=525), ALIGN), (dict(target=at(2) + 4), ALIGN), (dict(weight=at(3) + 2), ALIGN),
+    (dict(stats=at(4) + 1), ALIGN), (dict(dW=at(8) + 2), ALIGN), (dict(dX=at(0)), INVALID), (dict(dX=at(1)), INVALID),
+    (dict(dW=at(1)), INVALID), (dict(loss=at(6)), INVALID), (dict(lse=at(3)), INVALID), (dict(stats=at(5)), INVALID),
+    (dict(ws=at(0)), INVALID), (dict(ws=at(1)), INVALID), (dict(ws=at(7)), INVALID), (dict(ws=at(8)), INVALID),
+    (dict(loss=at(9) + 64), INVALID), (dict(loss=at(2)), INVALID), (dict(lddx=512), INVALID), (dict(lddw=1), INVALID)])
+def test_entropy_refuses(kw, status):
+    refused(status, entropy, **kw)
+
+
+@pytest.mark.parametrize("kw,says", [
+    (dict(X=zeros(100, 513, dtype=F16)), "X: a tensor of torch.bfloat16"), (dict(W=zeros(100, 513)), "W: a tensor of 2565000"),
+    (dict(target=zeros(100, dtype=torch.int32)), "target: a tensor of torch.int64"), (dict(weight=zeros(100)), "weight: a tensor of"),
+    (dict(stats=zeros(1, dtype=F32)), "stats: a tensor of 2"), (dict(loss=zeros(99, dtype=F32)), "loss: a tensor of 100"),
+    (dict(dW=zeros(5000, 513)), "dW: a tensor of torch.float32"), (dict(dX=zeros(100, 513)), "dX: a tensor on the GPU"),
+    (dict(ws=zeros(1 << 10), ws_bytes=1 << 20), "workspace: a tensor of 1048576")])
+def test_entropy_looks_at_tensors(kw, says):
+    with pytest.raises(ValueError, match=says):
+        entropy(**kw)
