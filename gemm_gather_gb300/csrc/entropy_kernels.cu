@@ -71,21 +71,26 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
     wait_dependencies();
     launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t blocks = gridDim.x, me = blockIdx.x;
-    int64_t base = 0;
+    const uint32_t blocks = gridDim.x, me = blockIdx.x;
+    const int T = (int)a.T;
+    int base = 0;
     float top = 0.0f;
-    for (int64_t c0 = 0; c0 < a.T; c0 += kChunkTokens) {
+    for (int64_t c0 = 0; c0 < T; c0 += kChunkTokens) {
+        const int steps = T - c0 >= kChunkTokens ? kEach : (int)((T - c0 + kThreads - 1) / kThreads);
+        const int64_t t0 = c0 + threadIdx.x;
         float w[kEach];
         int64_t tg[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int64_t t = c0 + k * kThreads + threadIdx.x;
-            w[k] = t < a.T ? a.weight[t] : 0.0f;
-            tg[k] = t < a.T ? a.target[t] : 0;
+            const bool in = t0 + k * kThreads < T;
+            w[k] = in ? a.weight[t0 + k * kThreads] : 0.0f;
+            tg[k] = in ? a.target[t0 + k * kThreads] : 0;
         }
         unsigned live[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
+            if (k >= steps)
+                break;
             bool counts_in = w[k] != 0.0f;
             if (counts_in && (tg[k] < 0 || tg[k] >= a.V)) {
                 counts_in = false;
@@ -101,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
         if (threadIdx.x == 0)
             listed = 0;
         __syncthreads();
-        if (warp < kEach) {  // warp k: the 32 warps of step k
+        if (warp < steps) {  // warp k: the 32 warps of step k
             const int own = counts[warp * 32 + lane];
             int sum = own;
 #pragma unroll
@@ -114,23 +119,24 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
                 sums[warp] = sum;
         }
         __syncthreads();
-        int before = 0;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int64_t t = c0 + k * kThreads + threadIdx.x;
+            if (k >= steps)
+                break;
+            const int t = (int)c0 + k * kThreads + (int)threadIdx.x;
             const bool on = live[k] >> lane & 1;
-            const int64_t p = base + before + offsets[k * 32 + warp] + __popc(live[k] & ((1u << lane) - 1u));
-            before += sums[k];
-            if (on && p % blocks == me) {
+            const int p = base + offsets[k * 32 + warp] + __popc(live[k] & ((1u << lane) - 1u));
+            base += sums[k];
+            if (on && (uint32_t)p % blocks == me) {
                 const int at = atomicAdd(&listed, 1);
-                list_token[at] = (int)t;
-                list_place[at] = (int)p;
+                list_token[at] = t;
+                list_place[at] = p;
             }
             // the small per-token arrays: a warp's 32 tokens by one block
-            if (t < a.T && (t / 32) % blocks == me) {
-                a.place[t] = on ? (int)p : -1;
+            if ((uint32_t)(t / 32) % blocks == me && t < T) {
+                a.place[t] = on ? p : -1;
                 if (on) {
-                    a.token[p] = (int)t;
+                    a.token[p] = t;
                     a.tgt[p] = (int)tg[k];
                     a.wt[p] = w[k];
                 } else {
@@ -144,13 +150,12 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
         for (int r = warp; r < listed; r += 32)
             copy_row(reinterpret_cast<uint16_t *>(a.x) + (int64_t)list_place[r] * a.ldw,
                      reinterpret_cast<const uint16_t *>(a.X) + (int64_t)list_token[r] * a.ldx, a.K, lane);
-        base += before;
         __syncthreads();  // the lists and counts are written again
     }
-    const int n = (int)base;
-    const int64_t pad = gg_min64(a.T, (base + kPad - 1) / kPad * kPad);
-    for (int64_t p = base + warp; p < pad; p += 32)
-        if (p % blocks == me) {
+    const int n = base;
+    const int64_t pad = gg_min64(a.T, ((int64_t)base + kPad - 1) / kPad * kPad);
+    for (int64_t p = (int64_t)base + warp; p < pad; p += 32)
+        if ((uint32_t)p % blocks == me) {
             uint16_t *row = reinterpret_cast<uint16_t *>(a.x) + p * a.ldw;
             for (int64_t c = lane; c < a.K; c += 32)
                 row[c] = 0;
@@ -184,22 +189,11 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
     }
 }
 
-// (largest, sum) of two parts.
-__device__ __forceinline__ void merge(float &m, float &s, float m1, float s1)
-{
-    const float top = fmaxf(m, m1);
-    if (top == -INFINITY) {  // nothing yet; a NaN's sum is NaN and stays
-        s += s1;
-        return;
-    }
-    s = s * expf(m - top) + s1 * expf(m1 - top);
-    m = top;
-}
-
-// 32 tokens a block, 32 shares of the rows.
+// 32 tokens a block, 32 shares of the rows; the rows twice (the second time from L2), so that no
+// exponential waits for another.  A sum of NaN stays NaN; rows of nothing but -inf have sum 0.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ EntropyArgs a)
 {
-    __shared__ float ms[32][33], ss[32][33];
+    __shared__ float part[32][33];
     __shared__ unsigned turn;
     __shared__ double sums[2][32];
     wait_dependencies();
@@ -207,23 +201,34 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int live = a.head->live, pad = a.head->live_pad;
     const int64_t p = (int64_t)blockIdx.x * 32 + lane;
-    float m = -INFINITY, s = 0.0f;
-    if (p < live) {
-#pragma unroll 4
-        for (int64_t r = g; r < a.rows; r += 32) {
-            const float2 q = a.partial[r * a.T + p];
-            merge(m, s, q.x, q.y);
-        }
+    const float2 *rows = a.partial + p;
+    const int64_t n = p < live ? a.rows : 0;
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int64_t r = g; r < n; r += 32)
+        m = fmaxf(m, rows[r * a.T].x);
+    part[g][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        m = fmaxf(m, part[k][lane]);
+    const float from = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t r = g; r < n; r += 32) {
+        const float2 q = rows[r * a.T];
+        s += q.y * expf(q.x - from);
     }
-    ms[g][lane] = m;
-    ss[g][lane] = s;
+    __syncthreads();
+    part[g][lane] = s;
     __syncthreads();
     if (g == 0 && p < pad) {
         float lse = 0.0f;
         if (p < live) {
-#pragma unroll 1
-            for (int k = 1; k < 32; ++k)
-                merge(m, s, ms[k][lane], ss[k][lane]);
+            s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                s += part[k][lane];
             lse = m + logf(s);
             const float loss = lse - a.ztarget[p];
             const int t = a.token[p];
@@ -285,10 +290,10 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
         const float *from = a.dx32 + p * a.ldw + n;  // (rows of whole 8 elements)
         if constexpr (V == 8) {
             float v[8] = {};
-            if (p >= 0) {
+            for (int s = 0; p >= 0 && s < a.shares; ++s, from += a.T * a.ldw) {
                 const float4 x = *reinterpret_cast<const float4 *>(from), y = *reinterpret_cast<const float4 *>(from + 4);
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u)
@@ -298,7 +303,10 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
                                        pair16_of<BF16>(v[4], v[5]), pair16_of<BF16>(v[6], v[7]))
                           : make_uint4(0u, 0u, 0u, 0u));
         } else {
-            store16(out, 0, p >= 0 ? *from * alpha : 0.0f, BF16);
+            float v = 0.0f;
+            for (int s = 0; p >= 0 && s < a.shares; ++s, from += a.T * a.ldw)
+                v += *from;
+            store16(out, 0, v * alpha, BF16);
         }
     }
 }

@@ -136,6 +136,21 @@ int64_t piece_of(int64_t V, int64_t piece)
     return piece < most ? piece : most;
 }
 
+// The loss's product leaves a partial result of every 128 entries where CTA pairs compute it, else of
+// every 32.  Beyond a few hundred tokens the pairs always do (the others would be slower, and the
+// partial results an eighth of the 16-bit logits).
+bool pairs_only(int64_t T, int64_t K) { return T > 512 && K > 0; }
+
+int64_t partial_rows(int64_t V, bool pairs) { return pairs ? (V + 127) / 128 : (V + 31) / 32; }
+
+// Shares of dX's contraction (plan_vocab): only where a wave of the 76 CTA pairs has room for more
+// than its tiles of 256 x 256.
+int most_shares(int64_t T, int64_t K)
+{
+    const int64_t tiles = ((T + 255) / 256) * ((K + 255) / 256);
+    return tiles >= 76 ? 1 : (tiles >= 38 ? 2 : (tiles >= 19 ? 4 : 8));
+}
+
 // The workspace's parts, one behind the other on 256-byte boundaries.
 struct EntropyPlaces {
     uint64_t x, place, token, tgt, wt, lossc, lsec, coef, ztarget, partial, dx32, dz, end;
@@ -154,9 +169,9 @@ EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, boo
     w.x = take(t * kp * 2);
     for (uint64_t *p : {&w.place, &w.token, &w.tgt, &w.wt, &w.lossc, &w.lsec, &w.coef, &w.ztarget})
         *p = take(t * 4);
-    w.partial = take(t * (uint64_t)((V + 31) / 32) * 8);
+    w.partial = take(t * (uint64_t)partial_rows(V, pairs_only(T, K)) * 8);
     if (gradients) {
-        w.dx32 = take(t * kp * 4);
+        w.dx32 = take(t * kp * 4 * (uint64_t)most_shares(T, K));
         w.dz = take(t * (uint64_t)piece_of(V, piece) * 2);
     }
     w.end = at;
@@ -264,7 +279,6 @@ gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw
     e.a.dX = const_cast<void *>(dX);
     e.a.lddx = lddx;
     e.a.ldw = (K + 7) / 8 * 8;
-    e.a.rows = (V + 31) / 32;
     e.W = W;
     e.ldw = ldw;
     e.kn = kn;
@@ -279,21 +293,28 @@ gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw
 
 gg_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? GG_OK : op_cuda_fail(e, what); }
 
-gg_status product(int epi, const LinearArgs &a, cudaStream_t s)
+gg_status product(int epi, const LinearArgs &a, const LinearPlan &plan, cudaStream_t s)
 {
     const char *why = nullptr;
-    const cudaError_t e = launch_linear(epi, a, plan_linear(epi, a, GG_LINEAR_AUTO), s, &why);
+    const cudaError_t e = launch_linear(epi, a, plan, s, &why);
     return launched(e, why ? why : "launching a product of the vocabulary");
+}
+
+gg_status product(int epi, const LinearArgs &a, cudaStream_t s)
+{
+    return product(epi, a, plan_linear(epi, a, GG_LINEAR_AUTO), s);
 }
 
 gg_status run_entropy(const Entropy &e, cudaStream_t s)
 {
-    const EntropyArgs &a = e.a;
+    EntropyArgs a = e.a;
     LinearArgs l{};
     l.is_bf16 = a.is_bf16;
     l.status = a.status;
     l.wait_limit_ns = op_wait_limit_ns();
     l.inject_stall = op_inject_stall();
+    l.shares = 1;
+    a.shares = 1;
     if (a.T == 0) {
         if (a.stats)
             GG_TRY(launched(cudaMemsetAsync(a.stats, 0, 8, s), "clearing the statistics"));
@@ -332,10 +353,14 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
     z.partial = a.partial;
     z.ldpartial = a.T;
     z.ztarget = a.ztarget;
-    GG_TRY(product(kEpiLse, z, s));
+    const LinearPlan plan = plan_linear(kEpiLse, z, pairs_only(a.T, a.K) ? GG_LINEAR_PAIR : GG_LINEAR_AUTO);
+    a.rows = partial_rows(a.V, plan.kernel == GG_LINEAR_PAIR);
+    GG_TRY(product(kEpiLse, z, plan, s));
     GG_TRY(launched(launch_entropy_join(a, s), "joining the vocabulary's sums"));
     if ((!a.dX && !e.dW) || a.K == 0)
         return op_ok();
+    bool both = false;
+    int bt_dx = 0, bt_dw = 0;
     for (int64_t v0 = 0; v0 < a.V; v0 += e.piece) {
         const int64_t n = a.V - v0 < e.piece ? a.V - v0 : e.piece;
         z = logits(v0, n, &a.head->live_pad);
@@ -373,10 +398,13 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         w.live = &a.head->live_pad;
         w.live_k = 1;
         w.alpha = &a.head->alpha;
-        int bt_dx, bt_dw;
-        if (a.dX && e.dW &&
-            plan_both(x, w, plan_linear(kEpiVocab, x, GG_LINEAR_AUTO), plan_linear(kEpiVocab, w, GG_LINEAR_AUTO),
-                      GG_LINEAR_AUTO, &bt_dx, &bt_dw)) {
+        if (v0 == 0 && a.dX && e.dW) {  // (the pieces are alike, and share dX's rows)
+            const double apart =
+                plan_linear(kEpiVocab, x, GG_LINEAR_AUTO).ns + plan_linear(kEpiVocab, w, GG_LINEAR_AUTO).ns;
+            both = plan_vocab(x, w, apart, most_shares(a.T, a.K), &bt_dx, &bt_dw, &a.shares);
+        }
+        x.shares = a.shares;
+        if (both) {
             const char *why = nullptr;
             const cudaError_t err = launch_both(kEpiVocab, x, bt_dx, w, bt_dw, s, &why);
             GG_TRY(launched(err, why ? why : "launching the gradients of a piece"));

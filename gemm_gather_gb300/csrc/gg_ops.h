@@ -28,7 +28,7 @@ constexpr int kEpiGradIn = 1;   // acc * act'(aux)
 constexpr int kEpiGradW = 2;    // acc (+ out)
 constexpr int kEpiGradIn8 = 3;  // acc * act'(aux), aux kept in 8 bits (codes, with scales)
 // The vocabulary's products (entropy_kernels.cu): i is a vocabulary entry of a piece, j a token.
-constexpr int kEpiLse = 4;       // (largest, sum of exponentials) of every 32 entries, and the target's logit
+constexpr int kEpiLse = 4;       // (largest, sum of exponentials) of 32 or 128 entries, and the target's logit
 constexpr int kEpiSoftGrad = 5;  // coef (exp(acc - lse) - (i is the target)), in 16 bits
 constexpr int kEpiVocab = 6;     // alpha acc (+ out): what the gradient of the logits is multiplied into
 
@@ -57,9 +57,10 @@ struct LinearArgs {
     // live_k, K is the most there can be).
     const int *live;
     int live_k;
+    int shares;            // kEpiVocab: of the contraction, share s into rows s J of out (else 1)
     const int *target;     // a token's, within the vocabulary
     int v0;                // the piece's first entry
-    float2 *partial;       // kEpiLse: (I + 31) / 32 rows, a place per token
+    float2 *partial;       // kEpiLse: a row for every 128 entries (split kernel: 32), a place per token
     int64_t ldpartial;
     float *ztarget;
     const float *lse, *coef;
@@ -84,6 +85,10 @@ cudaError_t launch_linear(int epi, const LinearArgs &a, const LinearPlan &p, cud
 // Both gradients of a layer in one launch (plan_both: whether, and their tiles).
 bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &plan_dx, const LinearPlan &plan_dw,
                int path, int *bt_dx, int *bt_dw);
+// The same for what the gradient of a piece of logits is multiplied into (kEpiVocab), where it takes less
+// than other_ns.
+bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int most_shares, int *bt_dx, int *bt_dw,
+                int *shares);
 cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
                         const char **why);
 
@@ -191,7 +196,8 @@ struct EntropyArgs {
     float *wt, *lossc, *lsec, *coef, *ztarget;
     float2 *partial;     // rows x T
     int64_t rows;
-    float *dx32;         // compact dX before its rounding, pitch ldw
+    float *dx32;         // compact dX before its rounding, pitch ldw, a share's T rows behind another's
+    int shares;
     int *status;
 };
 cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s);  // counts and gathers the tokens

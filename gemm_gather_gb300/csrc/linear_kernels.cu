@@ -164,9 +164,9 @@ __device__ __forceinline__ void emit_lse(const LinearArgs &a, int64_t i, int64_t
 
 // The same of 16 neighbouring columns in 2 KB of shared memory: a lane turns from a vocabulary entry
 // to half a column's entries (the exclusive or spreads both over the banks).  target: lane c mod 16
-// has column c's.
-__device__ __forceinline__ void emit_lse16(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane, int target,
-                                           const float (&v)[16], uint8_t *stage)
+// has column c's, and gets its result.
+__device__ __forceinline__ float2 lse16(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane, int target,
+                                        const float (&v)[16], uint8_t *stage)
 {
     float *t = reinterpret_cast<float *>(stage);
     const bool in = i0 + lane < a.I;
@@ -191,10 +191,26 @@ __device__ __forceinline__ void emit_lse16(const LinearArgs &a, int64_t i0, int6
         const int64_t at = (int64_t)target - i0;
         if (at >= half && at < half + 16 && at + i0 < a.I)
             a.ztarget[j0 + c] = t[c * 32 + ((int)at ^ c)];
-        if (half == 0 && i0 < a.I)
-            a.partial[i0 / 32 * a.ldpartial + j0 + c] = make_float2(m, s);
     }
     __syncwarp();
+    return make_float2(m, s);
+}
+
+// Whether all of 128 threads (the four warps of one group of columns) say yes; a barrier between them.
+__device__ __forceinline__ bool group_agrees(int group, bool yes)
+{
+    int all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all)
+                 : "r"((int)yes), "r"(1 + group)
+                 : "memory");
+    return all != 0;
+}
+
+__device__ __forceinline__ void group_sync(int group)
+{
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
 // One feature's sums for columns j0, j0 + jstep, ... (n of them, at most C):
@@ -618,6 +634,8 @@ struct Geo {
 
 struct Tile {
     int ti, tj;
+    // kLive: the share of the contraction that is this tile's, its first k-block and how many
+    int share, kb0, num_kb;
 };
 
 // Tile order: feature tiles in groups of a.group; group by group, every token
@@ -632,7 +650,7 @@ __device__ __forceinline__ Tile tile_at(const LinearArgs &a, uint32_t tiles_j, u
     const uint32_t r = t - g * full;
     const uint32_t left = (uint32_t)a.tiles_i - g * (uint32_t)a.group;
     const uint32_t width = left < (uint32_t)a.group ? left : (uint32_t)a.group;
-    Tile c;
+    Tile c = {};
     c.tj = (int)(r / width);
     c.ti = (int)(g * (uint32_t)a.group + r - (uint32_t)c.tj * width);
     return c;
@@ -647,22 +665,23 @@ struct Product {
     // kLive: the columns and their tiles that the device knows (see columns_of and tiles_of)
     int64_t J;
     uint32_t tiles_j;
-    __device__ __forceinline__ Product() : kb0(0), num_kb(0), total(0), first(0), tile{0, 0}, J(0), tiles_j(0) {}
+    __device__ __forceinline__ Product() : kb0(0), num_kb(0), total(0), first(0), tile{}, J(0), tiles_j(0) {}
     __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts, uint32_t first_)
         : kb0(0), num_kb(a.num_kb), total((uint32_t)a.tiles_i * (uint32_t)a.tiles_j), first(first_),
-          tile(first_ < total ? tile_at(a, (uint32_t)a.tiles_j, first_) : Tile{0, 0})
+          tile(first_ < total ? tile_at(a, (uint32_t)a.tiles_j, first_) : Tile{})
     {
         if (parts > 1)  // 2 or 4
             share_of(a.num_kb, part, parts, kb0, num_kb);
     }
     // The same with the tokens that the device counted; the launches before have to be waited for.
+    // Where a.shares > 1, every tile comes that many times, with a share of the contraction each.
     __device__ __forceinline__ void count(const LinearArgs &a, int part, int parts)
     {
         const int live = *a.live;
         num_kb = a.live_k ? (live + kBK - 1) / kBK : a.num_kb;
         J = a.live_k ? a.J : (int64_t)live;
         tiles_j = (uint32_t)((J + a.bt - 1) / a.bt);
-        total = (uint32_t)a.tiles_i * tiles_j;
+        total = (uint32_t)a.tiles_i * tiles_j * (uint32_t)a.shares;
         if (parts > 1)
             share_of(num_kb, part, parts, kb0, num_kb);
     }
@@ -670,10 +689,31 @@ struct Product {
     {
         first = first_;
         if (first < total)
-            tile = tile_at(a, tiles_j, first);
+            tile = live_tile(a, first);
+    }
+    __device__ __forceinline__ Tile live_tile(const LinearArgs &a, uint32_t t) const
+    {
+        if (a.shares == 1) {
+            Tile c = tile_at(a, tiles_j, t);
+            c.kb0 = kb0;
+            c.num_kb = num_kb;
+            return c;
+        }
+        const uint32_t tiles = (uint32_t)a.tiles_i * tiles_j, share = t / tiles;
+        Tile c = tile_at(a, tiles_j, t - share * tiles);
+        c.share = (int)share;
+        share_of(num_kb, (int)share, a.shares, c.kb0, c.num_kb);
+        return c;
     }
 };
 
+template <bool LIVE>
+__device__ __forceinline__ Tile tile_of(const LinearArgs &a, const Product &p, uint32_t t)
+{
+    if constexpr (LIVE)
+        return p.live_tile(a, t);
+    return tile_at(a, (uint32_t)a.tiles_j, t);
+}
 template <int EPI>
 __device__ __forceinline__ int64_t columns_of(const LinearArgs &a, const Product &p)
 {
@@ -681,14 +721,6 @@ __device__ __forceinline__ int64_t columns_of(const LinearArgs &a, const Product
         return p.J;
     return a.J;
 }
-template <bool LIVE>
-__device__ __forceinline__ uint32_t tiles_of(const LinearArgs &a, const Product &p)
-{
-    if constexpr (LIVE)
-        return p.tiles_j;
-    return (uint32_t)a.tiles_j;
-}
-
 // Where a thread block stands: the same for all its roles but the fields a role moves.
 struct Place {
     uint32_t base;          // shared memory, 1024-aligned
@@ -728,8 +760,9 @@ __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensor
         const int i0 = c.ti * kTileI + (int)at.rank * 128;
         const int j0 = c.tj * a.bt + (int)at.rank * (a.bt / 2);
         const int skip = (int)(at.count + at.half) & 1;  // the other producer's
-        int k0 = (p.kb0 + skip) * kBK;
-        for (int kb = skip; kb < p.num_kb; kb += 2, k0 += 2 * kBK) {
+        const int num_kb = LIVE ? c.num_kb : p.num_kb;
+        int k0 = ((LIVE ? c.kb0 : p.kb0) + skip) * kBK;
+        for (int kb = skip; kb < num_kb; kb += 2, k0 += 2 * kBK) {
             const uint32_t bar_at = (uint32_t)at.stage * 8;
             if (!role_wait(empty0 + bar_at, at.phase ^ 1u, a.wait_limit_ns, at.abort_flag))
                 return false;
@@ -746,16 +779,16 @@ __device__ __forceinline__ bool produce(const CUtensorMap &map_a, const CUtensor
                 at.phase ^= 1u;
             }
         }
-        at.count += p.num_kb;
+        at.count += num_kb;
         t += at.nunits;
         if (t < p.total)
-            c = tile_at(a, tiles_of<LIVE>(a, p), t);
+            c = tile_of<LIVE>(a, p, t);
     }
     return true;
 }
 
 // The MMA issuer's share of the same.
-template <int BT>
+template <int BT, bool LIVE>
 __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, Place &at, bool *issued_any)
 {
     using G = Geo<BT>;
@@ -768,7 +801,8 @@ __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, 
     const uint16_t both = (uint16_t)(3u << at.lead);
     for (uint32_t t = p.first; t < p.total; t += at.nunits) {
         int in_chunk = 0;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        const int num_kb = LIVE ? p.live_tile(a, t).num_kb : p.num_kb;
+        for (int kb = 0; kb < num_kb; ++kb) {
             const int acc = (int)(at.count & 1);  // chunks issued so far: accumulator count & 1
             if (in_chunk == 0 &&
                 !role_wait(ptx::smem_addr(&at.sh->tmem_empty[acc]), (uint32_t)((at.count >> 1) & 1) ^ 1u,
@@ -785,7 +819,7 @@ __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, 
             mma_commit_to(empty0 + (uint32_t)at.stage * 8, both);
             *issued_any = true;
             ++in_chunk;
-            if (in_chunk == a.chunk || kb + 1 == p.num_kb) {
+            if (in_chunk == a.chunk || kb + 1 == num_kb) {
                 mma_commit_to(ptx::smem_addr(&at.sh->tmem_full[acc]), both);
                 ++at.count;
                 in_chunk = 0;
@@ -814,14 +848,18 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
     float *partial = reinterpret_cast<float *>(at.smem) + at.group * kStageCols * 128 + at.q * 32 + lane;
     const Rows aux = aux_of<EPI>(a);
     const bool early = aux.p != nullptr && at.parts == 1;
-    const int chunks = (p.num_kb + a.chunk - 1) / a.chunk;
+    int chunks = kLive<EPI> ? 0 : (p.num_kb + a.chunk - 1) / a.chunk;
     const auto column = [](int u) { return u / kStageCols * kStep + u % kStageCols; };
     for (uint32_t t = p.first; t < p.total; t += at.nunits) {
-        const Tile c = tile_at(a, tiles_of<kLive<EPI>>(a, p), t);
+        const Tile c = tile_of<kLive<EPI>>(a, p, t);
+        if (kLive<EPI>)
+            chunks = (c.num_kb + a.chunk - 1) / a.chunk;
         const int64_t i0 = (int64_t)c.ti * kTileI + (int)at.rank * 128 + at.q * 32;
         const int64_t j0 = (int64_t)c.tj * a.bt + at.group * kStageCols;
         // the first token that is not this tile's
         const int64_t end = gg_min64(columns_of<EPI>(a, p), (int64_t)(c.tj + 1) * a.bt);
+        // each share has rows of its own
+        const int64_t row0 = EPI == kEpiVocab ? c.share * a.J : 0;
         const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
         uint4 pre[kRowSteps];
         if (!kSums<EPI> && early)  // the first group's rows, while the MMAs run
@@ -842,7 +880,8 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
             const int acc = (int)(at.count & 1);
             const bool got = role_wait(ptx::smem_addr(&at.sh->tmem_full[acc]),
                                        (uint32_t)((at.count >> 1) & 1), a.wait_limit_ns, at.abort_flag);
-            if (!__all_sync(0xffffffffu, got))
+            // (the warps of a group meet below: they give up together)
+            if (EPI == kEpiLse ? !group_agrees(at.group, got) : !__all_sync(0xffffffffu, got))
                 return false;
             fence_after();
             const uint32_t t_addr = t_lane + (uint32_t)(acc * BT);
@@ -894,6 +933,8 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                 mbar_arrive_cluster(empty0 + (uint32_t)(acc * sizeof(uint64_t)));
         }
         if constexpr (EPI == kEpiLse) {
+            // each warp its 32 entries, then the four of a group their 128
+            float2 own[kCols / 16];
 #pragma unroll
             for (int col = 0; col < kCols; col += 16) {
                 const int64_t jc = j0 + column(col);
@@ -906,8 +947,36 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                     v[u] = sum[col + u];
                 const int target =
                     __shfl_sync(0xffffffffu, terms[col / kStageCols].target, (lane & 15) + col % kStageCols);
-                emit_lse16(a, i0, jc, n, lane, target, v, at.stage_buf);
+                own[col / 16] = lse16(a, i0, jc, n, lane, target, v, at.stage_buf);
             }
+            float2 *mine = reinterpret_cast<float2 *>(at.stage_buf);
+#pragma unroll
+            for (int col = 0; col < kCols; col += 16)
+                if (lane < 16)
+                    mine[col + lane] = own[col / 16];
+            group_sync(at.group);
+            // warp q finishes a quarter of the columns
+            constexpr int kEach = kCols / 4;
+            const int col = at.q * kEach + lane;
+            const int64_t j = j0 + column(col);
+            if (lane < kEach && j < end) {
+                const uint8_t *first = at.stage_buf - ((at.q + 2) & 3) * kWarpStage;  // q = (2, 3, 0, 1)
+                float2 x[4];
+                float m = -INFINITY, s = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[k] = reinterpret_cast<const float2 *>(first + k * kWarpStage)[col];
+                    m = fmaxf(m, x[k].x);
+                }
+                const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s += x[k].y * ex2_approx((x[k].x - from) * kLog2e);
+                const int64_t row = (i0 - at.q * 32) / 128;
+                if (row * 128 < a.I)
+                    a.partial[row * a.ldpartial + j] = make_float2(m, s);
+            }
+            group_sync(at.group);
         } else if constexpr (kSums<EPI>) {
             if (at.parts > 1) {
 #pragma unroll
@@ -921,15 +990,15 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                     for (int u = 0; u < 16; ++u)
                         v[u] = sum[col + u];
                     const int64_t jc = j0 + column(col);
-                    emit16<EPI>(a, i0 + lane, jc, 1, valid16(end, jc), v, 0.0f);
+                    emit16<EPI>(a, i0 + lane, row0 + jc, 1, valid16(end, jc), v, 0.0f);
                 }
             } else {
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     const int64_t jg = j0 + g * kStep;
                     if (early)
-                        read_aux<EPI>(a, aux, i0, jg, valid_rows(end, jg), lane, pre);
-                    emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
+                        read_aux<EPI>(a, aux, i0, row0 + jg, valid_rows(end, jg), lane, pre);
+                    emit_rows<EPI>(a, i0, row0 + jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
                                    [&](int col, float(&v)[16]) {
 #pragma unroll
                                        for (int u = 0; u < 16; ++u)
@@ -951,7 +1020,7 @@ __device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p
     const int lane = at.lane, parts = at.parts;
     if (kLive<EPI> && at.unit >= p.total)
         return;
-    const Tile c = tile_at(a, tiles_of<kLive<EPI>>(a, p), at.unit);
+    const Tile c = tile_of<kLive<EPI>>(a, p, at.unit);
     // 16 columns a warp at least: with 32 left for a pair, half the warps finish them
     const int cols = BT / parts >= 64 ? BT / parts / 4 : 16;
     const int col0 = at.part * (BT / parts) + at.group * cols;
@@ -1117,9 +1186,9 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         // ===================== MMA issuer (one thread of the leader CTA) ====
         if (at.rank == 0 && ptx::elect_one_sync()) {
             bool issued_any = false;
-            ok = pair::multiply<BT>(a, p, at, &issued_any);
+            ok = pair::multiply<BT, kLive<EPI>>(a, p, at, &issued_any);
             if (kTwo && ok)
-                ok = pair::multiply<BT>(a1, p1, at, &issued_any);
+                ok = pair::multiply<BT, kLive<EPI>>(a1, p1, at, &issued_any);
             if (!ok) {
                 *at.abort_flag = 1;
                 report_status(a.status, kStatusTimeout);
@@ -1960,6 +2029,50 @@ static cudaError_t launch_both_of(const LinearArgs &x, int bt_dx, const LinearAr
 {
     return bt_dx > 128 || bt_dw > 128 ? launch_pair<EPI, EPI1, 256>(x, bt_dx, 1, &w, bt_dw, s, why)
                                       : launch_pair<EPI, EPI1, 128>(x, bt_dx, 1, &w, bt_dw, s, why);
+}
+
+// The products that the gradient of a piece's logits goes into, in one walk of the pairs: dX's tiles are few
+// and long (its contraction is the piece), dW's many and short.  A pair with one long tile more than the others
+// would end long after them, so a long contraction is dealt out in shares (up to most_shares), each into
+// float32 rows of its own; the walk deals tiles in turn, so three pairs show the last to end.  Tiles whose
+// contraction is shorter than their epilogue take the epilogue's time.  777 tokens, V = 32768, K = 2011: one
+// share 196 us, see the table of the design for now.
+bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int most_shares, int *bt_dx, int *bt_dw,
+                int *shares)
+{
+    const auto tiles = [](const LinearArgs &x, int bt) { return ((x.I + 255) / 256) * ((x.J + bt - 1) / bt); };
+    const auto tile_ns = [](double kbs, double kb_ns, int bt) {
+        const double ns = kbs * kb_ns, epilogue = 23.2 * bt;
+        return (ns > epilogue ? ns : epilogue) + 196.0;
+    };
+    const int64_t kb0 = (dx.K + kBK - 1) / kBK, kb1 = (dw.K + kBK - 1) / kBK;
+    const bool lines_dx = on_lines(dx), lines_dw = on_lines(dw);
+    double least = other_ns;
+    bool found = false;
+    for (int b0 = 64; b0 <= 256; b0 += 32)
+        for (int b1 = 128; b1 <= 256; b1 += 128)
+            for (int s = 1; s <= most_shares && s <= kb0; s += s < 4 ? 1 : 2) {
+                const int64_t n0 = tiles(dx, b0) * s, n1 = tiles(dw, b1);
+                const double ctas = 2.0 * (double)(n0 + n1 < 76 ? n0 + n1 : 76);
+                const double w0 = tile_ns((double)((kb0 + s - 1) / s), pair_kb_ns(b0, lines_dx, ctas), b0);
+                const double w1 = tile_ns((double)kb1, pair_kb_ns(b1, lines_dw, ctas), b1);
+                double ns = 0.0;
+                for (const int64_t u : {(int64_t)0, n0 % 76, (n0 + 75) % 76}) {
+                    const int64_t c0 = u < n0 ? (n0 - u + 75) / 76 : 0;
+                    const int64_t all = u < n0 + n1 ? (n0 + n1 - u + 75) / 76 : 0;
+                    const double here = (double)c0 * w0 + (double)(all - c0) * w1;
+                    ns = here > ns ? here : ns;
+                }
+                ns += pair_ns(b0 > b1 ? b0 : b1);
+                if (ns < least) {
+                    least = ns;
+                    *bt_dx = b0;
+                    *bt_dw = b1;
+                    *shares = s;
+                    found = true;
+                }
+            }
+    return found;
 }
 
 cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,

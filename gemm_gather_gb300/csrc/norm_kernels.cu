@@ -19,14 +19,19 @@
 // adds the blocks' rows.  Fixed orders throughout: the same bits on every run.
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "act.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
 #include "pack8.cuh"
-#include "ptx.cuh"
+#include "tc.cuh"
 
 namespace gg {
 namespace {
+
+using tc::launch_dependents;
+using tc::wait_dependencies;
 
 constexpr int kSMs = 152;
 constexpr int kMaxWarps = 32;
@@ -115,35 +120,94 @@ __device__ __forceinline__ uint4 halves8(const float (&v)[8])
                       pair16_of<BF16>(v[6], v[7]));
 }
 
+// ---- rows in flight ---------------------------------------------------------------------
+// Where a block walks several rows, its threads copy the next rows' vectors into slots of their own in
+// shared memory (D rows deep, one commit group a row) while they work on the present one; nobody else
+// reads a thread's slots, so there is nothing to wait for but its own copies.  D = 1: one row a block and
+// no copies ahead, vectors come straight into registers.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's slots: vector k of input i of the row in slot d.
+template <int VPT, int INPUTS>
+struct Slots {
+    uint4 *mine;
+    __device__ __forceinline__ explicit Slots(uint8_t *smem) : mine(reinterpret_cast<uint4 *>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ uint4 *at(int d, int i, int k) const
+    {
+        return mine + ((d * INPUTS + i) * VPT + k) * (int)blockDim.x;
+    }
+    // Vector k of a row, `left` elements to the row's end (0 or less: none, and zeros in the slot).
+    __device__ __forceinline__ void copy(int d, int i, int k, const uint16_t *row, int64_t n, int64_t left) const
+    {
+        const int bytes = left >= 8 ? 16 : (left > 0 ? (int)left * 2 : 0);
+        copy16(ptx::smem_addr(at(d, i, k)), left > 0 ? row + n : row, bytes);
+    }
+};
+
 // ---- forward ------------------------------------------------------------------------------
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a, const RowShape s)
+template <bool BF16, int VPT, int D, bool RES>
+__global__ void __launch_bounds__(VPT > 2 && D > 1 ? 512 : 1024)
+    norm_kernel(const __grid_constant__ NormArgs a, const RowShape s)
 {
     __shared__ float sums[2][kMaxWarps];
+    extern __shared__ __align__(16) uint8_t ring[];
+    const Slots<VPT, RES ? 2 : 1> slots(ring);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp % s.R;
     const int64_t step = (int64_t)gridDim.x * s.rows;
     const uint16_t *x = reinterpret_cast<const uint16_t *>(a.x), *r = reinterpret_cast<const uint16_t *>(a.residual);
-    int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * s.rows; row0 < a.M; row0 += step, turn ^= 1) {
-        const int64_t row = row0 + warp / s.R;
+    const auto column = [&](int k) { return (int64_t)((k * s.R + sub) * 32 + lane) * kVec; };
+    int64_t row = (int64_t)blockIdx.x * s.rows + warp / s.R;
+    const auto ahead = [&](int64_t at, int d) {
+        if (at < a.M) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t n = column(k);
+                slots.copy(d, 0, k, x + at * a.ldx, n, a.N - n);
+                if (RES)
+                    slots.copy(d, RES ? 1 : 0, k, r + at * a.ldr, n, a.N - n);
+            }
+        }
+        copies_commit();
+    };
+    if constexpr (D > 1) {
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d)
+            ahead(row + d * step, d);
+    }
+    int turn = 0, slot = 0;
+    // the block's rows end together: its first one decides
+    for (int64_t row0 = (int64_t)blockIdx.x * s.rows; row0 < a.M; row0 += step, row += step, turn ^= 1) {
         const bool live = row < a.M;
         uint4 h[VPT];
         float sq = 0.0f;
+        if constexpr (D > 1) {
+            ahead(row + (D - 1) * step, slot == 0 ? D - 1 : slot - 1);
+            copies_wait<D - 1>();
+        }
         if (live) {
             uint4 q[VPT];
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec;
-                h[k] = load8(x + row * a.ldx + n, a.N - n);
-                if (r)
-                    q[k] = load8(r + row * a.ldr + n, a.N - n);
+                const int64_t n = column(k);
+                h[k] = D > 1 ? *slots.at(slot, 0, k) : load8(x + row * a.ldx + n, a.N - n);
+                if (RES)
+                    q[k] = D > 1 ? *slots.at(slot, RES ? 1 : 0, k) : load8(r + row * a.ldr + n, a.N - n);
             }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float v[8];
                 floats8<BF16>(h[k], v);
-                if (r) {
+                if (RES) {
                     float t[8];
                     floats8<BF16>(q[k], t);
 #pragma unroll
@@ -159,11 +223,16 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
             if (a.h) {
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
-                    const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec;
+                    const int64_t n = column(k);
                     store8(reinterpret_cast<uint16_t *>(a.h) + row * a.ldh + n, a.N - n, h[k]);
                 }
             }
         }
+        if constexpr (D > 1)
+            slot = slot + 1 == D ? 0 : slot + 1;
+        float w[8];
+        if (VPT == 1 && live)  // few rows: the weights' latency beside the sum's
+            load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, column(0), a.N - column(0), w);
         const float total = row_sum(sq, s, sums, turn);
         if (!live)
             continue;
@@ -172,10 +241,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
             a.rstd[row] = rstd;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec, left = a.N - n;
-            float v[8], w[8];
+            const int64_t n = column(k), left = a.N - n;
+            float v[8];
             floats8<BF16>(h[k], v);
-            load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left, w);
+            if (VPT > 1)
+                load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left, w);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 v[u] = v[u] * rstd * w[u];
@@ -261,45 +331,74 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const __grid_constant__ N
 }
 
 // ---- backward -----------------------------------------------------------------------------
-template <bool BF16, int VPT>
+template <bool BF16, int VPT, int D, bool IN>
 __global__ void __launch_bounds__(VPT > 2 ? 512 : 1024) norm_backward_kernel(const __grid_constant__ NormBackwardArgs a,
                                                                              const RowShape s)
 {
     __shared__ float sums[2][kMaxWarps];
-    extern __shared__ float columns[];  // where a block has several rows: their sums
+    // the rows in flight; at the end, where a block has several rows at a time, their sums
+    extern __shared__ __align__(16) uint8_t ring[];
+    constexpr int kInputs = IN ? 3 : 2;
+    const Slots<VPT, kInputs> slots(ring);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp % s.R;
     const int64_t step = (int64_t)gridDim.x * s.rows;
     const uint16_t *dy = reinterpret_cast<const uint16_t *>(a.dy), *h = reinterpret_cast<const uint16_t *>(a.h),
                    *in = reinterpret_cast<const uint16_t *>(a.dh_in);
+    const auto column = [&](int k) { return (int64_t)((k * s.R + sub) * 32 + lane) * kVec; };
     float dw[VPT][8];
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             dw[k][u] = 0.0f;
-    int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * s.rows; row0 < a.M; row0 += step, turn ^= 1) {
-        const int64_t row = row0 + warp / s.R;
+    int64_t row = (int64_t)blockIdx.x * s.rows + warp / s.R;
+    const auto ahead = [&](int64_t at, int d) {
+        if (at < a.M) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t n = column(k);
+                slots.copy(d, 0, k, dy + at * a.lddy, n, a.N - n);
+                slots.copy(d, 1, k, h + at * a.ldh, n, a.N - n);
+                if (IN)
+                    slots.copy(d, kInputs - 1, k, in + at * a.lddhin, n, a.N - n);
+            }
+        }
+        copies_commit();
+    };
+    if constexpr (D > 1) {
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d)
+            ahead(row + d * step, d);
+    }
+    int turn = 0, slot = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * s.rows; row0 < a.M; row0 += step, row += step, turn ^= 1) {
         const bool live = row < a.M;
         uint4 qy[VPT], qh[VPT], qi[VPT];
         float dot = 0.0f, rstd = 0.0f;
-        if (live) {
+        if (live)
             rstd = a.rstd[row];
+        if constexpr (D > 1) {
+            ahead(row + (D - 1) * step, slot == 0 ? D - 1 : slot - 1);
+            copies_wait<D - 1>();
+        }
+        if (live) {
+            if constexpr (D == 1) {
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec;
-                qy[k] = load8(dy + row * a.lddy + n, a.N - n);
-                qh[k] = load8(h + row * a.ldh + n, a.N - n);
-                if (in)
-                    qi[k] = load8(in + row * a.lddhin + n, a.N - n);
+                for (int k = 0; k < VPT; ++k) {
+                    const int64_t n = column(k);
+                    qy[k] = load8(dy + row * a.lddy + n, a.N - n);
+                    qh[k] = load8(h + row * a.ldh + n, a.N - n);
+                    if (IN)
+                        qi[k] = load8(in + row * a.lddhin + n, a.N - n);
+                }
             }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec;
+                const int64_t n = column(k);
                 float y[8], u8[8], w[8];
-                floats8<BF16>(qy[k], y);
-                floats8<BF16>(qh[k], u8);
+                floats8<BF16>(D > 1 ? *slots.at(slot, 0, k) : qy[k], y);
+                floats8<BF16>(D > 1 ? *slots.at(slot, 1, k) : qh[k], u8);
                 load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, a.N - n, w);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
@@ -310,36 +409,44 @@ __global__ void __launch_bounds__(VPT > 2 ? 512 : 1024) norm_backward_kernel(con
             }
         }
         const float c = row_sum(dot, s, sums, turn) / (float)a.N;
-        if (!live || !a.dh)
-            continue;
+        if (live && a.dh) {
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec, left = a.N - n;
-            float y[8], v[8], w[8];
-            floats8<BF16>(qy[k], y);
-            floats8<BF16>(qh[k], v);
-            load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left, w);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                v[u] = rstd * (y[u] * w[u] - v[u] * rstd * c);
-            if (in) {
-                float t[8];
-                floats8<BF16>(qi[k], t);
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t n = column(k), left = a.N - n;
+                float y[8], v[8], w[8];
+                floats8<BF16>(D > 1 ? *slots.at(slot, 0, k) : qy[k], y);
+                floats8<BF16>(D > 1 ? *slots.at(slot, 1, k) : qh[k], v);
+                load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left, w);
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    v[u] += t[u];
+                    v[u] = rstd * (y[u] * w[u] - v[u] * rstd * c);
+                if (IN) {
+                    float t[8];
+                    floats8<BF16>(D > 1 ? *slots.at(slot, kInputs - 1, k) : qi[k], t);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        v[u] += t[u];
+                }
+                store8(reinterpret_cast<uint16_t *>(a.dh) + row * a.lddh + n, left, halves8<BF16>(v));
             }
-            store8(reinterpret_cast<uint16_t *>(a.dh) + row * a.lddh + n, left, halves8<BF16>(v));
         }
+        if constexpr (D > 1)
+            slot = slot + 1 == D ? 0 : slot + 1;
     }
+    launch_dependents();
     if (!a.partial)
         return;
     float *out = a.partial + (int64_t)blockIdx.x * a.N;
+    float *columns = reinterpret_cast<float *>(ring);
+    if (D > 1 && s.rows > 1) {
+        copies_wait<0>();
+        __syncthreads();  // the slots become the columns' sums
+    }
     for (int g = 0; g < s.rows; ++g) {  // row group by row group, in order
         if (warp / s.R == g) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = (int64_t)((k * s.R + sub) * 32 + lane) * kVec;
+                const int64_t n = column(k);
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
                     if (n + u < a.N) {
@@ -396,17 +503,19 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
     a.partial[blockIdx.y * a.N + n] = t;
 }
 
-// dw from the blocks' rows: 32 columns a block, eight shares of the rows, added in order.
-__global__ void __launch_bounds__(256) norm_join_kernel(const float *partial, int parts, int64_t N, void *out, int out_f32,
-                                                        int is_bf16, int accumulate)
+// dw from the blocks' rows: 32 columns a block, 32 shares of the rows, added in order.  It begins while the
+// launch before it ends, and waits for that.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float *partial, int parts, int64_t N, void *out, int out_f32,
+                                                         int is_bf16, int accumulate)
 {
-    __shared__ float share[8][32];
+    __shared__ float share[32][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+    wait_dependencies();
     float t = 0.0f;
     if (n < N) {
-        const int from = parts * g / 8, to = parts * (g + 1) / 8;
-#pragma unroll 8
+        const int from = parts * g / 32, to = parts * (g + 1) / 32;
+#pragma unroll 10
         for (int p = from; p < to; ++p)
             t += partial[p * N + n];
     }
@@ -416,7 +525,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const float *partial, in
         return;
     t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 32; ++k)
         t += share[k][lane];
     if (out_f32) {
         float *o = reinterpret_cast<float *>(out) + n;
@@ -427,27 +536,41 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const float *partial, in
 }
 
 // ---- 8-bit activations by themselves --------------------------------------------------------
-// 16 lanes a block of 128 elements.
-template <bool BF16>
+// 16 lanes a block of 128 elements; kAhead blocks' loads in flight.  I: 32-bit indices where all
+// blocks have one (a 64-bit division costs as much as the rest of a block).
+constexpr int kAhead = 4;
+template <bool BF16, typename I>
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a)
 {
-    const int64_t units = (a.N + kPackBlock - 1) / kPackBlock;  // blocks of a row
-    const int64_t total = a.M * units;
-    const int64_t step = (int64_t)gridDim.x * 16;
+    const I units = (I)((a.N + kPackBlock - 1) / kPackBlock);  // blocks of a row
+    const I total = (I)a.M * units;
     const int lane = threadIdx.x & 15;
-    // a warp's two halves end together
-    for (int64_t t0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; t0 < total; t0 += step) {
-        const int64_t t = t0 + ((threadIdx.x >> 4) & 1);
-        const int64_t row = t / units, b = t - row * units, n = b * kPackBlock + lane * kVec;
-        const int64_t left = t < total ? a.N - n : 0;
-        float v[8];
-        floats8<BF16>(load8(reinterpret_cast<const uint16_t *>(a.x) + row * a.ldx + n, left), v);
-        int e;
-        const uint2 c = pack_group(v, &e);
-        if (left > 0) {
-            store_codes8(a.codes + row * a.ldc + n, left, c);
-            if (lane == 0)
-                a.scales[row * a.lds + b] = power_of_two(e);
+    // a block of threads takes 16 neighbouring units kAhead times
+    for (I t0 = (I)blockIdx.x * (16 * kAhead) + (threadIdx.x >> 5) * 2; t0 < total; t0 += (I)gridDim.x * (16 * kAhead)) {
+        uint4 q[kAhead];
+        int64_t row[kAhead], n[kAhead];
+        int left[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const I t = t0 + 16 * k + ((threadIdx.x >> 4) & 1);
+            const I r = t / units;
+            row[k] = r;
+            n[k] = (int64_t)(t - r * units) * kPackBlock + lane * kVec;
+            const int64_t l = t < total ? a.N - n[k] : 0;
+            left[k] = l >= 8 ? 8 : (int)l;
+            q[k] = load8(reinterpret_cast<const uint16_t *>(a.x) + row[k] * a.ldx + n[k], left[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            float v[8];
+            floats8<BF16>(q[k], v);
+            int e;
+            const uint2 c = pack_group(v, &e);
+            if (left[k] > 0) {
+                store_codes8(a.codes + row[k] * a.ldc + n[k], left[k], c);
+                if (lane == 0)
+                    a.scales[row[k] * a.lds + n[k] / kPackBlock] = power_of_two(e);
+            }
         }
     }
 }
@@ -475,38 +598,52 @@ __global__ void __launch_bounds__(256) pack_any_kernel(const __grid_constant__ P
     }
 }
 
-// V elements per thread and step, as act_backward.
-template <bool BF16, int V>
+// V elements per thread and step (8 where rows of out are 16-byte and rows of codes 8-byte aligned), kAhead
+// steps' loads in flight.
+template <bool BF16, int V, typename I>
 __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ UnpackArgs a)
 {
-    const int64_t units = (a.N + V - 1) / V;
-    const int64_t total = a.M * units;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += step) {
-        const int64_t row = t / units, n = (t - row * units) * V;
-        const int64_t left = V == 8 ? a.N - n : 1;
-        const float scale = a.scales[row * a.lds + n / kPackBlock];
-        float v[8] = {};
-        {
-            const uint8_t *p = a.codes + row * a.ldc + n;
-            const uint2 c = V == 8 ? load_codes8(p, left) : make_uint2(*p, 0u);
-            float x[4];
-            unpack4(c.x, x);
+    const I units = (I)((a.N + V - 1) / V);
+    const I total = (I)a.M * units;
+    for (I t0 = (I)blockIdx.x * (256 * kAhead) + threadIdx.x; t0 < total; t0 += (I)gridDim.x * (256 * kAhead)) {
+        uint2 c[kAhead];
+        float scale[kAhead];
+        uint16_t *out[kAhead];
+        int left[kAhead];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                v[u] = held16<BF16>(x[u] * scale);
-            unpack4(c.y, x);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                v[4 + u] = held16<BF16>(x[u] * scale);
+        for (int k = 0; k < kAhead; ++k) {
+            const I t = t0 + 256 * k;
+            const I row = t / units;
+            const int64_t n = (int64_t)(t - row * units) * V;
+            left[k] = 0;
+            if (t < total) {
+                left[k] = V == 8 ? (a.N - n >= 8 ? 8 : (int)(a.N - n)) : 1;
+                const uint8_t *p = a.codes + row * a.ldc + n;
+                c[k] = V == 8 ? load_codes8(p, left[k]) : make_uint2(*p, 0u);
+                scale[k] = a.scales[row * a.lds + n / kPackBlock];
+                out[k] = reinterpret_cast<uint16_t *>(a.out) + row * a.ldo + n;
+            }
         }
-        if (a.act != GG_ACT_NONE)
-            with_act(a.act, [&](auto k) { apply_act<decltype(k)::value>(v); });
-        uint16_t *out = reinterpret_cast<uint16_t *>(a.out) + row * a.ldo + n;
-        if (V == 8)
-            store8(out, left, halves8<BF16>(v));
-        else
-            store16(out, 0, v[0], BF16);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (left[k] == 0)
+                break;
+            float v[8], x[4];
+            unpack4(c[k].x, x);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v[u] = held16<BF16>(x[u] * scale[k]);
+            unpack4(c[k].y, x);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v[4 + u] = held16<BF16>(x[u] * scale[k]);
+            if (a.act != GG_ACT_NONE)
+                with_act(a.act, [&](auto f) { apply_act<decltype(f)::value>(v); });
+            if (V == 8)
+                store8(out[k], left[k], halves8<BF16>(v));
+            else
+                store16(out[k], 0, v[0], BF16);
+        }
     }
 }
 
@@ -514,31 +651,88 @@ __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unp
 bool on16(const void *p, int64_t ld) { return ((reinterpret_cast<uint64_t>(p) | (uint64_t)(ld * 2)) & 15) == 0; }
 bool on8(const void *p, int64_t ld) { return ((reinterpret_cast<uint64_t>(p) | (uint64_t)ld) & 7) == 0; }
 
-// Warps and vectors a thread for rows of N elements.  Few rows: as many warps as there are, since
-// then a row's own latency is the time; many: up to 4 vectors a thread, so that a block has several
-// rows' loads in flight.
-bool row_shape(int64_t M, int64_t N, int most_vpt_at_1024, RowShape *s, int *vpt)
+// Warps and vectors a thread for rows of N elements.  While the rows' vectors, one a thread, fit the GPU's
+// threads about once, a row's own latency is the time, so it gets as many warps as it has vectors for;
+// else up to 4 vectors a thread, so that more rows are in flight: 777 x 1523 takes 5 us with one and 8 with
+// four, 16384 x 8192 (forward) 240 us with one and 195 with four.  `most`: vectors a thread that 1024 threads hold.
+bool row_shape(int64_t M, int64_t N, int most, RowShape *s, int *vpt)
 {
     const int64_t warps = (N + 32 * kVec - 1) / (32 * kVec);  // at one vector a thread
-    if (warps > 32 * most_vpt_at_1024)
+    if (warps > 32 * most)
         return false;
-    int v = M <= kSMs ? 1 : 4;
+    int v = M * warps <= kSMs * 32 ? 1 : 4;
     while (v > 1 && warps < v)
         v /= 2;
-    while ((warps + v - 1) / v > (v > most_vpt_at_1024 ? 16 : 32))
+    while ((warps + v - 1) / v > (v > most ? 16 : 32))
         v *= 2;
-    int R = 1;
-    while (R * v < warps)
-        R *= 2;
+    s->R = (int)((warps + v - 1) / v);
+    s->rows = s->R >= 8 ? 1 : 8 / s->R;
     *vpt = v;
-    s->R = R;
-    s->rows = R >= 8 ? 1 : 8 / R;
     return true;
 }
 
-int row_blocks(int64_t M, const RowShape &s, int per_sm)
+// Blocks of a launch and how deep their rows' copies go: two blocks of up to 110 KB an SM, where that
+// makes every block walk a few rows and its slots fit; else a block a row group.
+struct RowPlan {
+    int grid, threads, depth, smem;
+};
+
+RowPlan row_plan(int64_t M, const RowShape &s, int vpt, int inputs, int most_blocks)
 {
-    return (int)gg_min64((M + s.rows - 1) / s.rows, (int64_t)kSMs * per_sm);
+    RowPlan p{};
+    p.threads = 32 * s.R * s.rows;
+    const int64_t groups = (M + s.rows - 1) / s.rows;
+    const int slot = p.threads * vpt * inputs * 16;
+    const int per_sm = p.threads <= 512 ? 512 / p.threads : 0;
+    const int depth = per_sm > 0 ? (220 * 1024 / per_sm - 1024) / slot : 0;
+    if (vpt == 4 && depth >= 2 && groups >= 2 * kSMs * per_sm) {
+        p.depth = depth >= 3 ? 3 : 2;
+        p.smem = p.depth * slot;
+        p.grid = (int)gg_min64(most_blocks, (int64_t)kSMs * per_sm);
+    } else {
+        p.depth = 1;
+        p.grid = (int)gg_min64(gg_min64(groups, most_blocks), (int64_t)kSMs * (2048 / p.threads));
+    }
+    return p;
+}
+
+// Dynamic shared memory of a kernel, set once per device.
+constexpr int kMaxDevices = 64;
+template <typename K>
+cudaError_t allow_smem(K kernel, std::once_flag *once, cudaError_t *result)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        dev = 0;
+    std::call_once(once[dev], [&] {
+        result[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+    });
+    return result[dev];
+}
+
+template <bool BF16, int VPT, int D, bool RES>
+cudaError_t launch_norm_kernel(const NormArgs &a, const RowShape &r, const RowPlan &p, cudaStream_t s)
+{
+    if constexpr (D > 1) {
+        static std::once_flag once[kMaxDevices];
+        static cudaError_t result[kMaxDevices];
+        const cudaError_t e = allow_smem(norm_kernel<BF16, VPT, D, RES>, once, result);
+        if (e != cudaSuccess)
+            return e;
+    }
+    norm_kernel<BF16, VPT, D, RES><<<p.grid, p.threads, p.smem, s>>>(a, r);
+    return cudaGetLastError();
+}
+
+template <bool BF16, bool RES>
+cudaError_t norm_rows(const NormArgs &a, const RowShape &r, int vpt, cudaStream_t s)
+{
+    const RowPlan p = row_plan(a.M, r, vpt, RES ? 2 : 1, 1 << 30);
+    if (p.depth > 1)
+        return p.depth == 3 ? launch_norm_kernel<BF16, 4, 3, RES>(a, r, p, s) : launch_norm_kernel<BF16, 4, 2, RES>(a, r, p, s);
+    return vpt == 1 ? launch_norm_kernel<BF16, 1, 1, RES>(a, r, p, s)
+                    : (vpt == 2 ? launch_norm_kernel<BF16, 2, 1, RES>(a, r, p, s)
+                                : launch_norm_kernel<BF16, 4, 1, RES>(a, r, p, s));
 }
 
 template <bool BF16>
@@ -552,15 +746,35 @@ cudaError_t norm_of(const NormArgs &a, cudaStream_t s)
         norm_any_kernel<BF16><<<(int)gg_min64(a.M, kSMs * 4), 512, 0, s>>>(a);
         return cudaGetLastError();
     }
-    const int threads = 32 * r.R * r.rows;
-    const int grid = row_blocks(a.M, r, 2048 / threads);
-    if (vpt == 1)
-        norm_kernel<BF16, 1><<<grid, threads, 0, s>>>(a, r);
-    else if (vpt == 2)
-        norm_kernel<BF16, 2><<<grid, threads, 0, s>>>(a, r);
-    else
-        norm_kernel<BF16, 4><<<grid, threads, 0, s>>>(a, r);
+    return a.residual ? norm_rows<BF16, true>(a, r, vpt, s) : norm_rows<BF16, false>(a, r, vpt, s);
+}
+
+template <bool BF16, int VPT, int D, bool IN>
+cudaError_t launch_backward_kernel(const NormBackwardArgs &a, const RowShape &r, const RowPlan &p, cudaStream_t s)
+{
+    if constexpr (D > 1) {
+        static std::once_flag once[kMaxDevices];
+        static cudaError_t result[kMaxDevices];
+        const cudaError_t e = allow_smem(norm_backward_kernel<BF16, VPT, D, IN>, once, result);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int columns = r.rows > 1 ? (int)a.N * 4 : 0;
+    norm_backward_kernel<BF16, VPT, D, IN><<<p.grid, p.threads, p.smem > columns ? p.smem : columns, s>>>(a, r);
     return cudaGetLastError();
+}
+
+template <bool BF16, bool IN>
+cudaError_t norm_backward_rows(const NormBackwardArgs &a, const RowShape &r, int vpt, int *parts, cudaStream_t s)
+{
+    const RowPlan p = row_plan(a.M, r, vpt, IN ? 3 : 2, norm_backward_parts(a.M));
+    *parts = p.grid;
+    if (p.depth > 1)
+        return p.depth == 3 ? launch_backward_kernel<BF16, 4, 3, IN>(a, r, p, s)
+                            : launch_backward_kernel<BF16, 4, 2, IN>(a, r, p, s);
+    return vpt == 1 ? launch_backward_kernel<BF16, 1, 1, IN>(a, r, p, s)
+                    : (vpt == 2 ? launch_backward_kernel<BF16, 2, 1, IN>(a, r, p, s)
+                                : launch_backward_kernel<BF16, 4, 1, IN>(a, r, p, s));
 }
 
 template <bool BF16>
@@ -568,21 +782,14 @@ cudaError_t norm_backward_of(const NormBackwardArgs &a, cudaStream_t s)
 {
     RowShape r;
     int vpt, parts = 0;
+    cudaError_t e = cudaSuccess;
     const bool wide = on16(a.dy, a.lddy) && on16(a.h, a.ldh) && (!a.dh_in || on16(a.dh_in, a.lddhin)) &&
                       (!a.dh || on16(a.dh, a.lddh));
     if (a.M == 0) {
         // no rows: the sums are zero
     } else if (wide && row_shape(a.M, a.N, 2, &r, &vpt)) {
-        const int threads = 32 * r.R * r.rows;
-        const int grid = row_blocks(a.M, r, norm_backward_parts(a.M) / kSMs > 0 ? norm_backward_parts(a.M) / kSMs : 1);
-        const int smem = r.rows > 1 ? (int)a.N * 4 : 0;
-        parts = grid;
-        if (vpt == 1)
-            norm_backward_kernel<BF16, 1><<<grid, threads, smem, s>>>(a, r);
-        else if (vpt == 2)
-            norm_backward_kernel<BF16, 2><<<grid, threads, smem, s>>>(a, r);
-        else
-            norm_backward_kernel<BF16, 4><<<grid, threads, smem, s>>>(a, r);
+        e = a.dh_in ? norm_backward_rows<BF16, true>(a, r, vpt, &parts, s)
+                    : norm_backward_rows<BF16, false>(a, r, vpt, &parts, s);
     } else {
         if (a.partial) {  // first: dh may lie over what it reads
             parts = norm_backward_parts(a.M);
@@ -590,12 +797,20 @@ cudaError_t norm_backward_of(const NormBackwardArgs &a, cudaStream_t s)
         }
         if (a.dh)
             norm_backward_any_kernel<BF16><<<(int)gg_min64(a.M, kSMs * 4), 512, 0, s>>>(a);
-    }
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.dweight) {
-        norm_join_kernel<<<(int)((a.N + 31) / 32), 256, 0, s>>>(a.partial, parts, a.N, a.dweight, a.grad_f32, BF16,
-                                                                 a.accumulate);
         e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && a.dweight) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute early;
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)((a.N + 31) / 32), 1, 1);
+        cfg.blockDim = dim3(1024, 1, 1);
+        cfg.stream = s;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, norm_join_kernel, (const float *)a.partial, parts, a.N, a.dweight, a.grad_f32,
+                               (int)BF16, a.accumulate);
     }
     return e;
 }
@@ -605,11 +820,14 @@ cudaError_t unpack_of(const UnpackArgs &a, cudaStream_t s)
 {
     const bool wide = on16(a.out, a.ldo) && on8(a.codes, a.ldc);
     const int64_t total = a.M * (wide ? (a.N + 7) / 8 : a.N);
-    const int grid = (int)gg_min64((total + 255) / 256, kSMs * 8);
-    if (wide)
-        unpack_kernel<BF16, 8><<<grid, 256, 0, s>>>(a);
+    const int grid = (int)gg_min64((total + 256 * kAhead - 1) / (256 * kAhead), kSMs * 8);
+    const bool small = total < (1ll << 31) - kSMs * 8 * 256 * kAhead;  // the last step does not overflow
+    if (wide && small)
+        unpack_kernel<BF16, 8, int><<<grid, 256, 0, s>>>(a);
+    else if (wide)
+        unpack_kernel<BF16, 8, int64_t><<<grid, 256, 0, s>>>(a);
     else
-        unpack_kernel<BF16, 1><<<grid, 256, 0, s>>>(a);
+        unpack_kernel<BF16, 1, int64_t><<<grid, 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -617,10 +835,13 @@ template <bool BF16>
 cudaError_t pack_of(const PackArgs &a, cudaStream_t s)
 {
     const int64_t blocks = a.M * ((a.N + kPackBlock - 1) / kPackBlock);
-    if (on16(a.x, a.ldx) && on8(a.codes, a.ldc))
-        pack_kernel<BF16><<<(int)gg_min64((blocks + 15) / 16, kSMs * 8), 256, 0, s>>>(a);
-    else
+    const int grid = (int)gg_min64((blocks + 16 * kAhead - 1) / (16 * kAhead), kSMs * 8);
+    if (!(on16(a.x, a.ldx) && on8(a.codes, a.ldc)))
         pack_any_kernel<BF16><<<(int)gg_min64((blocks + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
+    else if (blocks < (1ll << 31) - kSMs * 8 * 16 * kAhead)
+        pack_kernel<BF16, int><<<grid, 256, 0, s>>>(a);
+    else
+        pack_kernel<BF16, int64_t><<<grid, 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
