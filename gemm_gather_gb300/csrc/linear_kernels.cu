@@ -404,17 +404,10 @@ __device__ __forceinline__ void read_codes(const LinearArgs &a, int64_t i, int64
                     if (i + u < a.I)
                         (u < 4 ? c.x : c.y) |= (uint32_t)q[u] << (8 * (u & 3));
             }
-            const float scale = s[(int64_t)(8 * k) * a.lds];
-            float v[4], w[4];
-            unpack4(c.x, v);
-            unpack4(c.y, w);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                v[u] = held16<BF16>(v[u] * scale);
-                w[u] = held16<BF16>(w[u] * scale);
-            }
-            x[k] = make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]), pair16_of<BF16>(w[0], w[1]),
-                              pair16_of<BF16>(w[2], w[3]));
+            float v[8];
+            values8<BF16>(c, s[(int64_t)(8 * k) * a.lds], v);
+            x[k] = make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]), pair16_of<BF16>(v[4], v[5]),
+                              pair16_of<BF16>(v[6], v[7]));
         }
     }
 }

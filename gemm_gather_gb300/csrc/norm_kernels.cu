@@ -69,55 +69,73 @@ __device__ __forceinline__ float row_sum(float v, const RowShape &s, float (&buf
     return t;
 }
 
-// Eight neighbouring weights.
+// Eight neighbouring 16-bit elements, or weights, as pairs of floats.
+struct Eight {
+    F2 v[4];
+};
+
 template <bool BF16>
-__device__ __forceinline__ void load_weights(const void *w, int f32, int vec, int64_t n, int64_t left, float (&v)[8])
+__device__ __forceinline__ Eight eight_of(const uint4 &q)
 {
+    const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+    Eight r;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float2 f = pair16<BF16>(h[u]);
+        r.v[u] = pair_of(f.x, f.y);
+    }
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 halves8(const Eight &e)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float2 f = halves_of(e.v[u]);
+        w[u] = pair16_of<BF16>(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// a + b, rounded once to the type.
+template <bool BF16>
+__device__ __forceinline__ uint32_t add16(uint32_t a, uint32_t b)
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ Eight load_weights(const void *w, int f32, int vec, int n, int left)
+{
+    Eight r;
     if (f32) {
         const float *p = reinterpret_cast<const float *>(w) + n;
         if (left >= 8 && vec) {
             const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            return;
+            r.v[0] = pair_of(a.x, a.y), r.v[1] = pair_of(a.z, a.w);
+            r.v[2] = pair_of(b.x, b.y), r.v[3] = pair_of(b.z, b.w);
+            return r;
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            v[u] = u < left ? p[u] : 0.0f;
-        return;
+        for (int u = 0; u < 4; ++u)
+            r.v[u] = pair_of(2 * u < left ? p[2 * u] : 0.0f, 2 * u + 1 < left ? p[2 * u + 1] : 0.0f);
+        return r;
     }
     const uint16_t *p = reinterpret_cast<const uint16_t *>(w) + n;
-    if (left >= 8 && vec) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+    if (left >= 8 && vec)
+        return eight_of<BF16>(*reinterpret_cast<const uint4 *>(p));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2 f = pair16<BF16>(h[u]);
-            v[2 * u] = f.x, v[2 * u + 1] = f.y;
-        }
-        return;
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-        v[u] = u < left ? load16(p, u, BF16) : 0.0f;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void floats8(const uint4 &q, float (&v)[8])
-{
-    const uint32_t h[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float2 f = pair16<BF16>(h[u]);
-        v[2 * u] = f.x, v[2 * u + 1] = f.y;
-    }
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint4 halves8(const float (&v)[8])
-{
-    return make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]), pair16_of<BF16>(v[4], v[5]),
-                      pair16_of<BF16>(v[6], v[7]));
+    for (int u = 0; u < 4; ++u)
+        r.v[u] = pair_of(2 * u < left ? load16(p, 2 * u, BF16) : 0.0f, 2 * u + 1 < left ? load16(p, 2 * u + 1, BF16) : 0.0f);
+    return r;
 }
 
 // ---- rows in flight ---------------------------------------------------------------------
@@ -145,122 +163,121 @@ struct Slots {
     {
         return mine + ((d * INPUTS + i) * VPT + k) * (int)blockDim.x;
     }
-    // Vector k of a row, `left` elements to the row's end (0 or less: none, and zeros in the slot).
-    __device__ __forceinline__ void copy(int d, int i, int k, const uint16_t *row, int64_t n, int64_t left) const
+    __device__ __forceinline__ void clear(int depth) const
     {
-        const int bytes = left >= 8 ? 16 : (left > 0 ? (int)left * 2 : 0);
-        copy16(ptx::smem_addr(at(d, i, k)), left > 0 ? row + n : row, bytes);
+        for (int v = 0; v < depth * INPUTS * VPT; ++v)
+            mine[v * (int)blockDim.x] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // Vector k of a row, `left` elements to the row's end.  WHOLE: rows of whole vectors; one past the end is
+    // not copied (its slot holds zeros).  Else a vector's missing elements come as zeros.
+    template <bool WHOLE>
+    __device__ __forceinline__ void copy(int d, int i, int k, const uint16_t *row, int n, int left) const
+    {
+        if (WHOLE) {
+            if (left > 0)
+                copy16(ptx::smem_addr(at(d, i, k)), row + n, 16);
+        } else {
+            const int bytes = left >= 8 ? 16 : (left > 0 ? left * 2 : 0);
+            copy16(ptx::smem_addr(at(d, i, k)), left > 0 ? row + n : row, bytes);
+        }
     }
 };
 
+template <bool WHOLE>
+__device__ __forceinline__ uint4 load_vector(const uint16_t *p, int left)
+{
+    if (!WHOLE)
+        return load8(p, left);
+    return left > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void store_vector(uint16_t *p, int left, const uint4 &v)
+{
+    if (!WHOLE)
+        store8(p, left, v);
+    else if (left > 0)
+        *reinterpret_cast<uint4 *>(p) = v;
+}
+
 // ---- forward ------------------------------------------------------------------------------
-template <bool BF16, int VPT, int D, bool RES>
-__global__ void __launch_bounds__(VPT > 2 && D > 1 ? 512 : 1024)
-    norm_kernel(const __grid_constant__ NormArgs a, const RowShape s)
+// A block a row group: with a new block's loads starting wherever one has ended, reads and writes mix
+// evenly, which HBM rewards: 16384 x 8192 (residual, codes) takes 180 us, at the copy rate; blocks that walk
+// rows with the next one's loads in flight 215, and 203 without.
+template <bool BF16, int VPT, bool RES, bool WHOLE>
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a, const RowShape s)
 {
     __shared__ float sums[2][kMaxWarps];
-    extern __shared__ __align__(16) uint8_t ring[];
-    const Slots<VPT, RES ? 2 : 1> slots(ring);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = warp % s.R;
-    const int64_t step = (int64_t)gridDim.x * s.rows;
-    const uint16_t *x = reinterpret_cast<const uint16_t *>(a.x), *r = reinterpret_cast<const uint16_t *>(a.residual);
-    const auto column = [&](int k) { return (int64_t)((k * s.R + sub) * 32 + lane) * kVec; };
-    int64_t row = (int64_t)blockIdx.x * s.rows + warp / s.R;
-    const auto ahead = [&](int64_t at, int d) {
-        if (at < a.M) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int64_t n = column(k);
-                slots.copy(d, 0, k, x + at * a.ldx, n, a.N - n);
-                if (RES)
-                    slots.copy(d, RES ? 1 : 0, k, r + at * a.ldr, n, a.N - n);
-            }
-        }
-        copies_commit();
-    };
-    if constexpr (D > 1) {
-#pragma unroll
-        for (int d = 0; d < D - 1; ++d)
-            ahead(row + d * step, d);
-    }
-    int turn = 0, slot = 0;
-    // the block's rows end together: its first one decides
-    for (int64_t row0 = (int64_t)blockIdx.x * s.rows; row0 < a.M; row0 += step, row += step, turn ^= 1) {
-        const bool live = row < a.M;
-        uint4 h[VPT];
-        float sq = 0.0f;
-        if constexpr (D > 1) {
-            ahead(row + (D - 1) * step, slot == 0 ? D - 1 : slot - 1);
-            copies_wait<D - 1>();
-        }
-        if (live) {
-            uint4 q[VPT];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int64_t n = column(k);
-                h[k] = D > 1 ? *slots.at(slot, 0, k) : load8(x + row * a.ldx + n, a.N - n);
-                if (RES)
-                    q[k] = D > 1 ? *slots.at(slot, RES ? 1 : 0, k) : load8(r + row * a.ldr + n, a.N - n);
-            }
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float v[8];
-                floats8<BF16>(h[k], v);
-                if (RES) {
-                    float t[8];
-                    floats8<BF16>(q[k], t);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        v[u] += t[u];
-                    h[k] = halves8<BF16>(v);
-                    floats8<BF16>(h[k], v);
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    sq = fmaf(v[u], v[u], sq);
-            }
-            if (a.h) {
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int64_t n = column(k);
-                    store8(reinterpret_cast<uint16_t *>(a.h) + row * a.ldh + n, a.N - n, h[k]);
-                }
-            }
-        }
-        if constexpr (D > 1)
-            slot = slot + 1 == D ? 0 : slot + 1;
-        float w[8];
-        if (VPT == 1 && live)  // few rows: the weights' latency beside the sum's
-            load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, column(0), a.N - column(0), w);
-        const float total = row_sum(sq, s, sums, turn);
-        if (!live)
-            continue;
-        const float rstd = 1.0f / sqrtf(total / (float)a.N + a.eps);
-        if (a.rstd && sub == 0 && lane == 0)
-            a.rstd[row] = rstd;
+    const int sub = warp % s.R, N = (int)a.N;
+    const int64_t row = (int64_t)blockIdx.x * s.rows + warp / s.R;
+    const bool live = row < a.M;
+    const auto column = [&](int k) { return ((k * s.R + sub) * 32 + lane) * kVec; };
+    uint4 h[VPT];
+    F2 sq = pair_of(0.0f);
+    Eight w;
+    if (live) {
+        const uint16_t *x = reinterpret_cast<const uint16_t *>(a.x) + row * a.ldx;
+        const uint16_t *r = RES ? reinterpret_cast<const uint16_t *>(a.residual) + row * a.ldr : nullptr;
+        uint4 q[VPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int64_t n = column(k), left = a.N - n;
-            float v[8];
-            floats8<BF16>(h[k], v);
-            if (VPT > 1)
-                load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left, w);
+            const int n = column(k);
+            h[k] = load_vector<WHOLE>(x + n, N - n);
+            if (RES)
+                q[k] = load_vector<WHOLE>(r + n, N - n);
+        }
+        if (VPT == 1)  // few rows: the weights' latency beside the row's
+            w = load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, column(0), N - column(0));
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                v[u] = v[u] * rstd * w[u];
-            const uint4 y = halves8<BF16>(v);
-            if (a.y)
-                store8(reinterpret_cast<uint16_t *>(a.y) + row * a.ldy + n, left, y);
-            if (a.codes) {
-                floats8<BF16>(y, v);
-                int e;
-                const uint2 c = pack_group(v, &e);
-                if (left > 0) {
-                    store_codes8(a.codes + row * a.ldc + n, left, c);
-                    if ((lane & 15) == 0)
-                        a.scales[row * a.lds + n / kPackBlock] = power_of_two(e);
-                }
+        for (int k = 0; k < VPT; ++k) {
+            if (RES)
+                h[k] = make_uint4(add16<BF16>(h[k].x, q[k].x), add16<BF16>(h[k].y, q[k].y),
+                                  add16<BF16>(h[k].z, q[k].z), add16<BF16>(h[k].w, q[k].w));
+            const Eight v = eight_of<BF16>(h[k]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                sq = fma2(v.v[u], v.v[u], sq);
+        }
+        if (a.h) {
+            uint16_t *out = reinterpret_cast<uint16_t *>(a.h) + row * a.ldh;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                store_vector<WHOLE>(out + column(k), N - column(k), h[k]);
+        }
+    }
+    const float2 both = halves_of(sq);
+    const float total = row_sum(both.x + both.y, s, sums, 0);
+    if (!live)
+        return;
+    const float rstd = 1.0f / sqrtf(total / (float)N + a.eps);
+    if (a.rstd && sub == 0 && lane == 0)
+        a.rstd[row] = rstd;
+    uint16_t *out = reinterpret_cast<uint16_t *>(a.y) + row * a.ldy;
+    uint8_t *codes = a.codes + row * a.ldc;
+    float *scales = a.scales + row * a.lds;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int n = column(k), left = N - n;
+        Eight v = eight_of<BF16>(h[k]);
+        if (VPT > 1)
+            w = load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            v.v[u] = mul2(mul2(v.v[u], pair_of(rstd)), w.v[u]);
+        const uint4 y = halves8<BF16>(v);
+        if (a.y)
+            store_vector<WHOLE>(out + n, left, y);
+        if (a.codes) {
+            int e;
+            const uint2 c = pack_group<BF16>(y, &e);
+            if (left > 0) {
+                if (WHOLE)
+                    *reinterpret_cast<uint2 *>(codes + n) = c;
+                else
+                    store_codes8(codes + n, left, c);
+                if ((lane & 15) == 0)
+                    scales[n / kPackBlock] = power_of_two(e);
             }
         }
     }
@@ -331,9 +348,9 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const __grid_constant__ N
 }
 
 // ---- backward -----------------------------------------------------------------------------
-template <bool BF16, int VPT, int D, bool IN>
-__global__ void __launch_bounds__(VPT > 2 ? 512 : 1024) norm_backward_kernel(const __grid_constant__ NormBackwardArgs a,
-                                                                             const RowShape s)
+template <bool BF16, int VPT, int D, bool IN, bool WHOLE>
+__global__ void __launch_bounds__(D > 1 ? 256 : (VPT > 2 ? 512 : 1024), D > 1 ? 2 : 1)
+    norm_backward_kernel(const __grid_constant__ NormBackwardArgs a, const RowShape s)
 {
     __shared__ float sums[2][kMaxWarps];
     // the rows in flight; at the end, where a block has several rows at a time, their sums
@@ -341,32 +358,39 @@ __global__ void __launch_bounds__(VPT > 2 ? 512 : 1024) norm_backward_kernel(con
     constexpr int kInputs = IN ? 3 : 2;
     const Slots<VPT, kInputs> slots(ring);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = warp % s.R;
+    const int sub = warp % s.R, N = (int)a.N;
     const int64_t step = (int64_t)gridDim.x * s.rows;
     const uint16_t *dy = reinterpret_cast<const uint16_t *>(a.dy), *h = reinterpret_cast<const uint16_t *>(a.h),
                    *in = reinterpret_cast<const uint16_t *>(a.dh_in);
-    const auto column = [&](int k) { return (int64_t)((k * s.R + sub) * 32 + lane) * kVec; };
-    float dw[VPT][8];
+    const auto column = [&](int k) { return ((k * s.R + sub) * 32 + lane) * kVec; };
+    Eight dw[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            dw[k][u] = 0.0f;
+        for (int u = 0; u < 4; ++u)
+            dw[k].v[u] = pair_of(0.0f);
     int64_t row = (int64_t)blockIdx.x * s.rows + warp / s.R;
     const auto ahead = [&](int64_t at, int d) {
         if (at < a.M) {
+            const uint16_t *yr = dy + at * a.lddy, *hr = h + at * a.ldh, *ir = IN ? in + at * a.lddhin : nullptr;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = column(k);
-                slots.copy(d, 0, k, dy + at * a.lddy, n, a.N - n);
-                slots.copy(d, 1, k, h + at * a.ldh, n, a.N - n);
+                const int n = column(k);
+                slots.template copy<WHOLE>(d, 0, k, yr, n, N - n);
+                slots.template copy<WHOLE>(d, 1, k, hr, n, N - n);
                 if (IN)
-                    slots.copy(d, kInputs - 1, k, in + at * a.lddhin, n, a.N - n);
+                    slots.template copy<WHOLE>(d, kInputs - 1, k, ir, n, N - n);
             }
         }
         copies_commit();
     };
+    Eight w[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+        w[k] = load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, column(k), N - column(k));
     if constexpr (D > 1) {
+        if (WHOLE)
+            slots.clear(D);
 #pragma unroll
         for (int d = 0; d < D - 1; ++d)
             ahead(row + d * step, d);
@@ -384,50 +408,51 @@ __global__ void __launch_bounds__(VPT > 2 ? 512 : 1024) norm_backward_kernel(con
         }
         if (live) {
             if constexpr (D == 1) {
+                const uint16_t *yr = dy + row * a.lddy, *hr = h + row * a.ldh, *ir = IN ? in + row * a.lddhin : nullptr;
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
-                    const int64_t n = column(k);
-                    qy[k] = load8(dy + row * a.lddy + n, a.N - n);
-                    qh[k] = load8(h + row * a.ldh + n, a.N - n);
+                    const int n = column(k);
+                    qy[k] = load8(yr + n, N - n);
+                    qh[k] = load8(hr + n, N - n);
                     if (IN)
-                        qi[k] = load8(in + row * a.lddhin + n, a.N - n);
+                        qi[k] = load8(ir + n, N - n);
                 }
             }
+            F2 part = pair_of(0.0f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = column(k);
-                float y[8], u8[8], w[8];
-                floats8<BF16>(D > 1 ? *slots.at(slot, 0, k) : qy[k], y);
-                floats8<BF16>(D > 1 ? *slots.at(slot, 1, k) : qh[k], u8);
-                load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, a.N - n, w);
+                const Eight y = eight_of<BF16>(D > 1 ? *slots.at(slot, 0, k) : qy[k]);
+                const Eight v = eight_of<BF16>(D > 1 ? *slots.at(slot, 1, k) : qh[k]);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float t = u8[u] * rstd;
-                    dot = fmaf(y[u] * w[u], t, dot);
-                    dw[k][u] = fmaf(y[u], t, dw[k][u]);
+                for (int u = 0; u < 4; ++u) {
+                    const F2 t = mul2(v.v[u], pair_of(rstd));
+                    part = fma2(mul2(y.v[u], w[k].v[u]), t, part);
+                    dw[k].v[u] = fma2(y.v[u], t, dw[k].v[u]);
                 }
             }
+            const float2 both = halves_of(part);
+            dot = both.x + both.y;
         }
-        const float c = row_sum(dot, s, sums, turn) / (float)a.N;
+        // dh = rstd (g - u c) + dh_in: g rstd, and u by -rstd c
+        const float c = row_sum(dot, s, sums, turn) / (float)N;
         if (live && a.dh) {
+            uint16_t *out = reinterpret_cast<uint16_t *>(a.dh) + row * a.lddh;
+            const F2 r2 = pair_of(rstd), less = pair_of(-rstd * c);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = column(k), left = a.N - n;
-                float y[8], v[8], w[8];
-                floats8<BF16>(D > 1 ? *slots.at(slot, 0, k) : qy[k], y);
-                floats8<BF16>(D > 1 ? *slots.at(slot, 1, k) : qh[k], v);
-                load_weights<BF16>(a.weight, a.weight_f32, a.weight_vec, n, left, w);
+                const int n = column(k);
+                const Eight y = eight_of<BF16>(D > 1 ? *slots.at(slot, 0, k) : qy[k]);
+                Eight v = eight_of<BF16>(D > 1 ? *slots.at(slot, 1, k) : qh[k]);
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    v[u] = rstd * (y[u] * w[u] - v[u] * rstd * c);
+                for (int u = 0; u < 4; ++u)
+                    v.v[u] = fma2(mul2(y.v[u], w[k].v[u]), r2, mul2(mul2(v.v[u], r2), less));
                 if (IN) {
-                    float t[8];
-                    floats8<BF16>(D > 1 ? *slots.at(slot, kInputs - 1, k) : qi[k], t);
+                    const Eight t = eight_of<BF16>(D > 1 ? *slots.at(slot, kInputs - 1, k) : qi[k]);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        v[u] += t[u];
+                    for (int u = 0; u < 4; ++u)
+                        v.v[u] = add2(v.v[u], t.v[u]);
                 }
-                store8(reinterpret_cast<uint16_t *>(a.dh) + row * a.lddh + n, left, halves8<BF16>(v));
+                store_vector<WHOLE>(out + n, N - n, halves8<BF16>(v));
             }
         }
         if constexpr (D > 1)
@@ -446,11 +471,14 @@ __global__ void __launch_bounds__(VPT > 2 ? 512 : 1024) norm_backward_kernel(con
         if (warp / s.R == g) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t n = column(k);
+                const int n = column(k);
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (n + u < a.N) {
-                        const float t = g > 0 ? columns[n + u] + dw[k][u] : dw[k][u];
+                    if (n + u < N) {
+                        const float2 mine = halves_of(dw[k].v[u / 2]);
+                        float t = u & 1 ? mine.y : mine.x;
+                        if (g > 0)
+                            t += columns[n + u];
                         if (g + 1 == s.rows)
                             out[n + u] = t;
                         else
@@ -536,40 +564,55 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float *partial, i
 }
 
 // ---- 8-bit activations by themselves --------------------------------------------------------
-// 16 lanes a block of 128 elements; kAhead blocks' loads in flight.  I: 32-bit indices where all
-// blocks have one (a 64-bit division costs as much as the rest of a block).
-constexpr int kAhead = 4;
-template <bool BF16, typename I>
+// Eight lanes a block of 128 elements, two vectors each; kAhead blocks' loads in flight.  A lane's place
+// (row, block of the row) is stepped, not divided for: one division of a place costs as much as a
+// quarter of the block's arithmetic.
+constexpr int kAhead = 2;
+template <bool BF16>
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a)
 {
-    const I units = (I)((a.N + kPackBlock - 1) / kPackBlock);  // blocks of a row
-    const I total = (I)a.M * units;
-    const int lane = threadIdx.x & 15;
-    // a block of threads takes 16 neighbouring units kAhead times
-    for (I t0 = (I)blockIdx.x * (16 * kAhead) + (threadIdx.x >> 5) * 2; t0 < total; t0 += (I)gridDim.x * (16 * kAhead)) {
-        uint4 q[kAhead];
-        int64_t row[kAhead], n[kAhead];
-        int left[kAhead];
+    const int units = (int)((a.N + kPackBlock - 1) / kPackBlock);  // blocks of a row
+    const int lane = threadIdx.x & 7;
+    const int64_t total = a.M * units, step = (int64_t)gridDim.x * 32;
+    const int64_t first = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    const int64_t step_rows = step / units;
+    const int step_units = (int)(step - step_rows * units);
+    int64_t row = first / units;
+    int unit = (int)(first - row * units);
+    // a warp's four groups end together
+    for (int64_t t0 = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 5) * 4; t0 < total; t0 += step * kAhead) {
+        uint4 q[kAhead][2];
+        int64_t at[kAhead];
+        int b[kAhead], left[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const I t = t0 + 16 * k + ((threadIdx.x >> 4) & 1);
-            const I r = t / units;
-            row[k] = r;
-            n[k] = (int64_t)(t - r * units) * kPackBlock + lane * kVec;
-            const int64_t l = t < total ? a.N - n[k] : 0;
-            left[k] = l >= 8 ? 8 : (int)l;
-            q[k] = load8(reinterpret_cast<const uint16_t *>(a.x) + row[k] * a.ldx + n[k], left[k]);
+            at[k] = row;
+            b[k] = unit;
+            const int64_t n = (int64_t)unit * kPackBlock + lane * kVec;
+            const int64_t l = row < a.M ? a.N - n : 0;
+            left[k] = l > 127 ? 127 : (int)l;
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(a.x) + row * a.ldx + n;
+            q[k][0] = load8(p, left[k]);
+            q[k][1] = load8(p + 64, left[k] - 64);
+            row += step_rows;
+            unit += step_units;
+            if (unit >= units) {
+                unit -= units;
+                ++row;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            float v[8];
-            floats8<BF16>(q[k], v);
             int e;
-            const uint2 c = pack_group(v, &e);
+            uint2 c[2];
+            pack_block<BF16>(q[k], &e, c);
             if (left[k] > 0) {
-                store_codes8(a.codes + row[k] * a.ldc + n[k], left[k], c);
+                uint8_t *p = a.codes + at[k] * a.ldc + b[k] * kPackBlock + lane * kVec;
+                store_codes8(p, left[k], c[0]);
+                if (left[k] > 64)
+                    store_codes8(p + 64, left[k] - 64, c[1]);
                 if (lane == 0)
-                    a.scales[row[k] * a.lds + n[k] / kPackBlock] = power_of_two(e);
+                    a.scales[at[k] * a.lds + b[k]] = power_of_two(e);
             }
         }
     }
@@ -598,20 +641,21 @@ __global__ void __launch_bounds__(256) pack_any_kernel(const __grid_constant__ P
     }
 }
 
-// V elements per thread and step (8 where rows of out are 16-byte and rows of codes 8-byte aligned), kAhead
-// steps' loads in flight.
+// V elements per thread and step (8 where rows of out are 16-byte and rows of codes 8-byte aligned), kSteps
+// steps' loads in flight.  I: 32-bit indices where all vectors have one.
+constexpr int kSteps = 4;
 template <bool BF16, int V, typename I>
 __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ UnpackArgs a)
 {
     const I units = (I)((a.N + V - 1) / V);
     const I total = (I)a.M * units;
-    for (I t0 = (I)blockIdx.x * (256 * kAhead) + threadIdx.x; t0 < total; t0 += (I)gridDim.x * (256 * kAhead)) {
-        uint2 c[kAhead];
-        float scale[kAhead];
-        uint16_t *out[kAhead];
-        int left[kAhead];
+    for (I t0 = (I)blockIdx.x * (256 * kSteps) + threadIdx.x; t0 < total; t0 += (I)gridDim.x * (256 * kSteps)) {
+        uint2 c[kSteps];
+        float scale[kSteps];
+        uint16_t *out[kSteps];
+        int left[kSteps];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < kSteps; ++k) {
             const I t = t0 + 256 * k;
             const I row = t / units;
             const int64_t n = (int64_t)(t - row * units) * V;
@@ -625,22 +669,16 @@ __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unp
             }
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < kSteps; ++k) {
             if (left[k] == 0)
                 break;
-            float v[8], x[4];
-            unpack4(c[k].x, x);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                v[u] = held16<BF16>(x[u] * scale[k]);
-            unpack4(c[k].y, x);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                v[4 + u] = held16<BF16>(x[u] * scale[k]);
+            float v[8];
+            values8<BF16>(c[k], scale[k], v);
             if (a.act != GG_ACT_NONE)
                 with_act(a.act, [&](auto f) { apply_act<decltype(f)::value>(v); });
             if (V == 8)
-                store8(out[k], left[k], halves8<BF16>(v));
+                store8(out[k], left[k], make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]),
+                                                   pair16_of<BF16>(v[4], v[5]), pair16_of<BF16>(v[6], v[7])));
             else
                 store16(out[k], 0, v[0], BF16);
         }
@@ -671,24 +709,26 @@ bool row_shape(int64_t M, int64_t N, int most, RowShape *s, int *vpt)
     return true;
 }
 
-// Blocks of a launch and how deep their rows' copies go: two blocks of up to 110 KB an SM, where that
-// makes every block walk a few rows and its slots fit; else a block a row group.
+// Blocks of a launch and how deep their rows' copies go: two blocks of up to 256 threads and 110 KB an SM,
+// where that makes every block walk a few rows; else a block a row group.
 struct RowPlan {
     int grid, threads, depth, smem;
 };
 
-RowPlan row_plan(int64_t M, const RowShape &s, int vpt, int inputs, int most_blocks)
+template <int INPUTS>
+constexpr int kDepth = INPUTS == 3 ? 2 : 3;  // 256 threads, 4 vectors: 96 KB
+
+template <int INPUTS>
+RowPlan row_plan(int64_t M, const RowShape &s, int vpt, int most_blocks)
 {
     RowPlan p{};
     p.threads = 32 * s.R * s.rows;
     const int64_t groups = (M + s.rows - 1) / s.rows;
-    const int slot = p.threads * vpt * inputs * 16;
-    const int per_sm = p.threads <= 512 ? 512 / p.threads : 0;
-    const int depth = per_sm > 0 ? (220 * 1024 / per_sm - 1024) / slot : 0;
-    if (vpt == 4 && depth >= 2 && groups >= 2 * kSMs * per_sm) {
-        p.depth = depth >= 3 ? 3 : 2;
+    const int slot = p.threads * vpt * INPUTS * 16;
+    if (vpt == 4 && p.threads <= 256 && groups >= 4 * kSMs) {
+        p.depth = kDepth<INPUTS>;
         p.smem = p.depth * slot;
-        p.grid = (int)gg_min64(most_blocks, (int64_t)kSMs * per_sm);
+        p.grid = 2 * kSMs;
     } else {
         p.depth = 1;
         p.grid = (int)gg_min64(gg_min64(groups, most_blocks), (int64_t)kSMs * (2048 / p.threads));
@@ -710,29 +750,18 @@ cudaError_t allow_smem(K kernel, std::once_flag *once, cudaError_t *result)
     return result[dev];
 }
 
-template <bool BF16, int VPT, int D, bool RES>
-cudaError_t launch_norm_kernel(const NormArgs &a, const RowShape &r, const RowPlan &p, cudaStream_t s)
-{
-    if constexpr (D > 1) {
-        static std::once_flag once[kMaxDevices];
-        static cudaError_t result[kMaxDevices];
-        const cudaError_t e = allow_smem(norm_kernel<BF16, VPT, D, RES>, once, result);
-        if (e != cudaSuccess)
-            return e;
-    }
-    norm_kernel<BF16, VPT, D, RES><<<p.grid, p.threads, p.smem, s>>>(a, r);
-    return cudaGetLastError();
-}
-
-template <bool BF16, bool RES>
+template <bool BF16, bool RES, bool WHOLE>
 cudaError_t norm_rows(const NormArgs &a, const RowShape &r, int vpt, cudaStream_t s)
 {
-    const RowPlan p = row_plan(a.M, r, vpt, RES ? 2 : 1, 1 << 30);
-    if (p.depth > 1)
-        return p.depth == 3 ? launch_norm_kernel<BF16, 4, 3, RES>(a, r, p, s) : launch_norm_kernel<BF16, 4, 2, RES>(a, r, p, s);
-    return vpt == 1 ? launch_norm_kernel<BF16, 1, 1, RES>(a, r, p, s)
-                    : (vpt == 2 ? launch_norm_kernel<BF16, 2, 1, RES>(a, r, p, s)
-                                : launch_norm_kernel<BF16, 4, 1, RES>(a, r, p, s));
+    const unsigned grid = (unsigned)((a.M + r.rows - 1) / r.rows);
+    const int threads = 32 * r.R * r.rows;
+    if (vpt == 1)
+        norm_kernel<BF16, 1, RES, WHOLE><<<grid, threads, 0, s>>>(a, r);
+    else if (vpt == 2)
+        norm_kernel<BF16, 2, RES, WHOLE><<<grid, threads, 0, s>>>(a, r);
+    else
+        norm_kernel<BF16, 4, RES, WHOLE><<<grid, threads, 0, s>>>(a, r);
+    return cudaGetLastError();
 }
 
 template <bool BF16>
@@ -746,32 +775,34 @@ cudaError_t norm_of(const NormArgs &a, cudaStream_t s)
         norm_any_kernel<BF16><<<(int)gg_min64(a.M, kSMs * 4), 512, 0, s>>>(a);
         return cudaGetLastError();
     }
-    return a.residual ? norm_rows<BF16, true>(a, r, vpt, s) : norm_rows<BF16, false>(a, r, vpt, s);
+    if (a.N % kVec == 0)
+        return a.residual ? norm_rows<BF16, true, true>(a, r, vpt, s) : norm_rows<BF16, false, true>(a, r, vpt, s);
+    return a.residual ? norm_rows<BF16, true, false>(a, r, vpt, s) : norm_rows<BF16, false, false>(a, r, vpt, s);
 }
 
-template <bool BF16, int VPT, int D, bool IN>
+template <bool BF16, int VPT, int D, bool IN, bool WHOLE = false>
 cudaError_t launch_backward_kernel(const NormBackwardArgs &a, const RowShape &r, const RowPlan &p, cudaStream_t s)
 {
     if constexpr (D > 1) {
         static std::once_flag once[kMaxDevices];
         static cudaError_t result[kMaxDevices];
-        const cudaError_t e = allow_smem(norm_backward_kernel<BF16, VPT, D, IN>, once, result);
+        const cudaError_t e = allow_smem(norm_backward_kernel<BF16, VPT, D, IN, WHOLE>, once, result);
         if (e != cudaSuccess)
             return e;
     }
     const int columns = r.rows > 1 ? (int)a.N * 4 : 0;
-    norm_backward_kernel<BF16, VPT, D, IN><<<p.grid, p.threads, p.smem > columns ? p.smem : columns, s>>>(a, r);
+    norm_backward_kernel<BF16, VPT, D, IN, WHOLE><<<p.grid, p.threads, p.smem > columns ? p.smem : columns, s>>>(a, r);
     return cudaGetLastError();
 }
 
 template <bool BF16, bool IN>
 cudaError_t norm_backward_rows(const NormBackwardArgs &a, const RowShape &r, int vpt, int *parts, cudaStream_t s)
 {
-    const RowPlan p = row_plan(a.M, r, vpt, IN ? 3 : 2, norm_backward_parts(a.M));
+    const RowPlan p = row_plan<IN ? 3 : 2>(a.M, r, vpt, norm_backward_parts(a.M));
     *parts = p.grid;
     if (p.depth > 1)
-        return p.depth == 3 ? launch_backward_kernel<BF16, 4, 3, IN>(a, r, p, s)
-                            : launch_backward_kernel<BF16, 4, 2, IN>(a, r, p, s);
+        return a.N % kVec == 0 ? launch_backward_kernel<BF16, 4, kDepth<IN ? 3 : 2>, IN, true>(a, r, p, s)
+                               : launch_backward_kernel<BF16, 4, kDepth<IN ? 3 : 2>, IN>(a, r, p, s);
     return vpt == 1 ? launch_backward_kernel<BF16, 1, 1, IN>(a, r, p, s)
                     : (vpt == 2 ? launch_backward_kernel<BF16, 2, 1, IN>(a, r, p, s)
                                 : launch_backward_kernel<BF16, 4, 1, IN>(a, r, p, s));
@@ -820,8 +851,8 @@ cudaError_t unpack_of(const UnpackArgs &a, cudaStream_t s)
 {
     const bool wide = on16(a.out, a.ldo) && on8(a.codes, a.ldc);
     const int64_t total = a.M * (wide ? (a.N + 7) / 8 : a.N);
-    const int grid = (int)gg_min64((total + 256 * kAhead - 1) / (256 * kAhead), kSMs * 8);
-    const bool small = total < (1ll << 31) - kSMs * 8 * 256 * kAhead;  // the last step does not overflow
+    const int grid = (int)gg_min64((total + 256 * kSteps - 1) / (256 * kSteps), 1 << 17);
+    const bool small = total < 1ll << 30;  // the last step does not overflow
     if (wide && small)
         unpack_kernel<BF16, 8, int><<<grid, 256, 0, s>>>(a);
     else if (wide)
@@ -835,20 +866,17 @@ template <bool BF16>
 cudaError_t pack_of(const PackArgs &a, cudaStream_t s)
 {
     const int64_t blocks = a.M * ((a.N + kPackBlock - 1) / kPackBlock);
-    const int grid = (int)gg_min64((blocks + 16 * kAhead - 1) / (16 * kAhead), kSMs * 8);
-    if (!(on16(a.x, a.ldx) && on8(a.codes, a.ldc)))
-        pack_any_kernel<BF16><<<(int)gg_min64((blocks + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
-    else if (blocks < (1ll << 31) - kSMs * 8 * 16 * kAhead)
-        pack_kernel<BF16, int><<<grid, 256, 0, s>>>(a);
+    if (on16(a.x, a.ldx) && on8(a.codes, a.ldc))
+        pack_kernel<BF16><<<(int)gg_min64((blocks + 31) / 32, kSMs * 8), 256, 0, s>>>(a);
     else
-        pack_kernel<BF16, int64_t><<<grid, 256, 0, s>>>(a);
+        pack_any_kernel<BF16><<<(int)gg_min64((blocks + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// Blocks' rows of dw's sums: two blocks an SM.
-int norm_backward_parts(int64_t M) { return (int)gg_min64(M, 2 * kSMs); }
+// Rows of dw's sums that blocks leave, at most: four blocks an SM.
+int norm_backward_parts(int64_t M) { return (int)gg_min64(M, 4 * kSMs); }
 
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t s) { return a.is_bf16 ? norm_of<true>(a, s) : norm_of<false>(a, s); }
 

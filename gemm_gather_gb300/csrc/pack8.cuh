@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "../../include/gemm_gather.h"
+#include "f32x2.cuh"
 
 namespace gg {
 
@@ -54,17 +55,21 @@ __device__ __forceinline__ int pack_exponent(float top)
 
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
 
-// Codes of four values, already divided by their scale (|x| <= 448 or not finite).
-__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
+// Codes of two pairs of values, already divided by their scale (|x| <= 448, or NaN).
+__device__ __forceinline__ uint32_t pack4(float2 a, float2 b)
 {
-    // an infinity would be held at 448
-    a = is_finite(a) ? a : __int_as_float(0x7fffffff);
-    b = is_finite(b) ? b : __int_as_float(0x7fffffff);
-    c = is_finite(c) ? c : __int_as_float(0x7fffffff);
-    d = is_finite(d) ? d : __int_as_float(0x7fffffff);
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
-           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+    uint32_t codes;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(codes)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return codes;
 }
+
+// NaN for what is not finite (an infinity would be held at 448).
+__device__ __forceinline__ float nan_unless_finite(float x) { return is_finite(x) ? x : __int_as_float(0x7fffffff); }
 
 // The e4m3 values of four codes.
 __device__ __forceinline__ void unpack4(uint32_t codes, float (&x)[4])
@@ -79,12 +84,32 @@ __device__ __forceinline__ void unpack4(uint32_t codes, float (&x)[4])
 }
 
 // A value from its code and scale: rounded up on the way into 8 bits it may lie just beyond the
-// 16-bit type's range, and is its largest number then.
+// 16-bit type's range, and is its largest number then.  Only blocks of the largest scale have such.
 template <bool BF16>
 __device__ __forceinline__ float held16(float x)
 {
     constexpr float kTop = BF16 ? 3.3895313892515355e38f : 65504.0f;
     return x > kTop ? kTop : (x < -kTop ? -kTop : x);
+}
+
+// The values of eight codes under one scale.
+template <bool BF16>
+__device__ __forceinline__ void values8(const uint2 &codes, float scale, float (&v)[8])
+{
+    float x[4], y[4];
+    unpack4(codes.x, x);
+    unpack4(codes.y, y);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        v[u] = x[u] * scale;
+        v[4 + u] = y[u] * scale;
+    }
+    constexpr float kBig = BF16 ? 1.329227995784916e36f : 256.0f;  // 2^120, 2^8
+    if (scale >= kBig) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[u] = held16<BF16>(v[u]);
+    }
 }
 
 // Eight neighbouring elements of a row, of which `left` exist; the others are zero and not read.
@@ -138,22 +163,77 @@ __device__ __forceinline__ void store_codes8(uint8_t *p, int64_t left, const uin
             p[u] = (uint8_t)(w[u >> 2] >> (8 * (u & 3)));
 }
 
-// Eight values of a 16-lane group's 128: the group's scale exponent and this lane's codes.  The
-// whole warp calls it.
-__device__ __forceinline__ uint2 pack_group(const float (&x)[8], int *exponent)
+// 16-bit patterns without their signs, two in a word: their order is that of the magnitudes, and from
+// kInf16 on they are not finite.
+template <bool BF16>
+constexpr uint32_t kInf16 = BF16 ? 0x7f80u : 0x7c00u;
+
+// The larger of each half (unsigned).
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
 {
-    float top = 0.0f;
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 8 VECS 16-bit values of 128 that a group of 16 / VECS neighbouring lanes holds: the block's scale
+// exponent and this lane's codes.  The whole warp calls it.
+template <bool BF16, int VECS>
+__device__ __forceinline__ void pack_block(const uint4 (&q)[VECS], int *exponent, uint2 (&codes)[VECS])
+{
+    uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-        top = pack_top(top, x[u]);
+    for (int v = 0; v < VECS; ++v) {
+        top = max_halves(top, max_halves(q[v].x & 0x7fff7fffu, q[v].y & 0x7fff7fffu));
+        top = max_halves(top, max_halves(q[v].z & 0x7fff7fffu, q[v].w & 0x7fff7fffu));
+    }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const int e = pack_exponent(top);
-    const float inv = power_of_two(-e);
+    for (int d = 8 / VECS; d > 0; d >>= 1)
+        top = max_halves(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = max(top & 0xffffu, top >> 16);
+    const float largest = BF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+    int e = pack_exponent(largest);
+    const bool odd = __any_sync(0xffffffffu, top >= kInf16<BF16>);
+    if (odd) {  // rare: what is not finite stays out of the scale
+        float finite = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            const uint32_t w[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float2 x = pair16<BF16>(w[u]);
+                finite = pack_top(pack_top(finite, x.x), x.y);
+            }
+        }
+#pragma unroll
+        for (int d = 8 / VECS; d > 0; d >>= 1)
+            finite = fmaxf(finite, __shfl_xor_sync(0xffffffffu, finite, d));
+        e = pack_exponent(finite);
+    }
     *exponent = e;
-    return make_uint2(pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                      pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+    const F2 inv = pair_of(power_of_two(-e));
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+        const uint32_t w[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
+        float2 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            x[u] = pair16<BF16>(w[u]);
+            if (odd)
+                x[u] = make_float2(nan_unless_finite(x[u].x), nan_unless_finite(x[u].y));
+            x[u] = halves_of(mul2(pair_of(x[u].x, x[u].y), inv));
+        }
+        codes[v] = make_uint2(pack4(x[0], x[1]), pack4(x[2], x[3]));
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint2 pack_group(const uint4 &q, int *exponent)
+{
+    const uint4 one[1] = {q};
+    uint2 codes[1];
+    pack_block<BF16>(one, exponent, codes);
+    return codes[0];
 }
 
 // The same for any alignment: a warp and its block, four elements a lane, 32 apart.
@@ -169,7 +249,8 @@ __device__ __forceinline__ uint32_t pack_warp(const float (&x)[4], int *exponent
     const int e = pack_exponent(top);
     const float inv = power_of_two(-e);
     *exponent = e;
-    return pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    return pack4(make_float2(nan_unless_finite(x[0] * inv), nan_unless_finite(x[1] * inv)),
+                 make_float2(nan_unless_finite(x[2] * inv), nan_unless_finite(x[3] * inv)));
 }
 
 }  // namespace gg

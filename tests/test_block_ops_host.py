@@ -72,7 +72,7 @@ def test_norm_backward_accepts():
     backward(M=0, dy=None, h=None, rstd=None, w=None, ws=None, ws_bytes=0, dh=None)
     backward(dh=None, dh_in=at(6))                        # not read, so it may lie anywhere
     assert gg.rms_norm_backward_workspace(100, 200) == 100 * 200 * 4
-    assert gg.rms_norm_backward_workspace(1 << 20, 10) == 304 * 10 * 4
+    assert gg.rms_norm_backward_workspace(1 << 20, 10) == 608 * 10 * 4
     assert gg.rms_norm_backward_workspace(0, 5) == gg.rms_norm_backward_workspace(-3, 5) == 0
 
 
