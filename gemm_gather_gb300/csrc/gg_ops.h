@@ -31,6 +31,8 @@ constexpr int kEpiGradIn8 = 3;  // acc * act'(aux), aux kept in 8 bits (codes, w
 constexpr int kEpiLse = 4;       // (largest, sum of exponentials) of 32 or 128 entries, and the target's logit
 constexpr int kEpiSoftGrad = 5;  // coef (exp(acc - lse) - (i is the target)), in 16 bits
 constexpr int kEpiVocab = 6;     // alpha acc (+ out): what the gradient of the logits is multiplied into
+// kEpiGradW and kEpiVocab of a contraction that is one chunk (linear_kernels.cu chooses them).
+constexpr int kEpiGradWShort = 7, kEpiVocabShort = 8;
 
 struct LinearArgs {
     int64_t I, J, K;

@@ -89,7 +89,15 @@ constexpr int kRowSteps = kStageCols / 8;    // 16-byte accesses of a lane
 template <int EPI>
 constexpr bool kSums = EPI == kEpiGradW || EPI == kEpiVocab || EPI == kEpiLse;
 template <int EPI>
-constexpr bool kLive = EPI == kEpiLse || EPI == kEpiSoftGrad || EPI == kEpiVocab;
+constexpr bool kLive = EPI == kEpiLse || EPI == kEpiSoftGrad || EPI == kEpiVocab || EPI == kEpiVocabShort;
+// Results that may be float32, and may be added to what is there.  The short ones, of a contraction of
+// one chunk, need no sums in registers; a zero is made positive as by the sums.
+template <int EPI>
+constexpr bool kShort = EPI == kEpiGradWShort || EPI == kEpiVocabShort;
+template <int EPI>
+constexpr bool kOwn = EPI == kEpiGradW || EPI == kEpiVocab || kShort<EPI>;
+template <int EPI>
+constexpr bool kScaled = EPI == kEpiVocab || EPI == kEpiVocabShort;
 constexpr float kLog2e = 1.44269504f;
 
 struct Shared {
@@ -226,13 +234,18 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
     }
     if (i >= a.I)
         return;
-    if constexpr (EPI == kEpiVocab) {
+    if constexpr (kShort<EPI>) {
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+            v[u] += 0.0f;
+    }
+    if constexpr (kScaled<EPI>) {
         const float alpha = a.alpha ? *a.alpha : 1.0f;
 #pragma unroll
         for (int u = 0; u < C; ++u)
             v[u] *= alpha;
     }
-    if constexpr (EPI == kEpiGradW || EPI == kEpiVocab) {
+    if constexpr (kOwn<EPI>) {
         if (a.out_f32) {
             float *o = reinterpret_cast<float *>(a.out) + j0 * a.ldo + i;
             const int64_t step = (int64_t)jstep * a.ldo;
@@ -255,9 +268,8 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
         }
     }
     float x[C];
-    constexpr bool kOwn = EPI == kEpiGradW || EPI == kEpiVocab;  // added to what is there
-    const void *aux = kOwn ? (a.accumulate ? a.out : nullptr) : (EPI == kEpiSoftGrad ? nullptr : a.aux);
-    const int64_t ldaux = kOwn ? a.ldo : a.ldaux;
+    const void *aux = kOwn<EPI> ? (a.accumulate ? a.out : nullptr) : (EPI == kEpiSoftGrad ? nullptr : a.aux);
+    const int64_t ldaux = kOwn<EPI> ? a.ldo : a.ldaux;
     if (aux != nullptr) {
 #pragma unroll
         for (int u = 0; u < C; ++u)
@@ -337,9 +349,26 @@ __device__ __forceinline__ int valid16(int64_t J, int64_t j0)
 // would write 64-byte pieces two bytes a lane: measured, 20 cycles of an SM for
 // each such store, 40,000 for a 256 x 256 tile, as long as a contraction over
 // 8192.  Instead a warp turns 32 features x 32 tokens around in 2 KB of its
-// own shared memory: two-byte stores along a row there, then 16 bytes a lane,
-// 8 rows of 64 bytes per global access.  Tensors read in the epilogue come
-// the same way, loaded into registers ahead of the accumulator.
+// own shared memory, in words of two neighbouring tokens: a lane stores its
+// feature's 16 words, then takes 8 features of a pair, which are 16 bytes of each
+// of the two rows, so that a global access is 8 rows of 64 bytes.  (Two-byte
+// stores in the rows' own order took 4.5 of the SM's shared-memory cycles each, a
+// third of a short contraction's tile.)  Tensors read in the epilogue come the same
+// way, loaded into registers ahead of the accumulator.
+//
+// Pair p's word of feature f lies in row p (128 bytes), its 16-byte pieces swapped in
+// odd rows, which keeps the pieces of neighbouring rows in different banks.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+
+// Piece `half` (0 or 1) of this lane's 8 features of pair (lane / 4) + 8 h.
+__device__ __forceinline__ int piece_at(int lane, int h, int half)
+{
+    return ((lane >> 2) + 8 * h) * 128 + ((((lane & 3) * 2 + half) ^ (lane >> 2 & 1)) * 16);
+}
+
+// A lane's row of global access k: tokens of one pair are k and k + 1.
+__device__ __forceinline__ int row_of(int lane, int k) { return (lane >> 2) * 2 + (k & 1) + 16 * (k >> 1); }
 
 // One 16-bit M x N tensor of the epilogue; vec: 16-byte accesses are aligned.
 struct Rows {
@@ -358,17 +387,17 @@ __device__ __forceinline__ Rows rows_of(const void *p, int64_t ld)
 }
 
 // 32 features from i0 of `n` tokens from j0: lane l takes features 8 (l mod 4)
-// on of tokens l / 4 + 8 k.
+// on of tokens row_of(l, k).
 __device__ __forceinline__ void read_rows(const Rows &t, int64_t I, int64_t i0, int64_t j0, int n, int lane,
                                           uint4 (&x)[kRowSteps])
 {
     const int64_t i = i0 + (lane & 3) * 8;
-    const uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
+    const uint16_t *p = t.p + (j0 + row_of(lane, 0)) * t.ld + i;
 #pragma unroll
     for (int k = 0; k < kRowSteps; ++k) {
         x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if ((lane >> 2) + 8 * k < n) {
-            const uint16_t *q = p + (int64_t)(8 * k) * t.ld;
+        if (row_of(lane, k) < n) {
+            const uint16_t *q = p + (int64_t)row_of(0, k) * t.ld;
             if (t.vec && i + 8 <= I) {
                 x[k] = *reinterpret_cast<const uint4 *>(q);
             } else {
@@ -388,13 +417,13 @@ template <bool BF16>
 __device__ __forceinline__ void read_codes(const LinearArgs &a, int64_t i, int64_t j0, int n, int lane, bool vec,
                                            uint4 (&x)[kRowSteps])
 {
-    const uint8_t *p = reinterpret_cast<const uint8_t *>(a.aux) + (j0 + (lane >> 2)) * a.ldaux + i;
-    const float *s = a.scales + (j0 + (lane >> 2)) * a.lds + i / kPackBlock;
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(a.aux) + (j0 + row_of(lane, 0)) * a.ldaux + i;
+    const float *s = a.scales + (j0 + row_of(lane, 0)) * a.lds + i / kPackBlock;
 #pragma unroll
     for (int k = 0; k < kRowSteps; ++k) {
         x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if ((lane >> 2) + 8 * k < n && i < a.I) {
-            const uint8_t *q = p + (int64_t)(8 * k) * a.ldaux;
+        if (row_of(lane, k) < n && i < a.I) {
+            const uint8_t *q = p + (int64_t)row_of(0, k) * a.ldaux;
             uint2 c = make_uint2(0u, 0u);
             if (vec && i + 8 <= a.I) {
                 c = *reinterpret_cast<const uint2 *>(q);
@@ -405,7 +434,7 @@ __device__ __forceinline__ void read_codes(const LinearArgs &a, int64_t i, int64
                         (u < 4 ? c.x : c.y) |= (uint32_t)q[u] << (8 * (u & 3));
             }
             float v[8];
-            values8<BF16>(c, s[(int64_t)(8 * k) * a.lds], v);
+            values8<BF16>(c, s[(int64_t)row_of(0, k) * a.lds], v);
             x[k] = make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]), pair16_of<BF16>(v[4], v[5]),
                               pair16_of<BF16>(v[6], v[7]));
         }
@@ -427,54 +456,122 @@ __device__ __forceinline__ void read_aux(const LinearArgs &a, const Rows &t, int
     }
 }
 
+__device__ __forceinline__ void stage_pair(uint8_t *stage, int lane, int h, const uint4 &a, const uint4 &b)
+{
+    *reinterpret_cast<uint4 *>(stage + piece_at(lane, h, 0)) =
+        make_uint4(low_halves(a.x, b.x), high_halves(a.x, b.x), low_halves(a.y, b.y), high_halves(a.y, b.y));
+    *reinterpret_cast<uint4 *>(stage + piece_at(lane, h, 1)) =
+        make_uint4(low_halves(a.z, b.z), high_halves(a.z, b.z), low_halves(a.w, b.w), high_halves(a.w, b.w));
+}
+
 __device__ __forceinline__ void stage_rows(uint8_t *stage, int lane, const uint4 (&x)[kRowSteps])
 {
 #pragma unroll
-    for (int k = 0; k < kRowSteps; ++k)
-        *reinterpret_cast<uint4 *>(stage + k * 512 + lane * 16) = x[k];
+    for (int h = 0; h < kRowSteps / 2; ++h)
+        stage_pair(stage, lane, h, x[2 * h], x[2 * h + 1]);
     __syncwarp();
 }
 
+// read_rows and stage_rows, two rows of a lane at a time.
+__device__ __forceinline__ void fetch_rows(const Rows &t, int64_t I, int64_t i0, int64_t j0, int n, int lane,
+                                           uint8_t *stage)
+{
+    const int64_t i = i0 + (lane & 3) * 8;
+#pragma unroll 1
+    for (int h = 0; h < kRowSteps / 2; ++h) {
+        uint4 x[2];
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+            const int row = row_of(lane, 2 * h + odd);
+            x[odd] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < n) {
+                const uint16_t *q = t.p + (j0 + row) * t.ld + i;
+                if (t.vec && i + 8 <= I) {
+                    x[odd] = *reinterpret_cast<const uint4 *>(q);
+                } else {
+                    uint16_t e[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        e[u] = i + u < I ? q[u] : (uint16_t)0;
+                    x[odd] = *reinterpret_cast<uint4 *>(e);
+                }
+            }
+        }
+        stage_pair(stage, lane, h, x[0], x[1]);
+    }
+    __syncwarp();
+}
+
+// This lane's word of tokens col and col + 1 (col even).
+__device__ __forceinline__ uint32_t *staged(uint8_t *stage, int lane, int col)
+{
+    const int p = col >> 1;
+    return reinterpret_cast<uint32_t *>(stage + p * 128) + (p & 1 ? lane ^ 4 : lane);
+}
+
 __device__ __forceinline__ void write_rows(const Rows &t, int64_t I, int64_t i0, int64_t j0, int n, int lane,
-                                           const uint8_t *stage)
+                                           uint8_t *stage)
 {
     __syncwarp();
     if (!t.vec) {  // a token at a time, its 32 features side by side (see above: 64-byte pieces)
         uint16_t *q = t.p + j0 * t.ld + i0 + lane;
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(stage) + lane;
         if (i0 + lane < I) {
-#pragma unroll 8
-            for (int r = 0; r < n; ++r)
-                q[r * t.ld] = h[r * 32];
+#pragma unroll 4
+            for (int r = 0; r < n; r += 2) {
+                const uint32_t w = *staged(stage, lane, r);
+                q[r * t.ld] = (uint16_t)w;
+                if (r + 1 < n)
+                    q[(r + 1) * t.ld] = (uint16_t)(w >> 16);
+            }
         }
         __syncwarp();
         return;
     }
     const int64_t i = i0 + (lane & 3) * 8;
-    uint16_t *p = t.p + (j0 + (lane >> 2)) * t.ld + i;
+    uint16_t *p = t.p + (j0 + row_of(lane, 0)) * t.ld + i;
 #pragma unroll
-    for (int k = 0; k < kRowSteps; ++k) {
-        if ((lane >> 2) + 8 * k < n) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(stage + k * 512 + lane * 16);
-            uint16_t *q = p + (int64_t)(8 * k) * t.ld;
+    for (int h = 0; h < kRowSteps / 2; ++h) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(stage + piece_at(lane, h, 0));
+        const uint4 b = *reinterpret_cast<const uint4 *>(stage + piece_at(lane, h, 1));
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+            if (row_of(lane, 2 * h + odd) >= n)
+                continue;
+            const uint4 x = odd ? make_uint4(high_halves(a.x, a.y), high_halves(a.z, a.w), high_halves(b.x, b.y),
+                                             high_halves(b.z, b.w))
+                                : make_uint4(low_halves(a.x, a.y), low_halves(a.z, a.w), low_halves(b.x, b.y),
+                                             low_halves(b.z, b.w));
+            uint16_t *q = p + (int64_t)row_of(0, 2 * h + odd) * t.ld;
             if (i + 8 <= I) {
                 *reinterpret_cast<uint4 *>(q) = x;
             } else {
-                const uint16_t *h = reinterpret_cast<const uint16_t *>(&x);
+                const uint16_t *e = reinterpret_cast<const uint16_t *>(&x);
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
                     if (i + u < I)
-                        q[u] = h[u];
+                        q[u] = e[u];
             }
         }
     }
     __syncwarp();
 }
 
-// This lane's element of a staged token.
-__device__ __forceinline__ uint16_t *staged(uint8_t *stage, int lane, int col)
+// 16 tokens' values of this lane's feature from col on, rounded; and what is staged there.
+__device__ __forceinline__ void stage16(const LinearArgs &a, const float (&v)[16], uint8_t *stage, int lane, int col)
 {
-    return reinterpret_cast<uint16_t *>(stage + col * 64) + lane;
+#pragma unroll
+    for (int u = 0; u < 16; u += 2)
+        *staged(stage, lane, col + u) = a.is_bf16 ? pair16_of<true>(v[u], v[u + 1]) : pair16_of<false>(v[u], v[u + 1]);
+}
+
+__device__ __forceinline__ void unstage16(const LinearArgs &a, float (&x)[16], uint8_t *stage, int lane, int col)
+{
+#pragma unroll
+    for (int u = 0; u < 16; u += 2) {
+        const uint32_t w = *staged(stage, lane, col + u);
+        const float2 f = a.is_bf16 ? pair16<true>(w) : pair16<false>(w);
+        x[u] = f.x, x[u + 1] = f.y;
+    }
 }
 
 // The tensor an epilogue reads beside the sums, or a null pointer.
@@ -483,7 +580,7 @@ __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
 {
     if constexpr (EPI == kEpiLse || EPI == kEpiSoftGrad)
         return rows_of(nullptr, 0);
-    if constexpr (EPI == kEpiGradW || EPI == kEpiVocab)
+    if constexpr (kOwn<EPI>)
         return rows_of(a.accumulate && !a.out_f32 ? a.out : nullptr, a.ldo);
     if constexpr (EPI == kEpiGradIn8) {  // codes: eight bytes a lane
         Rows r = rows_of(a.aux, 0);
@@ -496,13 +593,13 @@ __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
 // The epilogue of a warp's 32 features (from i0) and up to 32 tokens (from j0, n
 // of them).  sums(col, v) gives this lane's sums of columns col .. col + 15; it
 // may be called twice.  aux: the rows read beside them (has_aux).
-template <int EPI, typename Sums>
+template <int EPI, bool REGISTERS = false, typename Sums>
 __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane,
                                        float bias, bool has_aux, const uint4 (&aux)[kRowSteps],
                                        uint8_t *stage, Sums sums, const TokenTerms &terms = TokenTerms{})
 {
     // sums in registers need constant columns; the others keep the code small
-    constexpr int kUnroll = kSums<EPI> ? kStageCols / 16 : 1;
+    constexpr int kUnroll = REGISTERS ? kStageCols / 16 : 1;
     if constexpr (EPI == kEpiForward) {
         if (a.zout != nullptr) {
 #pragma unroll 1
@@ -511,29 +608,35 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
                 sums(c, v);
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
-                    store16(staged(stage, lane, c + u), 0, v[u] + bias, a.is_bf16);
+                    v[u] += bias;
+                stage16(a, v, stage, lane, c);
             }
             write_rows(rows_of(a.zout, a.ldz), a.I, i0, j0, n, lane, stage);
         }
     }
-    if (has_aux)
+    if (has_aux && !REGISTERS)
         stage_rows(stage, lane, aux);
+    if (has_aux && REGISTERS)  // beside the sums there is room for half of them
+        fetch_rows(aux_of<EPI>(a), a.I, i0, j0, n, lane, stage);
 #pragma unroll(kUnroll)
     for (int c = 0; c < kStageCols; c += 16) {
         if (c >= n)
             break;
         float v[16], x[16];
         sums(c, v);
-        if constexpr (EPI == kEpiVocab) {
+        if constexpr (kShort<EPI>) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                v[u] += 0.0f;
+        }
+        if constexpr (kScaled<EPI>) {
             const float alpha = a.alpha ? *a.alpha : 1.0f;
 #pragma unroll
             for (int u = 0; u < 16; ++u)
                 v[u] *= alpha;
         }
         if (has_aux) {  // a lane reads its own elements before it writes over them
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-                x[u] = load16(staged(stage, lane, c + u), 0, a.is_bf16);
+            unstage16(a, x, stage, lane, c);
         }
         if constexpr (EPI == kEpiForward) {
 #pragma unroll
@@ -560,9 +663,7 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
             for (int u = 0; u < 16; ++u)
                 v[u] += x[u];
         }
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-            store16(staged(stage, lane, c + u), 0, v[u], a.is_bf16);
+        stage16(a, v, stage, lane, c);
     }
     write_rows(rows_of(a.out, a.ldo), a.I, i0, j0, n, lane, stage);
 }
@@ -852,11 +953,11 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
         // the first token that is not this tile's
         const int64_t end = gg_min64(columns_of<EPI>(a, p), (int64_t)(c.tj + 1) * a.bt);
         // each share has rows of its own
-        const int64_t row0 = EPI == kEpiVocab ? c.share * a.J : 0;
+        const int64_t row0 = kScaled<EPI> ? c.share * a.J : 0;
         const float bias = EPI == kEpiForward ? load_bias(a, i0 + lane) : 0.0f;
         uint4 pre[kRowSteps];
         if (!kSums<EPI> && early)  // the first group's rows, while the MMAs run
-            read_aux<EPI>(a, aux, i0, j0, valid_rows(end, j0), lane, pre);
+            read_aux<EPI>(a, aux, i0, row0 + j0, valid_rows(end, j0), lane, pre);
         TokenTerms terms[kGroups];
         if constexpr (EPI == kEpiLse || EPI == kEpiSoftGrad) {
 #pragma unroll
@@ -906,17 +1007,28 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                     for (int u = 0; u < 16; ++u)
                         partial[(column(col) + u) * 128] = v[u];
                 }
+            } else if (kShort<EPI> && a.out_f32) {
+#pragma unroll 1
+                for (int col = 0; col < kCols; col += 16) {
+                    const int64_t jc = j0 + column(col);
+                    const int n = valid16(end, jc);
+                    if (n <= 0)
+                        continue;
+                    float v[16];
+                    from_tmem(column(col), v);
+                    emit16<EPI>(a, i0 + lane, row0 + jc, 1, n, v, 0.0f);
+                }
             } else {
 #pragma unroll 1
                 for (int g = 0; g < kGroups; ++g) {
                     const int64_t jg = j0 + g * kStep;
                     if (valid_rows(end, jg) <= 0)
                         break;
-                    emit_rows<EPI>(a, i0, jg, valid_rows(end, jg), lane, bias, early, pre, at.stage_buf,
+                    emit_rows<EPI>(a, i0, row0 + jg, valid_rows(end, jg), lane, bias, early, pre, at.stage_buf,
                                    [&](int col, float(&v)[16]) { from_tmem(g * kStep + col, v); },
                                    terms[kGroups > 1 && g > 0 ? kGroups - 1 : 0]);
                     if (early && g + 1 < kGroups)
-                        read_aux<EPI>(a, aux, i0, jg + kStep, valid_rows(end, jg + kStep), lane, pre);
+                        read_aux<EPI>(a, aux, i0, row0 + jg + kStep, valid_rows(end, jg + kStep), lane, pre);
                 }
             }
             // accumulator read: hand it back to the leader's MMA warp
@@ -924,6 +1036,20 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_cluster(empty0 + (uint32_t)(acc * sizeof(uint64_t)));
+        }
+        if constexpr (EPI == kEpiVocabShort) {
+            if (chunks == 0 && at.parts > 1) {  // no token counts, or none in this share: zeros
+#pragma unroll 1
+                for (int u = 0; u < kCols; ++u)
+                    partial[column(u) * 128] = 0.0f;
+            } else if (chunks == 0) {
+#pragma unroll 1
+                for (int col = 0; col < kCols; col += 16) {
+                    float v[16] = {};
+                    const int64_t jc = j0 + column(col);
+                    emit16<EPI>(a, i0 + lane, row0 + jc, 1, valid16(end, jc), v, 0.0f);
+                }
+            }
         }
         if constexpr (EPI == kEpiLse) {
             // each warp its 32 entries, then the four of a group their 128
@@ -989,9 +1115,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     const int64_t jg = j0 + g * kStep;
-                    if (early)
-                        read_aux<EPI>(a, aux, i0, row0 + jg, valid_rows(end, jg), lane, pre);
-                    emit_rows<EPI>(a, i0, row0 + jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
+                    emit_rows<EPI, true>(a, i0, row0 + jg, valid_rows(end, jg), lane, 0.0f, early, pre, at.stage_buf,
                                    [&](int col, float(&v)[16]) {
 #pragma unroll
                                        for (int u = 0; u < 16; ++u)
@@ -1040,7 +1164,7 @@ __device__ __forceinline__ void join_parts(const LinearArgs &a, const Product &p
                 v[h + u] = (x[0][u] + x[1][u]) + (x[2][u] + x[3][u]);
         }
     };
-    if ((EPI == kEpiGradW || EPI == kEpiVocab) && a.out_f32) {
+    if (kOwn<EPI> && a.out_f32) {
         // nothing is read past the last feature or token: reads that no store waits for
         // could outlive the CTA (the staged rows below store all that they read)
 #pragma unroll 1
@@ -1489,9 +1613,7 @@ __global__ void __launch_bounds__(split::kThreads, 2)
 #pragma unroll
                     for (int g = 0; g < BT; g += kStageCols) {
                         const int n = valid_rows(J, jt + g);
-                        if (aux.p)
-                            read_aux<EPI>(a, aux, i0, jt + g, n, lane, pre);
-                        emit_rows<EPI>(a, i0, jt + g, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
+                        emit_rows<EPI, true>(a, i0, jt + g, n, lane, 0.0f, aux.p != nullptr, pre, stage_buf,
                                        [&](int col, float(&v)[16]) {
 #pragma unroll
                                            for (int u = 0; u < 16; ++u)
@@ -1868,6 +1990,11 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
     return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }
 
+// Whether a sum over many tokens is over so few that it is one chunk: 64 sums a thread leave the epilogue
+// too few registers, which the products of a long contraction hide and those of a short one do not (the
+// 32768 x 2048 gradient of 64 tokens takes 59 us with them and 35 without; of 576, 76 and 57).
+bool one_chunk(const LinearArgs &a) { return a.K <= kChunk * kBK; }
+
 template <int EPI>
 cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s, const char **why)
 {
@@ -1876,9 +2003,16 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
         empty_kernel<EPI><<<(int)gg_min64((groups + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
         return cudaGetLastError();
     }
-    if (p.kernel == GG_LINEAR_PAIR)
+    if (p.kernel == GG_LINEAR_PAIR) {
+        if constexpr (EPI == kEpiGradW || EPI == kEpiVocab) {
+            constexpr int kBrief = EPI == kEpiGradW ? kEpiGradWShort : kEpiVocabShort;
+            if (one_chunk(a))
+                return p.bt > 128 ? launch_pair<kBrief, -1, 256>(a, p.bt, p.split, nullptr, 0, s, why)
+                                  : launch_pair<kBrief, -1, 128>(a, p.bt, p.split, nullptr, 0, s, why);
+        }
         return p.bt > 128 ? launch_pair<EPI, -1, 256>(a, p.bt, p.split, nullptr, 0, s, why)
                           : launch_pair<EPI, -1, 128>(a, p.bt, p.split, nullptr, 0, s, why);
+    }
     switch (p.bt) {
     case 16:
         if constexpr (EPI != kEpiGradW && EPI != kEpiVocab)
@@ -2078,10 +2212,17 @@ cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearAr
     LinearArgs x = dx, w = dw;
     x.chunk = epi == kEpiVocab ? kChunk : 1 << 30;
     w.chunk = kChunk;
+    const bool brief = one_chunk(w);
     switch (epi) {
-    case kEpiVocab: return launch_both_of<kEpiVocab, kEpiVocab>(x, bt_dx, w, bt_dw, s, why);
-    case kEpiGradIn8: return launch_both_of<kEpiGradIn8, kEpiGradW>(x, bt_dx, w, bt_dw, s, why);
-    default: return launch_both_of<kEpiGradIn, kEpiGradW>(x, bt_dx, w, bt_dw, s, why);
+    case kEpiVocab:
+        return brief ? launch_both_of<kEpiVocab, kEpiVocabShort>(x, bt_dx, w, bt_dw, s, why)
+                     : launch_both_of<kEpiVocab, kEpiVocab>(x, bt_dx, w, bt_dw, s, why);
+    case kEpiGradIn8:
+        return brief ? launch_both_of<kEpiGradIn8, kEpiGradWShort>(x, bt_dx, w, bt_dw, s, why)
+                     : launch_both_of<kEpiGradIn8, kEpiGradW>(x, bt_dx, w, bt_dw, s, why);
+    default:
+        return brief ? launch_both_of<kEpiGradIn, kEpiGradWShort>(x, bt_dx, w, bt_dw, s, why)
+                     : launch_both_of<kEpiGradIn, kEpiGradW>(x, bt_dx, w, bt_dw, s, why);
     }
 }
 
