@@ -9,7 +9,8 @@
 // 2. The product z = X W over the whole vocabulary, in 32-bit sums that stay on chip: its epilogue keeps
 //    of every 32 entries the largest logit and the sum of exponentials (8 bytes for 32 logits).
 // 3. join_kernel makes lse and loss of them.
-// 4. For a piece of the vocabulary at a time: the product again, its epilogue turning the logits into
+// 4. For a piece of the vocabulary at a time, the last one first: the product again (but for the last piece,
+//    whose exponentials step 2 kept in the workspace: kept_kernel finishes them), its epilogue turning the logits into
 //    dZ in 16 bits; then dX += dZ W^T (float32, in memory) and the piece's dW = X^T dZ in one launch.
 // 5. dx_kernel rounds dX once, in the tokens' own order, zeros for the masked ones.
 //
@@ -203,9 +204,19 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const int64_t p = (int64_t)blockIdx.x * 32 + lane;
     const float2 *rows = a.partial + p;
     const int64_t n = p < live ? a.rows : 0;
+    constexpr int kHeld = 8;  // rows of a thread that stay in registers
+    float2 held[kHeld];
     float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        const int64_t r = g + 32 * k;
+        held[k] = r < n ? rows[r * a.T] : make_float2(-INFINITY, 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        m = fmaxf(m, held[k].x);
 #pragma unroll 8
-    for (int64_t r = g; r < n; r += 32)
+    for (int64_t r = g + 32 * kHeld; r < n; r += 32)
         m = fmaxf(m, rows[r * a.T].x);
     part[g][lane] = m;
     __syncthreads();
@@ -214,8 +225,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         m = fmaxf(m, part[k][lane]);
     const float from = m == -INFINITY ? 0.0f : m;
     float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        s += held[k].y * expf(held[k].x - from);
 #pragma unroll 8
-    for (int64_t r = g; r < n; r += 32) {
+    for (int64_t r = g + 32 * kHeld; r < n; r += 32) {
         const float2 q = rows[r * a.T];
         s += q.y * expf(q.x - from);
     }
@@ -243,14 +257,18 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     if (!a.stats)
         return;
     // the last block to be done adds up the statistics, in an order that does not depend on which it is
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0)
-        turn = atomicAdd(&a.head->ticket, 1u);
-    __syncthreads();
-    if (turn + 1 != gridDim.x)
-        return;
-    __threadfence();
+    if (gridDim.x > 1) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            turn = atomicAdd(&a.head->ticket, 1u);
+        __syncthreads();
+        if (turn + 1 != gridDim.x)
+            return;
+        __threadfence();
+    } else {
+        __syncthreads();
+    }
     double loss = 0.0, weight = 0.0;
     for (int k = threadIdx.x; k < live; k += kThreads) {
         const double w = (double)a.wt[k];
@@ -267,11 +285,74 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         sums[1][g] = weight;
     }
     __syncthreads();
-    if (threadIdx.x < 2) {
-        double t = 0.0;
-        for (int k = 0; k < 32; ++k)
-            t += sums[threadIdx.x][k];
-        a.stats[threadIdx.x] = (float)t;
+    if (g < 2) {
+        double t = sums[g][lane];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            t += __shfl_xor_sync(0xffffffffu, t, d);
+        if (lane == 0)
+            a.stats[g] = (float)t;
+    }
+}
+
+// The kept exponentials exp(z - top) of a piece to the gradient of its logits, in place:
+// coef (exp(top - lse) of it - (v is the target)), rounded a second time.  A block takes 32 tokens and 1024
+// entries, whose 32 x 32 factors it makes once.  Bound: a read and a write of the piece, from L2 as far as it
+// stayed there.
+template <bool BF16>
+__global__ void __launch_bounds__(256) kept_kernel(const __grid_constant__ EntropyArgs a)
+{
+    __shared__ float factor[32][33];
+    wait_dependencies();
+    launch_dependents();
+    const int live = a.head->live, pad = a.head->live_pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t p0 = (int64_t)blockIdx.y * 32, c0 = (int64_t)blockIdx.x * 1024;
+    if (p0 >= pad)
+        return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int g = warp + 8 * k;
+        float f = 0.0f;
+        if (p0 + lane < live && c0 + g * 32 < a.kept_n) {
+            const float top = a.kept_top[(c0 / 32 + g) * a.T + p0 + lane];
+            f = ex2_approx((top - a.lsec[p0 + lane]) * 1.44269504f) * a.coef[p0 + lane] * (BF16 ? 1.0f : 0x1p-15f);
+        }
+        factor[lane][g] = f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = warp + 8 * k;
+        const int64_t p = p0 + r;
+        if (p >= pad)
+            break;
+        uint16_t *row = a.dz + p * a.piece + c0;
+        const int64_t target = (int64_t)a.tgt[p] - a.kept0 - c0;
+        const float coef = a.coef[p];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int c = (lane + 32 * m) * 8;
+            if (c0 + c >= a.kept_n)
+                break;
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (p < live) {
+                q = *reinterpret_cast<const uint4 *>(row + c);
+                const float f = factor[r][c / 32];
+                uint32_t *w = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float2 v = pair16<BF16>(w[u]);
+                    v.x *= f, v.y *= f;
+                    if (target == c + 2 * u)
+                        v.x -= coef;
+                    if (target == c + 2 * u + 1)
+                        v.y -= coef;
+                    w[u] = pair16_of<BF16>(v.x, v.y);
+                }
+            }
+            *reinterpret_cast<uint4 *>(row + c) = q;
+        }
     }
 }
 
@@ -313,13 +394,14 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
 
 // A launch that may begin its set-up while the one before it on the stream ends.
 template <typename... A>
-cudaError_t launch(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, const EntropyArgs &a)
+cudaError_t launch(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, const EntropyArgs &a,
+                   int64_t grid_y = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)grid_y, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;
@@ -337,6 +419,11 @@ cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s)
 cudaError_t launch_entropy_join(const EntropyArgs &a, cudaStream_t s)
 {
     return launch(join_kernel, (a.T + 31) / 32, kThreads, s, a);
+}
+
+cudaError_t launch_entropy_kept(const EntropyArgs &a, cudaStream_t s)
+{
+    return launch(a.is_bf16 ? kept_kernel<true> : kept_kernel<false>, (a.kept_n + 1023) / 1024, 256, s, a, (a.T + 31) / 32);
 }
 
 cudaError_t launch_entropy_dx(const EntropyArgs &a, cudaStream_t s)

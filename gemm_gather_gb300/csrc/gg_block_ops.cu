@@ -125,6 +125,11 @@ gg_status prepare_norm_backward(const void *dy, int64_t lddy, const void *h, int
 // its logits is what takes memory; equal pieces, in whole 128.
 constexpr int64_t kPiece = 32768;
 
+// From which length of a logit's contraction the loss's product keeps the last piece's exponentials for the
+// gradient, in place of a second product: 4096 tokens, V = 32768, with gradients: K = 256 375 us without and 401
+// with, 512 464 and 477, 1024 674 and 639; 600 tokens: 101 and 94, 128 and 121, 175 and 160.
+constexpr int64_t kKeepFrom = 512;
+
 int64_t piece_of(int64_t V, int64_t piece)
 {
     if (piece == 0) {
@@ -153,7 +158,7 @@ int most_shares(int64_t T, int64_t K)
 
 // The workspace's parts, one behind the other on 256-byte boundaries.
 struct EntropyPlaces {
-    uint64_t x, place, token, tgt, wt, lossc, lsec, coef, ztarget, partial, dx32, dz, end;
+    uint64_t x, place, token, tgt, wt, lossc, lsec, coef, ztarget, partial, dx32, dz, top, end;
 };
 
 EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, bool gradients)
@@ -173,6 +178,7 @@ EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, boo
     if (gradients) {
         w.dx32 = take(t * kp * 4 * (uint64_t)most_shares(T, K));
         w.dz = take(t * (uint64_t)piece_of(V, piece) * 2);
+        w.top = take(t * (uint64_t)(piece_of(V, piece) / 32) * 4);
     }
     w.end = at;
     return w;
@@ -186,8 +192,6 @@ struct Entropy {
     void *dW;
     int64_t lddw;
     int grad_f32, accumulate;
-    uint16_t *dz;
-    int64_t piece;
 };
 
 gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw, gg_weight_layout layout,
@@ -262,7 +266,8 @@ gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw
         e.a.ztarget = floats(at.ztarget);
         e.a.partial = reinterpret_cast<float2 *>(base + at.partial);
         e.a.dx32 = gradients ? floats(at.dx32) : nullptr;
-        e.dz = gradients ? reinterpret_cast<uint16_t *>(base + at.dz) : nullptr;
+        e.a.dz = gradients ? reinterpret_cast<uint16_t *>(base + at.dz) : nullptr;
+        e.a.kept_top = gradients ? floats(at.top) : nullptr;
     }
     e.a.X = X;
     e.a.ldx = ldx;
@@ -286,7 +291,7 @@ gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw
     e.lddw = lddw;
     e.grad_f32 = grad_dtype == GG_F32;
     e.accumulate = accumulate != 0;
-    e.piece = piece_of(V, piece);
+    e.a.piece = piece_of(V, piece);
     *out = e;
     return op_ok();
 }
@@ -355,20 +360,36 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
     z.ztarget = a.ztarget;
     const LinearPlan plan = plan_linear(kEpiLse, z, pairs_only(a.T, a.K) ? GG_LINEAR_PAIR : GG_LINEAR_AUTO);
     a.rows = partial_rows(a.V, plan.kernel == GG_LINEAR_PAIR);
+    const bool gradients = (a.dX || e.dW) && a.K > 0;
+    const int64_t last = (a.V - 1) / a.piece * a.piece;  // the last piece's first entry
+    const bool keeps = gradients && plan.kernel == GG_LINEAR_PAIR && a.K >= kKeepFrom;
+    if (keeps) {
+        a.kept0 = last;
+        a.kept_n = a.V - last;
+        z.kept = a.dz;
+        z.ldkept = a.piece;
+        z.kept0 = last;
+        z.kept_top = const_cast<float *>(a.kept_top);
+    }
     GG_TRY(product(kEpiLse, z, plan, s));
     GG_TRY(launched(launch_entropy_join(a, s), "joining the vocabulary's sums"));
-    if ((!a.dX && !e.dW) || a.K == 0)
+    if (!gradients)
         return op_ok();
     bool both = false;
     int bt_dx = 0, bt_dw = 0;
-    for (int64_t v0 = 0; v0 < a.V; v0 += e.piece) {
-        const int64_t n = a.V - v0 < e.piece ? a.V - v0 : e.piece;
-        z = logits(v0, n, &a.head->live_pad);
-        z.lse = a.lsec;
-        z.coef = a.coef;
-        z.out = e.dz;
-        z.ldo = e.piece;
-        GG_TRY(product(kEpiSoftGrad, z, s));
+    // the last piece first: its logits may still be there
+    for (int64_t v0 = last; v0 >= 0; v0 -= a.piece) {
+        const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
+        if (v0 == last && keeps) {
+            GG_TRY(launched(launch_entropy_kept(a, s), "the gradient of the kept logits"));
+        } else {
+            z = logits(v0, n, &a.head->live_pad);
+            z.lse = a.lsec;
+            z.coef = a.coef;
+            z.out = a.dz;
+            z.ldo = a.piece;
+            GG_TRY(product(kEpiSoftGrad, z, s));
+        }
         LinearArgs x = l, w = l;
         x.I = a.K;
         x.J = a.T;
@@ -376,20 +397,20 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         x.a = entries(v0);
         x.lda = e.ldw;
         x.a_mn = !e.kn;
-        x.b = e.dz;
-        x.ldb = e.piece;
+        x.b = a.dz;
+        x.ldb = a.piece;
         x.out = a.dx32;
         x.ldo = a.ldw;
         x.out_f32 = 1;
-        x.accumulate = v0 > 0;
+        x.accumulate = v0 != last;
         x.live = &a.head->live;
         w.I = e.kn ? n : a.K;
         w.J = e.kn ? a.K : n;
         w.K = a.T;
-        w.a = e.kn ? (const void *)e.dz : a.x;
-        w.lda = e.kn ? e.piece : a.ldw;
-        w.b = e.kn ? a.x : (const void *)e.dz;
-        w.ldb = e.kn ? a.ldw : e.piece;
+        w.a = e.kn ? (const void *)a.dz : a.x;
+        w.lda = e.kn ? a.piece : a.ldw;
+        w.b = e.kn ? a.x : (const void *)a.dz;
+        w.ldb = e.kn ? a.ldw : a.piece;
         w.a_mn = w.b_mn = 1;
         w.out = reinterpret_cast<uint8_t *>(e.dW) + v0 * (e.kn ? 1 : e.lddw) * (e.grad_f32 ? 4 : 2);
         w.ldo = e.lddw;
@@ -398,7 +419,7 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         w.live = &a.head->live_pad;
         w.live_k = 1;
         w.alpha = &a.head->alpha;
-        if (v0 == 0 && a.dX && e.dW) {  // (the pieces are alike, and share dX's rows)
+        if (v0 == last && a.dX && e.dW) {  // (the pieces are alike, and share dX's rows)
             const double apart =
                 plan_linear(kEpiVocab, x, GG_LINEAR_AUTO).ns + plan_linear(kEpiVocab, w, GG_LINEAR_AUTO).ns;
             both = plan_vocab(x, w, apart, most_shares(a.T, a.K), &bt_dx, &bt_dw, &a.shares);

@@ -31,8 +31,8 @@ constexpr int kEpiGradIn8 = 3;  // acc * act'(aux), aux kept in 8 bits (codes, w
 constexpr int kEpiLse = 4;       // (largest, sum of exponentials) of 32 or 128 entries, and the target's logit
 constexpr int kEpiSoftGrad = 5;  // coef (exp(acc - lse) - (i is the target)), in 16 bits
 constexpr int kEpiVocab = 6;     // alpha acc (+ out): what the gradient of the logits is multiplied into
-// kEpiGradW and kEpiVocab of a contraction that is one chunk (linear_kernels.cu chooses them).
-constexpr int kEpiGradWShort = 7, kEpiVocabShort = 8;
+// kEpiGradW, kEpiVocab and kEpiLse of a contraction that is one chunk (linear_kernels.cu chooses them).
+constexpr int kEpiGradWShort = 7, kEpiVocabShort = 8, kEpiLseShort = 9;
 
 struct LinearArgs {
     int64_t I, J, K;
@@ -65,6 +65,9 @@ struct LinearArgs {
     float2 *partial;       // kEpiLse: a row for every 128 entries (split kernel: 32), a place per token
     int64_t ldpartial;
     float *ztarget;
+    void *kept;            // kEpiLse on pairs: exp(acc - top) of entries kept0 on, in 16 bits, or null;
+    float *kept_top;       // top, of every 32 entries: rows of ldpartial tokens
+    int64_t ldkept, kept0;
     const float *lse, *coef;
     const float *alpha;    // kEpiVocab; null: 1
     int skip;              // pairs of the grid past the end of the first product's walk
@@ -198,12 +201,17 @@ struct EntropyArgs {
     float *wt, *lossc, *lsec, *coef, *ztarget;
     float2 *partial;     // rows x T
     int64_t rows;
+    uint16_t *dz;        // compact gradient of a piece's logits, pitch piece
+    int64_t piece;
+    const float *kept_top;  // of the piece whose exponentials lie in dz (launch_entropy_kept)
+    int64_t kept0, kept_n;
     float *dx32;         // compact dX before its rounding, pitch ldw, a share's T rows behind another's
     int shares;
     int *status;
 };
 cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s);  // counts and gathers the tokens
 cudaError_t launch_entropy_join(const EntropyArgs &a, cudaStream_t s);    // partial sums to losses
+cudaError_t launch_entropy_kept(const EntropyArgs &a, cudaStream_t s);    // the kept exponentials to the gradient
 cudaError_t launch_entropy_dx(const EntropyArgs &a, cudaStream_t s);      // dX, rounded, in the tokens' order
 
 // ---- policy loss -------------------------------------------------------------------

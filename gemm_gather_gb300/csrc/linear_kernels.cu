@@ -89,7 +89,9 @@ constexpr int kRowSteps = kStageCols / 8;    // 16-byte accesses of a lane
 template <int EPI>
 constexpr bool kSums = EPI == kEpiGradW || EPI == kEpiVocab || EPI == kEpiLse;
 template <int EPI>
-constexpr bool kLive = EPI == kEpiLse || EPI == kEpiSoftGrad || EPI == kEpiVocab || EPI == kEpiVocabShort;
+constexpr bool kLogSum = EPI == kEpiLse || EPI == kEpiLseShort;
+template <int EPI>
+constexpr bool kLive = kLogSum<EPI> || EPI == kEpiSoftGrad || EPI == kEpiVocab || EPI == kEpiVocabShort;
 // Results that may be float32, and may be added to what is there.  The short ones, of a contraction of
 // one chunk, need no sums in registers; a zero is made positive as by the sums.
 template <int EPI>
@@ -172,7 +174,8 @@ __device__ __forceinline__ void emit_lse(const LinearArgs &a, int64_t i, int64_t
 
 // The same of 16 neighbouring columns in 2 KB of shared memory: a lane turns from a vocabulary entry
 // to half a column's entries (the exclusive or spreads both over the banks).  target: lane c mod 16
-// has column c's, and gets its result.
+// has column c's, and gets its result.  The exponent is one fused operation: what rounding the largest
+// logit's product costs (2^-24 of it) is the same for a column's terms, and no more than lse's own.
 __device__ __forceinline__ float2 lse16(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane, int target,
                                         const float (&v)[16], uint8_t *stage)
 {
@@ -193,7 +196,7 @@ __device__ __forceinline__ float2 lse16(const LinearArgs &a, int64_t i0, int64_t
     const float from = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-        s += ex2_approx((x[k] - from) * kLog2e);
+        s += ex2_approx(fmaf(x[k], kLog2e, -from * kLog2e));
     s += __shfl_xor_sync(0xffffffffu, s, 16);
     if (c < n) {
         const int64_t at = (int64_t)target - i0;
@@ -228,7 +231,7 @@ template <int EPI, int C = 16>
 __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j0, int jstep, int n,
                                        float (&v)[16], float bias)
 {
-    if constexpr (EPI == kEpiLse) {
+    if constexpr (kLogSum<EPI>) {
         emit_lse<C>(a, i, j0, jstep, n, v);
         return;
     }
@@ -578,7 +581,7 @@ __device__ __forceinline__ void unstage16(const LinearArgs &a, float (&x)[16], u
 template <int EPI>
 __device__ __forceinline__ Rows aux_of(const LinearArgs &a)
 {
-    if constexpr (EPI == kEpiLse || EPI == kEpiSoftGrad)
+    if constexpr (kLogSum<EPI> || EPI == kEpiSoftGrad)
         return rows_of(nullptr, 0);
     if constexpr (kOwn<EPI>)
         return rows_of(a.accumulate && !a.out_f32 ? a.out : nullptr, a.ldo);
@@ -673,7 +676,7 @@ template <int EPI>
 __device__ __forceinline__ TokenTerms terms_of(const LinearArgs &a, int64_t j0, int n, int lane)
 {
     TokenTerms t{0.0f, 0.0f, -1};
-    if constexpr (EPI == kEpiLse) {
+    if constexpr (kLogSum<EPI>) {
         if (lane < n)
             t.target = a.target[j0 + lane];
     }
@@ -927,6 +930,85 @@ __device__ __forceinline__ bool multiply(const LinearArgs &a, const Product &p, 
     return true;
 }
 
+// The log-sum's epilogue of a tile: each warp its 32 entries, then the four of a group their 128, of this
+// group's kCols columns (every fourth 32).  logits(col, v) gives columns col .. col + 15 of them; it is called
+// twice where the piece's exponentials are kept.
+template <int kCols, typename Logits>
+__device__ __forceinline__ void log_sums(const LinearArgs &a, const Place &at, int64_t i0, int64_t j0, int64_t end,
+                                         const TokenTerms *terms, Logits logits)
+{
+    const auto column = [](int u) { return u / kStageCols * 4 * kStageCols + u % kStageCols; };
+    const int lane = at.lane;
+    float2 own[kCols / 16];
+#pragma unroll
+    for (int col = 0; col < kCols; col += 16) {
+        const int64_t jc = j0 + column(col);
+        const int n = valid16(end, jc);
+        if (n <= 0)
+            continue;
+        float v[16];
+        logits(col, v);
+        const int target = __shfl_sync(0xffffffffu, terms[col / kStageCols].target, (lane & 15) + col % kStageCols);
+        own[col / 16] = lse16(a, i0, jc, n, lane, target, v, at.stage_buf);
+    }
+    if (a.kept && i0 >= a.kept0 && i0 < a.I) {
+        // the last piece's exponentials, from the largest of each 32: the gradient of its logits needs no
+        // second product.  float16 holds them times 2^15.
+        const float up = a.is_bf16 ? 0.0f : 15.0f;
+#pragma unroll
+        for (int g = 0; g < kCols; g += kStageCols) {
+            const int64_t jg = j0 + column(g);
+            const int n = valid_rows(end, jg);
+            if (n <= 0)
+                continue;
+#pragma unroll
+            for (int c = 0; c < kStageCols; c += 16) {
+                if (c >= n)
+                    continue;
+                const float m = own[(g + c) / 16].x;
+                const float from = (m == -INFINITY ? 0.0f : m) * kLog2e - up;
+                if (lane < 16 && c + lane < n)
+                    a.kept_top[(i0 - a.kept0) / 32 * a.ldpartial + jg + c + lane] = m;
+                float v[16];
+                logits(g + c, v);
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] = ex2_approx(fmaf(v[u], kLog2e, -__shfl_sync(0xffffffffu, from, u)));
+                stage16(a, v, at.stage_buf, lane, c);
+            }
+            write_rows(rows_of(a.kept, a.ldkept), a.I - a.kept0, i0 - a.kept0, jg, n, lane, at.stage_buf);
+        }
+    }
+    float2 *mine = reinterpret_cast<float2 *>(at.stage_buf);
+#pragma unroll
+    for (int col = 0; col < kCols; col += 16)
+        if (lane < 16)
+            mine[col + lane] = own[col / 16];
+    group_sync(at.group);
+    // warp q finishes a quarter of the columns
+    constexpr int kEach = kCols / 4;
+    const int col = at.q * kEach + lane;
+    const int64_t j = j0 + column(col);
+    if (lane < kEach && j < end) {
+        const uint8_t *first = at.stage_buf - ((at.q + 2) & 3) * kWarpStage;  // q = (2, 3, 0, 1)
+        float2 x[4];
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = reinterpret_cast<const float2 *>(first + k * kWarpStage)[col];
+            m = fmaxf(m, x[k].x);
+        }
+        const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            s += x[k].y * ex2_approx((x[k].x - from) * kLog2e);
+        const int64_t row = (i0 - at.q * 32) / 128;
+        if (row * 128 < a.I)
+            a.partial[row * a.ldpartial + j] = make_float2(m, s);
+    }
+    group_sync(at.group);
+}
+
 // An epilogue warp's share of the same.
 template <int EPI, int BT>
 __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Place &at)
@@ -959,7 +1041,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
         if (!kSums<EPI> && early)  // the first group's rows, while the MMAs run
             read_aux<EPI>(a, aux, i0, row0 + j0, valid_rows(end, j0), lane, pre);
         TokenTerms terms[kGroups];
-        if constexpr (EPI == kEpiLse || EPI == kEpiSoftGrad) {
+        if constexpr (kLogSum<EPI> || EPI == kEpiSoftGrad) {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
                 terms[g] = terms_of<EPI>(a, j0 + g * kStep, valid_rows(end, j0 + g * kStep), lane);
@@ -975,7 +1057,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
             const bool got = role_wait(ptx::smem_addr(&at.sh->tmem_full[acc]),
                                        (uint32_t)((at.count >> 1) & 1), a.wait_limit_ns, at.abort_flag);
             // (the warps of a group meet below: they give up together)
-            if (EPI == kEpiLse ? !group_agrees(at.group, got) : !__all_sync(0xffffffffu, got))
+            if (kLogSum<EPI> ? !group_agrees(at.group, got) : !__all_sync(0xffffffffu, got))
                 return false;
             fence_after();
             const uint32_t t_addr = t_lane + (uint32_t)(acc * BT);
@@ -1007,6 +1089,8 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                     for (int u = 0; u < 16; ++u)
                         partial[(column(col) + u) * 128] = v[u];
                 }
+            } else if constexpr (EPI == kEpiLseShort) {
+                log_sums<kCols>(a, at, i0, j0, end, terms, [&](int col, float(&v)[16]) { from_tmem(column(col), v); });
             } else if (kShort<EPI> && a.out_f32) {
 #pragma unroll 1
                 for (int col = 0; col < kCols; col += 16) {
@@ -1052,50 +1136,11 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
             }
         }
         if constexpr (EPI == kEpiLse) {
-            // each warp its 32 entries, then the four of a group their 128
-            float2 own[kCols / 16];
-#pragma unroll
-            for (int col = 0; col < kCols; col += 16) {
-                const int64_t jc = j0 + column(col);
-                const int n = valid16(end, jc);
-                if (n <= 0)
-                    continue;
-                float v[16];
+            log_sums<kCols>(a, at, i0, j0, end, terms, [&](int col, float(&v)[16]) {
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
                     v[u] = sum[col + u];
-                const int target =
-                    __shfl_sync(0xffffffffu, terms[col / kStageCols].target, (lane & 15) + col % kStageCols);
-                own[col / 16] = lse16(a, i0, jc, n, lane, target, v, at.stage_buf);
-            }
-            float2 *mine = reinterpret_cast<float2 *>(at.stage_buf);
-#pragma unroll
-            for (int col = 0; col < kCols; col += 16)
-                if (lane < 16)
-                    mine[col + lane] = own[col / 16];
-            group_sync(at.group);
-            // warp q finishes a quarter of the columns
-            constexpr int kEach = kCols / 4;
-            const int col = at.q * kEach + lane;
-            const int64_t j = j0 + column(col);
-            if (lane < kEach && j < end) {
-                const uint8_t *first = at.stage_buf - ((at.q + 2) & 3) * kWarpStage;  // q = (2, 3, 0, 1)
-                float2 x[4];
-                float m = -INFINITY, s = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[k] = reinterpret_cast<const float2 *>(first + k * kWarpStage)[col];
-                    m = fmaxf(m, x[k].x);
-                }
-                const float from = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s += x[k].y * ex2_approx((x[k].x - from) * kLog2e);
-                const int64_t row = (i0 - at.q * 32) / 128;
-                if (row * 128 < a.I)
-                    a.partial[row * a.ldpartial + j] = make_float2(m, s);
-            }
-            group_sync(at.group);
+            });
         } else if constexpr (kSums<EPI>) {
             if (at.parts > 1) {
 #pragma unroll
@@ -1333,7 +1378,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     if constexpr (!kTwo) {
         if (at.parts > 1) {
             cluster_sync();
-            if constexpr (EPI != kEpiLse && EPI != kEpiSoftGrad) {  // (these do not split tiles)
+            if constexpr (!kLogSum<EPI> && EPI != kEpiSoftGrad) {  // (these do not split tiles)
                 if (warp >= 2 && warp < pair::kProducer2 && ok)
                     pair::join_parts<EPI, BT>(a, p, at);
             }
@@ -1990,6 +2035,10 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
     return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }
 
+// Logits of longer contractions are summed in chunks for lse, whose tiles hide that: truncation costs 2e-6 of a
+// logit at 2048, and grows with the length.
+constexpr int64_t kPlainLse = 2048;
+
 // Whether a sum over many tokens is over so few that it is one chunk: 64 sums a thread leave the epilogue
 // too few registers, which the products of a long contraction hide and those of a short one do not (the
 // 32768 x 2048 gradient of 64 tokens takes 59 us with them and 35 without; of 576, 76 and 57).
@@ -2004,9 +2053,10 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
         return cudaGetLastError();
     }
     if (p.kernel == GG_LINEAR_PAIR) {
-        if constexpr (EPI == kEpiGradW || EPI == kEpiVocab) {
-            constexpr int kBrief = EPI == kEpiGradW ? kEpiGradWShort : kEpiVocabShort;
-            if (one_chunk(a))
+        if constexpr (EPI == kEpiGradW || EPI == kEpiVocab || EPI == kEpiLse) {
+            constexpr int kBrief =
+                EPI == kEpiGradW ? kEpiGradWShort : (EPI == kEpiVocab ? kEpiVocabShort : kEpiLseShort);
+            if (EPI == kEpiLse ? a.K <= kPlainLse : one_chunk(a))
                 return p.bt > 128 ? launch_pair<kBrief, -1, 256>(a, p.bt, p.split, nullptr, 0, s, why)
                                   : launch_pair<kBrief, -1, 128>(a, p.bt, p.split, nullptr, 0, s, why);
         }
@@ -2236,7 +2286,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
         return cudaErrorNotSupported;
     }
     LinearArgs a = args;
-    a.chunk = epi == kEpiGradW || epi == kEpiVocab || epi == kEpiLse ? kChunk : 1 << 30;
+    a.chunk = epi == kEpiGradW || epi == kEpiVocab || (epi == kEpiLse && a.K > kPlainLse) ? kChunk : 1 << 30;
     switch (epi) {
     case kEpiForward: return launch_epi<kEpiForward>(a, p, s, why);
     case kEpiGradIn: return launch_epi<kEpiGradIn>(a, p, s, why);

@@ -3,9 +3,10 @@
 Bounds, from the arithmetic: a logit is a float32 sum over K, off by bz = K 2^-23 sum |x w| (which also
 covers an accumulator that truncates); its exponential's argument is a difference times log2 e, (|z - lse| + 1)
 2^-22; so lse is off by the largest bz and 2^-20 + |lse| 2^-23, the loss by twice that.  A probability is
-off by the factor d = bz + d(lse) + (|z - lse| + 4) 2^-22.  dZ adds its one rounding to 16 bits (half a
-step, and float16's least step of 2^-24 at weights whose largest lies in [2^13, 2^14)); dX and dW are sums of
-dZ's errors times the other operand, a float32 sum's own bound, and half an ulp of the output.
+off by the factor d = bz + d(lse) + (|z - lse| + 4) 2^-22.  dZ adds its rounding to 16 bits (half a step, and
+float16's least step of 2^-24 at weights whose largest lies in [2^13, 2^14)), twice in the piece whose
+exponentials were kept; dX and dW are sums of dZ's errors times the other operand, a float32 sum's own bound,
+and half an ulp of the output.
 """
 import math
 
@@ -78,7 +79,7 @@ class Case:
         coef = (tw * grad_scale)[:, None]
         dz = coef * (p - hot)
         d = bz + dl[:, None] + ((z - lse[:, None]).abs() + 4) * 2.0 ** -22
-        half = 2.0 ** (-11 if dt is F16 else -8)
+        half = 2 * 2.0 ** (-11 if dt is F16 else -8)
         least = float(coef.abs().max()) * 2.0 ** -37 if dt is F16 else 0.0
         err = coef.abs() * (p * torch.expm1(d) + 2.0 ** -23) + dz.abs() * half + least
         dx = self.dx if dx is None else dx
@@ -266,7 +267,7 @@ def test_gradients_against_differences():
             e = e.view(t.shape)
             a = (f(x + e, w) - f(x - e, w)) if t is x else (f(x, w + e) - f(x, w - e))
             slope, got = float(a) / 2e-5, float(g.contiguous().view(-1)[i])
-            # dZ's rounding of half a step, its sum's terms of either sign; the output's own
+            # dZ's roundings of half a step, its sum's terms of either sign; the output's own
             assert abs(got - slope) <= 2.0 ** -7 * float(tw.max()) * 4
 
 
