@@ -25,6 +25,7 @@
 #include "act.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
+#include "launch.cuh"
 #include "pack8.cuh"
 #include "tc.cuh"
 
@@ -37,30 +38,25 @@ constexpr int kSMs = 152;
 constexpr int kThreads = 1024;
 constexpr int kEach = 16;                      // tokens of a thread at a time
 constexpr int kChunkTokens = kThreads * kEach;
-constexpr int kMaxRows = 64;                   // rows a block copies for one such chunk
+constexpr int kMaxRows = 128;                  // rows a block copies for one such chunk
 constexpr int kPad = 64;                       // a k-block of the products
 
 // What the blocks of a launch share out: at most kChunkTokens / kBlocks + 1 rows each.
-constexpr int kBlocks = 2 * kSMs;
+constexpr int kBlocks = kSMs;  // 1024 threads of 64 registers: one an SM
 static_assert(kChunkTokens / kBlocks + 2 <= kMaxRows, "a block's list of rows");
 
-__device__ __forceinline__ void copy_row(uint16_t *to, const uint16_t *from, int64_t K, int lane)
+// Piece m of a row of K elements, kPiece of them: four vectors a lane.
+constexpr int kPiece = 1024;
+__device__ __forceinline__ void copy_piece(uint16_t *to, const uint16_t *from, int64_t K, int m, int lane)
 {
-    const int64_t whole = K / 8;
-    int64_t c = lane;
-    for (; c + 96 < whole; c += 128) {
-        uint4 q[4];
+    const int64_t n0 = (int64_t)m * kPiece + lane * 8;
+    uint4 q[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            q[u] = reinterpret_cast<const uint4 *>(from)[c + 32 * u];
+    for (int u = 0; u < 4; ++u)
+        q[u] = load8(from + n0 + u * 256, K - n0 - u * 256);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            reinterpret_cast<uint4 *>(to)[c + 32 * u] = q[u];
-    }
-    for (; c < whole; c += 32)
-        reinterpret_cast<uint4 *>(to)[c] = reinterpret_cast<const uint4 *>(from)[c];
-    if (whole * 8 + lane < K)
-        to[whole * 8 + lane] = from[whole * 8 + lane];
+    for (int u = 0; u < 4; ++u)
+        store8(to + n0 + u * 256, K - n0 - u * 256, q[u]);
 }
 
 // Every block counts all the tokens (so that none waits for another) and copies its share of rows.
@@ -148,9 +144,13 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
             }
         }
         __syncthreads();
-        for (int r = warp; r < listed; r += 32)
-            copy_row(reinterpret_cast<uint16_t *>(a.x) + (int64_t)list_place[r] * a.ldw,
-                     reinterpret_cast<const uint16_t *>(a.X) + (int64_t)list_token[r] * a.ldx, a.K, lane);
+        const int pieces = (int)((a.K + kPiece - 1) / kPiece);
+        for (int it = warp; it < listed * pieces; it += 32) {
+            const int r = it / pieces;
+            copy_piece(reinterpret_cast<uint16_t *>(a.x) + (int64_t)list_place[r] * a.ldw,
+                       reinterpret_cast<const uint16_t *>(a.X) + (int64_t)list_token[r] * a.ldx, a.K, it - r * pieces,
+                       lane);
+        }
         __syncthreads();  // the lists and counts are written again
     }
     const int n = base;
@@ -190,13 +190,20 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
     }
 }
 
+__device__ __forceinline__ double warp_total(double v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
 // 32 tokens a block, 32 shares of the rows; the rows twice (the second time from L2), so that no
 // exponential waits for another.  A sum of NaN stays NaN; rows of nothing but -inf have sum 0.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ EntropyArgs a)
 {
     __shared__ float part[32][33];
     __shared__ unsigned turn;
-    __shared__ double sums[2][32];
     wait_dependencies();
     launch_dependents();
     const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -204,6 +211,15 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const int64_t p = (int64_t)blockIdx.x * 32 + lane;
     const float2 *rows = a.partial + p;
     const int64_t n = p < live ? a.rows : 0;
+    float weight = 0.0f, target = 0.0f;
+    int token = 0;
+    if (g == 0 && p < pad) {
+        weight = a.wt[p];
+        if (p < live) {
+            target = a.ztarget[p];
+            token = a.token[p];
+        }
+    }
     constexpr int kHeld = 8;  // rows of a thread that stay in registers
     float2 held[kHeld];
     float m = -INFINITY;
@@ -236,7 +252,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     __syncthreads();
     part[g][lane] = s;
     __syncthreads();
-    if (g == 0 && p < pad) {
+    if (g > 0)
+        return;
+    double sum = 0.0, total = 0.0;  // of the block's 32 tokens
+    if (p < pad) {
         float lse = 0.0f;
         if (p < live) {
             s = 0.0f;
@@ -244,54 +263,44 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
             for (int k = 0; k < 32; ++k)
                 s += part[k][lane];
             lse = m + logf(s);
-            const float loss = lse - a.ztarget[p];
-            const int t = a.token[p];
-            a.loss[t] = loss;
+            const float loss = lse - target;
+            a.loss[token] = loss;
             if (a.lse)
-                a.lse[t] = lse;
-            a.lossc[p] = loss;
+                a.lse[token] = lse;
+            sum = (double)weight * (double)loss;
+            total = (double)weight;
         }
         a.lsec[p] = lse;
-        a.coef[p] = a.wt[p] * a.head->scale;
+        a.coef[p] = weight * a.head->scale;
     }
     if (!a.stats)
         return;
-    // the last block to be done adds up the statistics, in an order that does not depend on which it is
+    sum = warp_total(sum);
+    total = warp_total(total);
+    // the last block to be done adds up the blocks' sums, in an order that does not depend on which it is
     if (gridDim.x > 1) {
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
+        double2 *sums = reinterpret_cast<double2 *>(a.sums);
+        if (lane == 0) {
+            sums[blockIdx.x] = make_double2(sum, total);
+            __threadfence();
             turn = atomicAdd(&a.head->ticket, 1u);
-        __syncthreads();
+        }
+        __syncwarp();
         if (turn + 1 != gridDim.x)
             return;
         __threadfence();
-    } else {
-        __syncthreads();
-    }
-    double loss = 0.0, weight = 0.0;
-    for (int k = threadIdx.x; k < live; k += kThreads) {
-        const double w = (double)a.wt[k];
-        loss += w * (double)__ldcg(a.lossc + k);
-        weight += w;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        loss += __shfl_xor_sync(0xffffffffu, loss, d);
-        weight += __shfl_xor_sync(0xffffffffu, weight, d);
+        sum = total = 0.0;
+        for (unsigned b = lane; b < gridDim.x; b += 32) {
+            const double2 q = __ldcg(sums + b);
+            sum += q.x;
+            total += q.y;
+        }
+        sum = warp_total(sum);
+        total = warp_total(total);
     }
     if (lane == 0) {
-        sums[0][g] = loss;
-        sums[1][g] = weight;
-    }
-    __syncthreads();
-    if (g < 2) {
-        double t = sums[g][lane];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            t += __shfl_xor_sync(0xffffffffu, t, d);
-        if (lane == 0)
-            a.stats[g] = (float)t;
+        a.stats[0] = (float)sum;
+        a.stats[1] = (float)total;
     }
 }
 
@@ -307,51 +316,66 @@ __global__ void __launch_bounds__(256) kept_kernel(const __grid_constant__ Entro
     launch_dependents();
     const int live = a.head->live, pad = a.head->live_pad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t p0 = (int64_t)blockIdx.y * 32, c0 = (int64_t)blockIdx.x * 1024;
+    const int64_t p0 = (int64_t)blockIdx.x * 32;
     if (p0 >= pad)
         return;
+    for (int64_t c0 = (int64_t)blockIdx.y * 1024; c0 < a.kept_n; c0 += (int64_t)gridDim.y * 1024) {
+        __syncthreads();  // the factors are made anew
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int g = warp + 8 * k;
-        float f = 0.0f;
-        if (p0 + lane < live && c0 + g * 32 < a.kept_n) {
-            const float top = a.kept_top[(c0 / 32 + g) * a.T + p0 + lane];
-            f = ex2_approx((top - a.lsec[p0 + lane]) * 1.44269504f) * a.coef[p0 + lane] * (BF16 ? 1.0f : 0x1p-15f);
+        for (int k = 0; k < 4; ++k) {
+            const int g = warp + 8 * k;
+            float f = 0.0f;
+            if (p0 + lane < live && c0 + g * 32 < a.kept_n) {
+                const float top = a.kept_top[(c0 / 32 + g) * a.T + p0 + lane];
+                f = ex2_approx((top - a.lsec[p0 + lane]) * 1.44269504f) * a.coef[p0 + lane] * (BF16 ? 1.0f : 0x1p-15f);
+            }
+            factor[lane][g] = f;
         }
-        factor[lane][g] = f;
-    }
-    __syncthreads();
+        __syncthreads();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            uint4 q[2][4];  // two rows of a warp, all loads in flight
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int r = warp + 8 * k;
-        const int64_t p = p0 + r;
-        if (p >= pad)
-            break;
-        uint16_t *row = a.dz + p * a.piece + c0;
-        const int64_t target = (int64_t)a.tgt[p] - a.kept0 - c0;
-        const float coef = a.coef[p];
+            for (int k = 0; k < 2; ++k) {
+                const int64_t p = p0 + warp + 8 * (2 * half + k);
+                const uint16_t *row = a.dz + p * a.piece + c0;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int c = (lane + 32 * m) * 8;
-            if (c0 + c >= a.kept_n)
-                break;
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (p < live) {
-                q = *reinterpret_cast<const uint4 *>(row + c);
-                const float f = factor[r][c / 32];
-                uint32_t *w = reinterpret_cast<uint32_t *>(&q);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float2 v = pair16<BF16>(w[u]);
-                    v.x *= f, v.y *= f;
-                    if (target == c + 2 * u)
-                        v.x -= coef;
-                    if (target == c + 2 * u + 1)
-                        v.y -= coef;
-                    w[u] = pair16_of<BF16>(v.x, v.y);
+                for (int m = 0; m < 4; ++m) {
+                    const int c = (lane + 32 * m) * 8;
+                    q[k][m] = p < live && c0 + c < a.kept_n ? *reinterpret_cast<const uint4 *>(row + c)
+                                                            : make_uint4(0u, 0u, 0u, 0u);
                 }
             }
-            *reinterpret_cast<uint4 *>(row + c) = q;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = warp + 8 * (2 * half + k);
+                const int64_t p = p0 + r;
+                if (p >= pad)
+                    continue;
+                uint16_t *row = a.dz + p * a.piece + c0;
+                const int64_t target = (int64_t)a.tgt[p] - a.kept0 - c0;  // behind the last token: none
+                const float coef = a.coef[p];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int c = (lane + 32 * m) * 8;
+                    if (c0 + c >= a.kept_n)
+                        continue;
+                    const float f = factor[r][c / 32];
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&q[k][m]);
+                    const bool here = target >= c && target < c + 8;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float2 v = pair16<BF16>(w[u]);
+                        v.x *= f, v.y *= f;
+                        if (here && target == c + 2 * u)
+                            v.x -= coef;
+                        if (here && target == c + 2 * u + 1)
+                            v.y -= coef;
+                        w[u] = pair16_of<BF16>(v.x, v.y);
+                    }
+                    *reinterpret_cast<uint4 *>(row + c) = q[k][m];
+                }
+            }
         }
     }
 }
@@ -392,48 +416,33 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
     }
 }
 
-// A launch that may begin its set-up while the one before it on the stream ends.
-template <typename... A>
-cudaError_t launch(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, const EntropyArgs &a,
-                   int64_t grid_y = 1)
-{
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)grid_y, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 }  // namespace
 
 cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s)
 {
-    return launch(tokens_kernel, gg_min64(a.T, kBlocks), kThreads, s, a);
+    return launch_early(tokens_kernel, dim3((unsigned)gg_min64(a.T, kBlocks)), kThreads, 0, s, a);
 }
 
 cudaError_t launch_entropy_join(const EntropyArgs &a, cudaStream_t s)
 {
-    return launch(join_kernel, (a.T + 31) / 32, kThreads, s, a);
+    return launch_early(join_kernel, dim3((unsigned)((a.T + 31) / 32)), kThreads, 0, s, a);
 }
 
 cudaError_t launch_entropy_kept(const EntropyArgs &a, cudaStream_t s)
 {
-    return launch(a.is_bf16 ? kept_kernel<true> : kept_kernel<false>, (a.kept_n + 1023) / 1024, 256, s, a, (a.T + 31) / 32);
+    // (pieces have fewer than 2^21 times 1024 entries; token groups go down the grid's long side)
+    const dim3 grid((unsigned)((a.T + 31) / 32), (unsigned)gg_min64((a.kept_n + 1023) / 1024, 65535));
+    return launch_early(a.is_bf16 ? kept_kernel<true> : kept_kernel<false>, grid, 256, 0, s, a);
 }
 
 cudaError_t launch_entropy_dx(const EntropyArgs &a, cudaStream_t s)
 {
     const bool wide = ((reinterpret_cast<uint64_t>(a.dX) | (uint64_t)(a.lddx * 2)) & 15) == 0;
     const int64_t total = a.T * (wide ? (a.K + 7) / 8 : a.K);
-    const int64_t grid = gg_min64((total + 255) / 256, kSMs * 8);
+    const dim3 grid((unsigned)gg_min64((total + 255) / 256, kSMs * 8));
     if (wide)
-        return launch(a.is_bf16 ? dx_kernel<true, 8> : dx_kernel<false, 8>, grid, 256, s, a);
-    return launch(a.is_bf16 ? dx_kernel<true, 1> : dx_kernel<false, 1>, grid, 256, s, a);
+        return launch_early(a.is_bf16 ? dx_kernel<true, 8> : dx_kernel<false, 8>, grid, 256, 0, s, a);
+    return launch_early(a.is_bf16 ? dx_kernel<true, 1> : dx_kernel<false, 1>, grid, 256, 0, s, a);
 }
 
 }  // namespace gg

@@ -153,12 +153,12 @@ int64_t partial_rows(int64_t V, bool pairs) { return pairs ? (V + 127) / 128 : (
 int most_shares(int64_t T, int64_t K)
 {
     const int64_t tiles = ((T + 255) / 256) * ((K + 255) / 256);
-    return tiles >= 76 ? 1 : (tiles >= 38 ? 2 : (tiles >= 19 ? 4 : 8));
+    return tiles >= 76 ? 1 : (tiles >= 38 ? 4 : 8);
 }
 
 // The workspace's parts, one behind the other on 256-byte boundaries.
 struct EntropyPlaces {
-    uint64_t x, place, token, tgt, wt, lossc, lsec, coef, ztarget, partial, dx32, dz, top, end;
+    uint64_t x, place, token, tgt, wt, sums, lsec, coef, ztarget, partial, dx32, dz, top, end;
 };
 
 EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, bool gradients)
@@ -172,8 +172,9 @@ EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, boo
     };
     const uint64_t t = (uint64_t)T, kp = (uint64_t)((K + 7) / 8 * 8);
     w.x = take(t * kp * 2);
-    for (uint64_t *p : {&w.place, &w.token, &w.tgt, &w.wt, &w.lossc, &w.lsec, &w.coef, &w.ztarget})
+    for (uint64_t *p : {&w.place, &w.token, &w.tgt, &w.wt, &w.lsec, &w.coef, &w.ztarget})
         *p = take(t * 4);
+    w.sums = take((t + 31) / 32 * 16);
     w.partial = take(t * (uint64_t)partial_rows(V, pairs_only(T, K)) * 8);
     if (gradients) {
         w.dx32 = take(t * kp * 4 * (uint64_t)most_shares(T, K));
@@ -260,7 +261,7 @@ gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw
         e.a.token = ints(at.token);
         e.a.tgt = ints(at.tgt);
         e.a.wt = floats(at.wt);
-        e.a.lossc = floats(at.lossc);
+        e.a.sums = base + at.sums;
         e.a.lsec = floats(at.lsec);
         e.a.coef = floats(at.coef);
         e.a.ztarget = floats(at.ztarget);

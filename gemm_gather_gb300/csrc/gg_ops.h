@@ -198,7 +198,8 @@ struct EntropyArgs {
     int *place;          // a token's compact place, or -1
     int *token;          // compact: its token
     int *tgt;            // compact targets (-1 behind the last)
-    float *wt, *lossc, *lsec, *coef, *ztarget;
+    float *wt, *lsec, *coef, *ztarget;
+    void *sums;          // two doubles for every 32 tokens
     float2 *partial;     // rows x T
     int64_t rows;
     uint16_t *dz;        // compact gradient of a piece's logits, pitch piece

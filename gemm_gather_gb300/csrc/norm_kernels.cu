@@ -24,6 +24,7 @@
 #include "act.cuh"
 #include "gg_internal.h"
 #include "gg_ops.h"
+#include "launch.cuh"
 #include "pack8.cuh"
 #include "tc.cuh"
 
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     uint4 h[VPT];
     F2 sq = pair_of(0.0f);
     Eight w;
+    wait_dependencies();
     if (live) {
         const uint16_t *x = reinterpret_cast<const uint16_t *>(a.x) + row * a.ldx;
         const uint16_t *r = RES ? reinterpret_cast<const uint16_t *>(a.residual) + row * a.ldr : nullptr;
@@ -248,6 +250,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     }
     const float2 both = halves_of(sq);
     const float total = row_sum(both.x + both.y, s, sums, 0);
+    launch_dependents();  // (earlier, the next launch's blocks take places from this one's)
     if (!live)
         return;
     const float rstd = 1.0f / sqrtf(total / (float)N + a.eps);
@@ -292,6 +295,8 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const __grid_constant__ N
     const RowShape s{(int)blockDim.x / 32, 1};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int turn = 0;
+    wait_dependencies();
+    launch_dependents();
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
         const auto sum_at = [&](int64_t n) {
             float v = load16(a.x, row * a.ldx + n, BF16);
@@ -384,6 +389,8 @@ __global__ void __launch_bounds__(D > 1 ? 256 : (VPT > 2 ? 512 : 1024), D > 1 ? 
         }
         copies_commit();
     };
+    wait_dependencies();
+    launch_dependents();
     Eight w[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
@@ -458,7 +465,6 @@ __global__ void __launch_bounds__(D > 1 ? 256 : (VPT > 2 ? 512 : 1024), D > 1 ? 
         if constexpr (D > 1)
             slot = slot + 1 == D ? 0 : slot + 1;
     }
-    launch_dependents();
     if (!a.partial)
         return;
     float *out = a.partial + (int64_t)blockIdx.x * a.N;
@@ -540,6 +546,7 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float *partial, i
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t n = (int64_t)blockIdx.x * 32 + lane;
     wait_dependencies();
+    launch_dependents();
     float t = 0.0f;
     if (n < N) {
         const int from = parts * g / 32, to = parts * (g + 1) / 32;
@@ -579,6 +586,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
     const int step_units = (int)(step - step_rows * units);
     int64_t row = first / units;
     int unit = (int)(first - row * units);
+    wait_dependencies();
+    launch_dependents();
     // a warp's four groups end together
     for (int64_t t0 = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 5) * 4; t0 < total; t0 += step * kAhead) {
         uint4 q[kAhead][2];
@@ -624,6 +633,8 @@ __global__ void __launch_bounds__(256) pack_any_kernel(const __grid_constant__ P
     const int64_t units = (a.N + kPackBlock - 1) / kPackBlock;
     const int64_t total = a.M * units;
     const int lane = threadIdx.x & 31;
+    wait_dependencies();
+    launch_dependents();
     for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < total; t += (int64_t)gridDim.x * 8) {
         const int64_t row = t / units, b = t - row * units, n0 = b * kPackBlock + lane;
         float v[4];
@@ -649,6 +660,8 @@ __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unp
 {
     const I units = (I)((a.N + V - 1) / V);
     const I total = (I)a.M * units;
+    wait_dependencies();
+    launch_dependents();
     for (I t0 = (I)blockIdx.x * (256 * kSteps) + threadIdx.x; t0 < total; t0 += (I)gridDim.x * (256 * kSteps)) {
         uint2 c[kSteps];
         float scale[kSteps];
@@ -705,6 +718,9 @@ bool row_shape(int64_t M, int64_t N, int most, RowShape *s, int *vpt)
         v *= 2;
     s->R = (int)((warps + v - 1) / v);
     s->rows = s->R >= 8 ? 1 : 8 / s->R;
+    // (the backward pass leaves a block's sums behind: fewer blocks, each with its rows side by side)
+    while (most == 2 && v == 1 && s->R * s->rows <= 8 && M > (int64_t)kSMs * 2 * s->rows)
+        s->rows *= 2;
     *vpt = v;
     return true;
 }
@@ -755,13 +771,9 @@ cudaError_t norm_rows(const NormArgs &a, const RowShape &r, int vpt, cudaStream_
 {
     const unsigned grid = (unsigned)((a.M + r.rows - 1) / r.rows);
     const int threads = 32 * r.R * r.rows;
-    if (vpt == 1)
-        norm_kernel<BF16, 1, RES, WHOLE><<<grid, threads, 0, s>>>(a, r);
-    else if (vpt == 2)
-        norm_kernel<BF16, 2, RES, WHOLE><<<grid, threads, 0, s>>>(a, r);
-    else
-        norm_kernel<BF16, 4, RES, WHOLE><<<grid, threads, 0, s>>>(a, r);
-    return cudaGetLastError();
+    return launch_early(vpt == 1 ? norm_kernel<BF16, 1, RES, WHOLE>
+                                 : (vpt == 2 ? norm_kernel<BF16, 2, RES, WHOLE> : norm_kernel<BF16, 4, RES, WHOLE>),
+                        dim3(grid), threads, 0, s, a, r);
 }
 
 template <bool BF16>
@@ -771,10 +783,8 @@ cudaError_t norm_of(const NormArgs &a, cudaStream_t s)
     int vpt;
     const bool wide = on16(a.x, a.ldx) && (!a.residual || on16(a.residual, a.ldr)) && (!a.h || on16(a.h, a.ldh)) &&
                       (!a.y || on16(a.y, a.ldy)) && (!a.codes || on8(a.codes, a.ldc));
-    if (!wide || !row_shape(a.M, a.N, 4, &r, &vpt)) {
-        norm_any_kernel<BF16><<<(int)gg_min64(a.M, kSMs * 4), 512, 0, s>>>(a);
-        return cudaGetLastError();
-    }
+    if (!wide || !row_shape(a.M, a.N, 4, &r, &vpt))
+        return launch_early(norm_any_kernel<BF16>, dim3((unsigned)gg_min64(a.M, kSMs * 4)), 512, 0, s, a);
     if (a.N % kVec == 0)
         return a.residual ? norm_rows<BF16, true, true>(a, r, vpt, s) : norm_rows<BF16, false, true>(a, r, vpt, s);
     return a.residual ? norm_rows<BF16, true, false>(a, r, vpt, s) : norm_rows<BF16, false, false>(a, r, vpt, s);
@@ -791,8 +801,8 @@ cudaError_t launch_backward_kernel(const NormBackwardArgs &a, const RowShape &r,
             return e;
     }
     const int columns = r.rows > 1 ? (int)a.N * 4 : 0;
-    norm_backward_kernel<BF16, VPT, D, IN, WHOLE><<<p.grid, p.threads, p.smem > columns ? p.smem : columns, s>>>(a, r);
-    return cudaGetLastError();
+    return launch_early(norm_backward_kernel<BF16, VPT, D, IN, WHOLE>, dim3((unsigned)p.grid), p.threads,
+                        p.smem > columns ? p.smem : columns, s, a, r);
 }
 
 template <bool BF16, bool IN>
@@ -831,17 +841,8 @@ cudaError_t norm_backward_of(const NormBackwardArgs &a, cudaStream_t s)
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && a.dweight) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute early;
-        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        early.val.programmaticStreamSerializationAllowed = 1;
-        cfg.gridDim = dim3((unsigned)((a.N + 31) / 32), 1, 1);
-        cfg.blockDim = dim3(1024, 1, 1);
-        cfg.stream = s;
-        cfg.attrs = &early;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, norm_join_kernel, (const float *)a.partial, parts, a.N, a.dweight, a.grad_f32,
-                               (int)BF16, a.accumulate);
+        e = launch_early(norm_join_kernel, dim3((unsigned)((a.N + 31) / 32)), 1024, 0, s, (const float *)a.partial, parts,
+                         a.N, a.dweight, a.grad_f32, (int)BF16, a.accumulate);
     }
     return e;
 }
@@ -853,13 +854,9 @@ cudaError_t unpack_of(const UnpackArgs &a, cudaStream_t s)
     const int64_t total = a.M * (wide ? (a.N + 7) / 8 : a.N);
     const int grid = (int)gg_min64((total + 256 * kSteps - 1) / (256 * kSteps), 1 << 17);
     const bool small = total < 1ll << 30;  // the last step does not overflow
-    if (wide && small)
-        unpack_kernel<BF16, 8, int><<<grid, 256, 0, s>>>(a);
-    else if (wide)
-        unpack_kernel<BF16, 8, int64_t><<<grid, 256, 0, s>>>(a);
-    else
-        unpack_kernel<BF16, 1, int64_t><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(wide ? (small ? unpack_kernel<BF16, 8, int> : unpack_kernel<BF16, 8, int64_t>)
+                             : unpack_kernel<BF16, 1, int64_t>,
+                        dim3((unsigned)grid), 256, 0, s, a);
 }
 
 template <bool BF16>
@@ -867,10 +864,8 @@ cudaError_t pack_of(const PackArgs &a, cudaStream_t s)
 {
     const int64_t blocks = a.M * ((a.N + kPackBlock - 1) / kPackBlock);
     if (on16(a.x, a.ldx) && on8(a.codes, a.ldc))
-        pack_kernel<BF16><<<(int)gg_min64((blocks + 31) / 32, kSMs * 8), 256, 0, s>>>(a);
-    else
-        pack_any_kernel<BF16><<<(int)gg_min64((blocks + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
-    return cudaGetLastError();
+        return launch_early(pack_kernel<BF16>, dim3((unsigned)gg_min64((blocks + 31) / 32, kSMs * 8)), 256, 0, s, a);
+    return launch_early(pack_any_kernel<BF16>, dim3((unsigned)gg_min64((blocks + 7) / 8, kSMs * 8)), 256, 0, s, a);
 }
 
 }  // namespace
