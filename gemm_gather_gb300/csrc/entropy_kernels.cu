@@ -15,9 +15,10 @@
 // 5. dx_kernel rounds dX once, in the tokens' own order, zeros for the masked ones.
 //
 // Logits are multiplied twice (8 T V K operations instead of 6) so that they need not be kept, nor rounded
-// to 16 bits before the softmax.  dZ is the only 16-bit step: weights enter it times a power of two that
-// takes the largest into [2^13, 2^14), which keeps probabilities down to 2^-27 at float16's full
-// precision whatever the weights' size, and leaves dX and dW again in float32.
+// to 16 bits before the softmax.  dZ is the only 16-bit step: weights enter it relative to the largest, which
+// counts 2^13, and dX and dW are taken back in float32.  That keeps probabilities down to 2^-27 at float16's
+// full precision whatever the weights' size; and where all weights are equal, as most often, the targets' terms,
+// -8192 (1 - p), lose next to nothing (a weight of 1 / 10 would be off by 2^-10 in all of them alike).
 //
 // Bound: the tensor cores, under the power limit.
 #include <cuda_runtime.h>
@@ -180,13 +181,12 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
     for (int d = 16; d > 0; d >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     if (lane == 0) {
-        const int e = top > 0.0f ? ilogbf(top) : 13;
-        const int k = 13 - e < -100 ? -100 : (13 - e > 100 ? 100 : 13 - e);
+        top = top > 0x1p-100f ? top : (top > 0.0f ? 0x1p-100f : 1.0f);
         a.head->live = n;
         a.head->live_pad = (int)pad;
         a.head->ticket = 0;
-        a.head->scale = power_of_two(k);
-        a.head->alpha = a.grad_scale * power_of_two(-k);
+        a.head->scale = 8192.0f / top;
+        a.head->alpha = a.grad_scale * (top * 0x1p-13f);
     }
 }
 
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 // The kept exponentials exp(z - top) of a piece to the gradient of its logits, in place:
-// coef (exp(top - lse) of it - (v is the target)), rounded a second time.  A block takes 32 tokens and 1024
+// coef (exp(top - lse) of it - (v is the target)), from the 16 bits of kept_code to the layer's type.  A block takes 32 tokens and 1024
 // entries, whose 32 x 32 factors it makes once.  Bound: a read and a write of the piece, from L2 as far as it
 // stayed there.
 template <bool BF16>
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) kept_kernel(const __grid_constant__ Entro
             float f = 0.0f;
             if (p0 + lane < live && c0 + g * 32 < a.kept_n) {
                 const float top = a.kept_top[(c0 / 32 + g) * a.T + p0 + lane];
-                f = ex2_approx((top - a.lsec[p0 + lane]) * 1.44269504f) * a.coef[p0 + lane] * (BF16 ? 1.0f : 0x1p-15f);
+                f = ex2_approx((top - a.lsec[p0 + lane]) * 1.44269504f) * a.coef[p0 + lane];
             }
             factor[lane][g] = f;
         }
@@ -365,8 +365,7 @@ __global__ void __launch_bounds__(256) kept_kernel(const __grid_constant__ Entro
                     const bool here = target >= c && target < c + 8;
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        float2 v = pair16<BF16>(w[u]);
-                        v.x *= f, v.y *= f;
+                        float2 v = make_float2(kept_value(w[u] & 0xffffu) * f, kept_value(w[u] >> 16) * f);
                         if (here && target == c + 2 * u)
                             v.x -= coef;
                         if (here && target == c + 2 * u + 1)

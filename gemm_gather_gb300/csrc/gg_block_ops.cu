@@ -568,7 +568,7 @@ gg_status gg_unpack8(const void *codes, int64_t ldc, const float *scales, int64_
     if (M == 0 || N == 0)
         return op_ok();
     const UnpackArgs a{reinterpret_cast<const uint8_t *>(codes), ldc, scales, lds, (int)act, out, ldo, M, N,
-                       dtype == GG_BF16};
+                       dtype == GG_BF16, nullptr};
     const cudaError_t e = launch_unpack(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? op_ok() : op_cuda_fail(e, "unpacking activations");
 }

@@ -223,17 +223,23 @@ gg_status run_backward(Backward *b, int *dev_status, gg_stream_t stream)
     return op_ok();
 }
 
-// Device bytes of gg_linear_backward8: X in 16 bits, rows on 16-byte boundaries.
+// Device bytes of gg_linear_backward8: X in 16 bits, and what that rounding left of it, rows on 16-byte
+// boundaries.
 int64_t unpacked_pitch(int64_t K) { return (K + 7) / 8 * 8; }
+uint64_t unpacked_bytes(int64_t M, int64_t K) { return 2 * (uint64_t)M * (uint64_t)unpacked_pitch(K) * 2; }
+
+// Whether act(P) needs more than 16 bits where float32 is to come of it: P itself and max(P, 0) do not.
+bool smooth(gg_activation act) { return act != GG_ACT_NONE && act != GG_ACT_RELU; }
 
 // Validation of gg_linear_backward8: the plan of gg_linear_backward on the unpacked X, with z_in read
-// from the codes.  *u: what unpacks X (M == 0 where nothing reads it).
+// from the codes.  *u: what unpacks X (M == 0 where nothing reads it); *rest: the product that adds what X's
+// rounding to 16 bits left (J == 0: none).
 gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int64_t ldc, const float *scales,
                             int64_t lds, gg_activation act, const void *W, int64_t ldw, gg_weight_layout layout,
                             const void *dX, int64_t lddx, const void *dW, int64_t lddw, const void *dbias,
                             gg_dtype grad_dtype, int accumulate, const void *workspace, uint64_t workspace_bytes,
                             int64_t M, int64_t N, int64_t K, gg_dtype dtype, gg_linear_path path, Backward *out,
-                            gg::UnpackArgs *u)
+                            gg::UnpackArgs *u, gg::LinearArgs *rest)
 {
     GG_TRY(check_types(dtype, act, "linear_backward8"));
     GG_TRY(check_sizes(M, N, K));
@@ -245,9 +251,9 @@ gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int
     GG_TRY(check_mat(c, true));
     GG_TRY(check_mat(sc, true));
     const int64_t ldx = unpacked_pitch(K);
-    const Mat ws{"workspace", workspace, unpacks ? M : 0, ldx, ldx, 2};
-    if (unpacks && (!workspace || workspace_bytes < (uint64_t)M * (uint64_t)ldx * 2))
-        return op_fail(GG_ERR_INVALID_ARG, "workspace: %lld bytes are needed", (long long)(M * ldx * 2));
+    const Mat ws{"workspace", workspace, unpacks ? 2 * M : 0, ldx, ldx, 2};
+    if (unpacks && (!workspace || workspace_bytes < unpacked_bytes(M, K)))
+        return op_fail(GG_ERR_INVALID_ARG, "workspace: %llu bytes are needed", (unsigned long long)unpacked_bytes(M, K));
     Backward r;
     // the workspace is checked as X is: 16-byte aligned, apart from the outputs
     GG_TRY(prepare_backward(dZ, lddz, unpacks ? workspace : nullptr, ldx, W, ldw, layout, nullptr, 0, act, dX, lddx,
@@ -260,6 +266,8 @@ gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int
             GG_TRY(check_apart(*o, *in));
         GG_TRY(check_apart(ws, *in));
     }
+    for (const Mat *o : {&gx, &gw, &gb})
+        GG_TRY(check_apart(*o, ws));
     const Mat dz{"dZ", dZ, M, N, lddz, 2}, w{"W", W, r.run_dx ? (kn ? K : N) : 0, kn ? N : K, ldw, 2};
     GG_TRY(check_apart(ws, dz));
     GG_TRY(check_apart(ws, w));
@@ -269,8 +277,17 @@ gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int
     r.dx.scales = scales;
     r.dx.lds = lds;
     *out = r;
-    *u = gg::UnpackArgs{reinterpret_cast<const uint8_t *>(codes), ldc, scales, lds, (int)act,
-                        const_cast<void *>(workspace), ldx, unpacks ? M : 0, K, dtype == GG_BF16};
+    // Float32 gradients are those of act(P), not of its rounding: X goes through the product in two parts
+    const bool two = unpacks && grad_dtype == GG_F32 && smooth(act);
+    uint16_t *const x16 = reinterpret_cast<uint16_t *>(const_cast<void *>(workspace));
+    *rest = gg::LinearArgs{};
+    if (two) {
+        *rest = r.dw;
+        (kn ? rest->b : rest->a) = x16 + M * ldx;
+        rest->accumulate = 1;
+    }
+    *u = gg::UnpackArgs{reinterpret_cast<const uint8_t *>(codes), ldc, scales, lds, (int)act, x16, ldx,
+                        unpacks ? M : 0, K, dtype == GG_BF16, two ? x16 + M * ldx : nullptr};
     return op_ok();
 }
 
@@ -530,14 +547,16 @@ gg_status gg_linear_backward8(const void *dZ, int64_t lddz, const void *codes, i
 {
     Backward b;
     gg::UnpackArgs u;
+    gg::LinearArgs rest;
     GG_TRY(prepare_backward8(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx, dW, lddw, dbias,
-                             grad_dtype, accumulate, workspace, workspace_bytes, M, N, K, dtype, path, &b, &u));
+                             grad_dtype, accumulate, workspace, workspace_bytes, M, N, K, dtype, path, &b, &u, &rest));
     if (u.M > 0) {
         const cudaError_t e = gg::launch_unpack(u, reinterpret_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)
             return op_cuda_fail(e, "unpacking the activations");
     }
-    return run_backward(&b, dev_status, stream);
+    GG_TRY(run_backward(&b, dev_status, stream));
+    return run_product(gg::kEpiGradW, &rest, gg::plan_linear(gg::kEpiGradW, rest, path), dev_status, stream);
 }
 
 gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *codes, int64_t ldc,
@@ -550,9 +569,10 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
 {
     Backward b{};
     gg::UnpackArgs u;
+    gg::LinearArgs rest;
     const gg_status st = prepare_backward8(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx, dW,
                                            lddw, dbias, grad_dtype, accumulate, workspace, workspace_bytes, M, N,
-                                           K, dtype, path, &b, &u);
+                                           K, dtype, path, &b, &u, &rest);
     if (chosen_dx)
         *chosen_dx = b.plan_dx.kernel;
     if (chosen_dw)
@@ -562,7 +582,7 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
 
 uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K)
 {
-    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? (uint64_t)M * (uint64_t)unpacked_pitch(K) * 2 : 0;
+    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? unpacked_bytes(M, K) : 0;
 }
 
 gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz, void *dz,

@@ -168,6 +168,7 @@ struct UnpackArgs {
     void *out;
     int64_t ldo, M, N;
     int is_bf16;
+    void *rest;  // or null: what out's rounding left, rounded (pitch ldo)
 };
 cudaError_t launch_unpack(const UnpackArgs &a, cudaStream_t s);
 
@@ -176,7 +177,7 @@ cudaError_t launch_unpack(const UnpackArgs &a, cudaStream_t s);
 struct EntropyHead {
     int live, live_pad;  // tokens that count; the same in whole k-blocks of 64, at most T
     unsigned ticket;     // blocks of the join that are done
-    float scale;         // power of two that takes the largest |weight| to [2^13, 2^14)
+    float scale;         // takes the largest |weight| to 2^13
     float alpha;         // grad_scale / scale
 };
 

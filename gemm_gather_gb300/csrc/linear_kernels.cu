@@ -953,8 +953,7 @@ __device__ __forceinline__ void log_sums(const LinearArgs &a, const Place &at, i
     }
     if (a.kept && i0 >= a.kept0 && i0 < a.I) {
         // the last piece's exponentials, from the largest of each 32: the gradient of its logits needs no
-        // second product.  float16 holds them times 2^15.
-        const float up = a.is_bf16 ? 0.0f : 15.0f;
+        // second product
 #pragma unroll
         for (int g = 0; g < kCols; g += kStageCols) {
             const int64_t jg = j0 + column(g);
@@ -966,7 +965,7 @@ __device__ __forceinline__ void log_sums(const LinearArgs &a, const Place &at, i
                 if (c >= n)
                     continue;
                 const float m = own[(g + c) / 16].x;
-                const float from = (m == -INFINITY ? 0.0f : m) * kLog2e - up;
+                const float from = (m == -INFINITY ? 0.0f : m) * kLog2e;
                 if (lane < 16 && c + lane < n)
                     a.kept_top[(i0 - a.kept0) / 32 * a.ldpartial + jg + c + lane] = m;
                 float v[16];
@@ -974,7 +973,9 @@ __device__ __forceinline__ void log_sums(const LinearArgs &a, const Place &at, i
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
                     v[u] = ex2_approx(fmaf(v[u], kLog2e, -__shfl_sync(0xffffffffu, from, u)));
-                stage16(a, v, at.stage_buf, lane, c);
+#pragma unroll
+                for (int u = 0; u < 16; u += 2)
+                    *staged(at.stage_buf, lane, c + u) = kept_code(v[u]) | kept_code(v[u + 1]) << 16;
             }
             write_rows(rows_of(a.kept, a.ldkept), a.I - a.kept0, i0 - a.kept0, jg, n, lane, at.stage_buf);
         }
@@ -1069,7 +1070,14 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                 for (int u = 0; u < 16; ++u)
                     v[u] = __uint_as_float(r[u]);
             };
-            if constexpr (kSums<EPI>) {
+            if (EPI == kEpiLse && h + 1 == chunks) {  // the last chunk straight from TMEM
+                log_sums<kCols>(a, at, i0, j0, end, terms, [&](int col, float(&v)[16]) {
+                    from_tmem(column(col), v);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        v[u] += sum[kSums<EPI> ? col + u : 0];
+                });
+            } else if constexpr (kSums<EPI>) {
 #pragma unroll
                 for (int col = 0; col < kCols; col += 16) {
                     if (valid_rows(end, j0 + column(col)) <= 0)
@@ -1135,13 +1143,7 @@ __device__ __forceinline__ bool finish(const LinearArgs &a, const Product &p, Pl
                 }
             }
         }
-        if constexpr (EPI == kEpiLse) {
-            log_sums<kCols>(a, at, i0, j0, end, terms, [&](int col, float(&v)[16]) {
-#pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    v[u] = sum[col + u];
-            });
-        } else if constexpr (kSums<EPI>) {
+        if constexpr (kSums<EPI> && EPI != kEpiLse) {
             if (at.parts > 1) {
 #pragma unroll
                 for (int u = 0; u < kCols; ++u)
@@ -2035,9 +2037,10 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
     return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }
 
-// Logits of longer contractions are summed in chunks for lse, whose tiles hide that: truncation costs 2e-6 of a
-// logit at 2048, and grows with the length.
-constexpr int64_t kPlainLse = 2048;
+// Logits of longer contractions are summed in chunks for lse, whose tiles hide that (100003 entries, 4096
+// tokens, K = 1024: 570 us in chunks, 460 without): losses are off by 4.5e-7 of them at 1024, and without
+// chunks by 1.1e-6 at 2011.
+constexpr int64_t kPlainLse = 1024;
 
 // Whether a sum over many tokens is over so few that it is one chunk: 64 sums a thread leave the epilogue
 // too few registers, which the products of a long contraction hide and those of a short one do not (the
@@ -2286,7 +2289,9 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
         return cudaErrorNotSupported;
     }
     LinearArgs a = args;
-    a.chunk = epi == kEpiGradW || epi == kEpiVocab || (epi == kEpiLse && a.K > kPlainLse) ? kChunk : 1 << 30;
+    a.chunk = epi == kEpiGradW || epi == kEpiVocab ? kChunk : 1 << 30;
+    if (epi == kEpiLse && a.K > kPlainLse)
+        a.chunk = (int)(kPlainLse / kBK);
     switch (epi) {
     case kEpiForward: return launch_epi<kEpiForward>(a, p, s, why);
     case kEpiGradIn: return launch_epi<kEpiGradIn>(a, p, s, why);

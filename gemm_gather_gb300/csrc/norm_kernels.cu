@@ -689,11 +689,26 @@ __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unp
             values8<BF16>(c[k], scale[k], v);
             if (a.act != GG_ACT_NONE)
                 with_act(a.act, [&](auto f) { apply_act<decltype(f)::value>(v); });
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                w[u] = pair16_of<BF16>(v[2 * u], v[2 * u + 1]);
             if (V == 8)
-                store8(out[k], left[k], make_uint4(pair16_of<BF16>(v[0], v[1]), pair16_of<BF16>(v[2], v[3]),
-                                                   pair16_of<BF16>(v[4], v[5]), pair16_of<BF16>(v[6], v[7])));
+                store8(out[k], left[k], make_uint4(w[0], w[1], w[2], w[3]));
             else
-                store16(out[k], 0, v[0], BF16);
+                *out[k] = (uint16_t)w[0];
+            if (a.rest) {
+                uint16_t *rest = reinterpret_cast<uint16_t *>(a.rest) + (out[k] - reinterpret_cast<uint16_t *>(a.out));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float2 f = pair16<BF16>(w[u]);
+                    w[u] = pair16_of<BF16>(v[2 * u] - f.x, v[2 * u + 1] - f.y);
+                }
+                if (V == 8)
+                    store8(rest, left[k], make_uint4(w[0], w[1], w[2], w[3]));
+                else
+                    *rest = (uint16_t)w[0];
+            }
         }
     }
 }

@@ -112,6 +112,19 @@ __device__ __forceinline__ void values8(const uint2 &codes, float scale, float (
     }
 }
 
+// An exponential between 0 and 1 in 16 bits: five of exponent and eleven of mantissa, to nearest (half a step is
+// 2^-12 of it, an eighth of bfloat16's and half of float16's); below 2^-31 it is 0.
+__device__ __forceinline__ uint32_t kept_code(float e)
+{
+    const uint32_t code = (__float_as_uint(e) + 0x800u) >> 12;
+    return min(max(code, 96u << 11) - (96u << 11), 0xffffu);
+}
+
+__device__ __forceinline__ float kept_value(uint32_t code)
+{
+    return code == 0 ? 0.0f : __uint_as_float((code + (96u << 11)) << 12);
+}
+
 // Eight neighbouring elements of a row, of which `left` exist; the others are zero and not read.
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int64_t left)
 {

@@ -557,11 +557,12 @@ gg_status gg_unpack8(const void *codes, int64_t ldc, const float *scales, int64_
  * GG_ACT_NONE the packed input itself (a norm's codes):
  *   dX = (dZ W^T) act'(P), dW (+)= act(P)^T dZ, dbias (+)= the column sums of dZ.
  * P is taken in `dtype` (as gg_unpack8 with GG_ACT_NONE gives it) for act', and X as
- * gg_unpack8 gives it.  Types, layouts, alignment, accumulation and errors as for
+ * gg_unpack8 gives it; for a float32 dW of a smooth activation what X's rounding left is
+ * multiplied as well (a product more), so that dW is act(P)'s and not its rounding's.  Types, layouts, alignment, accumulation and errors as for
  * gg_linear_backward; codes and scales may have any alignment and pitch.
  * workspace: device memory, 16-byte aligned, of at least
- * gg_linear_backward8_workspace(M, K) bytes where dW is asked for (X in 16 bits), else
- * not used.  What it held is lost; calls that may run at the same time, or replays of
+ * gg_linear_backward8_workspace(M, K) bytes where dW is asked for (X in 16 bits, and the
+ * rest), else not used.  What it held is lost; calls that may run at the same time, or replays of
  * graphs that captured them, need workspaces of their own.
  * ------------------------------------------------------------------------- */
 uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K);
@@ -720,8 +721,8 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * (dev_status, or the library's when NULL) and its token counts as masked.  Logits of
  * -inf are entries of probability 0; a row of nothing else, or one with NaN or +inf,
  * gives NaN.  Sums, softmax and both gradients' sums are float32; dZ is multiplied in
- * `dtype`, for which weights are scaled by a power of two (so that their size
- * does not matter to float16); logits are computed twice.
+ * `dtype`, with weights relative to the largest (so that their size does not matter to
+ * float16); logits of all pieces but one are computed twice.
  * The gradients go through the vocabulary in pieces: `piece` entries (a multiple of
  * 128) at a time, 0 for the library's choice (equal pieces of at most 32768).  The
  * values differ by the order of float32 sums only.

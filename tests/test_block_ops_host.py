@@ -115,7 +115,7 @@ def packed(**kw):
 
 
 def test_linear_backward8_accepts():
-    assert gg.linear_backward8_workspace(100, 500) == 100 * 504 * 2 and gg.linear_backward8_workspace(0, 5) == 0
+    assert gg.linear_backward8_workspace(100, 500) == 2 * 100 * 504 * 2 and gg.linear_backward8_workspace(0, 5) == 0
     assert packed() == ("pair", "pair") and packed(path="split") == ("split", "split")
     assert packed(dX=None, W=None, path="split") == ("none", "split")
     assert packed(dW=None, ws=None, ws_bytes=0, path="pair") == ("pair", "none")
@@ -133,7 +133,7 @@ def test_linear_backward8_accepts():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=F32), UNSUP), (dict(gdt=F16), UNSUP), (dict(K=-1), INVALID), (dict(dZ=None), INVALID), (dict(W=None), INVALID),
-    (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=100 * 504 * 2 - 1), INVALID),
+    (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=2 * 100 * 504 * 2 - 1), INVALID),
     (dict(ws=at(7) + 8), ALIGN), (dict(lddz=201), ALIGN), (dict(W=at(3) + 2), ALIGN), (dict(ldc=499), INVALID),
     (dict(lds=3), INVALID), (dict(scales=at(2) + 2), ALIGN), (dict(dX=at(1)), INVALID), (dict(dW=at(2)), INVALID),
     (dict(db=at(1) + 40), INVALID), (dict(ws=at(1)), INVALID), (dict(ws=at(2)), INVALID), (dict(ws=at(0)), INVALID),

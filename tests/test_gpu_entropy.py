@@ -4,8 +4,8 @@ Bounds, from the arithmetic: a logit is a float32 sum over K, off by bz = K 2^-2
 covers an accumulator that truncates); its exponential's argument is a difference times log2 e, (|z - lse| + 1)
 2^-22; so lse is off by the largest bz and 2^-20 + |lse| 2^-23, the loss by twice that.  A probability is
 off by the factor d = bz + d(lse) + (|z - lse| + 4) 2^-22.  dZ adds its rounding to 16 bits (half a step, and
-float16's least step of 2^-24 at weights whose largest lies in [2^13, 2^14)), twice in the piece whose
-exponentials were kept; dX and dW are sums of dZ's errors times the other operand, a float32 sum's own bound,
+float16's least step of 2^-24 at a largest weight of 2^13); in the piece whose exponentials
+were kept these are off by 2^-12 before, and 0 from 2^-31 of the largest of 32 on; dX and dW are sums of dZ's errors times the other operand, a float32 sum's own bound,
 and half an ulp of the output.
 """
 import math
@@ -79,8 +79,9 @@ class Case:
         coef = (tw * grad_scale)[:, None]
         dz = coef * (p - hot)
         d = bz + dl[:, None] + ((z - lse[:, None]).abs() + 4) * 2.0 ** -22
-        half = 2 * 2.0 ** (-11 if dt is F16 else -8)
+        half = 2.0 ** (-11 if dt is F16 else -8) + 2.0 ** -12
         least = float(coef.abs().max()) * 2.0 ** -37 if dt is F16 else 0.0
+        least = least + coef.abs() * p.amax(1, keepdim=True) * 2.0 ** -31
         err = coef.abs() * (p * torch.expm1(d) + 2.0 ** -23) + dz.abs() * half + least
         dx = self.dx if dx is None else dx
         if dx is not None:
