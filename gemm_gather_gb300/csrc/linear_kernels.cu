@@ -139,7 +139,8 @@ struct TokenTerms {
 __device__ __forceinline__ float soft_grad(float z, int64_t i, const TokenTerms &t)
 {
     const float p = ex2_approx((z - t.lse) * kLog2e);
-    return ((int)i == t.target ? p - 1.0f : p) * t.coef;
+    // (what rows of zeros fill a k-block up with is 0, whatever W holds)
+    return t.coef != 0.0f ? ((int)i == t.target ? p - 1.0f : p) * t.coef : 0.0f;
 }
 
 // (largest z, sum of exp(z - largest)) of a warp's 32 vocabulary entries, for each of n columns: a row of

@@ -423,7 +423,8 @@ gg_status gg_matmul_all_gather_check(const gg_heap *heap, int rank, const void *
  * allocate nothing, keep nothing between calls and give the same bits for the
  * same inputs, sizes, pitches and path, wherever these lie in memory (the policy
  * loss: wherever the logits lie at the same offset from a 16-byte boundary, at
- * which it starts its vectors).  Matrices are row-major with a row pitch (ld) in
+ * which it starts its vectors; the norm and its gradients: wherever their rows are, or
+ * are not, aligned for the fast case).  Matrices are row-major with a row pitch (ld) in
  * elements.
  * Sums and statistics are held in float32.  Sizes must be below 2^31 each;
  * offsets are 64-bit.  An output may overlap no other argument's elements,
@@ -622,8 +623,7 @@ gg_status gg_rms_norm_check(const void *x, int64_t ldx, const void *residual, in
  * dh_in (M x N or NULL) is what reaches h along the residual, so dh is the
  * gradient of x and of the residual.  dh and dweight may each be NULL; dh may be dy, h
  * or dh_in (same pointer and pitch).  accumulate != 0 adds to what dweight holds.  The
- * sums over rows are float32, in an order fixed by M, N, the pitches and whether rows
- * are 16-byte aligned.  M == 0 gives zero sums.
+ * sums over rows are float32.  M == 0 gives zero sums.
  * workspace: 4-byte aligned device memory of at least
  * gg_rms_norm_backward_workspace(M, N) bytes where dweight is asked for, else not used.
  * What it held is lost; calls that may run at the same time, or replays of graphs that
