@@ -184,6 +184,12 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
         top = top > 0x1p-100f ? top : (top > 0.0f ? 0x1p-100f : 1.0f);
         a.head->live = n;
         a.head->live_pad = (int)pad;
+        // a tile of dX is to be at most half of what a CTA pair has to do, but 16 k-blocks; dW's tiles are nine
+        // k-blocks' time at least
+        const int64_t dx = (int64_t)a.dx_tiles_i * ((n + a.dx_bt - 1) / a.dx_bt) * a.dx_kb;
+        const int64_t all = dx + a.dw_tiles * ((n + kPad - 1) / kPad > 9 ? (n + kPad - 1) / kPad : 9);
+        const int64_t want = gg_min64(a.dx_kb / 16, all > 0 ? (kSMs * (int64_t)a.dx_kb + all - 1) / all : 1);
+        a.head->shares = (int)(want < 1 ? 1 : gg_min64(want, a.most_shares));
         a.head->ticket = 0;
         a.head->scale = 8192.0f / top;
         a.head->alpha = a.grad_scale * (top * 0x1p-13f);
@@ -386,6 +392,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
     wait_dependencies();
     launch_dependents();
     const float alpha = a.head->alpha;
+    const int shares = a.head->shares;
     const int64_t units = (a.K + V - 1) / V, total = a.T * units;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t t = i / units, n = (i - t * units) * V;
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
         const float *from = a.dx32 + p * a.ldw + n;  // (rows of whole 8 elements)
         if constexpr (V == 8) {
             float v[8] = {};
-            for (int s = 0; p >= 0 && s < a.shares; ++s, from += a.T * a.ldw) {
+            for (int s = 0; p >= 0 && s < shares; ++s, from += a.T * a.ldw) {
                 const float4 x = *reinterpret_cast<const float4 *>(from), y = *reinterpret_cast<const float4 *>(from + 4);
                 v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
                 v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ Entropy
                           : make_uint4(0u, 0u, 0u, 0u));
         } else {
             float v = 0.0f;
-            for (int s = 0; p >= 0 && s < a.shares; ++s, from += a.T * a.ldw)
+            for (int s = 0; p >= 0 && s < shares; ++s, from += a.T * a.ldw)
                 v += *from;
             store16(out, 0, v * alpha, BF16);
         }

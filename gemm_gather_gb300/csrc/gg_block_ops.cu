@@ -148,12 +148,15 @@ bool pairs_only(int64_t T, int64_t K) { return T > 512 && K > 0; }
 
 int64_t partial_rows(int64_t V, bool pairs) { return pairs ? (V + 127) / 128 : (V + 31) / 32; }
 
-// Shares of dX's contraction (plan_vocab): only where a wave of the 76 CTA pairs has room for more
-// than its tiles of 256 x 256.
+// Shares of dX's contraction that there is room for (plan_vocab): few tokens that count leave most CTA pairs
+// without a tile of dX otherwise.  A share is dX in float32; they may take a quarter of a gigabyte.
 int most_shares(int64_t T, int64_t K)
 {
-    const int64_t tiles = ((T + 255) / 256) * ((K + 255) / 256);
-    return tiles >= 76 ? 1 : (tiles >= 38 ? 4 : 8);
+    const uint64_t one = (uint64_t)T * (uint64_t)((K + 7) / 8 * 8) * 4;
+    for (int s = 8; s > 1; s /= 2)
+        if (one <= ((uint64_t)1 << 28) / (uint64_t)s)
+            return s;
+    return 1;
 }
 
 // The workspace's parts, one behind the other on 256-byte boundaries.
@@ -319,8 +322,6 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
     l.status = a.status;
     l.wait_limit_ns = op_wait_limit_ns();
     l.inject_stall = op_inject_stall();
-    l.shares = 1;
-    a.shares = 1;
     if (a.T == 0) {
         if (a.stats)
             GG_TRY(launched(cudaMemsetAsync(a.stats, 0, 8, s), "clearing the statistics"));
@@ -354,43 +355,11 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         z.v0 = (int)v0;
         return z;
     };
-    GG_TRY(launched(launch_entropy_tokens(a, s), "gathering the tokens"));
-    LinearArgs z = logits(0, a.V, &a.head->live);
-    z.partial = a.partial;
-    z.ldpartial = a.T;
-    z.ztarget = a.ztarget;
-    const LinearPlan plan = plan_linear(kEpiLse, z, pairs_only(a.T, a.K) ? GG_LINEAR_PAIR : GG_LINEAR_AUTO);
-    a.rows = partial_rows(a.V, plan.kernel == GG_LINEAR_PAIR);
     const bool gradients = (a.dX || e.dW) && a.K > 0;
     const int64_t last = (a.V - 1) / a.piece * a.piece;  // the last piece's first entry
-    const bool keeps = gradients && plan.kernel == GG_LINEAR_PAIR && a.K >= kKeepFrom;
-    if (keeps) {
-        a.kept0 = last;
-        a.kept_n = a.V - last;
-        z.kept = a.dz;
-        z.ldkept = a.piece;
-        z.kept0 = last;
-        z.kept_top = const_cast<float *>(a.kept_top);
-    }
-    GG_TRY(product(kEpiLse, z, plan, s));
-    GG_TRY(launched(launch_entropy_join(a, s), "joining the vocabulary's sums"));
-    if (!gradients)
-        return op_ok();
-    bool both = false;
-    int bt_dx = 0, bt_dw = 0;
-    // the last piece first: its logits may still be there
-    for (int64_t v0 = last; v0 >= 0; v0 -= a.piece) {
+    // dX and dW of a piece
+    const auto gradient_of = [&](int64_t v0, LinearArgs *dx, LinearArgs *dw) {
         const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
-        if (v0 == last && keeps) {
-            GG_TRY(launched(launch_entropy_kept(a, s), "the gradient of the kept logits"));
-        } else {
-            z = logits(v0, n, &a.head->live_pad);
-            z.lse = a.lsec;
-            z.coef = a.coef;
-            z.out = a.dz;
-            z.ldo = a.piece;
-            GG_TRY(product(kEpiSoftGrad, z, s));
-        }
         LinearArgs x = l, w = l;
         x.I = a.K;
         x.J = a.T;
@@ -420,13 +389,63 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         w.live = &a.head->live_pad;
         w.live_k = 1;
         w.alpha = &a.head->alpha;
-        if (v0 == last && a.dX && e.dW) {  // (the pieces are alike, and share dX's rows)
-            const double apart =
-                plan_linear(kEpiVocab, x, GG_LINEAR_AUTO).ns + plan_linear(kEpiVocab, w, GG_LINEAR_AUTO).ns;
-            both = plan_vocab(x, w, apart, most_shares(a.T, a.K), &bt_dx, &bt_dw, &a.shares);
+        *dx = x;
+        *dw = w;
+    };
+    // both in one walk of the pairs, or apart: chosen once, since the pieces are alike and share dX's rows
+    LinearArgs x, w;
+    bool both = false;
+    int bt_dx = 0, bt_dw = 0;
+    a.most_shares = 1;
+    a.dx_bt = 1;
+    if (gradients && a.dX && e.dW) {
+        gradient_of(last > 0 ? 0 : last, &x, &w);  // (a whole piece)
+        const double apart = plan_linear(kEpiVocab, x, GG_LINEAR_AUTO).ns + plan_linear(kEpiVocab, w, GG_LINEAR_AUTO).ns;
+        both = plan_vocab(x, w, apart, most_shares(a.T, a.K), &bt_dx, &bt_dw);
+    }
+    if (both) {
+        a.most_shares = most_shares(a.T, a.K);
+        a.dx_tiles_i = (int)((x.I + 255) / 256);
+        a.dx_bt = bt_dx;
+        a.dx_kb = (int)((x.K + 63) / 64);
+        a.dw_tiles = ((w.I + 255) / 256) * ((w.J + bt_dw - 1) / bt_dw);
+    }
+    GG_TRY(launched(launch_entropy_tokens(a, s), "gathering the tokens"));
+    LinearArgs z = logits(0, a.V, &a.head->live);
+    z.partial = a.partial;
+    z.ldpartial = a.T;
+    z.ztarget = a.ztarget;
+    const LinearPlan plan = plan_linear(kEpiLse, z, pairs_only(a.T, a.K) ? GG_LINEAR_PAIR : GG_LINEAR_AUTO);
+    a.rows = partial_rows(a.V, plan.kernel == GG_LINEAR_PAIR);
+    const bool keeps = gradients && plan.kernel == GG_LINEAR_PAIR && a.K >= kKeepFrom;
+    if (keeps) {
+        a.kept0 = last;
+        a.kept_n = a.V - last;
+        z.kept = a.dz;
+        z.ldkept = a.piece;
+        z.kept0 = last;
+        z.kept_top = const_cast<float *>(a.kept_top);
+    }
+    GG_TRY(product(kEpiLse, z, plan, s));
+    GG_TRY(launched(launch_entropy_join(a, s), "joining the vocabulary's sums"));
+    if (!gradients)
+        return op_ok();
+    // the last piece first: its logits may still be there
+    for (int64_t v0 = last; v0 >= 0; v0 -= a.piece) {
+        const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
+        if (v0 == last && keeps) {
+            GG_TRY(launched(launch_entropy_kept(a, s), "the gradient of the kept logits"));
+        } else {
+            z = logits(v0, n, &a.head->live_pad);
+            z.lse = a.lsec;
+            z.coef = a.coef;
+            z.out = a.dz;
+            z.ldo = a.piece;
+            GG_TRY(product(kEpiSoftGrad, z, s));
         }
-        x.shares = a.shares;
+        gradient_of(v0, &x, &w);
         if (both) {
+            x.shares = &a.head->shares;
             const char *why = nullptr;
             const cudaError_t err = launch_both(kEpiVocab, x, bt_dx, w, bt_dw, s, &why);
             GG_TRY(launched(err, why ? why : "launching the gradients of a piece"));

@@ -59,7 +59,7 @@ struct LinearArgs {
     // live_k, K is the most there can be).
     const int *live;
     int live_k;
-    int shares;            // kEpiVocab: of the contraction, share s into rows s J of out (else 1)
+    const int *shares;     // kEpiVocab: of the contraction, share s into rows s J of out (null: 1)
     const int *target;     // a token's, within the vocabulary
     int v0;                // the piece's first entry
     float2 *partial;       // kEpiLse: a row for every 128 entries (split kernel: 32), a place per token
@@ -92,8 +92,7 @@ bool plan_both(const LinearArgs &dx, const LinearArgs &dw, const LinearPlan &pla
                int path, int *bt_dx, int *bt_dw);
 // The same for what the gradient of a piece of logits is multiplied into (kEpiVocab), where it takes less
 // than other_ns.
-bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int most_shares, int *bt_dx, int *bt_dw,
-                int *shares);
+bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int most_shares, int *bt_dx, int *bt_dw);
 cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearArgs &dw, int bt_dw, cudaStream_t s,
                         const char **why);
 
@@ -176,6 +175,7 @@ cudaError_t launch_unpack(const UnpackArgs &a, cudaStream_t s);
 // What the device knows of a call, at the start of its workspace.
 struct EntropyHead {
     int live, live_pad;  // tokens that count; the same in whole k-blocks of 64, at most T
+    int shares;          // of dX's contraction
     unsigned ticket;     // blocks of the join that are done
     float scale;         // takes the largest |weight| to 2^13
     float alpha;         // grad_scale / scale
@@ -208,7 +208,10 @@ struct EntropyArgs {
     const float *kept_top;  // of the piece whose exponentials lie in dz (launch_entropy_kept)
     int64_t kept0, kept_n;
     float *dx32;         // compact dX before its rounding, pitch ldw, a share's T rows behind another's
-    int shares;
+    // What the shares are chosen by: those there is room for; dX's feature tiles, tokens of its tiles and
+    // k-blocks of its contraction; dW's tiles.
+    int most_shares, dx_tiles_i, dx_bt, dx_kb;
+    int64_t dw_tiles;
     int *status;
 };
 cudaError_t launch_entropy_tokens(const EntropyArgs &a, cudaStream_t s);  // counts and gathers the tokens

@@ -760,10 +760,10 @@ struct Product {
     int kb0, num_kb;
     uint32_t total, first;
     Tile tile;  // the first
-    // kLive: the columns and their tiles that the device knows (see columns_of and tiles_of)
+    // kLive: the columns, their tiles and the shares of the contraction that the device knows
     int64_t J;
-    uint32_t tiles_j;
-    __device__ __forceinline__ Product() : kb0(0), num_kb(0), total(0), first(0), tile{}, J(0), tiles_j(0) {}
+    uint32_t tiles_j, shares;
+    __device__ __forceinline__ Product() : kb0(0), num_kb(0), total(0), first(0), tile{}, J(0), tiles_j(0), shares(1) {}
     __device__ __forceinline__ Product(const LinearArgs &a, int part, int parts, uint32_t first_)
         : kb0(0), num_kb(a.num_kb), total((uint32_t)a.tiles_i * (uint32_t)a.tiles_j), first(first_),
           tile(first_ < total ? tile_at(a, (uint32_t)a.tiles_j, first_) : Tile{})
@@ -772,14 +772,15 @@ struct Product {
             share_of(a.num_kb, part, parts, kb0, num_kb);
     }
     // The same with the tokens that the device counted; the launches before have to be waited for.
-    // Where a.shares > 1, every tile comes that many times, with a share of the contraction each.
+    // Where there are shares, every tile comes that many times, with a share of the contraction each.
     __device__ __forceinline__ void count(const LinearArgs &a, int part, int parts)
     {
         const int live = *a.live;
         num_kb = a.live_k ? (live + kBK - 1) / kBK : a.num_kb;
         J = a.live_k ? a.J : (int64_t)live;
         tiles_j = (uint32_t)((J + a.bt - 1) / a.bt);
-        total = (uint32_t)a.tiles_i * tiles_j * (uint32_t)a.shares;
+        shares = a.shares ? (uint32_t)*a.shares : 1u;
+        total = (uint32_t)a.tiles_i * tiles_j * shares;
         if (parts > 1)
             share_of(num_kb, part, parts, kb0, num_kb);
     }
@@ -791,7 +792,7 @@ struct Product {
     }
     __device__ __forceinline__ Tile live_tile(const LinearArgs &a, uint32_t t) const
     {
-        if (a.shares == 1) {
+        if (shares == 1) {
             Tile c = tile_at(a, tiles_j, t);
             c.kb0 = kb0;
             c.num_kb = num_kb;
@@ -800,7 +801,7 @@ struct Product {
         const uint32_t tiles = (uint32_t)a.tiles_i * tiles_j, share = t / tiles;
         Tile c = tile_at(a, tiles_j, t - share * tiles);
         c.share = (int)share;
-        share_of(num_kb, (int)share, a.shares, c.kb0, c.num_kb);
+        share_of(num_kb, (int)share, (int)shares, c.kb0, c.num_kb);
         return c;
     }
 };
@@ -2043,10 +2044,16 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
 // chunks by 1.1e-6 at 2011.
 constexpr int64_t kPlainLse = 1024;
 
-// Whether a sum over many tokens is over so few that it is one chunk: 64 sums a thread leave the epilogue
-// too few registers, which the products of a long contraction hide and those of a short one do not (the
-// 32768 x 2048 gradient of 64 tokens takes 59 us with them and 35 without; of 576, 76 and 57).
-bool one_chunk(const LinearArgs &a) { return a.K <= kChunk * kBK; }
+// Whether a gradient's sum over tokens stays in one chunk: where it is no longer, and where a vocabulary's
+// weight gradient is rounded to 16 bits at the end (truncation costs 2e-5 of it at kPlainTokens, float16's
+// half step is 2.4e-4).  64 sums a thread leave the epilogue too few registers, which the products of a long
+// contraction hide and those of a short one do not: the 32768 x 2048 gradient of 64 tokens takes 59 us with
+// them and 35 without, of 576, 76 and 57.
+constexpr int64_t kPlainTokens = 16384;
+bool one_chunk(int epi, const LinearArgs &a)
+{
+    return a.K <= kChunk * kBK || (epi == kEpiVocab && a.live_k && !a.out_f32 && a.K <= kPlainTokens);
+}
 
 template <int EPI>
 cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s, const char **why)
@@ -2060,7 +2067,7 @@ cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s,
         if constexpr (EPI == kEpiGradW || EPI == kEpiVocab || EPI == kEpiLse) {
             constexpr int kBrief =
                 EPI == kEpiGradW ? kEpiGradWShort : (EPI == kEpiVocab ? kEpiVocabShort : kEpiLseShort);
-            if (EPI == kEpiLse ? a.K <= kPlainLse : one_chunk(a))
+            if (EPI == kEpiLse ? a.K <= kPlainLse : one_chunk(EPI, a))
                 return p.bt > 128 ? launch_pair<kBrief, -1, 256>(a, p.bt, p.split, nullptr, 0, s, why)
                                   : launch_pair<kBrief, -1, 128>(a, p.bt, p.split, nullptr, 0, s, why);
         }
@@ -2214,12 +2221,11 @@ static cudaError_t launch_both_of(const LinearArgs &x, int bt_dx, const LinearAr
 
 // The products that the gradient of a piece's logits goes into, in one walk of the pairs: dX's tiles are few
 // and long (its contraction is the piece), dW's many and short.  A pair with one long tile more than the others
-// would end long after them, so a long contraction is dealt out in shares (up to most_shares), each into
-// float32 rows of its own; the walk deals tiles in turn, so three pairs show the last to end.  Tiles whose
-// contraction is shorter than their epilogue take the epilogue's time.  777 tokens, V = 32768, K = 2011: one
-// share 196 us, see the table of the design for now.
-bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int most_shares, int *bt_dx, int *bt_dw,
-                int *shares)
+// would end long after them, so a long contraction is dealt out in shares (up to most_shares; how many, the
+// device decides when it has counted the tokens), each into float32 rows of its own; the walk deals tiles in
+// turn, so three pairs show the last to end.  Tiles whose contraction is shorter than their epilogue take the
+// epilogue's time.  777 tokens, 544 of which count, V = 32768, K = 2011: 160 us in one share, 123 in four.
+bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int most_shares, int *bt_dx, int *bt_dw)
 {
     const auto tiles = [](const LinearArgs &x, int bt) { return ((x.I + 255) / 256) * ((x.J + bt - 1) / bt); };
     const auto tile_ns = [](double kbs, double kb_ns, int bt) {
@@ -2249,7 +2255,6 @@ bool plan_vocab(const LinearArgs &dx, const LinearArgs &dw, double other_ns, int
                     least = ns;
                     *bt_dx = b0;
                     *bt_dw = b1;
-                    *shares = s;
                     found = true;
                 }
             }
@@ -2264,9 +2269,9 @@ cudaError_t launch_both(int epi, const LinearArgs &dx, int bt_dx, const LinearAr
         return cudaErrorNotSupported;
     }
     LinearArgs x = dx, w = dw;
+    const bool brief = one_chunk(epi == kEpiVocab ? kEpiVocab : kEpiGradW, w);
     x.chunk = epi == kEpiVocab ? kChunk : 1 << 30;
-    w.chunk = kChunk;
-    const bool brief = one_chunk(w);
+    w.chunk = brief ? 1 << 30 : kChunk;
     switch (epi) {
     case kEpiVocab:
         return brief ? launch_both_of<kEpiVocab, kEpiVocabShort>(x, bt_dx, w, bt_dw, s, why)
@@ -2290,7 +2295,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
         return cudaErrorNotSupported;
     }
     LinearArgs a = args;
-    a.chunk = epi == kEpiGradW || epi == kEpiVocab ? kChunk : 1 << 30;
+    a.chunk = (epi == kEpiGradW || epi == kEpiVocab) && !one_chunk(epi, a) ? kChunk : 1 << 30;
     if (epi == kEpiLse && a.K > kPlainLse)
         a.chunk = (int)(kPlainLse / kBK);
     switch (epi) {
