@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 // entries, whose 32 x 32 factors it makes once.  Bound: a read and a write of the piece, from L2 as far as it
 // stayed there.
 template <bool BF16>
-__global__ void __launch_bounds__(256) kept_kernel(const __grid_constant__ EntropyArgs a)
+__global__ void __launch_bounds__(256, 4) kept_kernel(const __grid_constant__ EntropyArgs a)
 {
     __shared__ float factor[32][33];
     wait_dependencies();

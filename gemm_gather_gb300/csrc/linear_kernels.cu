@@ -2039,10 +2039,12 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
     return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }
 
-// Logits of longer contractions are summed in chunks for lse, whose tiles hide that (100003 entries, 4096
-// tokens, K = 1024: 570 us in chunks, 460 without): losses are off by 4.5e-7 of them at 1024, and without
-// chunks by 1.1e-6 at 2011.
-constexpr int64_t kPlainLse = 1024;
+// Logits of longer contractions than kPlainLse are summed in chunks for lse: without them losses are off by
+// 4.5e-7 of their size at 1024 and 1.1e-6 at 2011, and that grows with the length.  In registers the sums of chunks
+// spill, which only tiles of long contractions hide: 4096 tokens, 100003 entries, K = 1024 take 570 us with and 460
+// without, 777 tokens, 32768 entries, K = 2011 100 and 65.
+constexpr int64_t kPlainLse = 1792;
+constexpr int kLseChunk = 16;  // k-blocks
 
 // Whether a gradient's sum over tokens stays in one chunk: where it is no longer, and where a vocabulary's
 // weight gradient is rounded to 16 bits at the end (truncation costs 2e-5 of it at kPlainTokens, float16's
@@ -2297,7 +2299,7 @@ cudaError_t launch_linear(int epi, const LinearArgs &args, const LinearPlan &p, 
     LinearArgs a = args;
     a.chunk = (epi == kEpiGradW || epi == kEpiVocab) && !one_chunk(epi, a) ? kChunk : 1 << 30;
     if (epi == kEpiLse && a.K > kPlainLse)
-        a.chunk = (int)(kPlainLse / kBK);
+        a.chunk = kLseChunk;
     switch (epi) {
     case kEpiForward: return launch_epi<kEpiForward>(a, p, s, why);
     case kEpiGradIn: return launch_epi<kEpiGradIn>(a, p, s, why);
