@@ -184,11 +184,11 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
         top = top > 0x1p-100f ? top : (top > 0.0f ? 0x1p-100f : 1.0f);
         a.head->live = n;
         a.head->live_pad = (int)pad;
-        // a tile of dX is to be at most half of what a CTA pair has to do, but 16 k-blocks; dW's tiles are nine
+        // a tile of dX is to be at most a quarter of what a CTA pair has to do, but 16 k-blocks; dW's tiles are nine
         // k-blocks' time at least
         const int64_t dx = (int64_t)a.dx_tiles_i * ((n + a.dx_bt - 1) / a.dx_bt) * a.dx_kb;
         const int64_t all = dx + a.dw_tiles * ((n + kPad - 1) / kPad > 9 ? (n + kPad - 1) / kPad : 9);
-        const int64_t want = gg_min64(a.dx_kb / 16, all > 0 ? (kSMs * (int64_t)a.dx_kb + all - 1) / all : 1);
+        const int64_t want = gg_min64(a.dx_kb / 16, all > 0 ? (2 * kSMs * (int64_t)a.dx_kb + all - 1) / all : 1);
         a.head->shares = (int)(want < 1 ? 1 : gg_min64(want, a.most_shares));
         a.head->ticket = 0;
         a.head->scale = 8192.0f / top;
