@@ -7,7 +7,8 @@
 // 1. tokens_kernel counts the tokens whose weight is not 0 and gathers their rows of X: a masked token
 //    costs no multiplication, and what its row holds (NaN, say) meets nothing.
 // 2. The product z = X W over the whole vocabulary, in 32-bit sums that stay on chip: its epilogue keeps
-//    of every 32 entries the largest logit and the sum of exponentials (8 bytes for 32 logits).
+//    of every 128 entries (CTA pairs) or 32 (the split kernel, few tokens) the largest logit and the sum of
+//    exponentials, 8 bytes.
 // 3. join_kernel makes lse and loss of them.
 // 4. For a piece of the vocabulary at a time, the last one first: the product again (but for the last piece,
 //    whose exponentials step 2 kept in the workspace: kept_kernel finishes them), its epilogue turning the logits into
@@ -121,20 +122,20 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
         for (int k = 0; k < kEach; ++k) {
             if (k >= steps)
                 break;
-            const int t = (int)c0 + k * kThreads + (int)threadIdx.x;
+            const uint32_t t = (uint32_t)c0 + k * kThreads + threadIdx.x;  // (passes 2^31 behind the last token)
             const bool on = live[k] >> lane & 1;
             const int p = base + offsets[k * 32 + warp] + __popc(live[k] & ((1u << lane) - 1u));
             base += sums[k];
             if (on && (uint32_t)p % blocks == me) {
                 const int at = atomicAdd(&listed, 1);
-                list_token[at] = t;
+                list_token[at] = (int)t;
                 list_place[at] = p;
             }
             // the small per-token arrays: a warp's 32 tokens by one block
-            if ((uint32_t)(t / 32) % blocks == me && t < T) {
+            if (t / 32 % blocks == me && t < (uint32_t)T) {
                 a.place[t] = on ? p : -1;
                 if (on) {
-                    a.token[p] = t;
+                    a.token[p] = (int)t;
                     a.tgt[p] = (int)tg[k];
                     a.wt[p] = w[k];
                 } else {

@@ -133,6 +133,14 @@ def test_pieces(T, V, K, piece, layout):
         assert torch.equal(a, b)                 # the loss does not depend on the pieces
 
 
+# dX's contraction goes in shares by the length of a whole piece: the last one, the shortest and first to be
+# computed, has fewer blocks of 64 entries than there are shares, which have to come out as zeros
+@pytest.mark.parametrize("T,K", [(100, 256), (200, 520)])
+@pytest.mark.parametrize("more", [1, 128, 200])
+def test_last_piece_shorter_than_the_shares(T, K, more):
+    Case(T, 8192 + more, K, BF16, masked=0.25, gdt=F32).call(8192).check()
+
+
 @pytest.mark.parametrize("T,V,K", [(16, 300, 64), (400, 3000, 520)])
 def test_parts_alone(T, V, K):
     c = Case(T, V, K, BF16, masked=0.2).call().check()
