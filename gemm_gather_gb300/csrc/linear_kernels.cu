@@ -47,6 +47,11 @@
 // float32 product's own 6.1e-7 at 4096 tokens, and 165 us for the gradient of an
 // 8192 x 3584 weight over them (512: 4.7e-7 and 182 us; one chunk: 4.4e-6, 163 us).
 //
+// The vocabulary's products (entropy_kernels.cu) run on the same kernels: logits whose epilogue keeps sums of
+// exponentials (kEpiLse), or the gradient of the logits (kEpiSoftGrad), and what that is multiplied into
+// (kEpiVocab).  The tokens that count are known on the device only (kLive): a launch is laid out for all
+// of them, and its walk ends at the last tile there is.
+//
 // Every mbarrier wait is bounded; one that gives up stores GG_ERR_TIMEOUT in
 // the status word and raises the CTA's abort flag, and every role drains what
 // it has in flight before TMEM is freed and the CTA exits.
@@ -355,9 +360,8 @@ __device__ __forceinline__ int valid16(int64_t J, int64_t j0)
 // 8192.  Instead a warp turns 32 features x 32 tokens around in 2 KB of its
 // own shared memory, in words of two neighbouring tokens: a lane stores its
 // feature's 16 words, then takes 8 features of a pair, which are 16 bytes of each
-// of the two rows, so that a global access is 8 rows of 64 bytes.  (Two-byte
-// stores in the rows' own order took 4.5 of the SM's shared-memory cycles each, a
-// third of a short contraction's tile.)  Tensors read in the epilogue come the same
+// of the two rows, so that a global access is 8 rows of 64 bytes, and half as many
+// stores are made as of single elements.  Tensors read in the epilogue come the same
 // way, loaded into registers ahead of the accumulator.
 //
 // Pair p's word of feature f lies in row p (128 bytes), its 16-byte pieces swapped in
@@ -2042,7 +2046,7 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
 // Logits of longer contractions than kPlainLse are summed in chunks for lse: without them losses are off by
 // 4.5e-7 of their size at 1024 and 1.1e-6 at 2011, and that grows with the length.  In registers the sums of chunks
 // spill, which only tiles of long contractions hide: 4096 tokens, 100003 entries, K = 1024 take 570 us with and 460
-// without, 777 tokens, 32768 entries, K = 2011 100 and 65.
+// without, the product of 777 tokens, 32768 entries, K = 2011 90 and 65.
 constexpr int64_t kPlainLse = 1792;
 constexpr int kLseChunk = 16;  // k-blocks
 
@@ -2060,10 +2064,12 @@ bool one_chunk(int epi, const LinearArgs &a)
 template <int EPI>
 cudaError_t launch_epi(const LinearArgs &a, const LinearPlan &p, cudaStream_t s, const char **why)
 {
-    if (a.K == 0) {
-        const int64_t groups = ((a.I + 31) / 32) * ((a.J + 15) / 16);
-        empty_kernel<EPI><<<(int)gg_min64((groups + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
-        return cudaGetLastError();
+    if constexpr (EPI != kEpiSoftGrad && EPI != kEpiVocab) {  // (these are called for a contraction only)
+        if (a.K == 0) {
+            const int64_t groups = ((a.I + 31) / 32) * ((a.J + 15) / 16);
+            empty_kernel<EPI><<<(int)gg_min64((groups + 7) / 8, kSMs * 8), 256, 0, s>>>(a);
+            return cudaGetLastError();
+        }
     }
     if (p.kernel == GG_LINEAR_PAIR) {
         if constexpr (EPI == kEpiGradW || EPI == kEpiVocab || EPI == kEpiLse) {

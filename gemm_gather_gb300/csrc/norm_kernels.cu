@@ -11,7 +11,8 @@
 //
 // Row kernels.  A row belongs to R warps (1 to 32) of a block, VPT vectors of eight elements a
 // thread, so that it stays in registers between its sum and its use; blocks of at least eight
-// warps take 8 / R rows side by side and walk the rows with the grid's stride.  Rows that are not
+// warps take 8 / R rows side by side.  Forward, a block ends with its row group; backward, where dw's
+// sums stay in registers, blocks walk the rows with the grid's stride.  Rows that are not
 // 16-byte aligned, or longer than 32 warps hold, go through kernels that read a row twice.
 //
 // dw: a thread keeps the sums of its own columns over all its rows in registers; a block adds its
@@ -140,10 +141,10 @@ __device__ __forceinline__ Eight load_weights(const void *w, int f32, int vec, i
 }
 
 // ---- rows in flight ---------------------------------------------------------------------
-// Where a block walks several rows, its threads copy the next rows' vectors into slots of their own in
+// Backward, where a block walks several rows, its threads copy the next rows' vectors into slots of their own in
 // shared memory (D rows deep, one commit group a row) while they work on the present one; nobody else
-// reads a thread's slots, so there is nothing to wait for but its own copies.  D = 1: one row a block and
-// no copies ahead, vectors come straight into registers.
+// reads a thread's slots, so there is nothing to wait for but its own copies.  D = 1: no
+// copies ahead, vectors come straight into registers.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -720,7 +721,7 @@ bool on8(const void *p, int64_t ld) { return ((reinterpret_cast<uint64_t>(p) | (
 // Warps and vectors a thread for rows of N elements.  While the rows' vectors, one a thread, fit the GPU's
 // threads about once, a row's own latency is the time, so it gets as many warps as it has vectors for;
 // else up to 4 vectors a thread, so that more rows are in flight: 777 x 1523 takes 5 us with one and 8 with
-// four, 16384 x 8192 (forward) 240 us with one and 195 with four.  `most`: vectors a thread that 1024 threads hold.
+// four, 16384 x 8192 (forward) 315 us with one, 209 to 225 with two and 180 with four.  `most`: vectors a thread that 1024 threads hold.
 bool row_shape(int64_t M, int64_t N, int most, RowShape *s, int *vpt)
 {
     const int64_t warps = (N + 32 * kVec - 1) / (32 * kVec);  // at one vector a thread

@@ -731,8 +731,9 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * statistics and a zero (or kept) dW; K == 0 gives logits of 0.
  * workspace: 16-byte aligned device memory of at least
  * gg_linear_cross_entropy_workspace(T, V, K, piece, gradients) bytes (gradients: whether dX or
- * dW is asked for): about 2 T K + T V / 16 bytes for the loss, 4 T K + 2 T piece more for the
- * gradients.  What it held is lost; calls that may run at the same time, or replays of
+ * dW is asked for): about 2 T K bytes and T V / 16 (T V / 4 up to 512 tokens) for the
+ * loss; for the gradients 4 T K more, up to eight times that within 256 MB, and 2 T piece
+ * + T piece / 8.  What it held is lost; calls that may run at the same time, or replays of
  * graphs that captured them, need workspaces of their own.
  * dev_status: as for gg_linear.
  * ------------------------------------------------------------------------- */
