@@ -269,8 +269,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 32; ++k)
                 s += part[k][lane];
-            lse = m + logf(s);
-            const float loss = lse - target;
+            // (the loss from the logits' difference: lse is rounded to its own size, which a confident
+            // token's loss is far below)
+            const float rest = logf(s), loss = m - target + rest;
+            lse = m + rest;
             a.loss[token] = loss;
             if (a.lse)
                 a.lse[token] = lse;

@@ -1,0 +1,67 @@
+"""Tokens that the vocabulary's loss is sure of, and logits of any size, against float64.
+
+Hidden states are rows of the unit matrix, so that a token's logits are a column of W, exactly: no product is
+rounded, and what is off is the softmax alone.  An exponential (2^-22 of it), a sum of them and its logarithm
+leave a loss off by 2^-21 of 1 + its size, whatever the logits' size.  lse is
+rounded to its own size.
+"""
+import pytest
+import torch
+
+from tests.block_oracle import BF16, F16, F32
+from tests.test_gpu_entropy import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def exact_logits(T, V, K, dtype, logits, layout="nk", **kw):
+    """A case whose token t has the logits of column t mod K of ``logits``, a V x K matrix."""
+    c = Case(T, V, K, dtype, layout, gdt=F32, **kw)
+    c.x[:] = torch.eye(K, device="cuda").to(dtype).repeat(-(-T // K), 1)[:T]
+    c.w.copy_((logits if layout == "nk" else logits.t()).to(dtype))
+    return c
+
+
+def check_losses(c):
+    """Losses relative to 1 + their size."""
+    w = c.w.double() if c.layout == "nk" else c.w.double().t()
+    z = w.t()[torch.arange(c.T, device="cuda") % c.K]
+    top = z.amax(1)
+    rest = torch.log(torch.exp(z - top[:, None]).sum(1))
+    loss = top - z.gather(1, c.target[:, None])[:, 0] + rest
+    assert ((c.loss.double() - loss).abs() <= (1 + loss) * 2.0 ** -21).all()
+    assert ((c.lse.double() - top - rest).abs() <= 2.0 ** -21 + c.lse.double().abs() * 2.0 ** -24).all()
+
+
+def sure(T, V, K, dtype, layout="nk", **kw):
+    """Targets are the largest logit, 100 to 250, and 2 to 12 above the others: probabilities up to 1 - 0.002."""
+    g = torch.Generator().manual_seed(T + K)
+    top = 100 + torch.randint(0, 151, (K,), generator=g).float()
+    gap = 2 + torch.randint(0, 11, (K,), generator=g).float()
+    logits = top - gap - torch.randint(0, 5, (V, K), generator=g)
+    a = torch.randint(0, V, (K,), generator=g)
+    logits[a, torch.arange(K)] = top
+    c = exact_logits(T, V, K, dtype, logits.cuda(), layout, **kw)
+    c.target = a[torch.arange(T) % K].cuda()
+    return c
+
+
+def huge(T, V, K, layout="nk", **kw):
+    """Two entries share the largest logit, of 2^33 to 2^40 and either sign; the others are far below."""
+    g = torch.Generator().manual_seed(T + K)
+    size = torch.exp2(33 + 7 * torch.rand((K,), generator=g)).to(BF16).float()
+    size = torch.where(torch.rand((K,), generator=g) < 0.5, size, -size)
+    logits = (size - size.abs() * (0.1 + torch.rand((V, K), generator=g))).to(BF16)
+    a = torch.randint(0, V, (K,), generator=g)
+    b = (a + 1 + torch.randint(0, V - 1, (K,), generator=g)) % V
+    k = torch.arange(K)
+    logits[a, k] = logits[b, k] = size.to(BF16)
+    c = exact_logits(T, V, K, BF16, logits.cuda(), layout, **kw)
+    c.target = torch.where(torch.rand((T,), generator=g) < 0.5, a[torch.arange(T) % K], b[torch.arange(T) % K]).cuda()
+    return c
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_losses_of_few_tokens(layout):
+    for c in (sure(40, 300, 64, BF16, layout), sure(40, 300, 64, F16, layout), huge(40, 300, 64, layout)):
+        check_losses(c.call())
