@@ -148,6 +148,13 @@ __device__ __forceinline__ float soft_grad(float z, int64_t i, const TokenTerms 
     return t.coef != 0.0f ? ((int)i == t.target ? p - 1.0f : p) * t.coef : 0.0f;
 }
 
+// exp of two logits less what they are taken from.
+__device__ __forceinline__ float2 above(float z0, float z1, float from0, float from1)
+{
+    const float2 d = halves_of(mul2(add2(pair_of(z0, z1), pair_of(-from0, -from1)), pair_of(kLog2e)));
+    return make_float2(ex2_approx(d.x), ex2_approx(d.y));
+}
+
 // (largest z, sum of exp(z - largest)) of a warp's 32 vocabulary entries, for each of n columns: a row of
 // the partial results is the warp's, place j is token j.  Every lane calls it; where all of them are past
 // the vocabulary's end there is no such row.
@@ -180,8 +187,9 @@ __device__ __forceinline__ void emit_lse(const LinearArgs &a, int64_t i, int64_t
 
 // The same of 16 neighbouring columns in 2 KB of shared memory: a lane turns from a vocabulary entry
 // to half a column's entries (the exclusive or spreads both over the banks).  target: lane c mod 16
-// has column c's, and gets its result.  The exponent is one fused operation: what rounding the largest
-// logit's product costs (2^-24 of it) is the same for a column's terms, and no more than lse's own.
+// has column c's, and gets its result.  The difference comes first, as everywhere: log2 e times each of two
+// large logits would be rounded apart, which costs a confident token's loss 2^-24 of the logit, and logits
+// beyond 2^30 everything.
 __device__ __forceinline__ float2 lse16(const LinearArgs &a, int64_t i0, int64_t j0, int n, int lane, int target,
                                         const float (&v)[16], uint8_t *stage)
 {
@@ -201,8 +209,11 @@ __device__ __forceinline__ float2 lse16(const LinearArgs &a, int64_t i0, int64_t
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
     const float from = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        s += ex2_approx(fmaf(x[k], kLog2e, -from * kLog2e));
+    for (int k = 0; k < 16; k += 2) {
+        const float2 e = above(x[k], x[k + 1], from, from);
+        s += e.x;
+        s += e.y;
+    }
     s += __shfl_xor_sync(0xffffffffu, s, 16);
     if (c < n) {
         const int64_t at = (int64_t)target - i0;
@@ -971,17 +982,17 @@ __device__ __forceinline__ void log_sums(const LinearArgs &a, const Place &at, i
                 if (c >= n)
                     continue;
                 const float m = own[(g + c) / 16].x;
-                const float from = (m == -INFINITY ? 0.0f : m) * kLog2e;
+                const float from = m == -INFINITY ? 0.0f : m;
                 if (lane < 16 && c + lane < n)
                     a.kept_top[(i0 - a.kept0) / 32 * a.ldpartial + jg + c + lane] = m;
                 float v[16];
                 logits(g + c, v);
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    v[u] = ex2_approx(fmaf(v[u], kLog2e, -__shfl_sync(0xffffffffu, from, u)));
-#pragma unroll
-                for (int u = 0; u < 16; u += 2)
-                    *staged(at.stage_buf, lane, c + u) = kept_code(v[u]) | kept_code(v[u + 1]) << 16;
+                for (int u = 0; u < 16; u += 2) {
+                    const float2 e = above(v[u], v[u + 1], __shfl_sync(0xffffffffu, from, u),
+                                           __shfl_sync(0xffffffffu, from, u + 1));
+                    *staged(at.stage_buf, lane, c + u) = kept_code(e.x) | kept_code(e.y) << 16;
+                }
             }
             write_rows(rows_of(a.kept, a.ldkept), a.I - a.kept0, i0 - a.kept0, jg, n, lane, at.stage_buf);
         }

@@ -1,9 +1,11 @@
 """Tokens that the vocabulary's loss is sure of, and logits of any size, against float64.
 
 Hidden states are rows of the unit matrix, so that a token's logits are a column of W, exactly: no product is
-rounded, and what is off is the softmax alone.  An exponential (2^-22 of it), a sum of them and its logarithm
-leave a loss off by 2^-21 of 1 + its size, whatever the logits' size.  lse is
-rounded to its own size.
+rounded, and what is off is the softmax alone.  A term of the sum of exponentials is off by its argument's rounding
+and log2 e's (the argument times 2^-23) and by three exponentials on its way (of its 32 entries' largest logit, of
+the tile's, of all: 2^-22 each); a sum of up to 700 entries rounds 32 times (16 in a thread, 1, 5, and at most 10
+partial sums that are not 0): 2^-24 each.  So a loss is off by 44 2^-24, the mean argument times 2^-23, and its own
+logarithm's and sum's rounding, 2^-22 of it, whatever the logits' size.  lse is rounded to its own size.
 """
 import pytest
 import torch
@@ -12,6 +14,10 @@ from tests.block_oracle import BF16, F16, F32
 from tests.test_gpu_entropy import Case
 
 pytestmark = pytest.mark.gpu
+
+
+# T, V, K: pairs without and with kept exponentials, and with logits in chunks
+PAIRS = [(600, 700, 64), (600, 700, 512), (600, 300, 2112)]
 
 
 def exact_logits(T, V, K, dtype, logits, layout="nk", **kw):
@@ -23,14 +29,16 @@ def exact_logits(T, V, K, dtype, logits, layout="nk", **kw):
 
 
 def check_losses(c):
-    """Losses relative to 1 + their size."""
     w = c.w.double() if c.layout == "nk" else c.w.double().t()
     z = w.t()[torch.arange(c.T, device="cuda") % c.K]
     top = z.amax(1)
-    rest = torch.log(torch.exp(z - top[:, None]).sum(1))
+    below = top[:, None] - z
+    rest = torch.log(torch.exp(-below).sum(1))
+    mean = (torch.exp(-below - rest[:, None]) * below).sum(1)
+    tol = (44 + 2 * mean) * 2.0 ** -24
     loss = top - z.gather(1, c.target[:, None])[:, 0] + rest
-    assert ((c.loss.double() - loss).abs() <= (1 + loss) * 2.0 ** -21).all()
-    assert ((c.lse.double() - top - rest).abs() <= 2.0 ** -21 + c.lse.double().abs() * 2.0 ** -24).all()
+    assert ((c.loss.double() - loss).abs() <= tol + loss * 2.0 ** -22).all()
+    assert ((c.lse.double() - top - rest).abs() <= tol + rest * 2.0 ** -22 + c.lse.double().abs() * 2.0 ** -24).all()
 
 
 def sure(T, V, K, dtype, layout="nk", **kw):
@@ -65,3 +73,12 @@ def huge(T, V, K, layout="nk", **kw):
 def test_losses_of_few_tokens(layout):
     for c in (sure(40, 300, 64, BF16, layout), sure(40, 300, 64, F16, layout), huge(40, 300, 64, layout)):
         check_losses(c.call())
+
+
+@pytest.mark.parametrize("T,V,K", PAIRS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("gradients", [False, True])
+def test_losses_on_pairs(T, V, K, dtype, gradients):
+    check_losses(sure(T, V, K, dtype, dx=gradients, dw=gradients).call())
+    if dtype is BF16:
+        check_losses(huge(T, V, K, dx=gradients, dw=gradients).call())
