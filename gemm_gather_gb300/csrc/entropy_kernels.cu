@@ -9,7 +9,8 @@
 // 2. The product z = X W over the whole vocabulary, in 32-bit sums that stay on chip: its epilogue keeps
 //    of every 128 entries (CTA pairs) or 32 (the split kernel, few tokens) the largest logit and the sum of
 //    exponentials, 8 bytes.
-// 3. join_kernel makes lse and loss of them.
+// 3. join_kernel makes lse and loss of them, and for the gradient a token's largest logit and its weight over the sum:
+//    lse rounded would be all that is left of a confident token's p - 1 (2e-6 of the weight at lse = 20).
 // 4. For a piece of the vocabulary at a time, the last one first: the product again (but for the last piece,
 //    whose exponentials step 2 kept in the workspace: kept_kernel finishes them), its epilogue turning the logits into
 //    dZ in 16 bits; then dX += dZ W^T (float32, in memory) and the piece's dW = X^T dZ in one launch.
@@ -263,7 +264,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         return;
     double sum = 0.0, total = 0.0;  // of the block's 32 tokens
     if (p < pad) {
-        float lse = 0.0f;
+        const float coef = weight * a.head->scale;
+        float inv = 0.0f;
         if (p < live) {
             s = 0.0f;
 #pragma unroll
@@ -272,15 +274,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
             // (the loss from the logits' difference: lse is rounded to its own size, which a confident
             // token's loss is far below)
             const float rest = logf(s), loss = m - target + rest;
-            lse = m + rest;
             a.loss[token] = loss;
             if (a.lse)
-                a.lse[token] = lse;
+                a.lse[token] = m + rest;
             sum = (double)weight * (double)loss;
             total = (double)weight;
+            inv = coef / s;
         }
-        a.lsec[p] = lse;
-        a.coef[p] = weight * a.head->scale;
+        a.largest[p] = m;
+        a.inv[p] = inv;
+        a.coef[p] = coef;
     }
     if (!a.stats)
         return;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 // The kept exponentials exp(z - top) of a piece to the gradient of its logits, in place:
-// coef (exp(top - lse) of it - (v is the target)), from the 16 bits of kept_code to the layer's type.  A block takes 32 tokens and 1024
+// inv exp(top - largest) of it, less coef at the target, from the 16 bits of kept_code to the layer's type.  A block takes 32 tokens and 1024
 // entries, whose 32 x 32 factors it makes once.  Bound: a read and a write of the piece, from L2 as far as it
 // stayed there.
 template <bool BF16>
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(256, 4) kept_kernel(const __grid_constant__ En
             float f = 0.0f;
             if (p0 + lane < live && c0 + g * 32 < a.kept_n) {
                 const float top = a.kept_top[(c0 / 32 + g) * a.T + p0 + lane];
-                f = ex2_approx((top - a.lsec[p0 + lane]) * 1.44269504f) * a.coef[p0 + lane];
+                f = ex2_approx((top - a.largest[p0 + lane]) * 1.44269504f) * a.inv[p0 + lane];
             }
             factor[lane][g] = f;
         }

@@ -29,7 +29,7 @@ constexpr int kEpiGradW = 2;    // acc (+ out)
 constexpr int kEpiGradIn8 = 3;  // acc * act'(aux), aux kept in 8 bits (codes, with scales)
 // The vocabulary's products (entropy_kernels.cu): i is a vocabulary entry of a piece, j a token.
 constexpr int kEpiLse = 4;       // (largest, sum of exponentials) of 32 or 128 entries, and the target's logit
-constexpr int kEpiSoftGrad = 5;  // coef (exp(acc - lse) - (i is the target)), in 16 bits
+constexpr int kEpiSoftGrad = 5;  // coef (softmax - (i is the target)), in 16 bits
 constexpr int kEpiVocab = 6;     // alpha acc (+ out): what the gradient of the logits is multiplied into
 // kEpiGradW, kEpiVocab and kEpiLse of a contraction that is one chunk (linear_kernels.cu chooses them).
 constexpr int kEpiGradWShort = 7, kEpiVocabShort = 8, kEpiLseShort = 9;
@@ -68,7 +68,7 @@ struct LinearArgs {
     void *kept;            // kEpiLse on pairs: exp(acc - top) of entries kept0 on, in 16 bits, or null;
     float *kept_top;       // top, of every 32 entries: rows of ldpartial tokens
     int64_t ldkept, kept0;
-    const float *lse, *coef;
+    const float *largest, *inv, *coef;  // kEpiSoftGrad: a token's largest logit, coef / sum of exponentials, coef
     const float *alpha;    // kEpiVocab; null: 1
     int skip;              // pairs of the grid past the end of the first product's walk
     int *status;
@@ -199,7 +199,7 @@ struct EntropyArgs {
     int *place;          // a token's compact place, or -1
     int *token;          // compact: its token
     int *tgt;            // compact targets (-1 behind the last)
-    float *wt, *lsec, *coef, *ztarget;
+    float *wt, *largest, *inv, *coef, *ztarget;  // (coef: weight scale; inv: coef / sum of exponentials)
     void *sums;          // two doubles for every 32 tokens
     float2 *partial;     // rows x T
     int64_t rows;

@@ -134,18 +134,18 @@ __device__ __forceinline__ float load_aux(const LinearArgs &a, const void *p, in
 
 // ---- the vocabulary's softmax -----------------------------------------------------------
 // The gradient over a logit z of token j, for vocabulary entry i of a piece:
-// coef (exp(z - lse) - (i is the target)).  The difference first: it is small where it counts,
-// however large z and lse are.
+// coef (exp(z - largest) / total - (i is the target)).  The difference first: it is small where it counts, however
+// large the logits are.  From the largest and the sum, not from lse, whose rounding to its own size would be all that
+// is left of a confident token's p - 1.  The target's coef is taken off where a target lies: once a token.
 struct TokenTerms {
-    float lse, coef;
-    int target;  // within the piece; any other number: not there
+    float largest, inv;  // inv: coef / total
+    int target;          // within the piece; any other number: not there
 };
 
-__device__ __forceinline__ float soft_grad(float z, int64_t i, const TokenTerms &t)
+__device__ __forceinline__ float soft_grad(float z, float largest, float inv)
 {
-    const float p = ex2_approx((z - t.lse) * kLog2e);
     // (what rows of zeros fill a k-block up with is 0, whatever W holds)
-    return t.coef != 0.0f ? ((int)i == t.target ? p - 1.0f : p) * t.coef : 0.0f;
+    return inv != 0.0f ? ex2_approx((z - largest) * kLog2e) * inv : 0.0f;
 }
 
 // exp of two logits less what they are taken from.
@@ -333,7 +333,7 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
         for (int u = 0; u < C; ++u)
             if (u < n) {
                 const int64_t j = j0 + (int64_t)u * jstep;
-                v[u] = soft_grad(v[u], i, TokenTerms{a.lse[j], a.coef[j], a.target[j] - a.v0});
+                v[u] = soft_grad(v[u], a.largest[j], a.inv[j]) - ((int)i == a.target[j] - a.v0 ? a.coef[j] : 0.0f);
             }
     } else if (aux != nullptr) {
 #pragma unroll
@@ -637,6 +637,9 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
         stage_rows(stage, lane, aux);
     if (has_aux && REGISTERS)  // beside the sums there is room for half of them
         fetch_rows(aux_of<EPI>(a), a.I, i0, j0, n, lane, stage);
+    // columns whose target is one of the warp's features: few
+    const uint32_t hits =
+        EPI == kEpiSoftGrad ? __ballot_sync(0xffffffffu, terms.target >= i0 && terms.target < i0 + 32) : 0u;
 #pragma unroll(kUnroll)
     for (int c = 0; c < kStageCols; c += 16) {
         if (c >= n)
@@ -673,10 +676,17 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
         } else if constexpr (EPI == kEpiSoftGrad) {  // lane c has column c's terms
 #pragma unroll
             for (int u = 0; u < 16; ++u)
-                v[u] = soft_grad(v[u], i0 + lane,
-                                 TokenTerms{__shfl_sync(0xffffffffu, terms.lse, c + u),
-                                            __shfl_sync(0xffffffffu, terms.coef, c + u),
-                                            __shfl_sync(0xffffffffu, terms.target, c + u)});
+                v[u] = soft_grad(v[u], __shfl_sync(0xffffffffu, terms.largest, c + u),
+                                 __shfl_sync(0xffffffffu, terms.inv, c + u));
+#pragma unroll 1
+            for (uint32_t left = hits >> c & 0xffffu; left != 0; left &= left - 1) {
+                const int at = __ffs((int)left) - 1;
+                const bool mine = __shfl_sync(0xffffffffu, terms.target, c + at) == (int)i0 + lane;
+                const float coef = mine ? a.coef[j0 + c + at] : 0.0f;
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    v[u] -= u == at ? coef : 0.0f;
+            }
         } else if (has_aux) {
 #pragma unroll
             for (int u = 0; u < 16; ++u)
@@ -698,7 +708,7 @@ __device__ __forceinline__ TokenTerms terms_of(const LinearArgs &a, int64_t j0, 
     }
     if constexpr (EPI == kEpiSoftGrad) {
         if (lane < n)
-            t = TokenTerms{a.lse[j0 + lane], a.coef[j0 + lane], a.target[j0 + lane] - a.v0};
+            t = TokenTerms{a.largest[j0 + lane], a.inv[j0 + lane], a.target[j0 + lane] - a.v0};
     }
     return t;
 }

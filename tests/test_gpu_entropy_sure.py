@@ -82,3 +82,40 @@ def test_losses_on_pairs(T, V, K, dtype, gradients):
     check_losses(sure(T, V, K, dtype, dx=gradients, dw=gradients).call())
     if dtype is BF16:
         check_losses(huge(T, V, K, dx=gradients, dw=gradients).call())
+
+
+def check_gradients(c):
+    """dW's columns: sums of the gradients of their tokens' logits.
+
+    A probability is off by what the sum of exponentials is, its own argument and exponential, and two roundings;
+    1 is taken from a target's with one more.  Then half a step of 16 bits, before that of an exponential that was
+    kept (2^-12, nothing below 2^-31 of the largest; the largest is 1, exactly), and a truncating sum of the tokens that
+    are not 0."""
+    w = c.w.double() if c.layout == "nk" else c.w.double().t()
+    k = torch.arange(c.T, device="cuda") % c.K
+    z = w.t()[k]
+    below = z.amax(1, keepdim=True) - z
+    e = torch.exp(-below)
+    total = e.sum(1, keepdim=True)
+    p = e / total
+    mean = (p * below).sum(1, keepdim=True)
+    hot = torch.zeros_like(p).scatter_(1, c.target[:, None], 1.0)
+    coef = c.weight.double()[:, None]
+    others = torch.where(hot > 0, 0.0, e).sum(1, keepdim=True)       # 1 - p of a target without the cancellation
+    dz = coef * torch.where(hot > 0, -others / total, p)
+    err = coef * p * ((48 + 2 * mean) * 2.0 ** -24 + below * 2.0 ** -23 + 2.0 ** -22) + coef * hot * 2.0 ** -23
+    err = err + coef * torch.where(below == 0, 0.0, p) * 2.0 ** -12 + coef * p.amax(1, keepdim=True) * 2.0 ** -31
+    err = (err + dz.abs() * 2.0 ** (-11 if c.dtype is F16 else -8)) + (float(coef.max()) * 2.0 ** -37 if c.dtype is F16 else 0)
+    got = c.dw.double() if c.layout == "nk" else c.dw.double().t()
+    want, bound = torch.zeros_like(got), torch.zeros_like(got)
+    want.index_add_(1, k, dz.t())
+    bound.index_add_(1, k, (err + dz.abs() * (-(-c.T // c.K) * 2.0 ** -23)).t())
+    assert ((got - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("T,V,K", [(40, 300, 64)] + PAIRS)
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("piece", [0, 128])
+def test_gradients(T, V, K, layout, piece):
+    for c in (sure(T, V, K, F16, layout), sure(T, V, K, BF16, layout), huge(T, V, K, layout)):
+        check_gradients(c.call(piece))
