@@ -719,8 +719,8 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * they hold, its loss and lse are 0, its dX row is zero, and it costs no
  * multiplication.  A target outside [0, V) stores GG_ERR_INVALID_ARG in the status word
  * (dev_status, or the library's when NULL) and its token counts as masked.  Logits of
- * -inf are entries of probability 0; a row of nothing else, or one with NaN or +inf,
- * gives NaN.  Sums, softmax and both gradients' sums are float32; dZ is multiplied in
+ * -inf are entries of probability 0; a row of nothing else has lse -inf and NaN for its loss
+ * and gradients, one with NaN or +inf gives NaN for all of them.  Sums, softmax and both gradients' sums are float32; dZ is multiplied in
  * `dtype`, with weights relative to the largest (so that their size does not matter to
  * float16); logits of all pieces but one are computed twice.
  * The gradients go through the vocabulary in pieces: `piece` entries (a multiple of
