@@ -3,8 +3,7 @@ weights of very different sizes."""
 import pytest
 import torch
 
-from tests import block_oracle as o
-from tests.block_oracle import BF16, F16, F32
+from tests.block_oracle import BF16, F32
 from tests.test_gpu_entropy import Case
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +29,28 @@ def test_rows_of_nothing_but_minus_infinity(T, V, K):
     assert torch.equal(c.loss.isnan(), bad) and c.stats[0].isnan()
     assert torch.equal(c.dx.isnan().any(1), bad) and c.dx[5].isnan().all()
     assert c.dw[:, 1].isnan().all()
+
+
+@pytest.mark.parametrize("T,V,K", SIZES)
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_rows_that_fill_up_a_block_stay_zero_whatever_the_weights_hold(T, V, K, layout):
+    """Tokens that count are padded to 64 with rows of zeros, whose logits beside infinite weights are NaN: dW meets
+    nothing of them."""
+    weights = torch.zeros((T,))
+    weights[: T - 23 - T % 64] = 1.0 / T
+    assert int((weights != 0).sum()) % 64 != 0
+    c = Case(T, V, K, BF16, layout, weights=weights, gdt=F32, dx=False)
+    c.x[:] = c.x.abs() + 0.1
+    rows = c.w if layout == "nk" else c.w.t()
+    rows[3], rows[V - 1] = -float("inf"), -float("inf")
+    c.target[(c.target == 3) | (c.target == V - 1)] = 7
+    c.call()
+    got = c.dw if layout == "nk" else c.dw.t()
+    assert got.isfinite().all() and (got[3] == 0).all() and (got[V - 1] == 0).all()
+    # the others' are what they are without the two
+    d = Case(T, V, K, BF16, layout, weights=weights, gdt=F32, dx=False)
+    d.x.copy_(c.x), d.w.copy_(c.w), d.target.copy_(c.target)
+    rows = d.w if layout == "nk" else d.w.t()
+    rows[3], rows[V - 1] = -1e4, -1e4
+    d.call()
+    assert torch.equal(got, d.dw if layout == "nk" else d.dw.t())
