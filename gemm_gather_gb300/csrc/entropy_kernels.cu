@@ -19,7 +19,9 @@
 // Logits are multiplied twice (8 T V K operations instead of 6) so that they need not be kept, nor rounded
 // to 16 bits before the softmax.  dZ is the only 16-bit step: weights enter it relative to the largest, which
 // counts 2^13, and dX and dW are taken back in float32.  That keeps probabilities down to 2^-27 at float16's
-// full precision whatever the weights' size; and where all weights are equal, as most often, the targets' terms,
+// full precision however large or small all weights are (of a token r times the largest: 2^-27 / r, and below
+// 2^-38 / r nothing is left; a factor a token would help dX but not dW, whose terms have to have one scale); and
+// where all weights are equal, as most often, the targets' terms,
 // -8192 (1 - p), lose next to nothing (a weight of 1 / 10 would be off by 2^-10 in all of them alike).
 //
 // Bound: the tensor cores, under the power limit.

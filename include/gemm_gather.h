@@ -721,8 +721,10 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * (dev_status, or the library's when NULL) and its token counts as masked.  Logits of
  * -inf are entries of probability 0; a row of nothing else has lse -inf and NaN for its loss
  * and gradients, one with NaN or +inf gives NaN for all of them.  Sums, softmax and both gradients' sums are float32; dZ is multiplied in
- * `dtype`, with weights relative to the largest (so that their size does not matter to
- * float16); logits of all pieces but one are computed twice.
+ * `dtype`, with weights relative to the largest one's size, which counts 2^13: the size of all of them
+ * does not matter to float16, but a token whose weight is r times the largest has float16's full
+ * precision for terms of softmax - onehot from 2^-27 / r on, and loses those below 2^-38 / r (bfloat16
+ * loses none); logits of all pieces but one are computed twice.
  * The gradients go through the vocabulary in pieces: `piece` entries (a multiple of
  * 128) at a time, 0 for the library's choice (equal pieces of at most 32768).  The
  * values differ by the order of float32 sums only.
