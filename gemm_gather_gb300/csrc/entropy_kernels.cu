@@ -11,8 +11,9 @@
 //    exponentials, 8 bytes.
 // 3. join_kernel makes lse and loss of them, and for the gradient a token's largest logit and its weight over the sum:
 //    lse rounded would be all that is left of a confident token's p - 1 (2e-6 of the weight at lse = 20).
-// 4. For a piece of the vocabulary at a time, the last one first: the product again (but for the last piece,
-//    whose exponentials step 2 kept in the workspace: kept_kernel finishes them), its epilogue turning the logits into
+// 4. For a piece of the vocabulary at a time, the last one first: the product again (but for the last piece where
+//    CTA pairs computed step 2 and K >= 512: its exponentials were kept in the workspace, and kept_kernel finishes
+//    them; chunks of a long contraction are not added apart here, dZ's 16 bits being far coarser), its epilogue turning the logits into
 //    dZ in 16 bits; then dX += dZ W^T (float32, in memory) and the piece's dW = X^T dZ in one launch.
 // 5. dx_kernel rounds dX once, in the tokens' own order, zeros for the masked ones.
 //

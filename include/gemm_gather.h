@@ -724,7 +724,8 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * `dtype`, with weights relative to the largest one's size, which counts 2^13: the size of all of them
  * does not matter to float16, but a token whose weight is r times the largest has float16's full
  * precision for terms of softmax - onehot from 2^-27 / r on, and loses those below 2^-38 / r (bfloat16
- * loses none); logits of all pieces but one are computed twice.
+ * loses none).  With gradients logits are computed twice, but for those of the last piece where K >= 512 and
+ * CTA pairs compute the loss (always beyond 512 tokens).
  * The gradients go through the vocabulary in pieces: `piece` entries (a multiple of
  * 128) at a time, 0 for the library's choice (equal pieces of at most 32768).  The
  * values differ by the order of float32 sums only.
