@@ -9,11 +9,13 @@
 // 2. The product z = X W over the whole vocabulary, in 32-bit sums that stay on chip: its epilogue keeps
 //    of every 128 entries (CTA pairs) or 32 (the split kernel, few tokens) the largest logit and the sum of
 //    exponentials, 8 bytes.
-// 3. join_kernel makes lse and loss of them, and for the gradient a token's largest logit and its weight over the sum:
-//    lse rounded would be all that is left of a confident token's p - 1 (2e-6 of the weight at lse = 20).
+// 3. join_kernel makes lse and loss of them, and for the gradient a token's largest logit, its weight over the sum
+//    and the target's term.  The rounding of lse would be all that is left of a confident token's p - 1 (2e-6 of the
+//    weight at lse = 20), and so would a logit's own that is summed differently in step 4 (one chunk: 2e-6 of it at
+//    K = 3584).
 // 4. For a piece of the vocabulary at a time, the last one first: the product again (but for the last piece where
 //    CTA pairs computed step 2 and K >= 512: its exponentials were kept in the workspace, and kept_kernel finishes
-//    them; chunks of a long contraction are not added apart here, dZ's 16 bits being far coarser), its epilogue turning the logits into
+//    them; a long contraction is one chunk here, dZ's 16 bits being far coarser), its epilogue turning the logits into
 //    dZ in 16 bits; then dX += dZ W^T (float32, in memory) and the piece's dW = X^T dZ in one launch.
 // 5. dx_kernel rounds dX once, in the tokens' own order, zeros for the masked ones.
 //
@@ -267,8 +269,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         return;
     double sum = 0.0, total = 0.0;  // of the block's 32 tokens
     if (p < pad) {
-        const float coef = weight * a.head->scale;
-        float inv = 0.0f;
+        float inv = 0.0f, tgrad = 0.0f;
         if (p < live) {
             s = 0.0f;
 #pragma unroll
@@ -282,11 +283,13 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
                 a.lse[token] = m + rest;
             sum = (double)weight * (double)loss;
             total = (double)weight;
+            const float coef = weight * a.head->scale;
             inv = coef / s;
+            tgrad = inv * expf(target - m) - coef;
         }
         a.largest[p] = m;
         a.inv[p] = inv;
-        a.coef[p] = coef;
+        a.tgrad[p] = tgrad;
     }
     if (!a.stats)
         return;
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 // The kept exponentials exp(z - top) of a piece to the gradient of its logits, in place:
-// inv exp(top - largest) of it, less coef at the target, from the 16 bits of kept_code to the layer's type.  A block takes 32 tokens and 1024
+// inv exp(top - largest) of it, but at the target tgrad, from the 16 bits of kept_code to the layer's type.  A block takes 32 tokens and 1024
 // entries, whose 32 x 32 factors it makes once.  Bound: a read and a write of the piece, from L2 as far as it
 // stayed there.
 template <bool BF16>
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(256, 4) kept_kernel(const __grid_constant__ En
                     continue;
                 uint16_t *row = a.dz + p * a.piece + c0;
                 const int64_t target = (int64_t)a.tgt[p] - a.kept0 - c0;  // behind the last token: none
-                const float coef = a.coef[p];
+                const float tgrad = a.tgrad[p];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int c = (lane + 32 * m) * 8;
@@ -382,9 +385,9 @@ __global__ void __launch_bounds__(256, 4) kept_kernel(const __grid_constant__ En
                     for (int u = 0; u < 4; ++u) {
                         float2 v = make_float2(kept_value(w[u] & 0xffffu) * f, kept_value(w[u] >> 16) * f);
                         if (here && target == c + 2 * u)
-                            v.x -= coef;
+                            v.x = tgrad;
                         if (here && target == c + 2 * u + 1)
-                            v.y -= coef;
+                            v.y = tgrad;
                         w[u] = pair16_of<BF16>(v.x, v.y);
                     }
                     *reinterpret_cast<uint4 *>(row + c) = q[k][m];

@@ -161,7 +161,7 @@ int most_shares(int64_t T, int64_t K)
 
 // The workspace's parts, one behind the other on 256-byte boundaries.
 struct EntropyPlaces {
-    uint64_t x, place, token, tgt, wt, sums, largest, inv, coef, ztarget, partial, dx32, dz, top, end;
+    uint64_t x, place, token, tgt, wt, sums, largest, inv, tgrad, ztarget, partial, dx32, dz, top, end;
 };
 
 EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, bool gradients)
@@ -175,7 +175,7 @@ EntropyPlaces entropy_places(int64_t T, int64_t V, int64_t K, int64_t piece, boo
     };
     const uint64_t t = (uint64_t)T, kp = (uint64_t)((K + 7) / 8 * 8);
     w.x = take(t * kp * 2);
-    for (uint64_t *p : {&w.place, &w.token, &w.tgt, &w.wt, &w.largest, &w.inv, &w.coef, &w.ztarget})
+    for (uint64_t *p : {&w.place, &w.token, &w.tgt, &w.wt, &w.largest, &w.inv, &w.tgrad, &w.ztarget})
         *p = take(t * 4);
     w.sums = take((t + 31) / 32 * 16);
     w.partial = take(t * (uint64_t)partial_rows(V, pairs_only(T, K)) * 8);
@@ -267,7 +267,7 @@ gg_status prepare_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw
         e.a.sums = base + at.sums;
         e.a.largest = floats(at.largest);
         e.a.inv = floats(at.inv);
-        e.a.coef = floats(at.coef);
+        e.a.tgrad = floats(at.tgrad);
         e.a.ztarget = floats(at.ztarget);
         e.a.partial = reinterpret_cast<float2 *>(base + at.partial);
         e.a.dx32 = gradients ? floats(at.dx32) : nullptr;
@@ -440,7 +440,7 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
             z = logits(v0, n, &a.head->live_pad);
             z.largest = a.largest;
             z.inv = a.inv;
-            z.coef = a.coef;
+            z.tgrad = a.tgrad;
             z.out = a.dz;
             z.ldo = a.piece;
             GG_TRY(product(kEpiSoftGrad, z, s));

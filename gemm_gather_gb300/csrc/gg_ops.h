@@ -68,7 +68,8 @@ struct LinearArgs {
     void *kept;            // kEpiLse on pairs: exp(acc - top) of entries kept0 on, in 16 bits, or null;
     float *kept_top;       // top, of every 32 entries: rows of ldpartial tokens
     int64_t ldkept, kept0;
-    const float *largest, *inv, *coef;  // kEpiSoftGrad: a token's largest logit, coef / sum of exponentials, coef
+    const float *largest, *inv, *tgrad;  // kEpiSoftGrad: a token's largest logit, coef / sum of exponentials, and
+                                         // what comes out at its target
     const float *alpha;    // kEpiVocab; null: 1
     int skip;              // pairs of the grid past the end of the first product's walk
     int *status;
@@ -199,7 +200,8 @@ struct EntropyArgs {
     int *place;          // a token's compact place, or -1
     int *token;          // compact: its token
     int *tgt;            // compact targets (-1 behind the last)
-    float *wt, *largest, *inv, *coef, *ztarget;  // (coef: weight scale; inv: coef / sum of exponentials)
+    float *wt, *largest, *inv, *tgrad, *ztarget;  // (coef: weight scale; inv: coef / sum of exponentials; tgrad: the
+                                                  // gradient of the target's logit, inv exp(ztarget - largest) - coef)
     void *sums;          // two doubles for every 32 tokens
     float2 *partial;     // rows x T
     int64_t rows;

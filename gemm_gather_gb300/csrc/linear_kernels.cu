@@ -136,7 +136,8 @@ __device__ __forceinline__ float load_aux(const LinearArgs &a, const void *p, in
 // The gradient over a logit z of token j, for vocabulary entry i of a piece:
 // coef (exp(z - largest) / total - (i is the target)).  The difference first: it is small where it counts, however
 // large the logits are.  From the largest and the sum, not from lse, whose rounding to its own size would be all that
-// is left of a confident token's p - 1.  The target's coef is taken off where a target lies: once a token.
+// is left of a confident token's p - 1.  That term, the target's, is the join's (of the logits that the loss has): it
+// is read where a target lies, once a token.
 struct TokenTerms {
     float largest, inv;  // inv: coef / total
     int target;          // within the piece; any other number: not there
@@ -333,7 +334,7 @@ __device__ __forceinline__ void emit16(const LinearArgs &a, int64_t i, int64_t j
         for (int u = 0; u < C; ++u)
             if (u < n) {
                 const int64_t j = j0 + (int64_t)u * jstep;
-                v[u] = soft_grad(v[u], a.largest[j], a.inv[j]) - ((int)i == a.target[j] - a.v0 ? a.coef[j] : 0.0f);
+                v[u] = (int)i == a.target[j] - a.v0 ? a.tgrad[j] : soft_grad(v[u], a.largest[j], a.inv[j]);
             }
     } else if (aux != nullptr) {
 #pragma unroll
@@ -682,10 +683,10 @@ __device__ __forceinline__ void emit_rows(const LinearArgs &a, int64_t i0, int64
             for (uint32_t left = hits >> c & 0xffffu; left != 0; left &= left - 1) {
                 const int at = __ffs((int)left) - 1;
                 const bool mine = __shfl_sync(0xffffffffu, terms.target, c + at) == (int)i0 + lane;
-                const float coef = mine ? a.coef[j0 + c + at] : 0.0f;
+                const float own = mine ? a.tgrad[j0 + c + at] : 0.0f;
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
-                    v[u] -= u == at ? coef : 0.0f;
+                    v[u] = mine && u == at ? own : v[u];
             }
         } else if (has_aux) {
 #pragma unroll

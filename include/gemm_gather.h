@@ -727,8 +727,9 @@ gg_status gg_policy_loss_check(const void *logits, int64_t ld, const int64_t *ta
  * loses none).  With gradients logits are computed twice, but for those of the last piece where K >= 512 and
  * CTA pairs compute the loss (always beyond 512 tokens).
  * The gradients go through the vocabulary in pieces: `piece` entries (a multiple of
- * 128) at a time, 0 for the library's choice (equal pieces of at most 32768).  The
- * values differ by the order of float32 sums only.
+ * 128) at a time, 0 for the library's choice (equal pieces of at most 32768).  The loss does
+ * not depend on them; gradients differ by the order of float32 sums, and in terms of dZ that are not a target's by
+ * one rounding to 12 bits (entries whose exponentials were kept) and a logit's float32 sum.
  * Alignment: X and W 16-byte aligned with pitches that are multiples of 8; every other
  * argument at its element's alignment, any pitch.  V >= 1 where T > 0; T == 0 gives zero
  * statistics and a zero (or kept) dW; K == 0 gives logits of 0.

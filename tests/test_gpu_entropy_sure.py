@@ -119,3 +119,36 @@ def check_gradients(c):
 def test_gradients(T, V, K, layout, piece):
     for c in (sure(T, V, K, F16, layout), sure(T, V, K, BF16, layout), huge(T, V, K, layout)):
         check_gradients(c.call(piece))
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_the_targets_gradient_does_not_depend_on_the_pieces(layout):
+    """Confident tokens with logits of about 110 from a long contraction, whose sums differ by 2e-6 of that when they are
+    summed in one chunk and in several: as much as 2 % of 1 - p.  A target's row of dW is its token's term, the same
+    in every piece, and the others' probabilities, each off by a logit of one chunk (5.5e-10 K 115 <= 2^-12 of it) or a
+    kept exponential (2^-12), and half a step of 2^-11 either way: 3 2^-11 between the two.  float32 sums: 2^-20."""
+    T, V, K = 600, 1500, 3584
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((T, K), generator=g)
+    x[:, :64] = 1
+    w = torch.randn((V, K), generator=g) * 0.5 * K ** -0.5
+    w[:, :64] = 100 / 64
+    target = torch.randperm(V, generator=g)[:T]
+    w[target, 64:] += x[:, 64:] * (11.5 / x[:, 64:].square().sum(1, keepdim=True))
+    c = Case(T, V, K, F16, layout, gdt=F32)
+    c.x.copy_(x.to(F16)), c.w.copy_((w if layout == "nk" else w.t()).to(F16))
+    c.target = target.cuda()
+    rows = []
+    for piece in (0, 128):
+        c.call(piece)
+        rows.append((c.dw if layout == "nk" else c.dw.t())[c.target].double())
+    x64 = c.x.double()
+    w64 = c.w.double() if layout == "nk" else c.w.double().t()
+    p = torch.softmax(x64 @ w64.t(), 1)[:, c.target]
+    rest = 1 - p.diagonal()
+    assert float(rest.median()) < 0.02 and float((x64 @ w64.t()).max()) < 115
+    others = c.weight.double()[:, None] * p
+    others.fill_diagonal_(0)
+    own = (c.weight.double() * rest)[:, None] * x64.abs()
+    bound = (others.t() @ x64.abs()) * 3 * 2.0 ** -11 + (others.t() @ x64.abs() + own) * 2.0 ** -20
+    assert ((rows[0] - rows[1]).abs() <= bound).all()
