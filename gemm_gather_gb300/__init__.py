@@ -471,7 +471,7 @@ def linear_backward8(dZ, lddz: int, codes, ldc: int, scales, lds: int, act: str,
     """``linear_backward`` of a layer whose input is act(P), P kept in 8 bits: dX = (dZ W^T) act'(P),
     dW (+)= act(P)^T dZ, dbias (+)= column sums of dZ (gg_linear_backward8).  ``workspace``: a contiguous tensor
     on the GPU of at least ``linear_backward8_workspace(M, K)`` bytes where dW is asked for (or an address, with
-    ``workspace_bytes``)."""
+    ``workspace_bytes``); half of that is enough unless dW is float32 and the activation smooth."""
     check(lib.gg_linear_backward8(*_backward8_args(dZ, lddz, codes, ldc, scales, lds, act, W, ldw, layout, dX, lddx,
                                                    dW, lddw, dbias, grad_dtype, accumulate, workspace,
                                                    workspace_bytes, M, N, K, dtype),

@@ -223,10 +223,13 @@ gg_status run_backward(Backward *b, int *dev_status, gg_stream_t stream)
     return op_ok();
 }
 
-// Device bytes of gg_linear_backward8: X in 16 bits, and what that rounding left of it, rows on 16-byte
-// boundaries.
+// Device bytes of gg_linear_backward8: `parts` matrices of 16 bits, X and (2) what that rounding left of it, rows
+// on 16-byte boundaries.
 int64_t unpacked_pitch(int64_t K) { return (K + 7) / 8 * 8; }
-uint64_t unpacked_bytes(int64_t M, int64_t K) { return 2 * (uint64_t)M * (uint64_t)unpacked_pitch(K) * 2; }
+uint64_t unpacked_bytes(int64_t M, int64_t K, int parts)
+{
+    return (uint64_t)parts * (uint64_t)M * (uint64_t)unpacked_pitch(K) * 2;
+}
 
 // Whether act(P) needs more than 16 bits where float32 is to come of it: P itself and max(P, 0) do not.
 bool smooth(gg_activation act) { return act != GG_ACT_NONE && act != GG_ACT_RELU; }
@@ -250,10 +253,13 @@ gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int
         sc{"scales", scales, rows, (K + GG_PACK_BLOCK - 1) / GG_PACK_BLOCK, lds, 4};
     GG_TRY(check_mat(c, true));
     GG_TRY(check_mat(sc, true));
+    // Float32 gradients are those of act(P), not of its rounding: X goes through the product in two parts
+    const bool two = unpacks && grad_dtype == GG_F32 && smooth(act);
     const int64_t ldx = unpacked_pitch(K);
-    const Mat ws{"workspace", workspace, unpacks ? 2 * M : 0, ldx, ldx, 2};
-    if (unpacks && (!workspace || workspace_bytes < unpacked_bytes(M, K)))
-        return op_fail(GG_ERR_INVALID_ARG, "workspace: %llu bytes are needed", (unsigned long long)unpacked_bytes(M, K));
+    const Mat ws{"workspace", workspace, unpacks ? (two ? 2 * M : M) : 0, ldx, ldx, 2};
+    const uint64_t need = unpacks ? unpacked_bytes(M, K, two ? 2 : 1) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return op_fail(GG_ERR_INVALID_ARG, "workspace: %llu bytes are needed", (unsigned long long)need);
     Backward r;
     // the workspace is checked as X is: 16-byte aligned, apart from the outputs
     GG_TRY(prepare_backward(dZ, lddz, unpacks ? workspace : nullptr, ldx, W, ldw, layout, nullptr, 0, act, dX, lddx,
@@ -277,8 +283,6 @@ gg_status prepare_backward8(const void *dZ, int64_t lddz, const void *codes, int
     r.dx.scales = scales;
     r.dx.lds = lds;
     *out = r;
-    // Float32 gradients are those of act(P), not of its rounding: X goes through the product in two parts
-    const bool two = unpacks && grad_dtype == GG_F32 && smooth(act);
     uint16_t *const x16 = reinterpret_cast<uint16_t *>(const_cast<void *>(workspace));
     *rest = gg::LinearArgs{};
     if (two) {
@@ -582,7 +586,7 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
 
 uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K)
 {
-    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? unpacked_bytes(M, K) : 0;
+    return M > 0 && K > 0 && M <= kMaxSize && K <= kMaxSize ? unpacked_bytes(M, K, 2) : 0;
 }
 
 gg_status gg_act_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz, void *dz,

@@ -562,8 +562,9 @@ gg_status gg_unpack8(const void *codes, int64_t ldc, const float *scales, int64_
  * multiplied as well (a product more), so that dW is act(P)'s and not its rounding's.  Types, layouts, alignment, accumulation and errors as for
  * gg_linear_backward; codes and scales may have any alignment and pitch.
  * workspace: device memory, 16-byte aligned, of at least
- * gg_linear_backward8_workspace(M, K) bytes where dW is asked for (X in 16 bits, and the
- * rest), else not used.  What it held is lost; calls that may run at the same time, or replays of
+ * gg_linear_backward8_workspace(M, K) bytes where dW is asked for (X in 16 bits, and what that rounding
+ * left: 4 M K), else not used; half of it is enough for a dW in 16 bits, and without an activation or
+ * with relu, where no rest is multiplied.  What it held is lost; calls that may run at the same time, or replays of
  * graphs that captured them, need workspaces of their own.
  * ------------------------------------------------------------------------- */
 uint64_t gg_linear_backward8_workspace(int64_t M, int64_t K);
