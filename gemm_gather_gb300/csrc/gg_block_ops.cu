@@ -405,10 +405,11 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         both = plan_vocab(x, w, apart, most_shares(a.T, a.K), &bt_dx, &bt_dw);
     }
     if (both) {
-        a.most_shares = most_shares(a.T, a.K);
         a.dx_tiles_i = (int)((x.I + 255) / 256);
         a.dx_bt = bt_dx;
         a.dx_kb = (int)((x.K + 63) / 64);
+        const int room = most_shares(a.T, a.K), all = a.dx_kb / 16 > 1 ? a.dx_kb / 16 : 1;  // (tokens_kernel)
+        a.most_shares = room < all ? room : all;
         a.dw_tiles = ((w.I + 255) / 256) * ((w.J + bt_dw - 1) / bt_dw);
     }
     GG_TRY(launched(launch_entropy_tokens(a, s), "gathering the tokens"));
@@ -448,6 +449,7 @@ gg_status run_entropy(const Entropy &e, cudaStream_t s)
         gradient_of(v0, &x, &w);
         if (both) {
             x.shares = &a.head->shares;
+            x.most_shares = a.most_shares;
             const char *why = nullptr;
             const cudaError_t err = launch_both(kEpiVocab, x, bt_dx, w, bt_dw, s, &why);
             GG_TRY(launched(err, why ? why : "launching the gradients of a piece"));

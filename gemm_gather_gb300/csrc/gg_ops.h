@@ -60,6 +60,7 @@ struct LinearArgs {
     const int *live;
     int live_k;
     const int *shares;     // kEpiVocab: of the contraction, share s into rows s J of out (null: 1)
+    int most_shares;       // what *shares is at most: the grid has pairs for that many
     const int *target;     // a token's, within the vocabulary
     int v0;                // the piece's first entry
     float2 *partial;       // kEpiLse: a row for every 128 entries (split kernel: 32), a place per token

@@ -2021,7 +2021,7 @@ cudaError_t launch_pair(const LinearArgs &args, int bt, int parts, const LinearA
         x.tiles_i = (int)tiles_i;
         x.tiles_j = (int)tiles_j;
         x.num_kb = (int)((x.K + kBK - 1) / kBK);
-        tiles += tiles_i * tiles_j;
+        tiles += tiles_i * tiles_j * (x.shares ? x.most_shares : 1);
     }
     if (tiles >= 1ll << 31) {
         *why = "more than 2^31 tiles";

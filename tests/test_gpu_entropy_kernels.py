@@ -5,6 +5,7 @@ bounds, and the losses to the closer one of entropy_oracle.py."""
 import pytest
 import torch
 
+import gemm_gather_gb300 as gg
 from tests import entropy_oracle as e
 from tests.block_oracle import BF16, F16, F32
 from tests.launched import variants
@@ -107,3 +108,21 @@ def test_large_logits_and_kept_exponentials(T, V, K):
     c = Case(T, V, K, BF16, scale=150.0).call().check()
     assert float(c.lse.max()) > 200
     assert products(c)[1] == 1
+
+
+@pytest.mark.parametrize("T,V,K", [(100, 8192, 256), (64, 16000, 256), (300, 2000, 512)])
+def test_a_pair_for_every_share_of_dx(T, V, K):
+    """Where few tiles are left to the pairs, the shares of dX's contraction are tiles too."""
+    c = Case(T, V, K, BF16)
+    room = torch.zeros((gg.linear_cross_entropy_workspace(T, V, K),), dtype=torch.uint8, device="cuda")
+
+    def call():
+        c.call(workspace=room)
+    call()
+    c.check()
+    shares = int(room[:12].view(torch.int32)[2])                   # as the device decided
+    kernel, numbers, grid = variants(call, "pair_kernel")[-1]
+    assert numbers[0] == VOCAB and numbers[1] >= 0 and shares > 1
+    most = numbers[2]                                              # tokens (dX) and entries (dW) of a tile, at most
+    tiles = -(-K // 256) * -(-T // most) * shares + -(-K // 256) * -(-V // most)
+    assert grid[0] // 2 >= min(76, tiles)
