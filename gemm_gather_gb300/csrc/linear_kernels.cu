@@ -2065,8 +2065,10 @@ cudaError_t launch_split(const LinearArgs &args, int parts, cudaStream_t s, cons
     return cudaLaunchKernelEx(&l.cfg, split_kernel<EPI, BT>, map_a, map_b, a);
 }
 
-// Logits of longer contractions than kPlainLse are summed in chunks for lse: without them losses are off by
-// 4.5e-7 of their size at 1024 and 1.1e-6 at 2011, and that grows with the length.  In registers the sums of chunks
+// Logits of longer contractions than kPlainLse are summed in chunks for lse, which holds all tokens' losses
+// together within 1.2e-6 of their size.  Measured against float64 (600 tokens, V = 4000, logits of deviation 2.5;
+// bfloat16, float16): in one chunk 5.3e-7, 6.4e-7 at 1024, 8.1e-7, 9.7e-7 at 1536, 9.8e-7, 1.14e-6 at kPlainLse, and on
+// with the length; in chunks of 1024 4.7e-7 to 6.3e-7 at 1800 to 8192; a float32 product 1e-7 to 4e-7.  In registers the sums of chunks
 // spill, which only tiles of long contractions hide: 4096 tokens, 100003 entries, K = 1024 take 570 us with and 460
 // without, the product of 777 tokens, 32768 entries, K = 2011 90 and 65.
 constexpr int64_t kPlainLse = 1792;

@@ -4,7 +4,7 @@ from __future__ import annotations
 import torch
 
 # The tensor cores' accumulator truncates, which costs losses 4.5e-7 of their size (relative errors of all tokens'
-# losses together) after a contraction of 1024 and 1.1e-6 after 2011: 5.5e-10 an element at most, of the longest
+# losses together) after a contraction of 1024 and 1.1e-6 after 2011: some 5.5e-10 an element, of the longest
 # contraction that is one chunk.  Twice that, and a rounding to float32 of each of lse and the loss.
 PER_ELEMENT = 2 * 5.5e-10
 ROUNDINGS = 2 * 2.0 ** -24
