@@ -599,7 +599,9 @@ gg_status gg_linear_backward8_check(const void *dZ, int64_t lddz, const void *co
  * residual, h, rstd, codes and scales may be NULL, y only with codes.  h and y may each
  * be x or residual (same pointer and pitch), not both the same one.  The squares are
  * summed in float32: rows beyond 1e19 in size, or with an infinity, have rstd 0 (y is
- * NaN at the infinity).  A row of zeros with eps 0, or one that holds NaN, gives NaN.
+ * NaN at the infinity); where eps does not cover them, rows below 1e-19 in size lose
+ * digits of rstd, and with eps 0 rows below 1e-23 have an infinite one.  A row of zeros
+ * with eps 0, or one that holds NaN, gives NaN.
  * Any alignment and pitch; 16-byte aligned rows (8-byte aligned codes) of up to 32768
  * elements are the fast case, where each row is read once.
  * ------------------------------------------------------------------------- */

@@ -105,3 +105,25 @@ def test_backward_of_rows_that_are_not_ordinary_with_rows_in_flight():
     want, size, _, _ = gradients64(dy, h, rstd, w, dh_in)
     tol = size * (N / 512 + 52) * 2.0 ** -24 + o.half_ulp(want, BF16) * 1.01
     assert ((dh.double() - want).abs() <= tol)[keep].all()
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+def test_forward_of_the_smallest_rows(pad):
+    """Squares are summed in float32: with eps 0, rows down to 1e-19 are normed like others, and rows whose squares
+    all vanish have an infinite rstd; an eps covers them."""
+    N = 700
+    x, _, w = make(6, N, BF16, residual=False, pad=pad)
+    x[0] *= 2.0 ** -60
+    x[1:3] *= 2.0 ** -90
+    x[3] *= 2.0 ** -120
+    x[4, 1:] = 0
+    for eps in (0.0, 1e-6):
+        y, rstd = o.room(6, N, BF16, pad), torch.empty((6,), device="cuda")
+        norm(x, None, w, eps=eps, y=y, rstd=rstd)
+        if eps == 0:
+            check_norm(x[[0, 4, 5]], None, w, eps, None, y[[0, 4, 5]], None, None, rstd[[0, 4, 5]])
+            assert (rstd[1:4] == float("inf")).all()
+            assert (y[1:4].isinf() | (x[1:4] == 0)).all()
+        else:
+            assert ((rstd[:4] - 1000).abs() < 1e-2).all()
+            check_norm(x[[0, 1, 2, 4, 5]], None, w, eps, None, y[[0, 1, 2, 4, 5]], None, None, rstd[[0, 1, 2, 4, 5]])
