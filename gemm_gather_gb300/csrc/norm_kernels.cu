@@ -71,6 +71,58 @@ __device__ __forceinline__ float row_sum(float v, const RowShape &s, float (&buf
     return t;
 }
 
+// A sum with what its roundings left: squares of a row, whose sum decides its rstd's last bit, and with it that of
+// thousands of elements of y and of their codes.  The sums that are small beside the row's are plain (a warp's where
+// it is one of eight or more, else an eighth of it): their roundings hardly show.  rstd is then what an exact sum gives for
+// 90 to 94 % of bfloat16 rows (plain sums: 81 to 86 %, 66 % of rows of 32 warps) and 83 to 91 % of float16's (65 to 85 %),
+// whose squares' last bits are not evenly spread, so that a thread's own sum loses some; 16384 x 8192 takes 181.8 us for 180.3.
+struct Exact {
+    float sum, rest;
+};
+
+__device__ __forceinline__ Exact plus(Exact a, Exact b)
+{
+    const float s = a.sum + b.sum, other = s - a.sum;
+    const float lost = (a.sum - (s - other)) + (b.sum - other);  // exactly, in either order
+    return Exact{s, a.rest + b.rest + lost};
+}
+
+__device__ __forceinline__ Exact plus_lane(Exact t, int d)
+{
+    return plus(t, Exact{__shfl_xor_sync(0xffffffffu, t.sum, d), __shfl_xor_sync(0xffffffffu, t.rest, d)});
+}
+
+// The sum over a row's R warps of each thread's v, as row_sum's.  Where it overflows it is infinite, or NaN as one of
+// its terms.
+__device__ __forceinline__ float row_sum_exact(float v, const RowShape &s, float2 (&buf)[kMaxWarps])
+{
+#pragma unroll
+    for (int d = 16; d > 2; d >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, d);
+    Exact t{v, 0.0f};
+    if (s.R < 8) {
+        t = plus_lane(plus_lane(t, 2), 1);
+    } else {
+        t.sum += __shfl_xor_sync(0xffffffffu, t.sum, 2);
+        t.sum += __shfl_xor_sync(0xffffffffu, t.sum, 1);
+    }
+    if (s.R > 1) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0)
+            buf[warp] = make_float2(t.sum, t.rest);
+        __syncthreads();
+        // the row's warps, side by side in every group of lanes that holds them
+        const int at = lane & ((2 << (31 - __clz(s.R - 1))) - 1);
+        const float2 own = at < s.R ? buf[warp / s.R * s.R + at] : make_float2(0.0f, 0.0f);
+        t = Exact{own.x, own.y};
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2)
+            if (d < s.R)
+                t = plus_lane(t, d);
+    }
+    return t.sum <= 3.402823466e38f ? t.sum + t.rest : t.sum;  // (what infinities leave is NaN)
+}
+
 // Eight neighbouring 16-bit elements, or weights, as pairs of floats.
 struct Eight {
     F2 v[4];
@@ -209,7 +261,7 @@ __device__ __forceinline__ void store_vector(uint16_t *p, int left, const uint4 
 template <bool BF16, int VPT, bool RES, bool WHOLE>
 __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a, const RowShape s)
 {
-    __shared__ float sums[2][kMaxWarps];
+    __shared__ float2 sums[kMaxWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp % s.R, N = (int)a.N;
     const int64_t row = (int64_t)blockIdx.x * s.rows + warp / s.R;
@@ -250,7 +302,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
         }
     }
     const float2 both = halves_of(sq);
-    const float total = row_sum(both.x + both.y, s, sums, 0);
+    const float total = row_sum_exact(both.x + both.y, s, sums);
     launch_dependents();  // (earlier, the next launch's blocks take places from this one's)
     if (!live)
         return;
@@ -292,7 +344,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
 template <bool BF16>
 __global__ void __launch_bounds__(512) norm_any_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float sums[2][kMaxWarps];
+    __shared__ float2 sums[2][kMaxWarps];  // in turn, so that one barrier a row is enough
     const RowShape s{(int)blockDim.x / 32, 1};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int turn = 0;
@@ -320,7 +372,7 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const __grid_constant__ N
                     sq = fmaf(v, v, sq);
                 }
             }
-        const float rstd = 1.0f / sqrtf(row_sum(sq, s, sums, turn) / (float)a.N + a.eps);
+        const float rstd = 1.0f / sqrtf(row_sum_exact(sq, s, sums[turn]) / (float)a.N + a.eps);
         if (a.rstd && threadIdx.x == 0)
             a.rstd[row] = rstd;
         for (int64_t b = (int64_t)warp * kPackBlock; b < a.N; b += (int64_t)s.R * kPackBlock) {
