@@ -1,7 +1,8 @@
 // Declarations shared by the operators' translation units (host side): the
 // linear layer (linear_kernels.cu), the policy loss (loss_kernels.cu), AdamW
-// (adamw_kernels.cu), the norm and 8-bit activations (norm_kernels.cu), whose C
-// entry points are in gg_ops.cu and gg_block_ops.cu.
+// (adamw_kernels.cu), the norm and 8-bit activations (norm_kernels.cu) and the
+// vocabulary's cross entropy (entropy_kernels.cu, its products in linear_kernels.cu),
+// whose C entry points are in gg_ops.cu and gg_block_ops.cu.
 #pragma once
 #include <cuda_runtime.h>
 
